@@ -90,7 +90,7 @@ def draw(rng):
                     rng.random() < 0.3, shape)
     else:
         rows = min(n_req * _spread(rng, 1, 32), 256)
-        ctx = min(_spread(rng, 1, 131072), 32 * 16384 // n_req)
+        ctx = min(_spread(rng, 1, 131072), 24 * 16384 // n_req)
         c = _tree("", op, n_req, rows, ctx if op == "attend" else min(ctx, 8192), heads, rng.choice([1, 4, 5, 8]), block, rot,
                   pairs, rng.random() < 0.3, shape)
     del c["name"]
