@@ -12,8 +12,10 @@
  * Around it: the quick pass on the 8-bit view planes (w12_gemm_q,
  * w12_lmhead_argmax_q, w12_verify_step_q), the certified LM head
  * (w12_head_cert_norms, w12_lmhead_argmax_certified), the TLV splice of two
- * trees (w12_tlv_chain, w12_tlv_splice) and a recurrent (Gated DeltaNet)
- * layer over a tree (w12_gdn_tree_verify, w12_gdn_commit).
+ * trees (w12_tlv_chain, w12_tlv_splice), a recurrent (Gated DeltaNet)
+ * layer over a tree (w12_gdn_tree_verify, w12_gdn_commit), attention over a
+ * paged 8-bit KV cache (w12_kv_append, w12_tree_attention, w12_kv_commit) and
+ * acceptance by sampling (w12_tree_verify_sampled).
  *
  * Sources (SpecPilot explainer at jaehun.me, "SpecPilot: Autonomous Algorithm
  * Discovery and Systems Optimization for Speculative Decoding"; the summary
@@ -482,6 +484,138 @@ w12_status w12_tlv_chain(const int32_t *c_len, const int32_t *t1_row_off, int32_
 w12_status w12_tlv_splice(const w12_tree *t1, const int32_t *c_tok, const int32_t *c_len, const int32_t *c_node,
                           int32_t n_req, int32_t p1_max, const int32_t *m, const w12_tree *t2, w12_tree *out,
                           void *ws, size_t ws_bytes, w12_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over a paged 8-bit KV cache
+ *
+ * The cache holds the committed tokens of every request, in blocks of
+ * block_tokens tokens: E4M3 codes under one power-of-two scale per block and
+ * key/value head (value = code * scale).  Keys are stored turned by their
+ * position, values transposed.  The rows of a draft tree stay outside the
+ * cache until they are accepted:
+ *
+ *   prompt rows --w12_kv_append--> cache
+ *   tree rows + cache --w12_tree_attention--> outputs per row
+ *   accepted row (w12_tree_accept, w12_tree_verify_sampled) --w12_kv_commit--> cache
+ *
+ * Limits: head_dim 128; block_tokens 32, 64 or 128; at most 64 query heads to
+ * a key/value head; n_req <= 512; anything else is W12_E_UNSUPPORTED.
+ * ---------------------------------------------------------------------- */
+
+typedef struct {
+    int32_t n_kv_heads, head_dim, block_tokens;
+    int32_t n_blocks;            /* blocks in the pool */
+    int32_t max_blocks;          /* row length of block_table */
+    uint8_t *k;                  /* device [n_blocks][n_kv_heads][block_tokens][head_dim], 16-byte aligned */
+    uint8_t *v;                  /* device [n_blocks][n_kv_heads][head_dim][block_tokens], 16-byte aligned */
+    float *k_scale, *v_scale;    /* device [n_blocks][n_kv_heads], powers of two */
+    const int32_t *block_table;  /* device [n_req][max_blocks]: block of tokens i*block_tokens.. of each request */
+    const int32_t *len;          /* device [n_req]: committed tokens */
+} w12_kv_cache;
+
+/*
+ * Position rotation of the first rot_dim dimensions of a head (the rest stay):
+ * pair (a, b) becomes (a cos - b sin, b cos + a sin), in FP32.  Pairs are
+ * (i, i + rot_dim/2), or (2i, 2i + 1) with adjacent = 1.  NULL in place of
+ * the struct, or rot_dim 0: no rotation.
+ */
+typedef struct {
+    int32_t rot_dim;             /* even, <= head_dim */
+    int32_t adjacent;
+    int32_t max_pos;             /* positions in the tables */
+    const float *cos, *sin;      /* device [max_pos][rot_dim / 2] */
+} w12_rope;
+
+/*
+ * Append k/v rows row_off[r] .. row_off[r+1]-1 (device BF16 [n_rows][n_kv_heads][head_dim],
+ * rows k_stride / v_stride elements apart, 16-byte aligned) to request r's
+ * tokens, for every request (row_off: device [n_req + 1]); request r's first
+ * new token takes position len[r].  A block filled from its first token gets
+ * the least power-of-two scale (not under 2^-32) that its new tokens need; a
+ * block that holds tokens keeps the larger of its own and theirs, its codes
+ * rounded again if the scale grows.  Slots past the new end stay as they are;
+ * a value that is not finite is stored as NaN and counts for no scale.
+ * len_out[r] (device, may be cache->len) = the new length.  The blocks that the new
+ * tokens fall into must be in the table, and no block may be in it twice.
+ * Device checks: row offsets out of order, a length past the table or the
+ * rotation tables, or a block outside the pool set W12_E_INVAL in the status
+ * word and leave that request as it was.
+ * ws: as for w12_tree_build.
+ */
+w12_status w12_kv_append(const w12_kv_cache *cache, const w12_rope *rope, int32_t n_req, const uint16_t *k,
+                         int64_t k_stride, const uint16_t *v, int64_t v_stride, int32_t n_rows,
+                         const int32_t *row_off, int32_t *len_out, void *ws, size_t ws_bytes, w12_stream_t stream);
+
+/*
+ * The same for the accepted path of a tree: request r gets the rows from its
+ * root down to acc_node[r] (device [n_req], from the acceptance), k and v
+ * being the tree's rows.  Device check: a row outside the request sets
+ * W12_E_INVAL and leaves that request as it was.
+ */
+w12_status w12_kv_commit(const w12_kv_cache *cache, const w12_rope *rope, const w12_tree *tree, int32_t n_req,
+                         const int32_t *acc_node, const uint16_t *k, int64_t k_stride, const uint16_t *v,
+                         int64_t v_stride, int32_t *len_out, void *ws, size_t ws_bytes, w12_stream_t stream);
+
+/*
+ * Attention of a tree's rows: row i of request r stands at position
+ * len[r] + depth[i] and attends to request r's cached tokens and to its own
+ * root path (ancestors and itself, from the k and v rows given), with n_heads
+ * query heads, head hq reading key/value head hq / (n_heads / n_kv_heads).
+ * q, k, v: the linears' rows before rotation (device BF16, rows *_stride
+ * elements apart, 16-byte aligned; slices of one fused row are fine).
+ * scale: the softmax scale.  out: device BF16 [R][n_heads][head_dim], 16-byte aligned.
+ * The softmax statistics and all sums are FP32.  Rows off a root path and
+ * cache slots past len[r] cannot reach an output, whatever they hold.
+ * aws: device, 256-byte aligned, w12_attn_workspace_bytes(...) bytes, no
+ * initialisation; ws: as for w12_tree_build.  Device checks: tree arrays that
+ * contradict each other, or lengths, positions or blocks out of range, set
+ * W12_E_INVAL in the status word (the affected rows are zero or undefined).
+ */
+size_t w12_attn_workspace_bytes(int32_t R, int32_t n_heads, int32_t n_kv_heads, int32_t n_req);
+w12_status w12_tree_attention(const w12_kv_cache *cache, const w12_rope *rope, const w12_tree *tree, int32_t n_req,
+                              int32_t n_heads, const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                              int64_t k_stride, const uint16_t *v, int64_t v_stride, float scale, uint16_t *out,
+                              void *ws, size_t ws_bytes, void *aws, size_t aws_bytes, w12_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Sampled verification
+ * ---------------------------------------------------------------------- */
+
+typedef struct {
+    const void *logits;          /* device [R][vocab], rows logits_stride elements apart */
+    int32_t logits_f32;          /* 0: BF16, 1: FP32 */
+    int64_t vocab, logits_stride;
+    const float *temperature;    /* device [n_req], or NULL (1); 0: greedy */
+    const float *draft_p;        /* device [R][vocab]: the drafter's probabilities at each row, or NULL */
+    int64_t draft_stride;
+    const float *u_accept;       /* device [R] in [0, 1): decides on row j as a draft (needed with draft_p) */
+    const float *u_sample;       /* device [R] in [0, 1): draws row i's own token */
+} w12_sampling;
+
+/*
+ * One token per tree row, distributed as the target's p = softmax(logits / T)
+ * at that row, so that accepting children that carry their parent's token is
+ * lossless.  With draft_p (children drawn independently from it): children in
+ * row order are accepted if u_accept q(x) < p(x), each rejection turning p
+ * into max(0, p - q) / sum; the accepted child's token, or a token drawn from
+ * what is left by the inverse CDF at u_sample.  Without: drawn from p.
+ * Weights exp(z - max) are summed as whole multiples of 2^-40, so tokens do
+ * not depend on the batch or the machine's order; ties go to the lowest index.
+ * row_tok (device [R]); row_logp (device [R], nullable): log p of it.  A row
+ * whose logits are all -inf or NaN gets -1 and -inf; NaN counts as -inf.
+ * vocab <= w12_sample_max_vocab().  ws: as for w12_tree_build.
+ */
+int64_t w12_sample_max_vocab(void);
+w12_status w12_tree_sample(const w12_sampling *dist, const w12_tree *tree, int32_t n_req, int32_t *row_tok,
+                           float *row_logp, void *ws, size_t ws_bytes, w12_stream_t stream);
+
+/*
+ * w12_tree_sample followed by the acceptance of w12_tree_accept on row_tok:
+ * acc_tok, acc_len, acc_node (nullable) and p_max as there.
+ */
+w12_status w12_tree_verify_sampled(const w12_sampling *dist, const w12_tree *tree, int32_t n_req, int32_t p_max,
+                                   int32_t *row_tok, float *row_logp, int32_t *acc_tok, int32_t *acc_len,
+                                   int32_t *acc_node, void *ws, size_t ws_bytes, w12_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -9,7 +9,9 @@ below raises -- there is no fallback.
 Entry points (same names as the C ABI): ``w12_pack``, ``w12_unpack``,
 ``w12_load_check``, ``w12_gemm``, ``w12_lmhead_argmax``, ``w12_tree_build``,
 ``w12_tree_accept``, ``w12_verify_step``, the TLV calls (``w12_verify_step_q``,
-``w12_tlv_chain``, ``w12_tlv_splice``), plus the workspace helpers.
+``w12_tlv_chain``, ``w12_tlv_splice``), the attention layer's
+``w12_kv_append``, ``w12_tree_attention``, ``w12_kv_commit``, and
+``w12_tree_verify_sampled``, plus the workspace helpers.
 """
 from __future__ import annotations
 
@@ -109,6 +111,13 @@ def lib():
             "w12_gdn_wy_verify": ([p, p, i32, p, p, p, sz, p], C.c_int),
             "w12_gdn_wy_commit": ([p, p, i32, p, p, p, p, sz, p], C.c_int),
             "w12_tlv_splice": ([p, p, p, p, i32, i32, p, p, p, p, sz, p], C.c_int),
+            "w12_kv_append": ([p, p, i32, p, i64, p, i64, i32, p, p, p, sz, p], C.c_int),
+            "w12_kv_commit": ([p, p, p, i32, p, p, i64, p, i64, p, p, sz, p], C.c_int),
+            "w12_attn_workspace_bytes": ([i32, i32, i32, i32], sz),
+            "w12_tree_attention": ([p, p, p, i32, i32, p, i64, p, i64, p, i64, C.c_float, p, p, sz, p, sz, p], C.c_int),
+            "w12_sample_max_vocab": ([], i64),
+            "w12_tree_sample": ([p, p, i32, p, p, p, sz, p], C.c_int),
+            "w12_tree_verify_sampled": ([p, p, i32, i32, p, p, p, p, p, p, sz, p], C.c_int),
             "w12_debug_set": ([i32, C.c_uint64], None),
             "w12_debug_num_sms": ([], i32),
             "w12_debug_profile": ([i32], None),
@@ -343,6 +352,24 @@ class DeviceTree:
         self.c = TreeC(0, *(t.data_ptr() for t in (self.parent, self.token, self.depth, self.req, self.score,
                                                     self.rank, self.req_row_off)))
 
+    @classmethod
+    def from_arrays(cls, parent, depth, req, req_row_off, token=None):
+        """A tree from its device arrays (a tree built elsewhere, a chain of
+        single tokens): parent, req (int32 [R]), depth (uint8 [R]), req_row_off
+        (int32 [n_req + 1]) and optionally the rows' tokens (int32 [R])."""
+        import torch
+        R, n_req = int(parent.shape[0]), int(req_row_off.shape[0]) - 1
+        t = cls(R, n_req, device=parent.device)
+        for dst, src, dt in ((t.parent, parent, torch.int32), (t.depth, depth, torch.uint8), (t.req, req, torch.int32),
+                             (t.req_row_off, req_row_off, torch.int32), (t.token, token, torch.int32)):
+            if src is None:
+                continue
+            if src.dtype != dt or src.shape != dst.shape:
+                raise ValueError("tree arrays: int32 [R] (depth: uint8), req_row_off int32 [n_req + 1]")
+            dst.copy_(src)
+        t.c.R = R
+        return t
+
     @property
     def R(self) -> int:
         return int(self.c.R)
@@ -496,6 +523,228 @@ def w12_gdn_wy_commit(layer: GdnLayer, tree: DeviceTree, n_req: int, acc_node, u
                                    C.c_void_p(u.data_ptr()), C.c_void_p(state.data_ptr()), ws.ptr, ws.nbytes,
                                    _stream(stream)), "w12_gdn_wy_commit")
     return state
+
+
+# ---------------------------------------------------------------------------
+# attention over a paged 8-bit KV cache
+# ---------------------------------------------------------------------------
+
+class KvCacheC(C.Structure):
+    _fields_ = [("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("block_tokens", C.c_int32),
+                ("n_blocks", C.c_int32), ("max_blocks", C.c_int32), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("block_table", C.c_void_p), ("len", C.c_void_p)]
+
+
+class RopeC(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("adjacent", C.c_int32), ("max_pos", C.c_int32), ("cos", C.c_void_p),
+                ("sin", C.c_void_p)]
+
+
+def _want(t, dtype, shape, what):
+    """A contiguous device tensor of this type and shape (None: any size)."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)) \
+            or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous {dtype} {shape} wanted, got {t.dtype} {tuple(t.shape)}")
+
+
+class KvCache:
+    """A paged KV cache: E4M3 codes k (uint8 [n_blocks][H][block_tokens][128])
+    and v (uint8 [n_blocks][H][128][block_tokens]), power-of-two scales
+    (float32 [n_blocks][H]), the block table (int32 [n_req][max_blocks]) and
+    the committed lengths (int32 [n_req]).  The tensors stay the caller's."""
+
+    def __init__(self, k, v, k_scale, v_scale, block_table, length):
+        import torch
+        n, H, bt, d = k.shape
+        _want(k, torch.uint8, (n, H, bt, d), "k")
+        _want(v, torch.uint8, (n, H, d, bt), "v")
+        _want(k_scale, torch.float32, (n, H), "k_scale")
+        _want(v_scale, torch.float32, (n, H), "v_scale")
+        _want(block_table, torch.int32, (None, None), "block_table")
+        _want(length, torch.int32, (block_table.shape[0],), "length")
+        self.k, self.v, self.k_scale, self.v_scale, self.block_table, self.len = k, v, k_scale, v_scale, block_table, length
+        self.n_req, self.H, self.bt, self.d = int(block_table.shape[0]), int(H), int(bt), int(d)
+        self.c = KvCacheC(H, d, bt, n, block_table.shape[1], k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                          v_scale.data_ptr(), block_table.data_ptr(), length.data_ptr())
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def empty(cls, n_blocks, n_kv_heads, block_tokens, block_table, device="cuda"):
+        """A zeroed pool of n_blocks blocks; every request starts without tokens."""
+        import torch
+        z = lambda *s, dt=torch.uint8: torch.zeros(s, dtype=dt, device=device)
+        return cls(z(n_blocks, n_kv_heads, block_tokens, 128), z(n_blocks, n_kv_heads, 128, block_tokens),
+                   torch.ones(n_blocks, n_kv_heads, device=device), torch.ones(n_blocks, n_kv_heads, device=device),
+                   block_table, z(block_table.shape[0], dt=torch.int32))
+
+
+class Rope:
+    """Position tables: cos and sin, float32 [max_pos][rot_dim / 2]; pairs
+    (i, i + rot_dim / 2), or (2 i, 2 i + 1) with ``adjacent``."""
+
+    def __init__(self, cos, sin, adjacent: bool = False):
+        import torch
+        _want(cos, torch.float32, (None, None), "cos")
+        _want(sin, torch.float32, tuple(cos.shape), "sin")
+        self.cos, self.sin = cos, sin
+        self.c = RopeC(2 * cos.shape[1], int(adjacent), cos.shape[0], cos.data_ptr(), sin.data_ptr())
+        self.ref = C.byref(self.c)
+
+
+class AttentionWorkspace:
+    """Device scratch of ``w12_tree_attention`` for up to R rows of n_req requests."""
+
+    def __init__(self, R: int, n_heads: int, n_kv_heads: int, n_req: int, device="cuda"):
+        import torch
+        self.nbytes = int(lib().w12_attn_workspace_bytes(int(R), int(n_heads), int(n_kv_heads), int(n_req)))
+        if self.nbytes == 0:
+            raise W12Error(W12_E_UNSUPPORTED, "w12_attn_workspace_bytes")
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.ptr = C.c_void_p(self.buf.data_ptr())
+
+
+def _bf16_rows(t, rows, what):
+    """(pointer, elements between rows) of bf16 rows whose elements are contiguous."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.stride(1) != 1 or t.shape[0] < rows:
+        raise ValueError(f"{what}: bfloat16 rows [>= {rows}][heads * 128] with contiguous elements wanted")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), -(-t.shape[1] // 8) * 8))
+
+
+def _kv_rows(cache, k, v, rows):
+    for t, what in ((k, "k"), (v, "v")):
+        if t.shape[-1] != cache.H * cache.d:
+            raise ValueError(f"{what}: rows of {cache.H * cache.d} elements wanted")
+    return (*_bf16_rows(k, rows, "k"), *_bf16_rows(v, rows, "v"))
+
+
+def w12_kv_append(cache: KvCache, rope: Optional[Rope], k, v, row_off, ws: Workspace, len_out=None, stream=None):
+    """Append rows row_off[r]..row_off[r+1]-1 of k and v (bfloat16 [T][H * 128],
+    row slices allowed) to every request's tokens; the new lengths go to
+    ``len_out`` (default: in place)."""
+    import torch
+    _want(row_off, torch.int32, (cache.n_req + 1,), "row_off")
+    len_out = cache.len if len_out is None else len_out
+    _want(len_out, torch.int32, (cache.n_req,), "len_out")
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v: the same number of rows wanted")
+    kp, ks, vp, vs = _kv_rows(cache, k, v, T)
+    _check(lib().w12_kv_append(cache.ref, rope.ref if rope else None, cache.n_req, kp, ks, vp, vs, T,
+                               row_off.data_ptr(), len_out.data_ptr(), ws.ptr, ws.nbytes, _stream(stream)),
+           "w12_kv_append")
+    return len_out
+
+
+def w12_kv_commit(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n_req: int, acc_node, k, v, ws: Workspace,
+                  len_out=None, stream=None):
+    """Append the accepted path of every request (root .. acc_node[r]) to its
+    tokens; k and v are the tree's rows."""
+    import torch
+    if n_req != cache.n_req:
+        raise ValueError("the cache's table and the tree: the same requests wanted")
+    _want(acc_node, torch.int32, (n_req,), "acc_node")
+    len_out = cache.len if len_out is None else len_out
+    _want(len_out, torch.int32, (n_req,), "len_out")
+    kp, ks, vp, vs = _kv_rows(cache, k, v, tree.c.R)
+    _check(lib().w12_kv_commit(cache.ref, rope.ref if rope else None, C.byref(tree.c), n_req, acc_node.data_ptr(), kp,
+                               ks, vp, vs, len_out.data_ptr(), ws.ptr, ws.nbytes, _stream(stream)), "w12_kv_commit")
+    return len_out
+
+
+def w12_tree_attention(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n_req: int, q, k, v, ws: Workspace,
+                       aws: AttentionWorkspace, scale: Optional[float] = None, out=None, stream=None):
+    """Attention of the tree's rows over the cache and their root paths ->
+    bfloat16 [R][n_heads][128].  q (bfloat16 [R][n_heads * 128]), k, v: the
+    linears' rows before rotation (slices of a fused row are fine); scale:
+    default 128 ** -0.5."""
+    import torch
+    if n_req != cache.n_req:
+        raise ValueError("the cache's table and the tree: the same requests wanted")
+    R, Hq = tree.c.R, q.shape[1] // cache.d
+    if out is None:
+        out = torch.empty((R, Hq, cache.d), dtype=torch.bfloat16, device=q.device)
+    elif out.shape[0] < R or out.shape[1:] != (Hq, cache.d) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        raise ValueError(f"out: contiguous bfloat16 [{R}][{Hq}][{cache.d}] wanted")
+    qp, qs = _bf16_rows(q, R, "q")
+    kp, ks, vp, vs = _kv_rows(cache, k, v, R)
+    _check(lib().w12_tree_attention(cache.ref, rope.ref if rope else None, C.byref(tree.c), n_req, Hq, qp, qs, kp, ks,
+                                    vp, vs, cache.d ** -0.5 if scale is None else scale, out.data_ptr(), ws.ptr,
+                                    ws.nbytes, aws.ptr, aws.nbytes, _stream(stream)), "w12_tree_attention")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# sampled verification
+# ---------------------------------------------------------------------------
+
+class SamplingC(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("logits_f32", C.c_int32), ("vocab", C.c_int64), ("logits_stride", C.c_int64),
+                ("temperature", C.c_void_p), ("draft_p", C.c_void_p), ("draft_stride", C.c_int64),
+                ("u_accept", C.c_void_p), ("u_sample", C.c_void_p)]
+
+
+class SampleRows:
+    """The target's logits (bfloat16 or float32 [R][vocab]) and the random
+    numbers of one sampled verification: u_sample (float32 [R]), temperature
+    (float32 [n_req], optional; 0 = greedy) and, for a drafter that samples,
+    its probabilities draft_p (float32 [R][vocab]) with u_accept (float32 [R])."""
+
+    def __init__(self, logits, u_sample, temperature=None, draft_p=None, u_accept=None):
+        import torch
+        R, V = logits.shape
+        if logits.dtype not in (torch.bfloat16, torch.float32) or logits.stride(1) != 1:
+            raise ValueError("logits: bfloat16 or float32 [R][vocab] with contiguous elements wanted")
+        _want(u_sample, torch.float32, (R,), "u_sample")
+        if temperature is not None:
+            _want(temperature, torch.float32, (None,), "temperature")
+        if draft_p is not None:
+            if draft_p.dtype != torch.float32 or draft_p.shape != logits.shape or draft_p.stride(1) != 1:
+                raise ValueError("draft_p: float32 [R][vocab] with contiguous elements wanted")
+            if u_accept is None:
+                raise ValueError("draft_p needs u_accept")
+        if u_accept is not None:
+            _want(u_accept, torch.float32, (R,), "u_accept")
+        self.logits, self.u_sample, self.temperature, self.draft_p, self.u_accept = \
+            logits, u_sample, temperature, draft_p, u_accept
+        row = lambda t: t.stride(0) if R > 1 else max(t.stride(0), V)
+        self.c = SamplingC(logits.data_ptr(), int(logits.dtype == torch.float32), V, row(logits), _dp(temperature),
+                           _dp(draft_p), row(draft_p) if draft_p is not None else 0, _dp(u_accept), _dp(u_sample))
+        self.ref = C.byref(self.c)
+
+    def _fits(self, tree, n_req):
+        if self.logits.shape[0] < tree.c.R or (self.temperature is not None and self.temperature.shape[0] < n_req):
+            raise ValueError("logits: a row for every row of the tree wanted, and a temperature for every request")
+
+
+def w12_tree_sample(dist: SampleRows, tree: DeviceTree, n_req: int, ws: Workspace, row_tok=None, row_logp=None,
+                    stream=None):
+    """One token per tree row, distributed as the target's probabilities
+    there -> int32 [R]; its log-probability to ``row_logp`` (float32 [R])."""
+    import torch
+    dist._fits(tree, n_req)
+    if row_tok is None:
+        row_tok = torch.empty(tree.c.R, dtype=torch.int32, device=dist.logits.device)
+    _check(lib().w12_tree_sample(dist.ref, C.byref(tree.c), n_req, row_tok.data_ptr(), _dp(row_logp), ws.ptr,
+                                 ws.nbytes, _stream(stream)), "w12_tree_sample")
+    return row_tok
+
+
+def w12_tree_verify_sampled(dist: SampleRows, tree: DeviceTree, n_req: int, p_max: int, ws: Workspace, row_tok=None,
+                            row_logp=None, acc_tok=None, acc_len=None, acc_node=None, stream=None):
+    """``w12_tree_sample`` and the acceptance of the children that carry their
+    parent's token -> acc_tok, acc_len, acc_node."""
+    import torch
+    dist._fits(tree, n_req)
+    new = lambda *s: torch.empty(s, dtype=torch.int32, device=dist.logits.device)
+    row_tok = row_tok if row_tok is not None else new(tree.c.R)
+    acc_tok = acc_tok if acc_tok is not None else new(n_req, p_max + 1)
+    acc_len = acc_len if acc_len is not None else new(n_req)
+    acc_node = acc_node if acc_node is not None else new(n_req)
+    _check(lib().w12_tree_verify_sampled(dist.ref, C.byref(tree.c), n_req, p_max, row_tok.data_ptr(), _dp(row_logp),
+                                         acc_tok.data_ptr(), acc_len.data_ptr(), acc_node.data_ptr(), ws.ptr,
+                                         ws.nbytes, _stream(stream)), "w12_tree_verify_sampled")
+    return acc_tok, acc_len, acc_node
 
 
 def debug_set(flags: int = 0, timeout_ns: int = 0):

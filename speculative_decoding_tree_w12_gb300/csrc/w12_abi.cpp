@@ -148,6 +148,7 @@ struct Ws {
     uint8_t *base;
     WsLayout L;
     int32_t *status() const { return reinterpret_cast<int32_t *>(base + L.status); }
+    int32_t *arrive() const { return reinterpret_cast<int32_t *>(base + L.arrive); }
     int64_t *mismatch() const { return reinterpret_cast<int64_t *>(base + L.status + 64); }
     int32_t *counters(int slot) const
     {
@@ -197,6 +198,8 @@ WsLayout layout_for(int32_t R, int64_t max_n, int64_t vocab, int32_t n_req)
     size_t o = 0;
     L.status = o;
     o += 256;
+    L.arrive = o;
+    o += static_cast<size_t>(kMaxBudget) * 4;
     // the chain words end exactly where the counters start
     L.grid = o;
     o += static_cast<size_t>(kGridWords) * 4;
@@ -852,6 +855,227 @@ w12_status w12_tlv_splice(const w12_tree *t1, const int32_t *c_tok, const int32_
     a.score = out->score;
     a.status = W.status();
     return cuda_status(launch_tlv_splice(a, stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// paged 8-bit KV cache, tree attention, sampled verification
+// ---------------------------------------------------------------------------
+
+namespace {
+
+w12_status cache_ok(const w12_kv_cache *c, int32_t n_req)
+{
+    if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->block_table || !c->len) return W12_E_INVAL;
+    if (n_req < 1 || c->n_kv_heads < 1 || c->n_blocks < 1 || c->max_blocks < 1) return W12_E_INVAL;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return W12_E_INVAL;
+    if (c->head_dim != kKvDim || n_req > kMaxBudget || c->n_kv_heads > 1024) return W12_E_UNSUPPORTED;
+    if (c->block_tokens != 32 && c->block_tokens != 64 && c->block_tokens != 128) return W12_E_UNSUPPORTED;
+    // rows and positions are 32-bit numbers in the kernels and in the tensor maps
+    if ((int64_t)c->n_blocks * c->n_kv_heads > INT32_MAX / c->block_tokens) return W12_E_UNSUPPORTED;
+    if (c->max_blocks > INT32_MAX / c->block_tokens - 1) return W12_E_UNSUPPORTED;
+    return W12_OK;
+}
+
+w12_status rope_ok(const w12_rope *r, RopeArgs &a)
+{
+    a = RopeArgs{};
+    if (!r || r->rot_dim == 0) return W12_OK;
+    if (r->rot_dim < 0 || r->rot_dim % 2 || r->max_pos < 1 || !r->cos || !r->sin) return W12_E_INVAL;
+    if (r->rot_dim > kKvDim) return W12_E_UNSUPPORTED;
+    a.cos = r->cos;
+    a.sin = r->sin;
+    a.rot = r->rot_dim;
+    a.adjacent = r->adjacent != 0;
+    a.max_pos = r->max_pos;
+    return W12_OK;
+}
+
+// rows of `width` BF16 values: 16-byte aligned, `stride` elements apart
+bool rows_ok(const uint16_t *x, int64_t stride, int64_t width)
+{
+    return x && aligned(x, 16) && stride >= width && stride % 8 == 0;
+}
+
+w12_status kv_entry(const w12_kv_cache *c, const w12_rope *rope, int32_t n_req, const uint16_t *k, int64_t k_stride,
+                    const uint16_t *v, int64_t v_stride, int32_t n_rows, const int32_t *off, const int32_t *parent,
+                    const int32_t *acc_node, int32_t *len_out, void *ws, size_t ws_bytes, w12_stream_t stream)
+{
+    w12_status s = cache_ok(c, n_req);
+    if (s != W12_OK) return s;
+    KvArgs a{};
+    if ((s = rope_ok(rope, a.rope)) != W12_OK) return s;
+    const int64_t width = (int64_t)c->n_kv_heads * kKvDim;
+    if (n_rows < 0 || !off || !len_out) return W12_E_INVAL;
+    if (n_rows > 0 && (!rows_ok(k, k_stride, width) || !rows_ok(v, v_stride, width))) return W12_E_INVAL;
+    const WsLayout L = layout_for(1, 0, 0, n_req);
+    if ((s = ws_check(ws, ws_bytes, L)) != W12_OK) return s;
+    Ws W{static_cast<uint8_t *>(ws), L};
+    a.H = c->n_kv_heads;
+    a.bt = c->block_tokens;
+    a.n_blocks = c->n_blocks;
+    a.max_blocks = c->max_blocks;
+    a.n_req = n_req;
+    a.n_rows = n_rows;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.kc = c->k;
+    a.vc = c->v;
+    a.ks = c->k_scale;
+    a.vs = c->v_scale;
+    a.table = c->block_table;
+    a.len = c->len;
+    a.off = off;
+    a.parent = parent;
+    a.acc_node = acc_node;
+    a.k = k;
+    a.v = v;
+    a.len_out = len_out;
+    a.arrive = W.arrive();
+    a.status = W.status();
+    return cuda_status(launch_kv_write(a, stream));
+}
+
+w12_status sample_entry(const w12_sampling *d, const w12_tree *tree, int32_t n_req, int32_t p_max, int32_t *row_tok,
+                        float *row_logp, int32_t *acc_tok, int32_t *acc_len, int32_t *acc_node, void *ws,
+                        size_t ws_bytes, w12_stream_t stream)
+{
+    w12_status s = tree_ok(tree, true);
+    if (s != W12_OK) return s;
+    if (!tree->req || !d || !d->logits || !d->u_sample || !row_tok || n_req < 1 || p_max < 0) return W12_E_INVAL;
+    if (d->draft_p && !d->u_accept) return W12_E_INVAL;
+    if (d->vocab < 1 || d->logits_stride < d->vocab || (d->draft_p && d->draft_stride < d->vocab)) return W12_E_INVAL;
+    if (!aligned(d->logits, d->logits_f32 ? 4 : 2) || !aligned(d->draft_p, 4)) return W12_E_INVAL;
+    if (n_req > kMaxBudget || p_max > kMaxDepth || d->vocab > sample_max_vocab()) return W12_E_UNSUPPORTED;
+    const WsLayout L = layout_for(1, 0, 0, n_req);
+    if ((s = ws_check(ws, ws_bytes, L)) != W12_OK) return s;
+    Ws W{static_cast<uint8_t *>(ws), L};
+    SampleArgs a{};
+    a.logits = d->logits;
+    a.f32 = d->logits_f32 != 0;
+    a.stride = d->logits_stride;
+    a.vocab = d->vocab;
+    a.temperature = d->temperature;
+    a.draft_p = d->draft_p;
+    a.draft_stride = d->draft_stride;
+    a.u_accept = d->u_accept;
+    a.u_sample = d->u_sample;
+    a.R = tree->R;
+    a.n_req = n_req;
+    a.p_max = p_max;
+    a.parent = tree->parent;
+    a.token = tree->token;
+    a.req = tree->req;
+    a.off = tree->req_row_off;
+    a.row_tok = row_tok;
+    a.row_logp = row_logp;
+    a.acc_tok = acc_tok;
+    a.acc_len = acc_len;
+    a.acc_node = acc_node;
+    a.status = W.status();
+    return cuda_status(launch_sample(a, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+w12_status w12_kv_append(const w12_kv_cache *cache, const w12_rope *rope, int32_t n_req, const uint16_t *k,
+                         int64_t k_stride, const uint16_t *v, int64_t v_stride, int32_t n_rows,
+                         const int32_t *row_off, int32_t *len_out, void *ws, size_t ws_bytes, w12_stream_t stream)
+{
+    return kv_entry(cache, rope, n_req, k, k_stride, v, v_stride, n_rows, row_off, nullptr, nullptr, len_out, ws,
+                    ws_bytes, stream);
+}
+
+w12_status w12_kv_commit(const w12_kv_cache *cache, const w12_rope *rope, const w12_tree *tree, int32_t n_req,
+                         const int32_t *acc_node, const uint16_t *k, int64_t k_stride, const uint16_t *v,
+                         int64_t v_stride, int32_t *len_out, void *ws, size_t ws_bytes, w12_stream_t stream)
+{
+    w12_status s = tree_ok(tree, true);
+    if (s != W12_OK) return s;
+    if (!acc_node) return W12_E_INVAL;
+    return kv_entry(cache, rope, n_req, k, k_stride, v, v_stride, tree->R, tree->req_row_off, tree->parent, acc_node,
+                    len_out, ws, ws_bytes, stream);
+}
+
+size_t w12_attn_workspace_bytes(int32_t R, int32_t n_heads, int32_t n_kv_heads, int32_t n_req)
+{
+    if (R < 1 || R > kMaxBudget || n_req < 1 || n_req > kMaxBudget) return 0;
+    if (n_kv_heads < 1 || n_heads < n_kv_heads || n_heads % n_kv_heads || n_heads / n_kv_heads > kMaxGroup) return 0;
+    if (n_kv_heads > 1024) return 0;
+    return attn_ws_bytes(R, n_heads, n_kv_heads, n_req, kMaxCtas);
+}
+
+w12_status w12_tree_attention(const w12_kv_cache *cache, const w12_rope *rope, const w12_tree *tree, int32_t n_req,
+                              int32_t n_heads, const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                              int64_t k_stride, const uint16_t *v, int64_t v_stride, float scale, uint16_t *out,
+                              void *ws, size_t ws_bytes, void *aws, size_t aws_bytes, w12_stream_t stream)
+{
+    w12_status s = tree_ok(tree, true);
+    if (s != W12_OK) return s;
+    if ((s = cache_ok(cache, n_req)) != W12_OK) return s;
+    AttnArgs a{};
+    if ((s = rope_ok(rope, a.rope)) != W12_OK) return s;
+    const int32_t H = cache->n_kv_heads;
+    if (!tree->req || !out || !aligned(out, 16) || n_heads < H || n_heads % H) return W12_E_INVAL;
+    if (!(scale > 0.f) || scale > 1e30f) return W12_E_INVAL;
+    if (n_heads / H > kMaxGroup) return W12_E_UNSUPPORTED;
+    const int64_t width = (int64_t)H * kKvDim;
+    if (!rows_ok(q, q_stride, (int64_t)n_heads * kKvDim) || !rows_ok(k, k_stride, width) || !rows_ok(v, v_stride, width))
+        return W12_E_INVAL;
+    const WsLayout L = layout_for(1, 0, 0, n_req);
+    if ((s = ws_check(ws, ws_bytes, L)) != W12_OK) return s;
+    if (!aws || !aligned(aws, 256) || aws_bytes < w12_attn_workspace_bytes(tree->R, n_heads, H, n_req))
+        return W12_E_WORKSPACE;
+    Ws W{static_cast<uint8_t *>(ws), L};
+    a.H = H;
+    a.Hq = n_heads;
+    a.bt = cache->block_tokens;
+    a.n_blocks = cache->n_blocks;
+    a.max_blocks = cache->max_blocks;
+    a.n_req = n_req;
+    a.R = tree->R;
+    a.num_sms = num_sms();
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.kc = cache->k;
+    a.vc = cache->v;
+    a.ks = cache->k_scale;
+    a.vs = cache->v_scale;
+    a.table = cache->block_table;
+    a.len = cache->len;
+    a.off = tree->req_row_off;
+    a.parent = tree->parent;
+    a.req = tree->req;
+    a.depth = tree->depth;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.scale = scale;
+    a.out = out;
+    a.work = aws;
+    a.status = W.status();
+    a.timeout_ns = g_timeout_ns;
+    return cuda_status(launch_attn(a, stream));
+}
+
+int64_t w12_sample_max_vocab(void) { return sample_max_vocab(); }
+
+w12_status w12_tree_sample(const w12_sampling *dist, const w12_tree *tree, int32_t n_req, int32_t *row_tok,
+                           float *row_logp, void *ws, size_t ws_bytes, w12_stream_t stream)
+{
+    return sample_entry(dist, tree, n_req, 0, row_tok, row_logp, nullptr, nullptr, nullptr, ws, ws_bytes, stream);
+}
+
+w12_status w12_tree_verify_sampled(const w12_sampling *dist, const w12_tree *tree, int32_t n_req, int32_t p_max,
+                                   int32_t *row_tok, float *row_logp, int32_t *acc_tok, int32_t *acc_len,
+                                   int32_t *acc_node, void *ws, size_t ws_bytes, w12_stream_t stream)
+{
+    if (!acc_tok || !acc_len) return W12_E_INVAL;
+    return sample_entry(dist, tree, n_req, p_max, row_tok, row_logp, acc_tok, acc_len, acc_node, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

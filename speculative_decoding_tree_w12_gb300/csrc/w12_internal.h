@@ -26,6 +26,7 @@ constexpr int32_t kDevOk = 0;
 // Byte layout of the caller's workspace.  Every region is 256-byte aligned.
 struct WsLayout {
     size_t status;        // int32[64]: [0] status, [1] detail, [8] mismatch count (int64)
+    size_t arrive;        // int32[kMaxBudget]: per-request arrival counters of the KV cache writer (zero between calls)
     size_t grid;          // uint32[kGridWords]: [0] abort word of a GEMM chain, [1 + j] CTAs done with GEMM j
     size_t counters;      // int32[kGemmSlots][max_tiles_n]: split-tile arrival counters
     size_t partial;       // float[kGemmSlots][max_ctas][2][rows8][128]
@@ -175,6 +176,64 @@ struct SpliceArgs {
     int32_t *status;
 };
 int launch_tlv_splice(const SpliceArgs &a, void *stream);
+
+// paged 8-bit KV cache (k_kv.cu) and tree attention over it (k_attn.cu)
+constexpr int kKvDim = 128;         // head dimension
+constexpr int kMaxGroup = 64;       // query heads of one key/value head
+struct RopeArgs {
+    const float *cos, *sin;         // [max_pos][rot / 2]
+    int32_t rot, adjacent, max_pos; // rot = 0: no rotation
+};
+struct KvArgs {
+    int32_t H, bt, n_blocks, max_blocks, n_req, n_rows;
+    int64_t k_stride, v_stride;     // elements between rows
+    uint8_t *kc, *vc;
+    float *ks, *vs;
+    const int32_t *table, *len, *off;
+    const int32_t *parent, *acc_node;   // commit: both set; append: null
+    const uint16_t *k, *v;
+    RopeArgs rope;
+    int32_t *len_out, *arrive, *status;
+};
+int launch_kv_write(const KvArgs &a, void *stream);
+
+struct AttnArgs {
+    int32_t H, Hq, bt, n_blocks, max_blocks, n_req, R;
+    int num_sms;
+    int64_t q_stride, k_stride, v_stride;
+    const uint8_t *kc, *vc;
+    const float *ks, *vs;
+    const int32_t *table, *len, *off, *parent, *req;
+    const uint8_t *depth;
+    const uint16_t *q, *k, *v;
+    RopeArgs rope;
+    float scale;
+    uint16_t *out;                  // [R][Hq][kKvDim] BF16
+    void *work;                     // attn_ws_bytes
+    int32_t *status;
+    uint64_t timeout_ns;
+};
+size_t attn_ws_bytes(int32_t R, int32_t Hq, int32_t H, int32_t n_req, int num_sms);
+int launch_attn(const AttnArgs &a, void *stream);
+
+// sampled verification (k_sample.cu)
+struct SampleArgs {
+    const void *logits;
+    int32_t f32;
+    int64_t stride, vocab;          // elements between rows; tokens
+    const float *temperature;       // [n_req] or null (1)
+    const float *draft_p;           // [R][vocab] or null
+    int64_t draft_stride;
+    const float *u_accept, *u_sample;
+    int32_t R, n_req, p_max;
+    const int32_t *parent, *token, *req, *off;
+    int32_t *row_tok;
+    float *row_logp;
+    int32_t *acc_tok, *acc_len, *acc_node;   // acc_tok null: rows only
+    int32_t *status;
+};
+int64_t sample_max_vocab();
+int launch_sample(const SampleArgs &a, void *stream);
 
 int launch_tree_accept(const int32_t *parent, const int32_t *token, const uint8_t *depth,
                        const int32_t *req_row_off, int32_t R, int32_t n_req, int32_t p_max, const int32_t *argmax,

@@ -1,0 +1,75 @@
+// Device helpers of the 8-bit KV cache: E4M3 codes, block scales, the position
+// rotation.  Shared by the cache writer and the tree attention.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "w12_internal.h"
+
+namespace w12d {
+
+__device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+// two floats -> two E4M3 codes (round to nearest even; |x| <= 448 here, NaN -> NaN), `lo` in the low byte
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
+{
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// A value that is not finite has no code under a finite scale: it is stored as NaN.
+__device__ __forceinline__ uint8_t to_e4m3(float x)
+{
+    if (fabsf(x) == INFINITY) x = __int_as_float(0x7FC00000);
+    return (uint8_t)(to_e4m3x2(x, 0.f) & 0xFFu);
+}
+
+// two E4M3 codes -> f16x2 (exact: every E4M3 value is an f16 value)
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)codes));
+    return d;
+}
+
+__device__ __forceinline__ float e4m3_f32(uint8_t code)
+{
+    float f;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(e4m3x2_f16x2(code)));
+    return f;
+}
+
+// The least power of two s with top <= 448 s, not under 2^-32 (a block of
+// zeros, or of values so small that their absolute error no longer matters).
+__device__ __forceinline__ float block_scale(float top)
+{
+    const uint32_t u = __float_as_uint(top);
+    const int e = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);   // 448 = 1.75 * 2^8
+    return __uint_as_float((uint32_t)(e < 95 ? 95 : e) << 23);                  // 95: 2^-32
+}
+
+// element d of a row of kKvDim BF16 values, turned by position pos
+__device__ __forceinline__ float rotated(const uint16_t *row, int d, int pos, const w12i::RopeArgs &r)
+{
+    const float x = bf16_f32(row[d]);
+    if (d >= r.rot) return x;
+    const int half = r.rot >> 1;
+    int f, o;
+    bool second;
+    if (r.adjacent) {
+        f = d >> 1;
+        o = d ^ 1;
+        second = d & 1;
+    } else {
+        second = d >= half;
+        f = second ? d - half : d;
+        o = second ? d - half : d + half;
+    }
+    const float c = __ldg(r.cos + (int64_t)pos * half + f), s = __ldg(r.sin + (int64_t)pos * half + f);
+    const float y = bf16_f32(row[o]);
+    return second ? __fadd_rn(__fmul_rn(x, c), __fmul_rn(y, s)) : __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+}
+
+}  // namespace w12d
