@@ -21,11 +21,18 @@
 // products, which is read once per tile whatever the number of queries.
 //   S^T = K Q^T  kind::f8f6f4: K's codes as they lie in the cache; Q in three
 //                E4M3 pieces that add up to twelve significant bits (2^-17 of
-//                the head's largest at least), one product each into the same
-//                accumulators.
-//   O^T = V^T P  kind::f16: V's codes widened to F16 (exact) by a warpgroup of
-//                its own; P in F16, eleven significant bits, scaled so that
+//                the head's largest at least).  Up to kStack columns the
+//                pieces are stacked as further columns (a product costs the
+//                tensor cores its A operand, so one of 48 columns is a third
+//                of three of 16) and added up by the reader; above, each piece
+//                is a product of its own into the same accumulators.
+//   O^T = V^T P  kind::f16: V's codes widened to F16 (exact) by warpgroups of
+//                their own; P in F16, eleven significant bits, scaled so that
 //                there are 2^-18 below a weight of 1 before the subnormals.
+// Two softmax warpgroups take alternate tiles, each with its own scores, P,
+// maxima and sums, so the latencies of one tile's chain (product, reads,
+// exponentials, writes, product) hide behind the other's; they merge at the
+// end of a segment.
 // The maximum is lazy: P refers to a column maximum that is only raised when a
 // score passes it by 2^6 (P stays under F16's top), so the usual tile has no
 // reduction over lanes at all; the same slow path raises the reference of the
@@ -46,20 +53,19 @@ using namespace w12i;
 constexpr int kD = kKvDim;
 constexpr int kPath = kMaxDepth + 1;       // rows of a root path
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kCols = 80;                  // query rows of a segment: shared memory holds three Q pieces and two P tiles of them
 constexpr int kTile = 128;                 // tokens of a tile
-constexpr int kStages = 3;                 // K and V tiles in flight
-constexpr int kScaleRing = 8;              // tiles whose block scales are kept (the producer runs at most 4 ahead of their readers)
+constexpr int kStack = 16;                 // columns up to which Q's pieces are stacked
+constexpr int kMaxCols = 80;               // query columns of a segment, see Shape
+constexpr int kScaleRing = 8;              // tiles whose block scales are kept (the producer runs at most 6 ahead of their readers)
 constexpr int kMaxReq = kMaxBudget;
-constexpr int kThreads = 512;              // warps: 0 producer, 1 MMA, 4-11 softmax, 12-15 V conversion
-constexpr int kSoft = 256;
-constexpr int kChunks = 3;                 // 16-column chunks of one softmax warpgroup (of kCols / 16 in all)
+constexpr int kSoft = 256;                 // softmax threads
 constexpr float kHead = 16.f;              // P of a weight of 1 under the reference scale
 constexpr float kRaise = 6.f;              // a score may pass the column's reference by this (log2) before it is raised
 constexpr float kScaleRaise = 16.f;        // ... and a value scale its reference by this factor: 16 * 2^6 * 16 < 2^15
 
 struct AttnParams {
     int32_t H, Hq, G, bt, n_blocks, max_blocks, n_req, R, ctas;
+    int32_t cols;                           // query columns of a segment at most
     int64_t q_stride, k_stride, v_stride;
     const uint8_t *kc, *vc;
     const float *ks, *vs;
@@ -70,8 +76,8 @@ struct AttnParams {
     float scale2;                           // softmax scale * log2(e)
     uint16_t *out;
     int64_t *plan;                          // [n_req + 1] first tile of every request
-    float *part;                            // [R * Hq + ctas * kCols][kD] sums
-    float2 *ml;                             // [R * Hq + ctas * kCols] maximum (log2), normaliser
+    float *part;                            // [R * Hq + ctas * cols][kD] sums
+    float2 *ml;                             // [R * Hq + ctas * cols] maximum (log2), normaliser
     int32_t *status;
     uint64_t timeout_ns;
 };
@@ -79,10 +85,10 @@ struct AttnParams {
 __device__ __forceinline__ void fail(int32_t *status) { atomicCAS(status, 0, (int32_t)W12_E_INVAL); }
 
 // rows of a request's groups: as many as fit the columns, evenly
-__host__ __device__ __forceinline__ int group_count(int rows, int G) { return (rows + kCols / G - 1) / (kCols / G); }
-__device__ __forceinline__ int group_rows(int rows, int G)
+__device__ __forceinline__ int group_count(int rows, int fit) { return (rows + fit - 1) / fit; }
+__device__ __forceinline__ int group_rows(int rows, int fit)
 {
-    const int g = group_count(rows, G);
+    const int g = group_count(rows, fit);
     return (rows + g - 1) / g;
 }
 
@@ -107,41 +113,65 @@ __device__ __forceinline__ int request_of(const AttnParams &p, int row)
     return r;
 }
 
-// four consecutive elements d0 .. d0 + 3 of a BF16 row, turned by position pos
-__device__ __forceinline__ void rotated4(const uint16_t *row, int d0, int pos, const RopeArgs &r, float (&x)[4])
+// Four consecutive elements d0 .. d0 + 3 of a BF16 row and what turns them by
+// position pos; loaded apart from the arithmetic, so that the loads of several
+// rows are in flight together.
+struct Raw4 {
+    uint2 w, v;                             // the elements, their partners
+    float c[4], s[4];
+};
+
+__device__ __forceinline__ void load4(Raw4 &x, const uint16_t *row, int d0, int pos, const RopeArgs &r)
 {
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(row + d0));
-    x[0] = bf16_f32((uint16_t)w.x);
-    x[1] = bf16_f32((uint16_t)(w.x >> 16));
-    x[2] = bf16_f32((uint16_t)w.y);
-    x[3] = bf16_f32((uint16_t)(w.y >> 16));
-    if (d0 >= r.rot) return;
-    if (r.rot & 7) {                        // pairs that cross the groups of four
+    x.w = __ldg(reinterpret_cast<const uint2 *>(row + d0));
+    x.v = make_uint2(0, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = rotated(row, d0 + i, pos, r);
-        return;
-    }
+    for (int i = 0; i < 4; ++i) x.c[i] = 1.f, x.s[i] = 0.f;
+    if (d0 >= r.rot) return;
     const int half = r.rot >> 1;
     const float *ct = r.cos + (int64_t)pos * half, *st = r.sin + (int64_t)pos * half;
     if (r.adjacent) {
+        x.v = make_uint2((x.w.x >> 16) | (x.w.x << 16), (x.w.y >> 16) | (x.w.y << 16));
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            const float c = __ldg(ct + ((d0 + i) >> 1)), s = __ldg(st + ((d0 + i) >> 1));
-            const float a = x[i], b = x[i + 1];
-            x[i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-            x[i + 1] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-        }
+        for (int i = 0; i < 4; ++i)
+            if (d0 + i < r.rot) x.c[i] = __ldg(ct + ((d0 + i) >> 1)), x.s[i] = __ldg(st + ((d0 + i) >> 1));
+            else if (i & 2) x.v.y = 0;      // rot ends in the middle of the four
         return;
     }
-    const bool second = d0 >= half;
-    const int f = second ? d0 - half : d0, o = second ? d0 - half : d0 + half;
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + o));
-    const float y[4] = {bf16_f32((uint16_t)v.x), bf16_f32((uint16_t)(v.x >> 16)), bf16_f32((uint16_t)v.y),
-                        bf16_f32((uint16_t)(v.y >> 16))};
+    if (r.rot & 7) {                        // partners that straddle the groups of four
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = d0 + i;
+            y[i] = 0;
+            if (d < r.rot) {
+                const int f = d < half ? d : d - half;
+                y[i] = row[d < half ? d + half : d - half];
+                x.c[i] = __ldg(ct + f), x.s[i] = __ldg(st + f);
+            }
+        }
+        x.v = make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
+        return;
+    }
+    const int f = d0 < half ? d0 : d0 - half;
+    x.v = __ldg(reinterpret_cast<const uint2 *>(row + (d0 < half ? d0 + half : d0 - half)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.c[i] = __ldg(ct + f + i), x.s[i] = __ldg(st + f + i);
+}
+
+__device__ __forceinline__ void turn4(const Raw4 &r, int d0, const RopeArgs &rope, float (&x)[4])
+{
+    x[0] = bf16_f32((uint16_t)r.w.x);
+    x[1] = bf16_f32((uint16_t)(r.w.x >> 16));
+    x[2] = bf16_f32((uint16_t)r.w.y);
+    x[3] = bf16_f32((uint16_t)(r.w.y >> 16));
+    const float y[4] = {bf16_f32((uint16_t)r.v.x), bf16_f32((uint16_t)(r.v.x >> 16)), bf16_f32((uint16_t)r.v.y),
+                        bf16_f32((uint16_t)(r.v.y >> 16))};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float c = __ldg(ct + f + i), s = __ldg(st + f + i);
-        x[i] = second ? __fadd_rn(__fmul_rn(x[i], c), __fmul_rn(y[i], s)) : __fsub_rn(__fmul_rn(x[i], c), __fmul_rn(y[i], s));
+        const bool second = rope.adjacent ? (i & 1) : d0 + i >= (rope.rot >> 1);
+        const float a = __fmul_rn(x[i], r.c[i]), b = __fmul_rn(y[i], r.s[i]);
+        x[i] = second ? __fadd_rn(a, b) : __fsub_rn(a, b);
     }
 }
 
@@ -149,34 +179,58 @@ __device__ __forceinline__ void rotated4(const uint16_t *row, int d0, int pos, c
 // the cached context
 // ---------------------------------------------------------------------------
 
-struct Shared {
-    uint64_t full[kStages], empty[kStages];            // K and V tile loaded / both consumed
-    uint64_t s_full[2], s_empty[2];                    // scores in tensor memory / read
-    uint64_t p_full[2], pv_done[2];                    // weights in shared memory / their product added
-    uint64_t q_full, v_full, drain;
-    int64_t pre[kMaxReq + 1];                          // first tile of every request
-    int64_t wsum[kThreads / 32];
-    float2 scale[kScaleRing][kTile / 32];              // K and V scale of a tile's blocks
-    float cf[kCols], mref[kCols], delta[kCols];        // score factor, reference maximum, its last raise (log2)
-    float red[8][kCols];                               // per softmax warp
-    uint32_t tmem;
-    int32_t abort;
+// What a launch is compiled for: the query columns of a segment.  A request
+// with more gets several groups of rows, each reading the context again (from
+// L2, side by side), so any shape serves any tree; the host picks the least
+// one that holds an average request's.  Fewer columns leave shared memory for
+// more tiles in flight and registers for more converting warps.
+template <int kCols>
+struct Shape {
+    static constexpr int kChunks = kCols / 16;
+    static constexpr bool kStacked = kCols <= kStack;
+    static constexpr int kConv = kCols <= 48 ? 2 : 1;            // warpgroups widening V
+    static constexpr int kThreads = 128 + kSoft + kConv * 128;   // warps: 0 producer, 1 MMA, 4-11 softmax, 12- conversion
+    static constexpr int kStK = kCols <= 16 ? 4 : 3;             // K tiles in flight
+    static constexpr int kStV = kCols <= 16 ? 4 : kCols <= 48 ? 3 : 2;
+    static constexpr int kKBytes = kTile * kD;                   // one K or V tile: 16 KB
+    static constexpr int kPBytes = kCols * kTile * 2;
+    static constexpr int kQBytes = kCols * kD;
+    static constexpr int kOffK = 0;
+    static constexpr int kOffV = kOffK + kStK * kKBytes;
+    static constexpr int kOffV16 = kOffV + kStV * kKBytes;       // [2][2 token halves][128 d][64 tokens] F16
+    static constexpr int kOffP = kOffV16 + 4 * kKBytes;          // [2][kCols / 16 slabs][128 tokens][16] F16
+    static constexpr int kOffQ = kOffP + 2 * kPBytes;            // [3 pieces][kCols][128] E4M3
+    static constexpr int kOffShared = kOffQ + 3 * kQBytes;
 };
 
-constexpr int kKBytes = kTile * kD;                    // one K or V tile: 16 KB
-constexpr int kOffK = 0;
-constexpr int kOffV = kOffK + kStages * kKBytes;
-constexpr int kOffV16 = kOffV + kStages * kKBytes;     // [2 token halves][128 d][64 tokens] F16
-constexpr int kOffP = kOffV16 + 2 * kKBytes;           // [2][kCols / 16 slabs][128 tokens][16] F16
-constexpr int kPBytes = kCols * kTile * 2;
-constexpr int kOffQ = kOffP + 2 * kPBytes;             // [3 pieces][kCols][128] E4M3
-constexpr int kQBytes = kCols * kD;
-constexpr int kOffShared = kOffQ + 3 * kQBytes;
-constexpr int kSmem = kOffShared + (int)sizeof(Shared) + 1024;
-static_assert(kPBytes % 1024 == 0 && kQBytes % 1024 == 0, "operand tiles keep their swizzle atoms aligned");
-static_assert(kSmem <= 227 * 1024, "one CTA per SM");
+struct Shared {
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];   // K and V tiles loaded / consumed
+    uint64_t s_full[2], s_empty[2];                    // scores in tensor memory / read
+    uint64_t p_full[2], v16_full[2], pv_done[2];       // weights and widened values in shared memory / their product added
+    uint64_t q_full, drain;
+    int64_t pre[kMaxReq + 1];                          // first tile of every request
+    int64_t wsum[24];
+    alignas(16) float cf[kMaxCols];                    // score factor of a column
+    alignas(16) float mref[2][kMaxCols];               // per warpgroup: reference maximum, its last raise (log2)
+    alignas(16) float delta[2][kMaxCols];
+    float lsum[2][kMaxCols], red[8][kMaxCols];         // normalisers; per softmax warp
+    float2 scale[kScaleRing][kTile / 32];              // K and V scale of a tile's blocks
+    float top_v[kScaleRing];                           // the largest of the V scales
+    float back[2];
+    uint32_t tmem;
+    int32_t abort;
+    int32_t k_asked;                                   // the producer's last K tile
+};
 
-constexpr uint32_t kTmS = 0, kTmO = 256, kTmCols = 512;   // scores at columns 0 and 128, sums at 256
+template <int kCols>
+constexpr int smem_bytes()
+{
+    return Shape<kCols>::kOffShared + (int)sizeof(Shared) + 1024;
+}
+static_assert(smem_bytes<16>() <= 227 * 1024 && smem_bytes<48>() <= 227 * 1024 && smem_bytes<80>() <= 227 * 1024,
+              "one CTA per SM");
+
+constexpr uint32_t kTmO = 256, kTmCols = 512;             // scores at columns 0 and 128, sums at 256 and 384
 
 // a stretch of tiles t0 .. t1 - 1 of one segment
 struct Seg {
@@ -198,7 +252,7 @@ __device__ __forceinline__ Seg segment(const AttnParams &p, const int64_t *pre, 
     s.rows = p.off[a + 1] - s.lo;
     s.len = p.len[a];
     const int nt = (s.len + kTile - 1) / kTile;
-    const int g = group_count(s.rows, p.G), per = group_rows(s.rows, p.G);
+    const int fit = p.cols / p.G, g = group_count(s.rows, fit), per = group_rows(s.rows, fit);
     const int64_t i = at - pre[a];
     const int seg = (int)(i / nt);
     s.t0 = (int)(i % nt);
@@ -263,23 +317,26 @@ __device__ __forceinline__ float reduce16(const float *x, int lane)
     return kMax ? fmaxf(v[0], o) : v[0] + o;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kCols>
+__global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
     k_attn_ctx(const __grid_constant__ CUtensorMap kmap, const AttnParams p)
 {
+    typedef Shape<kCols> T;
     extern __shared__ uint8_t raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    Shared &s = *reinterpret_cast<Shared *>(sm + kOffShared);
+    Shared &s = *reinterpret_cast<Shared *>(sm + T::kOffShared);
     const uint32_t base = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cta = blockIdx.x;
     auto bar = [&](const uint64_t &b) { return smem_u32(&b); };
 
     // ---- the tile list: tiles of every request, summed up
+    const int fit = kCols / p.G;
     int64_t mine = 0;
     if (tid < p.n_req) {
         int lo, rows, len;
         if (request_ok(p, tid, lo, rows, len))
-            mine = rows ? (int64_t)((len + kTile - 1) / kTile) * p.H * group_count(rows, p.G) : 0;
+            mine = rows ? (int64_t)((len + kTile - 1) / kTile) * p.H * group_count(rows, fit) : 0;
         else
             fail(p.status);
     }
@@ -292,18 +349,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) s.wsum[warp] = incl;
     if (tid == 0) {
         s.abort = 0;
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(bar(s.full[i]), 1);
-            mbar_init(bar(s.empty[i]), 2);               // scores computed, values widened
+        s.k_asked = -1;
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(s.k_full[i]), 1);
+            mbar_init(bar(s.k_empty[i]), 1);
+            mbar_init(bar(s.v_full[i]), 1);
+            mbar_init(bar(s.v_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(s.s_full[i]), 1);
-            mbar_init(bar(s.s_empty[i]), kSoft / 32);
-            mbar_init(bar(s.p_full[i]), kSoft / 32);
+            mbar_init(bar(s.s_empty[i]), 4);
+            mbar_init(bar(s.p_full[i]), 4);
+            mbar_init(bar(s.v16_full[i]), 1);
             mbar_init(bar(s.pv_done[i]), 1);
         }
         mbar_init(bar(s.q_full), kSoft / 32);
-        mbar_init(bar(s.v_full), 1);
         mbar_init(bar(s.drain), 1);
         fence_mbar_init();
         prefetch_tmap(&kmap);
@@ -318,11 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     const int64_t total = s.pre[p.n_req];
-    if (cta == 0 && tid <= p.n_req) p.plan[tid] = s.pre[tid];
-    if (cta == 0 && tid == 0 && p.n_req == kThreads) p.plan[p.n_req] = total;
+    if (cta == 0)
+        for (int i = tid; i <= p.n_req; i += T::kThreads) p.plan[i] = s.pre[i];
     const int64_t share = (total + p.ctas - 1) / p.ctas;
     const int64_t first = min(total, cta * share), end = min(total, first + share);
-    const int nb = kTile / p.bt;                          // blocks of a tile
+    const int bs = p.bt == 32 ? 5 : p.bt == 64 ? 6 : 7;   // log2 of a block's tokens
+    const int nb = kTile >> bs;                           // blocks of a tile
     volatile int32_t *abort = &s.abort;
     const uint64_t to = p.timeout_ns;
 
@@ -334,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int64_t at = first; at < end && ok;) {
             const Seg g = segment(p, s.pre, at, end);
-            const int b0 = g.t0 * nb, b1 = min((g.len + p.bt - 1) / p.bt, g.t1 * nb);
+            const int b0 = g.t0 * nb, b1 = min((g.len + p.bt - 1) >> bs, g.t1 * nb);
             const int32_t *table = p.table + (int64_t)g.r * p.max_blocks;
             int blk = 0;
             float2 sc = make_float2(0.f, 0.f);
@@ -356,24 +417,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int blk2;
                 float2 sc2;
                 fetch(b + 32 + lane, blk2, sc2);
+                float top = sc.y;                             // the tile's largest V scale
+                for (int d = 1; d < nb; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                 for (int l = 0; l < 32 && b + l < b1; l += nb, ++j) {
-                    const int st = j % kStages;
-                    ok = __all_sync(0xffffffffu, j < kStages || mbar_wait(bar(s.empty[st]), (j / kStages - 1) & 1, to,
+                    const int sk = j % T::kStK, sv = j % T::kStV;
+                    const int n = min(nb, b1 - (b + l));      // blocks of this tile that hold tokens
+                    const bool in = lane >= l && lane < l + nb, copy = in && lane < l + n;
+                    const int row = (blk * p.H + g.h) << bs;
+                    const uint32_t off = (uint32_t)(lane - l) * (uint32_t)(p.bt * kD), bytes = (uint32_t)(p.bt * kD);
+                    ok = __all_sync(0xffffffffu, j < T::kStK || mbar_wait(bar(s.k_empty[sk]), (j / T::kStK - 1) & 1, to,
                                                                           p.status, abort));
                     if (!ok) break;
-                    const int n = min(nb, b1 - (b + l));      // blocks of this tile that hold tokens
-                    const bool in = lane >= l && lane < l + nb;
                     if (in) s.scale[j % kScaleRing][lane - l] = sc;
+                    if (lane == l) s.top_v[j % kScaleRing] = top;
                     __syncwarp();
-                    if (lane == 0) mbar_expect_tx(bar(s.full[st]), (uint32_t)(n * p.bt * kD * 2));
+                    if (lane == 0) mbar_expect_tx(bar(s.k_full[sk]), n * bytes);
                     __syncwarp();
-                    if (in && lane < l + n) {
-                        const int row = (blk * p.H + g.h) * p.bt;
-                        tma_load_2d(base + kOffK + st * kKBytes + (lane - l) * p.bt * kD, &kmap, 0, row, bar(s.full[st]));
-                        bulk_g2s(base + kOffV + st * kKBytes + (lane - l) * p.bt * kD, p.vc + (int64_t)row * kD,
-                                 (uint32_t)(p.bt * kD), bar(s.full[st]));
-                    }
+                    if (lane == 0) s.k_asked = (int32_t)j;
+                    if (copy) tma_load_2d(base + T::kOffK + sk * T::kKBytes + off, &kmap, 0, row, bar(s.k_full[sk]));
+                    ok = __all_sync(0xffffffffu, j < T::kStV || mbar_wait(bar(s.v_empty[sv]), (j / T::kStV - 1) & 1, to,
+                                                                          p.status, abort));
+                    if (!ok) break;
+                    if (lane == 0) mbar_expect_tx(bar(s.v_full[sv]), n * bytes);
                     __syncwarp();
+                    if (copy)
+                        bulk_g2s(base + T::kOffV + sv * T::kKBytes + off, p.vc + (int64_t)row * kD, bytes, bar(s.v_full[sv]));
                 }
                 blk = blk2;
                 sc = sc2;
@@ -382,51 +450,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) {                                            // copies in flight land before the CTA leaves
             const uint64_t t0 = globaltimer();
-            for (uint32_t i = j > kStages ? j - kStages : 0; i < j; ++i)
-                while (!mbar_try_wait_sleep(bar(s.full[i % kStages]), (i / kStages) & 1, kWaitSleepNs))
+            auto land = [&](const uint64_t &b, uint32_t phase) {
+                while (!mbar_try_wait_sleep(bar(b), phase & 1, kWaitSleepNs))
                     if (globaltimer() - t0 > to) break;
+            };
+            for (uint32_t i = j >= T::kStV ? j - T::kStV : 0; i < j; ++i) land(s.v_full[i % T::kStV], i / T::kStV);
+            for (uint32_t i = j >= T::kStK ? j - T::kStK : 0; i < j; ++i) land(s.k_full[i % T::kStK], i / T::kStK);
+            if (s.k_asked == (int32_t)j) land(s.k_full[j % T::kStK], j / T::kStK);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
         if (lane == 0) {
-            uint32_t j = 0, q = 0;
+            uint32_t j = 0, q = 0, done = 0;                  // tiles scored, segments, tiles multiplied
             bool ok = true;
-            auto pv = [&](uint32_t i, bool fresh, uint32_t idesc) -> bool {
-                const int b = i & 1;
-                if (!mbar_wait(bar(s.p_full[b]), (i >> 1) & 1, to, p.status, abort)) return false;
-                if (!mbar_wait(bar(s.v_full), i & 1, to, p.status, abort)) return false;
-                tc_fence_after();
-                const uint64_t pd = smem_desc_mn_sw32(base + kOffP + b * kPBytes, kTile * 32);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint64_t vd = smem_desc_sw128(base + kOffV16 + (k >> 2) * kKBytes + (k & 3) * 32);
-                    tc_mma_ss_f16(tmem + kTmO, vd, pd + (uint64_t)(k * (512 >> 4)), idesc, !(fresh && k == 0));
-                }
-                tc_commit(bar(s.pv_done[b]));
-                return true;
-            };
             for (int64_t at = first; at < end && ok; ++q) {
                 const Seg g = segment(p, s.pre, at, end);
                 const int n = (g.nrows * p.G + 15) & ~15;
-                const uint32_t i_qk = idesc_e4m3_f32(kTile, n), i_pv = idesc_f16_f32_bmn(kD, n);
+                const uint32_t i_qk = idesc_e4m3_f32(kTile, T::kStacked ? 3 * kCols : n), i_pv = idesc_f16_f32_bmn(kD, n);
+                const uint32_t start = j;
+                auto pv = [&](uint32_t i) -> bool {
+                    const int b = i & 1;
+                    if (!mbar_wait(bar(s.v16_full[b]), (i >> 1) & 1, to, p.status, abort)) return false;
+                    if (!mbar_wait(bar(s.p_full[b]), (i >> 1) & 1, to, p.status, abort)) return false;
+                    tc_fence_after();
+                    const bool fresh = i - start < 2;
+                    const uint64_t pd = smem_desc_mn_sw32(base + T::kOffP + b * T::kPBytes, kTile * 32);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tc_mma_ss_f16(tmem + kTmO + b * 128,
+                                      smem_desc_sw128(base + T::kOffV16 + b * 2 * T::kKBytes + (k >> 2) * T::kKBytes + (k & 3) * 32),
+                                      pd + (uint64_t)(k * (512 >> 4)), i_pv, !(fresh && k == 0));
+                    tc_commit(bar(s.pv_done[b]));
+                    return true;
+                };
                 ok = mbar_wait(bar(s.q_full), q & 1, to, p.status, abort);
                 for (int t = g.t0; t < g.t1 && ok; ++t, ++j) {
-                    const int st = j % kStages, b = j & 1;
-                    ok = mbar_wait(bar(s.full[st]), (j / kStages) & 1, to, p.status, abort) &&
+                    const int st = j % T::kStK, b = j & 1;
+                    ok = mbar_wait(bar(s.k_full[st]), (j / T::kStK) & 1, to, p.status, abort) &&
                          (j < 2 || mbar_wait(bar(s.s_empty[b]), ((j >> 1) - 1) & 1, to, p.status, abort));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < 3; ++c)
+                    for (int c = 0; c < (T::kStacked ? 1 : 3); ++c)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            tc_mma_ss_f8(tmem + kTmS + b * 128, smem_desc_sw128(base + kOffK + st * kKBytes + k * 32),
-                                         smem_desc_sw128(base + kOffQ + c * kQBytes + k * 32), i_qk, c + k > 0);
+                            tc_mma_ss_f8(tmem + b * 128, smem_desc_sw128(base + T::kOffK + st * T::kKBytes + k * 32),
+                                         smem_desc_sw128(base + T::kOffQ + c * T::kQBytes + k * 32), i_qk, c + k > 0);
                     tc_commit(bar(s.s_full[b]));
-                    tc_commit(bar(s.empty[st]));
-                    if (t > g.t0) ok = pv(j - 1, t - 1 == g.t0, i_pv);
+                    tc_commit(bar(s.k_empty[st]));
+                    if (j - done >= 2) ok = pv(done++);
                 }
-                if (ok) ok = pv(j - 1, g.t1 - 1 == g.t0, i_pv);
+                while (ok && done < j) ok = pv(done++);
                 at += g.t1 - g.t0;
             }
             if (!ok) {                                        // products in flight end before tensor memory is freed
@@ -439,30 +513,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= 12) {
         // ------------------------------------------------------------ V to F16
-        const int t128 = tid - 384;
+        const int t128 = (tid - 384) & 127, wg = (tid - 384) >> 7;
         uint32_t j = 0;
         bool ok = true;
-        const int cs = p.bt == 32 ? 1 : p.bt == 64 ? 2 : 3;   // log2 of the 16-token chunks of a row of a block
+        const int cs = bs - 4;                                // log2 of the 16-token chunks of a row of a block
         for (int64_t at = first; at < end && ok;) {
             const Seg g = segment(p, s.pre, at, end);
             for (int t = g.t0; t < g.t1; ++t, ++j) {
-                const int st = j % kStages;
-                ok = mbar_wait(bar(s.full[st]), (j / kStages) & 1, to, p.status, abort) &&
-                     (j < 1 || mbar_wait(bar(s.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, to, p.status, abort));
-                if (bar_or(3, 128, !ok)) {
+                if (T::kConv == 2 && (int)(j & 1) != wg) continue;
+                const int st = j % T::kStV, b = j & 1;
+                ok = mbar_wait(bar(s.v_full[st]), (j / T::kStV) & 1, to, p.status, abort) &&
+                     (j < 2 || mbar_wait(bar(s.pv_done[b]), ((j >> 1) - 1) & 1, to, p.status, abort));
+                if (bar_or(2 + wg, 128, !ok)) {
                     ok = false;
                     break;
                 }
                 const int valid = min(kTile, g.len - t * kTile);
-                const uint8_t *src = sm + kOffV + st * kKBytes;
+                const uint8_t *src = sm + T::kOffV + st * T::kKBytes;
+                uint8_t *to16 = sm + T::kOffV16 + b * 2 * T::kKBytes;
+                uint4 w[8];
+#pragma unroll
+                for (int it = 0; it < 8; ++it) w[it] = *reinterpret_cast<const uint4 *>(src + (it * 128 + t128) * 16);
 #pragma unroll
                 for (int it = 0; it < 8; ++it) {
                     const int i = it * 128 + t128;
                     const int row = i >> cs, d = row & (kD - 1);             // row: (block, d)
-                    const int tok = (row >> 7) * p.bt + (i & ((1 << cs) - 1)) * 16;
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (tok < valid) w = *reinterpret_cast<const uint4 *>(src + i * 16);
-                    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                    const int tok = ((row >> 7) << bs) + (i & ((1 << cs) - 1)) * 16;
+                    uint32_t x[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
                     if (tok + 16 > valid)                                     // what lies past the last token is not a value
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -475,220 +552,269 @@ __global__ void __launch_bounds__(kThreads, 1)
                         y[2 * c] = e4m3x2_f16x2(x[c] & 0xFFFFu);
                         y[2 * c + 1] = e4m3x2_f16x2(x[c] >> 16);
                     }
-                    uint8_t *dst = sm + kOffV16 + (tok >> 6) * kKBytes + d * 128;
+                    uint8_t *dst = to16 + (tok >> 6) * T::kKBytes + d * 128;
                     const int c = (tok & 63) >> 3;
                     *reinterpret_cast<uint4 *>(dst + ((c ^ (d & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
                     *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (d & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
                 }
                 fence_async_shared();
-                named_bar(3, 128);
+                named_bar(2 + wg, 128);
                 if (t128 == 0) {
-                    mbar_arrive(bar(s.empty[st]));
-                    mbar_arrive(bar(s.v_full));
+                    mbar_arrive(bar(s.v_empty[st]));
+                    mbar_arrive(bar(s.v16_full[b]));
                 }
             }
             at += g.t1 - g.t0;
         }
     } else if (warp >= 4) {
-        // ------------------------------------------------------------ softmax
+        // ------------------------------------------------------------ softmax: warpgroup wg takes the tiles j with j % 2 == wg
         const int sw = warp - 4, wg = sw >> 2, quad = warp & 3;
         const int tok = quad * 32 + lane;                     // this thread's token of the tile
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const uint32_t tm_s = tmem + lanes + wg * 128, tm_o = tmem + lanes + kTmO + wg * 128;
+        const float4 *cf4 = reinterpret_cast<const float4 *>(s.cf), *mr4 = reinterpret_cast<const float4 *>(s.mref[wg]);
         uint32_t j = 0;
         bool ok = true;
         for (int64_t at = first; at < end && ok;) {
             const Seg g = segment(p, s.pre, at, end);
-            const int ncol = g.nrows * p.G, npad = (ncol + 15) & ~15;
+            const int ncol = g.nrows * p.G, npad = (ncol + 15) & ~15, nch = npad >> 4;
             // ---- Q: turned, scaled to E4M3's range by a power of two, in three pieces
             named_bar(4, kSoft);                              // the last segment's columns are done with
-            for (int n = sw; n < npad; n += 8) {
-                float x[4] = {0.f, 0.f, 0.f, 0.f};
-                float f = 0.f;
-                if (n < ncol) {
-                    const int row = g.lo + g.row0 + n / p.G;
-                    int pos = g.len + (int)p.depth[row];
-                    if (p.rope.rot && pos >= p.rope.max_pos) {
+            const int n_q = T::kStacked ? kCols : npad;       // stacked pieces are products of all their columns
+#pragma unroll 1
+            for (int n0 = sw; n0 < n_q; n0 += 8 * 2) {
+                Raw4 rw[2];
+                int pos[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int n = min(n0 + 8 * u, ncol - 1);
+                    pos[u] = g.len + (int)__ldg(p.depth + g.lo + g.row0 + n / p.G);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int n = min(n0 + 8 * u, ncol - 1);
+                    if (p.rope.rot && pos[u] >= p.rope.max_pos) {
                         fail(p.status);
-                        pos = 0;
+                        pos[u] = 0;
                     }
-                    rotated4(p.q + row * p.q_stride + (int64_t)(g.h * p.G + n % p.G) * kD, lane * 4, pos, p.rope, x);
+                    load4(rw[u], p.q + (int64_t)(g.lo + g.row0 + n / p.G) * p.q_stride + (int64_t)(g.h * p.G + n % p.G) * kD,
+                          lane * 4, pos[u], p.rope);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int n = n0 + 8 * u;
+                    if (n >= n_q) break;
+                    float x[4];
+                    turn4(rw[u], lane * 4, p.rope, x);
                     float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
                     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                     const float qs = block_scale(top), qi = 1.f / qs;
-                    f = qs * p.scale2;
+                    const bool pad = n >= ncol;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] *= qi;
-                }
-                const uint32_t dst = (uint32_t)(n * kD + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4);
+                    for (int i = 0; i < 4; ++i) x[i] = pad ? 0.f : x[i] * qi;
+                    const uint32_t dst = (uint32_t)(n * kD + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4);
 #pragma unroll
-                for (int c = 0; c < 3; ++c) {
-                    uint32_t w = 0;
+                    for (int c = 0; c < 3; ++c) {
+                        uint32_t w = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t code = to_e4m3(x[i]);
-                        w |= code << (8 * i);
-                        x[i] -= e4m3_f32((uint8_t)code);
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t code = to_e4m3(x[i]);
+                            w |= code << (8 * i);
+                            x[i] -= e4m3_f32((uint8_t)code);
+                        }
+                        *reinterpret_cast<uint32_t *>(sm + T::kOffQ + c * T::kQBytes + dst) = w;
                     }
-                    *reinterpret_cast<uint32_t *>(sm + kOffQ + c * kQBytes + dst) = w;
-                }
-                if (lane == 0) {
-                    s.cf[n] = f;
-                    s.mref[n] = 0.f;
+                    if (lane == 0) {
+                        s.cf[n] = pad ? 0.f : qs * p.scale2;
+                        s.mref[0][n] = 0.f;
+                        s.mref[1][n] = 0.f;
+                    }
                 }
             }
             fence_async_shared();
             named_bar(4, kSoft);
             if (lane == 0) mbar_arrive(bar(s.q_full));
 
-            // ---- tiles; this warpgroup's 16-column chunks: c0 .. c0 + nch - 1
-            const int all = npad >> 4, half = (all + 1) >> 1;
-            const int c0 = wg ? half : 0, nch = wg ? all - half : half;
-            float l[kChunks * 16];
+            float l[kCols];
 #pragma unroll
-            for (int i = 0; i < kChunks * 16; ++i) l[i] = 0.f;
+            for (int i = 0; i < kCols; ++i) l[i] = 0.f;
             float sref = 0.f;
-            for (int t = g.t0; t < g.t1; ++t, ++j) {
-                const int b = j & 1;
-                const bool fresh = t == g.t0;
-                ok = mbar_wait(bar(s.s_full[b]), (j >> 1) & 1, to, p.status, abort);
+            bool fresh = true;
+            const uint32_t j0 = j;
+            j += g.t1 - g.t0;
+            for (uint32_t jj = j0 + ((j0 ^ wg) & 1); jj < j; jj += 2) {
+                const int t = g.t0 + (int)(jj - j0);
+                ok = mbar_wait(bar(s.s_full[wg]), (jj >> 1) & 1, to, p.status, abort);
                 __syncwarp();
                 tc_fence_after();
-                float y[kChunks * 16];
-                uint32_t *yr = reinterpret_cast<uint32_t *>(y);
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-                    if (c < nch) tmem_ld_x16(tmem + lanes + kTmS + b * 128 + (c0 + c) * 16, yr + c * 16);
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(s.s_empty[b]));
-                // the block scales of the tile
-                const float2 *sc = s.scale[j % kScaleRing];
-                const float2 my = sc[tok / p.bt];
-                float top_v = 0.f;
-                for (int i = 0; i < nb; ++i) top_v = fmaxf(top_v, sc[i].y);
-                top_v = fmaxf(top_v, 1e-30f);
+                const float2 my = s.scale[jj % kScaleRing][tok >> bs];
+                const float top_v = fmaxf(s.top_v[jj % kScaleRing], 1e-30f);
                 const bool live = t * kTile + tok < g.len;
-                bool raise = fresh || top_v > kScaleRaise * sref;
+                // 16 columns of scores against their references, in log2 units
+                auto scores = [&](int c, float (&y)[16]) {
+                    uint32_t *r = reinterpret_cast<uint32_t *>(y);
+                    tmem_ld_x16(tm_s + c * 16, r);
+                    if (T::kStacked) {
+                        float y1[16], y2[16];
+                        tmem_ld_x16(tm_s + kCols + c * 16, reinterpret_cast<uint32_t *>(y1));
+                        tmem_ld_x16(tm_s + 2 * kCols + c * 16, reinterpret_cast<uint32_t *>(y2));
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[i] += y1[i] + y2[i];
+                    } else {
+                        tmem_ld_wait();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 f = cf4[c * 4 + (i >> 2)], m = mr4[c * 4 + (i >> 2)];
+                        y[i] = fmaf(y[i], f.x * my.x, -m.x);
+                        y[i + 1] = fmaf(y[i + 1], f.y * my.x, -m.y);
+                        y[i + 2] = fmaf(y[i + 2], f.z * my.x, -m.z);
+                        y[i + 3] = fmaf(y[i + 3], f.w * my.x, -m.w);
+                    }
+                };
                 float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c)
+                for (int c = 0; c < T::kChunks; ++c)
                     if (c < nch) {
+                        float y[16];
+                        scores(c, y);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int n = (c0 + c) * 16 + i;
-                            float v = fmaf(y[c * 16 + i], s.cf[n] * my.x, -s.mref[n]);
-                            v = live ? v : -INFINITY;
-                            y[c * 16 + i] = v;
-                            top = fmaxf(top, v);
-                        }
+                        for (int i = 0; i < 16; ++i) top = fmaxf(top, y[i]);
                     }
-                raise |= top > kRaise;
-                // this tile's P buffer is free once the product of two tiles ago is done
-                if (ok && j >= 2) ok = mbar_wait(bar(s.pv_done[b]), ((j >> 1) - 1) & 1, to, p.status, abort);
-                if (bar_or(5 + wg, 128, raise || !ok)) {
+                // this warpgroup's P and sums are free once its last product is done
+                if (ok && jj >= 2) ok = mbar_wait(bar(s.pv_done[wg]), ((jj >> 1) - 1) & 1, to, p.status, abort);
+                if (bar_or(5 + wg, 128, fresh || top_v > kScaleRaise * sref || (live && top > kRaise) || !ok)) {
                     // ---- raise the references (first tile: set them)
-                    if (ok && !fresh) ok = mbar_wait(bar(s.pv_done[b ^ 1]), ((j - 1) >> 1) & 1, to, p.status, abort);
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
+                    for (int c = 0; c < T::kChunks; ++c)
                         if (c < nch) {
-                            const float m = reduce16<true>(y + c * 16, lane);
+                            float y[16];
+                            scores(c, y);
+                            if (!live)
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) y[i] = -INFINITY;
+                            const float m = reduce16<true>(y, lane);
                             if (lane < 16) s.red[sw][c * 16 + lane_col(lane)] = m;
                         }
                     if (bar_or(5 + wg, 128, !ok)) {
                         ok = false;
                         break;
                     }
-                    if (tok < nch * 16) {
+                    if (tok < npad) {
                         float m = fmaxf(fmaxf(s.red[wg * 4][tok], s.red[wg * 4 + 1][tok]),
                                         fmaxf(s.red[wg * 4 + 2][tok], s.red[wg * 4 + 3][tok]));
                         if (!fresh) m = fmaxf(m, 0.f);
                         if (!(m > -INFINITY)) m = 0.f;
-                        s.delta[c0 * 16 + tok] = m;
-                        s.mref[c0 * 16 + tok] += m;
+                        s.delta[wg][tok] = m;
+                        s.mref[wg][tok] += m;
                     }
                     named_bar(5 + wg, 128);
                     const float ref = fresh || top_v > kScaleRaise * sref ? top_v : sref;
                     const float fs = fresh ? 0.f : sref / ref;
                     sref = ref;
-                    tc_fence_after();
+                    if (!fresh) {
+                        tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
-                        if (c < nch) {
-                            float o[16];
-                            uint32_t *r = reinterpret_cast<uint32_t *>(o);
-                            const uint32_t ta = tmem + lanes + kTmO + (c0 + c) * 16;
-                            if (!fresh) {
-                                tmem_ld_x16(ta, r);
+                        for (int c = 0; c < T::kChunks; ++c)
+                            if (c < nch) {
+                                float o[16];
+                                uint32_t *r = reinterpret_cast<uint32_t *>(o);
+                                tmem_ld_x16(tm_o + c * 16, r);
                                 tmem_ld_wait();
-                            }
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float dl = s.delta[(c0 + c) * 16 + i];
-                                const float f = ex2(-dl);
-                                y[c * 16 + i] -= dl;
-                                l[c * 16 + i] *= f;
-                                o[i] *= f * fs;
+                                for (int i = 0; i < 16; ++i) {
+                                    const float f = ex2(-s.delta[wg][c * 16 + i]);
+                                    l[c * 16 + i] *= f;
+                                    o[i] *= f * fs;
+                                }
+                                tmem_st_x16(tm_o + c * 16, r);
                             }
-                            if (!fresh) tmem_st_x16(ta, r);
-                        }
-                    tmem_st_wait();
-                    tc_fence_before();
+                        tmem_st_wait();
+                        tc_fence_before();
+                    }
                 }
+                fresh = false;
                 // ---- weights
                 const float rt = kHead * (my.y / sref);
-                uint8_t *prow = sm + kOffP + b * kPBytes + tok * 32;
-                const int sw_bit = (tok >> 2) & 1;
+                uint8_t *prow = sm + T::kOffP + wg * T::kPBytes + tok * 32;
+                const int flip = (tok >> 2) & 1;
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c)
+                for (int c = 0; c < T::kChunks; ++c)
                     if (c < nch) {
+                        float y[16];
+                        scores(c, y);
                         uint32_t w[8];
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            const float e0 = ex2(y[c * 16 + i]), e1 = ex2(y[c * 16 + i + 1]);
+                            const float e0 = live ? ex2(y[i]) : 0.f, e1 = live ? ex2(y[i + 1]) : 0.f;
                             l[c * 16 + i] += e0;
                             l[c * 16 + i + 1] += e1;
-                            w[i >> 1] = pack_f16x2(live ? e0 * rt : 0.f, live ? e1 * rt : 0.f);
+                            w[i >> 1] = pack_f16x2(e0 * rt, e1 * rt);
                         }
-                        uint4 *dst = reinterpret_cast<uint4 *>(prow + (c0 + c) * (kTile * 32));
-                        dst[sw_bit] = make_uint4(w[0], w[1], w[2], w[3]);
-                        dst[sw_bit ^ 1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        uint4 *dst = reinterpret_cast<uint4 *>(prow + c * (kTile * 32));
+                        dst[flip] = make_uint4(w[0], w[1], w[2], w[3]);
+                        dst[flip ^ 1] = make_uint4(w[4], w[5], w[6], w[7]);
                     }
+                tc_fence_before();
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(s.p_full[b]));
+                if (lane == 0) {
+                    mbar_arrive(bar(s.s_empty[wg]));
+                    mbar_arrive(bar(s.p_full[wg]));
+                }
             }
-            // ---- the segment's sums
-            const uint32_t jl = j - 1;
-            if (ok) ok = mbar_wait(bar(s.pv_done[jl & 1]), (jl >> 1) & 1, to, p.status, abort);
+            // ---- the segment's sums: each warpgroup's normalisers, then both
+            // warpgroups' sums merged, alternate chunks to each
+            const uint32_t last = j - 1 - ((j - 1 - wg) & 1);  // the last tile of this warpgroup's parity, if it had one
+            const bool used = !fresh;
+            if (ok && used) ok = mbar_wait(bar(s.pv_done[wg]), (last >> 1) & 1, to, p.status, abort);
+#pragma unroll
+            for (int c = 0; c < T::kChunks; ++c)
+                if (c < nch) {
+                    const float x = reduce16<false>(l + c * 16, lane);
+                    if (lane < 16) s.red[sw][c * 16 + lane_col(lane)] = x;
+                }
+            named_bar(5 + wg, 128);
+            if (tok < npad) {
+                s.lsum[wg][tok] = (s.red[wg * 4][tok] + s.red[wg * 4 + 1][tok]) + (s.red[wg * 4 + 2][tok] + s.red[wg * 4 + 3][tok]);
+                if (!used) s.mref[wg][tok] = -INFINITY;
+            }
+            if (tok == 0) s.back[wg] = sref / kHead;
             if (bar_or(4, kSoft, !ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const int64_t col0 = (int64_t)g.lo * p.Hq + (int64_t)(g.h * g.rows + g.row0) * p.G + (int64_t)cta * kCols;
-            const float back = sref / kHead;
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-                if (c < nch) {
-                    float o[16];
-                    tmem_ld_x16(tmem + lanes + kTmO + (c0 + c) * 16, reinterpret_cast<uint32_t *>(o));
+            for (int c = 0; c < T::kChunks; ++c)
+                if (c < nch && (c & 1) == wg) {
+                    float o0[16], o1[16];
+                    tmem_ld_x16(tmem + lanes + kTmO + c * 16, reinterpret_cast<uint32_t *>(o0));
+                    tmem_ld_x16(tmem + lanes + kTmO + 128 + c * 16, reinterpret_cast<uint32_t *>(o1));
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const int n = (c0 + c) * 16 + i;
-                        if (n < ncol) p.part[(col0 + n) * kD + tok] = o[i] * back;
+                        const int n = c * 16 + i;
+                        if (n < ncol) {
+                            const float m0 = s.mref[0][n], m1 = s.mref[1][n], m = fmaxf(m0, m1);
+                            float x = 0.f;
+                            if (m0 > -INFINITY) x = o0[i] * (ex2(m0 - m) * s.back[0]);
+                            if (m1 > -INFINITY) x = fmaf(o1[i], ex2(m1 - m) * s.back[1], x);
+                            p.part[(col0 + n) * kD + tok] = x;
+                        }
                     }
-                    const float x = reduce16<false>(l + c * 16, lane);
-                    if (lane < 16) s.red[sw][c * 16 + lane_col(lane)] = x;
                 }
+            if (wg == 0 && tok < ncol) {
+                const float m0 = s.mref[0][tok], m1 = s.mref[1][tok], m = fmaxf(m0, m1);
+                float x = 0.f;
+                if (m0 > -INFINITY) x = s.lsum[0][tok] * ex2(m0 - m);
+                if (m1 > -INFINITY) x = fmaf(s.lsum[1][tok], ex2(m1 - m), x);
+                p.ml[col0 + tok] = make_float2(m, x);
+            }
             tc_fence_before();
-            named_bar(5 + wg, 128);
-            if (tok < nch * 16 && c0 * 16 + tok < ncol)
-                p.ml[col0 + c0 * 16 + tok] =
-                    make_float2(s.mref[c0 * 16 + tok], (s.red[wg * 4][tok] + s.red[wg * 4 + 1][tok]) +
-                                                           (s.red[wg * 4 + 2][tok] + s.red[wg * 4 + 3][tok]));
             at += g.t1 - g.t0;
         }
     }
@@ -743,7 +869,9 @@ __global__ void __launch_bounds__(128) k_attn_join(const AttnParams p)
     for (int a = warp; a < nA; a += 4) {
         const int64_t j = s_path[a];
         float x[4];
-        rotated4(p.k + j * p.k_stride + h * kD, lane * 4, len + (int)p.depth[j], p.rope, x);
+        Raw4 rw;
+        load4(rw, p.k + j * p.k_stride + h * kD, lane * 4, len + (int)p.depth[j], p.rope);
+        turn4(rw, lane * 4, p.rope, x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sk[a * (kD + 1) + lane * 4 + i] = x[i];
         const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.v + j * p.v_stride + h * kD + lane * 4));
@@ -756,12 +884,14 @@ __global__ void __launch_bounds__(128) k_attn_join(const AttnParams p)
     pdl_wait();
     const int64_t total = __ldcg(p.plan + p.n_req), share = (total + p.ctas - 1) / p.ctas;
     const int nt = (len + kTile - 1) / kTile;
-    const int i0 = row - lo, grp = i0 / group_rows(rows, G);
-    const int64_t a0 = __ldcg(p.plan + r) + (int64_t)(h * group_count(rows, G) + grp) * nt;
+    const int fit = p.cols / G, i0 = row - lo, grp = i0 / group_rows(rows, fit);
+    const int64_t a0 = __ldcg(p.plan + r) + (int64_t)(h * group_count(rows, fit) + grp) * nt;
     const int cta0 = nt ? (int)(a0 / share) : 0, cta1 = nt ? (int)((a0 + nt - 1) / share) : -1;
     for (int g = warp; g < G; g += 4) {
         float x[4];
-        rotated4(p.q + row * p.q_stride + (int64_t)(h * G + g) * kD, lane * 4, len + (int)p.depth[row], p.rope, x);
+        Raw4 rw;
+        load4(rw, p.q + row * p.q_stride + (int64_t)(h * G + g) * kD, lane * 4, len + (int)p.depth[row], p.rope);
+        turn4(rw, lane * 4, p.rope, x);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) sq[warp * kD + lane * 4 + i] = x[i] * p.scale2;
@@ -778,7 +908,7 @@ __global__ void __launch_bounds__(128) k_attn_join(const AttnParams p)
             m = fmaxf(m, d0 + d1);
         }
         const int64_t col = (int64_t)lo * p.Hq + (int64_t)(h * rows + i0) * G + g;
-        for (int c = cta0 + lane; c <= cta1; c += 32) m = fmaxf(m, __ldcg(p.ml + col + (int64_t)c * kCols).x);
+        for (int c = cta0 + lane; c <= cta1; c += 32) m = fmaxf(m, __ldcg(p.ml + col + (int64_t)c * p.cols).x);
 #pragma unroll
         for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
         if (!(m > -INFINITY)) m = 0.f;                  // nothing but NaN and -inf: the sums say so
@@ -795,8 +925,8 @@ __global__ void __launch_bounds__(128) k_attn_join(const AttnParams p)
         }
 #pragma unroll 4
         for (int c = cta0; c <= cta1; ++c) {
-            const float2 q = __ldcg(p.ml + col + (int64_t)c * kCols);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (col + (int64_t)c * kCols) * kD) + lane);
+            const float2 q = __ldcg(p.ml + col + (int64_t)c * p.cols);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (col + (int64_t)c * p.cols) * kD) + lane);
             const float e = ex2(q.x - m);
             l = fmaf(e, q.y, l);
             acc[0] = fmaf(e, v.x, acc[0]);
@@ -829,7 +959,7 @@ EncodeTiledFn encode_fn()
 }
 
 size_t plan_bytes() { return (size_t)((kMaxReq + 1) * 8 + 255) / 256 * 256; }
-size_t part_columns(int32_t R, int32_t Hq, int ctas) { return (size_t)R * Hq + (size_t)ctas * kCols; }
+size_t part_columns(int32_t R, int32_t Hq, int ctas) { return (size_t)R * Hq + (size_t)ctas * kMaxCols; }
 
 }  // namespace
 
@@ -892,10 +1022,22 @@ int launch_attn(const AttnArgs &a, void *stream)
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return (int)cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(k_attn_ctx, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return (int)e;
-    k_attn_ctx<<<p.ctas, kThreads, kSmem, st>>>(kmap, p);
-    e = cudaGetLastError();
+    // columns of a segment: the least shape that holds an average request's rows and one row's heads
+    const int64_t avg = (int64_t)((a.R + a.n_req - 1) / a.n_req) * p.G;
+    p.cols = avg <= 16 ? 16 : avg <= 48 ? 48 : 80;
+    cudaError_t e;
+    auto go = [&](auto kernel, int threads, int bytes) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return;
+        kernel<<<p.ctas, threads, bytes, st>>>(kmap, p);
+        e = cudaGetLastError();
+    };
+    if (p.cols == 16)
+        go(k_attn_ctx<16>, Shape<16>::kThreads, smem_bytes<16>());
+    else if (p.cols == 48)
+        go(k_attn_ctx<48>, Shape<48>::kThreads, smem_bytes<48>());
+    else
+        go(k_attn_ctx<80>, Shape<80>::kThreads, smem_bytes<80>());
     if (e != cudaSuccess) return (int)e;
     constexpr int smem = (kPath * (2 * kD + 1) + 4 * (kD + kPath)) * 4;
     cudaLaunchConfig_t cfg{};
