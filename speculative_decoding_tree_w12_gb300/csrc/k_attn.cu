@@ -27,8 +27,10 @@
 //                of three of 16) and added up by the reader; above, each piece
 //                is a product of its own into the same accumulators.
 //   O^T = V^T P  kind::f16: V's codes widened to F16 (exact) by warpgroups of
-//                their own; P in F16, eleven significant bits, scaled so that
-//                there are 2^-18 below a weight of 1 before the subnormals.
+//                their own, into tensor memory (through shared memory they
+//                would cost four times the bandwidth, which bounds the tile);
+//                P in F16, eleven significant bits, scaled so that there are
+//                2^-18 below a weight of 1 before the subnormals.
 // Two softmax warpgroups take alternate tiles, each with its own scores, P,
 // maxima and sums, so the latencies of one tile's chain (product, reads,
 // exponentials, writes, product) hide behind the other's; they merge at the
@@ -54,13 +56,19 @@ constexpr int kD = kKvDim;
 constexpr int kPath = kMaxDepth + 1;       // rows of a root path
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 128;                 // tokens of a tile
-constexpr int kStack = 16;                 // columns up to which Q's pieces are stacked
+constexpr int kStack = 48;                 // columns up to which Q's pieces are stacked
 constexpr int kMaxCols = 80;               // query columns of a segment, see Shape
-constexpr int kScaleRing = 8;              // tiles whose block scales are kept (the producer runs at most 6 ahead of their readers)
+constexpr int kScaleRing = 16;             // tiles whose block scales are kept (the copies run at most 8 ahead of their readers)
 constexpr int kMaxReq = kMaxBudget;
 constexpr int kSoft = 256;                 // softmax threads
+// registers a thread: at launch (640 threads under 65536 registers), of the
+// softmax warps (a normaliser for each of 80 columns and 32 scores in flight),
+// of the others.  The shares add up to no more than the launch has.
+constexpr int kRegsLaunch = 96, kRegsSoft = 144, kRegsOther = 64;
+static_assert(kSoft * kRegsSoft + (640 - kSoft) * kRegsOther <= 640 * kRegsLaunch, "a larger share would wait forever");
 constexpr float kHead = 16.f;              // P of a weight of 1 under the reference scale
 constexpr float kRaise = 6.f;              // a score may pass the column's reference by this (log2) before it is raised
+constexpr float kCap = 8.f;                // scores are held under this until then
 constexpr float kScaleRaise = 16.f;        // ... and a value scale its reference by this factor: 16 * 2^6 * 16 < 2^15
 
 struct AttnParams {
@@ -75,7 +83,7 @@ struct AttnParams {
     RopeArgs rope;
     float scale2;                           // softmax scale * log2(e)
     uint16_t *out;
-    int64_t *plan;                          // [n_req + 1] first tile of every request
+    int32_t *plan;                          // [n_req + 1] first tile of every request
     float *part;                            // [R * Hq + ctas * cols][kD] sums
     float2 *ml;                             // [R * Hq + ctas * cols] maximum (log2), normaliser
     int32_t *status;
@@ -121,42 +129,45 @@ struct Raw4 {
     float c[4], s[4];
 };
 
-__device__ __forceinline__ void load4(Raw4 &x, const uint16_t *row, int d0, int pos, const RopeArgs &r)
+__device__ __forceinline__ void load4_row(Raw4 &x, const uint16_t *row, int d0, const RopeArgs &r)
 {
     x.w = __ldg(reinterpret_cast<const uint2 *>(row + d0));
     x.v = make_uint2(0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x.c[i] = 1.f, x.s[i] = 0.f;
     if (d0 >= r.rot) return;
     const int half = r.rot >> 1;
-    const float *ct = r.cos + (int64_t)pos * half, *st = r.sin + (int64_t)pos * half;
     if (r.adjacent) {
         x.v = make_uint2((x.w.x >> 16) | (x.w.x << 16), (x.w.y >> 16) | (x.w.y << 16));
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (d0 + i < r.rot) x.c[i] = __ldg(ct + ((d0 + i) >> 1)), x.s[i] = __ldg(st + ((d0 + i) >> 1));
-            else if (i & 2) x.v.y = 0;      // rot ends in the middle of the four
-        return;
-    }
-    if (r.rot & 7) {                        // partners that straddle the groups of four
+        if (d0 + 2 >= r.rot) x.v.y = 0;     // rot ends in the middle of the four
+    } else if (r.rot & 7) {                 // partners that straddle the groups of four
         uint32_t y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int d = d0 + i;
-            y[i] = 0;
-            if (d < r.rot) {
-                const int f = d < half ? d : d - half;
-                y[i] = row[d < half ? d + half : d - half];
-                x.c[i] = __ldg(ct + f), x.s[i] = __ldg(st + f);
-            }
+            y[i] = d < r.rot ? row[d < half ? d + half : d - half] : 0;
         }
         x.v = make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
-        return;
+    } else {
+        x.v = __ldg(reinterpret_cast<const uint2 *>(row + (d0 < half ? d0 + half : d0 - half)));
     }
-    const int f = d0 < half ? d0 : d0 - half;
-    x.v = __ldg(reinterpret_cast<const uint2 *>(row + (d0 < half ? d0 + half : d0 - half)));
+}
+
+__device__ __forceinline__ void load4_turn(Raw4 &x, int d0, int pos, const RopeArgs &r)
+{
+    const int half = r.rot >> 1;
+    const float *ct = r.cos + (int64_t)pos * half, *st = r.sin + (int64_t)pos * half;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x.c[i] = __ldg(ct + f + i), x.s[i] = __ldg(st + f + i);
+    for (int i = 0; i < 4; ++i) {
+        const int d = d0 + i, f = r.adjacent ? d >> 1 : d < half ? d : d - half;
+        const bool in = d < r.rot;
+        x.c[i] = in ? __ldg(ct + f) : 1.f;
+        x.s[i] = in ? __ldg(st + f) : 0.f;
+    }
+}
+
+__device__ __forceinline__ void load4(Raw4 &x, const uint16_t *row, int d0, int pos, const RopeArgs &r)
+{
+    load4_row(x, row, d0, r);
+    load4_turn(x, d0, pos, r);
 }
 
 __device__ __forceinline__ void turn4(const Raw4 &r, int d0, const RopeArgs &rope, float (&x)[4])
@@ -183,43 +194,53 @@ __device__ __forceinline__ void turn4(const Raw4 &r, int d0, const RopeArgs &rop
 // with more gets several groups of rows, each reading the context again (from
 // L2, side by side), so any shape serves any tree; the host picks the least
 // one that holds an average request's.  Fewer columns leave shared memory for
-// more tiles in flight and registers for more converting warps.
+// more tiles in flight.
 template <int kCols>
 struct Shape {
     static constexpr int kChunks = kCols / 16;
     static constexpr bool kStacked = kCols <= kStack;
-    static constexpr int kConv = kCols <= 48 ? 2 : 1;            // warpgroups widening V
-    static constexpr int kThreads = 128 + kSoft + kConv * 128;   // warps: 0 producer, 1 MMA, 4-11 softmax, 12- conversion
-    static constexpr int kStK = kCols <= 16 ? 4 : 3;             // K tiles in flight
-    static constexpr int kStV = kCols <= 16 ? 4 : kCols <= 48 ? 3 : 2;
+    // warps: 0 K copies, 1 scores, 2 V copies, 3 sums, 4-11 softmax, 12-19 conversion
+    static constexpr int kThreads = 128 + kSoft + 256;
+    static constexpr int kStK = kCols <= 16 ? 6 : 5;             // K tiles in flight
+    static constexpr int kStV = kCols <= 16 ? 6 : kCols <= 48 ? 5 : 4;
     static constexpr int kKBytes = kTile * kD;                   // one K or V tile: 16 KB
     static constexpr int kPBytes = kCols * kTile * 2;
     static constexpr int kQBytes = kCols * kD;
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kStK * kKBytes;
-    static constexpr int kOffV16 = kOffV + kStV * kKBytes;       // [2][2 token halves][128 d][64 tokens] F16
-    static constexpr int kOffP = kOffV16 + 4 * kKBytes;          // [2][kCols / 16 slabs][128 tokens][16] F16
+    static constexpr int kOffP = kOffV + kStV * kKBytes;         // [2][kCols / 16 slabs][128 tokens][16] F16
     static constexpr int kOffQ = kOffP + 2 * kPBytes;            // [3 pieces][kCols][128] E4M3
     static constexpr int kOffShared = kOffQ + 3 * kQBytes;
+    // tensor memory: scores of two tiles, sums of the two warpgroups, two V tiles in F16 (two tokens to a column)
+    static constexpr int kTmS = kStacked ? 3 * kCols : kCols;    // columns of one tile's scores
+    static constexpr int kTmO = 2 * kTmS;
+    static constexpr int kTmV = kTmO + 2 * kCols;
+    static constexpr int kTmUsed = kTmV + kTile;
+    static constexpr int kTmCols = kTmUsed <= 256 ? 256 : 512;
+    static_assert(kTmUsed <= 512, "tensor memory");
 };
 
+constexpr int kMaxStages = 6;
+
 struct Shared {
-    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];   // K and V tiles loaded / consumed
+    uint64_t k_full[kMaxStages], k_empty[kMaxStages];  // K and V tiles loaded / consumed
+    uint64_t v_full[kMaxStages], v_empty[kMaxStages];
     uint64_t s_full[2], s_empty[2];                    // scores in tensor memory / read
     uint64_t p_full[2], v16_full[2], pv_done[2];       // weights and widened values in shared memory / their product added
-    uint64_t q_full, drain;
-    int64_t pre[kMaxReq + 1];                          // first tile of every request
+    uint64_t q_full, drain[2];
     int64_t wsum[24];
+    int32_t pre[kMaxReq + 1];                          // first tile of every request
     alignas(16) float cf[kMaxCols];                    // score factor of a column
-    alignas(16) float mref[2][kMaxCols];               // per warpgroup: reference maximum, its last raise (log2)
-    alignas(16) float delta[2][kMaxCols];
+    alignas(16) float mneg[2][kMaxCols];               // per warpgroup: minus the reference maximum, the factor of its last raise;
+    alignas(16) float delta[2][kMaxCols];              // at the end, what the warpgroup's sums count for in the segment's
     float lsum[2][kMaxCols], red[8][kMaxCols];         // normalisers; per softmax warp
+    int32_t len[kMaxReq];                              // of every request: cached tokens,
+    uint16_t lo[kMaxReq], rows[kMaxReq];               // first row, rows
     float2 scale[kScaleRing][kTile / 32];              // K and V scale of a tile's blocks
     float top_v[kScaleRing];                           // the largest of the V scales
-    float back[2];
+    float sref[2];
     uint32_t tmem;
     int32_t abort;
-    int32_t k_asked;                                   // the producer's last K tile
 };
 
 template <int kCols>
@@ -230,7 +251,6 @@ constexpr int smem_bytes()
 static_assert(smem_bytes<16>() <= 227 * 1024 && smem_bytes<48>() <= 227 * 1024 && smem_bytes<80>() <= 227 * 1024,
               "one CTA per SM");
 
-constexpr uint32_t kTmO = 256, kTmCols = 512;             // scores at columns 0 and 128, sums at 256 and 384
 
 // a stretch of tiles t0 .. t1 - 1 of one segment
 struct Seg {
@@ -238,27 +258,26 @@ struct Seg {
 };
 
 // the segment that tile `at` lies in, up to tile `end` of the whole list
-__device__ __forceinline__ Seg segment(const AttnParams &p, const int64_t *pre, int64_t at, int64_t end)
+__device__ __forceinline__ Seg segment(const AttnParams &p, const Shared &sh, int32_t at, int32_t end)
 {
     int a = 0, b = p.n_req;                 // pre[a] <= at < pre[b]
     while (b - a > 1) {
         const int m = (a + b) >> 1;
-        if (pre[m] <= at) a = m;
+        if (sh.pre[m] <= at) a = m;
         else b = m;
     }
     Seg s;
     s.r = a;
-    s.lo = p.off[a];
-    s.rows = p.off[a + 1] - s.lo;
-    s.len = p.len[a];
-    const int nt = (s.len + kTile - 1) / kTile;
+    s.lo = sh.lo[a];
+    s.rows = sh.rows[a];
+    s.len = sh.len[a];
+    const uint32_t nt = (uint32_t)(s.len + kTile - 1) / kTile;
     const int fit = p.cols / p.G, g = group_count(s.rows, fit), per = group_rows(s.rows, fit);
-    const int64_t i = at - pre[a];
-    const int seg = (int)(i / nt);
-    s.t0 = (int)(i % nt);
-    s.t1 = (int)min((int64_t)nt, s.t0 + (end - at));
-    s.h = seg / g;
-    s.row0 = seg % g * per;
+    const uint32_t i = (uint32_t)(at - sh.pre[a]), seg = i / nt;
+    s.t0 = (int)(i - seg * nt);
+    s.t1 = min((int)nt, s.t0 + (end - at));
+    s.h = (int)(seg / (uint32_t)g);
+    s.row0 = (int)(seg % (uint32_t)g) * per;
     s.nrows = min(per, s.rows - s.row0);
     return s;
 }
@@ -278,6 +297,75 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// two FP32 operations at a time
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// 32 lanes x 8 columns
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, float *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// the loads before it are complete, and these registers of theirs are read after it only
+__device__ __forceinline__ void ld_done8(float *y)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(y[0]), "+f"(y[1]), "+f"(y[2]), "+f"(y[3]), "+f"(y[4]), "+f"(y[5]), "+f"(y[6]), "+f"(y[7])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void ld_done(float (&y)[16])
+{
+    ld_done8(y);
+    asm volatile("" : "+f"(y[8]), "+f"(y[9]), "+f"(y[10]), "+f"(y[11]), "+f"(y[12]), "+f"(y[13]), "+f"(y[14]), "+f"(y[15]));
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
@@ -319,7 +407,7 @@ __device__ __forceinline__ float reduce16(const float *x, int lane)
 
 template <int kCols>
 __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
-    k_attn_ctx(const __grid_constant__ CUtensorMap kmap, const AttnParams p)
+    k_attn_ctx(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnParams p)
 {
     typedef Shape<kCols> T;
     extern __shared__ uint8_t raw[];
@@ -339,6 +427,9 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
             mine = rows ? (int64_t)((len + kTile - 1) / kTile) * p.H * group_count(rows, fit) : 0;
         else
             fail(p.status);
+        s.lo[tid] = (uint16_t)lo;
+        s.rows[tid] = (uint16_t)rows;
+        s.len[tid] = len;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -349,52 +440,72 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
     if (lane == 31) s.wsum[warp] = incl;
     if (tid == 0) {
         s.abort = 0;
-        s.k_asked = -1;
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(bar(s.k_full[i]), 1);
             mbar_init(bar(s.k_empty[i]), 1);
             mbar_init(bar(s.v_full[i]), 1);
-            mbar_init(bar(s.v_empty[i]), 1);
+            mbar_init(bar(s.v_empty[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(s.s_full[i]), 1);
             mbar_init(bar(s.s_empty[i]), 4);
             mbar_init(bar(s.p_full[i]), 4);
-            mbar_init(bar(s.v16_full[i]), 1);
+            mbar_init(bar(s.v16_full[i]), 4);
             mbar_init(bar(s.pv_done[i]), 1);
         }
         mbar_init(bar(s.q_full), kSoft / 32);
-        mbar_init(bar(s.drain), 1);
+        mbar_init(bar(s.drain[0]), 1);
+        mbar_init(bar(s.drain[1]), 1);
         fence_mbar_init();
         prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
     }
-    if (warp == 1) tmem_alloc(smem_u32(&s.tmem), kTmCols);
+    if (warp == 1) tmem_alloc(smem_u32(&s.tmem), T::kTmCols);
     __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += s.wsum[w];
-    if (tid < p.n_req) s.pre[tid + 1] = incl;
+    int64_t all = 0;
+    for (int w = 0; w < T::kThreads / 32; ++w) {
+        if (w < warp) incl += s.wsum[w];
+        all += s.wsum[w];
+    }
+    const bool fits = all <= INT32_MAX;                   // else there is nothing to do but say so
+    if (!fits && tid == 0) atomicCAS(p.status, 0, (int32_t)W12_E_UNSUPPORTED);
+    if (tid < p.n_req) s.pre[tid + 1] = fits ? (int32_t)incl : 0;
     if (tid == 0) s.pre[0] = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
-    const int64_t total = s.pre[p.n_req];
+    const int32_t total = s.pre[p.n_req];
     if (cta == 0)
         for (int i = tid; i <= p.n_req; i += T::kThreads) p.plan[i] = s.pre[i];
-    const int64_t share = (total + p.ctas - 1) / p.ctas;
-    const int64_t first = min(total, cta * share), end = min(total, first + share);
+    const int64_t share = ((int64_t)total + p.ctas - 1) / p.ctas;
+    const int32_t first = (int32_t)min((int64_t)total, cta * share), end = (int32_t)min((int64_t)total, first + share);
     const int bs = p.bt == 32 ? 5 : p.bt == 64 ? 6 : 7;   // log2 of a block's tokens
     const int nb = kTile >> bs;                           // blocks of a tile
     volatile int32_t *abort = &s.abort;
     const uint64_t to = p.timeout_ns;
+    // after a wait that ran out: products in flight end before tensor memory is freed
+    auto drain = [&](const uint64_t &b) {
+        tc_commit(bar(b));
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait_sleep(bar(b), 0, kWaitSleepNs))
+            if (globaltimer() - t0 > to) break;
+    };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        // Block numbers and scales are fetched 32 blocks at a time, one batch
-        // ahead of their copies.
-        uint32_t j = 0;
+    if (warp == 0 || warp == 2) {
+        // ------------------------------------------------------------ copies: warp 0 K and the block scales, warp 2 V
+        // Block numbers (and scales) are fetched 32 blocks at a time, one
+        // batch ahead of their copies.  A thread's loop of wait, expect and
+        // copy takes some 200 ns a turn, so K and V have one each.
+        regs_dec<kRegsOther>();
+        const bool is_k = warp == 0;
+        const int stages = is_k ? T::kStK : T::kStV;
+        const uint32_t full = smem_u32(is_k ? s.k_full : s.v_full), empty = smem_u32(is_k ? s.k_empty : s.v_empty);
+        const uint32_t tile0 = base + (is_k ? T::kOffK : T::kOffV), bytes = (uint32_t)(p.bt * kD);
+        uint32_t j = 0, st = 0, par = 1;                      // tile, its stage, the parity its stage's last use left
         bool ok = true;
-        for (int64_t at = first; at < end && ok;) {
-            const Seg g = segment(p, s.pre, at, end);
+        for (int32_t at = first; at < end && ok;) {
+            const Seg g = segment(p, s, at, end);
             const int b0 = g.t0 * nb, b1 = min((g.len + p.bt - 1) >> bs, g.t1 * nb);
             const int32_t *table = p.table + (int64_t)g.r * p.max_blocks;
             int blk = 0;
@@ -409,7 +520,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                         id = 0;
                     }
                     const int64_t i = (int64_t)id * p.H + g.h;
-                    v = make_float2(__ldg(p.ks + i), __ldg(p.vs + i));
+                    if (is_k) v = make_float2(__ldg(p.ks + i), __ldg(p.vs + i));
                 }
             };
             fetch(b0 + lane, blk, sc);
@@ -419,29 +530,25 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                 fetch(b + 32 + lane, blk2, sc2);
                 float top = sc.y;                             // the tile's largest V scale
                 for (int d = 1; d < nb; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const int row = is_k ? (blk * p.H + g.h) << bs : (blk * p.H + g.h) * kD;   // of the pool seen as rows
                 for (int l = 0; l < 32 && b + l < b1; l += nb, ++j) {
-                    const int sk = j % T::kStK, sv = j % T::kStV;
                     const int n = min(nb, b1 - (b + l));      // blocks of this tile that hold tokens
-                    const bool in = lane >= l && lane < l + nb, copy = in && lane < l + n;
-                    const int row = (blk * p.H + g.h) << bs;
-                    const uint32_t off = (uint32_t)(lane - l) * (uint32_t)(p.bt * kD), bytes = (uint32_t)(p.bt * kD);
-                    ok = __all_sync(0xffffffffu, j < T::kStK || mbar_wait(bar(s.k_empty[sk]), (j / T::kStK - 1) & 1, to,
-                                                                          p.status, abort));
+                    const bool in = lane >= l && lane < l + nb;
+                    const uint32_t f = full + st * 8;
+                    ok = __all_sync(0xffffffffu, mbar_wait(empty + st * 8, par, to, p.status, abort));
                     if (!ok) break;
-                    if (in) s.scale[j % kScaleRing][lane - l] = sc;
-                    if (lane == l) s.top_v[j % kScaleRing] = top;
+                    if (is_k) {
+                        if (in) s.scale[j % kScaleRing][lane - l] = sc;
+                        if (lane == l) s.top_v[j % kScaleRing] = top;
+                        __syncwarp();
+                    }
+                    if (lane == l) mbar_expect_tx(f, n * bytes);
                     __syncwarp();
-                    if (lane == 0) mbar_expect_tx(bar(s.k_full[sk]), n * bytes);
-                    __syncwarp();
-                    if (lane == 0) s.k_asked = (int32_t)j;
-                    if (copy) tma_load_2d(base + T::kOffK + sk * T::kKBytes + off, &kmap, 0, row, bar(s.k_full[sk]));
-                    ok = __all_sync(0xffffffffu, j < T::kStV || mbar_wait(bar(s.v_empty[sv]), (j / T::kStV - 1) & 1, to,
-                                                                          p.status, abort));
-                    if (!ok) break;
-                    if (lane == 0) mbar_expect_tx(bar(s.v_full[sv]), n * bytes);
-                    __syncwarp();
-                    if (copy)
-                        bulk_g2s(base + T::kOffV + sv * T::kKBytes + off, p.vc + (int64_t)row * kD, bytes, bar(s.v_full[sv]));
+                    if (in && lane < l + n) {
+                        const uint32_t dst = tile0 + st * T::kKBytes + (uint32_t)(lane - l) * bytes;
+                        tma_load_2d(dst, is_k ? &kmap : &vmap, 0, row, f);
+                    }
+                    if (++st == (uint32_t)stages) st = 0, par ^= 1;
                 }
                 blk = blk2;
                 sc = sc2;
@@ -450,133 +557,137 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
         }
         if (!ok) {                                            // copies in flight land before the CTA leaves
             const uint64_t t0 = globaltimer();
-            auto land = [&](const uint64_t &b, uint32_t phase) {
-                while (!mbar_try_wait_sleep(bar(b), phase & 1, kWaitSleepNs))
+            for (uint32_t i = j >= (uint32_t)stages ? j - stages : 0; i < j; ++i)
+                while (!mbar_try_wait_sleep(full + i % stages * 8, (i / stages) & 1, kWaitSleepNs))
                     if (globaltimer() - t0 > to) break;
-            };
-            for (uint32_t i = j >= T::kStV ? j - T::kStV : 0; i < j; ++i) land(s.v_full[i % T::kStV], i / T::kStV);
-            for (uint32_t i = j >= T::kStK ? j - T::kStK : 0; i < j; ++i) land(s.k_full[i % T::kStK], i / T::kStK);
-            if (s.k_asked == (int32_t)j) land(s.k_full[j % T::kStK], j / T::kStK);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA
+        // ------------------------------------------------------------ scores: S^T = K Q^T
+        regs_dec<kRegsOther>();
         if (lane == 0) {
-            uint32_t j = 0, q = 0, done = 0;                  // tiles scored, segments, tiles multiplied
+            uint32_t j = 0, q = 0, st = 0, par = 0;
             bool ok = true;
-            for (int64_t at = first; at < end && ok; ++q) {
-                const Seg g = segment(p, s.pre, at, end);
+            const uint64_t kd = smem_desc_sw128(base + T::kOffK), qd = smem_desc_sw128(base + T::kOffQ);
+            for (int32_t at = first; at < end && ok; ++q) {
+                const Seg g = segment(p, s, at, end);
                 const int n = (g.nrows * p.G + 15) & ~15;
-                const uint32_t i_qk = idesc_e4m3_f32(kTile, T::kStacked ? 3 * kCols : n), i_pv = idesc_f16_f32_bmn(kD, n);
-                const uint32_t start = j;
-                auto pv = [&](uint32_t i) -> bool {
-                    const int b = i & 1;
-                    if (!mbar_wait(bar(s.v16_full[b]), (i >> 1) & 1, to, p.status, abort)) return false;
-                    if (!mbar_wait(bar(s.p_full[b]), (i >> 1) & 1, to, p.status, abort)) return false;
-                    tc_fence_after();
-                    const bool fresh = i - start < 2;
-                    const uint64_t pd = smem_desc_mn_sw32(base + T::kOffP + b * T::kPBytes, kTile * 32);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        tc_mma_ss_f16(tmem + kTmO + b * 128,
-                                      smem_desc_sw128(base + T::kOffV16 + b * 2 * T::kKBytes + (k >> 2) * T::kKBytes + (k & 3) * 32),
-                                      pd + (uint64_t)(k * (512 >> 4)), i_pv, !(fresh && k == 0));
-                    tc_commit(bar(s.pv_done[b]));
-                    return true;
-                };
+                const uint32_t idesc = idesc_e4m3_f32(kTile, T::kStacked ? 3 * kCols : n);
                 ok = mbar_wait(bar(s.q_full), q & 1, to, p.status, abort);
                 for (int t = g.t0; t < g.t1 && ok; ++t, ++j) {
-                    const int st = j % T::kStK, b = j & 1;
-                    ok = mbar_wait(bar(s.k_full[st]), (j / T::kStK) & 1, to, p.status, abort) &&
-                         (j < 2 || mbar_wait(bar(s.s_empty[b]), ((j >> 1) - 1) & 1, to, p.status, abort));
+                    const int b = j & 1;
+                    ok = (j < 2 || mbar_wait(bar(s.s_empty[b]), ((j >> 1) - 1) & 1, to, p.status, abort)) &&
+                         mbar_wait(bar(s.k_full[st]), par, to, p.status, abort);
                     if (!ok) break;
                     tc_fence_after();
+                    const uint64_t ka = kd + (uint64_t)(st * (T::kKBytes >> 4));
 #pragma unroll
                     for (int c = 0; c < (T::kStacked ? 1 : 3); ++c)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            tc_mma_ss_f8(tmem + b * 128, smem_desc_sw128(base + T::kOffK + st * T::kKBytes + k * 32),
-                                         smem_desc_sw128(base + T::kOffQ + c * T::kQBytes + k * 32), i_qk, c + k > 0);
+                            tc_mma_ss_f8(tmem + b * T::kTmS, ka + k * 2, qd + (uint64_t)((c * T::kQBytes + k * 32) >> 4), idesc, c + k > 0);
                     tc_commit(bar(s.s_full[b]));
                     tc_commit(bar(s.k_empty[st]));
-                    if (j - done >= 2) ok = pv(done++);
+                    if (++st == T::kStK) st = 0, par ^= 1;
                 }
-                while (ok && done < j) ok = pv(done++);
                 at += g.t1 - g.t0;
             }
-            if (!ok) {                                        // products in flight end before tensor memory is freed
-                tc_commit(bar(s.drain));
-                const uint64_t t0 = globaltimer();
-                while (!mbar_try_wait_sleep(bar(s.drain), 0, kWaitSleepNs))
-                    if (globaltimer() - t0 > to) break;
+            if (!ok) drain(s.drain[0]);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ sums: O^T += V^T P
+        regs_dec<kRegsOther>();
+        if (lane == 0) {
+            uint32_t j = 0;
+            bool ok = true;
+            const uint64_t pd = smem_desc_mn_sw32(base + T::kOffP, kTile * 32);
+            for (int32_t at = first; at < end && ok;) {
+                const Seg g = segment(p, s, at, end);
+                const uint32_t idesc = idesc_f16_f32_bmn(kD, (g.nrows * p.G + 15) & ~15);
+                for (int t = g.t0; t < g.t1 && ok; ++t, ++j) {
+                    const int b = j & 1;
+                    ok = mbar_wait(bar(s.v16_full[b]), (j >> 1) & 1, to, p.status, abort) &&
+                         mbar_wait(bar(s.p_full[b]), (j >> 1) & 1, to, p.status, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t keep = t - g.t0 >= 2;      // each parity's first tile starts its sums
+                    const uint64_t pb = pd + (uint64_t)(b * (T::kPBytes >> 4));
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tc_mma_ts(tmem + T::kTmO + b * kCols, tmem + T::kTmV + b * (kTile / 2) + k * 8, pb + (uint64_t)(k * (512 >> 4)),
+                                  idesc, keep | (k > 0));
+                    tc_commit(bar(s.pv_done[b]));
+                }
+                at += g.t1 - g.t0;
             }
+            if (!ok) drain(s.drain[1]);
         }
         __syncwarp();
     } else if (warp >= 12) {
         // ------------------------------------------------------------ V to F16
-        const int t128 = (tid - 384) & 127, wg = (tid - 384) >> 7;
+        regs_dec<kRegsOther>();
+        const int wg = (warp - 12) >> 2, quad = warp & 3, d = quad * 32 + lane;   // a dimension to a thread, as the lanes lie
+        const int cs = bs - 4;                                // log2 of the 16-token chunks of a row of a block
+        const int swz = bs == 5 ? (d >> 2) & 1 : bs == 6 ? (d >> 1) & 3 : d & 7;   // the copy's swizzle: one row's bytes wide
+        const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + T::kTmV + wg * (kTile / 2);
         uint32_t j = 0;
         bool ok = true;
-        const int cs = bs - 4;                                // log2 of the 16-token chunks of a row of a block
-        for (int64_t at = first; at < end && ok;) {
-            const Seg g = segment(p, s.pre, at, end);
+        for (int32_t at = first; at < end && ok;) {
+            const Seg g = segment(p, s, at, end);
             for (int t = g.t0; t < g.t1; ++t, ++j) {
-                if (T::kConv == 2 && (int)(j & 1) != wg) continue;
-                const int st = j % T::kStV, b = j & 1;
-                ok = mbar_wait(bar(s.v_full[st]), (j / T::kStV) & 1, to, p.status, abort) &&
-                     (j < 2 || mbar_wait(bar(s.pv_done[b]), ((j >> 1) - 1) & 1, to, p.status, abort));
-                if (bar_or(2 + wg, 128, !ok)) {
-                    ok = false;
-                    break;
-                }
+                if ((int)(j & 1) != wg) continue;
+                const int st = j % T::kStV;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(s.v_full[st]), (j / T::kStV) & 1, to, p.status, abort) &&
+                                                 (j < 2 || mbar_wait(bar(s.pv_done[wg]), ((j >> 1) - 1) & 1, to, p.status, abort)));
+                if (!ok) break;
+                tc_fence_after();
                 const int valid = min(kTile, g.len - t * kTile);
-                const uint8_t *src = sm + T::kOffV + st * T::kKBytes;
-                uint8_t *to16 = sm + T::kOffV16 + b * 2 * T::kKBytes;
-                uint4 w[8];
+                const uint8_t *src = sm + T::kOffV + st * T::kKBytes + (d << bs);
 #pragma unroll
-                for (int it = 0; it < 8; ++it) w[it] = *reinterpret_cast<const uint4 *>(src + (it * 128 + t128) * 16);
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t y[32];
 #pragma unroll
-                for (int it = 0; it < 8; ++it) {
-                    const int i = it * 128 + t128;
-                    const int row = i >> cs, d = row & (kD - 1);             // row: (block, d)
-                    const int tok = ((row >> 7) << bs) + (i & ((1 << cs) - 1)) * 16;
-                    uint32_t x[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
-                    if (tok + 16 > valid)                                     // what lies past the last token is not a value
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = half * 4 + i, tok = c * 16;             // chunk c of the tile's eight
+                        const int blk = c >> cs, in = c & ((1 << cs) - 1);
+                        const uint4 w = *reinterpret_cast<const uint4 *>(src + ((blk * kD) << bs) + ((in ^ swz) << 4));
+                        uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                        if (tok + 16 > valid)                                 // what lies past the last token is not a value
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int left = valid - tok - 4 * c;
-                            x[c] &= left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+                            for (int q = 0; q < 4; ++q) {
+                                const int left = valid - tok - 4 * q;
+                                x[q] &= left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+                            }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            y[i * 8 + 2 * q] = e4m3x2_f16x2(x[q] & 0xFFFFu);
+                            y[i * 8 + 2 * q + 1] = e4m3x2_f16x2(x[q] >> 16);
                         }
-                    uint32_t y[8];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        y[2 * c] = e4m3x2_f16x2(x[c] & 0xFFFFu);
-                        y[2 * c + 1] = e4m3x2_f16x2(x[c] >> 16);
                     }
-                    uint8_t *dst = to16 + (tok >> 6) * T::kKBytes + d * 128;
-                    const int c = (tok & 63) >> 3;
-                    *reinterpret_cast<uint4 *>(dst + ((c ^ (d & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                    *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (d & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+                    tmem_st_x32(dst + half * 32, y);
                 }
-                fence_async_shared();
-                named_bar(2 + wg, 128);
-                if (t128 == 0) {
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
                     mbar_arrive(bar(s.v_empty[st]));
-                    mbar_arrive(bar(s.v16_full[b]));
+                    mbar_arrive(bar(s.v16_full[wg]));
                 }
             }
             at += g.t1 - g.t0;
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax: warpgroup wg takes the tiles j with j % 2 == wg
+        regs_inc<kRegsSoft>();
         const int sw = warp - 4, wg = sw >> 2, quad = warp & 3;
         const int tok = quad * 32 + lane;                     // this thread's token of the tile
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t tm_s = tmem + lanes + wg * 128, tm_o = tmem + lanes + kTmO + wg * 128;
-        const float4 *cf4 = reinterpret_cast<const float4 *>(s.cf), *mr4 = reinterpret_cast<const float4 *>(s.mref[wg]);
+        const uint32_t tm_s = tmem + lanes + wg * T::kTmS, tm_o = tmem + lanes + T::kTmO + wg * kCols;
+        const float4 *cf4 = reinterpret_cast<const float4 *>(s.cf), *mn4 = reinterpret_cast<const float4 *>(s.mneg[wg]);
         uint32_t j = 0;
         bool ok = true;
-        for (int64_t at = first; at < end && ok;) {
-            const Seg g = segment(p, s.pre, at, end);
+        for (int32_t at = first; at < end && ok;) {
+            const Seg g = segment(p, s, at, end);
             const int ncol = g.nrows * p.G, npad = (ncol + 15) & ~15, nch = npad >> 4;
             // ---- Q: turned, scaled to E4M3's range by a power of two, in three pieces
             named_bar(4, kSoft);                              // the last segment's columns are done with
@@ -584,21 +695,17 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
 #pragma unroll 1
             for (int n0 = sw; n0 < n_q; n0 += 8 * 2) {
                 Raw4 rw[2];
-                int pos[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int n = min(n0 + 8 * u, ncol - 1);
-                    pos[u] = g.len + (int)__ldg(p.depth + g.lo + g.row0 + n / p.G);
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int n = min(n0 + 8 * u, ncol - 1);
-                    if (p.rope.rot && pos[u] >= p.rope.max_pos) {
+                    const int n = min(n0 + 8 * u, ncol - 1), row = g.lo + g.row0 + n / p.G;
+                    const uint16_t *q = p.q + (int64_t)row * p.q_stride + (int64_t)(g.h * p.G + n % p.G) * kD;
+                    int pos = g.len + (int)__ldg(p.depth + row);
+                    load4_row(rw[u], q, lane * 4, p.rope);
+                    if (p.rope.rot && pos >= p.rope.max_pos) {
                         fail(p.status);
-                        pos[u] = 0;
+                        pos = 0;
                     }
-                    load4(rw[u], p.q + (int64_t)(g.lo + g.row0 + n / p.G) * p.q_stride + (int64_t)(g.h * p.G + n % p.G) * kD,
-                          lane * 4, pos[u], p.rope);
+                    load4_turn(rw[u], lane * 4, pos, p.rope);
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
@@ -627,8 +734,8 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                     }
                     if (lane == 0) {
                         s.cf[n] = pad ? 0.f : qs * p.scale2;
-                        s.mref[0][n] = 0.f;
-                        s.mref[1][n] = 0.f;
+                        s.mneg[0][n] = 0.f;
+                        s.mneg[1][n] = 0.f;
                     }
                 }
             }
@@ -636,9 +743,9 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
             named_bar(4, kSoft);
             if (lane == 0) mbar_arrive(bar(s.q_full));
 
-            float l[kCols];
+            uint64_t l[kCols / 2];                            // this thread's tokens' part of the normalisers, in pairs
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) l[i] = 0.f;
+            for (int i = 0; i < kCols / 2; ++i) l[i] = 0ull;
             float sref = 0.f;
             bool fresh = true;
             const uint32_t j0 = j;
@@ -646,55 +753,93 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
             for (uint32_t jj = j0 + ((j0 ^ wg) & 1); jj < j; jj += 2) {
                 const int t = g.t0 + (int)(jj - j0);
                 ok = mbar_wait(bar(s.s_full[wg]), (jj >> 1) & 1, to, p.status, abort);
+                // this warpgroup's P and sums are free once its last product is done
+                if (ok && jj >= 2) ok = mbar_wait(bar(s.pv_done[wg]), ((jj >> 1) - 1) & 1, to, p.status, abort);
                 __syncwarp();
                 tc_fence_after();
                 const float2 my = s.scale[jj % kScaleRing][tok >> bs];
                 const float top_v = fmaxf(s.top_v[jj % kScaleRing], 1e-30f);
                 const bool live = t * kTile + tok < g.len;
-                // 16 columns of scores against their references, in log2 units
-                auto scores = [&](int c, float (&y)[16]) {
-                    uint32_t *r = reinterpret_cast<uint32_t *>(y);
-                    tmem_ld_x16(tm_s + c * 16, r);
-                    if (T::kStacked) {
-                        float y1[16], y2[16];
-                        tmem_ld_x16(tm_s + kCols + c * 16, reinterpret_cast<uint32_t *>(y1));
-                        tmem_ld_x16(tm_s + 2 * kCols + c * 16, reinterpret_cast<uint32_t *>(y2));
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] += y1[i] + y2[i];
-                    } else {
-                        tmem_ld_wait();
+                const uint64_t ks2 = pair(my.x, my.x);
+                // 8 columns' raw scores: asked for, and turned into scores against the references in log2 units
+                auto ask = [&](int c, float *y) { tmem_ld_x8(tm_s + c * 8, y); };
+                auto scores = [&](int c, float *y) {
+                    float y1[T::kStacked ? 8 : 1], y2[T::kStacked ? 8 : 1];
+                    if constexpr (T::kStacked) {
+                        tmem_ld_x8(tm_s + kCols + c * 8, y1);
+                        tmem_ld_x8(tm_s + 2 * kCols + c * 8, y2);
+                        ld_done8(y1);
+                        ld_done8(y2);
                     }
+                    ld_done8(y);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 f = cf4[c * 4 + (i >> 2)], m = mr4[c * 4 + (i >> 2)];
-                        y[i] = fmaf(y[i], f.x * my.x, -m.x);
-                        y[i + 1] = fmaf(y[i + 1], f.y * my.x, -m.y);
-                        y[i + 2] = fmaf(y[i + 2], f.z * my.x, -m.z);
-                        y[i + 3] = fmaf(y[i + 3], f.w * my.x, -m.w);
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 f = cf4[c * 2 + (i >> 2)], m = mn4[c * 2 + (i >> 2)];
+                        uint64_t a = pair(y[i], y[i + 1]), b = pair(y[i + 2], y[i + 3]);
+                        if constexpr (T::kStacked) {
+                            a = add2(a, add2(pair(y1[i], y1[i + 1]), pair(y2[i], y2[i + 1])));
+                            b = add2(b, add2(pair(y1[i + 2], y1[i + 3]), pair(y2[i + 2], y2[i + 3])));
+                        }
+                        unpair(fma2(a, mul2(pair(f.x, f.y), ks2), pair(m.x, m.y)), y[i], y[i + 1]);
+                        unpair(fma2(b, mul2(pair(f.z, f.w), ks2), pair(m.z, m.w)), y[i + 2], y[i + 3]);
                     }
                 };
-                float top = -INFINITY;
+                // the tile's weights into P and the normalisers; returns this
+                // token's largest score, over kRaise if the references have to
+                // be raised first (the weights are held finite until then)
+                auto weights = [&]() -> float {
+                    const float rt = kHead * (my.y / sref);
+                    const uint64_t rt2 = pair(rt, rt);
+                    uint8_t *prow = sm + T::kOffP + wg * T::kPBytes + tok * 32;
+                    const int flip = ((tok >> 2) & 1) << 4;
+                    float top = -INFINITY;
+                    float y[2][8];
+                    ask(0, y[0]);
 #pragma unroll
-                for (int c = 0; c < T::kChunks; ++c)
-                    if (c < nch) {
-                        float y[16];
-                        scores(c, y);
+                    for (int c = 0; c < 2 * T::kChunks; ++c)
+                        if (c < 2 * nch) {
+                            scores(c, y[c & 1]);
+                            if (c + 1 < 2 * nch) ask(c + 1, y[(c + 1) & 1]);
+                            uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) top = fmaxf(top, y[i]);
-                    }
-                // this warpgroup's P and sums are free once its last product is done
-                if (ok && jj >= 2) ok = mbar_wait(bar(s.pv_done[wg]), ((jj >> 1) - 1) & 1, to, p.status, abort);
-                if (bar_or(5 + wg, 128, fresh || top_v > kScaleRaise * sref || (live && top > kRaise) || !ok)) {
-                    // ---- raise the references (first tile: set them)
+                            for (int i = 0; i < 8; i += 2) {
+                                const float a = y[c & 1][i], b = y[c & 1][i + 1];
+                                top = fmaxf(fmaxf(top, a), b);
+                                const float ea = ex2(min_nan(a, kCap)), eb = ex2(min_nan(b, kCap));
+                                const uint64_t e = pair(live ? ea : 0.f, live ? eb : 0.f);
+                                l[c * 4 + (i >> 1)] = add2(l[c * 4 + (i >> 1)], e);
+                                float u, v;
+                                unpair(mul2(e, rt2), u, v);
+                                w[i >> 1] = pack_f16x2(u, v);
+                            }
+                            *reinterpret_cast<uint4 *>(prow + (c >> 1) * (kTile * 32) + (((c & 1) << 4) ^ flip)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    return top;
+                };
+                const bool must = fresh || top_v > kScaleRaise * sref;          // the same for every thread
+                bool raise = must;
+                if (!must) {
+                    const float top = weights();
+                    raise = bar_or(5 + wg, 128, (live && top > kRaise) || !ok);
+                }
+                if (raise) {
+                    // ---- raise the references (first tile: set them), and do the tile again
 #pragma unroll
                     for (int c = 0; c < T::kChunks; ++c)
                         if (c < nch) {
                             float y[16];
-                            scores(c, y);
-                            if (!live)
+                            ask(2 * c, y);
+                            scores(2 * c, y);
+                            ask(2 * c + 1, y + 8);
+                            scores(2 * c + 1, y + 8);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) y[i] = -INFINITY;
+                            for (int i = 0; i < 16; i += 2) {
+                                if (!must && live)                              // take this tile's weights back
+                                    l[c * 8 + (i >> 1)] = add2(l[c * 8 + (i >> 1)],
+                                                               pair(-ex2(min_nan(y[i], kCap)), -ex2(min_nan(y[i + 1], kCap))));
+                                if (!live) y[i] = y[i + 1] = -INFINITY;
+                            }
                             const float m = reduce16<true>(y, lane);
                             if (lane < 16) s.red[sw][c * 16 + lane_col(lane)] = m;
                         }
@@ -707,56 +852,33 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                                         fmaxf(s.red[wg * 4 + 2][tok], s.red[wg * 4 + 3][tok]));
                         if (!fresh) m = fmaxf(m, 0.f);
                         if (!(m > -INFINITY)) m = 0.f;
-                        s.delta[wg][tok] = m;
-                        s.mref[wg][tok] += m;
+                        s.delta[wg][tok] = ex2(-m);
+                        s.mneg[wg][tok] -= m;
                     }
                     named_bar(5 + wg, 128);
-                    const float ref = fresh || top_v > kScaleRaise * sref ? top_v : sref;
-                    const float fs = fresh ? 0.f : sref / ref;
+                    const float ref = must ? top_v : sref, fs = sref / ref;
                     sref = ref;
                     if (!fresh) {
-                        tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < T::kChunks; ++c)
                             if (c < nch) {
                                 float o[16];
-                                uint32_t *r = reinterpret_cast<uint32_t *>(o);
-                                tmem_ld_x16(tm_o + c * 16, r);
-                                tmem_ld_wait();
+                                tmem_ld_x16(tm_o + c * 16, reinterpret_cast<uint32_t *>(o));
+                                ld_done(o);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const float f = ex2(-s.delta[wg][c * 16 + i]);
-                                    l[c * 16 + i] *= f;
-                                    o[i] *= f * fs;
+                                for (int i = 0; i < 16; i += 2) {
+                                    const float f0 = s.delta[wg][c * 16 + i], f1 = s.delta[wg][c * 16 + i + 1];
+                                    l[c * 8 + (i >> 1)] = mul2(l[c * 8 + (i >> 1)], pair(f0, f1));
+                                    o[i] *= f0 * fs;
+                                    o[i + 1] *= f1 * fs;
                                 }
-                                tmem_st_x16(tm_o + c * 16, r);
+                                tmem_st_x16(tm_o + c * 16, reinterpret_cast<uint32_t *>(o));
                             }
                         tmem_st_wait();
-                        tc_fence_before();
                     }
+                    weights();
                 }
                 fresh = false;
-                // ---- weights
-                const float rt = kHead * (my.y / sref);
-                uint8_t *prow = sm + T::kOffP + wg * T::kPBytes + tok * 32;
-                const int flip = (tok >> 2) & 1;
-#pragma unroll
-                for (int c = 0; c < T::kChunks; ++c)
-                    if (c < nch) {
-                        float y[16];
-                        scores(c, y);
-                        uint32_t w[8];
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float e0 = live ? ex2(y[i]) : 0.f, e1 = live ? ex2(y[i + 1]) : 0.f;
-                            l[c * 16 + i] += e0;
-                            l[c * 16 + i + 1] += e1;
-                            w[i >> 1] = pack_f16x2(e0 * rt, e1 * rt);
-                        }
-                        uint4 *dst = reinterpret_cast<uint4 *>(prow + c * (kTile * 32));
-                        dst[flip] = make_uint4(w[0], w[1], w[2], w[3]);
-                        dst[flip ^ 1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    }
                 tc_fence_before();
                 fence_async_shared();
                 __syncwarp();
@@ -773,47 +895,50 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < T::kChunks; ++c)
                 if (c < nch) {
-                    const float x = reduce16<false>(l + c * 16, lane);
+                    float y[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) unpair(l[c * 8 + i], y[2 * i], y[2 * i + 1]);
+                    const float x = reduce16<false>(y, lane);
                     if (lane < 16) s.red[sw][c * 16 + lane_col(lane)] = x;
                 }
             named_bar(5 + wg, 128);
             if (tok < npad) {
                 s.lsum[wg][tok] = (s.red[wg * 4][tok] + s.red[wg * 4 + 1][tok]) + (s.red[wg * 4 + 2][tok] + s.red[wg * 4 + 3][tok]);
-                if (!used) s.mref[wg][tok] = -INFINITY;
+                if (!used) s.mneg[wg][tok] = INFINITY;         // no maximum: this warpgroup had no tile
             }
-            if (tok == 0) s.back[wg] = sref / kHead;
+            if (tok == 0) s.sref[wg] = sref;
             if (bar_or(4, kSoft, !ok)) {
                 ok = false;
                 break;
             }
-            tc_fence_after();
             const int64_t col0 = (int64_t)g.lo * p.Hq + (int64_t)(g.h * g.rows + g.row0) * p.G + (int64_t)cta * kCols;
+            if (wg == 0 && tok < npad) {
+                const float m0 = -s.mneg[0][tok], m1 = -s.mneg[1][tok], m = fmaxf(m0, m1);
+                const float f0 = m0 > -INFINITY ? ex2(m0 - m) : 0.f, f1 = m1 > -INFINITY ? ex2(m1 - m) : 0.f;
+                s.delta[0][tok] = f0 * s.sref[0] / kHead;
+                s.delta[1][tok] = f1 * s.sref[1] / kHead;
+                if (tok < ncol)
+                    p.ml[col0 + tok] = make_float2(m, (f0 > 0.f ? f0 * s.lsum[0][tok] : 0.f) + (f1 > 0.f ? f1 * s.lsum[1][tok] : 0.f));
+            }
+            named_bar(4, kSoft);
+            tc_fence_after();
+            // a warpgroup without a tile has left no sums: whatever stands there counts for nothing
+            const bool has0 = s.sref[0] > 0.f, has1 = s.sref[1] > 0.f;
 #pragma unroll
             for (int c = 0; c < T::kChunks; ++c)
                 if (c < nch && (c & 1) == wg) {
                     float o0[16], o1[16];
-                    tmem_ld_x16(tmem + lanes + kTmO + c * 16, reinterpret_cast<uint32_t *>(o0));
-                    tmem_ld_x16(tmem + lanes + kTmO + 128 + c * 16, reinterpret_cast<uint32_t *>(o1));
-                    tmem_ld_wait();
+                    tmem_ld_x16(tmem + lanes + T::kTmO + c * 16, reinterpret_cast<uint32_t *>(o0));
+                    tmem_ld_x16(tmem + lanes + T::kTmO + kCols + c * 16, reinterpret_cast<uint32_t *>(o1));
+                    ld_done(o0);
+                    ld_done(o1);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int n = c * 16 + i;
-                        if (n < ncol) {
-                            const float m0 = s.mref[0][n], m1 = s.mref[1][n], m = fmaxf(m0, m1);
-                            float x = 0.f;
-                            if (m0 > -INFINITY) x = o0[i] * (ex2(m0 - m) * s.back[0]);
-                            if (m1 > -INFINITY) x = fmaf(o1[i], ex2(m1 - m) * s.back[1], x);
-                            p.part[(col0 + n) * kD + tok] = x;
-                        }
+                        if (n < ncol)
+                            p.part[(col0 + n) * kD + tok] = (has0 ? o0[i] * s.delta[0][n] : 0.f) + (has1 ? o1[i] * s.delta[1][n] : 0.f);
                     }
                 }
-            if (wg == 0 && tok < ncol) {
-                const float m0 = s.mref[0][tok], m1 = s.mref[1][tok], m = fmaxf(m0, m1);
-                float x = 0.f;
-                if (m0 > -INFINITY) x = s.lsum[0][tok] * ex2(m0 - m);
-                if (m1 > -INFINITY) x = fmaf(s.lsum[1][tok], ex2(m1 - m), x);
-                p.ml[col0 + tok] = make_float2(m, x);
-            }
             tc_fence_before();
             at += g.t1 - g.t0;
         }
@@ -821,7 +946,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, kTmCols);
+    if (warp == 1) tmem_dealloc(tmem, T::kTmCols);
 }
 
 // ---------------------------------------------------------------------------
@@ -883,7 +1008,7 @@ __global__ void __launch_bounds__(128) k_attn_join(const AttnParams p)
     // the shares that hold a part of this row's segment
     pdl_wait();
     const int64_t total = __ldcg(p.plan + p.n_req), share = (total + p.ctas - 1) / p.ctas;
-    const int nt = (len + kTile - 1) / kTile;
+    const int nt = total ? (len + kTile - 1) / kTile : 0;
     const int fit = p.cols / G, i0 = row - lo, grp = i0 / group_rows(rows, fit);
     const int64_t a0 = __ldcg(p.plan + r) + (int64_t)(h * group_count(rows, fit) + grp) * nt;
     const int cta0 = nt ? (int)(a0 / share) : 0, cta1 = nt ? (int)((a0 + nt - 1) / share) : -1;
@@ -958,7 +1083,7 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-size_t plan_bytes() { return (size_t)((kMaxReq + 1) * 8 + 255) / 256 * 256; }
+size_t plan_bytes() { return (size_t)((kMaxReq + 1) * 4 + 255) / 256 * 256; }
 size_t part_columns(int32_t R, int32_t Hq, int ctas) { return (size_t)R * Hq + (size_t)ctas * kMaxCols; }
 
 }  // namespace
@@ -1005,7 +1130,7 @@ int launch_attn(const AttnArgs &a, void *stream)
     p.out = a.out;
     uint8_t *w = static_cast<uint8_t *>(a.work);
     const size_t cols = part_columns(a.R, a.Hq, p.ctas);
-    p.plan = reinterpret_cast<int64_t *>(w);
+    p.plan = reinterpret_cast<int32_t *>(w);
     p.part = reinterpret_cast<float *>(w + plan_bytes());
     p.ml = reinterpret_cast<float2 *>(w + plan_bytes() + cols * kD * 4);
     p.status = a.status;
@@ -1014,13 +1139,22 @@ int launch_attn(const AttnArgs &a, void *stream)
 
     EncodeTiledFn fn = encode_fn();
     if (!fn) return (int)cudaErrorNotSupported;
-    CUtensorMap kmap;
-    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)a.n_blocks * a.H * a.bt};
-    const cuuint64_t strides[1] = {(cuuint64_t)kD};
-    const cuuint32_t box[2] = {(cuuint32_t)kD, (cuuint32_t)a.bt}, es[2] = {1, 1};
-    if (fn(&kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(a.kc), dims, strides, box, es,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    // K as rows of a token's 128 codes, V as rows of a dimension's bt codes; a
+    // block of a head is one box, swizzled over its row length
+    CUtensorMap kmap, vmap;
+    auto encode = [&](CUtensorMap *m, const uint8_t *pool, int width, int height, CUtensorMapSwizzle swz) {
+        const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)a.n_blocks * a.H * height};
+        const cuuint64_t strides[1] = {(cuuint64_t)width};
+        const cuuint32_t box[2] = {(cuuint32_t)width, (cuuint32_t)height}, es[2] = {1, 1};
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(pool), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (!encode(&kmap, a.kc, kD, a.bt, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode(&vmap, a.vc, a.bt, kD,
+                a.bt == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                : a.bt == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                             : CU_TENSOR_MAP_SWIZZLE_128B))
         return (int)cudaErrorInvalidValue;
     // columns of a segment: the least shape that holds an average request's rows and one row's heads
     const int64_t avg = (int64_t)((a.R + a.n_req - 1) / a.n_req) * p.G;
@@ -1029,7 +1163,15 @@ int launch_attn(const AttnArgs &a, void *stream)
     auto go = [&](auto kernel, int threads, int bytes) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return;
-        kernel<<<p.ctas, threads, bytes, st>>>(kmap, p);
+        static const int regs = [&] {       // the register shares need a launch with this many
+            cudaFuncAttributes f{};
+            return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
+        }();
+        if (regs < kRegsLaunch) {
+            e = cudaErrorInvalidConfiguration;
+            return;
+        }
+        kernel<<<p.ctas, threads, bytes, st>>>(kmap, vmap, p);
         e = cudaGetLastError();
     };
     if (p.cols == 16)

@@ -873,7 +873,7 @@ w12_status cache_ok(const w12_kv_cache *c, int32_t n_req)
     if (c->head_dim != kKvDim || n_req > kMaxBudget || c->n_kv_heads > 1024) return W12_E_UNSUPPORTED;
     if (c->block_tokens != 32 && c->block_tokens != 64 && c->block_tokens != 128) return W12_E_UNSUPPORTED;
     // rows and positions are 32-bit numbers in the kernels and in the tensor maps
-    if ((int64_t)c->n_blocks * c->n_kv_heads > INT32_MAX / c->block_tokens) return W12_E_UNSUPPORTED;
+    if ((int64_t)c->n_blocks * c->n_kv_heads > INT32_MAX / kKvDim) return W12_E_UNSUPPORTED;
     if (c->max_blocks > INT32_MAX / c->block_tokens - 1) return W12_E_UNSUPPORTED;
     return W12_OK;
 }
