@@ -520,10 +520,10 @@ typedef struct {
  * the struct, or rot_dim 0: no rotation.
  */
 typedef struct {
-    int32_t rot_dim;             /* even, <= head_dim */
+    int32_t rot_dim;             /* a multiple of 8, <= head_dim */
     int32_t adjacent;
     int32_t max_pos;             /* positions in the tables */
-    const float *cos, *sin;      /* device [max_pos][rot_dim / 2] */
+    const float *cos, *sin;      /* device [max_pos][rot_dim / 2], 16-byte aligned */
 } w12_rope;
 
 /*

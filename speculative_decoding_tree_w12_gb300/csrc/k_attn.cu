@@ -60,6 +60,7 @@ constexpr int kStack = 48;                 // columns up to which Q's pieces are
 constexpr int kMaxCols = 80;               // query columns of a segment, see Shape
 constexpr int kScaleRing = 16;             // tiles whose block scales are kept (the copies run at most 8 ahead of their readers)
 constexpr int kMaxReq = kMaxBudget;
+constexpr uint64_t kDrainNs = 1000000000;  // limit of the waits after a failed one
 constexpr int kSoft = 256;                 // softmax threads
 // registers a thread: at launch (640 threads under 65536 registers), of the
 // softmax warps (a normaliser for each of 80 columns and 32 scores in flight),
@@ -73,7 +74,7 @@ constexpr float kScaleRaise = 16.f;        // ... and a value scale its referenc
 
 struct AttnParams {
     int32_t H, Hq, G, bt, n_blocks, max_blocks, n_req, R, ctas;
-    int32_t cols;                           // query columns of a segment at most
+    int32_t cols, fit;                      // query columns of a segment at most; rows of so many
     int64_t q_stride, k_stride, v_stride;
     const uint8_t *kc, *vc;
     const float *ks, *vs;
@@ -87,19 +88,13 @@ struct AttnParams {
     float *part;                            // [R * Hq + ctas * cols][kD] sums
     float2 *ml;                             // [R * Hq + ctas * cols] maximum (log2), normaliser
     int32_t *status;
-    uint64_t timeout_ns;
+    int32_t sleeps;                         // of kWaitSleepNs: a wait's limit
 };
 
 __device__ __forceinline__ void fail(int32_t *status) { atomicCAS(status, 0, (int32_t)W12_E_INVAL); }
 
 // rows of a request's groups: as many as fit the columns, evenly
 __device__ __forceinline__ int group_count(int rows, int fit) { return (rows + fit - 1) / fit; }
-__device__ __forceinline__ int group_rows(int rows, int fit)
-{
-    const int g = group_count(rows, fit);
-    return (rows + g - 1) / g;
-}
-
 // a request's rows and cached tokens; false where they contradict each other or the tables
 __device__ __forceinline__ bool request_ok(const AttnParams &p, int r, int &lo, int &rows, int &len)
 {
@@ -123,67 +118,65 @@ __device__ __forceinline__ int request_of(const AttnParams &p, int row)
 
 // Four consecutive elements d0 .. d0 + 3 of a BF16 row and what turns them by
 // position pos; loaded apart from the arithmetic, so that the loads of several
-// rows are in flight together.
+// rows are in flight together.  The rotated part is a multiple of 8 wide, so a
+// pair's two halves lie in two such groups, or in one with adjacent pairs.
 struct Raw4 {
     uint2 w, v;                             // the elements, their partners
-    float c[4], s[4];
+    float4 c, s;
 };
-
-__device__ __forceinline__ void load4_row(Raw4 &x, const uint16_t *row, int d0, const RopeArgs &r)
-{
-    x.w = __ldg(reinterpret_cast<const uint2 *>(row + d0));
-    x.v = make_uint2(0, 0);
-    if (d0 >= r.rot) return;
-    const int half = r.rot >> 1;
-    if (r.adjacent) {
-        x.v = make_uint2((x.w.x >> 16) | (x.w.x << 16), (x.w.y >> 16) | (x.w.y << 16));
-        if (d0 + 2 >= r.rot) x.v.y = 0;     // rot ends in the middle of the four
-    } else if (r.rot & 7) {                 // partners that straddle the groups of four
-        uint32_t y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int d = d0 + i;
-            y[i] = d < r.rot ? row[d < half ? d + half : d - half] : 0;
-        }
-        x.v = make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
-    } else {
-        x.v = __ldg(reinterpret_cast<const uint2 *>(row + (d0 < half ? d0 + half : d0 - half)));
-    }
-}
-
-__device__ __forceinline__ void load4_turn(Raw4 &x, int d0, int pos, const RopeArgs &r)
-{
-    const int half = r.rot >> 1;
-    const float *ct = r.cos + (int64_t)pos * half, *st = r.sin + (int64_t)pos * half;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int d = d0 + i, f = r.adjacent ? d >> 1 : d < half ? d : d - half;
-        const bool in = d < r.rot;
-        x.c[i] = in ? __ldg(ct + f) : 1.f;
-        x.s[i] = in ? __ldg(st + f) : 0.f;
-    }
-}
 
 __device__ __forceinline__ void load4(Raw4 &x, const uint16_t *row, int d0, int pos, const RopeArgs &r)
 {
-    load4_row(x, row, d0, r);
-    load4_turn(x, d0, pos, r);
+    x.w = __ldg(reinterpret_cast<const uint2 *>(row + d0));
+    x.v = make_uint2(0, 0);
+    x.c = make_float4(1.f, 1.f, 1.f, 1.f);
+    x.s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (d0 >= r.rot) return;
+    const int half = r.rot >> 1;
+    const int64_t t = (int64_t)pos * half;
+    if (r.adjacent) {
+        x.v = make_uint2((x.w.x >> 16) | (x.w.x << 16), (x.w.y >> 16) | (x.w.y << 16));
+        const float2 c = __ldg(reinterpret_cast<const float2 *>(r.cos + t + (d0 >> 1)));
+        const float2 s = __ldg(reinterpret_cast<const float2 *>(r.sin + t + (d0 >> 1)));
+        x.c = make_float4(c.x, c.x, c.y, c.y);
+        x.s = make_float4(-s.x, s.x, -s.y, s.y);
+    } else {
+        const bool second = d0 >= half;
+        const int o = second ? d0 - half : d0 + half, f = second ? o : d0;
+        x.v = __ldg(reinterpret_cast<const uint2 *>(row + o));
+        x.c = __ldg(reinterpret_cast<const float4 *>(r.cos + t + f));
+        x.s = __ldg(reinterpret_cast<const float4 *>(r.sin + t + f));
+        if (!second) x.s = make_float4(-x.s.x, -x.s.y, -x.s.z, -x.s.w);
+    }
 }
 
-__device__ __forceinline__ void turn4(const Raw4 &r, int d0, const RopeArgs &rope, float (&x)[4])
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ float4 turn4(const Raw4 &r)
 {
-    x[0] = bf16_f32((uint16_t)r.w.x);
-    x[1] = bf16_f32((uint16_t)(r.w.x >> 16));
-    x[2] = bf16_f32((uint16_t)r.w.y);
-    x[3] = bf16_f32((uint16_t)(r.w.y >> 16));
-    const float y[4] = {bf16_f32((uint16_t)r.v.x), bf16_f32((uint16_t)(r.v.x >> 16)), bf16_f32((uint16_t)r.v.y),
-                        bf16_f32((uint16_t)(r.v.y >> 16))};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool second = rope.adjacent ? (i & 1) : d0 + i >= (rope.rot >> 1);
-        const float a = __fmul_rn(x[i], r.c[i]), b = __fmul_rn(y[i], r.s[i]);
-        x[i] = second ? __fadd_rn(a, b) : __fsub_rn(a, b);
+    return make_float4(__fadd_rn(__fmul_rn(bf16_lo(r.w.x), r.c.x), __fmul_rn(bf16_lo(r.v.x), r.s.x)),
+                       __fadd_rn(__fmul_rn(bf16_hi(r.w.x), r.c.y), __fmul_rn(bf16_hi(r.v.x), r.s.y)),
+                       __fadd_rn(__fmul_rn(bf16_lo(r.w.y), r.c.z), __fmul_rn(bf16_lo(r.v.y), r.s.z)),
+                       __fadd_rn(__fmul_rn(bf16_hi(r.w.y), r.c.w), __fmul_rn(bf16_hi(r.v.y), r.s.w)));
+}
+
+// Wait for a phase: false after about timeout_ns (W12_E_TIMEOUT in *status) or
+// once *abort is set.  As w12d::mbar_wait, counting sleeps instead of reading
+// the clock: it is inlined at every wait, and its size counts.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, int32_t sleeps, int32_t *status,
+                                           volatile int32_t *abort)
+{
+    bool done = mbar_try_wait(bar, parity);
+    for (int32_t n = 0; !done; ++n) {
+        done = mbar_try_wait_sleep(bar, parity, kWaitSleepNs);
+        if (!done && (n >= sleeps || *abort)) {
+            if (!*abort) atomicCAS(status, 0, (int32_t)W12_E_TIMEOUT);
+            *abort = 1;
+            break;
+        }
     }
+    return done;
 }
 
 // ---------------------------------------------------------------------------
@@ -260,19 +253,16 @@ struct Seg {
 // the segment that tile `at` lies in, up to tile `end` of the whole list
 __device__ __forceinline__ Seg segment(const AttnParams &p, const Shared &sh, int32_t at, int32_t end)
 {
-    int a = 0, b = p.n_req;                 // pre[a] <= at < pre[b]
-    while (b - a > 1) {
-        const int m = (a + b) >> 1;
-        if (sh.pre[m] <= at) a = m;
-        else b = m;
-    }
+    int a = 0;                              // pre[a] <= at < pre[a + 1]
+    for (int step = 512; step; step >>= 1)
+        if (a + step < p.n_req && sh.pre[a + step] <= at) a += step;
     Seg s;
     s.r = a;
     s.lo = sh.lo[a];
     s.rows = sh.rows[a];
     s.len = sh.len[a];
     const uint32_t nt = (uint32_t)(s.len + kTile - 1) / kTile;
-    const int fit = p.cols / p.G, g = group_count(s.rows, fit), per = group_rows(s.rows, fit);
+    const int g = group_count(s.rows, p.fit), per = (s.rows + g - 1) / g;
     const uint32_t i = (uint32_t)(at - sh.pre[a]), seg = i / nt;
     s.t0 = (int)(i - seg * nt);
     s.t1 = min((int)nt, s.t0 + (end - at));
@@ -326,10 +316,17 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return d;
 }
 
-__device__ __forceinline__ float min_nan(float a, float b)
+// the larger, or NaN
+__device__ __forceinline__ float max_nan(float a, float b)
 {
     float d;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -338,17 +335,14 @@ __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, float *r)
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
-                 : "r"(taddr)
-                 : "memory");
+                 : "r"(taddr));
 }
 
 // the loads before it are complete, and these registers of theirs are read after it only
 __device__ __forceinline__ void ld_done8(float *y)
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(y[0]), "+f"(y[1]), "+f"(y[2]), "+f"(y[3]), "+f"(y[4]), "+f"(y[5]), "+f"(y[6]), "+f"(y[7])
-                 :
-                 : "memory");
+                 : "+f"(y[0]), "+f"(y[1]), "+f"(y[2]), "+f"(y[3]), "+f"(y[4]), "+f"(y[5]), "+f"(y[6]), "+f"(y[7]));
 }
 
 __device__ __forceinline__ void ld_done(float (&y)[16])
@@ -375,34 +369,26 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return d;
 }
 
-// Reduce 16 columns over the 32 lanes of a warp: afterwards every lane holds
-// the result of column lane_col(lane).  16 shuffles instead of 80.
+// The maximum (or NaN) of each of 16 columns over the 32 lanes of a warp:
+// afterwards every lane holds that of column lane_col(lane).  16 shuffles
+// instead of 80.
 __device__ __forceinline__ int lane_col(int lane)
 {
     return ((lane & 1) << 3) | ((lane & 2) << 1) | ((lane & 4) >> 1) | ((lane & 8) >> 3);
 }
 
-template <bool kMax>
-__device__ __forceinline__ float reduce16(const float *x, int lane)
+__device__ __forceinline__ float max16(float (&v)[16], int lane)
 {
-    float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const bool up = lane & 1;
-        const float o = __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + 8], 1), k = up ? x[i + 8] : x[i];
-        v[i] = kMax ? fmaxf(k, o) : k + o;
-    }
-#pragma unroll
-    for (int n = 4, bit = 2; n; n >>= 1, bit <<= 1) {
+    for (int n = 8, bit = 1; n; n >>= 1, bit <<= 1) {
+        const bool up = lane & bit;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            const bool up = lane & bit;
             const float o = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], bit), k = up ? v[i + n] : v[i];
-            v[i] = kMax ? fmaxf(k, o) : k + o;
+            v[i] = max_nan(k, o);
         }
     }
-    const float o = __shfl_xor_sync(0xffffffffu, v[0], 16);
-    return kMax ? fmaxf(v[0], o) : v[0] + o;
+    return max_nan(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
 template <int kCols>
@@ -418,13 +404,13 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
     const int cta = blockIdx.x;
     auto bar = [&](const uint64_t &b) { return smem_u32(&b); };
 
+    pdl_launch_dependents();                              // the join may start wherever there is room
     // ---- the tile list: tiles of every request, summed up
-    const int fit = kCols / p.G;
     int64_t mine = 0;
     if (tid < p.n_req) {
         int lo, rows, len;
         if (request_ok(p, tid, lo, rows, len))
-            mine = rows ? (int64_t)((len + kTile - 1) / kTile) * p.H * group_count(rows, fit) : 0;
+            mine = rows ? (int64_t)((len + kTile - 1) / kTile) * p.H * group_count(rows, p.fit) : 0;
         else
             fail(p.status);
         s.lo[tid] = (uint16_t)lo;
@@ -483,13 +469,13 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
     const int bs = p.bt == 32 ? 5 : p.bt == 64 ? 6 : 7;   // log2 of a block's tokens
     const int nb = kTile >> bs;                           // blocks of a tile
     volatile int32_t *abort = &s.abort;
-    const uint64_t to = p.timeout_ns;
+    const int32_t to = p.sleeps;
     // after a wait that ran out: products in flight end before tensor memory is freed
     auto drain = [&](const uint64_t &b) {
         tc_commit(bar(b));
         const uint64_t t0 = globaltimer();
         while (!mbar_try_wait_sleep(bar(b), 0, kWaitSleepNs))
-            if (globaltimer() - t0 > to) break;
+            if (globaltimer() - t0 > kDrainNs) break;
     };
 
     if (warp == 0 || warp == 2) {
@@ -535,7 +521,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                     const int n = min(nb, b1 - (b + l));      // blocks of this tile that hold tokens
                     const bool in = lane >= l && lane < l + nb;
                     const uint32_t f = full + st * 8;
-                    ok = __all_sync(0xffffffffu, mbar_wait(empty + st * 8, par, to, p.status, abort));
+                    ok = __all_sync(0xffffffffu, wait_phase(empty + st * 8, par, to, p.status, abort));
                     if (!ok) break;
                     if (is_k) {
                         if (in) s.scale[j % kScaleRing][lane - l] = sc;
@@ -559,7 +545,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
             const uint64_t t0 = globaltimer();
             for (uint32_t i = j >= (uint32_t)stages ? j - stages : 0; i < j; ++i)
                 while (!mbar_try_wait_sleep(full + i % stages * 8, (i / stages) & 1, kWaitSleepNs))
-                    if (globaltimer() - t0 > to) break;
+                    if (globaltimer() - t0 > kDrainNs) break;
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ scores: S^T = K Q^T
@@ -572,11 +558,11 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                 const Seg g = segment(p, s, at, end);
                 const int n = (g.nrows * p.G + 15) & ~15;
                 const uint32_t idesc = idesc_e4m3_f32(kTile, T::kStacked ? 3 * kCols : n);
-                ok = mbar_wait(bar(s.q_full), q & 1, to, p.status, abort);
+                ok = wait_phase(bar(s.q_full), q & 1, to, p.status, abort);
                 for (int t = g.t0; t < g.t1 && ok; ++t, ++j) {
                     const int b = j & 1;
-                    ok = (j < 2 || mbar_wait(bar(s.s_empty[b]), ((j >> 1) - 1) & 1, to, p.status, abort)) &&
-                         mbar_wait(bar(s.k_full[st]), par, to, p.status, abort);
+                    ok = (j < 2 || wait_phase(bar(s.s_empty[b]), ((j >> 1) - 1) & 1, to, p.status, abort)) &&
+                         wait_phase(bar(s.k_full[st]), par, to, p.status, abort);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t ka = kd + (uint64_t)(st * (T::kKBytes >> 4));
@@ -606,8 +592,8 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                 const uint32_t idesc = idesc_f16_f32_bmn(kD, (g.nrows * p.G + 15) & ~15);
                 for (int t = g.t0; t < g.t1 && ok; ++t, ++j) {
                     const int b = j & 1;
-                    ok = mbar_wait(bar(s.v16_full[b]), (j >> 1) & 1, to, p.status, abort) &&
-                         mbar_wait(bar(s.p_full[b]), (j >> 1) & 1, to, p.status, abort);
+                    ok = wait_phase(bar(s.v16_full[b]), (j >> 1) & 1, to, p.status, abort) &&
+                         wait_phase(bar(s.p_full[b]), (j >> 1) & 1, to, p.status, abort);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t keep = t - g.t0 >= 2;      // each parity's first tile starts its sums
@@ -637,13 +623,13 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
             for (int t = g.t0; t < g.t1; ++t, ++j) {
                 if ((int)(j & 1) != wg) continue;
                 const int st = j % T::kStV;
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(s.v_full[st]), (j / T::kStV) & 1, to, p.status, abort) &&
-                                                 (j < 2 || mbar_wait(bar(s.pv_done[wg]), ((j >> 1) - 1) & 1, to, p.status, abort)));
+                ok = __all_sync(0xffffffffu, wait_phase(bar(s.v_full[st]), (j / T::kStV) & 1, to, p.status, abort) &&
+                                                 (j < 2 || wait_phase(bar(s.pv_done[wg]), ((j >> 1) - 1) & 1, to, p.status, abort)));
                 if (!ok) break;
                 tc_fence_after();
                 const int valid = min(kTile, g.len - t * kTile);
                 const uint8_t *src = sm + T::kOffV + st * T::kKBytes + (d << bs);
-#pragma unroll
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint32_t y[32];
 #pragma unroll
@@ -654,10 +640,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                         uint32_t x[4] = {w.x, w.y, w.z, w.w};
                         if (tok + 16 > valid)                                 // what lies past the last token is not a value
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int left = valid - tok - 4 * q;
-                                x[q] &= left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-                            }
+                            for (int q = 0; q < 4; ++q) x[q] &= __funnelshift_lc(0xFFFFFFFFu, 0u, 8 * max(valid - tok - 4 * q, 0));
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             y[i * 8 + 2 * q] = e4m3x2_f16x2(x[q] & 0xFFFFu);
@@ -692,51 +675,41 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
             // ---- Q: turned, scaled to E4M3's range by a power of two, in three pieces
             named_bar(4, kSoft);                              // the last segment's columns are done with
             const int n_q = T::kStacked ? kCols : npad;       // stacked pieces are products of all their columns
-#pragma unroll 1
-            for (int n0 = sw; n0 < n_q; n0 += 8 * 2) {
-                Raw4 rw[2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int n = min(n0 + 8 * u, ncol - 1), row = g.lo + g.row0 + n / p.G;
-                    const uint16_t *q = p.q + (int64_t)row * p.q_stride + (int64_t)(g.h * p.G + n % p.G) * kD;
-                    int pos = g.len + (int)__ldg(p.depth + row);
-                    load4_row(rw[u], q, lane * 4, p.rope);
-                    if (p.rope.rot && pos >= p.rope.max_pos) {
-                        fail(p.status);
-                        pos = 0;
-                    }
-                    load4_turn(rw[u], lane * 4, pos, p.rope);
+            // A column ahead: its loads are in flight while the last one is split.
+            Raw4 rw;
+            auto fetch = [&](int n) {
+                const int i = min(n, ncol - 1), row = g.lo + g.row0 + i / p.G;
+                int pos = g.len + (int)__ldg(p.depth + row);
+                if (p.rope.rot && pos >= p.rope.max_pos) {
+                    fail(p.status);
+                    pos = 0;
                 }
+                load4(rw, p.q + (int64_t)row * p.q_stride + (int64_t)(g.h * p.G + i % p.G) * kD, lane * 4, pos, p.rope);
+            };
+            fetch(sw);
+#pragma unroll 1
+            for (int n = sw; n < n_q; n += 8) {
+                float4 x = turn4(rw);
+                if (n + 8 < n_q) fetch(n + 8);
+                float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int n = n0 + 8 * u;
-                    if (n >= n_q) break;
-                    float x[4];
-                    turn4(rw[u], lane * 4, p.rope, x);
-                    float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const float qs = block_scale(top), f = n < ncol ? 1.f / qs : 0.f;
+                // infinities have no code: the column becomes NaN, as their products would
+                const float qi = top < INFINITY ? f : __int_as_float(0x7FC00000);
+                x = make_float4(x.x * qi, x.y * qi, x.z * qi, x.w * qi);
+                const uint32_t dst = (uint32_t)(n * kD + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4);
 #pragma unroll
-                    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    const float qs = block_scale(top), qi = 1.f / qs;
-                    const bool pad = n >= ncol;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = pad ? 0.f : x[i] * qi;
-                    const uint32_t dst = (uint32_t)(n * kD + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4);
-#pragma unroll
-                    for (int c = 0; c < 3; ++c) {
-                        uint32_t w = 0;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t code = to_e4m3(x[i]);
-                            w |= code << (8 * i);
-                            x[i] -= e4m3_f32((uint8_t)code);
-                        }
-                        *reinterpret_cast<uint32_t *>(sm + T::kOffQ + c * T::kQBytes + dst) = w;
-                    }
-                    if (lane == 0) {
-                        s.cf[n] = pad ? 0.f : qs * p.scale2;
-                        s.mneg[0][n] = 0.f;
-                        s.mneg[1][n] = 0.f;
-                    }
+                for (int c = 0; c < 3; ++c) {
+                    const uint32_t lo = to_e4m3x2(x.x, x.y), hi = to_e4m3x2(x.z, x.w);
+                    *reinterpret_cast<uint32_t *>(sm + T::kOffQ + c * T::kQBytes + dst) = lo | (hi << 16);
+                    const float2 a = f16x2_f32(e4m3x2_f16x2(lo)), b = f16x2_f32(e4m3x2_f16x2(hi));
+                    x = make_float4(x.x - a.x, x.y - a.y, x.z - b.x, x.w - b.y);
+                }
+                if (lane == 0) {
+                    s.cf[n] = n < ncol ? qs * p.scale2 : 0.f;
+                    s.mneg[0][n] = 0.f;
+                    s.mneg[1][n] = 0.f;
                 }
             }
             fence_async_shared();
@@ -752,9 +725,9 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
             j += g.t1 - g.t0;
             for (uint32_t jj = j0 + ((j0 ^ wg) & 1); jj < j; jj += 2) {
                 const int t = g.t0 + (int)(jj - j0);
-                ok = mbar_wait(bar(s.s_full[wg]), (jj >> 1) & 1, to, p.status, abort);
+                ok = wait_phase(bar(s.s_full[wg]), (jj >> 1) & 1, to, p.status, abort);
                 // this warpgroup's P and sums are free once its last product is done
-                if (ok && jj >= 2) ok = mbar_wait(bar(s.pv_done[wg]), ((jj >> 1) - 1) & 1, to, p.status, abort);
+                if (ok && jj >= 2) ok = wait_phase(bar(s.pv_done[wg]), ((jj >> 1) - 1) & 1, to, p.status, abort);
                 __syncwarp();
                 tc_fence_after();
                 const float2 my = s.scale[jj % kScaleRing][tok >> bs];
@@ -787,27 +760,30 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                 // the tile's weights into P and the normalisers; returns this
                 // token's largest score, over kRaise if the references have to
                 // be raised first (the weights are held finite until then)
-                auto weights = [&]() -> float {
-                    const float rt = kHead * (my.y / sref);
-                    const uint64_t rt2 = pair(rt, rt);
+                auto weights = [&](float sign) -> float {
+                    const float rt = kHead * (my.y / sref), cap = live ? kCap : -INFINITY;   // a dead token weighs nothing
+                    const uint64_t rt2 = pair(rt, rt), sg2 = pair(sign, sign);
                     uint8_t *prow = sm + T::kOffP + wg * T::kPBytes + tok * 32;
                     const int flip = ((tok >> 2) & 1) << 4;
                     float top = -INFINITY;
-                    float y[2][8];
+                    float y[3][8];                            // one step's weights, the next's scores, the one's after that on their way
                     ask(0, y[0]);
+                    scores(0, y[0]);
+                    ask(1, y[1]);
 #pragma unroll
                     for (int c = 0; c < 2 * T::kChunks; ++c)
                         if (c < 2 * nch) {
-                            scores(c, y[c & 1]);
-                            if (c + 1 < 2 * nch) ask(c + 1, y[(c + 1) & 1]);
+                            if (c + 1 < 2 * T::kChunks && c + 1 < 2 * nch) {
+                                scores(c + 1, y[(c + 1) % 3]);
+                                if (c + 2 < 2 * T::kChunks && c + 2 < 2 * nch) ask(c + 2, y[(c + 2) % 3]);
+                            }
                             uint32_t w[4];
 #pragma unroll
                             for (int i = 0; i < 8; i += 2) {
-                                const float a = y[c & 1][i], b = y[c & 1][i + 1];
-                                top = fmaxf(fmaxf(top, a), b);
-                                const float ea = ex2(min_nan(a, kCap)), eb = ex2(min_nan(b, kCap));
-                                const uint64_t e = pair(live ? ea : 0.f, live ? eb : 0.f);
-                                l[c * 4 + (i >> 1)] = add2(l[c * 4 + (i >> 1)], e);
+                                const float a = y[c % 3][i], b = y[c % 3][i + 1];
+                                top = max_nan(top, a, b);
+                                const uint64_t e = pair(ex2(fminf(a, cap)), ex2(fminf(b, cap)));
+                                l[c * 4 + (i >> 1)] = fma2(e, sg2, l[c * 4 + (i >> 1)]);
                                 float u, v;
                                 unpair(mul2(e, rt2), u, v);
                                 w[i >> 1] = pack_f16x2(u, v);
@@ -817,67 +793,69 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                         }
                     return top;
                 };
-                const bool must = fresh || top_v > kScaleRaise * sref;          // the same for every thread
-                bool raise = must;
-                if (!must) {
-                    const float top = weights();
-                    raise = bar_or(5 + wg, 128, (live && top > kRaise) || !ok);
-                }
-                if (raise) {
-                    // ---- raise the references (first tile: set them), and do the tile again
+                // Raise the references (first tile: set them).  A column with a
+                // NaN among its scores gets a NaN for its raise, and so carries
+                // it into its normaliser and sums.
+                auto raise = [&](bool must) -> bool {
+#pragma unroll 1
+                    for (int c = 0; c < nch; ++c) {
+                        float y[16];
+                        ask(2 * c, y);
+                        scores(2 * c, y);
+                        ask(2 * c + 1, y + 8);
+                        scores(2 * c + 1, y + 8);
 #pragma unroll
-                    for (int c = 0; c < T::kChunks; ++c)
-                        if (c < nch) {
-                            float y[16];
-                            ask(2 * c, y);
-                            scores(2 * c, y);
-                            ask(2 * c + 1, y + 8);
-                            scores(2 * c + 1, y + 8);
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                if (!must && live)                              // take this tile's weights back
-                                    l[c * 8 + (i >> 1)] = add2(l[c * 8 + (i >> 1)],
-                                                               pair(-ex2(min_nan(y[i], kCap)), -ex2(min_nan(y[i + 1], kCap))));
-                                if (!live) y[i] = y[i + 1] = -INFINITY;
-                            }
-                            const float m = reduce16<true>(y, lane);
-                            if (lane < 16) s.red[sw][c * 16 + lane_col(lane)] = m;
-                        }
-                    if (bar_or(5 + wg, 128, !ok)) {
-                        ok = false;
-                        break;
+                        for (int i = 0; i < 16; ++i) y[i] = live ? y[i] : -INFINITY;
+                        const float m = max16(y, lane);
+                        if (lane < 16) s.red[sw][c * 16 + lane_col(lane)] = m;
                     }
+                    if (bar_or(5 + wg, 128, !ok)) return false;
                     if (tok < npad) {
-                        float m = fmaxf(fmaxf(s.red[wg * 4][tok], s.red[wg * 4 + 1][tok]),
-                                        fmaxf(s.red[wg * 4 + 2][tok], s.red[wg * 4 + 3][tok]));
-                        if (!fresh) m = fmaxf(m, 0.f);
-                        if (!(m > -INFINITY)) m = 0.f;
+                        float m = max_nan(max_nan(s.red[wg * 4][tok], s.red[wg * 4 + 1][tok]),
+                                          max_nan(s.red[wg * 4 + 2][tok], s.red[wg * 4 + 3][tok]));
+                        if (!fresh) m = max_nan(m, 0.f);
+                        if (m == -INFINITY) m = 0.f;
                         s.delta[wg][tok] = ex2(-m);
                         s.mneg[wg][tok] -= m;
                     }
                     named_bar(5 + wg, 128);
                     const float ref = must ? top_v : sref, fs = sref / ref;
                     sref = ref;
+                    const float4 *d4 = reinterpret_cast<const float4 *>(s.delta[wg]);
+#pragma unroll
+                    for (int i = 0; i < kCols / 4; ++i) {       // (columns past npad hold anything, and are not looked at)
+                        const float4 f = d4[i];
+                        l[2 * i] = mul2(l[2 * i], pair(f.x, f.y));
+                        l[2 * i + 1] = mul2(l[2 * i + 1], pair(f.z, f.w));
+                    }
                     if (!fresh) {
+#pragma unroll 1
+                        for (int c = 0; c < nch; ++c) {
+                            float o[16];
+                            tmem_ld_x16(tm_o + c * 16, reinterpret_cast<uint32_t *>(o));
+                            ld_done(o);
 #pragma unroll
-                        for (int c = 0; c < T::kChunks; ++c)
-                            if (c < nch) {
-                                float o[16];
-                                tmem_ld_x16(tm_o + c * 16, reinterpret_cast<uint32_t *>(o));
-                                ld_done(o);
-#pragma unroll
-                                for (int i = 0; i < 16; i += 2) {
-                                    const float f0 = s.delta[wg][c * 16 + i], f1 = s.delta[wg][c * 16 + i + 1];
-                                    l[c * 8 + (i >> 1)] = mul2(l[c * 8 + (i >> 1)], pair(f0, f1));
-                                    o[i] *= f0 * fs;
-                                    o[i + 1] *= f1 * fs;
-                                }
-                                tmem_st_x16(tm_o + c * 16, reinterpret_cast<uint32_t *>(o));
-                            }
+                            for (int i = 0; i < 16; ++i) o[i] *= s.delta[wg][c * 16 + i] * fs;
+                            tmem_st_x16(tm_o + c * 16, reinterpret_cast<uint32_t *>(o));
+                        }
                         tmem_st_wait();
                     }
-                    weights();
+                    return true;
+                };
+                // Once over the scores, as a rule; where a score passes its
+                // reference, once more to take the weights back, and again
+                // under raised references.  One copy of the pass serves all
+                // three: its code is what the instruction caches have to hold.
+                const bool must = fresh || top_v > kScaleRaise * sref;          // the same for every thread
+                for (int turn = must ? 2 : 0;; ++turn) {
+                    if (turn == 2 && !raise(must)) {
+                        ok = false;
+                        break;
+                    }
+                    const float top = weights(turn == 1 ? -1.f : 1.f);
+                    if (turn == 2 || (turn == 0 && !bar_or(5 + wg, 128, (live && !(top <= kRaise)) || !ok))) break;
                 }
+                if (!ok) break;
                 fresh = false;
                 tc_fence_before();
                 fence_async_shared();
@@ -891,54 +869,62 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
             // warpgroups' sums merged, alternate chunks to each
             const uint32_t last = j - 1 - ((j - 1 - wg) & 1);  // the last tile of this warpgroup's parity, if it had one
             const bool used = !fresh;
-            if (ok && used) ok = mbar_wait(bar(s.pv_done[wg]), (last >> 1) & 1, to, p.status, abort);
+            if (ok && used) ok = wait_phase(bar(s.pv_done[wg]), (last >> 1) & 1, to, p.status, abort);
+            // normalisers over the tokens, through the warpgroup's own P (its last product is done): [column][token], as
+            // many columns at a time as P holds
+            constexpr int kPart = T::kPBytes / (kTile * 4);
+            float *lp = reinterpret_cast<float *>(sm + T::kOffP + wg * T::kPBytes);
 #pragma unroll
-            for (int c = 0; c < T::kChunks; ++c)
-                if (c < nch) {
-                    float y[16];
+            for (int n0 = 0; n0 < kCols; n0 += kPart) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) unpair(l[c * 8 + i], y[2 * i], y[2 * i + 1]);
-                    const float x = reduce16<false>(y, lane);
-                    if (lane < 16) s.red[sw][c * 16 + lane_col(lane)] = x;
+                for (int i = 0; i < kPart; i += 2) {
+                    float x, y;
+                    unpair(l[(n0 + i) / 2], x, y);
+                    lp[i * kTile + tok] = x;
+                    lp[(i + 1) * kTile + tok] = y;
                 }
-            named_bar(5 + wg, 128);
-            if (tok < npad) {
-                s.lsum[wg][tok] = (s.red[wg * 4][tok] + s.red[wg * 4 + 1][tok]) + (s.red[wg * 4 + 2][tok] + s.red[wg * 4 + 3][tok]);
-                if (!used) s.mneg[wg][tok] = INFINITY;         // no maximum: this warpgroup had no tile
+                named_bar(5 + wg, 128);
+#pragma unroll 1
+                for (int n = quad; n < kPart; n += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(lp + n * kTile + lane * 4);
+                    float v = (x.x + x.y) + (x.z + x.w);
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+                    if (lane == 0) s.lsum[wg][n0 + n] = v;
+                }
+                named_bar(5 + wg, 128);
             }
+            if (tok < npad && !used) s.mneg[wg][tok] = INFINITY;   // no maximum: this warpgroup had no tile
             if (tok == 0) s.sref[wg] = sref;
             if (bar_or(4, kSoft, !ok)) {
                 ok = false;
                 break;
             }
             const int64_t col0 = (int64_t)g.lo * p.Hq + (int64_t)(g.h * g.rows + g.row0) * p.G + (int64_t)cta * kCols;
+            // a warpgroup without a tile has left no sums: whatever stands there counts for nothing
+            const bool has0 = s.sref[0] > 0.f, has1 = s.sref[1] > 0.f;
             if (wg == 0 && tok < npad) {
-                const float m0 = -s.mneg[0][tok], m1 = -s.mneg[1][tok], m = fmaxf(m0, m1);
-                const float f0 = m0 > -INFINITY ? ex2(m0 - m) : 0.f, f1 = m1 > -INFINITY ? ex2(m1 - m) : 0.f;
+                const float m0 = -s.mneg[0][tok], m1 = -s.mneg[1][tok], m = max_nan(m0, m1);
+                const float f0 = has0 ? ex2(m0 - m) : 0.f, f1 = has1 ? ex2(m1 - m) : 0.f;
                 s.delta[0][tok] = f0 * s.sref[0] / kHead;
                 s.delta[1][tok] = f1 * s.sref[1] / kHead;
-                if (tok < ncol)
-                    p.ml[col0 + tok] = make_float2(m, (f0 > 0.f ? f0 * s.lsum[0][tok] : 0.f) + (f1 > 0.f ? f1 * s.lsum[1][tok] : 0.f));
+                if (tok < ncol) p.ml[col0 + tok] = make_float2(m, (has0 ? f0 * s.lsum[0][tok] : 0.f) + (has1 ? f1 * s.lsum[1][tok] : 0.f));
             }
             named_bar(4, kSoft);
             tc_fence_after();
-            // a warpgroup without a tile has left no sums: whatever stands there counts for nothing
-            const bool has0 = s.sref[0] > 0.f, has1 = s.sref[1] > 0.f;
+#pragma unroll 1
+            for (int c = wg; c < nch; c += 2) {
+                float o0[16], o1[16];
+                tmem_ld_x16(tmem + lanes + T::kTmO + c * 16, reinterpret_cast<uint32_t *>(o0));
+                tmem_ld_x16(tmem + lanes + T::kTmO + kCols + c * 16, reinterpret_cast<uint32_t *>(o1));
+                ld_done(o0);
+                ld_done(o1);
+                float *dst = p.part + (col0 + c * 16) * kD + tok;
 #pragma unroll
-            for (int c = 0; c < T::kChunks; ++c)
-                if (c < nch && (c & 1) == wg) {
-                    float o0[16], o1[16];
-                    tmem_ld_x16(tmem + lanes + T::kTmO + c * 16, reinterpret_cast<uint32_t *>(o0));
-                    tmem_ld_x16(tmem + lanes + T::kTmO + kCols + c * 16, reinterpret_cast<uint32_t *>(o1));
-                    ld_done(o0);
-                    ld_done(o1);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int n = c * 16 + i;
-                        if (n < ncol)
-                            p.part[(col0 + n) * kD + tok] = (has0 ? o0[i] * s.delta[0][n] : 0.f) + (has1 ? o1[i] * s.delta[1][n] : 0.f);
-                    }
-                }
+                for (int i = 0; i < 16; ++i)
+                    if (c * 16 + i < ncol)
+                        dst[i * kD] = (has0 ? o0[i] * s.delta[0][c * 16 + i] : 0.f) + (has1 ? o1[i] * s.delta[1][c * 16 + i] : 0.f);
+            }
             tc_fence_before();
             at += g.t1 - g.t0;
         }
@@ -954,91 +940,104 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
 // ---------------------------------------------------------------------------
 
 // One CTA per row and key/value head; a warp takes a query head of the group at
-// a time, four dimensions to a lane.
-__global__ void __launch_bounds__(128) k_attn_join(const AttnParams p)
+// a time, four dimensions to a lane.  It starts with the context's kernel (where
+// an SM has room) and waits for it after the path's keys are staged.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const AttnParams p)
 {
     extern __shared__ __align__(16) float smf[];
     float *sv = smf;                                    // [kPath][kD], read four at a time
-    float *sq = sv + kPath * kD;                        // [4 warps][kD]
-    float *sk = sq + 4 * kD;                            // [kPath][kD + 1] keys of the path, turned
-    float *ss = sk + kPath * (kD + 1);                  // [4 warps][kPath] weights
+    float *sq = sv + kPath * kD;                        // [8 warps][kD]
+    float *sk = sq + 8 * kD;                            // [kPath][kD + 1] keys of the path, turned
+    float *ss = sk + kPath * (kD + 1);                  // [8 warps][kPath] weights
     __shared__ int32_t s_parent[kMaxBudget], s_path[kPath + 1], s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x, h = blockIdx.y, G = p.G;
     const int r = request_of(p, row);
     const int lo = r < 0 ? row : p.off[r];
-    for (int j = lo + tid; j <= row; j += 128) s_parent[j - lo] = p.parent[j];
+    for (int j = lo + tid; j <= row; j += kJoinThreads) s_parent[j - lo] = p.parent[j];
     __syncthreads();
-    if (tid == 0) {
+    const int len = r < 0 ? 0 : p.len[r], rows = r < 0 ? 1 : p.off[r + 1] - lo;
+    if (warp == 0) {
         int n = 0, j = row;
         while (r >= 0 && j >= lo && n <= kPath) {
-            s_path[n++] = j;
+            if (lane == 0) s_path[n] = j;
+            ++n;
             const int q = s_parent[j - lo];
-            if (q >= j || (p.rope.rot && p.len[r] + (int)p.depth[j] >= p.rope.max_pos)) n = kPath + 1;   // a parent after its child, a position off the table
+            if (q >= j) n = kPath + 1;                  // a parent after its child
             else j = q;
         }
-        if (r < 0 || n > kPath || j >= 0) {             // ... or outside the request
-            n = 0;
-            fail(p.status);
+        const bool ok = r >= 0 && n <= kPath && j < 0;  // ... or outside the request
+        bool off = false;                               // a position off the table
+        __syncwarp();
+        if (ok && p.rope.rot)
+            for (int a = lane; a < n; a += 32) off |= len + (int)p.depth[s_path[a]] >= p.rope.max_pos;
+        off = __any_sync(0xffffffffu, off);
+        if (lane == 0) {
+            s_n = ok && !off ? n : 0;
+            if (!ok || off) fail(p.status);
         }
-        s_n = n;
     }
     __syncthreads();
     const int nA = s_n;
     uint16_t *o = p.out + ((int64_t)row * p.Hq + h * G) * kD;
     if (nA == 0) {                                      // malformed: zeros, and the status word says so
-        for (int i = tid; i < G * kD; i += 128) o[i] = 0;
+        for (int i = tid; i < G * kD; i += kJoinThreads) o[i] = 0;
         return;
     }
-    const int len = p.len[r], rows = p.off[r + 1] - lo;
-    for (int a = warp; a < nA; a += 4) {
+    for (int a = warp; a < nA; a += 8) {
         const int64_t j = s_path[a];
-        float x[4];
         Raw4 rw;
         load4(rw, p.k + j * p.k_stride + h * kD, lane * 4, len + (int)p.depth[j], p.rope);
-        turn4(rw, lane * 4, p.rope, x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sk[a * (kD + 1) + lane * 4 + i] = x[i];
         const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.v + j * p.v_stride + h * kD + lane * 4));
-        *reinterpret_cast<float4 *>(sv + a * kD + lane * 4) =
-            make_float4(bf16_f32((uint16_t)w.x), bf16_f32((uint16_t)(w.x >> 16)), bf16_f32((uint16_t)w.y),
-                        bf16_f32((uint16_t)(w.y >> 16)));
+        const float4 x = turn4(rw);
+        float *dst = sk + a * (kD + 1) + lane * 4;
+        dst[0] = x.x, dst[1] = x.y, dst[2] = x.z, dst[3] = x.w;
+        *reinterpret_cast<float4 *>(sv + a * kD + lane * 4) = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
     }
     __syncthreads();
-    // the shares that hold a part of this row's segment
-    pdl_wait();
-    const int64_t total = __ldcg(p.plan + p.n_req), share = (total + p.ctas - 1) / p.ctas;
-    const int nt = total ? (len + kTile - 1) / kTile : 0;
-    const int fit = p.cols / G, i0 = row - lo, grp = i0 / group_rows(rows, fit);
-    const int64_t a0 = __ldcg(p.plan + r) + (int64_t)(h * group_count(rows, fit) + grp) * nt;
-    const int cta0 = nt ? (int)(a0 / share) : 0, cta1 = nt ? (int)((a0 + nt - 1) / share) : -1;
-    for (int g = warp; g < G; g += 4) {
-        float x[4];
+    const int ng = group_count(rows, p.fit), per = (rows + ng - 1) / ng, i0 = row - lo, grp = i0 / per;
+    bool waited = false;
+    for (int g = warp; g < G; g += 8) {
         Raw4 rw;
         load4(rw, p.q + row * p.q_stride + (int64_t)(h * G + g) * kD, lane * 4, len + (int)p.depth[row], p.rope);
-        turn4(rw, lane * 4, p.rope, x);
+        const float4 x = turn4(rw);
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sq[warp * kD + lane * 4 + i] = x[i] * p.scale2;
+        *reinterpret_cast<float4 *>(sq + warp * kD + lane * 4) =
+            make_float4(x.x * p.scale2, x.y * p.scale2, x.z * p.scale2, x.w * p.scale2);
         __syncwarp();
         float m = -INFINITY;
         for (int a = lane; a < nA; a += 32) {
-            float d0 = 0.f, d1 = 0.f;
-#pragma unroll 8
-            for (int d = 0; d < kD; d += 2) {
-                d0 = fmaf(sq[warp * kD + d], sk[a * (kD + 1) + d], d0);
-                d1 = fmaf(sq[warp * kD + d + 1], sk[a * (kD + 1) + d + 1], d1);
+            const float *k = sk + a * (kD + 1);
+            float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
+#pragma unroll 4
+            for (int d = 0; d < kD; d += 4) {
+                const float4 q = *reinterpret_cast<const float4 *>(sq + warp * kD + d);
+                d0 = fmaf(q.x, k[d], d0);
+                d1 = fmaf(q.y, k[d + 1], d1);
+                d2 = fmaf(q.z, k[d + 2], d2);
+                d3 = fmaf(q.w, k[d + 3], d3);
             }
-            ss[warp * kPath + a] = d0 + d1;
-            m = fmaxf(m, d0 + d1);
+            const float y = (d0 + d1) + (d2 + d3);
+            ss[warp * kPath + a] = y;
+            m = fmaxf(m, y);
         }
+        if (!waited) pdl_wait();                        // the context's parts from here on
+        waited = true;
+        // the shares that hold a part of this row's segment
+        const int64_t total = __ldcg(p.plan + p.n_req), share = (total + p.ctas - 1) / p.ctas;
+        const int nt = total ? (len + kTile - 1) / kTile : 0;
+        const int64_t a0 = __ldcg(p.plan + r) + (int64_t)(h * ng + grp) * nt;
+        const int cta0 = nt ? (int)(a0 / share) : 0, cta1 = nt ? (int)((a0 + nt - 1) / share) : -1;
         const int64_t col = (int64_t)lo * p.Hq + (int64_t)(h * rows + i0) * G + g;
         for (int c = cta0 + lane; c <= cta1; c += 32) m = fmaxf(m, __ldcg(p.ml + col + (int64_t)c * p.cols).x);
 #pragma unroll
         for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if (!(m > -INFINITY)) m = 0.f;                  // nothing but NaN and -inf: the sums say so
+        if (m == -INFINITY) m = 0.f;                    // nothing but NaN and -inf: the sums say so
         __syncwarp();
         float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
         for (int a = 0; a < nA; ++a) {
             const float e = ex2(ss[warp * kPath + a] - m);
             const float4 v = *reinterpret_cast<const float4 *>(sv + a * kD + lane * 4);
@@ -1048,7 +1047,7 @@ __global__ void __launch_bounds__(128) k_attn_join(const AttnParams p)
             acc[2] = fmaf(e, v.z, acc[2]);
             acc[3] = fmaf(e, v.w, acc[3]);
         }
-#pragma unroll 4
+#pragma unroll 8
         for (int c = cta0; c <= cta1; ++c) {
             const float2 q = __ldcg(p.ml + col + (int64_t)c * p.cols);
             const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (col + (int64_t)c * p.cols) * kD) + lane);
@@ -1059,9 +1058,9 @@ __global__ void __launch_bounds__(128) k_attn_join(const AttnParams p)
             acc[2] = fmaf(e, v.z, acc[2]);
             acc[3] = fmaf(e, v.w, acc[3]);
         }
+        const float i = 1.f / l;
         *reinterpret_cast<uint2 *>(o + g * kD + lane * 4) =
-            make_uint2(pack_bf16x2(acc[0] / l, acc[1] / l), pack_bf16x2(acc[2] / l, acc[3] / l));
-        __syncwarp();
+            make_uint2(pack_bf16x2(acc[0] * i, acc[1] * i), pack_bf16x2(acc[2] * i, acc[3] * i));
     }
 }
 
@@ -1134,7 +1133,7 @@ int launch_attn(const AttnArgs &a, void *stream)
     p.part = reinterpret_cast<float *>(w + plan_bytes());
     p.ml = reinterpret_cast<float2 *>(w + plan_bytes() + cols * kD * 4);
     p.status = a.status;
-    p.timeout_ns = a.timeout_ns;
+    p.sleeps = (int32_t)(a.timeout_ns / kWaitSleepNs > 1000000000 ? 1000000000 : a.timeout_ns / kWaitSleepNs);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
 
     EncodeTiledFn fn = encode_fn();
@@ -1159,6 +1158,7 @@ int launch_attn(const AttnArgs &a, void *stream)
     // columns of a segment: the least shape that holds an average request's rows and one row's heads
     const int64_t avg = (int64_t)((a.R + a.n_req - 1) / a.n_req) * p.G;
     p.cols = avg <= 16 ? 16 : avg <= 48 ? 48 : 80;
+    p.fit = p.cols / p.G;
     cudaError_t e;
     auto go = [&](auto kernel, int threads, int bytes) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -1181,10 +1181,10 @@ int launch_attn(const AttnArgs &a, void *stream)
     else
         go(k_attn_ctx<80>, Shape<80>::kThreads, smem_bytes<80>());
     if (e != cudaSuccess) return (int)e;
-    constexpr int smem = (kPath * (2 * kD + 1) + 4 * (kD + kPath)) * 4;
+    constexpr int smem = (kPath * (2 * kD + 1) + 8 * (kD + kPath)) * 4;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.R, (unsigned)a.H);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

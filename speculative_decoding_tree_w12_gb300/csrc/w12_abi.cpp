@@ -883,7 +883,8 @@ w12_status rope_ok(const w12_rope *r, RopeArgs &a)
     a = RopeArgs{};
     if (!r || r->rot_dim == 0) return W12_OK;
     if (r->rot_dim < 0 || r->rot_dim % 2 || r->max_pos < 1 || !r->cos || !r->sin) return W12_E_INVAL;
-    if (r->rot_dim > kKvDim) return W12_E_UNSUPPORTED;
+    if (!aligned(r->cos, 16) || !aligned(r->sin, 16)) return W12_E_INVAL;
+    if (r->rot_dim > kKvDim || r->rot_dim % 8) return W12_E_UNSUPPORTED;
     a.cos = r->cos;
     a.sin = r->sin;
     a.rot = r->rot_dim;

@@ -34,11 +34,18 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes)
     return d;
 }
 
+__device__ __forceinline__ float2 f16x2_f32(uint32_t h)
+{
+    float2 f;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(h));
+    return f;
+}
+
 __device__ __forceinline__ float e4m3_f32(uint8_t code)
 {
-    float f;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(e4m3x2_f16x2(code)));
-    return f;
+    return f16x2_f32(e4m3x2_f16x2(code)).x;
 }
 
 // The least power of two s with top <= 448 s, not under 2^-32 (a block of
