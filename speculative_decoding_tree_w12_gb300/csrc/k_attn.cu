@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
 {
     typedef Shape<kCols> T;
     extern __shared__ uint8_t raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *sm = raw + (-smem_u32(raw) & 1023u);         // (arithmetic that leaves the compiler sure of shared memory)
     Shared &s = *reinterpret_cast<Shared *>(sm + T::kOffShared);
     const uint32_t base = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
