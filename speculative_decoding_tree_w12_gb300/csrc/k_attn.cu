@@ -88,7 +88,7 @@ struct AttnParams {
     float *part;                            // [R * Hq + ctas * cols][kD] sums
     float2 *ml;                             // [R * Hq + ctas * cols] maximum (log2), normaliser
     int32_t *status;
-    int32_t sleeps;                         // of kWaitSleepNs: a wait's limit
+    uint64_t timeout_ns;                    // a wait's limit
 };
 
 __device__ __forceinline__ void fail(int32_t *status) { atomicCAS(status, 0, (int32_t)W12_E_INVAL); }
@@ -162,21 +162,26 @@ __device__ __forceinline__ float4 turn4(const Raw4 &r)
 }
 
 // Wait for a phase: false after about timeout_ns (W12_E_TIMEOUT in *status) or
-// once *abort is set.  As w12d::mbar_wait, counting sleeps instead of reading
-// the clock: it is inlined at every wait, and its size counts.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, int32_t sleeps, int32_t *status,
+// once *abort is set.  try_wait without a time hint parks the warp in hardware;
+// with one it becomes a loop of sleeps, and twenty warps' sleep loops took more
+// issue slots here than the work did.  The clock and the abort word are looked
+// at every 256th time.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t timeout_ns, int32_t *status,
                                            volatile int32_t *abort)
 {
-    bool done = mbar_try_wait(bar, parity);
-    for (int32_t n = 0; !done; ++n) {
-        done = mbar_try_wait_sleep(bar, parity, kWaitSleepNs);
-        if (!done && (n >= sleeps || *abort)) {
-            if (!*abort) atomicCAS(status, 0, (int32_t)W12_E_TIMEOUT);
+    uint64_t t0 = 0;
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+        if (n & 255) continue;
+        const uint64_t t = globaltimer();
+        if (t0 == 0) t0 = t;
+        const bool late = t - t0 > timeout_ns;
+        if (late) atomicCAS(status, 0, (int32_t)W12_E_TIMEOUT);
+        if (late || *abort) {
             *abort = 1;
-            break;
+            return false;
         }
     }
-    return done;
+    return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
     const int bs = p.bt == 32 ? 5 : p.bt == 64 ? 6 : 7;   // log2 of a block's tokens
     const int nb = kTile >> bs;                           // blocks of a tile
     volatile int32_t *abort = &s.abort;
-    const int32_t to = p.sleeps;
+    const uint64_t to = p.timeout_ns;
     // after a wait that ran out: products in flight end before tensor memory is freed
     auto drain = [&](const uint64_t &b) {
         tc_commit(bar(b));
@@ -1133,7 +1138,7 @@ int launch_attn(const AttnArgs &a, void *stream)
     p.part = reinterpret_cast<float *>(w + plan_bytes());
     p.ml = reinterpret_cast<float2 *>(w + plan_bytes() + cols * kD * 4);
     p.status = a.status;
-    p.sleeps = (int32_t)(a.timeout_ns / kWaitSleepNs > 1000000000 ? 1000000000 : a.timeout_ns / kWaitSleepNs);
+    p.timeout_ns = a.timeout_ns;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
 
     EncodeTiledFn fn = encode_fn();
