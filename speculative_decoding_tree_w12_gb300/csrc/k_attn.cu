@@ -31,10 +31,10 @@
 //                would cost four times the bandwidth, which bounds the tile);
 //                P in F16, eleven significant bits, scaled so that there are
 //                2^-18 below a weight of 1 before the subnormals.
-// Two softmax warpgroups take alternate tiles, each with its own scores, P,
-// maxima and sums, so the latencies of one tile's chain (product, reads,
-// exponentials, writes, product) hide behind the other's; they merge at the
-// end of a segment.
+// Four softmax warpgroups share a tile's columns, a few each: sixteen warps
+// hide one another's latencies, the normalisers fit their registers, and a
+// pass over the scores is short code (two warpgroups of ten steps each ran at
+// the rate of the instruction fetches).
 // The maximum is lazy: P refers to a column maximum that is only raised when a
 // score passes it by 2^6 (P stays under F16's top), so the usual tile has no
 // reduction over lanes at all; the same slow path raises the reference of the
@@ -61,12 +61,12 @@ constexpr int kMaxCols = 80;               // query columns of a segment, see Sh
 constexpr int kScaleRing = 16;             // tiles whose block scales are kept (the copies run at most 8 ahead of their readers)
 constexpr int kMaxReq = kMaxBudget;
 constexpr uint64_t kDrainNs = 1000000000;  // limit of the waits after a failed one
-constexpr int kSoft = 256;                 // softmax threads
-// registers a thread: at launch (640 threads under 65536 registers), of the
-// softmax warps (a normaliser for each of 80 columns and 32 scores in flight),
-// of the others.  The shares add up to no more than the launch has.
-constexpr int kRegsLaunch = 96, kRegsSoft = 144, kRegsOther = 64;
-static_assert(kSoft * kRegsSoft + (640 - kSoft) * kRegsOther <= 640 * kRegsLaunch, "a larger share would wait forever");
+constexpr int kSoft = 512;                 // softmax threads, in four warpgroups
+constexpr int kThreads = 128 + kSoft + 256; // warps: 0 K copies, 1 scores, 2 V copies, 3 sums, 4-19 softmax, 20-27 V to F16
+// registers a thread: at launch, of the softmax and converting warps, of the
+// first four.  The shares add up to no more than the launch has.
+constexpr int kRegsLaunch = 72, kRegsSoft = 80, kRegsConv = 64, kRegsOther = 56;
+static_assert(kSoft * kRegsSoft + 256 * kRegsConv + 128 * kRegsOther <= kThreads * kRegsLaunch, "a larger share would wait forever");
 constexpr float kHead = 16.f;              // P of a weight of 1 under the reference scale
 constexpr float kRaise = 6.f;              // a score may pass the column's reference by this (log2) before it is raised
 constexpr float kCap = 8.f;                // scores are held under this until then
@@ -197,8 +197,7 @@ template <int kCols>
 struct Shape {
     static constexpr int kChunks = kCols / 16;
     static constexpr bool kStacked = kCols <= kStack;
-    // warps: 0 K copies, 1 scores, 2 V copies, 3 sums, 4-11 softmax, 12-19 conversion
-    static constexpr int kThreads = 128 + kSoft + 256;
+    static constexpr int kSteps = (2 * kChunks + 3) / 4;         // steps of 8 columns of a softmax warpgroup, at most
     static constexpr int kStK = kCols <= 16 ? 6 : 5;             // K tiles in flight
     static constexpr int kStV = kCols <= 16 ? 6 : kCols <= 48 ? 5 : 4;
     static constexpr int kKBytes = kTile * kD;                   // one K or V tile: 16 KB
@@ -209,10 +208,10 @@ struct Shape {
     static constexpr int kOffP = kOffV + kStV * kKBytes;         // [2][kCols / 16 slabs][128 tokens][16] F16
     static constexpr int kOffQ = kOffP + 2 * kPBytes;            // [3 pieces][kCols][128] E4M3
     static constexpr int kOffShared = kOffQ + 3 * kQBytes;
-    // tensor memory: scores of two tiles, sums of the two warpgroups, two V tiles in F16 (two tokens to a column)
+    // tensor memory: scores of two tiles, the sums, two V tiles in F16 (two tokens to a column)
     static constexpr int kTmS = kStacked ? 3 * kCols : kCols;    // columns of one tile's scores
     static constexpr int kTmO = 2 * kTmS;
-    static constexpr int kTmV = kTmO + 2 * kCols;
+    static constexpr int kTmV = kTmO + kCols;
     static constexpr int kTmUsed = kTmV + kTile;
     static constexpr int kTmCols = kTmUsed <= 256 ? 256 : 512;
     static_assert(kTmUsed <= 512, "tensor memory");
@@ -226,17 +225,16 @@ struct Shared {
     uint64_t s_full[2], s_empty[2];                    // scores in tensor memory / read
     uint64_t p_full[2], v16_full[2], pv_done[2];       // weights and widened values in shared memory / their product added
     uint64_t q_full, drain[2];
-    int64_t wsum[24];
+    int64_t wsum[kThreads / 32];
     int32_t pre[kMaxReq + 1];                          // first tile of every request
     alignas(16) float cf[kMaxCols];                    // score factor of a column
-    alignas(16) float mneg[2][kMaxCols];               // per warpgroup: minus the reference maximum, the factor of its last raise;
-    alignas(16) float delta[2][kMaxCols];              // at the end, what the warpgroup's sums count for in the segment's
-    float lsum[2][kMaxCols], red[8][kMaxCols];         // normalisers; per softmax warp
+    alignas(16) float mneg[kMaxCols];                  // minus its reference maximum
+    alignas(16) float delta[kMaxCols];                 // the factor of its last raise
+    float red[4][kMaxCols];                            // per warp of a warpgroup
     int32_t len[kMaxReq];                              // of every request: cached tokens,
     uint16_t lo[kMaxReq], rows[kMaxReq];               // first row, rows
     float2 scale[kScaleRing][kTile / 32];              // K and V scale of a tile's blocks
     float top_v[kScaleRing];                           // the largest of the V scales
-    float sref[2];
     uint32_t tmem;
     int32_t abort;
 };
@@ -350,10 +348,11 @@ __device__ __forceinline__ void ld_done8(float *y)
                  : "+f"(y[0]), "+f"(y[1]), "+f"(y[2]), "+f"(y[3]), "+f"(y[4]), "+f"(y[5]), "+f"(y[6]), "+f"(y[7]));
 }
 
-__device__ __forceinline__ void ld_done(float (&y)[16])
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const float *r)
 {
-    ld_done8(y);
-    asm volatile("" : "+f"(y[8]), "+f"(y[9]), "+f"(y[10]), "+f"(y[11]), "+f"(y[12]), "+f"(y[13]), "+f"(y[14]), "+f"(y[15]));
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "f"(r[0]),
+                 "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+                 : "memory");
 }
 
 template <int N>
@@ -374,18 +373,15 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return d;
 }
 
-// The maximum (or NaN) of each of 16 columns over the 32 lanes of a warp:
-// afterwards every lane holds that of column lane_col(lane).  16 shuffles
-// instead of 80.
-__device__ __forceinline__ int lane_col(int lane)
-{
-    return ((lane & 1) << 3) | ((lane & 2) << 1) | ((lane & 4) >> 1) | ((lane & 8) >> 3);
-}
+// The maximum (or NaN) of each of 8 columns over the 32 lanes of a warp:
+// afterwards every lane holds that of column lane_col(lane).  9 shuffles
+// instead of 40.
+__device__ __forceinline__ int lane_col(int lane) { return ((lane & 1) << 2) | (lane & 2) | ((lane & 4) >> 2); }
 
-__device__ __forceinline__ float max16(float (&v)[16], int lane)
+__device__ __forceinline__ float max8(float (&v)[8], int lane)
 {
 #pragma unroll
-    for (int n = 8, bit = 1; n; n >>= 1, bit <<= 1) {
+    for (int n = 4, bit = 1; n; n >>= 1, bit <<= 1) {
         const bool up = lane & bit;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
@@ -393,11 +389,12 @@ __device__ __forceinline__ float max16(float (&v)[16], int lane)
             v[i] = max_nan(k, o);
         }
     }
+    v[0] = max_nan(v[0], __shfl_xor_sync(0xffffffffu, v[0], 8));
     return max_nan(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
 template <int kCols>
-__global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     k_attn_ctx(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnParams p)
 {
     typedef Shape<kCols> T;
@@ -439,8 +436,8 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(s.s_full[i]), 1);
-            mbar_init(bar(s.s_empty[i]), 4);
-            mbar_init(bar(s.p_full[i]), 4);
+            mbar_init(bar(s.s_empty[i]), kSoft / 32);
+            mbar_init(bar(s.p_full[i]), kSoft / 32);
             mbar_init(bar(s.v16_full[i]), 4);
             mbar_init(bar(s.pv_done[i]), 1);
         }
@@ -454,7 +451,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
     if (warp == 1) tmem_alloc(smem_u32(&s.tmem), T::kTmCols);
     __syncthreads();
     int64_t all = 0;
-    for (int w = 0; w < T::kThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) incl += s.wsum[w];
         all += s.wsum[w];
     }
@@ -468,7 +465,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
     const uint32_t tmem = s.tmem;
     const int32_t total = s.pre[p.n_req];
     if (cta == 0)
-        for (int i = tid; i <= p.n_req; i += T::kThreads) p.plan[i] = s.pre[i];
+        for (int i = tid; i <= p.n_req; i += kThreads) p.plan[i] = s.pre[i];
     const int64_t share = ((int64_t)total + p.ctas - 1) / p.ctas;
     const int32_t first = (int32_t)min((int64_t)total, cta * share), end = (int32_t)min((int64_t)total, first + share);
     const int bs = p.bt == 32 ? 5 : p.bt == 64 ? 6 : 7;   // log2 of a block's tokens
@@ -601,11 +598,11 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                          wait_phase(bar(s.p_full[b]), (j >> 1) & 1, to, p.status, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t keep = t - g.t0 >= 2;      // each parity's first tile starts its sums
+                    const uint32_t keep = t > g.t0;           // the first tile starts the sums
                     const uint64_t pb = pd + (uint64_t)(b * (T::kPBytes >> 4));
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        tc_mma_ts(tmem + T::kTmO + b * kCols, tmem + T::kTmV + b * (kTile / 2) + k * 8, pb + (uint64_t)(k * (512 >> 4)),
+                        tc_mma_ts(tmem + T::kTmO, tmem + T::kTmV + b * (kTile / 2) + k * 8, pb + (uint64_t)(k * (512 >> 4)),
                                   idesc, keep | (k > 0));
                     tc_commit(bar(s.pv_done[b]));
                 }
@@ -614,10 +611,10 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
             if (!ok) drain(s.drain[1]);
         }
         __syncwarp();
-    } else if (warp >= 12) {
+    } else if (warp >= 20) {
         // ------------------------------------------------------------ V to F16
-        regs_dec<kRegsOther>();
-        const int wg = (warp - 12) >> 2, quad = warp & 3, d = quad * 32 + lane;   // a dimension to a thread, as the lanes lie
+        regs_dec<kRegsConv>();
+        const int wg = (warp - 20) >> 2, quad = warp & 3, d = quad * 32 + lane;   // a dimension to a thread, as the lanes lie
         const int cs = bs - 4;                                // log2 of the 16-token chunks of a row of a block
         const int swz = bs == 5 ? (d >> 2) & 1 : bs == 6 ? (d >> 1) & 3 : d & 7;   // the copy's swizzle: one row's bytes wide
         const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + T::kTmV + wg * (kTile / 2);
@@ -665,18 +662,16 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
             at += g.t1 - g.t0;
         }
     } else if (warp >= 4) {
-        // ------------------------------------------------------------ softmax: warpgroup wg takes the tiles j with j % 2 == wg
+        // ------------------------------------------------------------ softmax
         regs_inc<kRegsSoft>();
         const int sw = warp - 4, wg = sw >> 2, quad = warp & 3;
         const int tok = quad * 32 + lane;                     // this thread's token of the tile
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t tm_s = tmem + lanes + wg * T::kTmS, tm_o = tmem + lanes + T::kTmO + wg * kCols;
-        const float4 *cf4 = reinterpret_cast<const float4 *>(s.cf), *mn4 = reinterpret_cast<const float4 *>(s.mneg[wg]);
+        const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
         uint32_t j = 0;
         bool ok = true;
         for (int32_t at = first; at < end && ok;) {
             const Seg g = segment(p, s, at, end);
-            const int ncol = g.nrows * p.G, npad = (ncol + 15) & ~15, nch = npad >> 4;
+            const int ncol = g.nrows * p.G, npad = (ncol + 15) & ~15;
             // ---- Q: turned, scaled to E4M3's range by a power of two, in three pieces
             named_bar(4, kSoft);                              // the last segment's columns are done with
             const int n_q = T::kStacked ? kCols : npad;       // stacked pieces are products of all their columns
@@ -691,11 +686,11 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                 }
                 load4(rw, p.q + (int64_t)row * p.q_stride + (int64_t)(g.h * p.G + i % p.G) * kD, lane * 4, pos, p.rope);
             };
-            fetch(sw);
+            if (sw < n_q) fetch(sw);
 #pragma unroll 1
-            for (int n = sw; n < n_q; n += 8) {
+            for (int n = sw; n < n_q; n += kSoft / 32) {
                 float4 x = turn4(rw);
-                if (n + 8 < n_q) fetch(n + 8);
+                if (n + kSoft / 32 < n_q) fetch(n + kSoft / 32);
                 float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
                 for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -713,30 +708,32 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                 }
                 if (lane == 0) {
                     s.cf[n] = n < ncol ? qs * p.scale2 : 0.f;
-                    s.mneg[0][n] = 0.f;
-                    s.mneg[1][n] = 0.f;
+                    s.mneg[n] = 0.f;
                 }
             }
             fence_async_shared();
             named_bar(4, kSoft);
             if (lane == 0) mbar_arrive(bar(s.q_full));
 
-            uint64_t l[kCols / 2];                            // this thread's tokens' part of the normalisers, in pairs
+            // ---- this warpgroup's columns, 8 to a step
+            const int all = npad >> 3, s0 = all * wg >> 2, steps = (all * (wg + 1) >> 2) - s0;
+            const int n0 = s0 * 8, nw = steps * 8;
+            const float4 *cf4 = reinterpret_cast<const float4 *>(s.cf + n0), *mn4 = reinterpret_cast<const float4 *>(s.mneg + n0);
+            uint64_t l[T::kSteps * 4];                        // this token's part of the normalisers, in pairs
 #pragma unroll
-            for (int i = 0; i < kCols / 2; ++i) l[i] = 0ull;
+            for (int i = 0; i < T::kSteps * 4; ++i) l[i] = 0ull;
             float sref = 0.f;
-            bool fresh = true;
-            const uint32_t j0 = j;
-            j += g.t1 - g.t0;
-            for (uint32_t jj = j0 + ((j0 ^ wg) & 1); jj < j; jj += 2) {
-                const int t = g.t0 + (int)(jj - j0);
-                ok = wait_phase(bar(s.s_full[wg]), (jj >> 1) & 1, to, p.status, abort);
-                // this warpgroup's P and sums are free once its last product is done
-                if (ok && jj >= 2) ok = wait_phase(bar(s.pv_done[wg]), ((jj >> 1) - 1) & 1, to, p.status, abort);
+            for (int t = g.t0; t < g.t1; ++t, ++j) {
+                const int b = j & 1;
+                const bool fresh = t == g.t0;
+                ok = wait_phase(bar(s.s_full[b]), (j >> 1) & 1, to, p.status, abort);
+                // this tile's P is free once the product of two tiles ago is done
+                if (ok && j >= 2) ok = wait_phase(bar(s.pv_done[b]), ((j >> 1) - 1) & 1, to, p.status, abort);
                 __syncwarp();
                 tc_fence_after();
-                const float2 my = s.scale[jj % kScaleRing][tok >> bs];
-                const float top_v = fmaxf(s.top_v[jj % kScaleRing], 1e-30f);
+                const uint32_t tm_s = tm + b * T::kTmS + n0, tm_o = tm + T::kTmO + n0;
+                const float2 my = s.scale[j % kScaleRing][tok >> bs];
+                const float top_v = fmaxf(s.top_v[j % kScaleRing], 1e-30f);
                 const bool live = t * kTile + tok < g.len;
                 const uint64_t ks2 = pair(my.x, my.x);
                 // 8 columns' raw scores: asked for, and turned into scores against the references in log2 units
@@ -768,32 +765,33 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                 auto weights = [&](float sign) -> float {
                     const float rt = kHead * (my.y / sref), cap = live ? kCap : -INFINITY;   // a dead token weighs nothing
                     const uint64_t rt2 = pair(rt, rt), sg2 = pair(sign, sign);
-                    uint8_t *prow = sm + T::kOffP + wg * T::kPBytes + tok * 32;
-                    const int flip = ((tok >> 2) & 1) << 4;
+                    uint8_t *prow = sm + T::kOffP + b * T::kPBytes + tok * 32;
+                    const int flip = (tok >> 2) & 1;
                     float top = -INFINITY;
                     float y[3][8];                            // one step's weights, the next's scores, the one's after that on their way
                     ask(0, y[0]);
                     scores(0, y[0]);
-                    ask(1, y[1]);
+                    if (T::kSteps > 1 && steps > 1) ask(1, y[1]);
 #pragma unroll
-                    for (int c = 0; c < 2 * T::kChunks; ++c)
-                        if (c < 2 * nch) {
-                            if (c + 1 < 2 * T::kChunks && c + 1 < 2 * nch) {
+                    for (int c = 0; c < T::kSteps; ++c)
+                        if (c < steps) {
+                            if (c + 1 < T::kSteps && c + 1 < steps) {
                                 scores(c + 1, y[(c + 1) % 3]);
-                                if (c + 2 < 2 * T::kChunks && c + 2 < 2 * nch) ask(c + 2, y[(c + 2) % 3]);
+                                if (c + 2 < T::kSteps && c + 2 < steps) ask(c + 2, y[(c + 2) % 3]);
                             }
                             uint32_t w[4];
 #pragma unroll
                             for (int i = 0; i < 8; i += 2) {
-                                const float a = y[c % 3][i], b = y[c % 3][i + 1];
-                                top = max_nan(top, a, b);
-                                const uint64_t e = pair(ex2(fminf(a, cap)), ex2(fminf(b, cap)));
+                                const float x0 = y[c % 3][i], x1 = y[c % 3][i + 1];
+                                top = max_nan(top, x0, x1);
+                                const uint64_t e = pair(ex2(fminf(x0, cap)), ex2(fminf(x1, cap)));
                                 l[c * 4 + (i >> 1)] = fma2(e, sg2, l[c * 4 + (i >> 1)]);
                                 float u, v;
                                 unpair(mul2(e, rt2), u, v);
                                 w[i >> 1] = pack_f16x2(u, v);
                             }
-                            *reinterpret_cast<uint4 *>(prow + (c >> 1) * (kTile * 32) + (((c & 1) << 4) ^ flip)) =
+                            const int sc = s0 + c;
+                            *reinterpret_cast<uint4 *>(prow + (sc >> 1) * (kTile * 32) + (((sc & 1) ^ flip) << 4)) =
                                 make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     return top;
@@ -802,46 +800,51 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                 // NaN among its scores gets a NaN for its raise, and so carries
                 // it into its normaliser and sums.
                 auto raise = [&](bool must) -> bool {
+                    if (ok && !fresh) ok = wait_phase(bar(s.pv_done[b ^ 1]), ((j - 1) >> 1) & 1, to, p.status, abort);
+                    __syncwarp();
+                    tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < nch; ++c) {
-                        float y[16];
-                        ask(2 * c, y);
-                        scores(2 * c, y);
-                        ask(2 * c + 1, y + 8);
-                        scores(2 * c + 1, y + 8);
+                    for (int c = 0; c < steps; ++c) {
+                        float y[8];
+                        ask(c, y);
+                        scores(c, y);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = live ? y[i] : -INFINITY;
-                        const float m = max16(y, lane);
-                        if (lane < 16) s.red[sw][c * 16 + lane_col(lane)] = m;
+                        for (int i = 0; i < 8; ++i) y[i] = live ? y[i] : -INFINITY;
+                        const float m = max8(y, lane);
+                        if (lane < 8) s.red[quad][n0 + c * 8 + lane_col(lane)] = m;
                     }
                     if (bar_or(5 + wg, 128, !ok)) return false;
-                    if (tok < npad) {
-                        float m = max_nan(max_nan(s.red[wg * 4][tok], s.red[wg * 4 + 1][tok]),
-                                          max_nan(s.red[wg * 4 + 2][tok], s.red[wg * 4 + 3][tok]));
+                    if (tok < nw) {
+                        const int n = n0 + tok;
+                        float m = max_nan(max_nan(s.red[0][n], s.red[1][n]), max_nan(s.red[2][n], s.red[3][n]));
                         if (!fresh) m = max_nan(m, 0.f);
                         if (m == -INFINITY) m = 0.f;
-                        s.delta[wg][tok] = ex2(-m);
-                        s.mneg[wg][tok] -= m;
+                        s.delta[n] = ex2(-m);
+                        s.mneg[n] -= m;
                     }
                     named_bar(5 + wg, 128);
                     const float ref = must ? top_v : sref, fs = sref / ref;
                     sref = ref;
-                    const float4 *d4 = reinterpret_cast<const float4 *>(s.delta[wg]);
+                    const float4 *d4 = reinterpret_cast<const float4 *>(s.delta + n0);
 #pragma unroll
-                    for (int i = 0; i < kCols / 4; ++i) {       // (columns past npad hold anything, and are not looked at)
-                        const float4 f = d4[i];
-                        l[2 * i] = mul2(l[2 * i], pair(f.x, f.y));
-                        l[2 * i + 1] = mul2(l[2 * i + 1], pair(f.z, f.w));
-                    }
+                    for (int c = 0; c < T::kSteps; ++c)
+                        if (c < steps) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float4 f = d4[c * 2 + i];
+                                l[c * 4 + 2 * i] = mul2(l[c * 4 + 2 * i], pair(f.x, f.y));
+                                l[c * 4 + 2 * i + 1] = mul2(l[c * 4 + 2 * i + 1], pair(f.z, f.w));
+                            }
+                        }
                     if (!fresh) {
 #pragma unroll 1
-                        for (int c = 0; c < nch; ++c) {
-                            float o[16];
-                            tmem_ld_x16(tm_o + c * 16, reinterpret_cast<uint32_t *>(o));
-                            ld_done(o);
+                        for (int c = 0; c < steps; ++c) {
+                            float o[8];
+                            tmem_ld_x8(tm_o + c * 8, o);
+                            ld_done8(o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] *= s.delta[wg][c * 16 + i] * fs;
-                            tmem_st_x16(tm_o + c * 16, reinterpret_cast<uint32_t *>(o));
+                            for (int i = 0; i < 8; ++i) o[i] *= s.delta[n0 + c * 8 + i] * fs;
+                            tmem_st_x8(tm_o + c * 8, o);
                         }
                         tmem_st_wait();
                     }
@@ -849,86 +852,72 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, 1)
                 };
                 // Once over the scores, as a rule; where a score passes its
                 // reference, once more to take the weights back, and again
-                // under raised references.  One copy of the pass serves all
-                // three: its code is what the instruction caches have to hold.
-                const bool must = fresh || top_v > kScaleRaise * sref;          // the same for every thread
-                for (int turn = must ? 2 : 0;; ++turn) {
-                    if (turn == 2 && !raise(must)) {
-                        ok = false;
-                        break;
+                // under raised references.  One copy of the pass serves all three.
+                if (steps) {
+                    const bool must = fresh || top_v > kScaleRaise * sref;      // the same for every thread
+                    for (int turn = must ? 2 : 0;; ++turn) {
+                        if (turn == 2 && !raise(must)) {
+                            ok = false;
+                            break;
+                        }
+                        const float top = weights(turn == 1 ? -1.f : 1.f);
+                        if (turn == 2 || (turn == 0 && !bar_or(5 + wg, 128, (live && !(top <= kRaise)) || !ok))) break;
                     }
-                    const float top = weights(turn == 1 ? -1.f : 1.f);
-                    if (turn == 2 || (turn == 0 && !bar_or(5 + wg, 128, (live && !(top <= kRaise)) || !ok))) break;
                 }
-                if (!ok) break;
-                fresh = false;
+                if (__any_sync(0xffffffffu, !ok)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_before();
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(bar(s.s_empty[wg]));
-                    mbar_arrive(bar(s.p_full[wg]));
+                    mbar_arrive(bar(s.s_empty[b]));
+                    mbar_arrive(bar(s.p_full[b]));
                 }
             }
-            // ---- the segment's sums: each warpgroup's normalisers, then both
-            // warpgroups' sums merged, alternate chunks to each
-            const uint32_t last = j - 1 - ((j - 1 - wg) & 1);  // the last tile of this warpgroup's parity, if it had one
-            const bool used = !fresh;
-            if (ok && used) ok = wait_phase(bar(s.pv_done[wg]), (last >> 1) & 1, to, p.status, abort);
-            // normalisers over the tokens, through the warpgroup's own P (its last product is done): [column][token], as
-            // many columns at a time as P holds
-            constexpr int kPart = T::kPBytes / (kTile * 4);
-            float *lp = reinterpret_cast<float *>(sm + T::kOffP + wg * T::kPBytes);
-#pragma unroll
-            for (int n0 = 0; n0 < kCols; n0 += kPart) {
-#pragma unroll
-                for (int i = 0; i < kPart; i += 2) {
-                    float x, y;
-                    unpair(l[(n0 + i) / 2], x, y);
-                    lp[i * kTile + tok] = x;
-                    lp[(i + 1) * kTile + tok] = y;
-                }
-                named_bar(5 + wg, 128);
-#pragma unroll 1
-                for (int n = quad; n < kPart; n += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(lp + n * kTile + lane * 4);
-                    float v = (x.x + x.y) + (x.z + x.w);
-#pragma unroll
-                    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-                    if (lane == 0) s.lsum[wg][n0 + n] = v;
-                }
-                named_bar(5 + wg, 128);
-            }
-            if (tok < npad && !used) s.mneg[wg][tok] = INFINITY;   // no maximum: this warpgroup had no tile
-            if (tok == 0) s.sref[wg] = sref;
+            // ---- the segment's sums and normalisers
+            const uint32_t last = j - 1;
+            if (ok) ok = wait_phase(bar(s.pv_done[last & 1]), (last >> 1) & 1, to, p.status, abort);
             if (bar_or(4, kSoft, !ok)) {
                 ok = false;
                 break;
             }
-            const int64_t col0 = (int64_t)g.lo * p.Hq + (int64_t)(g.h * g.rows + g.row0) * p.G + (int64_t)cta * kCols;
-            // a warpgroup without a tile has left no sums: whatever stands there counts for nothing
-            const bool has0 = s.sref[0] > 0.f, has1 = s.sref[1] > 0.f;
-            if (wg == 0 && tok < npad) {
-                const float m0 = -s.mneg[0][tok], m1 = -s.mneg[1][tok], m = max_nan(m0, m1);
-                const float f0 = has0 ? ex2(m0 - m) : 0.f, f1 = has1 ? ex2(m1 - m) : 0.f;
-                s.delta[0][tok] = f0 * s.sref[0] / kHead;
-                s.delta[1][tok] = f1 * s.sref[1] / kHead;
-                if (tok < ncol) p.ml[col0 + tok] = make_float2(m, (has0 ? f0 * s.lsum[0][tok] : 0.f) + (has1 ? f1 * s.lsum[1][tok] : 0.f));
-            }
-            named_bar(4, kSoft);
             tc_fence_after();
-#pragma unroll 1
-            for (int c = wg; c < nch; c += 2) {
-                float o0[16], o1[16];
-                tmem_ld_x16(tmem + lanes + T::kTmO + c * 16, reinterpret_cast<uint32_t *>(o0));
-                tmem_ld_x16(tmem + lanes + T::kTmO + kCols + c * 16, reinterpret_cast<uint32_t *>(o1));
-                ld_done(o0);
-                ld_done(o1);
-                float *dst = p.part + (col0 + c * 16) * kD + tok;
+            // over the tokens, through the two P tiles (every product is done): [column][token]
+            float *lp = reinterpret_cast<float *>(sm + T::kOffP) + n0 * kTile;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c * 16 + i < ncol)
-                        dst[i * kD] = (has0 ? o0[i] * s.delta[0][c * 16 + i] : 0.f) + (has1 ? o1[i] * s.delta[1][c * 16 + i] : 0.f);
+            for (int c = 0; c < T::kSteps; ++c)
+                if (c < steps) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x, y;
+                        unpair(l[c * 4 + i], x, y);
+                        lp[(c * 8 + 2 * i) * kTile + tok] = x;
+                        lp[(c * 8 + 2 * i + 1) * kTile + tok] = y;
+                    }
+                }
+            named_bar(5 + wg, 128);
+            const int64_t col0 = (int64_t)g.lo * p.Hq + (int64_t)(g.h * g.rows + g.row0) * p.G + (int64_t)cta * kCols + n0;
+            const int mine_n = min(nw, ncol - n0);            // of this warpgroup's columns, those that exist
+#pragma unroll 1
+            for (int n = quad; n < mine_n; n += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(lp + n * kTile + lane * 4);
+                float v = (x.x + x.y) + (x.z + x.w);
+#pragma unroll
+                for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+                if (lane == 0) p.ml[col0 + n] = make_float2(-s.mneg[n0 + n], v);
+            }
+            const float back = sref / kHead;
+            float *dst = p.part + col0 * kD + tok;
+#pragma unroll 1
+            for (int c = 0; c < steps; ++c) {
+                float o[8];
+                tmem_ld_x8(tm + T::kTmO + n0 + c * 8, o);
+                ld_done8(o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c * 8 + i < mine_n) dst[(c * 8 + i) * kD] = o[i] * back;
             }
             tc_fence_before();
             at += g.t1 - g.t0;
@@ -1180,11 +1169,11 @@ int launch_attn(const AttnArgs &a, void *stream)
         e = cudaGetLastError();
     };
     if (p.cols == 16)
-        go(k_attn_ctx<16>, Shape<16>::kThreads, smem_bytes<16>());
+        go(k_attn_ctx<16>, kThreads, smem_bytes<16>());
     else if (p.cols == 48)
-        go(k_attn_ctx<48>, Shape<48>::kThreads, smem_bytes<48>());
+        go(k_attn_ctx<48>, kThreads, smem_bytes<48>());
     else
-        go(k_attn_ctx<80>, Shape<80>::kThreads, smem_bytes<80>());
+        go(k_attn_ctx<80>, kThreads, smem_bytes<80>());
     if (e != cudaSuccess) return (int)e;
     constexpr int smem = (kPath * (2 * kD + 1) + 8 * (kD + kPath)) * 4;
     cudaLaunchConfig_t cfg{};
