@@ -31,10 +31,15 @@
 //                would cost four times the bandwidth, which bounds the tile);
 //                P in F16, eleven significant bits, scaled so that there are
 //                2^-18 below a weight of 1 before the subnormals.
-// Four softmax warpgroups share a tile's columns, a few each: sixteen warps
-// hide one another's latencies, the normalisers fit their registers, and a
-// pass over the scores is short code (two warpgroups of ten steps each ran at
-// the rate of the instruction fetches).
+// Two groups of two softmax warpgroups take alternate tiles, each with its own
+// scores, P, maxima and sums, so that the latencies of one tile's chain
+// (product, reads, exponentials, vote, product) hide behind the other's; the
+// warpgroups of a group share the tile's columns.  The groups merge at the end
+// of a segment.  Scores come to the threads in the 16x256b fragments: a thread
+// holds two columns of each eight and four tokens, so a column's factors, its
+// maximum and its normaliser are registers (with a token to a thread they were
+// four 16-byte loads of shared memory to eight columns, and those bound the
+// pass), and P is stored by stmatrix.
 // The maximum is lazy: P refers to a column maximum that is only raised when a
 // score passes it by 2^6 (P stays under F16's top), so the usual tile has no
 // reduction over lanes at all; the same slow path raises the reference of the
@@ -63,10 +68,6 @@ constexpr int kMaxReq = kMaxBudget;
 constexpr uint64_t kDrainNs = 1000000000;  // limit of the waits after a failed one
 constexpr int kSoft = 512;                 // softmax threads, in four warpgroups
 constexpr int kThreads = 128 + kSoft + 256; // warps: 0 K copies, 1 scores, 2 V copies, 3 sums, 4-19 softmax, 20-27 V to F16
-// registers a thread: at launch, of the softmax and converting warps, of the
-// first four.  The shares add up to no more than the launch has.
-constexpr int kRegsLaunch = 72, kRegsSoft = 80, kRegsConv = 64, kRegsOther = 56;
-static_assert(kSoft * kRegsSoft + 256 * kRegsConv + 128 * kRegsOther <= kThreads * kRegsLaunch, "a larger share would wait forever");
 constexpr float kHead = 16.f;              // P of a weight of 1 under the reference scale
 constexpr float kRaise = 6.f;              // a score may pass the column's reference by this (log2) before it is raised
 constexpr float kCap = 8.f;                // scores are held under this until then
@@ -197,7 +198,7 @@ template <int kCols>
 struct Shape {
     static constexpr int kChunks = kCols / 16;
     static constexpr bool kStacked = kCols <= kStack;
-    static constexpr int kSteps = (2 * kChunks + 3) / 4;         // steps of 8 columns of a softmax warpgroup, at most
+    static constexpr int kSteps = kChunks;                       // steps of 8 columns of a softmax warpgroup, at most
     static constexpr int kStK = kCols <= 16 ? 6 : 5;             // K tiles in flight
     static constexpr int kStV = kCols <= 16 ? 6 : kCols <= 48 ? 5 : 4;
     static constexpr int kKBytes = kTile * kD;                   // one K or V tile: 16 KB
@@ -208,10 +209,10 @@ struct Shape {
     static constexpr int kOffP = kOffV + kStV * kKBytes;         // [2][kCols / 16 slabs][128 tokens][16] F16
     static constexpr int kOffQ = kOffP + 2 * kPBytes;            // [3 pieces][kCols][128] E4M3
     static constexpr int kOffShared = kOffQ + 3 * kQBytes;
-    // tensor memory: scores of two tiles, the sums, two V tiles in F16 (two tokens to a column)
+    // tensor memory: scores of two tiles, sums of the two groups, two V tiles in F16 (two tokens to a column)
     static constexpr int kTmS = kStacked ? 3 * kCols : kCols;    // columns of one tile's scores
     static constexpr int kTmO = 2 * kTmS;
-    static constexpr int kTmV = kTmO + kCols;
+    static constexpr int kTmV = kTmO + 2 * kCols;
     static constexpr int kTmUsed = kTmV + kTile;
     static constexpr int kTmCols = kTmUsed <= 256 ? 256 : 512;
     static_assert(kTmUsed <= 512, "tensor memory");
@@ -228,9 +229,11 @@ struct Shared {
     int64_t wsum[kThreads / 32];
     int32_t pre[kMaxReq + 1];                          // first tile of every request
     alignas(16) float cf[kMaxCols];                    // score factor of a column
-    alignas(16) float mneg[kMaxCols];                  // minus its reference maximum
-    alignas(16) float delta[kMaxCols];                 // the factor of its last raise
-    float red[4][kMaxCols];                            // per warp of a warpgroup
+    alignas(16) float mneg[2][kMaxCols];               // per group: minus its reference maximum,
+    alignas(16) float delta[2][kMaxCols];              // the factor of its last raise; at the end, of the group's sums
+    alignas(16) float red[2][4][kMaxCols];             // per warp
+    float lsum[2][kMaxCols];                           // normalisers
+    float sref[2];
     int32_t len[kMaxReq];                              // of every request: cached tokens,
     uint16_t lo[kMaxReq], rows[kMaxReq];               // first row, rows
     float2 scale[kScaleRing][kTile / 32];              // K and V scale of a tile's blocks
@@ -326,11 +329,24 @@ __device__ __forceinline__ float max_nan(float a, float b)
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
-__device__ __forceinline__ float max_nan(float a, float b, float c)
+
+// 32 lanes x 8 columns as two fragments of 16 lanes: thread t gets columns
+// 2 (t % 4) and the next of lanes t / 4 + 8 i in y[2 i], y[2 i + 1]
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float *y)
 {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(y[0]), "=f"(y[1]), "=f"(y[2]), "=f"(y[3])
+                 : "r"(taddr));
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(y[4]), "=f"(y[5]), "=f"(y[6]), "=f"(y[7])
+                 : "r"(taddr + (16u << 16)));
+}
+
+// four 8x8 matrices of 16-bit values, rows at the lanes' addresses
+__device__ __forceinline__ void stsm_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
 }
 
 // 32 lanes x 8 columns
@@ -348,6 +364,16 @@ __device__ __forceinline__ void ld_done8(float *y)
                  : "+f"(y[0]), "+f"(y[1]), "+f"(y[2]), "+f"(y[3]), "+f"(y[4]), "+f"(y[5]), "+f"(y[6]), "+f"(y[7]));
 }
 
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const float *r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "f"(r[0]),
@@ -355,42 +381,11 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const float *r)
                  : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void regs_inc()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
     uint32_t d;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
-}
-
-// The maximum (or NaN) of each of 8 columns over the 32 lanes of a warp:
-// afterwards every lane holds that of column lane_col(lane).  9 shuffles
-// instead of 40.
-__device__ __forceinline__ int lane_col(int lane) { return ((lane & 1) << 2) | (lane & 2) | ((lane & 4) >> 2); }
-
-__device__ __forceinline__ float max8(float (&v)[8], int lane)
-{
-#pragma unroll
-    for (int n = 4, bit = 1; n; n >>= 1, bit <<= 1) {
-        const bool up = lane & bit;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float o = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], bit), k = up ? v[i + n] : v[i];
-            v[i] = max_nan(k, o);
-        }
-    }
-    v[0] = max_nan(v[0], __shfl_xor_sync(0xffffffffu, v[0], 8));
-    return max_nan(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
 template <int kCols>
@@ -436,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(s.s_full[i]), 1);
-            mbar_init(bar(s.s_empty[i]), kSoft / 32);
-            mbar_init(bar(s.p_full[i]), kSoft / 32);
+            mbar_init(bar(s.s_empty[i]), kSoft / 64);
+            mbar_init(bar(s.p_full[i]), kSoft / 64);
             mbar_init(bar(s.v16_full[i]), 4);
             mbar_init(bar(s.pv_done[i]), 1);
         }
@@ -485,7 +480,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Block numbers (and scales) are fetched 32 blocks at a time, one
         // batch ahead of their copies.  A thread's loop of wait, expect and
         // copy takes some 200 ns a turn, so K and V have one each.
-        regs_dec<kRegsOther>();
         const bool is_k = warp == 0;
         const int stages = is_k ? T::kStK : T::kStV;
         const uint32_t full = smem_u32(is_k ? s.k_full : s.v_full), empty = smem_u32(is_k ? s.k_empty : s.v_empty);
@@ -551,7 +545,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ scores: S^T = K Q^T
-        regs_dec<kRegsOther>();
         if (lane == 0) {
             uint32_t j = 0, q = 0, st = 0, par = 0;
             bool ok = true;
@@ -584,7 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 3) {
         // ------------------------------------------------------------ sums: O^T += V^T P
-        regs_dec<kRegsOther>();
         if (lane == 0) {
             uint32_t j = 0;
             bool ok = true;
@@ -598,11 +590,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                          wait_phase(bar(s.p_full[b]), (j >> 1) & 1, to, p.status, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t keep = t > g.t0;           // the first tile starts the sums
+                    const uint32_t keep = t - g.t0 >= 2;      // each group's first tile starts its sums
                     const uint64_t pb = pd + (uint64_t)(b * (T::kPBytes >> 4));
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        tc_mma_ts(tmem + T::kTmO, tmem + T::kTmV + b * (kTile / 2) + k * 8, pb + (uint64_t)(k * (512 >> 4)),
+                        tc_mma_ts(tmem + T::kTmO + b * kCols, tmem + T::kTmV + b * (kTile / 2) + k * 8, pb + (uint64_t)(k * (512 >> 4)),
                                   idesc, keep | (k > 0));
                     tc_commit(bar(s.pv_done[b]));
                 }
@@ -613,7 +605,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= 20) {
         // ------------------------------------------------------------ V to F16
-        regs_dec<kRegsConv>();
         const int wg = (warp - 20) >> 2, quad = warp & 3, d = quad * 32 + lane;   // a dimension to a thread, as the lanes lie
         const int cs = bs - 4;                                // log2 of the 16-token chunks of a row of a block
         const int swz = bs == 5 ? (d >> 2) & 1 : bs == 6 ? (d >> 1) & 3 : d & 7;   // the copy's swizzle: one row's bytes wide
@@ -632,11 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int valid = min(kTile, g.len - t * kTile);
                 const uint8_t *src = sm + T::kOffV + st * T::kKBytes + (d << bs);
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t y[32];
+                for (int part = 0; part < 4; ++part) {
+                    uint32_t y[16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = half * 4 + i, tok = c * 16;             // chunk c of the tile's eight
+                    for (int i = 0; i < 2; ++i) {
+                        const int c = part * 2 + i, tok = c * 16;             // chunk c of the tile's eight
                         const int blk = c >> cs, in = c & ((1 << cs) - 1);
                         const uint4 w = *reinterpret_cast<const uint4 *>(src + ((blk * kD) << bs) + ((in ^ swz) << 4));
                         uint32_t x[4] = {w.x, w.y, w.z, w.w};
@@ -649,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             y[i * 8 + 2 * q + 1] = e4m3x2_f16x2(x[q] >> 16);
                         }
                     }
-                    tmem_st_x32(dst + half * 32, y);
+                    tmem_st_x16(dst + part * 16, y);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -662,9 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             at += g.t1 - g.t0;
         }
     } else if (warp >= 4) {
-        // ------------------------------------------------------------ softmax
-        regs_inc<kRegsSoft>();
-        const int sw = warp - 4, wg = sw >> 2, quad = warp & 3;
+        // ------------------------------------------------------------ softmax: group grp takes the tiles j with j % 2 == grp,
+        // its two warpgroups half of the columns each
+        const int sw = warp - 4, wg = sw >> 2, quad = warp & 3, grp = wg >> 1;
         const int tok = quad * 32 + lane;                     // this thread's token of the tile
         const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
         uint32_t j = 0;
@@ -708,91 +699,89 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) {
                     s.cf[n] = n < ncol ? qs * p.scale2 : 0.f;
-                    s.mneg[n] = 0.f;
+                    s.mneg[0][n] = 0.f;
+                    s.mneg[1][n] = 0.f;
                 }
             }
             fence_async_shared();
             named_bar(4, kSoft);
             if (lane == 0) mbar_arrive(bar(s.q_full));
 
-            // ---- this warpgroup's columns, 8 to a step
-            const int all = npad >> 3, s0 = all * wg >> 2, steps = (all * (wg + 1) >> 2) - s0;
-            const int n0 = s0 * 8, nw = steps * 8;
-            const float4 *cf4 = reinterpret_cast<const float4 *>(s.cf + n0), *mn4 = reinterpret_cast<const float4 *>(s.mneg + n0);
-            uint64_t l[T::kSteps * 4];                        // this token's part of the normalisers, in pairs
+            // ---- this warpgroup's columns, 8 to a step, two of them this thread's
+            const int all = npad >> 3, steps = all >> 1, s0 = (wg & 1) * steps, n0 = s0 * 8, my_n = n0 + (lane & 3) * 2;
+            uint64_t cf[T::kSteps], mneg[T::kSteps], l[T::kSteps];
 #pragma unroll
-            for (int i = 0; i < T::kSteps * 4; ++i) l[i] = 0ull;
-            float sref = 0.f;
-            for (int t = g.t0; t < g.t1; ++t, ++j) {
-                const int b = j & 1;
-                const bool fresh = t == g.t0;
-                ok = wait_phase(bar(s.s_full[b]), (j >> 1) & 1, to, p.status, abort);
-                // this tile's P is free once the product of two tiles ago is done
-                if (ok && j >= 2) ok = wait_phase(bar(s.pv_done[b]), ((j >> 1) - 1) & 1, to, p.status, abort);
+            for (int c = 0; c < T::kSteps; ++c)
+                if (c < steps) {
+                    cf[c] = *reinterpret_cast<const uint64_t *>(s.cf + my_n + c * 8);
+                    mneg[c] = l[c] = 0ull;
+                }
+            float sref = 0.f, inv_ref = 0.f;
+            bool fresh = true;
+            const uint32_t j0 = j;
+            j += g.t1 - g.t0;
+            const uint32_t tm_s = tm + grp * T::kTmS + n0, tm_o = tm + T::kTmO + grp * kCols + n0;
+            const uint32_t prow = base + T::kOffP + grp * T::kPBytes + tok * 32, flip = (tok >> 2) & 1;
+            for (uint32_t jj = j0 + ((j0 ^ grp) & 1); jj < j; jj += 2) {
+                const int t = g.t0 + (int)(jj - j0);
+                ok = wait_phase(bar(s.s_full[grp]), (jj >> 1) & 1, to, p.status, abort);
+                // the group's P and sums are free once its last product is done
+                if (ok && jj >= 2) ok = wait_phase(bar(s.pv_done[grp]), ((jj >> 1) - 1) & 1, to, p.status, abort);
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t tm_s = tm + b * T::kTmS + n0, tm_o = tm + T::kTmO + n0;
-                const float2 my = s.scale[j % kScaleRing][tok >> bs];
-                const float top_v = fmaxf(s.top_v[j % kScaleRing], 1e-30f);
-                const bool live = t * kTile + tok < g.len;
+                const float2 my = s.scale[jj % kScaleRing][(quad * 32) >> bs];   // of the block that this warp's 32 tokens lie in
+                const float top_v = fmaxf(s.top_v[jj % kScaleRing], 1e-30f);
+                const int valid = g.len - t * kTile - quad * 32 - (lane >> 2);   // token i of this thread's four is there if 8 i < valid
                 const uint64_t ks2 = pair(my.x, my.x);
-                // 8 columns' raw scores: asked for, and turned into scores against the references in log2 units
-                auto ask = [&](int c, float *y) { tmem_ld_x8(tm_s + c * 8, y); };
+                // a step's raw scores: asked for, and turned into scores against the references in log2 units
+                auto ask = [&](int c, float *y) { tmem_ld_frag(tm_s + c * 8, y); };
                 auto scores = [&](int c, float *y) {
                     float y1[T::kStacked ? 8 : 1], y2[T::kStacked ? 8 : 1];
                     if constexpr (T::kStacked) {
-                        tmem_ld_x8(tm_s + kCols + c * 8, y1);
-                        tmem_ld_x8(tm_s + 2 * kCols + c * 8, y2);
+                        tmem_ld_frag(tm_s + kCols + c * 8, y1);
+                        tmem_ld_frag(tm_s + 2 * kCols + c * 8, y2);
                         ld_done8(y1);
                         ld_done8(y2);
                     }
                     ld_done8(y);
+                    const uint64_t f = mul2(cf[c], ks2);
 #pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        const float4 f = cf4[c * 2 + (i >> 2)], m = mn4[c * 2 + (i >> 2)];
-                        uint64_t a = pair(y[i], y[i + 1]), b = pair(y[i + 2], y[i + 3]);
-                        if constexpr (T::kStacked) {
-                            a = add2(a, add2(pair(y1[i], y1[i + 1]), pair(y2[i], y2[i + 1])));
-                            b = add2(b, add2(pair(y1[i + 2], y1[i + 3]), pair(y2[i + 2], y2[i + 3])));
-                        }
-                        unpair(fma2(a, mul2(pair(f.x, f.y), ks2), pair(m.x, m.y)), y[i], y[i + 1]);
-                        unpair(fma2(b, mul2(pair(f.z, f.w), ks2), pair(m.z, m.w)), y[i + 2], y[i + 3]);
+                    for (int i = 0; i < 8; i += 2) {
+                        uint64_t a = pair(y[i], y[i + 1]);
+                        if constexpr (T::kStacked) a = add2(a, add2(pair(y1[i], y1[i + 1]), pair(y2[i], y2[i + 1])));
+                        unpair(fma2(a, f, mneg[c]), y[i], y[i + 1]);
                     }
                 };
-                // the tile's weights into P and the normalisers; returns this
-                // token's largest score, over kRaise if the references have to
-                // be raised first (the weights are held finite until then)
+                // The tile's weights into P and the normalisers; returns the
+                // largest score, over kRaise if the references have to be
+                // raised first.  Until then scores are held under kCap, which
+                // also stands for a NaN; a dead token's under everything.
                 auto weights = [&](float sign) -> float {
-                    const float rt = kHead * (my.y / sref), cap = live ? kCap : -INFINITY;   // a dead token weighs nothing
+                    const float rt = my.y * inv_ref;
                     const uint64_t rt2 = pair(rt, rt), sg2 = pair(sign, sign);
-                    uint8_t *prow = sm + T::kOffP + b * T::kPBytes + tok * 32;
-                    const int flip = (tok >> 2) & 1;
-                    float top = -INFINITY;
-                    float y[3][8];                            // one step's weights, the next's scores, the one's after that on their way
+                    float cap[4], top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cap[i] = 8 * i < valid ? kCap : -INFINITY;
+                    float y[2][8];
                     ask(0, y[0]);
-                    scores(0, y[0]);
-                    if (T::kSteps > 1 && steps > 1) ask(1, y[1]);
 #pragma unroll
                     for (int c = 0; c < T::kSteps; ++c)
                         if (c < steps) {
-                            if (c + 1 < T::kSteps && c + 1 < steps) {
-                                scores(c + 1, y[(c + 1) % 3]);
-                                if (c + 2 < T::kSteps && c + 2 < steps) ask(c + 2, y[(c + 2) % 3]);
-                            }
+                            scores(c, y[c & 1]);
+                            if (c + 1 < T::kSteps && c + 1 < steps) ask(c + 1, y[(c + 1) & 1]);
                             uint32_t w[4];
 #pragma unroll
-                            for (int i = 0; i < 8; i += 2) {
-                                const float x0 = y[c % 3][i], x1 = y[c % 3][i + 1];
-                                top = max_nan(top, x0, x1);
-                                const uint64_t e = pair(ex2(fminf(x0, cap)), ex2(fminf(x1, cap)));
-                                l[c * 4 + (i >> 1)] = fma2(e, sg2, l[c * 4 + (i >> 1)]);
+                            for (int i = 0; i < 4; ++i) {
+                                const float x0 = fminf(y[c & 1][2 * i], cap[i]), x1 = fminf(y[c & 1][2 * i + 1], cap[i]);
+                                top = fmaxf(fmaxf(top, x0), x1);
+                                const uint64_t e = pair(ex2(x0), ex2(x1));
+                                l[c] = fma2(e, sg2, l[c]);
                                 float u, v;
                                 unpair(mul2(e, rt2), u, v);
-                                w[i >> 1] = pack_f16x2(u, v);
+                                w[i] = pack_f16x2(u, v);
                             }
-                            const int sc = s0 + c;
-                            *reinterpret_cast<uint4 *>(prow + (sc >> 1) * (kTile * 32) + (((sc & 1) ^ flip) << 4)) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
+                            const uint32_t sc = s0 + c;
+                            stsm_x4(prow + (sc >> 1) * (kTile * 32) + (((sc & 1) ^ flip) << 4), w[0], w[1], w[2], w[3]);
                         }
                     return top;
                 };
@@ -800,41 +789,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // NaN among its scores gets a NaN for its raise, and so carries
                 // it into its normaliser and sums.
                 auto raise = [&](bool must) -> bool {
-                    if (ok && !fresh) ok = wait_phase(bar(s.pv_done[b ^ 1]), ((j - 1) >> 1) & 1, to, p.status, abort);
-                    __syncwarp();
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < steps; ++c) {
-                        float y[8];
-                        ask(c, y);
-                        scores(c, y);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = live ? y[i] : -INFINITY;
-                        const float m = max8(y, lane);
-                        if (lane < 8) s.red[quad][n0 + c * 8 + lane_col(lane)] = m;
-                    }
+                    for (int c = 0; c < T::kSteps; ++c)
+                        if (c < steps) {
+                            float y[8];
+                            ask(c, y);
+                            scores(c, y);
+                            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (8 * i < valid) m0 = max_nan(m0, y[2 * i]), m1 = max_nan(m1, y[2 * i + 1]);
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) {
+                                m0 = max_nan(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+                                m1 = max_nan(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+                            }
+                            if (lane < 4) *reinterpret_cast<float2 *>(&s.red[grp][quad][my_n + c * 8]) = make_float2(m0, m1);
+                        }
                     if (bar_or(5 + wg, 128, !ok)) return false;
-                    if (tok < nw) {
+                    if (tok < steps * 8) {
                         const int n = n0 + tok;
-                        float m = max_nan(max_nan(s.red[0][n], s.red[1][n]), max_nan(s.red[2][n], s.red[3][n]));
+                        float m = max_nan(max_nan(s.red[grp][0][n], s.red[grp][1][n]), max_nan(s.red[grp][2][n], s.red[grp][3][n]));
                         if (!fresh) m = max_nan(m, 0.f);
                         if (m == -INFINITY) m = 0.f;
-                        s.delta[n] = ex2(-m);
-                        s.mneg[n] -= m;
+                        s.delta[grp][n] = ex2(-m);
+                        s.mneg[grp][n] -= m;
                     }
                     named_bar(5 + wg, 128);
                     const float ref = must ? top_v : sref, fs = sref / ref;
                     sref = ref;
-                    const float4 *d4 = reinterpret_cast<const float4 *>(s.delta + n0);
+                    inv_ref = kHead / ref;
 #pragma unroll
                     for (int c = 0; c < T::kSteps; ++c)
                         if (c < steps) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const float4 f = d4[c * 2 + i];
-                                l[c * 4 + 2 * i] = mul2(l[c * 4 + 2 * i], pair(f.x, f.y));
-                                l[c * 4 + 2 * i + 1] = mul2(l[c * 4 + 2 * i + 1], pair(f.z, f.w));
-                            }
+                            l[c] = mul2(l[c], *reinterpret_cast<const uint64_t *>(&s.delta[grp][my_n + c * 8]));
+                            mneg[c] = *reinterpret_cast<const uint64_t *>(&s.mneg[grp][my_n + c * 8]);
                         }
                     if (!fresh) {
 #pragma unroll 1
@@ -843,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_ld_x8(tm_o + c * 8, o);
                             ld_done8(o);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] *= s.delta[n0 + c * 8 + i] * fs;
+                            for (int i = 0; i < 8; ++i) o[i] *= s.delta[grp][n0 + c * 8 + i] * fs;
                             tmem_st_x8(tm_o + c * 8, o);
                         }
                         tmem_st_wait();
@@ -853,71 +842,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Once over the scores, as a rule; where a score passes its
                 // reference, once more to take the weights back, and again
                 // under raised references.  One copy of the pass serves all three.
-                if (steps) {
-                    const bool must = fresh || top_v > kScaleRaise * sref;      // the same for every thread
-                    for (int turn = must ? 2 : 0;; ++turn) {
-                        if (turn == 2 && !raise(must)) {
-                            ok = false;
-                            break;
-                        }
-                        const float top = weights(turn == 1 ? -1.f : 1.f);
-                        if (turn == 2 || (turn == 0 && !bar_or(5 + wg, 128, (live && !(top <= kRaise)) || !ok))) break;
+                const bool must = fresh || top_v > kScaleRaise * sref;          // the same for every thread
+                for (int turn = must ? 2 : 0;; ++turn) {
+                    if (turn == 2 && !raise(must)) {
+                        ok = false;
+                        break;
                     }
+                    const float top = weights(turn == 1 ? -1.f : 1.f);
+                    if (turn == 2 || (turn == 0 && !bar_or(5 + wg, 128, top > kRaise || !ok))) break;
                 }
-                if (__any_sync(0xffffffffu, !ok)) {
-                    ok = false;
-                    break;
-                }
+                if (!ok) break;
+                fresh = false;
                 tc_fence_before();
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(bar(s.s_empty[b]));
-                    mbar_arrive(bar(s.p_full[b]));
+                    mbar_arrive(bar(s.s_empty[grp]));
+                    mbar_arrive(bar(s.p_full[grp]));
                 }
             }
-            // ---- the segment's sums and normalisers
-            const uint32_t last = j - 1;
-            if (ok) ok = wait_phase(bar(s.pv_done[last & 1]), (last >> 1) & 1, to, p.status, abort);
+            // ---- the segment's sums: each group's normalisers, then both groups' sums merged
+            const uint32_t last = j - 1 - ((j - 1 - grp) & 1);     // the last tile of this group's parity, if it had one
+            if (ok && !fresh) ok = wait_phase(bar(s.pv_done[grp]), (last >> 1) & 1, to, p.status, abort);
             if (bar_or(4, kSoft, !ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            // over the tokens, through the two P tiles (every product is done): [column][token]
-            float *lp = reinterpret_cast<float *>(sm + T::kOffP) + n0 * kTile;
 #pragma unroll
             for (int c = 0; c < T::kSteps; ++c)
                 if (c < steps) {
+                    float x, y;
+                    unpair(l[c], x, y);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x, y;
-                        unpair(l[c * 4 + i], x, y);
-                        lp[(c * 8 + 2 * i) * kTile + tok] = x;
-                        lp[(c * 8 + 2 * i + 1) * kTile + tok] = y;
+                    for (int d = 4; d < 32; d <<= 1) {
+                        x += __shfl_xor_sync(0xffffffffu, x, d);
+                        y += __shfl_xor_sync(0xffffffffu, y, d);
                     }
+                    if (lane < 4) *reinterpret_cast<float2 *>(&s.red[grp][quad][my_n + c * 8]) = make_float2(x, y);
                 }
             named_bar(5 + wg, 128);
-            const int64_t col0 = (int64_t)g.lo * p.Hq + (int64_t)(g.h * g.rows + g.row0) * p.G + (int64_t)cta * kCols + n0;
-            const int mine_n = min(nw, ncol - n0);            // of this warpgroup's columns, those that exist
-#pragma unroll 1
-            for (int n = quad; n < mine_n; n += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(lp + n * kTile + lane * 4);
-                float v = (x.x + x.y) + (x.z + x.w);
-#pragma unroll
-                for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-                if (lane == 0) p.ml[col0 + n] = make_float2(-s.mneg[n0 + n], v);
+            if (tok < steps * 8) {
+                const int n = n0 + tok;
+                s.lsum[grp][n] = (s.red[grp][0][n] + s.red[grp][1][n]) + (s.red[grp][2][n] + s.red[grp][3][n]);
+                if (fresh) s.mneg[grp][n] = INFINITY;          // no maximum: the group had no tile
             }
-            const float back = sref / kHead;
-            float *dst = p.part + col0 * kD + tok;
+            if (tok == 0) s.sref[grp] = sref;
+            named_bar(4, kSoft);
+            // a group without a tile has left no sums: whatever stands there counts for nothing
+            const bool has0 = s.sref[0] > 0.f, has1 = s.sref[1] > 0.f;
+            const int64_t col0 = (int64_t)g.lo * p.Hq + (int64_t)(g.h * g.rows + g.row0) * p.G + (int64_t)cta * kCols;
+            if (wg == 0 && tok < npad) {
+                const float m0 = -s.mneg[0][tok], m1 = -s.mneg[1][tok], m = max_nan(m0, m1);
+                const float f0 = has0 ? ex2(m0 - m) : 0.f, f1 = has1 ? ex2(m1 - m) : 0.f;
+                s.delta[0][tok] = f0 * s.sref[0] / kHead;
+                s.delta[1][tok] = f1 * s.sref[1] / kHead;
+                if (tok < ncol) p.ml[col0 + tok] = make_float2(m, (has0 ? f0 * s.lsum[0][tok] : 0.f) + (has1 ? f1 * s.lsum[1][tok] : 0.f));
+            }
+            named_bar(4, kSoft);
 #pragma unroll 1
-            for (int c = 0; c < steps; ++c) {
-                float o[8];
-                tmem_ld_x8(tm + T::kTmO + n0 + c * 8, o);
-                ld_done8(o);
+            for (int c = wg; c < all; c += 4) {
+                float o0[8], o1[8];
+                tmem_ld_x8(tm + T::kTmO + c * 8, o0);
+                tmem_ld_x8(tm + T::kTmO + kCols + c * 8, o1);
+                ld_done8(o0);
+                ld_done8(o1);
+                float *dst = p.part + (col0 + c * 8) * kD + tok;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (c * 8 + i < mine_n) dst[(c * 8 + i) * kD] = o[i] * back;
+                    if (c * 8 + i < ncol)
+                        dst[i * kD] = (has0 ? o0[i] * s.delta[0][c * 8 + i] : 0.f) + (has1 ? o1[i] * s.delta[1][c * 8 + i] : 0.f);
             }
             tc_fence_before();
             at += g.t1 - g.t0;
@@ -1157,14 +1151,6 @@ int launch_attn(const AttnArgs &a, void *stream)
     auto go = [&](auto kernel, int threads, int bytes) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return;
-        static const int regs = [&] {       // the register shares need a launch with this many
-            cudaFuncAttributes f{};
-            return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
-        }();
-        if (regs < kRegsLaunch) {
-            e = cudaErrorInvalidConfiguration;
-            return;
-        }
         kernel<<<p.ctas, threads, bytes, st>>>(kmap, vmap, p);
         e = cudaGetLastError();
     };
