@@ -68,6 +68,12 @@ constexpr int kMaxReq = kMaxBudget;
 constexpr uint64_t kDrainNs = 1000000000;  // limit of the waits after a failed one
 constexpr int kSoft = 512;                 // softmax threads, in four warpgroups
 constexpr int kThreads = 128 + kSoft + 256; // warps: 0 K copies, 1 scores, 2 V copies, 3 sums, 4-19 softmax, 20-27 V to F16
+// Registers a thread: at launch, of the softmax warps, of the others.  The
+// shares add up to no more than the launch has (a larger one would wait for
+// ever).  Shared memory leaves the L1 cache so little that a spilled register
+// is a read of L2, so the softmax warps must not spill.
+constexpr int kRegsLaunch = 72, kRegsSoft = 88, kRegsOther = 48;
+static_assert(kSoft * kRegsSoft + (kThreads - kSoft) * kRegsOther <= kThreads * kRegsLaunch, "register shares");
 constexpr float kHead = 16.f;              // P of a weight of 1 under the reference scale
 constexpr float kRaise = 6.f;              // a score may pass the column's reference by this (log2) before it is raised
 constexpr float kCap = 8.f;                // scores are held under this until then
@@ -381,6 +387,17 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const float *r)
                  : "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
     uint32_t d;
@@ -480,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Block numbers (and scales) are fetched 32 blocks at a time, one
         // batch ahead of their copies.  A thread's loop of wait, expect and
         // copy takes some 200 ns a turn, so K and V have one each.
+        regs_dec<kRegsOther>();
         const bool is_k = warp == 0;
         const int stages = is_k ? T::kStK : T::kStV;
         const uint32_t full = smem_u32(is_k ? s.k_full : s.v_full), empty = smem_u32(is_k ? s.k_empty : s.v_empty);
@@ -545,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ scores: S^T = K Q^T
+        regs_dec<kRegsOther>();
         if (lane == 0) {
             uint32_t j = 0, q = 0, st = 0, par = 0;
             bool ok = true;
@@ -577,6 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 3) {
         // ------------------------------------------------------------ sums: O^T += V^T P
+        regs_dec<kRegsOther>();
         if (lane == 0) {
             uint32_t j = 0;
             bool ok = true;
@@ -605,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= 20) {
         // ------------------------------------------------------------ V to F16
+        regs_dec<kRegsOther>();
         const int wg = (warp - 20) >> 2, quad = warp & 3, d = quad * 32 + lane;   // a dimension to a thread, as the lanes lie
         const int cs = bs - 4;                                // log2 of the 16-token chunks of a row of a block
         const int swz = bs == 5 ? (d >> 2) & 1 : bs == 6 ? (d >> 1) & 3 : d & 7;   // the copy's swizzle: one row's bytes wide
@@ -627,18 +648,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t y[16];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int c = part * 2 + i, tok = c * 16;             // chunk c of the tile's eight
+                        const int c = part * 2 + i;                           // chunk c of the tile's eight
                         const int blk = c >> cs, in = c & ((1 << cs) - 1);
                         const uint4 w = *reinterpret_cast<const uint4 *>(src + ((blk * kD) << bs) + ((in ^ swz) << 4));
-                        uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                        if (tok + 16 > valid)                                 // what lies past the last token is not a value
+                        y[i * 8] = e4m3x2_f16x2(w.x & 0xFFFFu), y[i * 8 + 1] = e4m3x2_f16x2(w.x >> 16);
+                        y[i * 8 + 2] = e4m3x2_f16x2(w.y & 0xFFFFu), y[i * 8 + 3] = e4m3x2_f16x2(w.y >> 16);
+                        y[i * 8 + 4] = e4m3x2_f16x2(w.z & 0xFFFFu), y[i * 8 + 5] = e4m3x2_f16x2(w.z >> 16);
+                        y[i * 8 + 6] = e4m3x2_f16x2(w.w & 0xFFFFu), y[i * 8 + 7] = e4m3x2_f16x2(w.w >> 16);
+                    }
+                    if (part * 32 + 32 > valid) {                             // what lies past the last token is not a value
+                        const int left = valid - part * 32;
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) x[q] &= __funnelshift_lc(0xFFFFFFFFu, 0u, 8 * max(valid - tok - 4 * q, 0));
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            y[i * 8 + 2 * q] = e4m3x2_f16x2(x[q] & 0xFFFFu);
-                            y[i * 8 + 2 * q + 1] = e4m3x2_f16x2(x[q] >> 16);
-                        }
+                        for (int i = 0; i < 16; ++i) y[i] = 2 * i + 1 < left ? y[i] : 2 * i < left ? y[i] & 0xFFFFu : 0u;
                     }
                     tmem_st_x16(dst + part * 16, y);
                 }
@@ -655,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax: group grp takes the tiles j with j % 2 == grp,
         // its two warpgroups half of the columns each
+        regs_inc<kRegsSoft>();
         const int sw = warp - 4, wg = sw >> 2, quad = warp & 3, grp = wg >> 1;
         const int tok = quad * 32 + lane;                     // this thread's token of the tile
         const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
@@ -663,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int32_t at = first; at < end && ok;) {
             const Seg g = segment(p, s, at, end);
             const int ncol = g.nrows * p.G, npad = (ncol + 15) & ~15;
+            const int col0 = g.lo * p.Hq + (g.h * g.rows + g.row0) * p.G + cta * kCols;   // its columns in the workspace
             // ---- Q: turned, scaled to E4M3's range by a power of two, in three pieces
             named_bar(4, kSoft);                              // the last segment's columns are done with
             const int n_q = T::kStacked ? kCols : npad;       // stacked pieces are products of all their columns
@@ -720,10 +743,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool fresh = true;
             const uint32_t j0 = j;
             j += g.t1 - g.t0;
+            const int left0 = g.len - g.t0 * kTile - quad * 32 - (lane >> 2);   // tokens from this thread's first on
             const uint32_t tm_s = tm + grp * T::kTmS + n0, tm_o = tm + T::kTmO + grp * kCols + n0;
             const uint32_t prow = base + T::kOffP + grp * T::kPBytes + tok * 32, flip = (tok >> 2) & 1;
             for (uint32_t jj = j0 + ((j0 ^ grp) & 1); jj < j; jj += 2) {
-                const int t = g.t0 + (int)(jj - j0);
                 ok = wait_phase(bar(s.s_full[grp]), (jj >> 1) & 1, to, p.status, abort);
                 // the group's P and sums are free once its last product is done
                 if (ok && jj >= 2) ok = wait_phase(bar(s.pv_done[grp]), ((jj >> 1) - 1) & 1, to, p.status, abort);
@@ -731,11 +754,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const float2 my = s.scale[jj % kScaleRing][(quad * 32) >> bs];   // of the block that this warp's 32 tokens lie in
                 const float top_v = fmaxf(s.top_v[jj % kScaleRing], 1e-30f);
-                const int valid = g.len - t * kTile - quad * 32 - (lane >> 2);   // token i of this thread's four is there if 8 i < valid
+                const int valid = left0 - (int)(jj - j0) * kTile;                // token i of this thread's four is there if 8 i < valid
                 const uint64_t ks2 = pair(my.x, my.x);
-                // a step's raw scores: asked for, and turned into scores against the references in log2 units
-                auto ask = [&](int c, float *y) { tmem_ld_frag(tm_s + c * 8, y); };
+                // a step's scores against the references, in log2 units
                 auto scores = [&](int c, float *y) {
+                    tmem_ld_frag(tm_s + c * 8, y);
                     float y1[T::kStacked ? 8 : 1], y2[T::kStacked ? 8 : 1];
                     if constexpr (T::kStacked) {
                         tmem_ld_frag(tm_s + kCols + c * 8, y1);
@@ -762,17 +785,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float cap[4], top = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) cap[i] = 8 * i < valid ? kCap : -INFINITY;
-                    float y[2][8];
-                    ask(0, y[0]);
 #pragma unroll
                     for (int c = 0; c < T::kSteps; ++c)
                         if (c < steps) {
-                            scores(c, y[c & 1]);
-                            if (c + 1 < T::kSteps && c + 1 < steps) ask(c + 1, y[(c + 1) & 1]);
+                            float y[8];
+                            scores(c, y);
                             uint32_t w[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const float x0 = fminf(y[c & 1][2 * i], cap[i]), x1 = fminf(y[c & 1][2 * i + 1], cap[i]);
+                                const float x0 = fminf(y[2 * i], cap[i]), x1 = fminf(y[2 * i + 1], cap[i]);
                                 top = fmaxf(fmaxf(top, x0), x1);
                                 const uint64_t e = pair(ex2(x0), ex2(x1));
                                 l[c] = fma2(e, sg2, l[c]);
@@ -793,7 +814,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < T::kSteps; ++c)
                         if (c < steps) {
                             float y[8];
-                            ask(c, y);
                             scores(c, y);
                             float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
@@ -891,7 +911,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_bar(4, kSoft);
             // a group without a tile has left no sums: whatever stands there counts for nothing
             const bool has0 = s.sref[0] > 0.f, has1 = s.sref[1] > 0.f;
-            const int64_t col0 = (int64_t)g.lo * p.Hq + (int64_t)(g.h * g.rows + g.row0) * p.G + (int64_t)cta * kCols;
             if (wg == 0 && tok < npad) {
                 const float m0 = -s.mneg[0][tok], m1 = -s.mneg[1][tok], m = max_nan(m0, m1);
                 const float f0 = has0 ? ex2(m0 - m) : 0.f, f1 = has1 ? ex2(m1 - m) : 0.f;
@@ -907,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_x8(tm + T::kTmO + kCols + c * 8, o1);
                 ld_done8(o0);
                 ld_done8(o1);
-                float *dst = p.part + (col0 + c * 8) * kD + tok;
+                float *dst = p.part + (int64_t)(col0 + c * 8) * kD + tok;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (c * 8 + i < ncol)
@@ -1151,6 +1170,14 @@ int launch_attn(const AttnArgs &a, void *stream)
     auto go = [&](auto kernel, int threads, int bytes) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return;
+        static const int regs = [&] {       // the register shares need a launch with this many
+            cudaFuncAttributes f{};
+            return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
+        }();
+        if (regs < kRegsLaunch) {
+            e = cudaErrorInvalidConfiguration;
+            return;
+        }
         kernel<<<p.ctas, threads, bytes, st>>>(kmap, vmap, p);
         e = cudaGetLastError();
     };
