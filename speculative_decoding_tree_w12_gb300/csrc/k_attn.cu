@@ -157,9 +157,6 @@ __device__ __forceinline__ void load4(Raw4 &x, const uint16_t *row, int d0, int 
     }
 }
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
 __device__ __forceinline__ float4 turn4(const Raw4 &r)
 {
     return make_float4(__fadd_rn(__fmul_rn(bf16_lo(r.w.x), r.c.x), __fmul_rn(bf16_lo(r.v.x), r.s.x)),

@@ -919,6 +919,7 @@ w12_status kv_entry(const w12_kv_cache *c, const w12_rope *rope, int32_t n_req, 
     a.max_blocks = c->max_blocks;
     a.n_req = n_req;
     a.n_rows = n_rows;
+    a.num_sms = num_sms();
     a.k_stride = k_stride;
     a.v_stride = v_stride;
     a.kc = c->k;

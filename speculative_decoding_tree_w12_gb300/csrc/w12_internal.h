@@ -186,6 +186,7 @@ struct RopeArgs {
 };
 struct KvArgs {
     int32_t H, bt, n_blocks, max_blocks, n_req, n_rows;
+    int num_sms;
     int64_t k_stride, v_stride;     // elements between rows
     uint8_t *kc, *vc;
     float *ks, *vs;

@@ -57,26 +57,7 @@ __device__ __forceinline__ float block_scale(float top)
     return __uint_as_float((uint32_t)(e < 95 ? 95 : e) << 23);                  // 95: 2^-32
 }
 
-// element d of a row of kKvDim BF16 values, turned by position pos
-__device__ __forceinline__ float rotated(const uint16_t *row, int d, int pos, const w12i::RopeArgs &r)
-{
-    const float x = bf16_f32(row[d]);
-    if (d >= r.rot) return x;
-    const int half = r.rot >> 1;
-    int f, o;
-    bool second;
-    if (r.adjacent) {
-        f = d >> 1;
-        o = d ^ 1;
-        second = d & 1;
-    } else {
-        second = d >= half;
-        f = second ? d - half : d;
-        o = second ? d - half : d + half;
-    }
-    const float c = __ldg(r.cos + (int64_t)pos * half + f), s = __ldg(r.sin + (int64_t)pos * half + f);
-    const float y = bf16_f32(row[o]);
-    return second ? __fadd_rn(__fmul_rn(x, c), __fmul_rn(y, s)) : __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
-}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 }  // namespace w12d
