@@ -50,12 +50,39 @@ struct KvParams {
 
 __device__ __forceinline__ void fail(int32_t *status) { atomicCAS(status, 0, (int32_t)W12_E_INVAL); }
 
-// codes of four values (not finite: NaN), the first in the low byte
-__device__ __forceinline__ uint32_t codes4(float4 x)
+__device__ __forceinline__ uint64_t pair(float a, float b)
 {
-    if (!(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))) <= 448.f))
-        return to_e4m3(x.x) | (to_e4m3(x.y) << 8) | (to_e4m3(x.z) << 16) | ((uint32_t)to_e4m3(x.w) << 24);
-    return to_e4m3x2(x.x, x.y) | (to_e4m3x2(x.z, x.w) << 16);
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair_bf16(uint32_t w) { return pair(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ float2 unpair(uint64_t d)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(d));
+    return f;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// codes of two pairs of values, the first in the low byte.  `odd`: some may
+// not be finite (their code is NaN, where the conversion alone would saturate).
+__device__ __forceinline__ uint32_t codes4(uint64_t a, uint64_t b, bool odd)
+{
+    const float2 x = unpair(a), y = unpair(b);
+    if (odd) return to_e4m3(x.x) | (to_e4m3(x.y) << 8) | (to_e4m3(y.x) << 16) | ((uint32_t)to_e4m3(y.y) << 24);
+    return to_e4m3x2(x.x, x.y) | (to_e4m3x2(y.x, y.y) << 16);
 }
 
 // four codes under another scale
@@ -65,12 +92,13 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f)
     return to_e4m3x2(a.x * f, a.y * f) | (to_e4m3x2(b.x * f, b.y * f) << 16);
 }
 
-__device__ __forceinline__ float top4(float t, float4 x)
+// the larger magnitude of a pair and t; `finite`: infinities count for nothing (a NaN never does)
+__device__ __forceinline__ float top2(float t, uint64_t a, bool finite)
 {
-    const float a[4] = {fabsf(x.x), fabsf(x.y), fabsf(x.z), fabsf(x.w)};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (a[i] < INFINITY) t = fmaxf(t, a[i]);
+    const float2 x = unpair(a);
+    if (!finite) return fmaxf(fmaxf(t, fabsf(x.x)), fabsf(x.y));
+    if (fabsf(x.x) < INFINITY) t = fmaxf(t, fabsf(x.x));
+    if (fabsf(x.y) < INFINITY) t = fmaxf(t, fabsf(x.y));
     return t;
 }
 
@@ -85,16 +113,16 @@ __device__ __forceinline__ uint4 xor_words(uint4 v, int x)
 // BT: tokens of a block.  kCommit: the new tokens are the root path of
 // acc_node[r], gathered by row; otherwise they are rows off[r] .. off[r + 1] - 1.
 template <int BT, bool kCommit>
-__global__ void __launch_bounds__(BT == 32 ? 256 : 512, 2) k_kv_write(const KvParams p)
+__global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
 {
-    constexpr int kWarps = BT == 32 ? 8 : 16, kThreads = kWarps * 32, kTok = BT / kWarps;   // tokens of a warp: 4 or 8
+    constexpr int kTok = 4, kWarps = BT / kTok, kThreads = kWarps * 32;      // a warp takes four tokens
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t *tile = smem;                                            // [128][BT] value codes, token groups exchanged
     float *tab = reinterpret_cast<float *>(smem + BT * kKvDim);      // [tokens][rot / 2] cosines, then sines
     __shared__ int32_t s_path[kMaxDepth + 2];
     __shared__ int32_t s_parent[kMaxBudget];
     __shared__ int32_t s_r, s_item, s_n, s_ok;
-    __shared__ float s_top[2][kWarps];
+    __shared__ float2 s_top[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h0 = blockIdx.y * p.heads, h1 = min(p.H, h0 + p.heads);
 
@@ -196,63 +224,89 @@ __global__ void __launch_bounds__(BT == 32 ? 256 : 512, 2) k_kv_write(const KvPa
         const int f = p.rope.adjacent ? d0 >> 1 : second ? d0 - half : d0;
         const int mate = !turns || p.rope.adjacent ? lane : second ? lane - (half >> 2) : lane + (half >> 2);
         const int slot0 = warp * kTok;
-        const int64_t row0 = kCommit ? 0 : p.off[r] + (int64_t)(first - len) - held;
+        const int lo_i = max(held - slot0, 0), hi_i = min(end - slot0, kTok);   // of this warp's tokens, the new ones
+        const int j0 = first - len - held + slot0;                  // the first one's place among the request's new tokens
+        const int row0 = kCommit ? 0 : p.off[r] + j0;
+        uint2 kr[kTok], vr[kTok];
+        // the rows of head h; each is asked for as soon as the last head's are used up
+        auto load = [&](uint2 (&x)[kTok], const uint16_t *src, int64_t stride, int h) {
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                x[i] = make_uint2(0, 0);
+                if (i >= lo_i && i < hi_i) {
+                    const int row = kCommit ? s_path[n_new - 1 - j0 - i] : row0 + i;
+                    x[i] = __ldg(reinterpret_cast<const uint2 *>(src + (row * stride + h * kKvDim + d0)));
+                }
+            }
+        };
+        load(kr, p.k, p.k_stride, h0);
+        load(vr, p.v, p.v_stride, h0);
         __syncthreads();
 #pragma unroll 1
         for (int h = h0; h < h1; ++h) {
             const int64_t si = (int64_t)blk * p.H + h;
             const float k_old = p.ks[si], v_old = p.vs[si];
-            uint2 kr[kTok], vr[kTok];
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                const int slot = slot0 + i;
-                kr[i] = vr[i] = make_uint2(0, 0);
-                if (slot >= held && slot < end) {
-                    const int64_t row = kCommit ? (int64_t)s_path[n_new - 1 - (first - len) - (slot - held)] : row0 + slot;
-                    kr[i] = __ldg(reinterpret_cast<const uint2 *>(p.k + row * p.k_stride + (int64_t)h * kKvDim + d0));
-                    vr[i] = __ldg(reinterpret_cast<const uint2 *>(p.v + row * p.v_stride + (int64_t)h * kKvDim + d0));
-                }
-            }
             // ---- turned keys, and the two maxima over finite values
-            float4 x[kTok];
+            uint64_t x[kTok][2];
             float tk = 0.f, tv = 0.f;
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
-                const int slot = slot0 + i;
-                x[i] = make_float4(bf16_lo(kr[i].x), bf16_hi(kr[i].x), bf16_lo(kr[i].y), bf16_hi(kr[i].y));
-                const uint2 o = make_uint2(__shfl_sync(0xffffffffu, kr[i].x, mate), __shfl_sync(0xffffffffu, kr[i].y, mate));
-                if (turns && slot >= held && slot < end) {
-                    float4 c, s, y;
+                x[i][0] = pair_bf16(kr[i].x);
+                x[i][1] = pair_bf16(kr[i].y);
+                const uint32_t o0 = __shfl_sync(0xffffffffu, kr[i].x, mate), o1 = __shfl_sync(0xffffffffu, kr[i].y, mate);
+                if (turns && i >= lo_i && i < hi_i) {
+                    const float *tc = tab + (slot0 + i - held) * half + f, *ts = sn + (slot0 + i - held) * half + f;
+                    uint64_t y[2], c[2], s[2];
                     if (p.rope.adjacent) {
-                        const float2 cc = *reinterpret_cast<const float2 *>(tab + (slot - held) * half + f);
-                        const float2 ss = *reinterpret_cast<const float2 *>(sn + (slot - held) * half + f);
-                        c = make_float4(cc.x, cc.x, cc.y, cc.y);
-                        s = make_float4(-ss.x, ss.x, -ss.y, ss.y);
-                        y = make_float4(x[i].y, x[i].x, x[i].w, x[i].z);
+                        const float2 cc = *reinterpret_cast<const float2 *>(tc), ss = *reinterpret_cast<const float2 *>(ts);
+                        c[0] = pair(cc.x, cc.x), c[1] = pair(cc.y, cc.y);
+                        s[0] = pair(-ss.x, ss.x), s[1] = pair(-ss.y, ss.y);
+                        y[0] = pair(bf16_hi(kr[i].x), bf16_lo(kr[i].x));
+                        y[1] = pair(bf16_hi(kr[i].y), bf16_lo(kr[i].y));
                     } else {
-                        c = *reinterpret_cast<const float4 *>(tab + (slot - held) * half + f);
-                        s = *reinterpret_cast<const float4 *>(sn + (slot - held) * half + f);
-                        if (!second) s = make_float4(-s.x, -s.y, -s.z, -s.w);
-                        y = make_float4(bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y));
+                        const float4 cc = *reinterpret_cast<const float4 *>(tc);
+                        float4 ss = *reinterpret_cast<const float4 *>(ts);
+                        if (!second) ss = make_float4(-ss.x, -ss.y, -ss.z, -ss.w);
+                        c[0] = pair(cc.x, cc.y), c[1] = pair(cc.z, cc.w);
+                        s[0] = pair(ss.x, ss.y), s[1] = pair(ss.z, ss.w);
+                        y[0] = pair_bf16(o0), y[1] = pair_bf16(o1);
                     }
-                    x[i] = make_float4(__fadd_rn(__fmul_rn(x[i].x, c.x), __fmul_rn(y.x, s.x)),
-                                       __fadd_rn(__fmul_rn(x[i].y, c.y), __fmul_rn(y.y, s.y)),
-                                       __fadd_rn(__fmul_rn(x[i].z, c.z), __fmul_rn(y.z, s.z)),
-                                       __fadd_rn(__fmul_rn(x[i].w, c.w), __fmul_rn(y.w, s.w)));
+                    x[i][0] = add2(mul2(x[i][0], c[0]), mul2(y[0], s[0]));
+                    x[i][1] = add2(mul2(x[i][1], c[1]), mul2(y[1], s[1]));
                 }
-                tk = top4(tk, x[i]);
-                tv = top4(tv, make_float4(bf16_lo(vr[i].x), bf16_hi(vr[i].x), bf16_lo(vr[i].y), bf16_hi(vr[i].y)));
+                tk = top2(top2(tk, x[i][0], false), x[i][1], false);
+                tv = top2(top2(tv, pair_bf16(vr[i].x), false), pair_bf16(vr[i].y), false);
             }
+            if (h + 1 < h1) load(kr, p.k, p.k_stride, h + 1);
+            auto reduce = [&]() {
 #pragma unroll
-            for (int d = 16; d; d >>= 1) {
-                tk = fmaxf(tk, __shfl_xor_sync(0xffffffffu, tk, d));
-                tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, d));
+                for (int d = 16; d; d >>= 1) {
+                    tk = fmaxf(tk, __shfl_xor_sync(0xffffffffu, tk, d));
+                    tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, d));
+                }
+                if (lane == 0) s_top[warp] = make_float2(tk, tv);
+                __syncthreads();
+                const float2 t = s_top[lane & (kWarps - 1)];
+                tk = t.x, tv = t.y;
+#pragma unroll
+                for (int d = kWarps / 2; d; d >>= 1) {
+                    tk = fmaxf(tk, __shfl_xor_sync(0xffffffffu, tk, d));
+                    tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, d));
+                }
+            };
+            reduce();
+            // a maximum that is not finite, or a NaN that no maximum shows: count the finite values alone, convert with care
+            bool odd = !(tk < INFINITY) || !(tv < INFINITY);
+            if (odd) {                                               // the same for the whole CTA
+                tk = tv = 0.f;
+#pragma unroll
+                for (int i = 0; i < kTok; ++i) {
+                    tk = top2(top2(tk, x[i][0], true), x[i][1], true);
+                    tv = top2(top2(tv, pair_bf16(vr[i].x), true), pair_bf16(vr[i].y), true);
+                }
+                __syncthreads();
+                reduce();
             }
-            if (lane == 0) s_top[0][warp] = tk, s_top[1][warp] = tv;
-            __syncthreads();
-            tk = tv = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) tk = fmaxf(tk, s_top[0][w]), tv = fmaxf(tv, s_top[1][w]);
             float k_s = block_scale(tk), v_s = block_scale(tv);
             bool k_re = false, v_re = false;
             if (held) {
@@ -262,6 +316,7 @@ __global__ void __launch_bounds__(BT == 32 ? 256 : 512, 2) k_kv_write(const KvPa
                 v_s = fmaxf(v_s, v_old);
             }
             const float k_i = 1.f / k_s, v_i = 1.f / v_s;            // exact: powers of two
+            const uint64_t k_i2 = pair(k_i, k_i), v_i2 = pair(v_i, v_i);
             uint8_t *gk = p.kc + si * (int64_t)(BT * kKvDim), *gv = p.vc + si * (int64_t)(BT * kKvDim);
             // ---- keys, and the held ones under a larger scale
             uint32_t vw[kTok];
@@ -269,42 +324,29 @@ __global__ void __launch_bounds__(BT == 32 ? 256 : 512, 2) k_kv_write(const KvPa
             for (int i = 0; i < kTok; ++i) {
                 const int slot = slot0 + i;
                 uint32_t *dst = reinterpret_cast<uint32_t *>(gk + slot * kKvDim) + lane;
-                if (slot >= held && slot < end)
-                    *dst = codes4(make_float4(x[i].x * k_i, x[i].y * k_i, x[i].z * k_i, x[i].w * k_i));
-                else if (slot < held && k_re)
-                    *dst = rescale4(*dst, k_old / k_s);
-                vw[i] = codes4(make_float4(bf16_lo(vr[i].x) * v_i, bf16_hi(vr[i].x) * v_i, bf16_lo(vr[i].y) * v_i,
-                                           bf16_hi(vr[i].y) * v_i));
+                if (i >= lo_i && i < hi_i) *dst = codes4(mul2(x[i][0], k_i2), mul2(x[i][1], k_i2), odd);
+                else if (slot < held && k_re) *dst = rescale4(*dst, k_old / k_s);
+                vw[i] = codes4(mul2(pair_bf16(vr[i].x), v_i2), mul2(pair_bf16(vr[i].y), v_i2), odd);
             }
-            // ---- values: 4 dimensions x 4 tokens at a time turned over, into the tile
-#pragma unroll
-            for (int i = 0; i < kTok; i += 4) {
-                const uint32_t a = prmt(vw[i], vw[i + 1], 0x5140u), b = prmt(vw[i + 2], vw[i + 3], 0x5140u);
-                const uint32_t c = prmt(vw[i], vw[i + 1], 0x7362u), d = prmt(vw[i + 2], vw[i + 3], 0x7362u);
-                vw[i] = prmt(a, b, 0x5410u);
-                vw[i + 1] = prmt(a, b, 0x7632u);
-                vw[i + 2] = prmt(c, d, 0x5410u);
-                vw[i + 3] = prmt(c, d, 0x7632u);
+            if (h + 1 < h1) load(vr, p.v, p.v_stride, h + 1);
+            // ---- values: 4 dimensions x 4 tokens turned over, into the tile
+            {
+                const uint32_t a = prmt(vw[0], vw[1], 0x5140u), b = prmt(vw[2], vw[3], 0x5140u);
+                const uint32_t c = prmt(vw[0], vw[1], 0x7362u), d = prmt(vw[2], vw[3], 0x7362u);
+                vw[0] = prmt(a, b, 0x5410u);
+                vw[1] = prmt(a, b, 0x7632u);
+                vw[2] = prmt(c, d, 0x5410u);
+                vw[3] = prmt(c, d, 0x7632u);
             }
             const int group = warp ^ (lane & (kWarps - 1));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint8_t *dst = tile + (d0 + i) * BT + group * kTok;
-                if (kTok == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(vw[i], vw[i + 4 < kTok ? i + 4 : i]);
-                else *reinterpret_cast<uint32_t *>(dst) = vw[i];
-            }
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t *>(tile + (d0 + i) * BT + group * 4) = vw[i];
             __syncthreads();
             for (int i = tid; i < BT * kKvDim / 16; i += kThreads) {
                 const int d = i / (BT / 16), c = i % (BT / 16), x4 = (d >> 2) & (kWarps - 1);
                 const int t = c * 16;
                 if (t + 16 <= (v_re ? 0 : held) || t >= end) continue;               // nothing here changes
-                uint4 w;
-                if (kTok == 8) {
-                    w = *reinterpret_cast<const uint4 *>(tile + d * BT + ((2 * c) ^ (x4 & ~1)) * 8);
-                    if (x4 & 1) w = make_uint4(w.z, w.w, w.x, w.y);
-                } else {
-                    w = xor_words(*reinterpret_cast<const uint4 *>(tile + d * BT + (c ^ (x4 >> 2)) * 16), x4 & 3);
-                }
+                uint4 w = xor_words(*reinterpret_cast<const uint4 *>(tile + d * BT + (c ^ (x4 >> 2)) * 16), x4 & 3);
                 uint4 *dst = reinterpret_cast<uint4 *>(gv + d * BT) + c;
                 if (t < held || t + 16 > end) {
                     // some of its tokens are old, or none yet: those bytes stay (or move to the larger scale)
@@ -372,15 +414,16 @@ int launch_kv_write(const KvArgs &a, void *stream)
     p.len_out = a.len_out;
     p.arrive = a.arrive;
     p.status = a.status;
-    // Heads of a CTA: as many as leave two CTAs to an SM (each one more shares
-    // the staged tables; fewer spread a short prompt)
+    // Heads of a CTA: as many as leave every SM two rounds of its threads' worth
+    // of CTAs (each head more shares the staged tables and hides the next one's
+    // loads; fewer spread a short prompt)
     const bool commit = a.acc_node != nullptr;
     // blocks that one request's new tokens can touch: n tokens reach over at
     // most (n - 1) / bt + 2 of them
     p.items = kMaxDepth / a.bt + 2;
     const int64_t x = commit ? (int64_t)a.n_req * p.items : (int64_t)a.n_rows / a.bt + 2ll * a.n_req;
     const int64_t blocks = commit ? a.n_req : std::max<int64_t>(a.n_rows / a.bt, 1);
-    p.heads = (int32_t)std::min<int64_t>(a.H, std::max<int64_t>(1, blocks * a.H / (2 * a.num_sms)));
+    p.heads = (int32_t)std::min<int64_t>(a.H, std::max<int64_t>(1, blocks * a.H * a.bt / (256 * a.num_sms)));
     const dim3 grid((unsigned)x, (unsigned)((a.H + p.heads - 1) / p.heads));
     const int smem = a.bt * (kKvDim + a.rope.rot * 4);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -393,7 +436,7 @@ int launch_kv_write(const KvArgs &a, void *stream)
     };
     if (a.bt == 32) commit ? go(k_kv_write<32, true>, 256) : go(k_kv_write<32, false>, 256);
     else if (a.bt == 64) commit ? go(k_kv_write<64, true>, 512) : go(k_kv_write<64, false>, 512);
-    else commit ? go(k_kv_write<128, true>, 512) : go(k_kv_write<128, false>, 512);
+    else commit ? go(k_kv_write<128, true>, 1024) : go(k_kv_write<128, false>, 1024);
     return (int)e;
 }
 
