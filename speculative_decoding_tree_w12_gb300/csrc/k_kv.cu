@@ -27,6 +27,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "w12_device.cuh"
 #include "w12_kv.cuh"
@@ -102,6 +103,9 @@ __device__ __forceinline__ float top2(float t, uint64_t a, bool finite)
     return t;
 }
 
+// 1 / s of a power of two
+__device__ __forceinline__ float inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
+
 // words 0..3 of a 16-byte chunk in the order i ^ x
 __device__ __forceinline__ uint4 xor_words(uint4 v, int x)
 {
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
     __shared__ int32_t s_path[kMaxDepth + 2];
     __shared__ int32_t s_parent[kMaxBudget];
     __shared__ int32_t s_r, s_item, s_n, s_ok;
-    __shared__ float2 s_top[kWarps];
+    __shared__ uint2 s_top[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h0 = blockIdx.y * p.heads, h1 = min(p.H, h0 + p.heads);
 
@@ -224,152 +228,156 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
         const int f = p.rope.adjacent ? d0 >> 1 : second ? d0 - half : d0;
         const int mate = !turns || p.rope.adjacent ? lane : second ? lane - (half >> 2) : lane + (half >> 2);
         const int slot0 = warp * kTok;
-        const int lo_i = max(held - slot0, 0), hi_i = min(end - slot0, kTok);   // of this warp's tokens, the new ones
-        const int j0 = first - len - held + slot0;                  // the first one's place among the request's new tokens
-        const int row0 = kCommit ? 0 : p.off[r] + j0;
-        uint2 kr[kTok], vr[kTok];
-        // the rows of head h; each is asked for as soon as the last head's are used up
-        auto load = [&](uint2 (&x)[kTok], const uint16_t *src, int64_t stride, int h) {
+        const int j0 = first - len - held + slot0;                   // the warp's first token's place among the request's new ones
+        const int lo_i = max(held - slot0, 0), hi_i = min(end - slot0, kTok);   // of the warp's tokens, the new ones
+        // each thread's 16-byte piece of the transposed values: dimension vd, tokens 16 vc ..
+        const int vd = tid / (BT / 16), vc = tid % (BT / 16), vx = (vd >> 2) & (kWarps - 1);
+        const uint4 *v_src = reinterpret_cast<const uint4 *>(tile + vd * BT) + (vc ^ (vx >> 2));
+        uint32_t *v_tile = reinterpret_cast<uint32_t *>(tile + d0 * BT) + (warp ^ (lane & (kWarps - 1)));
+        const float *tc = tab + (j0 - (first - len)) * half + f, *ts = tc + BT * half;
+        const uint32_t flip = p.rope.adjacent || second ? 0u : 0x80008000u;    // a first half's partner counts negative
+        int row[kTok];
 #pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                x[i] = make_uint2(0, 0);
-                if (i >= lo_i && i < hi_i) {
-                    const int row = kCommit ? s_path[n_new - 1 - j0 - i] : row0 + i;
-                    x[i] = __ldg(reinterpret_cast<const uint2 *>(src + (row * stride + h * kKvDim + d0)));
+        for (int i = 0; i < kTok; ++i) {
+            const bool here = i >= lo_i && i < hi_i;
+            row[i] = !here ? -1 : kCommit ? s_path[n_new - 1 - j0 - i] : p.off[r] + j0 + i;
+        }
+        __syncthreads();
+        // kFull: every slot of the block is new, as in all of a long prompt but its ends
+        auto heads = [&](auto full) {
+            constexpr bool kFull = decltype(full)::value;
+            uint2 kr[kTok], vr[kTok];
+            // the rows of head h; each is asked for as soon as the last head's are used up
+            auto load = [&](uint2 (&x)[kTok], const uint16_t *src, int64_t stride, int h) {
+                src += h * kKvDim + d0;
+                if (kFull && !kCommit) {
+                    src += row[0] * stride;
+#pragma unroll
+                    for (int i = 0; i < kTok; ++i, src += stride) x[i] = __ldg(reinterpret_cast<const uint2 *>(src));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kTok; ++i) {
+                        x[i] = make_uint2(0, 0);
+                        if (row[i] >= 0) x[i] = __ldg(reinterpret_cast<const uint2 *>(src + row[i] * stride));
+                    }
+                }
+            };
+            load(kr, p.k, p.k_stride, h0);
+            load(vr, p.v, p.v_stride, h0);
+#pragma unroll 1
+            for (int h = h0; h < h1; ++h) {
+                const int64_t si = (int64_t)blk * p.H + h;
+                const float k_old = held ? p.ks[si] : 0.f, v_old = held ? p.vs[si] : 0.f;
+                // ---- turned keys, and the two maxima (of the values as they are: their bits order like their magnitudes)
+                uint64_t x[kTok][2];
+                float tk = 0.f;
+                uint32_t vm = 0;
+#pragma unroll
+                for (int i = 0; i < kTok; ++i) {
+                    x[i][0] = pair_bf16(kr[i].x);
+                    x[i][1] = pair_bf16(kr[i].y);
+                    const uint32_t o0 = __shfl_sync(0xffffffffu, kr[i].x, mate) ^ flip, o1 = __shfl_sync(0xffffffffu, kr[i].y, mate) ^ flip;
+                    if (turns && (kFull || row[i] >= 0)) {
+                        uint64_t y[2], c[2], s[2];
+                        if (p.rope.adjacent) {
+                            const float2 cc = *reinterpret_cast<const float2 *>(tc + i * half), ss = *reinterpret_cast<const float2 *>(ts + i * half);
+                            c[0] = pair(cc.x, cc.x), c[1] = pair(cc.y, cc.y);
+                            s[0] = pair(-ss.x, ss.x), s[1] = pair(-ss.y, ss.y);
+                            y[0] = pair(bf16_hi(kr[i].x), bf16_lo(kr[i].x));
+                            y[1] = pair(bf16_hi(kr[i].y), bf16_lo(kr[i].y));
+                        } else {
+                            const float4 cc = *reinterpret_cast<const float4 *>(tc + i * half), ss = *reinterpret_cast<const float4 *>(ts + i * half);
+                            c[0] = pair(cc.x, cc.y), c[1] = pair(cc.z, cc.w);
+                            s[0] = pair(ss.x, ss.y), s[1] = pair(ss.z, ss.w);
+                            y[0] = pair_bf16(o0), y[1] = pair_bf16(o1);
+                        }
+                        x[i][0] = add2(mul2(x[i][0], c[0]), mul2(y[0], s[0]));
+                        x[i][1] = add2(mul2(x[i][1], c[1]), mul2(y[1], s[1]));
+                    }
+                    tk = top2(top2(tk, x[i][0], false), x[i][1], false);
+                    vm = __vmaxu2(__vmaxu2(vm, vr[i].x & 0x7FFF7FFFu), vr[i].y & 0x7FFF7FFFu);
+                }
+                if (h + 1 < h1) load(kr, p.k, p.k_stride, h + 1);
+                float tv = __uint_as_float(max(vm & 0xFFFFu, vm >> 16) << 16);
+                auto reduce = [&]() {                                    // over the CTA; magnitudes order like their bits
+                    const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(tk)), b = __reduce_max_sync(0xffffffffu, __float_as_uint(tv));
+                    if (lane == 0) s_top[warp] = make_uint2(a, b);
+                    __syncthreads();
+                    const uint2 t = s_top[lane & (kWarps - 1)];
+                    tk = __uint_as_float(__reduce_max_sync(0xffffffffu, t.x));
+                    tv = __uint_as_float(__reduce_max_sync(0xffffffffu, t.y));
+                };
+                reduce();
+                // an infinity (or, among the values, a NaN): count the finite values alone, convert with care
+                const bool odd = !(tk < INFINITY) || !(tv < INFINITY);
+                if (odd) {                                               // the same for the whole CTA
+                    tk = tv = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kTok; ++i) {
+                        tk = top2(top2(tk, x[i][0], true), x[i][1], true);
+                        tv = top2(top2(tv, pair_bf16(vr[i].x), true), pair_bf16(vr[i].y), true);
+                    }
+                    __syncthreads();
+                    reduce();
+                }
+                float k_s = block_scale(tk), v_s = block_scale(tv);
+                const bool k_re = held && k_s > k_old, v_re = held && v_s > v_old;
+                if (held) k_s = fmaxf(k_s, k_old), v_s = fmaxf(v_s, v_old);
+                const float k_i = inverse(k_s), v_i = inverse(v_s);
+                const uint64_t k_i2 = pair(k_i, k_i), v_i2 = pair(v_i, v_i);
+                uint8_t *gk = p.kc + si * (int64_t)(BT * kKvDim), *gv = p.vc + si * (int64_t)(BT * kKvDim);
+                // ---- keys, and the held ones under a larger scale
+                uint32_t *k_dst = reinterpret_cast<uint32_t *>(gk + slot0 * kKvDim) + lane;
+                uint32_t vw[kTok];
+#pragma unroll
+                for (int i = 0; i < kTok; ++i) {
+                    uint32_t *dst = k_dst + i * (kKvDim / 4);
+                    if (kFull || row[i] >= 0) *dst = codes4(mul2(x[i][0], k_i2), mul2(x[i][1], k_i2), odd);
+                    else if (k_re && slot0 + i < held) *dst = rescale4(*dst, k_old * k_i);
+                    vw[i] = codes4(mul2(pair_bf16(vr[i].x), v_i2), mul2(pair_bf16(vr[i].y), v_i2), odd);
+                }
+                if (h + 1 < h1) load(vr, p.v, p.v_stride, h + 1);
+                // ---- values: 4 dimensions x 4 tokens turned over, into the tile
+                {
+                    const uint32_t a = prmt(vw[0], vw[1], 0x5140u), b = prmt(vw[2], vw[3], 0x5140u);
+                    const uint32_t c = prmt(vw[0], vw[1], 0x7362u), d = prmt(vw[2], vw[3], 0x7362u);
+                    v_tile[0] = prmt(a, b, 0x5410u);
+                    v_tile[BT / 4] = prmt(a, b, 0x7632u);
+                    v_tile[2 * (BT / 4)] = prmt(c, d, 0x5410u);
+                    v_tile[3 * (BT / 4)] = prmt(c, d, 0x7632u);
+                }
+                __syncthreads();
+                uint4 w = xor_words(*v_src, vx & 3);
+                uint4 *dst = reinterpret_cast<uint4 *>(gv) + tid;
+                const int t = vc * 16;
+                if (kFull) {
+                    *dst = w;
+                } else if (t + 16 > (v_re ? 0 : held) && t < end) {
+                    if (t < held || t + 16 > end) {
+                        // some of its tokens are old, or none yet: those bytes stay (or move to the larger scale)
+                        const uint4 old = *dst;
+                        uint32_t n[4] = {w.x, w.y, w.z, w.w}, q[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int t4 = t + 4 * j;
+                            const int a = min(max(held - t4, 0), 4), b = min(max(end - t4, 0), 4);   // new bytes a .. b - 1
+                            const uint32_t below = a < 4 ? (1u << (8 * a)) - 1u : 0xFFFFFFFFu;
+                            const uint32_t upto = b < 4 ? (1u << (8 * b)) - 1u : 0xFFFFFFFFu;
+                            if (v_re) q[j] = bitmux(below, rescale4(q[j], v_old * v_i), q[j]);
+                            n[j] = bitmux(upto & ~below, n[j], q[j]);
+                        }
+                        w = make_uint4(n[0], n[1], n[2], n[3]);
+                    }
+                    *dst = w;
+                }
+                if (tid == 0) {
+                    p.ks[si] = k_s;
+                    p.vs[si] = v_s;
                 }
             }
         };
-        load(kr, p.k, p.k_stride, h0);
-        load(vr, p.v, p.v_stride, h0);
-        __syncthreads();
-#pragma unroll 1
-        for (int h = h0; h < h1; ++h) {
-            const int64_t si = (int64_t)blk * p.H + h;
-            const float k_old = p.ks[si], v_old = p.vs[si];
-            // ---- turned keys, and the two maxima over finite values
-            uint64_t x[kTok][2];
-            float tk = 0.f, tv = 0.f;
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                x[i][0] = pair_bf16(kr[i].x);
-                x[i][1] = pair_bf16(kr[i].y);
-                const uint32_t o0 = __shfl_sync(0xffffffffu, kr[i].x, mate), o1 = __shfl_sync(0xffffffffu, kr[i].y, mate);
-                if (turns && i >= lo_i && i < hi_i) {
-                    const float *tc = tab + (slot0 + i - held) * half + f, *ts = sn + (slot0 + i - held) * half + f;
-                    uint64_t y[2], c[2], s[2];
-                    if (p.rope.adjacent) {
-                        const float2 cc = *reinterpret_cast<const float2 *>(tc), ss = *reinterpret_cast<const float2 *>(ts);
-                        c[0] = pair(cc.x, cc.x), c[1] = pair(cc.y, cc.y);
-                        s[0] = pair(-ss.x, ss.x), s[1] = pair(-ss.y, ss.y);
-                        y[0] = pair(bf16_hi(kr[i].x), bf16_lo(kr[i].x));
-                        y[1] = pair(bf16_hi(kr[i].y), bf16_lo(kr[i].y));
-                    } else {
-                        const float4 cc = *reinterpret_cast<const float4 *>(tc);
-                        float4 ss = *reinterpret_cast<const float4 *>(ts);
-                        if (!second) ss = make_float4(-ss.x, -ss.y, -ss.z, -ss.w);
-                        c[0] = pair(cc.x, cc.y), c[1] = pair(cc.z, cc.w);
-                        s[0] = pair(ss.x, ss.y), s[1] = pair(ss.z, ss.w);
-                        y[0] = pair_bf16(o0), y[1] = pair_bf16(o1);
-                    }
-                    x[i][0] = add2(mul2(x[i][0], c[0]), mul2(y[0], s[0]));
-                    x[i][1] = add2(mul2(x[i][1], c[1]), mul2(y[1], s[1]));
-                }
-                tk = top2(top2(tk, x[i][0], false), x[i][1], false);
-                tv = top2(top2(tv, pair_bf16(vr[i].x), false), pair_bf16(vr[i].y), false);
-            }
-            if (h + 1 < h1) load(kr, p.k, p.k_stride, h + 1);
-            auto reduce = [&]() {
-#pragma unroll
-                for (int d = 16; d; d >>= 1) {
-                    tk = fmaxf(tk, __shfl_xor_sync(0xffffffffu, tk, d));
-                    tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, d));
-                }
-                if (lane == 0) s_top[warp] = make_float2(tk, tv);
-                __syncthreads();
-                const float2 t = s_top[lane & (kWarps - 1)];
-                tk = t.x, tv = t.y;
-#pragma unroll
-                for (int d = kWarps / 2; d; d >>= 1) {
-                    tk = fmaxf(tk, __shfl_xor_sync(0xffffffffu, tk, d));
-                    tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, d));
-                }
-            };
-            reduce();
-            // a maximum that is not finite, or a NaN that no maximum shows: count the finite values alone, convert with care
-            bool odd = !(tk < INFINITY) || !(tv < INFINITY);
-            if (odd) {                                               // the same for the whole CTA
-                tk = tv = 0.f;
-#pragma unroll
-                for (int i = 0; i < kTok; ++i) {
-                    tk = top2(top2(tk, x[i][0], true), x[i][1], true);
-                    tv = top2(top2(tv, pair_bf16(vr[i].x), true), pair_bf16(vr[i].y), true);
-                }
-                __syncthreads();
-                reduce();
-            }
-            float k_s = block_scale(tk), v_s = block_scale(tv);
-            bool k_re = false, v_re = false;
-            if (held) {
-                k_re = k_s > k_old;
-                v_re = v_s > v_old;
-                k_s = fmaxf(k_s, k_old);
-                v_s = fmaxf(v_s, v_old);
-            }
-            const float k_i = 1.f / k_s, v_i = 1.f / v_s;            // exact: powers of two
-            const uint64_t k_i2 = pair(k_i, k_i), v_i2 = pair(v_i, v_i);
-            uint8_t *gk = p.kc + si * (int64_t)(BT * kKvDim), *gv = p.vc + si * (int64_t)(BT * kKvDim);
-            // ---- keys, and the held ones under a larger scale
-            uint32_t vw[kTok];
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                const int slot = slot0 + i;
-                uint32_t *dst = reinterpret_cast<uint32_t *>(gk + slot * kKvDim) + lane;
-                if (i >= lo_i && i < hi_i) *dst = codes4(mul2(x[i][0], k_i2), mul2(x[i][1], k_i2), odd);
-                else if (slot < held && k_re) *dst = rescale4(*dst, k_old / k_s);
-                vw[i] = codes4(mul2(pair_bf16(vr[i].x), v_i2), mul2(pair_bf16(vr[i].y), v_i2), odd);
-            }
-            if (h + 1 < h1) load(vr, p.v, p.v_stride, h + 1);
-            // ---- values: 4 dimensions x 4 tokens turned over, into the tile
-            {
-                const uint32_t a = prmt(vw[0], vw[1], 0x5140u), b = prmt(vw[2], vw[3], 0x5140u);
-                const uint32_t c = prmt(vw[0], vw[1], 0x7362u), d = prmt(vw[2], vw[3], 0x7362u);
-                vw[0] = prmt(a, b, 0x5410u);
-                vw[1] = prmt(a, b, 0x7632u);
-                vw[2] = prmt(c, d, 0x5410u);
-                vw[3] = prmt(c, d, 0x7632u);
-            }
-            const int group = warp ^ (lane & (kWarps - 1));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t *>(tile + (d0 + i) * BT + group * 4) = vw[i];
-            __syncthreads();
-            for (int i = tid; i < BT * kKvDim / 16; i += kThreads) {
-                const int d = i / (BT / 16), c = i % (BT / 16), x4 = (d >> 2) & (kWarps - 1);
-                const int t = c * 16;
-                if (t + 16 <= (v_re ? 0 : held) || t >= end) continue;               // nothing here changes
-                uint4 w = xor_words(*reinterpret_cast<const uint4 *>(tile + d * BT + (c ^ (x4 >> 2)) * 16), x4 & 3);
-                uint4 *dst = reinterpret_cast<uint4 *>(gv + d * BT) + c;
-                if (t < held || t + 16 > end) {
-                    // some of its tokens are old, or none yet: those bytes stay (or move to the larger scale)
-                    uint4 old = *dst;
-                    uint32_t n[4] = {w.x, w.y, w.z, w.w}, q[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int t4 = t + 4 * j;
-                        const int a = min(max(held - t4, 0), 4), b = min(max(end - t4, 0), 4);   // new bytes a .. b - 1
-                        const uint32_t below = a < 4 ? (1u << (8 * a)) - 1u : 0xFFFFFFFFu;
-                        const uint32_t upto = b < 4 ? (1u << (8 * b)) - 1u : 0xFFFFFFFFu;
-                        if (v_re) q[j] = bitmux(below, rescale4(q[j], v_old / v_s), q[j]);
-                        n[j] = bitmux(upto & ~below, n[j], q[j]);
-                    }
-                    w = make_uint4(n[0], n[1], n[2], n[3]);
-                }
-                *dst = w;
-            }
-            if (tid == 0) {
-                p.ks[si] = k_s;
-                p.vs[si] = v_s;
-            }
-        }
+        if (held == 0 && end == BT) heads(std::true_type{});
+        else heads(std::false_type{});
     }
     // ---- the request's last CTA to get here writes its length (len_out may be
     // the cache's own array: every CTA has read it by then).  The counter goes
