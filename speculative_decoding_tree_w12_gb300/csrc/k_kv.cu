@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
         // kFull: every slot of the block is new, as in all of a long prompt but its ends
         auto heads = [&](auto full) {
             constexpr bool kFull = decltype(full)::value;
-            uint2 kr[kTok], vr[kTok];
+            uint2 kr[kTok], vr[kTok], vn[kTok];                      // next head's keys; this head's and the next one's values
             // the rows of head h; each is asked for as soon as the last head's are used up
             auto load = [&](uint2 (&x)[kTok], const uint16_t *src, int64_t stride, int h) {
                 src += h * kKvDim + d0;
@@ -263,12 +263,14 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
                 }
             };
             load(kr, p.k, p.k_stride, h0);
-            load(vr, p.v, p.v_stride, h0);
+            load(vn, p.v, p.v_stride, h0);
 #pragma unroll 1
             for (int h = h0; h < h1; ++h) {
                 const int64_t si = (int64_t)blk * p.H + h;
                 const float k_old = held ? p.ks[si] : 0.f, v_old = held ? p.vs[si] : 0.f;
                 // ---- turned keys, and the two maxima (of the values as they are: their bits order like their magnitudes)
+#pragma unroll
+                for (int i = 0; i < kTok; ++i) vr[i] = vn[i];
                 uint64_t x[kTok][2];
                 float tk = 0.f;
                 uint32_t vm = 0;
@@ -297,7 +299,10 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
                     tk = top2(top2(tk, x[i][0], false), x[i][1], false);
                     vm = __vmaxu2(__vmaxu2(vm, vr[i].x & 0x7FFF7FFFu), vr[i].y & 0x7FFF7FFFu);
                 }
-                if (h + 1 < h1) load(kr, p.k, p.k_stride, h + 1);
+                if (h + 1 < h1) {
+                    load(kr, p.k, p.k_stride, h + 1);
+                    load(vn, p.v, p.v_stride, h + 1);
+                }
                 float tv = __uint_as_float(max(vm & 0xFFFFu, vm >> 16) << 16);
                 auto reduce = [&]() {                                    // over the CTA; magnitudes order like their bits
                     const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(tk)), b = __reduce_max_sync(0xffffffffu, __float_as_uint(tv));
@@ -336,7 +341,6 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
                     else if (k_re && slot0 + i < held) *dst = rescale4(*dst, k_old * k_i);
                     vw[i] = codes4(mul2(pair_bf16(vr[i].x), v_i2), mul2(pair_bf16(vr[i].y), v_i2), odd);
                 }
-                if (h + 1 < h1) load(vr, p.v, p.v_stride, h + 1);
                 // ---- values: 4 dimensions x 4 tokens turned over, into the tile
                 {
                     const uint32_t a = prmt(vw[0], vw[1], 0x5140u), b = prmt(vw[2], vw[3], 0x5140u);
