@@ -149,6 +149,30 @@ def _stream(stream=None):
     return C.c_void_p(st.cuda_stream)
 
 
+# What the calls of a decode loop look up once: the types they accept and the
+# runtime's own query of the current stream (a call of some 0.2 us; building a
+# torch.cuda.Stream object takes fifteen times that).
+_torch = _raw_stream = None
+
+
+def _runtime():
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        if current is not None and device is not None:
+            _raw_stream = lambda: current(device())
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+        _torch = torch
+    return _torch
+
+
+def _st(stream) -> int:
+    return _raw_stream() if stream is None else stream.cuda_stream
+
+
 def _dp(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -225,7 +249,7 @@ class Workspace:
         if nbytes == 0:
             raise W12Error(W12_E_UNSUPPORTED, "w12_workspace_bytes")
         self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-        self.nbytes = nbytes
+        self.nbytes, self.addr = nbytes, self.buf.data_ptr()
         _check(lib().w12_workspace_init(self.ptr, nbytes, _stream()), "w12_workspace_init")
 
     @property
@@ -547,6 +571,22 @@ def _want(t, dtype, shape, what):
         raise ValueError(f"{what}: contiguous {dtype} {shape} wanted, got {t.dtype} {tuple(t.shape)}")
 
 
+def _ints(t, n, what) -> int:
+    """The address of n contiguous int32."""
+    if t.dtype is not _torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous int32 [{n}] wanted, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, rows, width, what):
+    """(address, elements between rows) of `rows` or more bfloat16 rows of `width` contiguous elements."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not _torch.bfloat16 or len(shape) != 2 or shape[1] != width or shape[0] < rows or stride[1] != 1:
+        raise ValueError(f"{what}: bfloat16 rows [>= {rows}][{width}] with contiguous elements wanted, got "
+                         f"{t.dtype} {tuple(shape)}")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], width)
+
+
 class KvCache:
     """A paged KV cache: E4M3 codes k (uint8 [n_blocks][H][block_tokens][128])
     and v (uint8 [n_blocks][H][128][block_tokens]), power-of-two scales
@@ -554,7 +594,8 @@ class KvCache:
     the committed lengths (int32 [n_req]).  The tensors stay the caller's."""
 
     def __init__(self, k, v, k_scale, v_scale, block_table, length):
-        import torch
+        torch = _runtime()
+        lib()
         n, H, bt, d = k.shape
         _want(k, torch.uint8, (n, H, bt, d), "k")
         _want(v, torch.uint8, (n, H, d, bt), "v")
@@ -600,39 +641,22 @@ class AttentionWorkspace:
         if self.nbytes == 0:
             raise W12Error(W12_E_UNSUPPORTED, "w12_attn_workspace_bytes")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
-        self.ptr = C.c_void_p(self.buf.data_ptr())
-
-
-def _bf16_rows(t, rows, what):
-    """(pointer, elements between rows) of bf16 rows whose elements are contiguous."""
-    import torch
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.stride(1) != 1 or t.shape[0] < rows:
-        raise ValueError(f"{what}: bfloat16 rows [>= {rows}][heads * 128] with contiguous elements wanted")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), -(-t.shape[1] // 8) * 8))
-
-
-def _kv_rows(cache, k, v, rows):
-    for t, what in ((k, "k"), (v, "v")):
-        if t.shape[-1] != cache.H * cache.d:
-            raise ValueError(f"{what}: rows of {cache.H * cache.d} elements wanted")
-    return (*_bf16_rows(k, rows, "k"), *_bf16_rows(v, rows, "v"))
+        self.addr = self.buf.data_ptr()
 
 
 def w12_kv_append(cache: KvCache, rope: Optional[Rope], k, v, row_off, ws: Workspace, len_out=None, stream=None):
     """Append rows row_off[r]..row_off[r+1]-1 of k and v (bfloat16 [T][H * 128],
     row slices allowed) to every request's tokens; the new lengths go to
     ``len_out`` (default: in place)."""
-    import torch
-    _want(row_off, torch.int32, (cache.n_req + 1,), "row_off")
-    len_out = cache.len if len_out is None else len_out
-    _want(len_out, torch.int32, (cache.n_req,), "len_out")
-    T = k.shape[0]
+    n, T, width = cache.n_req, k.shape[0], cache.H * cache.d
     if v.shape[0] != T:
         raise ValueError("k and v: the same number of rows wanted")
-    kp, ks, vp, vs = _kv_rows(cache, k, v, T)
-    _check(lib().w12_kv_append(cache.ref, rope.ref if rope else None, cache.n_req, kp, ks, vp, vs, T,
-                               row_off.data_ptr(), len_out.data_ptr(), ws.ptr, ws.nbytes, _stream(stream)),
-           "w12_kv_append")
+    if len_out is None:
+        len_out = cache.len
+    s = _lib.w12_kv_append(cache.ref, rope.ref if rope else None, n, *_rows(k, T, width, "k"), *_rows(v, T, width, "v"), T,
+                           _ints(row_off, n + 1, "row_off"), _ints(len_out, n, "len_out"), ws.addr, ws.nbytes, _st(stream))
+    if s:
+        raise W12Error(s, "w12_kv_append")
     return len_out
 
 
@@ -640,15 +664,16 @@ def w12_kv_commit(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n_req:
                   len_out=None, stream=None):
     """Append the accepted path of every request (root .. acc_node[r]) to its
     tokens; k and v are the tree's rows."""
-    import torch
     if n_req != cache.n_req:
         raise ValueError("the cache's table and the tree: the same requests wanted")
-    _want(acc_node, torch.int32, (n_req,), "acc_node")
-    len_out = cache.len if len_out is None else len_out
-    _want(len_out, torch.int32, (n_req,), "len_out")
-    kp, ks, vp, vs = _kv_rows(cache, k, v, tree.c.R)
-    _check(lib().w12_kv_commit(cache.ref, rope.ref if rope else None, C.byref(tree.c), n_req, acc_node.data_ptr(), kp,
-                               ks, vp, vs, len_out.data_ptr(), ws.ptr, ws.nbytes, _stream(stream)), "w12_kv_commit")
+    if len_out is None:
+        len_out = cache.len
+    R, width = tree.c.R, cache.H * cache.d
+    s = _lib.w12_kv_commit(cache.ref, rope.ref if rope else None, C.byref(tree.c), n_req, _ints(acc_node, n_req, "acc_node"),
+                           *_rows(k, R, width, "k"), *_rows(v, R, width, "v"), _ints(len_out, n_req, "len_out"), ws.addr,
+                           ws.nbytes, _st(stream))
+    if s:
+        raise W12Error(s, "w12_kv_commit")
     return len_out
 
 
@@ -658,19 +683,19 @@ def w12_tree_attention(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n
     bfloat16 [R][n_heads][128].  q (bfloat16 [R][n_heads * 128]), k, v: the
     linears' rows before rotation (slices of a fused row are fine); scale:
     default 128 ** -0.5."""
-    import torch
     if n_req != cache.n_req:
         raise ValueError("the cache's table and the tree: the same requests wanted")
-    R, Hq = tree.c.R, q.shape[1] // cache.d
+    R, d, width, width_q = tree.c.R, cache.d, cache.H * cache.d, q.shape[-1]
+    Hq = width_q // d
     if out is None:
-        out = torch.empty((R, Hq, cache.d), dtype=torch.bfloat16, device=q.device)
-    elif out.shape[0] < R or out.shape[1:] != (Hq, cache.d) or out.dtype != torch.bfloat16 or not out.is_contiguous():
-        raise ValueError(f"out: contiguous bfloat16 [{R}][{Hq}][{cache.d}] wanted")
-    qp, qs = _bf16_rows(q, R, "q")
-    kp, ks, vp, vs = _kv_rows(cache, k, v, R)
-    _check(lib().w12_tree_attention(cache.ref, rope.ref if rope else None, C.byref(tree.c), n_req, Hq, qp, qs, kp, ks,
-                                    vp, vs, cache.d ** -0.5 if scale is None else scale, out.data_ptr(), ws.ptr,
-                                    ws.nbytes, aws.ptr, aws.nbytes, _stream(stream)), "w12_tree_attention")
+        out = _torch.empty((R, Hq, d), dtype=_torch.bfloat16, device=q.device)
+    elif out.shape[0] < R or out.shape[1:] != (Hq, d) or out.dtype is not _torch.bfloat16 or not out.is_contiguous():
+        raise ValueError(f"out: contiguous bfloat16 [{R}][{Hq}][{d}] wanted")
+    s = _lib.w12_tree_attention(cache.ref, rope.ref if rope else None, C.byref(tree.c), n_req, Hq, *_rows(q, R, Hq * d, "q"),
+                                *_rows(k, R, width, "k"), *_rows(v, R, width, "v"), d ** -0.5 if scale is None else scale,
+                                out.data_ptr(), ws.addr, ws.nbytes, aws.addr, aws.nbytes, _st(stream))
+    if s:
+        raise W12Error(s, "w12_tree_attention")
     return out
 
 
@@ -691,7 +716,8 @@ class SampleRows:
     its probabilities draft_p (float32 [R][vocab]) with u_accept (float32 [R])."""
 
     def __init__(self, logits, u_sample, temperature=None, draft_p=None, u_accept=None):
-        import torch
+        torch = _runtime()
+        lib()
         R, V = logits.shape
         if logits.dtype not in (torch.bfloat16, torch.float32) or logits.stride(1) != 1:
             raise ValueError("logits: bfloat16 or float32 [R][vocab] with contiguous elements wanted")
@@ -711,9 +737,11 @@ class SampleRows:
         self.c = SamplingC(logits.data_ptr(), int(logits.dtype == torch.float32), V, row(logits), _dp(temperature),
                            _dp(draft_p), row(draft_p) if draft_p is not None else 0, _dp(u_accept), _dp(u_sample))
         self.ref = C.byref(self.c)
+        self.rows = R
+        self.requests = None if temperature is None else int(temperature.shape[0])
 
     def _fits(self, tree, n_req):
-        if self.logits.shape[0] < tree.c.R or (self.temperature is not None and self.temperature.shape[0] < n_req):
+        if self.rows < tree.c.R or (self.requests is not None and self.requests < n_req):
             raise ValueError("logits: a row for every row of the tree wanted, and a temperature for every request")
 
 
@@ -721,29 +749,44 @@ def w12_tree_sample(dist: SampleRows, tree: DeviceTree, n_req: int, ws: Workspac
                     stream=None):
     """One token per tree row, distributed as the target's probabilities
     there -> int32 [R]; its log-probability to ``row_logp`` (float32 [R])."""
-    import torch
     dist._fits(tree, n_req)
+    R = tree.c.R
     if row_tok is None:
-        row_tok = torch.empty(tree.c.R, dtype=torch.int32, device=dist.logits.device)
-    _check(lib().w12_tree_sample(dist.ref, C.byref(tree.c), n_req, row_tok.data_ptr(), _dp(row_logp), ws.ptr,
-                                 ws.nbytes, _stream(stream)), "w12_tree_sample")
+        row_tok = _torch.empty(R, dtype=_torch.int32, device=dist.logits.device)
+    s = _lib.w12_tree_sample(dist.ref, C.byref(tree.c), n_req, _ints(row_tok, R, "row_tok"), _floats(row_logp, R), ws.addr,
+                             ws.nbytes, _st(stream))
+    if s:
+        raise W12Error(s, "w12_tree_sample")
     return row_tok
+
+
+def _floats(t, n):
+    if t is None:
+        return None
+    if t.dtype is not _torch.float32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"row_logp: contiguous float32 [{n}] wanted")
+    return t.data_ptr()
 
 
 def w12_tree_verify_sampled(dist: SampleRows, tree: DeviceTree, n_req: int, p_max: int, ws: Workspace, row_tok=None,
                             row_logp=None, acc_tok=None, acc_len=None, acc_node=None, stream=None):
     """``w12_tree_sample`` and the acceptance of the children that carry their
     parent's token -> acc_tok, acc_len, acc_node."""
-    import torch
     dist._fits(tree, n_req)
-    new = lambda *s: torch.empty(s, dtype=torch.int32, device=dist.logits.device)
-    row_tok = row_tok if row_tok is not None else new(tree.c.R)
-    acc_tok = acc_tok if acc_tok is not None else new(n_req, p_max + 1)
-    acc_len = acc_len if acc_len is not None else new(n_req)
-    acc_node = acc_node if acc_node is not None else new(n_req)
-    _check(lib().w12_tree_verify_sampled(dist.ref, C.byref(tree.c), n_req, p_max, row_tok.data_ptr(), _dp(row_logp),
-                                         acc_tok.data_ptr(), acc_len.data_ptr(), acc_node.data_ptr(), ws.ptr,
-                                         ws.nbytes, _stream(stream)), "w12_tree_verify_sampled")
+    R = tree.c.R
+    if row_tok is None or acc_tok is None or acc_len is None or acc_node is None:
+        new = lambda *s: _torch.empty(s, dtype=_torch.int32, device=dist.logits.device)
+        row_tok = row_tok if row_tok is not None else new(R)
+        acc_tok = acc_tok if acc_tok is not None else new(n_req, p_max + 1)
+        acc_len = acc_len if acc_len is not None else new(n_req)
+        acc_node = acc_node if acc_node is not None else new(n_req)
+    if acc_tok.shape != (n_req, p_max + 1) or acc_tok.dtype is not _torch.int32 or not acc_tok.is_contiguous():
+        raise ValueError(f"acc_tok: contiguous int32 [{n_req}][{p_max + 1}] wanted")
+    s = _lib.w12_tree_verify_sampled(dist.ref, C.byref(tree.c), n_req, p_max, _ints(row_tok, R, "row_tok"),
+                                     _floats(row_logp, R), acc_tok.data_ptr(), _ints(acc_len, n_req, "acc_len"),
+                                     _ints(acc_node, n_req, "acc_node"), ws.addr, ws.nbytes, _st(stream))
+    if s:
+        raise W12Error(s, "w12_tree_verify_sampled")
     return acc_tok, acc_len, acc_node
 
 
