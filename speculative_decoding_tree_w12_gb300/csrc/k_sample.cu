@@ -15,9 +15,12 @@
 // and inverse-CDF boundaries are exact.  (Weights under 2^-40 of the largest
 // are never drawn.)
 //
-// A cluster of CTAs shares a row: each holds its slice of the weights in
-// shared memory, so the logits are read from memory once; maxima and sums
-// cross the cluster through distributed shared memory.
+// A cluster of CTAs shares a row; maxima and sums cross it through distributed
+// shared memory.  The logits are read from memory once, 16 bytes at a time, and
+// wait in registers for the maximum; only a drafter's probabilities, which
+// change the weights round by round, make the weights go to shared memory.
+// The token is found by the sums alone down to one warp's stretch of the row,
+// which that warp reads again in order.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -37,13 +40,12 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 49152;               // weights of one CTA: 192 KB
-constexpr float kUnit = 1099511627776.f;       // 2^40
 
 struct SampleParams {
     const void *logits;
     int64_t stride, draft_stride;
     const float *temperature, *draft_p, *u_accept, *u_sample;
-    int32_t vocab, slice, sub;                 // tokens; of one CTA; of one warp
+    int32_t vocab, sub;                        // tokens; 16-byte pieces of the row of one warp
     int32_t R, n_req;
     const int32_t *parent, *token, *req, *off;
     int32_t *row_tok;
@@ -51,24 +53,34 @@ struct SampleParams {
     int32_t *status;
 };
 
-// floor(a 2^40) for 0 <= a <= 1 (and a few units above)
-__device__ __forceinline__ u64 fixed40(float a)
+// Sums of whole numbers floor(e 2^40), 0 <= e <= 1.  Adding 8 with rounding
+// towards zero leaves floor(e 2^20) in the low bits of the sum, subtracting it
+// again the exact rest; 2^-17 splits that the same way.  Both parts are summed
+// as the bits they come in; what the added constants put there is taken off at
+// the end (modulo 2^32: a thread's own sums stay under 2^32).
+struct Sum40 {
+    uint32_t hi = 0, lo = 0, n = 0;
+    __device__ __forceinline__ void add(float e)
+    {
+        const float t = __fadd_rz(e, 8.f);
+        hi += __float_as_uint(t);
+        lo += __float_as_uint(__fadd_rz(__fsub_rn(e, __fsub_rn(t, 8.f)), 0x1p-17f));
+        ++n;
+    }
+    __device__ __forceinline__ u64 get() const
+    {
+        return ((u64)(hi - n * __float_as_uint(8.f)) << 20) + (lo - n * __float_as_uint(0x1p-17f));
+    }
+};
+
+__device__ __forceinline__ u64 fixed40(float e)
 {
-    const uint32_t u = __float_as_uint(a);
-    const int s = (int)(u >> 23) - 110;        // a = m 2^(e - 150): m 2^(e - 110)
-    const u64 m = (u & 0x7FFFFFu) | 0x800000u;
-    return s >= 0 ? m << s : (s > -24 ? m >> -s : 0ull);
+    Sum40 s;
+    s.add(e);
+    return s.get();
 }
 
-__device__ __forceinline__ float weight_of(u64 total) { return __fmul_rn(__ull2float_rn(total), 1.f / kUnit); }
-
-// larger float first, then the lower index (NaN is never entered)
-__device__ __forceinline__ u64 max_key(float z, int v)
-{
-    const uint32_t b = __float_as_uint(z);
-    const uint32_t o = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-    return ((u64)o << 32) | (uint32_t)~v;
-}
+__device__ __forceinline__ float weight_of(u64 total) { return __fmul_rn(__ull2float_rn(total), 0x1p-40f); }
 
 __device__ __forceinline__ u64 warp_sum(u64 x)
 {
@@ -77,37 +89,88 @@ __device__ __forceinline__ u64 warp_sum(u64 x)
     return x;
 }
 
-template <bool kF32>
-__device__ __forceinline__ float logit(const void *row, int64_t v)
+__device__ __forceinline__ float warp_max(float x)
 {
-    return kF32 ? __ldg(static_cast<const float *>(row) + v)
-                : bf16_f32(__ldg(static_cast<const unsigned short *>(row) + v));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
 }
 
+// A row of logits as 16-byte pieces on their own boundaries: piece v holds
+// tokens v kPer - shift .. ; the ends are read token by token.
+template <bool kF32>
+struct Row {
+    static constexpr int kPer = kF32 ? 4 : 8;
+    const void *base;                          // of piece 0, where the row's first token may lie `shift` tokens in
+    int shift, vocab;
+    __device__ Row(const void *logits, int64_t at, int n)
+    {
+        const char *p = static_cast<const char *>(logits) + at * (kF32 ? 4 : 2);
+        shift = (int)(reinterpret_cast<uintptr_t>(p) & 15) / (kF32 ? 4 : 2);
+        base = p - shift * (kF32 ? 4 : 2);
+        vocab = n;
+    }
+    __device__ __forceinline__ float token(int v) const
+    {
+        return kF32 ? __ldg(static_cast<const float *>(base) + shift + v)
+                    : bf16_f32(__ldg(static_cast<const unsigned short *>(base) + shift + v));
+    }
+    __device__ __forceinline__ uint4 piece(int v) const
+    {
+        const int t0 = v * kPer - shift;
+        if (t0 >= 0 && t0 + kPer <= vocab) return __ldg(static_cast<const uint4 *>(base) + v);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (kF32) {
+                w[i] = t0 + i >= 0 && t0 + i < vocab ? __float_as_uint(token(t0 + i)) : 0xFF800000u;   // -inf
+            } else {
+                const int a = t0 + 2 * i, b = a + 1;
+                const uint32_t lo = a >= 0 && a < vocab ? __float_as_uint(token(a)) >> 16 : 0xFF80u;
+                const uint32_t hi = b >= 0 && b < vocab ? __float_as_uint(token(b)) >> 16 : 0xFF80u;
+                w[i] = lo | (hi << 16);
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ static float get(const uint4 &x, int i)
+    {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        if (kF32) return __uint_as_float(w[i]);
+        return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+    }
+};
+
 struct Shared {
-    u64 key[kMaxCluster];                      // written by every CTA of the cluster
+    float top[kMaxCluster];                    // written by every CTA of the cluster
+    int32_t first[kMaxCluster];
     u64 total[2][kMaxCluster];
-    u64 wkey[kWarps], wsum[kWarps];
+    float wtop[kWarps];
+    u64 wsum[kWarps];
     int32_t kids[kMaxBudget];
+    float inv[kMaxBudget];                     // of the rounds that changed the weights
     int32_t n_kids;
 };
 
-template <bool kF32>
-__global__ void __launch_bounds__(kThreads) k_sample_rows(const SampleParams p)
+// kHold: pieces of a thread that stay in registers from the maximum to the
+// sums (any more are read twice).  kDraft: with the drafter's probabilities.
+template <bool kF32, bool kDraft>
+__global__ void __launch_bounds__(kThreads, 2) k_sample_rows(const SampleParams p)
 {
-    extern __shared__ __align__(16) float w[];  // the slice's weights
+    constexpr int kPer = Row<kF32>::kPer, kHold = kF32 ? 10 : 5;
+    extern __shared__ __align__(16) float w[];  // kDraft: the slice's weights
     __shared__ Shared s;
     cg::cluster_group cl = cg::this_cluster();
     cl.barrier_arrive();                        // waited for before the first write to another CTA
+    pdl_launch_dependents();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int row = blockIdx.x / C;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int v0 = rank * p.slice;
-    const int n = max(0, min(p.slice, p.vocab - v0));
-    const int lo = min(n, warp * p.sub), hi = min(n, lo + p.sub);   // this warp's weights, in order
-    const void *zr = kF32 ? static_cast<const void *>(static_cast<const float *>(p.logits) + row * p.stride)
-                          : static_cast<const void *>(static_cast<const uint16_t *>(p.logits) + row * p.stride);
-    const float *qr = p.draft_p ? p.draft_p + row * p.draft_stride : nullptr;
+    const Row<kF32> z(p.logits, row * p.stride, p.vocab);
+    const int pieces = (z.shift + p.vocab + kPer - 1) / kPer;
+    const int first = rank * kWarps * p.sub;    // this CTA's first piece
+    const int lo = min(pieces, first + warp * p.sub), hi = min(pieces, lo + p.sub);   // this warp's pieces, in order
+    const float *qr = kDraft ? p.draft_p + row * p.draft_stride : nullptr;
     const int r = p.req[row];
     const bool row_ok = r >= 0 && r < p.n_req;
     if (!row_ok && tid == 0 && rank == 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
@@ -115,24 +178,26 @@ __global__ void __launch_bounds__(kThreads) k_sample_rows(const SampleParams p)
     const bool greedy = !(temp > 0.f);
     const float inv_t = greedy ? 1.f : __fdiv_rn(1.f, temp);
 
-    // ---- z = logit / T and its maximum (lowest index on ties; NaN counts as -inf)
-    u64 key = 0;
-    for (int i = lo + lane; i < hi; i += 32) {
-        float z = logit<kF32>(zr, v0 + i);
-        if (z != z) z = -INFINITY;
-        if (!greedy) z = __fmul_rn(z, inv_t);
-        w[i] = z;
-        const u64 k = max_key(z, v0 + i);
-        key = k > key ? k : key;
-    }
+    // ---- the maximum of z = logit / T (a NaN counts as -inf)
+    uint4 held[kHold];
+    float m = -INFINITY;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const u64 o = __shfl_xor_sync(0xffffffffu, key, d);
-        key = o > key ? o : key;
+    for (int k = 0; k < kHold; ++k)
+        if (lo + k * 32 + lane < hi) held[k] = z.piece(lo + k * 32 + lane);
+#pragma unroll
+    for (int k = 0; k < kHold; ++k)
+        if (lo + k * 32 + lane < hi)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) m = fmaxf(m, Row<kF32>::get(held[k], i));
+    for (int v = lo + kHold * 32 + lane; v < hi; v += 32) {
+        const uint4 x = z.piece(v);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) m = fmaxf(m, Row<kF32>::get(x, i));
     }
-    if (lane == 0) s.wkey[warp] = key;
+    m = warp_max(greedy ? m : __fmul_rn(m, inv_t));      // (scaling by a positive number keeps the order)
+    if (lane == 0) s.wtop[warp] = m;
     // children of the row, in row order
-    if (warp == 0 && qr) {
+    if (kDraft && warp == 0) {
         int cnt = 0;
         const int end = row_ok ? min(p.R, p.off[r + 1]) : 0;
         for (int j0 = row + 1; j0 < end; j0 += 32) {
@@ -146,20 +211,12 @@ __global__ void __launch_bounds__(kThreads) k_sample_rows(const SampleParams p)
     __syncthreads();
     cl.barrier_wait();
     if (warp == 0) {
-        key = lane < kWarps ? s.wkey[lane] : 0;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const u64 o = __shfl_xor_sync(0xffffffffu, key, d);
-            key = o > key ? o : key;
-        }
-        if (lane < C) cl.map_shared_rank(s.key, lane)[rank] = key;
+        m = warp_max(lane < kWarps ? s.wtop[lane] : -INFINITY);
+        if (lane < C) cl.map_shared_rank(s.top, lane)[rank] = m;
     }
     cl.sync();
-    key = s.key[0];
-    for (int c = 1; c < C; ++c) key = s.key[c] > key ? s.key[c] : key;
-    const uint32_t ob = (uint32_t)(key >> 32);
-    const float m = __uint_as_float(ob & 0x80000000u ? ob & 0x7FFFFFFFu : ~ob);
-    const int top = (int)~(uint32_t)key;
+    m = s.top[0];
+    for (int c = 1; c < C; ++c) m = fmaxf(m, s.top[c]);
     if (!(m > -INFINITY) || !row_ok) {          // nothing can be drawn from this row
         if (rank == 0 && tid == 0) {
             p.row_tok[row] = -1;
@@ -169,14 +226,50 @@ __global__ void __launch_bounds__(kThreads) k_sample_rows(const SampleParams p)
     }
 
     // ---- weights exp(z - m) and their sums
-    u64 sum = 0;
-    for (int i = lo + lane; i < hi; i += 32) {
-        const float z = w[i];
-        float e = z == m ? 1.f : expf(__fsub_rn(z, m));
-        if (greedy) e = v0 + i == top ? 1.f : 0.f;
-        w[i] = e;
-        sum += fixed40(e);
+    int top = -1;
+    if (greedy) {                               // all of it on the largest logit, the lowest token of equals
+        top = p.vocab;
+        for (int v = lo + lane; v < hi; v += 32) {
+            const uint4 x = z.piece(v);
+#pragma unroll
+            for (int i = kPer - 1; i >= 0; --i)
+                if (Row<kF32>::get(x, i) == m) top = min(top, v * kPer - z.shift + i);
+        }
+        top = __reduce_min_sync(0xffffffffu, top);
+        if (lane == 0) s.wtop[warp] = __int_as_float(top);
+        __syncthreads();
+        if (warp == 0) {
+            top = __reduce_min_sync(0xffffffffu, lane < kWarps ? __float_as_int(s.wtop[lane]) : p.vocab);
+            if (lane < C) cl.map_shared_rank(s.first, lane)[rank] = top;
+        }
+        cl.sync();
+        top = s.first[0];
+        for (int c = 1; c < C; ++c) top = min(top, s.first[c]);
     }
+    const bool flat = greedy || m == INFINITY;
+    auto weight = [&](float x, int tok) -> float {
+        if (flat) return greedy ? (tok == top ? 1.f : 0.f) : (x == INFINITY ? 1.f : 0.f);
+        // fmaxf also turns a NaN into a weight of nothing
+        return expf(fmaxf(__fsub_rn(__fmul_rn(x, inv_t), m), -128.f));
+    };
+    // a piece's weights: to shared memory (kDraft), and summed
+    auto weigh = [&](const uint4 &x, int v, Sum40 &sum) {
+        float e[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            e[i] = weight(Row<kF32>::get(x, i), v * kPer - z.shift + i);
+            sum.add(e[i]);
+        }
+        if (kDraft)
+#pragma unroll
+            for (int i = 0; i < kPer; i += 4)
+                *reinterpret_cast<float4 *>(w + (v - first) * kPer + i) = make_float4(e[i], e[i + 1], e[i + 2], e[i + 3]);
+    };
+    Sum40 sum;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k)
+        if (lo + k * 32 + lane < hi) weigh(held[k], lo + k * 32 + lane, sum);
+    for (int v = lo + kHold * 32 + lane; v < hi; v += 32) weigh(z.piece(v), v, sum);
     int buf = 0;
     // sums over warps, CTA and cluster; the CTA's weights are complete after it
     auto totals = [&](u64 x) -> u64 {
@@ -192,36 +285,53 @@ __global__ void __launch_bounds__(kThreads) k_sample_rows(const SampleParams p)
         for (int c = 0; c < C; ++c) t += s.total[buf][c];
         return t;
     };
-    u64 total = totals(sum);
-    const float first = weight_of(total);
-    int took = -1;
-    if (qr) {
-        const int n_kids = s.n_kids;
+    u64 total = totals(sum.get());
+    const float mass = weight_of(total);
+    int took = -1, rounds = 0;
+    // what a weight becomes where a child is rejected; element i of the warp's stretch is token t0 + i
+    const int t0 = lo * kPer - z.shift, n = (hi - lo) * kPer;
+    float *wl = w + (lo - first) * kPer;
+    if (kDraft) {
+        auto residual = [&](float a, float inv, int tok) -> float {
+            return tok >= 0 && tok < p.vocab ? fmaxf(__fsub_rn(__fmul_rn(a, inv), __ldg(qr + tok)), 0.f) : 0.f;
+        };
+        const int n_kids = s.n_kids, per_cta = kWarps * p.sub * kPer;
         for (int c = 0; c < n_kids; ++c) {
             const int kid = s.kids[c], x = p.token[kid];
             if (x < 0 || x >= p.vocab) continue;                   // not a token: it cannot be accepted
-            const int owner = x / p.slice;
-            const float ax = cl.map_shared_rank(w, owner)[x - owner * p.slice];
+            const int owner = (x + z.shift) / per_cta;
+            const float ax = cl.map_shared_rank(w, owner)[x + z.shift - owner * per_cta];
             const float inv = __fdiv_rn(1.f, weight_of(total));
             if (__fmul_rn(p.u_accept[kid], __ldg(qr + x)) < __fmul_rn(ax, inv)) {
                 took = kid;
                 break;
             }
-            u64 left = 0;
-            for (int i = lo + lane; i < hi; i += 32)
-                left += fixed40(fmaxf(__fsub_rn(__fmul_rn(w[i], inv), __ldg(qr + v0 + i)), 0.f));
+            cl.sync();                                              // every CTA has read ax
+            Sum40 rest;
+            for (int i = lane; i < n; i += 32) {
+                const float a = residual(wl[i], inv, t0 + i);
+                wl[i] = a;
+                rest.add(a);
+            }
             const u64 keep = s.wsum[warp];
             buf ^= 1;
-            left = totals(left);
-            if (left == 0) {                                        // p = q: p stays (and so do its sums)
-                if (lane == 0) s.wsum[warp] = keep;
-                buf ^= 1;
-                cl.sync();                                          // every CTA has read the sums it leaves
+            const u64 left = totals(rest.get());
+            if (left) {
+                total = left;
+                if (tid == 0) s.inv[rounds] = inv;
+                ++rounds;
                 continue;
             }
-            total = left;
-            for (int i = lo + lane; i < hi; i += 32)
-                w[i] = fmaxf(__fsub_rn(__fmul_rn(w[i], inv), __ldg(qr + v0 + i)), 0.f);
+            // p = q: p stays, and so do its sums; the weights are made again
+            if (lane == 0) s.wsum[warp] = keep;
+            buf ^= 1;
+            __syncthreads();
+            for (int i = lane; i < n; i += 32) {
+                const int tok = t0 + i;
+                float a = tok >= 0 && tok < p.vocab ? weight(z.token(tok), tok) : 0.f;
+                for (int k = 0; k < rounds; ++k) a = residual(a, s.inv[k], tok);
+                wl[i] = a;
+            }
             cl.sync();
         }
     }
@@ -240,9 +350,18 @@ __global__ void __launch_bounds__(kThreads) k_sample_rows(const SampleParams p)
             int wi = 0;
             while (wi < kWarps - 1 && t >= s.wsum[wi]) t -= s.wsum[wi++];
             if (warp == wi) {
-                for (int i0 = lo; i0 < hi; i0 += 32) {
-                    const int i = i0 + lane;
-                    const u64 x = i < hi ? fixed40(w[i]) : 0ull;
+                for (int v0 = lo; v0 < hi; v0 += 32) {
+                    const int v = v0 + lane;
+                    float e[kPer];
+                    u64 x = 0;
+                    if (v < hi) {
+                        const uint4 y = kDraft ? make_uint4(0, 0, 0, 0) : z.piece(v);
+#pragma unroll
+                        for (int i = 0; i < kPer; ++i) {
+                            e[i] = kDraft ? w[(v - first) * kPer + i] : weight(Row<kF32>::get(y, i), v * kPer - z.shift + i);
+                            x += fixed40(e[i]);
+                        }
+                    }
                     u64 incl = x;
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) {
@@ -251,7 +370,16 @@ __global__ void __launch_bounds__(kThreads) k_sample_rows(const SampleParams p)
                     }
                     const unsigned b = __ballot_sync(0xffffffffu, incl > t);
                     if (b) {
-                        if (lane == __ffs(b) - 1) tok = v0 + i;
+                        if (lane == __ffs(b) - 1) {
+                            u64 c = incl - x;
+                            int i = 0;
+#pragma unroll
+                            for (int k = 0; k < kPer - 1; ++k) {
+                                c += fixed40(e[k]);
+                                if (c <= t) i = k + 1;
+                            }
+                            tok = v * kPer - z.shift + i;
+                        }
                         break;
                     }
                     t -= __shfl_sync(0xffffffffu, incl, 31);
@@ -262,14 +390,12 @@ __global__ void __launch_bounds__(kThreads) k_sample_rows(const SampleParams p)
     if (tok >= 0) {
         p.row_tok[row] = tok;
         if (p.row_logp) {
-            float z = logit<kF32>(zr, tok);
-            if (z != z) z = -INFINITY;
-            z = greedy ? (tok == top ? 0.f : -INFINITY) : __fmul_rn(z, inv_t);
-            p.row_logp[row] = z == m || greedy ? (greedy ? z : __fsub_rn(0.f, logf(first)))
-                                               : __fsub_rn(__fsub_rn(z, m), logf(first));
+            // (a NaN can only be an accepted child's)
+            const float x = __fmul_rn(fmaxf(z.token(tok), -INFINITY), inv_t);
+            p.row_logp[row] = greedy ? (tok == top ? 0.f : -INFINITY) : __fsub_rn(x == m ? 0.f : __fsub_rn(x, m), logf(mass));
         }
     }
-    cl.sync();                                  // no CTA leaves while another may read its weights
+    if (kDraft) cl.sync();                       // no CTA leaves while another may read its weights
 }
 
 // The accepted path: from the root to the child that carries the row's token,
@@ -341,27 +467,31 @@ int launch_sample(const SampleArgs &a, void *stream)
     p.row_tok = a.row_tok;
     p.row_logp = a.row_logp;
     p.status = a.status;
-    // as many CTAs to a row as leave each of them 2048 weights
+    // as many CTAs to a row as leave each of them 2048 tokens
     int c = 1;
     while (c < kMaxCluster && a.vocab > 2048 * c) c *= 2;
-    p.sub = (int32_t)((a.vocab + (int64_t)c * kWarps - 1) / ((int64_t)c * kWarps) + 31) / 32 * 32;
-    p.slice = p.sub * kWarps;
-    const size_t smem = (size_t)p.slice * 4;
-    const void *f = a.f32 ? (const void *)k_sample_rows<true> : (const void *)k_sample_rows<false>;
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return (int)e;
+    const int per = a.f32 ? 4 : 8;
+    const int64_t pieces = (a.vocab + per - 1) / per + 1;         // one more where the row starts inside a piece
+    p.sub = (int32_t)((pieces + (int64_t)c * kWarps - 1) / ((int64_t)c * kWarps));
+    const size_t smem = a.draft_p ? (size_t)p.sub * kWarps * per * 4 : 0;
+    cudaError_t e = cudaSuccess;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.R * c));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)c;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = a.f32 ? cudaLaunchKernelEx(&cfg, k_sample_rows<true>, p) : cudaLaunchKernelEx(&cfg, k_sample_rows<false>, p);
+    auto go = [&](auto kernel) {
+        if (smem) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, p);
+    };
+    if (a.f32) a.draft_p ? go(k_sample_rows<true, true>) : go(k_sample_rows<true, false>);
+    else a.draft_p ? go(k_sample_rows<false, true>) : go(k_sample_rows<false, false>);
     if (e != cudaSuccess || !a.acc_tok) return (int)e;
     cudaLaunchConfig_t cf{};
     cf.gridDim = dim3((unsigned)((a.n_req + 3) / 4));
