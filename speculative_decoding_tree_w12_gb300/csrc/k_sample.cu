@@ -16,9 +16,11 @@
 // are never drawn.)
 //
 // A cluster of CTAs shares a row; maxima and sums cross it through distributed
-// shared memory.  The logits are read from memory once, 16 bytes at a time, and
-// wait in registers for the maximum; only a drafter's probabilities, which
-// change the weights round by round, make the weights go to shared memory.
+// shared memory.  The logits are read 16 bytes at a time, from memory for the
+// maximum and from the L1 cache for the sums (a CTA's stretch is small; held in
+// registers it cost half of the warps, and with them the latency of the three
+// cluster barriers); only a drafter's probabilities, which change the weights
+// round by round, make the weights go to shared memory.
 // The token is found by the sums alone down to one warp's stretch of the row,
 // which that warp reads again in order.
 #include <cooperative_groups.h>
@@ -58,8 +60,56 @@ struct SampleParams {
 // again the exact rest; 2^-17 splits that the same way.  Both parts are summed
 // as the bits they come in; what the added constants put there is taken off at
 // the end (modulo 2^32: a thread's own sums stay under 2^32).
+// Two at a time where the machine adds two at a time.
+__device__ __forceinline__ u64 pair(float a, float b)
+{
+    u64 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float2 unpair(u64 d)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(d));
+    return f;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b)
+{
+    u64 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ u64 add2_rz(u64 a, u64 b)
+{
+    u64 d;
+    asm("add.rz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b)
+{
+    u64 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c)
+{
+    u64 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 struct Sum40 {
     uint32_t hi = 0, lo = 0, n = 0;
+    __device__ __forceinline__ void add(u64 e)
+    {
+        const u64 t = add2_rz(e, pair(8.f, 8.f));
+        const float2 a = unpair(t);
+        hi += __float_as_uint(a.x) + __float_as_uint(a.y);
+        const u64 rest = fma2(add2(t, pair(-8.f, -8.f)), pair(-1.f, -1.f), e);
+        const float2 b = unpair(add2_rz(rest, pair(0x1p-17f, 0x1p-17f)));
+        lo += __float_as_uint(b.x) + __float_as_uint(b.y);
+        n += 2;
+    }
     __device__ __forceinline__ void add(float e)
     {
         const float t = __fadd_rz(e, 8.f);
@@ -152,12 +202,11 @@ struct Shared {
     int32_t n_kids;
 };
 
-// kHold: pieces of a thread that stay in registers from the maximum to the
-// sums (any more are read twice).  kDraft: with the drafter's probabilities.
+// kDraft: with the drafter's probabilities.
 template <bool kF32, bool kDraft>
-__global__ void __launch_bounds__(kThreads, 2) k_sample_rows(const SampleParams p)
+__global__ void __launch_bounds__(kThreads, kDraft ? 2 : 4) k_sample_rows(const SampleParams p)
 {
-    constexpr int kPer = Row<kF32>::kPer, kHold = kF32 ? 10 : 5;
+    constexpr int kPer = Row<kF32>::kPer;
     extern __shared__ __align__(16) float w[];  // kDraft: the slice's weights
     __shared__ Shared s;
     cg::cluster_group cl = cg::this_cluster();
@@ -179,17 +228,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_rows(const SampleParams 
     const float inv_t = greedy ? 1.f : __fdiv_rn(1.f, temp);
 
     // ---- the maximum of z = logit / T (a NaN counts as -inf)
-    uint4 held[kHold];
     float m = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kHold; ++k)
-        if (lo + k * 32 + lane < hi) held[k] = z.piece(lo + k * 32 + lane);
-#pragma unroll
-    for (int k = 0; k < kHold; ++k)
-        if (lo + k * 32 + lane < hi)
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) m = fmaxf(m, Row<kF32>::get(held[k], i));
-    for (int v = lo + kHold * 32 + lane; v < hi; v += 32) {
+#pragma unroll 4
+    for (int v = lo + lane; v < hi; v += 32) {
         const uint4 x = z.piece(v);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) m = fmaxf(m, Row<kF32>::get(x, i));
@@ -253,23 +294,43 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_rows(const SampleParams 
         return expf(fmaxf(__fsub_rn(__fmul_rn(x, inv_t), m), -128.f));
     };
     // a piece's weights: to shared memory (kDraft), and summed
-    auto weigh = [&](const uint4 &x, int v, Sum40 &sum) {
-        float e[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            e[i] = weight(Row<kF32>::get(x, i), v * kPer - z.shift + i);
-            sum.add(e[i]);
-        }
-        if (kDraft)
-#pragma unroll
-            for (int i = 0; i < kPer; i += 4)
-                *reinterpret_cast<float4 *>(w + (v - first) * kPer + i) = make_float4(e[i], e[i + 1], e[i + 2], e[i + 3]);
-    };
     Sum40 sum;
+    auto keep4 = [&](int v, int i, float a, float b, float c, float d) {
+        if (kDraft) *reinterpret_cast<float4 *>(w + (v - first) * kPer + i) = make_float4(a, b, c, d);
+    };
+    if (flat) {
+#pragma unroll 1
+        for (int v = lo + lane; v < hi; v += 32) {
+            const uint4 x = z.piece(v);
 #pragma unroll
-    for (int k = 0; k < kHold; ++k)
-        if (lo + k * 32 + lane < hi) weigh(held[k], lo + k * 32 + lane, sum);
-    for (int v = lo + kHold * 32 + lane; v < hi; v += 32) weigh(z.piece(v), v, sum);
+            for (int i = 0; i < kPer; i += 4) {
+                float e[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) e[k] = weight(Row<kF32>::get(x, i + k), v * kPer - z.shift + i + k);
+                sum.add(pair(e[0], e[1]));
+                sum.add(pair(e[2], e[3]));
+                keep4(v, i, e[0], e[1], e[2], e[3]);
+            }
+        }
+    } else {
+        const u64 inv2 = pair(inv_t, inv_t), neg2 = pair(-m, -m);
+        auto two = [&](const uint4 &x, int i) -> u64 {             // the weights of tokens i and i + 1 of a piece
+            const float2 d = unpair(add2(mul2(pair(Row<kF32>::get(x, i), Row<kF32>::get(x, i + 1)), inv2), neg2));
+            return pair(expf(fmaxf(d.x, -128.f)), expf(fmaxf(d.y, -128.f)));   // (a NaN becomes a weight of nothing)
+        };
+#pragma unroll 2
+        for (int v = lo + lane; v < hi; v += 32) {
+            const uint4 x = z.piece(v);
+#pragma unroll
+            for (int i = 0; i < kPer; i += 4) {
+                const u64 a = two(x, i), b = two(x, i + 2);
+                sum.add(a);
+                sum.add(b);
+                const float2 e = unpair(a), f = unpair(b);
+                keep4(v, i, e.x, e.y, f.x, f.y);
+            }
+        }
+    }
     int buf = 0;
     // sums over warps, CTA and cluster; the CTA's weights are complete after it
     auto totals = [&](u64 x) -> u64 {
