@@ -16,17 +16,20 @@
 // are never drawn.)
 //
 // A cluster of CTAs shares a row; maxima and sums cross it through distributed
-// shared memory.  The logits are read 16 bytes at a time, from memory for the
-// maximum and from the L1 cache for the sums (a CTA's stretch is small; held in
-// registers it cost half of the warps, and with them the latency of the three
-// cluster barriers); only a drafter's probabilities, which change the weights
-// round by round, make the weights go to shared memory.
-// The token is found by the sums alone down to one warp's stretch of the row,
-// which that warp reads again in order.
+// shared memory.  Weights are never stored: a pass makes them from the logits
+// (16 bytes at a time; from L2 after the first pass, or from registers where
+// few rows leave room), so a row costs one read of the logits from memory, one
+// more pass for the sums, and one with the drafter's probabilities only where a
+// child is rejected.  The token is found by the sums alone down to one warp's
+// stretch of the row, which that warp goes through again in order.  What bounds
+// many rows is the issue rate of the sums' pass, some 16 instructions a token,
+// half of them expf.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "w12_device.cuh"
 #include "w12_kv.cuh"
@@ -41,7 +44,6 @@ typedef unsigned long long u64;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxSlice = 49152;               // weights of one CTA: 192 KB
 
 struct SampleParams {
     const void *logits;
@@ -139,11 +141,18 @@ __device__ __forceinline__ u64 warp_sum(u64 x)
     return x;
 }
 
-__device__ __forceinline__ float warp_max(float x)
+// the larger, or NaN
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-    return x;
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // A row of logits as 16-byte pieces on their own boundaries: piece v holds
@@ -196,18 +205,18 @@ struct Shared {
     int32_t first[kMaxCluster];
     u64 total[2][kMaxCluster];
     float wtop[kWarps];
-    u64 wsum[kWarps];
+    u64 wsum[2][kWarps];
     int32_t kids[kMaxBudget];
-    float inv[kMaxBudget];                     // of the rounds that changed the weights
+    float inv[kMaxBudget];                     // of the rejections so far
     int32_t n_kids;
 };
 
-// kDraft: with the drafter's probabilities.
-template <bool kF32, bool kDraft>
-__global__ void __launch_bounds__(kThreads, kDraft ? 2 : 4) k_sample_rows(const SampleParams p)
+// kDraft: with the drafter's probabilities.  kHold: a thread's first kHeld
+// pieces stay in registers from the maximum to the sums.
+template <bool kF32, bool kDraft, bool kHold>
+__global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample_rows(const SampleParams p)
 {
-    constexpr int kPer = Row<kF32>::kPer;
-    extern __shared__ __align__(16) float w[];  // kDraft: the slice's weights
+    constexpr int kPer = Row<kF32>::kPer, kHeld = kHold ? (kF32 ? 10 : 5) : 0;
     __shared__ Shared s;
     cg::cluster_group cl = cg::this_cluster();
     cl.barrier_arrive();                        // waited for before the first write to another CTA
@@ -217,8 +226,7 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 4) k_sample_rows(const 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Row<kF32> z(p.logits, row * p.stride, p.vocab);
     const int pieces = (z.shift + p.vocab + kPer - 1) / kPer;
-    const int first = rank * kWarps * p.sub;    // this CTA's first piece
-    const int lo = min(pieces, first + warp * p.sub), hi = min(pieces, lo + p.sub);   // this warp's pieces, in order
+    const int lo = min(pieces, (rank * kWarps + warp) * p.sub), hi = min(pieces, lo + p.sub);   // this warp's pieces, in order
     const float *qr = kDraft ? p.draft_p + row * p.draft_stride : nullptr;
     const int r = p.req[row];
     const bool row_ok = r >= 0 && r < p.n_req;
@@ -227,16 +235,23 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 4) k_sample_rows(const 
     const bool greedy = !(temp > 0.f);
     const float inv_t = greedy ? 1.f : __fdiv_rn(1.f, temp);
 
-    // ---- the maximum of z = logit / T (a NaN counts as -inf)
+    // ---- the largest logit, and whether there is a NaN
+    uint4 held[kHold ? kHeld : 1];
     float m = -INFINITY;
-#pragma unroll 4
-    for (int v = lo + lane; v < hi; v += 32) {
-        const uint4 x = z.piece(v);
+    auto larger = [&](const uint4 &x) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) m = fmaxf(m, Row<kF32>::get(x, i));
+        for (int i = 0; i < kPer; i += 2) m = max_nan(m, Row<kF32>::get(x, i), Row<kF32>::get(x, i + 1));
+    };
+    if (kHold) {
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+            if (lo + k * 32 + lane < hi) held[k] = z.piece(lo + k * 32 + lane);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+            if (lo + k * 32 + lane < hi) larger(held[k]);
     }
-    m = warp_max(greedy ? m : __fmul_rn(m, inv_t));      // (scaling by a positive number keeps the order)
-    if (lane == 0) s.wtop[warp] = m;
+#pragma unroll 4
+    for (int v = lo + kHeld * 32 + lane; v < hi; v += 32) larger(z.piece(v));
     // children of the row, in row order
     if (kDraft && warp == 0) {
         int cnt = 0;
@@ -249,15 +264,38 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 4) k_sample_rows(const 
         }
         if (lane == 0) s.n_kids = cnt;
     }
-    __syncthreads();
-    cl.barrier_wait();
-    if (warp == 0) {
-        m = warp_max(lane < kWarps ? s.wtop[lane] : -INFINITY);
-        if (lane < C) cl.map_shared_rank(s.top, lane)[rank] = m;
+    bool started = false;
+    auto cluster_max = [&]() {                  // of m, over the cluster
+#pragma unroll
+        for (int d = 16; d; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if (lane == 0) s.wtop[warp] = m;
+        __syncthreads();
+        if (!started) cl.barrier_wait();
+        started = true;
+        if (warp == 0) {
+            m = s.wtop[lane & (kWarps - 1)];
+#pragma unroll
+            for (int d = kWarps / 2; d; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+            if (lane < C) cl.map_shared_rank(s.top, lane)[rank] = m;
+        }
+        cl.sync();
+        m = s.top[0];
+        for (int c = 1; c < C; ++c) m = max_nan(m, s.top[c]);
+    };
+    cluster_max();
+    // NaN counts as -inf; rows that have one, or +inf, take the careful way from here on
+    bool careful = m == INFINITY;
+    if (m != m) {
+        careful = true;
+        m = -INFINITY;
+        for (int v = lo + lane; v < hi; v += 32) {
+            const uint4 x = z.piece(v);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) m = fmaxf(m, Row<kF32>::get(x, i));
+        }
+        cl.sync();                              // every CTA has read the last maxima
+        cluster_max();
     }
-    cl.sync();
-    m = s.top[0];
-    for (int c = 1; c < C; ++c) m = fmaxf(m, s.top[c]);
     if (!(m > -INFINITY) || !row_ok) {          // nothing can be drawn from this row
         if (rank == 0 && tid == 0) {
             p.row_tok[row] = -1;
@@ -265,11 +303,8 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 4) k_sample_rows(const 
         }
         return;                                 // uniform over the cluster, and nobody reads another's memory any more
     }
-
-    // ---- weights exp(z - m) and their sums
-    int top = -1;
-    if (greedy) {                               // all of it on the largest logit, the lowest token of equals
-        top = p.vocab;
+    if (greedy) {                               // the largest logit, the lowest token of equals, whatever the draft
+        int top = p.vocab;
         for (int v = lo + lane; v < hi; v += 32) {
             const uint4 x = z.piece(v);
 #pragma unroll
@@ -280,65 +315,80 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 4) k_sample_rows(const 
         if (lane == 0) s.wtop[warp] = __int_as_float(top);
         __syncthreads();
         if (warp == 0) {
-            top = __reduce_min_sync(0xffffffffu, lane < kWarps ? __float_as_int(s.wtop[lane]) : p.vocab);
-            if (lane < C) cl.map_shared_rank(s.first, lane)[rank] = top;
+            top = __reduce_min_sync(0xffffffffu, __float_as_int(s.wtop[lane & (kWarps - 1)]));
+            if (lane == 0) cl.map_shared_rank(s.first, 0)[rank] = top;
         }
         cl.sync();
-        top = s.first[0];
-        for (int c = 1; c < C; ++c) top = min(top, s.first[c]);
+        if (rank == 0 && tid == 0) {
+            for (int c = 0; c < C; ++c) top = min(top, s.first[c]);
+            p.row_tok[row] = top;
+            if (p.row_logp) p.row_logp[row] = 0.f;
+        }
+        return;
     }
-    const bool flat = greedy || m == INFINITY;
-    auto weight = [&](float x, int tok) -> float {
-        if (flat) return greedy ? (tok == top ? 1.f : 0.f) : (x == INFINITY ? 1.f : 0.f);
-        // fmaxf also turns a NaN into a weight of nothing
-        return expf(fmaxf(__fsub_rn(__fmul_rn(x, inv_t), m), -128.f));
+    m = __fmul_rn(m, inv_t);                    // of z = logit / T: scaling by a positive number keeps the order
+
+    // ---- weights exp(z - m)
+    auto one = [&](float x) -> float {
+        if (!careful) return expf(__fsub_rn(__fmul_rn(x, inv_t), m));
+        const float y = __fmul_rn(x, inv_t);
+        return y == m ? 1.f : y < m ? expf(__fsub_rn(y, m)) : 0.f;       // (a NaN is neither)
     };
-    // a piece's weights: to shared memory (kDraft), and summed
-    Sum40 sum;
-    auto keep4 = [&](int v, int i, float a, float b, float c, float d) {
-        if (kDraft) *reinterpret_cast<float4 *>(w + (v - first) * kPer + i) = make_float4(a, b, c, d);
+    const u64 inv2 = pair(inv_t, inv_t), neg2 = pair(-m, -m);
+    // the weights of tokens i and i + 1 of a piece
+    auto two = [&](const uint4 &x, int i) -> u64 {
+        const float a = Row<kF32>::get(x, i), b = Row<kF32>::get(x, i + 1);
+        if (careful) return pair(one(a), one(b));
+        const float2 d = unpair(add2(mul2(pair(a, b), inv2), neg2));
+        return pair(expf(d.x), expf(d.y));
     };
-    if (flat) {
-#pragma unroll 1
-        for (int v = lo + lane; v < hi; v += 32) {
-            const uint4 x = z.piece(v);
+    // what is left of a weight after the rejections so far
+    int rounds = 0;
+    auto rest = [&](float a, float q) -> float {
+        for (int k = 0; k < rounds; ++k) a = fmaxf(__fsub_rn(__fmul_rn(a, s.inv[k]), q), 0.f);
+        return a;
+    };
+    const bool q_even = kDraft && ((reinterpret_cast<uintptr_t>(qr) - 4 * z.shift) & 15) == 0;   // its pieces lie on 16 bytes too
+    // a piece's weights, in pairs
+    auto weights = [&](const uint4 &x, int v, u64 (&e)[kPer / 2]) {
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) e[i / 2] = two(x, i);
+        if (!kDraft || rounds == 0) return;
+        const int t0 = v * kPer - z.shift;
+        u64 q[kPer / 2];
+        if (q_even && t0 >= 0 && t0 + kPer <= p.vocab) {
 #pragma unroll
             for (int i = 0; i < kPer; i += 4) {
-                float e[4];
+                const float4 f = __ldg(reinterpret_cast<const float4 *>(qr + t0 + i));
+                q[i / 2] = pair(f.x, f.y);
+                q[i / 2 + 1] = pair(f.z, f.w);
+            }
+        } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) e[k] = weight(Row<kF32>::get(x, i + k), v * kPer - z.shift + i + k);
-                sum.add(pair(e[0], e[1]));
-                sum.add(pair(e[2], e[3]));
-                keep4(v, i, e[0], e[1], e[2], e[3]);
+            for (int i = 0; i < kPer; i += 2) {
+                float f[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) f[k] = t0 + i + k >= 0 && t0 + i + k < p.vocab ? __ldg(qr + t0 + i + k) : 2.f;
+                q[i / 2] = pair(f[0], f[1]);
             }
         }
-    } else {
-        const u64 inv2 = pair(inv_t, inv_t), neg2 = pair(-m, -m);
-        auto two = [&](const uint4 &x, int i) -> u64 {             // the weights of tokens i and i + 1 of a piece
-            const float2 d = unpair(add2(mul2(pair(Row<kF32>::get(x, i), Row<kF32>::get(x, i + 1)), inv2), neg2));
-            return pair(expf(fmaxf(d.x, -128.f)), expf(fmaxf(d.y, -128.f)));   // (a NaN becomes a weight of nothing)
-        };
-#pragma unroll 2
-        for (int v = lo + lane; v < hi; v += 32) {
-            const uint4 x = z.piece(v);
+        for (int k = 0; k < rounds; ++k) {
+            const u64 inv = pair(s.inv[k], s.inv[k]);
 #pragma unroll
-            for (int i = 0; i < kPer; i += 4) {
-                const u64 a = two(x, i), b = two(x, i + 2);
-                sum.add(a);
-                sum.add(b);
-                const float2 e = unpair(a), f = unpair(b);
-                keep4(v, i, e.x, e.y, f.x, f.y);
+            for (int i = 0; i < kPer / 2; ++i) {
+                const float2 a = unpair(fma2(q[i], pair(-1.f, -1.f), mul2(e[i], inv)));
+                e[i] = pair(fmaxf(a.x, 0.f), fmaxf(a.y, 0.f));
             }
         }
-    }
+    };
     int buf = 0;
-    // sums over warps, CTA and cluster; the CTA's weights are complete after it
+    // sums over warps, CTA and cluster
     auto totals = [&](u64 x) -> u64 {
         x = warp_sum(x);
-        if (lane == 0) s.wsum[warp] = x;
+        if (lane == 0) s.wsum[buf][warp] = x;
         __syncthreads();
         if (warp == 0) {
-            const u64 t = warp_sum(lane < kWarps ? s.wsum[lane] : 0ull);
+            const u64 t = warp_sum(lane < kWarps ? s.wsum[buf][lane] : 0ull);
             if (lane < C) cl.map_shared_rank(s.total[buf], lane)[rank] = t;
         }
         cl.sync();
@@ -346,54 +396,52 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 4) k_sample_rows(const 
         for (int c = 0; c < C; ++c) t += s.total[buf][c];
         return t;
     };
+    Sum40 sum;
+    auto weigh = [&](const uint4 &x) {
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) sum.add(two(x, i));
+    };
+    if (kHold) {
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+            if (lo + k * 32 + lane < hi) weigh(held[k]);
+    }
+#pragma unroll 2
+    for (int v = lo + kHeld * 32 + lane; v < hi; v += 32) weigh(z.piece(v));
     u64 total = totals(sum.get());
     const float mass = weight_of(total);
-    int took = -1, rounds = 0;
-    // what a weight becomes where a child is rejected; element i of the warp's stretch is token t0 + i
-    const int t0 = lo * kPer - z.shift, n = (hi - lo) * kPer;
-    float *wl = w + (lo - first) * kPer;
+    int took = -1;
     if (kDraft) {
-        auto residual = [&](float a, float inv, int tok) -> float {
-            return tok >= 0 && tok < p.vocab ? fmaxf(__fsub_rn(__fmul_rn(a, inv), __ldg(qr + tok)), 0.f) : 0.f;
-        };
-        const int n_kids = s.n_kids, per_cta = kWarps * p.sub * kPer;
+        const int n_kids = s.n_kids;
         for (int c = 0; c < n_kids; ++c) {
             const int kid = s.kids[c], x = p.token[kid];
             if (x < 0 || x >= p.vocab) continue;                   // not a token: it cannot be accepted
-            const int owner = (x + z.shift) / per_cta;
-            const float ax = cl.map_shared_rank(w, owner)[x + z.shift - owner * per_cta];
-            const float inv = __fdiv_rn(1.f, weight_of(total));
-            if (__fmul_rn(p.u_accept[kid], __ldg(qr + x)) < __fmul_rn(ax, inv)) {
+            const float q = __ldg(qr + x), a = rest(one(z.token(x)), q), inv = __fdiv_rn(1.f, weight_of(total));
+            if (__fmul_rn(p.u_accept[kid], q) < __fmul_rn(a, inv)) {
                 took = kid;
                 break;
             }
-            cl.sync();                                              // every CTA has read ax
-            Sum40 rest;
-            for (int i = lane; i < n; i += 32) {
-                const float a = residual(wl[i], inv, t0 + i);
-                wl[i] = a;
-                rest.add(a);
-            }
-            const u64 keep = s.wsum[warp];
-            buf ^= 1;
-            const u64 left = totals(rest.get());
-            if (left) {
-                total = left;
-                if (tid == 0) s.inv[rounds] = inv;
-                ++rounds;
-                continue;
-            }
-            // p = q: p stays, and so do its sums; the weights are made again
-            if (lane == 0) s.wsum[warp] = keep;
-            buf ^= 1;
+            __syncthreads();                                        // (everyone is done with the last entry)
+            if (tid == 0) s.inv[rounds] = inv;
             __syncthreads();
-            for (int i = lane; i < n; i += 32) {
-                const int tok = t0 + i;
-                float a = tok >= 0 && tok < p.vocab ? weight(z.token(tok), tok) : 0.f;
-                for (int k = 0; k < rounds; ++k) a = residual(a, s.inv[k], tok);
-                wl[i] = a;
+            ++rounds;
+            Sum40 left;
+            for (int v = lo + lane; v < hi; v += 32) {
+                const uint4 y = z.piece(v);
+                u64 e[kPer / 2];
+                weights(y, v, e);
+#pragma unroll
+                for (int i = 0; i < kPer / 2; ++i) left.add(e[i]);
             }
-            cl.sync();
+            buf ^= 1;
+            const u64 t = totals(left.get());
+            if (t) {
+                total = t;
+            } else {                                                // p = q: p stays, and so do its sums
+                --rounds;
+                buf ^= 1;
+                cl.sync();                                          // every CTA has read the sums it leaves
+            }
         }
     }
     // ---- the row's token
@@ -409,20 +457,18 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 4) k_sample_rows(const 
         if (at >= before && at < before + mine) {
             u64 t = at - before;
             int wi = 0;
-            while (wi < kWarps - 1 && t >= s.wsum[wi]) t -= s.wsum[wi++];
+            while (wi < kWarps - 1 && t >= s.wsum[buf][wi]) t -= s.wsum[buf][wi++];
             if (warp == wi) {
                 for (int v0 = lo; v0 < hi; v0 += 32) {
-                    const int v = v0 + lane;
-                    float e[kPer];
-                    u64 x = 0;
+                    const int v = v0 + lane, t0 = v * kPer - z.shift;
+                    u64 e[kPer / 2];
+                    Sum40 piece;
                     if (v < hi) {
-                        const uint4 y = kDraft ? make_uint4(0, 0, 0, 0) : z.piece(v);
+                        weights(z.piece(v), v, e);
 #pragma unroll
-                        for (int i = 0; i < kPer; ++i) {
-                            e[i] = kDraft ? w[(v - first) * kPer + i] : weight(Row<kF32>::get(y, i), v * kPer - z.shift + i);
-                            x += fixed40(e[i]);
-                        }
+                        for (int i = 0; i < kPer / 2; ++i) piece.add(e[i]);
                     }
+                    const u64 x = piece.get();
                     u64 incl = x;
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) {
@@ -436,10 +482,11 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 4) k_sample_rows(const 
                             int i = 0;
 #pragma unroll
                             for (int k = 0; k < kPer - 1; ++k) {
-                                c += fixed40(e[k]);
+                                const float2 f = unpair(e[k / 2]);
+                                c += fixed40(k & 1 ? f.y : f.x);
                                 if (c <= t) i = k + 1;
                             }
-                            tok = v * kPer - z.shift + i;
+                            tok = t0 + i;
                         }
                         break;
                     }
@@ -453,10 +500,9 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 4) k_sample_rows(const 
         if (p.row_logp) {
             // (a NaN can only be an accepted child's)
             const float x = __fmul_rn(fmaxf(z.token(tok), -INFINITY), inv_t);
-            p.row_logp[row] = greedy ? (tok == top ? 0.f : -INFINITY) : __fsub_rn(x == m ? 0.f : __fsub_rn(x, m), logf(mass));
+            p.row_logp[row] = __fsub_rn(x == m ? 0.f : __fsub_rn(x, m), logf(mass));
         }
     }
-    if (kDraft) cl.sync();                       // no CTA leaves while another may read its weights
 }
 
 // The accepted path: from the root to the child that carries the row's token,
@@ -506,7 +552,8 @@ __global__ void __launch_bounds__(128) k_sample_path(const int32_t *parent, cons
 
 namespace w12i {
 
-int64_t sample_max_vocab() { return (int64_t)kMaxCluster * kMaxSlice; }
+// (a thread's own sums of whole numbers stay under 2^32 up to 4096 tokens of its own)
+int64_t sample_max_vocab() { return (int64_t)kThreads * 2048; }
 
 int launch_sample(const SampleArgs &a, void *stream)
 {
@@ -528,13 +575,22 @@ int launch_sample(const SampleArgs &a, void *stream)
     p.row_tok = a.row_tok;
     p.row_logp = a.row_logp;
     p.status = a.status;
-    // as many CTAs to a row as leave each of them 2048 tokens
+    // CTAs of a row: up to 8 of 2048 tokens or more each, so that the waves of
+    // them, each as long as its stretch and some 16384 tokens' worth of barriers,
+    // take least (192 rows of 151936 tokens: 43 us with 8 CTAs to a row, three
+    // waves, and 36 us with 3, one wave).  With no more than two to an SM, half
+    // the registers of an SM hold the row between its two passes.
+    const int64_t slots = (a.draft_p ? 3ll : 4ll) * a.num_sms;
     int c = 1;
-    while (c < kMaxCluster && a.vocab > 2048 * c) c *= 2;
+    int64_t best = INT64_MAX;
+    for (int i = 1; i <= kMaxCluster && (i == 1 || a.vocab > 2048 * (i - 1)); ++i) {
+        const int64_t t = ((int64_t)a.R * i + slots - 1) / slots * (a.vocab / i + 16384);
+        if (t < best) best = t, c = i;
+    }
+    const bool hold = (int64_t)a.R * c <= 2ll * a.num_sms;
     const int per = a.f32 ? 4 : 8;
     const int64_t pieces = (a.vocab + per - 1) / per + 1;         // one more where the row starts inside a piece
     p.sub = (int32_t)((pieces + (int64_t)c * kWarps - 1) / ((int64_t)c * kWarps));
-    const size_t smem = a.draft_p ? (size_t)p.sub * kWarps * per * 4 : 0;
     cudaError_t e = cudaSuccess;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -543,16 +599,16 @@ int launch_sample(const SampleArgs &a, void *stream)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.R * c));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto go = [&](auto kernel) {
-        if (smem) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, p);
+    auto go = [&](auto kernel) { e = cudaLaunchKernelEx(&cfg, kernel, p); };
+    auto pick = [&](auto f32, auto draft) {
+        if (hold) go(k_sample_rows<decltype(f32)::value, decltype(draft)::value, true>);
+        else go(k_sample_rows<decltype(f32)::value, decltype(draft)::value, false>);
     };
-    if (a.f32) a.draft_p ? go(k_sample_rows<true, true>) : go(k_sample_rows<true, false>);
-    else a.draft_p ? go(k_sample_rows<false, true>) : go(k_sample_rows<false, false>);
+    if (a.f32) a.draft_p ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
+    else a.draft_p ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});
     if (e != cudaSuccess || !a.acc_tok) return (int)e;
     cudaLaunchConfig_t cf{};
     cf.gridDim = dim3((unsigned)((a.n_req + 3) / 4));

@@ -963,6 +963,7 @@ w12_status sample_entry(const w12_sampling *d, const w12_tree *tree, int32_t n_r
     a.draft_stride = d->draft_stride;
     a.u_accept = d->u_accept;
     a.u_sample = d->u_sample;
+    a.num_sms = num_sms();
     a.R = tree->R;
     a.n_req = n_req;
     a.p_max = p_max;

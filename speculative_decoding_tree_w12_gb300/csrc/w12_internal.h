@@ -226,6 +226,7 @@ struct SampleArgs {
     const float *draft_p;           // [R][vocab] or null
     int64_t draft_stride;
     const float *u_accept, *u_sample;
+    int num_sms;
     int32_t R, n_req, p_max;
     const int32_t *parent, *token, *req, *off;
     int32_t *row_tok;
