@@ -54,7 +54,9 @@ struct SampleParams {
     const int32_t *parent, *token, *req, *off;
     int32_t *row_tok;
     float *row_logp;
-    int32_t *status;
+    int32_t *acc_tok, *acc_len, *acc_node;     // acc_tok null: rows only
+    int32_t p_max;
+    int32_t *done, *status;                    // rows written so far
 };
 
 // Sums of whole numbers floor(e 2^40), 0 <= e <= 1.  Adding 8 with rounding
@@ -211,6 +213,56 @@ struct Shared {
     int32_t n_kids;
 };
 
+// The accepted path of request r: from the root to the first child in row order
+// that carries the row's token, as far as there is one.  One warp.
+__device__ void accept_path(const SampleParams &p, int r, int lane)
+{
+    const int lo = p.off[r], hi = p.off[r + 1];
+    int32_t *out = p.acc_tok + (int64_t)r * (p.p_max + 1);
+    int n = 0, cur = -1;
+    if (lo >= 0 && hi <= p.R && lo < hi) {
+        cur = lo;
+        for (;;) {
+            const int want = __ldcg(p.row_tok + cur);
+            if (lane == 0) out[n] = want;
+            ++n;
+            int next = -1;
+            if (n <= p.p_max)
+                for (int j0 = cur + 1; j0 < hi && next < 0; j0 += 32) {
+                    const int j = j0 + lane;
+                    const unsigned b = __ballot_sync(0xffffffffu, j < hi && p.parent[j] == cur && p.token[j] == want);
+                    if (b) next = j0 + __ffs(b) - 1;
+                }
+            if (next < 0) break;
+            cur = next;
+        }
+    }
+    for (int i = n + lane; i <= p.p_max; i += 32) out[i] = -1;
+    if (lane == 0) {
+        p.acc_len[r] = n;
+        if (p.acc_node) p.acc_node[r] = cur;
+    }
+}
+
+// After a CTA's thread has written the row's token: the CTA that writes the
+// last row's goes on to the accepted paths.  (The count goes back to zero for
+// the next launch.)
+__device__ __forceinline__ void row_done(const SampleParams &p)
+{
+    if (!p.acc_tok) return;
+    __shared__ int32_t s_last;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        s_last = atomicAdd(p.done, 1) == p.R - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    if (threadIdx.x == 0) *p.done = 0;
+    for (int r = threadIdx.x >> 5; r < p.n_req; r += kWarps) accept_path(p, r, threadIdx.x & 31);
+}
+
 // kDraft: with the drafter's probabilities.  kHold: a thread's first kHeld
 // pieces stay in registers from the maximum to the sums.
 template <bool kF32, bool kDraft, bool kHold>
@@ -220,7 +272,6 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
     __shared__ Shared s;
     cg::cluster_group cl = cg::this_cluster();
     cl.barrier_arrive();                        // waited for before the first write to another CTA
-    pdl_launch_dependents();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int row = blockIdx.x / C;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -297,9 +348,12 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
         cluster_max();
     }
     if (!(m > -INFINITY) || !row_ok) {          // nothing can be drawn from this row
-        if (rank == 0 && tid == 0) {
-            p.row_tok[row] = -1;
-            if (p.row_logp) p.row_logp[row] = -INFINITY;
+        if (rank == 0) {
+            if (tid == 0) {
+                p.row_tok[row] = -1;
+                if (p.row_logp) p.row_logp[row] = -INFINITY;
+            }
+            row_done(p);
         }
         return;                                 // uniform over the cluster, and nobody reads another's memory any more
     }
@@ -319,10 +373,13 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
             if (lane == 0) cl.map_shared_rank(s.first, 0)[rank] = top;
         }
         cl.sync();
-        if (rank == 0 && tid == 0) {
-            for (int c = 0; c < C; ++c) top = min(top, s.first[c]);
-            p.row_tok[row] = top;
-            if (p.row_logp) p.row_logp[row] = 0.f;
+        if (rank == 0) {
+            if (tid == 0) {
+                for (int c = 0; c < C; ++c) top = min(top, s.first[c]);
+                p.row_tok[row] = top;
+                if (p.row_logp) p.row_logp[row] = 0.f;
+            }
+            row_done(p);
         }
         return;
     }
@@ -349,19 +406,18 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
         return a;
     };
     const bool q_even = kDraft && ((reinterpret_cast<uintptr_t>(qr) - 4 * z.shift) & 15) == 0;   // its pieces lie on 16 bytes too
-    // a piece's weights, in pairs
-    auto weights = [&](const uint4 &x, int v, u64 (&e)[kPer / 2]) {
-#pragma unroll
-        for (int i = 0; i < kPer; i += 2) e[i / 2] = two(x, i);
-        if (!kDraft || rounds == 0) return;
-        const int t0 = v * kPer - z.shift;
+    struct Q {                                  // the drafter's probabilities of a piece, in pairs
         u64 q[kPer / 2];
+    };
+    auto drafts = [&](int v) -> Q {
+        Q r;
+        const int t0 = v * kPer - z.shift;
         if (q_even && t0 >= 0 && t0 + kPer <= p.vocab) {
 #pragma unroll
             for (int i = 0; i < kPer; i += 4) {
                 const float4 f = __ldg(reinterpret_cast<const float4 *>(qr + t0 + i));
-                q[i / 2] = pair(f.x, f.y);
-                q[i / 2 + 1] = pair(f.z, f.w);
+                r.q[i / 2] = pair(f.x, f.y);
+                r.q[i / 2 + 1] = pair(f.z, f.w);
             }
         } else {
 #pragma unroll
@@ -369,17 +425,24 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
                 float f[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) f[k] = t0 + i + k >= 0 && t0 + i + k < p.vocab ? __ldg(qr + t0 + i + k) : 2.f;
-                q[i / 2] = pair(f[0], f[1]);
+                r.q[i / 2] = pair(f[0], f[1]);
             }
         }
-        for (int k = 0; k < rounds; ++k) {
-            const u64 inv = pair(s.inv[k], s.inv[k]);
+        return r;
+    };
+    // a piece's weights, in pairs, after the rejections so far
+    auto weights = [&](const uint4 &x, const Q &q, u64 (&e)[kPer / 2]) {
 #pragma unroll
-            for (int i = 0; i < kPer / 2; ++i) {
-                const float2 a = unpair(fma2(q[i], pair(-1.f, -1.f), mul2(e[i], inv)));
-                e[i] = pair(fmaxf(a.x, 0.f), fmaxf(a.y, 0.f));
+        for (int i = 0; i < kPer; i += 2) e[i / 2] = two(x, i);
+        if (kDraft)
+            for (int k = 0; k < rounds; ++k) {
+                const u64 inv = pair(s.inv[k], s.inv[k]);
+#pragma unroll
+                for (int i = 0; i < kPer / 2; ++i) {
+                    const float2 a = unpair(fma2(q.q[i], pair(-1.f, -1.f), mul2(e[i], inv)));
+                    e[i] = pair(fmaxf(a.x, 0.f), fmaxf(a.y, 0.f));
+                }
             }
-        }
     };
     int buf = 0;
     // sums over warps, CTA and cluster
@@ -426,12 +489,21 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
             __syncthreads();
             ++rounds;
             Sum40 left;
-            for (int v = lo + lane; v < hi; v += 32) {
-                const uint4 y = z.piece(v);
-                u64 e[kPer / 2];
-                weights(y, v, e);
+            if (lo + lane < hi) {                                   // the next piece is on its way while one is summed
+                uint4 y = z.piece(lo + lane);
+                Q q = drafts(lo + lane);
+                for (int v = lo + lane; v < hi; v += 32) {
+                    const uint4 y0 = y;
+                    const Q q0 = q;
+                    if (v + 32 < hi) {
+                        y = z.piece(v + 32);
+                        q = drafts(v + 32);
+                    }
+                    u64 e[kPer / 2];
+                    weights(y0, q0, e);
 #pragma unroll
-                for (int i = 0; i < kPer / 2; ++i) left.add(e[i]);
+                    for (int i = 0; i < kPer / 2; ++i) left.add(e[i]);
+                }
             }
             buf ^= 1;
             const u64 t = totals(left.get());
@@ -446,8 +518,9 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
     }
     // ---- the row's token
     int tok = -1;
+    bool writes = took >= 0 && rank == 0;       // this CTA has the token
     if (took >= 0) {
-        if (rank == 0 && tid == 0) tok = p.token[took];
+        if (writes && tid == 0) tok = p.token[took];
     } else {
         u64 at = (u64)__dmul_rn((double)p.u_sample[row], (double)total);
         at = at < total ? at : total - 1;
@@ -455,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
         for (int c = 0; c < rank; ++c) before += s.total[buf][c];
         const u64 mine = s.total[buf][rank];
         if (at >= before && at < before + mine) {
+            writes = true;
             u64 t = at - before;
             int wi = 0;
             while (wi < kWarps - 1 && t >= s.wsum[buf][wi]) t -= s.wsum[buf][wi++];
@@ -464,7 +538,9 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
                     u64 e[kPer / 2];
                     Sum40 piece;
                     if (v < hi) {
-                        weights(z.piece(v), v, e);
+                        Q q;
+                        if (kDraft && rounds) q = drafts(v);
+                        weights(z.piece(v), q, e);
 #pragma unroll
                         for (int i = 0; i < kPer / 2; ++i) piece.add(e[i]);
                     }
@@ -503,49 +579,7 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
             p.row_logp[row] = __fsub_rn(x == m ? 0.f : __fsub_rn(x, m), logf(mass));
         }
     }
-}
-
-// The accepted path: from the root to the child that carries the row's token,
-// the first such child in row order, as far as there is one.  One warp per
-// request; the request's rows are read once, the walk runs in shared memory.
-__global__ void __launch_bounds__(128) k_sample_path(const int32_t *parent, const int32_t *token, const int32_t *off,
-                                                     int32_t R, int32_t n_req, int32_t p_max, const int32_t *row_tok,
-                                                     int32_t *acc_tok, int32_t *acc_len, int32_t *acc_node)
-{
-    __shared__ int32_t s_next[4][kMaxBudget];
-    const int lane = threadIdx.x & 31, wi = threadIdx.x >> 5;
-    const int r = blockIdx.x * 4 + wi;
-    if (r >= n_req) return;
-    int32_t *next = s_next[wi];
-    const int lo = off[r], hi = off[r + 1];
-    int32_t *out = acc_tok + (int64_t)r * (p_max + 1);
-    for (int i = lane; i <= p_max; i += 32) out[i] = -1;
-    if (lo < 0 || hi > R || lo >= hi || hi - lo > kMaxBudget) {
-        if (lane == 0) {
-            acc_len[r] = 0;
-            if (acc_node) acc_node[r] = -1;
-        }
-        return;
-    }
-    const int rows = hi - lo;
-    for (int j = lane; j < rows; j += 32) next[j] = kMaxBudget;
-    pdl_wait();
-    __syncwarp();
-    for (int j = lane; j < rows; j += 32) {
-        const int q = parent[lo + j] - lo;
-        if (q >= 0 && q < j && row_tok[lo + q] == token[lo + j]) atomicMin(&next[q], j);
-    }
-    __syncwarp();
-    if (lane == 0) {
-        int cur = 0, n = 0;
-        while (n < p_max && next[cur] < rows) {
-            out[n++] = row_tok[lo + cur];
-            cur = next[cur];
-        }
-        out[n] = row_tok[lo + cur];
-        acc_len[r] = n + 1;
-        if (acc_node) acc_node[r] = lo + cur;
-    }
+    if (writes) row_done(p);
 }
 
 }  // namespace
@@ -574,6 +608,11 @@ int launch_sample(const SampleArgs &a, void *stream)
     p.off = a.off;
     p.row_tok = a.row_tok;
     p.row_logp = a.row_logp;
+    p.acc_tok = a.acc_tok;
+    p.acc_len = a.acc_len;
+    p.acc_node = a.acc_node;
+    p.p_max = a.p_max;
+    p.done = a.done;
     p.status = a.status;
     // CTAs of a row: up to 8 of 2048 tokens or more each, so that the waves of
     // them, each as long as its stretch and some 16384 tokens' worth of barriers,
@@ -609,18 +648,7 @@ int launch_sample(const SampleArgs &a, void *stream)
     };
     if (a.f32) a.draft_p ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
     else a.draft_p ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});
-    if (e != cudaSuccess || !a.acc_tok) return (int)e;
-    cudaLaunchConfig_t cf{};
-    cf.gridDim = dim3((unsigned)((a.n_req + 3) / 4));
-    cf.blockDim = dim3(128);
-    cf.stream = cfg.stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cf.attrs = at;
-    cf.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&cf, k_sample_path, a.parent, a.token, a.off, a.R, a.n_req, a.p_max,
-                                   (const int32_t *)a.row_tok, a.acc_tok, a.acc_len, a.acc_node);
+    return (int)e;
 }
 
 }  // namespace w12i

@@ -199,7 +199,7 @@ WsLayout layout_for(int32_t R, int64_t max_n, int64_t vocab, int32_t n_req)
     L.status = o;
     o += 256;
     L.arrive = o;
-    o += static_cast<size_t>(kMaxBudget) * 4;
+    o += static_cast<size_t>(kMaxBudget + 64) * 4;
     // the chain words end exactly where the counters start
     L.grid = o;
     o += static_cast<size_t>(kGridWords) * 4;
@@ -976,6 +976,7 @@ w12_status sample_entry(const w12_sampling *d, const w12_tree *tree, int32_t n_r
     a.acc_tok = acc_tok;
     a.acc_len = acc_len;
     a.acc_node = acc_node;
+    a.done = W.arrive() + kMaxBudget;
     a.status = W.status();
     return cuda_status(launch_sample(a, stream));
 }
