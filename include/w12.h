@@ -590,6 +590,8 @@ typedef struct {
     int64_t draft_stride;
     const float *u_accept;       /* device [R] in [0, 1): decides on row j as a draft (needed with draft_p) */
     const float *u_sample;       /* device [R] in [0, 1): draws row i's own token */
+    void *scratch;               /* device, 16-byte aligned: w12_sample_scratch_bytes(scratch_rows, vocab) bytes, set to zero once */
+    int32_t scratch_rows;        /* rows the scratch is sized for, at least the tree's; calls that share it run in order */
 } w12_sampling;
 
 /*
@@ -606,6 +608,7 @@ typedef struct {
  * vocab <= w12_sample_max_vocab().  ws: as for w12_tree_build.
  */
 int64_t w12_sample_max_vocab(void);
+size_t w12_sample_scratch_bytes(int32_t R, int64_t vocab);
 w12_status w12_tree_sample(const w12_sampling *dist, const w12_tree *tree, int32_t n_req, int32_t *row_tok,
                            float *row_logp, void *ws, size_t ws_bytes, w12_stream_t stream);
 

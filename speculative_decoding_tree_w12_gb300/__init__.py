@@ -116,6 +116,7 @@ def lib():
             "w12_attn_workspace_bytes": ([i32, i32, i32, i32], sz),
             "w12_tree_attention": ([p, p, p, i32, i32, p, i64, p, i64, p, i64, C.c_float, p, p, sz, p, sz, p], C.c_int),
             "w12_sample_max_vocab": ([], i64),
+            "w12_sample_scratch_bytes": ([i32, i64], sz),
             "w12_tree_sample": ([p, p, i32, p, p, p, sz, p], C.c_int),
             "w12_tree_verify_sampled": ([p, p, i32, i32, p, p, p, p, p, p, sz, p], C.c_int),
             "w12_debug_set": ([i32, C.c_uint64], None),
@@ -706,14 +707,15 @@ def w12_tree_attention(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n
 class SamplingC(C.Structure):
     _fields_ = [("logits", C.c_void_p), ("logits_f32", C.c_int32), ("vocab", C.c_int64), ("logits_stride", C.c_int64),
                 ("temperature", C.c_void_p), ("draft_p", C.c_void_p), ("draft_stride", C.c_int64),
-                ("u_accept", C.c_void_p), ("u_sample", C.c_void_p)]
+                ("u_accept", C.c_void_p), ("u_sample", C.c_void_p), ("scratch", C.c_void_p), ("scratch_rows", C.c_int32)]
 
 
 class SampleRows:
     """The target's logits (bfloat16 or float32 [R][vocab]) and the random
     numbers of one sampled verification: u_sample (float32 [R]), temperature
     (float32 [n_req], optional; 0 = greedy) and, for a drafter that samples,
-    its probabilities draft_p (float32 [R][vocab]) with u_accept (float32 [R])."""
+    its probabilities draft_p (float32 [R][vocab]) with u_accept (float32 [R]).
+    Holds the calls' scratch; one object's calls run in order."""
 
     def __init__(self, logits, u_sample, temperature=None, draft_p=None, u_accept=None):
         torch = _runtime()
@@ -734,8 +736,13 @@ class SampleRows:
         self.logits, self.u_sample, self.temperature, self.draft_p, self.u_accept = \
             logits, u_sample, temperature, draft_p, u_accept
         row = lambda t: t.stride(0) if R > 1 else max(t.stride(0), V)
+        nbytes = int(lib().w12_sample_scratch_bytes(R, V))
+        if nbytes == 0:
+            raise W12Error(W12_E_UNSUPPORTED, "w12_sample_scratch_bytes")
+        self.scratch = torch.zeros(nbytes, dtype=torch.uint8, device=logits.device)
         self.c = SamplingC(logits.data_ptr(), int(logits.dtype == torch.float32), V, row(logits), _dp(temperature),
-                           _dp(draft_p), row(draft_p) if draft_p is not None else 0, _dp(u_accept), _dp(u_sample))
+                           _dp(draft_p), row(draft_p) if draft_p is not None else 0, _dp(u_accept), _dp(u_sample),
+                           self.scratch.data_ptr(), R)
         self.ref = C.byref(self.c)
         self.rows = R
         self.requests = None if temperature is None else int(temperature.shape[0])

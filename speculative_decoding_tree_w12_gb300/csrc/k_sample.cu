@@ -15,15 +15,16 @@
 // and inverse-CDF boundaries are exact.  (Weights under 2^-40 of the largest
 // are never drawn.)
 //
-// A cluster of CTAs shares a row; maxima and sums cross it through distributed
-// shared memory.  Weights are never stored: a pass makes them from the logits
-// (16 bytes at a time; from L2 after the first pass, or from registers where
-// few rows leave room), so a row costs one read of the logits from memory, one
-// more pass for the sums, and one with the drafter's probabilities only where a
-// child is rejected.  The token is found by the sums alone down to one warp's
-// stretch of the row, which that warp goes through again in order.  What bounds
-// many rows is the issue rate of the sums' pass, some 16 instructions a token,
-// half of them expf.
+// k_sample_max and k_sample_sum go over the logits in chunks, each chunk a CTA:
+// the first for the rows' maxima, the second (from L2, asked for before it has
+// to wait for the maxima) for the sums of the weights of every warp's stretch.
+// The CTA that completes a row finds the stretch its token lies in by these
+// sums, and goes through it once more in order.  With a drafter's probabilities
+// k_sample_draft takes over from there: a cluster to a row, which ends at once
+// where a child is accepted and goes over the row again for every rejection.
+// The CTA that completes the last row writes the accepted paths.
+// Many rows are bound by the issue rate of the sums' pass, some 15 instructions
+// a token, half of them expf; few rows by latency.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -41,15 +42,19 @@ using namespace w12d;
 using namespace w12i;
 typedef unsigned long long u64;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;                  // k_sample_draft
 constexpr int kWarps = kThreads / 32;
+constexpr int kChunkThreads = 256;             // k_sample_max, k_sample_sum
+constexpr int kChunkWarps = kChunkThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int64_t kMaxVocab = 1 << 20;
 
 struct SampleParams {
     const void *logits;
     int64_t stride, draft_stride;
     const float *temperature, *draft_p, *u_accept, *u_sample;
-    int32_t vocab, sub;                        // tokens; 16-byte pieces of the row of one warp
+    int32_t vocab, sub;                        // tokens; 16-byte pieces of the row of one warp of k_sample_draft
+    int32_t chunks;                            // of a row
     int32_t R, n_req;
     const int32_t *parent, *token, *req, *off;
     int32_t *row_tok;
@@ -57,6 +62,10 @@ struct SampleParams {
     int32_t *acc_tok, *acc_len, *acc_node;     // acc_tok null: rows only
     int32_t p_max;
     int32_t *done, *status;                    // rows written so far
+    // scratch
+    int32_t *arrived;                          // [R] chunks summed; zero between calls
+    float *top;                                // [R][chunks] largest logit
+    u64 *sums;                                 // [R][chunks][kChunkWarps] (greedy rows: lowest token with the largest logit)
 };
 
 // Sums of whole numbers floor(e 2^40), 0 <= e <= 1.  Adding 8 with rounding
@@ -143,20 +152,6 @@ __device__ __forceinline__ u64 warp_sum(u64 x)
     return x;
 }
 
-// the larger, or NaN
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ float max_nan(float a, float b, float c)
-{
-    float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // A row of logits as 16-byte pieces on their own boundaries: piece v holds
 // tokens v kPer - shift .. ; the ends are read token by token.
 template <bool kF32>
@@ -202,37 +197,31 @@ struct Row {
     }
 };
 
-struct Shared {
-    float top[kMaxCluster];                    // written by every CTA of the cluster
-    int32_t first[kMaxCluster];
-    u64 total[2][kMaxCluster];
-    float wtop[kWarps];
-    u64 wsum[2][kWarps];
-    int32_t kids[kMaxBudget];
-    float inv[kMaxBudget];                     // of the rejections so far
-    int32_t n_kids;
-};
-
 // The accepted path of request r: from the root to the first child in row order
-// that carries the row's token, as far as there is one.  One warp.
+// that carries the row's token, as far as there is one.  One warp; a request's
+// first 32 rows are fetched at once.
 __device__ void accept_path(const SampleParams &p, int r, int lane)
 {
     const int lo = p.off[r], hi = p.off[r + 1];
     int32_t *out = p.acc_tok + (int64_t)r * (p.p_max + 1);
     int n = 0, cur = -1;
     if (lo >= 0 && hi <= p.R && lo < hi) {
+        const bool in = lo + lane < hi;
+        const int parent = in ? p.parent[lo + lane] : -1, token = in ? p.token[lo + lane] : -1;
+        const int drawn = in ? __ldcg(p.row_tok + lo + lane) : -1;
         cur = lo;
         for (;;) {
-            const int want = __ldcg(p.row_tok + cur);
+            const int want = cur - lo < 32 ? __shfl_sync(0xffffffffu, drawn, cur - lo) : __ldcg(p.row_tok + cur);
             if (lane == 0) out[n] = want;
             ++n;
-            int next = -1;
-            if (n <= p.p_max)
-                for (int j0 = cur + 1; j0 < hi && next < 0; j0 += 32) {
-                    const int j = j0 + lane;
-                    const unsigned b = __ballot_sync(0xffffffffu, j < hi && p.parent[j] == cur && p.token[j] == want);
-                    if (b) next = j0 + __ffs(b) - 1;
-                }
+            if (n > p.p_max) break;
+            unsigned b = __ballot_sync(0xffffffffu, in && lo + lane > cur && parent == cur && token == want);
+            int next = b ? lo + __ffs(b) - 1 : -1;
+            for (int j0 = max(cur + 1, lo + 32); j0 < hi && next < 0; j0 += 32) {
+                const int j = j0 + lane;
+                b = __ballot_sync(0xffffffffu, j < hi && p.parent[j] == cur && p.token[j] == want);
+                if (b) next = j0 + __ffs(b) - 1;
+            }
             if (next < 0) break;
             cur = next;
         }
@@ -260,15 +249,300 @@ __device__ __forceinline__ void row_done(const SampleParams &p)
     if (!s_last) return;
     __threadfence();
     if (threadIdx.x == 0) *p.done = 0;
-    for (int r = threadIdx.x >> 5; r < p.n_req; r += kWarps) accept_path(p, r, threadIdx.x & 31);
+    for (int r = threadIdx.x >> 5; r < p.n_req; r += blockDim.x >> 5) accept_path(p, r, threadIdx.x & 31);
 }
 
-// kDraft: with the drafter's probabilities.  kHold: a thread's first kHeld
-// pieces stay in registers from the maximum to the sums.
-template <bool kF32, bool kDraft, bool kHold>
-__global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample_rows(const SampleParams p)
+// a greedy row's token: the lowest of the chunks' candidates.  One warp.
+__device__ __forceinline__ void draw_greedy(const SampleParams &p, int row, int lane)
 {
-    constexpr int kPer = Row<kF32>::kPer, kHeld = kHold ? (kF32 ? 10 : 5) : 0;
+    int tok = INT32_MAX;
+    for (int i = lane; i < p.chunks * kChunkWarps; i += 32)
+        tok = min(tok, (int)__ldcg(p.sums + (int64_t)row * p.chunks * kChunkWarps + i));
+    tok = __reduce_min_sync(0xffffffffu, tok);
+    if (lane == 0) {
+        p.row_tok[row] = tok;
+        if (p.row_logp) p.row_logp[row] = 0.f;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// what the kernels share: a row's temperature, weights and the search
+// ---------------------------------------------------------------------------
+
+struct Temper {
+    float inv_t;
+    bool ok, greedy;
+};
+
+__device__ __forceinline__ Temper temper(const SampleParams &p, int row)
+{
+    const int r = p.req[row];
+    Temper t;
+    t.ok = r >= 0 && r < p.n_req;
+    const float T = t.ok && p.temperature ? p.temperature[r] : 1.f;
+    t.greedy = !(T > 0.f);
+    t.inv_t = t.greedy ? 1.f : __fdiv_rn(1.f, T);
+    return t;
+}
+
+// exp(z - m), z = logit / T
+template <bool kF32>
+struct Weigher {
+    static constexpr int kPer = Row<kF32>::kPer;
+    float inv_t, m;                            // m: the largest z
+    __device__ Weigher(float inv_t_, float top) : inv_t(inv_t_), m(top * inv_t_) {}   // (a positive factor keeps the order)
+    __device__ __forceinline__ float one(float x) const
+    {
+        const float z = __fmul_rn(x, inv_t);
+        if (m == INFINITY) return z == INFINITY ? 1.f : 0.f;            // nothing but the infinite ones counts
+        return expf(fmaxf(__fsub_rn(z, m), -128.f));                    // (a NaN becomes a weight of nothing)
+    }
+    // of a piece's tokens, in pairs
+    __device__ __forceinline__ void piece(const uint4 &x, u64 (&e)[kPer / 2]) const
+    {
+        if (m == INFINITY) {
+#pragma unroll
+            for (int i = 0; i < kPer; i += 2) e[i / 2] = pair(one(Row<kF32>::get(x, i)), one(Row<kF32>::get(x, i + 1)));
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) {
+            const u64 z = mul2(pair(Row<kF32>::get(x, i), Row<kF32>::get(x, i + 1)), pair(inv_t, inv_t));
+            const float2 d = unpair(add2(z, pair(-m, -m)));
+            e[i / 2] = pair(expf(fmaxf(d.x, -128.f)), expf(fmaxf(d.y, -128.f)));
+        }
+    }
+};
+
+// The warp's token of a stretch of pieces lo .. hi - 1: the first whose weights
+// up to and with it sum to more than t; -1 on all lanes but the one that has it.
+// `piece(v, e)` gives a piece's weights in pairs.
+template <int kPer, class Piece>
+__device__ __forceinline__ int find_token(int lo, int hi, u64 t, int shift, int lane, Piece piece)
+{
+    for (int v0 = lo; v0 < hi; v0 += 32) {
+        const int v = v0 + lane;
+        u64 e[kPer / 2];
+        Sum40 s;
+        if (v < hi) {
+            piece(v, e);
+#pragma unroll
+            for (int i = 0; i < kPer / 2; ++i) s.add(e[i]);
+        }
+        const u64 x = s.get();
+        u64 incl = x;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const u64 o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        const unsigned b = __ballot_sync(0xffffffffu, incl > t);
+        if (b) {
+            if (lane != __ffs(b) - 1) return -1;
+            u64 c = incl - x;
+            int i = 0;
+#pragma unroll
+            for (int k = 0; k < kPer - 1; ++k) {
+                const float2 f = unpair(e[k / 2]);
+                c += fixed40(k & 1 ? f.y : f.x);
+                if (c <= t) i = k + 1;
+            }
+            return v * kPer - shift + i;
+        }
+        t -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return -1;
+}
+
+// where u of the mass lies
+__device__ __forceinline__ u64 place(float u, u64 total)
+{
+    const u64 at = (u64)__dmul_rn((double)u, (double)total);
+    return at < total ? at : total - 1;
+}
+
+template <bool kF32>
+__device__ __forceinline__ void write_row(const SampleParams &p, int row, int tok, const Row<kF32> &z, const Weigher<kF32> &w, u64 total)
+{
+    p.row_tok[row] = tok;
+    if (p.row_logp) {
+        // (a NaN can only be an accepted child's)
+        const float x = __fmul_rn(fmaxf(z.token(tok), -INFINITY), w.inv_t);
+        p.row_logp[row] = __fsub_rn(x == w.m ? 0.f : __fsub_rn(x, w.m), logf(weight_of(total)));
+    }
+}
+
+__device__ __forceinline__ void write_none(const SampleParams &p, int row)
+{
+    p.row_tok[row] = -1;
+    if (p.row_logp) p.row_logp[row] = -INFINITY;
+}
+
+// the row's largest logit, by every warp for itself
+__device__ __forceinline__ float row_top(const SampleParams &p, int row, int lane)
+{
+    float m = -INFINITY;
+    for (int c = lane; c < p.chunks; c += 32) m = fmaxf(m, __ldcg(p.top + (int64_t)row * p.chunks + c));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    return m;
+}
+
+// A row without rejections, by one warp: its token by the sums of the chunks' stretches.
+template <bool kF32>
+__device__ void draw(const SampleParams &p, int row, int lane, const Row<kF32> &z, const Weigher<kF32> &w, int stretch, int pieces)
+{
+    constexpr int kPer = Row<kF32>::kPer;
+    const u64 *sums = p.sums + (int64_t)row * p.chunks * kChunkWarps;
+    const int n = p.chunks * kChunkWarps;
+    u64 total = 0;
+    for (int i = lane; i < n; i += 32) total += __ldcg(sums + i);
+    total = warp_sum(total);
+    u64 t = place(p.u_sample[row], total);
+    int at = -1;
+    for (int i0 = 0; i0 < n && at < 0; i0 += 32) {
+        u64 incl = i0 + lane < n ? __ldcg(sums + i0 + lane) : 0ull;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const u64 o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        const unsigned b = __ballot_sync(0xffffffffu, incl > t);
+        if (b) {
+            at = i0 + __ffs(b) - 1;
+            t -= __ffs(b) > 1 ? __shfl_sync(0xffffffffu, incl, __ffs(b) - 2) : 0ull;
+        } else {
+            t -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    const int lo = at * stretch;
+    const int tok = find_token<kPer>(lo, min(pieces, lo + stretch), t, z.shift, lane, [&](int v, u64 (&e)[kPer / 2]) {
+        w.piece(z.piece(v), e);
+    });
+    if (tok >= 0) write_row(p, row, tok, z, w, total);
+}
+
+// ---------------------------------------------------------------------------
+// the two passes
+// ---------------------------------------------------------------------------
+
+// kP: pieces of a thread; a warp's stretch is 32 kP pieces
+template <bool kF32, int kP>
+__global__ void __launch_bounds__(kChunkThreads) k_sample_max(const SampleParams p)
+{
+    constexpr int kPer = Row<kF32>::kPer;
+    __shared__ float s_top[kChunkWarps];
+    const int row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Row<kF32> z(p.logits, row * p.stride, p.vocab);
+    const int pieces = (z.shift + p.vocab + kPer - 1) / kPer;
+    const int lo = (blockIdx.x * kChunkWarps + warp) * 32 * kP + lane;
+    pdl_launch_dependents();
+    float m = -INFINITY;
+    uint4 x[kP];
+#pragma unroll
+    for (int k = 0; k < kP; ++k)
+        if (lo + k * 32 < pieces) x[k] = z.piece(lo + k * 32);
+#pragma unroll
+    for (int k = 0; k < kP; ++k)
+        if (lo + k * 32 < pieces)
+#pragma unroll
+            for (int i = 0; i < kPer; i += 2) m = fmaxf(fmaxf(m, Row<kF32>::get(x[k], i)), Row<kF32>::get(x[k], i + 1));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (lane == 0) s_top[warp] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 1; w < kChunkWarps; ++w) m = fmaxf(m, s_top[w]);
+        p.top[(int64_t)row * p.chunks + blockIdx.x] = m;
+    }
+}
+
+template <bool kF32, int kP, bool kDraft>
+__global__ void __launch_bounds__(kChunkThreads) k_sample_sum(const SampleParams p)
+{
+    constexpr int kPer = Row<kF32>::kPer;
+    __shared__ int32_t s_last;
+    const int row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Row<kF32> z(p.logits, row * p.stride, p.vocab);
+    const int pieces = (z.shift + p.vocab + kPer - 1) / kPer;
+    const int lo = (blockIdx.x * kChunkWarps + warp) * 32 * kP + lane;
+    const Temper t = temper(p, row);
+    if (kDraft) pdl_launch_dependents();
+    uint4 x[kP];
+#pragma unroll
+    for (int k = 0; k < kP; ++k)
+        if (lo + k * 32 < pieces) x[k] = z.piece(lo + k * 32);
+    pdl_wait();
+    const float top = row_top(p, row, lane);
+    const Weigher<kF32> w(t.inv_t, top);
+    u64 *mine = p.sums + ((int64_t)row * p.chunks + blockIdx.x) * kChunkWarps + warp;
+    if (t.greedy) {                             // the largest logit, the lowest token of equals, whatever the draft
+        int tok = INT32_MAX;
+#pragma unroll
+        for (int k = 0; k < kP; ++k)
+            if (lo + k * 32 < pieces)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (Row<kF32>::get(x[k], i) == top) tok = min(tok, (lo + k * 32) * kPer - z.shift + i);
+        tok = __reduce_min_sync(0xffffffffu, tok);
+        if (lane == 0) *mine = (u64)tok;
+    } else {
+        Sum40 sum;
+#pragma unroll
+        for (int k = 0; k < kP; ++k)
+            if (lo + k * 32 < pieces) {
+                u64 e[kPer / 2];
+                w.piece(x[k], e);
+#pragma unroll
+                for (int i = 0; i < kPer / 2; ++i) sum.add(e[i]);
+            }
+        const u64 all = warp_sum(sum.get());
+        if (lane == 0) *mine = all;
+    }
+    if (kDraft) return;
+    // ---- the row's last CTA draws its token
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        s_last = atomicAdd(p.arrived + row, 1) == p.chunks - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    if (warp == 0) {
+        if (lane == 0) {
+            p.arrived[row] = 0;
+            if (!t.ok) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
+        }
+        if (!(top > -INFINITY) || !t.ok) {      // nothing can be drawn from this row
+            if (lane == 0) write_none(p, row);
+        } else if (t.greedy) {
+            draw_greedy(p, row, lane);
+        } else {
+            draw(p, row, lane, z, w, 32 * kP, pieces);
+        }
+    }
+    row_done(p);
+}
+
+// ---------------------------------------------------------------------------
+// rejection sampling
+// ---------------------------------------------------------------------------
+
+struct Shared {
+    u64 total[2][kMaxCluster];                 // written by every CTA of the cluster
+    u64 wsum[2][kWarps];
+    int32_t kids[kMaxBudget];
+    float inv[kMaxBudget];                     // of the rejections so far
+    int32_t n_kids;
+};
+
+// stretch: pieces of a warp of k_sample_sum
+template <bool kF32>
+__global__ void __launch_bounds__(kThreads, 2) k_sample_draft(const SampleParams p, int stretch)
+{
+    constexpr int kPer = Row<kF32>::kPer;
     __shared__ Shared s;
     cg::cluster_group cl = cg::this_cluster();
     cl.barrier_arrive();                        // waited for before the first write to another CTA
@@ -278,35 +552,12 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
     const Row<kF32> z(p.logits, row * p.stride, p.vocab);
     const int pieces = (z.shift + p.vocab + kPer - 1) / kPer;
     const int lo = min(pieces, (rank * kWarps + warp) * p.sub), hi = min(pieces, lo + p.sub);   // this warp's pieces, in order
-    const float *qr = kDraft ? p.draft_p + row * p.draft_stride : nullptr;
-    const int r = p.req[row];
-    const bool row_ok = r >= 0 && r < p.n_req;
-    if (!row_ok && tid == 0 && rank == 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
-    const float temp = row_ok && p.temperature ? p.temperature[r] : 1.f;
-    const bool greedy = !(temp > 0.f);
-    const float inv_t = greedy ? 1.f : __fdiv_rn(1.f, temp);
-
-    // ---- the largest logit, and whether there is a NaN
-    uint4 held[kHold ? kHeld : 1];
-    float m = -INFINITY;
-    auto larger = [&](const uint4 &x) {
-#pragma unroll
-        for (int i = 0; i < kPer; i += 2) m = max_nan(m, Row<kF32>::get(x, i), Row<kF32>::get(x, i + 1));
-    };
-    if (kHold) {
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k)
-            if (lo + k * 32 + lane < hi) held[k] = z.piece(lo + k * 32 + lane);
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k)
-            if (lo + k * 32 + lane < hi) larger(held[k]);
-    }
-#pragma unroll 4
-    for (int v = lo + kHeld * 32 + lane; v < hi; v += 32) larger(z.piece(v));
+    const float *qr = p.draft_p + row * p.draft_stride;
+    const Temper t = temper(p, row);
     // children of the row, in row order
-    if (kDraft && warp == 0) {
+    if (warp == 0) {
         int cnt = 0;
-        const int end = row_ok ? min(p.R, p.off[r + 1]) : 0;
+        const int end = t.ok ? min(p.R, p.off[p.req[row] + 1]) : 0;
         for (int j0 = row + 1; j0 < end; j0 += 32) {
             const bool kid = j0 + lane < end && p.parent[j0 + lane] == row;
             const unsigned b = __ballot_sync(0xffffffffu, kid);
@@ -315,97 +566,27 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
         }
         if (lane == 0) s.n_kids = cnt;
     }
-    bool started = false;
-    auto cluster_max = [&]() {                  // of m, over the cluster
-#pragma unroll
-        for (int d = 16; d; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if (lane == 0) s.wtop[warp] = m;
-        __syncthreads();
-        if (!started) cl.barrier_wait();
-        started = true;
+    __syncthreads();
+    cl.barrier_wait();
+    pdl_wait();
+    const float top = row_top(p, row, lane);
+    if (!t.ok || !(top > -INFINITY) || t.greedy) {          // the same for the whole cluster
+        if (rank) return;
         if (warp == 0) {
-            m = s.wtop[lane & (kWarps - 1)];
-#pragma unroll
-            for (int d = kWarps / 2; d; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-            if (lane < C) cl.map_shared_rank(s.top, lane)[rank] = m;
+            if (!t.ok && lane == 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
+            if (t.ok && top > -INFINITY) draw_greedy(p, row, lane);
+            else if (lane == 0) write_none(p, row);
         }
-        cl.sync();
-        m = s.top[0];
-        for (int c = 1; c < C; ++c) m = max_nan(m, s.top[c]);
-    };
-    cluster_max();
-    // NaN counts as -inf; rows that have one, or +inf, take the careful way from here on
-    bool careful = m == INFINITY;
-    if (m != m) {
-        careful = true;
-        m = -INFINITY;
-        for (int v = lo + lane; v < hi; v += 32) {
-            const uint4 x = z.piece(v);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) m = fmaxf(m, Row<kF32>::get(x, i));
-        }
-        cl.sync();                              // every CTA has read the last maxima
-        cluster_max();
-    }
-    if (!(m > -INFINITY) || !row_ok) {          // nothing can be drawn from this row
-        if (rank == 0) {
-            if (tid == 0) {
-                p.row_tok[row] = -1;
-                if (p.row_logp) p.row_logp[row] = -INFINITY;
-            }
-            row_done(p);
-        }
-        return;                                 // uniform over the cluster, and nobody reads another's memory any more
-    }
-    if (greedy) {                               // the largest logit, the lowest token of equals, whatever the draft
-        int top = p.vocab;
-        for (int v = lo + lane; v < hi; v += 32) {
-            const uint4 x = z.piece(v);
-#pragma unroll
-            for (int i = kPer - 1; i >= 0; --i)
-                if (Row<kF32>::get(x, i) == m) top = min(top, v * kPer - z.shift + i);
-        }
-        top = __reduce_min_sync(0xffffffffu, top);
-        if (lane == 0) s.wtop[warp] = __int_as_float(top);
-        __syncthreads();
-        if (warp == 0) {
-            top = __reduce_min_sync(0xffffffffu, __float_as_int(s.wtop[lane & (kWarps - 1)]));
-            if (lane == 0) cl.map_shared_rank(s.first, 0)[rank] = top;
-        }
-        cl.sync();
-        if (rank == 0) {
-            if (tid == 0) {
-                for (int c = 0; c < C; ++c) top = min(top, s.first[c]);
-                p.row_tok[row] = top;
-                if (p.row_logp) p.row_logp[row] = 0.f;
-            }
-            row_done(p);
-        }
+        row_done(p);
         return;
     }
-    m = __fmul_rn(m, inv_t);                    // of z = logit / T: scaling by a positive number keeps the order
-
-    // ---- weights exp(z - m)
-    auto one = [&](float x) -> float {
-        if (!careful) return expf(__fsub_rn(__fmul_rn(x, inv_t), m));
-        const float y = __fmul_rn(x, inv_t);
-        return y == m ? 1.f : y < m ? expf(__fsub_rn(y, m)) : 0.f;       // (a NaN is neither)
-    };
-    const u64 inv2 = pair(inv_t, inv_t), neg2 = pair(-m, -m);
-    // the weights of tokens i and i + 1 of a piece
-    auto two = [&](const uint4 &x, int i) -> u64 {
-        const float a = Row<kF32>::get(x, i), b = Row<kF32>::get(x, i + 1);
-        if (careful) return pair(one(a), one(b));
-        const float2 d = unpair(add2(mul2(pair(a, b), inv2), neg2));
-        return pair(expf(d.x), expf(d.y));
-    };
-    // what is left of a weight after the rejections so far
+    const Weigher<kF32> w(t.inv_t, top);
+    u64 total = 0;
+    for (int i = lane; i < p.chunks * kChunkWarps; i += 32) total += __ldcg(p.sums + (int64_t)row * p.chunks * kChunkWarps + i);
+    total = warp_sum(total);
+    const u64 whole = total;
+    const bool q_even = ((reinterpret_cast<uintptr_t>(qr) - 4 * z.shift) & 15) == 0;   // its pieces lie on 16 bytes too
     int rounds = 0;
-    auto rest = [&](float a, float q) -> float {
-        for (int k = 0; k < rounds; ++k) a = fmaxf(__fsub_rn(__fmul_rn(a, s.inv[k]), q), 0.f);
-        return a;
-    };
-    const bool q_even = kDraft && ((reinterpret_cast<uintptr_t>(qr) - 4 * z.shift) & 15) == 0;   // its pieces lie on 16 bytes too
     struct Q {                                  // the drafter's probabilities of a piece, in pairs
         u64 q[kPer / 2];
     };
@@ -430,19 +611,17 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
         }
         return r;
     };
-    // a piece's weights, in pairs, after the rejections so far
+    // what is left of a piece's weights after the rejections so far, in pairs
     auto weights = [&](const uint4 &x, const Q &q, u64 (&e)[kPer / 2]) {
+        w.piece(x, e);
+        for (int k = 0; k < rounds; ++k) {
+            const u64 inv = pair(s.inv[k], s.inv[k]);
 #pragma unroll
-        for (int i = 0; i < kPer; i += 2) e[i / 2] = two(x, i);
-        if (kDraft)
-            for (int k = 0; k < rounds; ++k) {
-                const u64 inv = pair(s.inv[k], s.inv[k]);
-#pragma unroll
-                for (int i = 0; i < kPer / 2; ++i) {
-                    const float2 a = unpair(fma2(q.q[i], pair(-1.f, -1.f), mul2(e[i], inv)));
-                    e[i] = pair(fmaxf(a.x, 0.f), fmaxf(a.y, 0.f));
-                }
+            for (int i = 0; i < kPer / 2; ++i) {
+                const float2 a = unpair(fma2(q.q[i], pair(-1.f, -1.f), mul2(e[i], inv)));
+                e[i] = pair(fmaxf(a.x, 0.f), fmaxf(a.y, 0.f));
             }
+        }
     };
     int buf = 0;
     // sums over warps, CTA and cluster
@@ -451,132 +630,77 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
         if (lane == 0) s.wsum[buf][warp] = x;
         __syncthreads();
         if (warp == 0) {
-            const u64 t = warp_sum(lane < kWarps ? s.wsum[buf][lane] : 0ull);
-            if (lane < C) cl.map_shared_rank(s.total[buf], lane)[rank] = t;
+            const u64 c = warp_sum(lane < kWarps ? s.wsum[buf][lane] : 0ull);
+            if (lane < C) cl.map_shared_rank(s.total[buf], lane)[rank] = c;
         }
         cl.sync();
-        u64 t = 0;
-        for (int c = 0; c < C; ++c) t += s.total[buf][c];
-        return t;
+        u64 c = 0;
+        for (int i = 0; i < C; ++i) c += s.total[buf][i];
+        return c;
     };
-    Sum40 sum;
-    auto weigh = [&](const uint4 &x) {
-#pragma unroll
-        for (int i = 0; i < kPer; i += 2) sum.add(two(x, i));
-    };
-    if (kHold) {
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k)
-            if (lo + k * 32 + lane < hi) weigh(held[k]);
-    }
-#pragma unroll 2
-    for (int v = lo + kHeld * 32 + lane; v < hi; v += 32) weigh(z.piece(v));
-    u64 total = totals(sum.get());
-    const float mass = weight_of(total);
     int took = -1;
-    if (kDraft) {
-        const int n_kids = s.n_kids;
-        for (int c = 0; c < n_kids; ++c) {
-            const int kid = s.kids[c], x = p.token[kid];
-            if (x < 0 || x >= p.vocab) continue;                   // not a token: it cannot be accepted
-            const float q = __ldg(qr + x), a = rest(one(z.token(x)), q), inv = __fdiv_rn(1.f, weight_of(total));
-            if (__fmul_rn(p.u_accept[kid], q) < __fmul_rn(a, inv)) {
-                took = kid;
-                break;
-            }
-            __syncthreads();                                        // (everyone is done with the last entry)
-            if (tid == 0) s.inv[rounds] = inv;
-            __syncthreads();
-            ++rounds;
-            Sum40 left;
-            if (lo + lane < hi) {                                   // the next piece is on its way while one is summed
-                uint4 y = z.piece(lo + lane);
-                Q q = drafts(lo + lane);
-                for (int v = lo + lane; v < hi; v += 32) {
-                    const uint4 y0 = y;
-                    const Q q0 = q;
-                    if (v + 32 < hi) {
-                        y = z.piece(v + 32);
-                        q = drafts(v + 32);
-                    }
-                    u64 e[kPer / 2];
-                    weights(y0, q0, e);
-#pragma unroll
-                    for (int i = 0; i < kPer / 2; ++i) left.add(e[i]);
+    const int n_kids = s.n_kids;
+    for (int c = 0; c < n_kids; ++c) {
+        const int kid = s.kids[c], x = p.token[kid];
+        if (x < 0 || x >= p.vocab) continue;                       // not a token: it cannot be accepted
+        const float q = __ldg(qr + x), inv = __fdiv_rn(1.f, weight_of(total));
+        float a = w.one(z.token(x));
+        for (int k = 0; k < rounds; ++k) a = fmaxf(__fsub_rn(__fmul_rn(a, s.inv[k]), q), 0.f);
+        if (__fmul_rn(p.u_accept[kid], q) < __fmul_rn(a, inv)) {
+            took = kid;
+            break;
+        }
+        __syncthreads();                                            // (everyone is done with the last entry)
+        if (tid == 0) s.inv[rounds] = inv;
+        __syncthreads();
+        ++rounds;
+        Sum40 left;
+        if (lo + lane < hi) {                                       // the next piece is on its way while one is summed
+            uint4 y = z.piece(lo + lane);
+            Q d = drafts(lo + lane);
+            for (int v = lo + lane; v < hi; v += 32) {
+                const uint4 y0 = y;
+                const Q d0 = d;
+                if (v + 32 < hi) {
+                    y = z.piece(v + 32);
+                    d = drafts(v + 32);
                 }
+                u64 e[kPer / 2];
+                weights(y0, d0, e);
+#pragma unroll
+                for (int i = 0; i < kPer / 2; ++i) left.add(e[i]);
             }
+        }
+        buf ^= 1;
+        const u64 r = totals(left.get());
+        if (r) {
+            total = r;
+        } else {                                                    // p = q: p stays, and so do its sums
+            --rounds;
             buf ^= 1;
-            const u64 t = totals(left.get());
-            if (t) {
-                total = t;
-            } else {                                                // p = q: p stays, and so do its sums
-                --rounds;
-                buf ^= 1;
-                cl.sync();                                          // every CTA has read the sums it leaves
-            }
+            cl.sync();                                              // every CTA has read the sums it leaves
         }
     }
     // ---- the row's token
-    int tok = -1;
-    bool writes = took >= 0 && rank == 0;       // this CTA has the token
+    bool writes = rank == 0;                                        // this CTA has it
     if (took >= 0) {
-        if (writes && tid == 0) tok = p.token[took];
+        if (writes && tid == 0) write_row(p, row, p.token[took], z, w, whole);
+    } else if (rounds == 0) {
+        if (writes && warp == 0) draw(p, row, lane, z, w, stretch, pieces);
     } else {
-        u64 at = (u64)__dmul_rn((double)p.u_sample[row], (double)total);
-        at = at < total ? at : total - 1;
+        const u64 at = place(p.u_sample[row], total);
         u64 before = 0;
         for (int c = 0; c < rank; ++c) before += s.total[buf][c];
-        const u64 mine = s.total[buf][rank];
-        if (at >= before && at < before + mine) {
-            writes = true;
-            u64 t = at - before;
+        writes = at >= before && at < before + s.total[buf][rank];
+        if (writes) {
+            u64 r = at - before;
             int wi = 0;
-            while (wi < kWarps - 1 && t >= s.wsum[buf][wi]) t -= s.wsum[buf][wi++];
+            while (wi < kWarps - 1 && r >= s.wsum[buf][wi]) r -= s.wsum[buf][wi++];
             if (warp == wi) {
-                for (int v0 = lo; v0 < hi; v0 += 32) {
-                    const int v = v0 + lane, t0 = v * kPer - z.shift;
-                    u64 e[kPer / 2];
-                    Sum40 piece;
-                    if (v < hi) {
-                        Q q;
-                        if (kDraft && rounds) q = drafts(v);
-                        weights(z.piece(v), q, e);
-#pragma unroll
-                        for (int i = 0; i < kPer / 2; ++i) piece.add(e[i]);
-                    }
-                    const u64 x = piece.get();
-                    u64 incl = x;
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const u64 o = __shfl_up_sync(0xffffffffu, incl, d);
-                        if (lane >= d) incl += o;
-                    }
-                    const unsigned b = __ballot_sync(0xffffffffu, incl > t);
-                    if (b) {
-                        if (lane == __ffs(b) - 1) {
-                            u64 c = incl - x;
-                            int i = 0;
-#pragma unroll
-                            for (int k = 0; k < kPer - 1; ++k) {
-                                const float2 f = unpair(e[k / 2]);
-                                c += fixed40(k & 1 ? f.y : f.x);
-                                if (c <= t) i = k + 1;
-                            }
-                            tok = t0 + i;
-                        }
-                        break;
-                    }
-                    t -= __shfl_sync(0xffffffffu, incl, 31);
-                }
+                const int tok = find_token<kPer>(lo, hi, r, z.shift, lane,
+                                                 [&](int v, u64 (&e)[kPer / 2]) { weights(z.piece(v), drafts(v), e); });
+                if (tok >= 0) write_row(p, row, tok, z, w, whole);
             }
-        }
-    }
-    if (tok >= 0) {
-        p.row_tok[row] = tok;
-        if (p.row_logp) {
-            // (a NaN can only be an accepted child's)
-            const float x = __fmul_rn(fmaxf(z.token(tok), -INFINITY), inv_t);
-            p.row_logp[row] = __fsub_rn(x == m ? 0.f : __fsub_rn(x, m), logf(mass));
         }
     }
     if (writes) row_done(p);
@@ -586,8 +710,49 @@ __global__ void __launch_bounds__(kThreads, kHold ? 2 : kDraft ? 3 : 4) k_sample
 
 namespace w12i {
 
-// (a thread's own sums of whole numbers stay under 2^32 up to 4096 tokens of its own)
-int64_t sample_max_vocab() { return (int64_t)kThreads * 2048; }
+int64_t sample_max_vocab() { return kMaxVocab; }
+
+// pieces of a thread of the two passes: as many, of 1, 2 and 4, as leave every
+// SM eight CTAs (few rows spread over the SMs, many keep 16 KB in flight a CTA)
+static int pieces_per_thread(int64_t R, int64_t vocab, bool f32, int num_sms)
+{
+    const int64_t pieces = (vocab + (f32 ? 4 : 8) - 1) / (f32 ? 4 : 8) + 1;
+    int k = 4;
+    while (k > 1 && R * ((pieces + kChunkThreads * k - 1) / (kChunkThreads * k)) < 8ll * num_sms) k /= 2;
+    return k;
+}
+
+// chunks of a row, which may start inside a piece
+static int64_t chunk_count(int64_t vocab, bool f32, int k)
+{
+    const int64_t pieces = (vocab + (f32 ? 4 : 8) - 1) / (f32 ? 4 : 8) + 1;
+    return (pieces + kChunkThreads * k - 1) / (kChunkThreads * k);
+}
+
+template <bool kF32, int kP>
+static cudaError_t passes(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *pdl, const SampleParams &p, bool draft)
+{
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_sample_max<kF32, kP>, p);
+    if (e != cudaSuccess) return e;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return draft ? cudaLaunchKernelEx(&cfg, k_sample_sum<kF32, kP, true>, p) : cudaLaunchKernelEx(&cfg, k_sample_sum<kF32, kP, false>, p);
+}
+
+template <bool kF32>
+static cudaError_t passes_of(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *pdl, const SampleParams &p, int k, bool draft)
+{
+    return k == 4 ? passes<kF32, 4>(cfg, pdl, p, draft) : k == 2 ? passes<kF32, 2>(cfg, pdl, p, draft) : passes<kF32, 1>(cfg, pdl, p, draft);
+}
+
+static size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
+
+// arrival counts, maxima and sums; sized for the smallest chunks
+size_t sample_scratch_bytes(int32_t R, int64_t vocab)
+{
+    const size_t chunks = (size_t)chunk_count(vocab, true, 1);
+    return align16((size_t)R * 4) + align16((size_t)R * chunks * 4) + (size_t)R * chunks * kChunkWarps * 8;
+}
 
 int launch_sample(const SampleArgs &a, void *stream)
 {
@@ -614,40 +779,39 @@ int launch_sample(const SampleArgs &a, void *stream)
     p.p_max = a.p_max;
     p.done = a.done;
     p.status = a.status;
-    // CTAs of a row: up to 8 of 2048 tokens or more each, so that the waves of
-    // them, each as long as its stretch and some 16384 tokens' worth of barriers,
-    // take least (192 rows of 151936 tokens: 43 us with 8 CTAs to a row, three
-    // waves, and 36 us with 3, one wave).  With no more than two to an SM, half
-    // the registers of an SM hold the row between its two passes.
-    const int64_t slots = (a.draft_p ? 3ll : 4ll) * a.num_sms;
+    const int k = pieces_per_thread(a.R, a.vocab, a.f32 != 0, a.num_sms);
+    p.chunks = (int32_t)chunk_count(a.vocab, a.f32 != 0, k);
+    uint8_t *scratch = static_cast<uint8_t *>(a.scratch);
+    p.arrived = reinterpret_cast<int32_t *>(scratch);
+    p.top = reinterpret_cast<float *>(scratch + align16((size_t)a.R_max * 4));
+    p.sums = reinterpret_cast<u64 *>(scratch + align16((size_t)a.R_max * 4) + align16((size_t)a.R * p.chunks * 4));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.chunks, (unsigned)a.R);
+    cfg.blockDim = dim3(kChunkThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute pdl[1], both[2];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaError_t e = cudaSuccess;
+    const bool draft = a.draft_p != nullptr;
+    e = a.f32 ? passes_of<true>(cfg, pdl, p, k, draft) : passes_of<false>(cfg, pdl, p, k, draft);
+    if (e != cudaSuccess || !draft) return (int)e;
+    // a rejection's pass is one row's own, so a row gets all the CTAs a cluster
+    // can have, down to 2048 tokens each
     int c = 1;
-    int64_t best = INT64_MAX;
-    for (int i = 1; i <= kMaxCluster && (i == 1 || a.vocab > 2048 * (i - 1)); ++i) {
-        const int64_t t = ((int64_t)a.R * i + slots - 1) / slots * (a.vocab / i + 16384);
-        if (t < best) best = t, c = i;
-    }
-    const bool hold = (int64_t)a.R * c <= 2ll * a.num_sms;
+    while (c < kMaxCluster && a.vocab > 2048 * c) c *= 2;
     const int per = a.f32 ? 4 : 8;
     const int64_t pieces = (a.vocab + per - 1) / per + 1;         // one more where the row starts inside a piece
     p.sub = (int32_t)((pieces + (int64_t)c * kWarps - 1) / ((int64_t)c * kWarps));
-    cudaError_t e = cudaSuccess;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)c;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.R * c));
     cfg.blockDim = dim3(kThreads);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    auto go = [&](auto kernel) { e = cudaLaunchKernelEx(&cfg, kernel, p); };
-    auto pick = [&](auto f32, auto draft) {
-        if (hold) go(k_sample_rows<decltype(f32)::value, decltype(draft)::value, true>);
-        else go(k_sample_rows<decltype(f32)::value, decltype(draft)::value, false>);
-    };
-    if (a.f32) a.draft_p ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
-    else a.draft_p ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});
+    both[0] = pdl[0];
+    both[1].id = cudaLaunchAttributeClusterDimension;
+    both[1].val.clusterDim.x = (unsigned)c;
+    both[1].val.clusterDim.y = both[1].val.clusterDim.z = 1;
+    cfg.attrs = both;
+    cfg.numAttrs = 2;
+    e = a.f32 ? cudaLaunchKernelEx(&cfg, k_sample_draft<true>, p, 32 * k) : cudaLaunchKernelEx(&cfg, k_sample_draft<false>, p, 32 * k);
     return (int)e;
 }
 

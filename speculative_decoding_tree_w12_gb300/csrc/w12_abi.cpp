@@ -952,6 +952,7 @@ w12_status sample_entry(const w12_sampling *d, const w12_tree *tree, int32_t n_r
     if (n_req > kMaxBudget || p_max > kMaxDepth || d->vocab > sample_max_vocab()) return W12_E_UNSUPPORTED;
     const WsLayout L = layout_for(1, 0, 0, n_req);
     if ((s = ws_check(ws, ws_bytes, L)) != W12_OK) return s;
+    if (!d->scratch || !aligned(d->scratch, 16) || d->scratch_rows < tree->R) return W12_E_WORKSPACE;
     Ws W{static_cast<uint8_t *>(ws), L};
     SampleArgs a{};
     a.logits = d->logits;
@@ -964,6 +965,8 @@ w12_status sample_entry(const w12_sampling *d, const w12_tree *tree, int32_t n_r
     a.u_accept = d->u_accept;
     a.u_sample = d->u_sample;
     a.num_sms = num_sms();
+    a.scratch = d->scratch;
+    a.R_max = d->scratch_rows;
     a.R = tree->R;
     a.n_req = n_req;
     a.p_max = p_max;
@@ -1067,6 +1070,12 @@ w12_status w12_tree_attention(const w12_kv_cache *cache, const w12_rope *rope, c
 }
 
 int64_t w12_sample_max_vocab(void) { return sample_max_vocab(); }
+
+size_t w12_sample_scratch_bytes(int32_t R, int64_t vocab)
+{
+    if (R < 1 || R > kMaxBudget || vocab < 1 || vocab > sample_max_vocab()) return 0;
+    return sample_scratch_bytes(R, vocab);
+}
 
 w12_status w12_tree_sample(const w12_sampling *dist, const w12_tree *tree, int32_t n_req, int32_t *row_tok,
                            float *row_logp, void *ws, size_t ws_bytes, w12_stream_t stream)

@@ -227,6 +227,8 @@ struct SampleArgs {
     int64_t draft_stride;
     const float *u_accept, *u_sample;
     int num_sms;
+    void *scratch;                  // sample_scratch_bytes(R_max, vocab), zeroed once
+    int32_t R_max;
     int32_t R, n_req, p_max;
     const int32_t *parent, *token, *req, *off;
     int32_t *row_tok;
@@ -235,6 +237,7 @@ struct SampleArgs {
     int32_t *done, *status;         // a counter that is zero between calls
 };
 int64_t sample_max_vocab();
+size_t sample_scratch_bytes(int32_t R, int64_t vocab);
 int launch_sample(const SampleArgs &a, void *stream);
 
 int launch_tree_accept(const int32_t *parent, const int32_t *token, const uint8_t *depth,
