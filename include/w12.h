@@ -590,7 +590,7 @@ typedef struct {
     int64_t draft_stride;
     const float *u_accept;       /* device [R] in [0, 1): decides on row j as a draft (needed with draft_p) */
     const float *u_sample;       /* device [R] in [0, 1): draws row i's own token */
-    void *scratch;               /* device, 16-byte aligned: w12_sample_scratch_bytes(scratch_rows, vocab) bytes, set to zero once */
+    void *scratch;               /* device, 16-byte aligned: w12_sample_scratch_bytes(scratch_rows, vocab) bytes */
     int32_t scratch_rows;        /* rows the scratch is sized for, at least the tree's; calls that share it run in order */
 } w12_sampling;
 

@@ -739,7 +739,7 @@ class SampleRows:
         nbytes = int(lib().w12_sample_scratch_bytes(R, V))
         if nbytes == 0:
             raise W12Error(W12_E_UNSUPPORTED, "w12_sample_scratch_bytes")
-        self.scratch = torch.zeros(nbytes, dtype=torch.uint8, device=logits.device)
+        self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=logits.device)
         self.c = SamplingC(logits.data_ptr(), int(logits.dtype == torch.float32), V, row(logits), _dp(temperature),
                            _dp(draft_p), row(draft_p) if draft_p is not None else 0, _dp(u_accept), _dp(u_sample),
                            self.scratch.data_ptr(), R)

@@ -20,8 +20,8 @@
 // to wait for the maxima) for the sums of the weights of every warp's stretch.
 // The CTA that completes a row finds the stretch its token lies in by these
 // sums, and goes through it once more in order.  With a drafter's probabilities
-// k_sample_draft takes over from there: a cluster to a row, which ends at once
-// where a child is accepted and goes over the row again for every rejection.
+// the rows whose first child was rejected are left to k_sample_draft: a cluster
+// to a row, which goes over it again for every rejection.
 // The CTA that completes the last row writes the accepted paths.
 // Many rows are bound by the issue rate of the sums' pass, some 15 instructions
 // a token, half of them expf; few rows by latency.
@@ -61,11 +61,20 @@ struct SampleParams {
     float *row_logp;
     int32_t *acc_tok, *acc_len, *acc_node;     // acc_tok null: rows only
     int32_t p_max;
-    int32_t *done, *status;                    // rows written so far
+    int32_t *status;
     // scratch
-    int32_t *arrived;                          // [R] chunks summed; zero between calls
+    int32_t *done, *n_left;                    // rows written, rows left to k_sample_draft
+    int32_t *arrived;                          // [R] chunks summed
     float *top;                                // [R][chunks] largest logit
+    struct Left *left;                         // [R]
     u64 *sums;                                 // [R][chunks][kChunkWarps] (greedy rows: lowest token with the largest logit)
+};
+
+// a row whose first child was rejected
+struct Left {
+    int32_t row;
+    float top;
+    u64 total;
 };
 
 // Sums of whole numbers floor(e 2^40), 0 <= e <= 1.  Adding 8 with rounding
@@ -234,8 +243,7 @@ __device__ void accept_path(const SampleParams &p, int r, int lane)
 }
 
 // After a CTA's thread has written the row's token: the CTA that writes the
-// last row's goes on to the accepted paths.  (The count goes back to zero for
-// the next launch.)
+// last row's goes on to the accepted paths.
 __device__ __forceinline__ void row_done(const SampleParams &p)
 {
     if (!p.acc_tok) return;
@@ -248,7 +256,6 @@ __device__ __forceinline__ void row_done(const SampleParams &p)
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    if (threadIdx.x == 0) *p.done = 0;
     for (int r = threadIdx.x >> 5; r < p.n_req; r += blockDim.x >> 5) accept_path(p, r, threadIdx.x & 31);
 }
 
@@ -390,14 +397,11 @@ __device__ __forceinline__ float row_top(const SampleParams &p, int row, int lan
 
 // A row without rejections, by one warp: its token by the sums of the chunks' stretches.
 template <bool kF32>
-__device__ void draw(const SampleParams &p, int row, int lane, const Row<kF32> &z, const Weigher<kF32> &w, int stretch, int pieces)
+__device__ void draw(const SampleParams &p, int row, int lane, const Row<kF32> &z, const Weigher<kF32> &w, int stretch, int pieces, u64 total)
 {
     constexpr int kPer = Row<kF32>::kPer;
     const u64 *sums = p.sums + (int64_t)row * p.chunks * kChunkWarps;
     const int n = p.chunks * kChunkWarps;
-    u64 total = 0;
-    for (int i = lane; i < n; i += 32) total += __ldcg(sums + i);
-    total = warp_sum(total);
     u64 t = place(p.u_sample[row], total);
     int at = -1;
     for (int i0 = 0; i0 < n && at < 0; i0 += 32) {
@@ -422,6 +426,24 @@ __device__ void draw(const SampleParams &p, int row, int lane, const Row<kF32> &
     if (tok >= 0) write_row(p, row, tok, z, w, total);
 }
 
+// The row's next child after row j, of those whose token is one.  One warp.
+__device__ __forceinline__ int next_child(const SampleParams &p, int row, int j, int lane)
+{
+    const int end = min(p.R, p.off[p.req[row] + 1]);
+    for (int j0 = j + 1; j0 < end; j0 += 32) {
+        const int k = j0 + lane;
+        const unsigned b = __ballot_sync(0xffffffffu, k < end && p.parent[k] == row && p.token[k] >= 0 && p.token[k] < p.vocab);
+        if (b) return j0 + __ffs(b) - 1;
+    }
+    return -1;
+}
+
+// u q < p with the child's weight a of the total's
+__device__ __forceinline__ bool accepted(const SampleParams &p, int kid, float q, float a, u64 total)
+{
+    return __fmul_rn(p.u_accept[kid], q) < __fmul_rn(a, __fdiv_rn(1.f, weight_of(total)));
+}
+
 // ---------------------------------------------------------------------------
 // the two passes
 // ---------------------------------------------------------------------------
@@ -436,6 +458,10 @@ __global__ void __launch_bounds__(kChunkThreads) k_sample_max(const SampleParams
     const Row<kF32> z(p.logits, row * p.stride, p.vocab);
     const int pieces = (z.shift + p.vocab + kPer - 1) / kPer;
     const int lo = (blockIdx.x * kChunkWarps + warp) * 32 * kP + lane;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.arrived[row] = 0;
+        if (row == 0) *p.done = *p.n_left = 0;
+    }
     pdl_launch_dependents();
     float m = -INFINITY;
     uint4 x[kP];
@@ -500,8 +526,7 @@ __global__ void __launch_bounds__(kChunkThreads) k_sample_sum(const SampleParams
         const u64 all = warp_sum(sum.get());
         if (lane == 0) *mine = all;
     }
-    if (kDraft) return;
-    // ---- the row's last CTA draws its token
+    // ---- the row's last CTA draws its token, or leaves it to k_sample_draft
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
@@ -510,20 +535,32 @@ __global__ void __launch_bounds__(kChunkThreads) k_sample_sum(const SampleParams
     __syncthreads();
     if (!s_last) return;
     __threadfence();
+    bool left = false;
     if (warp == 0) {
-        if (lane == 0) {
-            p.arrived[row] = 0;
-            if (!t.ok) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
-        }
+        if (!t.ok && lane == 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
         if (!(top > -INFINITY) || !t.ok) {      // nothing can be drawn from this row
             if (lane == 0) write_none(p, row);
         } else if (t.greedy) {
             draw_greedy(p, row, lane);
         } else {
-            draw(p, row, lane, z, w, 32 * kP, pieces);
+            u64 total = 0;
+            for (int i = lane; i < p.chunks * kChunkWarps; i += 32) total += __ldcg(p.sums + (int64_t)row * p.chunks * kChunkWarps + i);
+            total = warp_sum(total);
+            const int kid = kDraft ? next_child(p, row, row, lane) : -1;
+            if (kid < 0) {
+                draw(p, row, lane, z, w, 32 * kP, pieces, total);
+            } else if (lane == 0) {
+                const int x = p.token[kid];
+                if (accepted(p, kid, __ldg(p.draft_p + row * p.draft_stride + x), w.one(z.token(x)), total)) {
+                    write_row(p, row, x, z, w, total);
+                } else {
+                    p.left[atomicAdd(p.n_left, 1)] = {row, top, total};
+                    left = true;
+                }
+            }
         }
     }
-    row_done(p);
+    if (!kDraft || !__syncthreads_or(left)) row_done(p);
 }
 
 // ---------------------------------------------------------------------------
@@ -533,58 +570,22 @@ __global__ void __launch_bounds__(kChunkThreads) k_sample_sum(const SampleParams
 struct Shared {
     u64 total[2][kMaxCluster];                 // written by every CTA of the cluster
     u64 wsum[2][kWarps];
-    int32_t kids[kMaxBudget];
     float inv[kMaxBudget];                     // of the rejections so far
-    int32_t n_kids;
 };
 
-// stretch: pieces of a warp of k_sample_sum
 template <bool kF32>
-__global__ void __launch_bounds__(kThreads, 2) k_sample_draft(const SampleParams p, int stretch)
+__device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const cg::cluster_group &cl, const Left &job, int stretch)
 {
     constexpr int kPer = Row<kF32>::kPer;
-    __shared__ Shared s;
-    cg::cluster_group cl = cg::this_cluster();
-    cl.barrier_arrive();                        // waited for before the first write to another CTA
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-    const int row = blockIdx.x / C;
+    const int row = job.row;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Row<kF32> z(p.logits, row * p.stride, p.vocab);
     const int pieces = (z.shift + p.vocab + kPer - 1) / kPer;
     const int lo = min(pieces, (rank * kWarps + warp) * p.sub), hi = min(pieces, lo + p.sub);   // this warp's pieces, in order
     const float *qr = p.draft_p + row * p.draft_stride;
-    const Temper t = temper(p, row);
-    // children of the row, in row order
-    if (warp == 0) {
-        int cnt = 0;
-        const int end = t.ok ? min(p.R, p.off[p.req[row] + 1]) : 0;
-        for (int j0 = row + 1; j0 < end; j0 += 32) {
-            const bool kid = j0 + lane < end && p.parent[j0 + lane] == row;
-            const unsigned b = __ballot_sync(0xffffffffu, kid);
-            if (kid) s.kids[cnt + __popc(b & ((1u << lane) - 1u))] = j0 + lane;
-            cnt += __popc(b);
-        }
-        if (lane == 0) s.n_kids = cnt;
-    }
-    __syncthreads();
-    cl.barrier_wait();
-    pdl_wait();
-    const float top = row_top(p, row, lane);
-    if (!t.ok || !(top > -INFINITY) || t.greedy) {          // the same for the whole cluster
-        if (rank) return;
-        if (warp == 0) {
-            if (!t.ok && lane == 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
-            if (t.ok && top > -INFINITY) draw_greedy(p, row, lane);
-            else if (lane == 0) write_none(p, row);
-        }
-        row_done(p);
-        return;
-    }
-    const Weigher<kF32> w(t.inv_t, top);
-    u64 total = 0;
-    for (int i = lane; i < p.chunks * kChunkWarps; i += 32) total += __ldcg(p.sums + (int64_t)row * p.chunks * kChunkWarps + i);
-    total = warp_sum(total);
-    const u64 whole = total;
+    const Weigher<kF32> w(temper(p, row).inv_t, job.top);
+    u64 total = job.total;
     const bool q_even = ((reinterpret_cast<uintptr_t>(qr) - 4 * z.shift) & 15) == 0;   // its pieces lie on 16 bytes too
     int rounds = 0;
     struct Q {                                  // the drafter's probabilities of a piece, in pairs
@@ -639,19 +640,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_draft(const SampleParams
         return c;
     };
     int took = -1;
-    const int n_kids = s.n_kids;
-    for (int c = 0; c < n_kids; ++c) {
-        const int kid = s.kids[c], x = p.token[kid];
-        if (x < 0 || x >= p.vocab) continue;                       // not a token: it cannot be accepted
-        const float q = __ldg(qr + x), inv = __fdiv_rn(1.f, weight_of(total));
+    for (int kid = next_child(p, row, row, lane); kid >= 0; kid = next_child(p, row, kid, lane)) {
+        const int x = p.token[kid];
+        const float q = __ldg(qr + x);
         float a = w.one(z.token(x));
         for (int k = 0; k < rounds; ++k) a = fmaxf(__fsub_rn(__fmul_rn(a, s.inv[k]), q), 0.f);
-        if (__fmul_rn(p.u_accept[kid], q) < __fmul_rn(a, inv)) {
+        if (accepted(p, kid, q, a, total)) {
             took = kid;
             break;
         }
         __syncthreads();                                            // (everyone is done with the last entry)
-        if (tid == 0) s.inv[rounds] = inv;
+        if (tid == 0) s.inv[rounds] = __fdiv_rn(1.f, weight_of(total));
         __syncthreads();
         ++rounds;
         Sum40 left;
@@ -684,9 +683,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_draft(const SampleParams
     // ---- the row's token
     bool writes = rank == 0;                                        // this CTA has it
     if (took >= 0) {
-        if (writes && tid == 0) write_row(p, row, p.token[took], z, w, whole);
-    } else if (rounds == 0) {
-        if (writes && warp == 0) draw(p, row, lane, z, w, stretch, pieces);
+        if (writes && tid == 0) write_row(p, row, p.token[took], z, w, job.total);
+    } else if (rounds == 0) {                                       // p = q
+        if (writes && warp == 0) draw(p, row, lane, z, w, stretch, pieces, total);
     } else {
         const u64 at = place(p.u_sample[row], total);
         u64 before = 0;
@@ -699,11 +698,27 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_draft(const SampleParams
             if (warp == wi) {
                 const int tok = find_token<kPer>(lo, hi, r, z.shift, lane,
                                                  [&](int v, u64 (&e)[kPer / 2]) { weights(z.piece(v), drafts(v), e); });
-                if (tok >= 0) write_row(p, row, tok, z, w, whole);
+                if (tok >= 0) write_row(p, row, tok, z, w, job.total);
             }
         }
     }
     if (writes) row_done(p);
+}
+
+// stretch: pieces of a warp of k_sample_sum
+template <bool kF32>
+__global__ void __launch_bounds__(kThreads, 2) k_sample_draft(const SampleParams p, int stretch)
+{
+    __shared__ Shared s;
+    const cg::cluster_group cl = cg::this_cluster();
+    const int C = (int)cl.num_blocks();
+    pdl_wait();
+    const int n = __ldcg(p.n_left);
+    for (int i = blockIdx.x / C; i < n; i += gridDim.x / C) {       // the same for the whole cluster
+        cl.sync();                                                  // its CTAs have all started, and left the row before
+        const uint4 l = __ldcg(reinterpret_cast<const uint4 *>(p.left + i));
+        reject<kF32>(p, s, cl, {(int32_t)l.x, __uint_as_float(l.y), (u64)l.w << 32 | l.z}, stretch);
+    }
 }
 
 }  // namespace
@@ -747,11 +762,11 @@ static cudaError_t passes_of(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *pdl, 
 
 static size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 
-// arrival counts, maxima and sums; sized for the smallest chunks
+// the counts, the rows left over, the maxima and the sums
 size_t sample_scratch_bytes(int32_t R, int64_t vocab)
 {
     const size_t chunks = (size_t)chunk_count(vocab, true, 1);
-    return align16((size_t)R * 4) + align16((size_t)R * chunks * 4) + (size_t)R * chunks * kChunkWarps * 8;
+    return align16((size_t)(2 + R) * 4) + (size_t)R * sizeof(Left) + align16((size_t)R * chunks * 4) + (size_t)R * chunks * kChunkWarps * 8;
 }
 
 int launch_sample(const SampleArgs &a, void *stream)
@@ -777,14 +792,18 @@ int launch_sample(const SampleArgs &a, void *stream)
     p.acc_len = a.acc_len;
     p.acc_node = a.acc_node;
     p.p_max = a.p_max;
-    p.done = a.done;
     p.status = a.status;
     const int k = pieces_per_thread(a.R, a.vocab, a.f32 != 0, a.num_sms);
     p.chunks = (int32_t)chunk_count(a.vocab, a.f32 != 0, k);
     uint8_t *scratch = static_cast<uint8_t *>(a.scratch);
-    p.arrived = reinterpret_cast<int32_t *>(scratch);
-    p.top = reinterpret_cast<float *>(scratch + align16((size_t)a.R_max * 4));
-    p.sums = reinterpret_cast<u64 *>(scratch + align16((size_t)a.R_max * 4) + align16((size_t)a.R * p.chunks * 4));
+    p.done = reinterpret_cast<int32_t *>(scratch);
+    p.n_left = p.done + 1;
+    p.arrived = p.done + 2;
+    scratch += align16((size_t)(2 + a.R) * 4);
+    p.left = reinterpret_cast<Left *>(scratch);
+    scratch += (size_t)a.R * sizeof(Left);
+    p.top = reinterpret_cast<float *>(scratch);
+    p.sums = reinterpret_cast<u64 *>(scratch + align16((size_t)a.R * p.chunks * 4));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)p.chunks, (unsigned)a.R);
     cfg.blockDim = dim3(kChunkThreads);
@@ -803,7 +822,7 @@ int launch_sample(const SampleArgs &a, void *stream)
     const int per = a.f32 ? 4 : 8;
     const int64_t pieces = (a.vocab + per - 1) / per + 1;         // one more where the row starts inside a piece
     p.sub = (int32_t)((pieces + (int64_t)c * kWarps - 1) / ((int64_t)c * kWarps));
-    cfg.gridDim = dim3((unsigned)(a.R * c));
+    cfg.gridDim = dim3((unsigned)std::min(a.R * c, 2 * a.num_sms / c * c));
     cfg.blockDim = dim3(kThreads);
     both[0] = pdl[0];
     both[1].id = cudaLaunchAttributeClusterDimension;

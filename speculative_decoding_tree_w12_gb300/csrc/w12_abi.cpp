@@ -199,7 +199,7 @@ WsLayout layout_for(int32_t R, int64_t max_n, int64_t vocab, int32_t n_req)
     L.status = o;
     o += 256;
     L.arrive = o;
-    o += static_cast<size_t>(kMaxBudget + 64) * 4;
+    o += static_cast<size_t>(kMaxBudget) * 4;
     // the chain words end exactly where the counters start
     L.grid = o;
     o += static_cast<size_t>(kGridWords) * 4;
@@ -966,7 +966,6 @@ w12_status sample_entry(const w12_sampling *d, const w12_tree *tree, int32_t n_r
     a.u_sample = d->u_sample;
     a.num_sms = num_sms();
     a.scratch = d->scratch;
-    a.R_max = d->scratch_rows;
     a.R = tree->R;
     a.n_req = n_req;
     a.p_max = p_max;
@@ -979,7 +978,6 @@ w12_status sample_entry(const w12_sampling *d, const w12_tree *tree, int32_t n_r
     a.acc_tok = acc_tok;
     a.acc_len = acc_len;
     a.acc_node = acc_node;
-    a.done = W.arrive() + kMaxBudget;
     a.status = W.status();
     return cuda_status(launch_sample(a, stream));
 }

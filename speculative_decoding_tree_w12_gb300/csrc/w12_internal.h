@@ -26,7 +26,7 @@ constexpr int32_t kDevOk = 0;
 // Byte layout of the caller's workspace.  Every region is 256-byte aligned.
 struct WsLayout {
     size_t status;        // int32[64]: [0] status, [1] detail, [8] mismatch count (int64)
-    size_t arrive;        // int32[kMaxBudget + 64], zero between calls: arrivals per request (KV cache writer), rows done (sampling)
+    size_t arrive;        // int32[kMaxBudget], zero between calls: arrivals per request (KV cache writer)
     size_t grid;          // uint32[kGridWords]: [0] abort word of a GEMM chain, [1 + j] CTAs done with GEMM j
     size_t counters;      // int32[kGemmSlots][max_tiles_n]: split-tile arrival counters
     size_t partial;       // float[kGemmSlots][max_ctas][2][rows8][128]
@@ -227,14 +227,13 @@ struct SampleArgs {
     int64_t draft_stride;
     const float *u_accept, *u_sample;
     int num_sms;
-    void *scratch;                  // sample_scratch_bytes(R_max, vocab), zeroed once
-    int32_t R_max;
+    void *scratch;                  // sample_scratch_bytes(R, vocab)
     int32_t R, n_req, p_max;
     const int32_t *parent, *token, *req, *off;
     int32_t *row_tok;
     float *row_logp;
     int32_t *acc_tok, *acc_len, *acc_node;   // acc_tok null: rows only
-    int32_t *done, *status;         // a counter that is zero between calls
+    int32_t *status;
 };
 int64_t sample_max_vocab();
 size_t sample_scratch_bytes(int32_t R, int64_t vocab);
