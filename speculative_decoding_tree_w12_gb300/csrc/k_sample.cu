@@ -54,7 +54,7 @@ struct SampleParams {
     int64_t stride, draft_stride;
     const float *temperature, *draft_p, *u_accept, *u_sample;
     int32_t vocab, sub;                        // tokens; 16-byte pieces of the row of one warp of k_sample_draft
-    int32_t chunks;                            // of a row
+    int32_t chunks, per;                       // of a row; pieces of a thread of the two passes (a warp's stretch: 32 per)
     int32_t R, n_req;
     const int32_t *parent, *token, *req, *off;
     int32_t *row_tok;
@@ -180,7 +180,10 @@ struct Row {
         return kF32 ? __ldg(static_cast<const float *>(base) + shift + v)
                     : bf16_f32(__ldg(static_cast<const unsigned short *>(base) + shift + v));
     }
-    __device__ __forceinline__ uint4 piece(int v) const
+    // no token of pieces lo .. hi - 1 is outside the row
+    __device__ __forceinline__ bool inner(int lo, int hi) const { return lo * kPer >= shift && hi * kPer - shift <= vocab; }
+    __device__ __forceinline__ uint4 whole(int v) const { return __ldg(static_cast<const uint4 *>(base) + v); }
+    __device__ __forceinline__ uint4 piece(int v) const                  // -inf outside the row
     {
         const int t0 = v * kPer - shift;
         if (t0 >= 0 && t0 + kPer <= vocab) return __ldg(static_cast<const uint4 *>(base) + v);
@@ -197,6 +200,18 @@ struct Row {
             }
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // the lane's pieces of N * 32 from v0
+    template <int N>
+    __device__ __forceinline__ void load(int v0, int lane, uint4 (&x)[N]) const
+    {
+        if (inner(v0, v0 + N * 32)) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = whole(v0 + j * 32 + lane);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = piece(v0 + j * 32 + lane);
+        }
     }
     __device__ __forceinline__ static float get(const uint4 &x, int i)
     {
@@ -304,20 +319,25 @@ struct Weigher {
         if (m == INFINITY) return z == INFINITY ? 1.f : 0.f;            // nothing but the infinite ones counts
         return expf(fmaxf(__fsub_rn(z, m), -128.f));                    // (a NaN becomes a weight of nothing)
     }
-    // of a piece's tokens, in pairs
+    // of a piece's tokens, in pairs; kInf: there are infinite z
+    template <bool kInf = false>
     __device__ __forceinline__ void piece(const uint4 &x, u64 (&e)[kPer / 2]) const
     {
-        if (m == INFINITY) {
-#pragma unroll
-            for (int i = 0; i < kPer; i += 2) e[i / 2] = pair(one(Row<kF32>::get(x, i)), one(Row<kF32>::get(x, i + 1)));
-            return;
-        }
 #pragma unroll
         for (int i = 0; i < kPer; i += 2) {
+            if (kInf) {
+                e[i / 2] = pair(one(Row<kF32>::get(x, i)), one(Row<kF32>::get(x, i + 1)));
+                continue;
+            }
             const u64 z = mul2(pair(Row<kF32>::get(x, i), Row<kF32>::get(x, i + 1)), pair(inv_t, inv_t));
             const float2 d = unpair(add2(z, pair(-m, -m)));
             e[i / 2] = pair(expf(fmaxf(d.x, -128.f)), expf(fmaxf(d.y, -128.f)));
         }
+    }
+    __device__ __forceinline__ void any_piece(const uint4 &x, u64 (&e)[kPer / 2]) const
+    {
+        if (m == INFINITY) piece<true>(x, e);
+        else piece(x, e);
     }
 };
 
@@ -395,11 +415,12 @@ __device__ __forceinline__ float row_top(const SampleParams &p, int row, int lan
     return m;
 }
 
-// A row without rejections, by one warp: its token by the sums of the chunks' stretches.
+// A row without rejections, by one CTA: its token by the sums of the stretches.
 template <bool kF32>
-__device__ void draw(const SampleParams &p, int row, int lane, const Row<kF32> &z, const Weigher<kF32> &w, int stretch, int pieces, u64 total)
+__device__ void draw(const SampleParams &p, int row, const Row<kF32> &z, const Weigher<kF32> &w, u64 total, u64 *s_sum)
 {
     constexpr int kPer = Row<kF32>::kPer;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const u64 *sums = p.sums + (int64_t)row * p.chunks * kChunkWarps;
     const int n = p.chunks * kChunkWarps;
     u64 t = place(p.u_sample[row], total);
@@ -419,10 +440,30 @@ __device__ void draw(const SampleParams &p, int row, int lane, const Row<kF32> &
             t -= __shfl_sync(0xffffffffu, incl, 31);
         }
     }
-    const int lo = at * stretch;
-    const int tok = find_token<kPer>(lo, min(pieces, lo + stretch), t, z.shift, lane, [&](int v, u64 (&e)[kPer / 2]) {
-        w.piece(z.piece(v), e);
-    });
+    auto piece = [&](int v, u64 (&e)[kPer / 2]) { w.any_piece(z.piece(v), e); };
+    // every warp takes a part of the stretch
+    const int sub = (p.per + warps - 1) / warps * 32;
+    const int lo = at * 32 * p.per + warp * sub, hi = min((at + 1) * 32 * p.per, lo + sub);
+    bool mine = warp == 0;
+    if (p.per > 1) {
+        Sum40 sum;
+        for (int v = lo + lane; v < hi; v += 32) {
+            u64 e[kPer / 2];
+            piece(v, e);
+#pragma unroll
+            for (int i = 0; i < kPer / 2; ++i) sum.add(e[i]);
+        }
+        const u64 all = warp_sum(sum.get());
+        if (lane == 0) s_sum[warp] = all;
+        __syncthreads();
+        for (int i = 0; i < warp; ++i) {
+            if (t < s_sum[i]) return;
+            t -= s_sum[i];
+        }
+        mine = t < all;
+    }
+    if (!mine) return;
+    const int tok = find_token<kPer>(lo, hi, t, z.shift, lane, piece);
     if (tok >= 0) write_row(p, row, tok, z, w, total);
 }
 
@@ -448,31 +489,29 @@ __device__ __forceinline__ bool accepted(const SampleParams &p, int kid, float q
 // the two passes
 // ---------------------------------------------------------------------------
 
-// kP: pieces of a thread; a warp's stretch is 32 kP pieces
-template <bool kF32, int kP>
-__global__ void __launch_bounds__(kChunkThreads) k_sample_max(const SampleParams p)
+// N: pieces in flight of a thread, a divisor of per
+template <bool kF32, int N>
+__global__ void __launch_bounds__(kChunkThreads, 8) k_sample_max(const SampleParams p)
 {
     constexpr int kPer = Row<kF32>::kPer;
     __shared__ float s_top[kChunkWarps];
     const int row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Row<kF32> z(p.logits, row * p.stride, p.vocab);
-    const int pieces = (z.shift + p.vocab + kPer - 1) / kPer;
-    const int lo = (blockIdx.x * kChunkWarps + warp) * 32 * kP + lane;
+    const int lo = (blockIdx.x * kChunkWarps + warp) * 32 * p.per;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         p.arrived[row] = 0;
         if (row == 0) *p.done = *p.n_left = 0;
     }
     pdl_launch_dependents();
     float m = -INFINITY;
-    uint4 x[kP];
+    for (int k = 0; k < p.per; k += N) {
+        uint4 x[N];
+        z.load(lo + k * 32, lane, x);
 #pragma unroll
-    for (int k = 0; k < kP; ++k)
-        if (lo + k * 32 < pieces) x[k] = z.piece(lo + k * 32);
+        for (int j = 0; j < N; ++j)
 #pragma unroll
-    for (int k = 0; k < kP; ++k)
-        if (lo + k * 32 < pieces)
-#pragma unroll
-            for (int i = 0; i < kPer; i += 2) m = fmaxf(fmaxf(m, Row<kF32>::get(x[k], i)), Row<kF32>::get(x[k], i + 1));
+            for (int i = 0; i < kPer; i += 2) m = fmaxf(fmaxf(m, Row<kF32>::get(x[j], i)), Row<kF32>::get(x[j], i + 1));
+    }
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     if (lane == 0) s_top[warp] = m;
@@ -484,45 +523,53 @@ __global__ void __launch_bounds__(kChunkThreads) k_sample_max(const SampleParams
     }
 }
 
-template <bool kF32, int kP, bool kDraft>
-__global__ void __launch_bounds__(kChunkThreads) k_sample_sum(const SampleParams p)
+template <bool kF32, int N, bool kDraft>
+__global__ void __launch_bounds__(kChunkThreads, 5) k_sample_sum(const SampleParams p)
 {
     constexpr int kPer = Row<kF32>::kPer;
     __shared__ int32_t s_last;
+    __shared__ u64 s_sum[kChunkWarps];
     const int row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Row<kF32> z(p.logits, row * p.stride, p.vocab);
-    const int pieces = (z.shift + p.vocab + kPer - 1) / kPer;
-    const int lo = (blockIdx.x * kChunkWarps + warp) * 32 * kP + lane;
+    const int lo = (blockIdx.x * kChunkWarps + warp) * 32 * p.per;
     const Temper t = temper(p, row);
     if (kDraft) pdl_launch_dependents();
-    uint4 x[kP];
-#pragma unroll
-    for (int k = 0; k < kP; ++k)
-        if (lo + k * 32 < pieces) x[k] = z.piece(lo + k * 32);
+    uint4 x[N];
+    z.load(lo, lane, x);
     pdl_wait();
     const float top = row_top(p, row, lane);
     const Weigher<kF32> w(t.inv_t, top);
     u64 *mine = p.sums + ((int64_t)row * p.chunks + blockIdx.x) * kChunkWarps + warp;
     if (t.greedy) {                             // the largest logit, the lowest token of equals, whatever the draft
         int tok = INT32_MAX;
+        for (int k = 0;;) {
 #pragma unroll
-        for (int k = 0; k < kP; ++k)
-            if (lo + k * 32 < pieces)
+            for (int j = 0; j < N; ++j)
 #pragma unroll
                 for (int i = 0; i < kPer; ++i)
-                    if (Row<kF32>::get(x[k], i) == top) tok = min(tok, (lo + k * 32) * kPer - z.shift + i);
+                    if (Row<kF32>::get(x[j], i) == top) tok = min(tok, (lo + (k + j) * 32 + lane) * kPer - z.shift + i);
+            if ((k += N) >= p.per) break;
+            z.load(lo + k * 32, lane, x);
+        }
         tok = __reduce_min_sync(0xffffffffu, tok);
         if (lane == 0) *mine = (u64)tok;
     } else {
         Sum40 sum;
+        auto stretch = [&](auto inf) {
+            for (int k = 0;;) {
 #pragma unroll
-        for (int k = 0; k < kP; ++k)
-            if (lo + k * 32 < pieces) {
-                u64 e[kPer / 2];
-                w.piece(x[k], e);
+                for (int j = 0; j < N; ++j) {
+                    u64 e[kPer / 2];
+                    w.template piece<decltype(inf)::value>(x[j], e);
 #pragma unroll
-                for (int i = 0; i < kPer / 2; ++i) sum.add(e[i]);
+                    for (int i = 0; i < kPer / 2; ++i) sum.add(e[i]);
+                }
+                if ((k += N) >= p.per) break;
+                z.load(lo + k * 32, lane, x);
             }
+        };
+        if (w.m == INFINITY) stretch(std::true_type{});
+        else stretch(std::false_type{});
         const u64 all = warp_sum(sum.get());
         if (lane == 0) *mine = all;
     }
@@ -535,32 +582,29 @@ __global__ void __launch_bounds__(kChunkThreads) k_sample_sum(const SampleParams
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    bool left = false;
-    if (warp == 0) {
-        if (!t.ok && lane == 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
-        if (!(top > -INFINITY) || !t.ok) {      // nothing can be drawn from this row
-            if (lane == 0) write_none(p, row);
-        } else if (t.greedy) {
-            draw_greedy(p, row, lane);
+    const bool first = threadIdx.x == 0;
+    if (first && !t.ok) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
+    if (!(top > -INFINITY) || !t.ok) {          // nothing can be drawn from this row
+        if (first) write_none(p, row);
+    } else if (t.greedy) {
+        if (warp == 0) draw_greedy(p, row, lane);
+    } else {
+        u64 total = 0;
+        for (int i = lane; i < p.chunks * kChunkWarps; i += 32) total += __ldcg(p.sums + (int64_t)row * p.chunks * kChunkWarps + i);
+        total = warp_sum(total);
+        const int kid = kDraft ? next_child(p, row, row, lane) : -1;
+        if (kid < 0) {
+            draw(p, row, z, w, total, s_sum);
         } else {
-            u64 total = 0;
-            for (int i = lane; i < p.chunks * kChunkWarps; i += 32) total += __ldcg(p.sums + (int64_t)row * p.chunks * kChunkWarps + i);
-            total = warp_sum(total);
-            const int kid = kDraft ? next_child(p, row, row, lane) : -1;
-            if (kid < 0) {
-                draw(p, row, lane, z, w, 32 * kP, pieces, total);
-            } else if (lane == 0) {
-                const int x = p.token[kid];
-                if (accepted(p, kid, __ldg(p.draft_p + row * p.draft_stride + x), w.one(z.token(x)), total)) {
-                    write_row(p, row, x, z, w, total);
-                } else {
-                    p.left[atomicAdd(p.n_left, 1)] = {row, top, total};
-                    left = true;
-                }
+            const int c = p.token[kid];
+            if (!accepted(p, kid, __ldg(p.draft_p + row * p.draft_stride + c), w.one(z.token(c)), total)) {
+                if (first) p.left[atomicAdd(p.n_left, 1)] = {row, top, total};
+                return;
             }
+            if (first) write_row(p, row, c, z, w, total);
         }
     }
-    if (!kDraft || !__syncthreads_or(left)) row_done(p);
+    row_done(p);
 }
 
 // ---------------------------------------------------------------------------
@@ -574,15 +618,14 @@ struct Shared {
 };
 
 template <bool kF32>
-__device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const cg::cluster_group &cl, const Left &job, int stretch)
+__device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const cg::cluster_group &cl, const Left &job)
 {
     constexpr int kPer = Row<kF32>::kPer;
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int row = job.row;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Row<kF32> z(p.logits, row * p.stride, p.vocab);
-    const int pieces = (z.shift + p.vocab + kPer - 1) / kPer;
-    const int lo = min(pieces, (rank * kWarps + warp) * p.sub), hi = min(pieces, lo + p.sub);   // this warp's pieces, in order
+    const int lo = (rank * kWarps + warp) * p.sub, hi = lo + p.sub;   // this warp's pieces, in order
     const float *qr = p.draft_p + row * p.draft_stride;
     const Weigher<kF32> w(temper(p, row).inv_t, job.top);
     u64 total = job.total;
@@ -591,30 +634,31 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
     struct Q {                                  // the drafter's probabilities of a piece, in pairs
         u64 q[kPer / 2];
     };
+    auto whole_drafts = [&](int v) -> Q {
+        Q r;
+#pragma unroll
+        for (int i = 0; i < kPer; i += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(qr + v * kPer - z.shift + i));
+            r.q[i / 2] = pair(f.x, f.y);
+            r.q[i / 2 + 1] = pair(f.z, f.w);
+        }
+        return r;
+    };
     auto drafts = [&](int v) -> Q {
         Q r;
         const int t0 = v * kPer - z.shift;
-        if (q_even && t0 >= 0 && t0 + kPer <= p.vocab) {
 #pragma unroll
-            for (int i = 0; i < kPer; i += 4) {
-                const float4 f = __ldg(reinterpret_cast<const float4 *>(qr + t0 + i));
-                r.q[i / 2] = pair(f.x, f.y);
-                r.q[i / 2 + 1] = pair(f.z, f.w);
-            }
-        } else {
+        for (int i = 0; i < kPer; i += 2) {
+            float f[2];
 #pragma unroll
-            for (int i = 0; i < kPer; i += 2) {
-                float f[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) f[k] = t0 + i + k >= 0 && t0 + i + k < p.vocab ? __ldg(qr + t0 + i + k) : 2.f;
-                r.q[i / 2] = pair(f[0], f[1]);
-            }
+            for (int k = 0; k < 2; ++k) f[k] = t0 + i + k >= 0 && t0 + i + k < p.vocab ? __ldg(qr + t0 + i + k) : 2.f;
+            r.q[i / 2] = pair(f[0], f[1]);
         }
         return r;
     };
     // what is left of a piece's weights after the rejections so far, in pairs
     auto weights = [&](const uint4 &x, const Q &q, u64 (&e)[kPer / 2]) {
-        w.piece(x, e);
+        w.any_piece(x, e);
         for (int k = 0; k < rounds; ++k) {
             const u64 inv = pair(s.inv[k], s.inv[k]);
 #pragma unroll
@@ -654,21 +698,34 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
         __syncthreads();
         ++rounds;
         Sum40 left;
-        if (lo + lane < hi) {                                       // the next piece is on its way while one is summed
-            uint4 y = z.piece(lo + lane);
-            Q d = drafts(lo + lane);
-            for (int v = lo + lane; v < hi; v += 32) {
-                const uint4 y0 = y;
-                const Q d0 = d;
-                if (v + 32 < hi) {
-                    y = z.piece(v + 32);
-                    d = drafts(v + 32);
-                }
-                u64 e[kPer / 2];
-                weights(y0, d0, e);
+        constexpr int kBatch = kF32 ? 4 : 2;                        // pieces in flight of a thread
+        for (int v0 = lo; v0 < hi; v0 += 32 * kBatch) {
+            const int n = min(kBatch, (hi - v0) / 32);
+            uint4 y[kBatch];
+            Q d[kBatch];
+            if (q_even && z.inner(v0, v0 + n * 32)) {
 #pragma unroll
-                for (int i = 0; i < kPer / 2; ++i) left.add(e[i]);
+                for (int j = 0; j < kBatch; ++j)
+                    if (j < n) {
+                        y[j] = z.whole(v0 + j * 32 + lane);
+                        d[j] = whole_drafts(v0 + j * 32 + lane);
+                    }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    if (j < n) {
+                        y[j] = z.piece(v0 + j * 32 + lane);
+                        d[j] = drafts(v0 + j * 32 + lane);
+                    }
             }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (j < n) {
+                    u64 e[kPer / 2];
+                    weights(y[j], d[j], e);
+#pragma unroll
+                    for (int i = 0; i < kPer / 2; ++i) left.add(e[i]);
+                }
         }
         buf ^= 1;
         const u64 r = totals(left.get());
@@ -685,7 +742,7 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
     if (took >= 0) {
         if (writes && tid == 0) write_row(p, row, p.token[took], z, w, job.total);
     } else if (rounds == 0) {                                       // p = q
-        if (writes && warp == 0) draw(p, row, lane, z, w, stretch, pieces, total);
+        if (writes) draw(p, row, z, w, total, s.wsum[buf]);
     } else {
         const u64 at = place(p.u_sample[row], total);
         u64 before = 0;
@@ -705,9 +762,8 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
     if (writes) row_done(p);
 }
 
-// stretch: pieces of a warp of k_sample_sum
 template <bool kF32>
-__global__ void __launch_bounds__(kThreads, 2) k_sample_draft(const SampleParams p, int stretch)
+__global__ void __launch_bounds__(kThreads, 2) k_sample_draft(const SampleParams p)
 {
     __shared__ Shared s;
     const cg::cluster_group cl = cg::this_cluster();
@@ -717,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_draft(const SampleParams
     for (int i = blockIdx.x / C; i < n; i += gridDim.x / C) {       // the same for the whole cluster
         cl.sync();                                                  // its CTAs have all started, and left the row before
         const uint4 l = __ldcg(reinterpret_cast<const uint4 *>(p.left + i));
-        reject<kF32>(p, s, cl, {(int32_t)l.x, __uint_as_float(l.y), (u64)l.w << 32 | l.z}, stretch);
+        reject<kF32>(p, s, cl, {(int32_t)l.x, __uint_as_float(l.y), (u64)l.w << 32 | l.z});
     }
 }
 
@@ -727,37 +783,37 @@ namespace w12i {
 
 int64_t sample_max_vocab() { return kMaxVocab; }
 
-// pieces of a thread of the two passes: as many, of 1, 2 and 4, as leave every
-// SM eight CTAs (few rows spread over the SMs, many keep 16 KB in flight a CTA)
+static int64_t pieces_of(int64_t vocab, bool f32) { return (vocab + (f32 ? 4 : 8) - 1) / (f32 ? 4 : 8) + 1; }   // (a row may start inside one)
+
+static int64_t chunk_count(int64_t vocab, bool f32, int per)
+{
+    return (pieces_of(vocab, f32) + kChunkThreads * per - 1) / (kChunkThreads * per);
+}
+
+// Pieces of a thread of the two passes: the most, of powers of two up to 16,
+// that leave every SM eight CTAs.  Few rows are spread over the SMs; many get
+// long stretches, over which a warp's sums and searches weigh less.
 static int pieces_per_thread(int64_t R, int64_t vocab, bool f32, int num_sms)
 {
-    const int64_t pieces = (vocab + (f32 ? 4 : 8) - 1) / (f32 ? 4 : 8) + 1;
-    int k = 4;
-    while (k > 1 && R * ((pieces + kChunkThreads * k - 1) / (kChunkThreads * k)) < 8ll * num_sms) k /= 2;
-    return k;
+    int per = 16;
+    while (per > 1 && R * chunk_count(vocab, f32, per) < 8ll * num_sms) per /= 2;
+    return per;
 }
 
-// chunks of a row, which may start inside a piece
-static int64_t chunk_count(int64_t vocab, bool f32, int k)
-{
-    const int64_t pieces = (vocab + (f32 ? 4 : 8) - 1) / (f32 ? 4 : 8) + 1;
-    return (pieces + kChunkThreads * k - 1) / (kChunkThreads * k);
-}
-
-template <bool kF32, int kP>
+template <bool kF32, int N>
 static cudaError_t passes(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *pdl, const SampleParams &p, bool draft)
 {
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_sample_max<kF32, kP>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_sample_max<kF32, N>, p);
     if (e != cudaSuccess) return e;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return draft ? cudaLaunchKernelEx(&cfg, k_sample_sum<kF32, kP, true>, p) : cudaLaunchKernelEx(&cfg, k_sample_sum<kF32, kP, false>, p);
+    return draft ? cudaLaunchKernelEx(&cfg, k_sample_sum<kF32, N, true>, p) : cudaLaunchKernelEx(&cfg, k_sample_sum<kF32, N, false>, p);
 }
 
 template <bool kF32>
-static cudaError_t passes_of(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *pdl, const SampleParams &p, int k, bool draft)
+static cudaError_t passes_of(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *pdl, const SampleParams &p, bool draft)
 {
-    return k == 4 ? passes<kF32, 4>(cfg, pdl, p, draft) : k == 2 ? passes<kF32, 2>(cfg, pdl, p, draft) : passes<kF32, 1>(cfg, pdl, p, draft);
+    return p.per >= 4 ? passes<kF32, 4>(cfg, pdl, p, draft) : p.per == 2 ? passes<kF32, 2>(cfg, pdl, p, draft) : passes<kF32, 1>(cfg, pdl, p, draft);
 }
 
 static size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
@@ -793,8 +849,8 @@ int launch_sample(const SampleArgs &a, void *stream)
     p.acc_node = a.acc_node;
     p.p_max = a.p_max;
     p.status = a.status;
-    const int k = pieces_per_thread(a.R, a.vocab, a.f32 != 0, a.num_sms);
-    p.chunks = (int32_t)chunk_count(a.vocab, a.f32 != 0, k);
+    p.per = pieces_per_thread(a.R, a.vocab, a.f32 != 0, a.num_sms);
+    p.chunks = (int32_t)chunk_count(a.vocab, a.f32 != 0, p.per);
     uint8_t *scratch = static_cast<uint8_t *>(a.scratch);
     p.done = reinterpret_cast<int32_t *>(scratch);
     p.n_left = p.done + 1;
@@ -811,17 +867,14 @@ int launch_sample(const SampleArgs &a, void *stream)
     cudaLaunchAttribute pdl[1], both[2];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaError_t e = cudaSuccess;
     const bool draft = a.draft_p != nullptr;
-    e = a.f32 ? passes_of<true>(cfg, pdl, p, k, draft) : passes_of<false>(cfg, pdl, p, k, draft);
+    const cudaError_t e = a.f32 ? passes_of<true>(cfg, pdl, p, draft) : passes_of<false>(cfg, pdl, p, draft);
     if (e != cudaSuccess || !draft) return (int)e;
     // a rejection's pass is one row's own, so a row gets all the CTAs a cluster
     // can have, down to 2048 tokens each
     int c = 1;
     while (c < kMaxCluster && a.vocab > 2048 * c) c *= 2;
-    const int per = a.f32 ? 4 : 8;
-    const int64_t pieces = (a.vocab + per - 1) / per + 1;         // one more where the row starts inside a piece
-    p.sub = (int32_t)((pieces + (int64_t)c * kWarps - 1) / ((int64_t)c * kWarps));
+    p.sub = (int32_t)((pieces_of(a.vocab, a.f32 != 0) + 32ll * c * kWarps - 1) / (32ll * c * kWarps) * 32);
     cfg.gridDim = dim3((unsigned)std::min(a.R * c, 2 * a.num_sms / c * c));
     cfg.blockDim = dim3(kThreads);
     both[0] = pdl[0];
@@ -830,8 +883,7 @@ int launch_sample(const SampleArgs &a, void *stream)
     both[1].val.clusterDim.y = both[1].val.clusterDim.z = 1;
     cfg.attrs = both;
     cfg.numAttrs = 2;
-    e = a.f32 ? cudaLaunchKernelEx(&cfg, k_sample_draft<true>, p, 32 * k) : cudaLaunchKernelEx(&cfg, k_sample_draft<false>, p, 32 * k);
-    return (int)e;
+    return (int)(a.f32 ? cudaLaunchKernelEx(&cfg, k_sample_draft<true>, p) : cudaLaunchKernelEx(&cfg, k_sample_draft<false>, p));
 }
 
 }  // namespace w12i
