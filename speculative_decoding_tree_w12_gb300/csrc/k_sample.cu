@@ -63,7 +63,7 @@ struct SampleParams {
     int32_t p_max;
     int32_t *status;
     // scratch
-    int32_t *done, *n_left;                    // rows written, rows left to k_sample_draft
+    int32_t *done, *n_left, *taken;            // rows written, left to k_sample_draft, taken there behind every cluster's first
     int32_t *arrived;                          // [R] chunks summed
     float *top;                                // [R][chunks] largest logit
     struct Left *left;                         // [R]
@@ -415,37 +415,18 @@ __device__ __forceinline__ float row_top(const SampleParams &p, int row, int lan
     return m;
 }
 
-// A row without rejections, by one CTA: its token by the sums of the stretches.
-template <bool kF32>
-__device__ void draw(const SampleParams &p, int row, const Row<kF32> &z, const Weigher<kF32> &w, u64 total, u64 *s_sum)
+// The row's token, by one CTA: where the weights of the stretch of 32 n pieces
+// from `first` sum to more than t.  Every warp takes a part of the stretch.
+template <bool kF32, class Piece>
+__device__ __forceinline__ void search(const SampleParams &p, int row, int first, int n, u64 t, const Row<kF32> &z, const Weigher<kF32> &w,
+                                       u64 total, u64 *s_sum, Piece piece)
 {
     constexpr int kPer = Row<kF32>::kPer;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const u64 *sums = p.sums + (int64_t)row * p.chunks * kChunkWarps;
-    const int n = p.chunks * kChunkWarps;
-    u64 t = place(p.u_sample[row], total);
-    int at = -1;
-    for (int i0 = 0; i0 < n && at < 0; i0 += 32) {
-        u64 incl = i0 + lane < n ? __ldcg(sums + i0 + lane) : 0ull;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const u64 o = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += o;
-        }
-        const unsigned b = __ballot_sync(0xffffffffu, incl > t);
-        if (b) {
-            at = i0 + __ffs(b) - 1;
-            t -= __ffs(b) > 1 ? __shfl_sync(0xffffffffu, incl, __ffs(b) - 2) : 0ull;
-        } else {
-            t -= __shfl_sync(0xffffffffu, incl, 31);
-        }
-    }
-    auto piece = [&](int v, u64 (&e)[kPer / 2]) { w.any_piece(z.piece(v), e); };
-    // every warp takes a part of the stretch
-    const int sub = (p.per + warps - 1) / warps * 32;
-    const int lo = at * 32 * p.per + warp * sub, hi = min((at + 1) * 32 * p.per, lo + sub);
+    const int sub = (n + warps - 1) / warps * 32;
+    const int lo = first + warp * sub, hi = min(first + 32 * n, lo + sub);
     bool mine = warp == 0;
-    if (p.per > 1) {
+    if (n > 1) {
         Sum40 sum;
         for (int v = lo + lane; v < hi; v += 32) {
             u64 e[kPer / 2];
@@ -467,6 +448,34 @@ __device__ void draw(const SampleParams &p, int row, const Row<kF32> &z, const W
     if (tok >= 0) write_row(p, row, tok, z, w, total);
 }
 
+// A row without rejections, by one CTA: its token by the sums of the stretches.
+template <bool kF32>
+__device__ void draw(const SampleParams &p, int row, const Row<kF32> &z, const Weigher<kF32> &w, u64 total, u64 *s_sum)
+{
+    constexpr int kPer = Row<kF32>::kPer;
+    const int lane = threadIdx.x & 31;
+    const u64 *sums = p.sums + (int64_t)row * p.chunks * kChunkWarps;
+    const int n = p.chunks * kChunkWarps;
+    u64 t = place(p.u_sample[row], total);
+    int at = -1;
+    for (int i0 = 0; i0 < n && at < 0; i0 += 32) {
+        u64 incl = i0 + lane < n ? __ldcg(sums + i0 + lane) : 0ull;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const u64 o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        const unsigned b = __ballot_sync(0xffffffffu, incl > t);
+        if (b) {
+            at = i0 + __ffs(b) - 1;
+            t -= __ffs(b) > 1 ? __shfl_sync(0xffffffffu, incl, __ffs(b) - 2) : 0ull;
+        } else {
+            t -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    search(p, row, at * 32 * p.per, p.per, t, z, w, total, s_sum, [&](int v, u64 (&e)[kPer / 2]) { w.any_piece(z.piece(v), e); });
+}
+
 // The row's next child after row j, of those whose token is one.  One warp.
 __device__ __forceinline__ int next_child(const SampleParams &p, int row, int j, int lane)
 {
@@ -480,9 +489,9 @@ __device__ __forceinline__ int next_child(const SampleParams &p, int row, int j,
 }
 
 // u q < p with the child's weight a of the total's
-__device__ __forceinline__ bool accepted(const SampleParams &p, int kid, float q, float a, u64 total)
+__device__ __forceinline__ bool accepted(float u, float q, float a, u64 total)
 {
-    return __fmul_rn(p.u_accept[kid], q) < __fmul_rn(a, __fdiv_rn(1.f, weight_of(total)));
+    return __fmul_rn(u, q) < __fmul_rn(a, __fdiv_rn(1.f, weight_of(total)));
 }
 
 // ---------------------------------------------------------------------------
@@ -500,7 +509,7 @@ __global__ void __launch_bounds__(kChunkThreads, 8) k_sample_max(const SamplePar
     const int lo = (blockIdx.x * kChunkWarps + warp) * 32 * p.per;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         p.arrived[row] = 0;
-        if (row == 0) *p.done = *p.n_left = 0;
+        if (row == 0) *p.done = *p.n_left = *p.taken = 0;
     }
     pdl_launch_dependents();
     float m = -INFINITY;
@@ -597,7 +606,7 @@ __global__ void __launch_bounds__(kChunkThreads, 5) k_sample_sum(const SamplePar
             draw(p, row, z, w, total, s_sum);
         } else {
             const int c = p.token[kid];
-            if (!accepted(p, kid, __ldg(p.draft_p + row * p.draft_stride + c), w.one(z.token(c)), total)) {
+            if (!accepted(p.u_accept[kid], __ldg(p.draft_p + row * p.draft_stride + c), w.one(z.token(c)), total)) {
                 if (first) p.left[atomicAdd(p.n_left, 1)] = {row, top, total};
                 return;
             }
@@ -615,6 +624,12 @@ struct Shared {
     u64 total[2][kMaxCluster];                 // written by every CTA of the cluster
     u64 wsum[2][kWarps];
     float inv[kMaxBudget];                     // of the rejections so far
+    struct {
+        int32_t row;
+        float u, q, e;                         // its number, the drafter's probability, the weight
+    } kid[kMaxBudget];                         // children, in row order
+    int32_t n_kids;
+    int32_t next;                              // row, of those left over; written by the cluster's first CTA
 };
 
 template <bool kF32>
@@ -629,6 +644,19 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
     const float *qr = p.draft_p + row * p.draft_stride;
     const Weigher<kF32> w(temper(p, row).inv_t, job.top);
     u64 total = job.total;
+    if (warp == 0) {
+        int n = 0;
+        const int end = min(p.R, p.off[p.req[row] + 1]);
+        for (int j0 = row + 1; j0 < end; j0 += 32) {
+            const int j = j0 + lane, x = j < end && p.parent[j] == row ? p.token[j] : -1;
+            const bool is = x >= 0 && x < p.vocab;                  // (what is no token cannot be accepted)
+            const unsigned b = __ballot_sync(0xffffffffu, is);
+            if (is) s.kid[n + __popc(b & ((1u << lane) - 1u))] = {j, p.u_accept[j], __ldg(qr + x), w.one(z.token(x))};
+            n += __popc(b);
+        }
+        if (lane == 0) s.n_kids = n;
+    }
+    __syncthreads();
     const bool q_even = ((reinterpret_cast<uintptr_t>(qr) - 4 * z.shift) & 15) == 0;   // its pieces lie on 16 bytes too
     int rounds = 0;
     struct Q {                                  // the drafter's probabilities of a piece, in pairs
@@ -684,13 +712,13 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
         return c;
     };
     int took = -1;
-    for (int kid = next_child(p, row, row, lane); kid >= 0; kid = next_child(p, row, kid, lane)) {
-        const int x = p.token[kid];
-        const float q = __ldg(qr + x);
-        float a = w.one(z.token(x));
-        for (int k = 0; k < rounds; ++k) a = fmaxf(__fsub_rn(__fmul_rn(a, s.inv[k]), q), 0.f);
-        if (accepted(p, kid, q, a, total)) {
-            took = kid;
+    const int n_kids = s.n_kids;
+    for (int c = 0; c < n_kids; ++c) {
+        const auto kid = s.kid[c];
+        float a = kid.e;
+        for (int k = 0; k < rounds; ++k) a = fmaxf(__fsub_rn(__fmul_rn(a, s.inv[k]), kid.q), 0.f);
+        if (accepted(kid.u, kid.q, a, total)) {
+            took = kid.row;
             break;
         }
         __syncthreads();                                            // (everyone is done with the last entry)
@@ -742,7 +770,7 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
     if (took >= 0) {
         if (writes && tid == 0) write_row(p, row, p.token[took], z, w, job.total);
     } else if (rounds == 0) {                                       // p = q
-        if (writes) draw(p, row, z, w, total, s.wsum[buf]);
+        if (writes) draw(p, row, z, w, total, s.wsum[buf ^ 1]);
     } else {
         const u64 at = place(p.u_sample[row], total);
         u64 before = 0;
@@ -752,11 +780,8 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
             u64 r = at - before;
             int wi = 0;
             while (wi < kWarps - 1 && r >= s.wsum[buf][wi]) r -= s.wsum[buf][wi++];
-            if (warp == wi) {
-                const int tok = find_token<kPer>(lo, hi, r, z.shift, lane,
-                                                 [&](int v, u64 (&e)[kPer / 2]) { weights(z.piece(v), drafts(v), e); });
-                if (tok >= 0) write_row(p, row, tok, z, w, job.total);
-            }
+            search(p, row, (rank * kWarps + wi) * p.sub, p.sub / 32, r, z, w, job.total, s.wsum[buf ^ 1],
+                   [&](int v, u64 (&e)[kPer / 2]) { weights(z.piece(v), drafts(v), e); });
         }
     }
     if (writes) row_done(p);
@@ -770,10 +795,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_draft(const SampleParams
     const int C = (int)cl.num_blocks();
     pdl_wait();
     const int n = __ldcg(p.n_left);
-    for (int i = blockIdx.x / C; i < n; i += gridDim.x / C) {       // the same for the whole cluster
-        cl.sync();                                                  // its CTAs have all started, and left the row before
+    const int clusters = gridDim.x / C;
+    cl.sync();                                                      // its CTAs have all started
+    for (int i = blockIdx.x / C; i < n; i = s.next) {               // the same for the whole cluster
         const uint4 l = __ldcg(reinterpret_cast<const uint4 *>(p.left + i));
         reject<kF32>(p, s, cl, {(int32_t)l.x, __uint_as_float(l.y), (u64)l.w << 32 | l.z});
+        cl.sync();                                                  // (they have all read the last one)
+        if (cl.block_rank() == 0 && threadIdx.x < 32) {
+            int next = threadIdx.x == 0 ? clusters + atomicAdd(p.taken, 1) : 0;
+            next = __shfl_sync(0xffffffffu, next, 0);
+            if (threadIdx.x < C) *cl.map_shared_rank(&s.next, threadIdx.x) = next;
+        }
+        cl.sync();
     }
 }
 
@@ -822,7 +855,7 @@ static size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 size_t sample_scratch_bytes(int32_t R, int64_t vocab)
 {
     const size_t chunks = (size_t)chunk_count(vocab, true, 1);
-    return align16((size_t)(2 + R) * 4) + (size_t)R * sizeof(Left) + align16((size_t)R * chunks * 4) + (size_t)R * chunks * kChunkWarps * 8;
+    return align16((size_t)(3 + R) * 4) + (size_t)R * sizeof(Left) + align16((size_t)R * chunks * 4) + (size_t)R * chunks * kChunkWarps * 8;
 }
 
 int launch_sample(const SampleArgs &a, void *stream)
@@ -854,8 +887,9 @@ int launch_sample(const SampleArgs &a, void *stream)
     uint8_t *scratch = static_cast<uint8_t *>(a.scratch);
     p.done = reinterpret_cast<int32_t *>(scratch);
     p.n_left = p.done + 1;
-    p.arrived = p.done + 2;
-    scratch += align16((size_t)(2 + a.R) * 4);
+    p.taken = p.done + 2;
+    p.arrived = p.done + 3;
+    scratch += align16((size_t)(3 + a.R) * 4);
     p.left = reinterpret_cast<Left *>(scratch);
     scratch += (size_t)a.R * sizeof(Left);
     p.top = reinterpret_cast<float *>(scratch);
@@ -883,6 +917,10 @@ int launch_sample(const SampleArgs &a, void *stream)
     both[1].val.clusterDim.y = both[1].val.clusterDim.z = 1;
     cfg.attrs = both;
     cfg.numAttrs = 2;
+    // (clusters of more than 8 are for the kernel to allow)
+    static const cudaError_t wide[2] = {cudaFuncSetAttribute(k_sample_draft<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
+                                        cudaFuncSetAttribute(k_sample_draft<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)};
+    if (wide[a.f32 != 0] != cudaSuccess) return (int)wide[a.f32 != 0];
     return (int)(a.f32 ? cudaLaunchKernelEx(&cfg, k_sample_draft<true>, p) : cudaLaunchKernelEx(&cfg, k_sample_draft<false>, p));
 }
 
