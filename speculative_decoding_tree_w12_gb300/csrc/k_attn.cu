@@ -29,8 +29,8 @@
 //   O^T = V^T P  kind::f16: V's codes widened to F16 (exact) by warpgroups of
 //                their own, into tensor memory (through shared memory they
 //                would cost four times the bandwidth, which bounds the tile);
-//                P in F16, eleven significant bits, scaled so that there are
-//                2^-18 below a weight of 1 before the subnormals.
+//                P in F16, eleven significant bits down to 2^-15 of the
+//                largest weight there was when its reference was set.
 // Two groups of two softmax warpgroups take alternate tiles, each with its own
 // scores, P, maxima and sums, so that the latencies of one tile's chain
 // (product, reads, exponentials, vote, product) hide behind the other's; the
@@ -43,7 +43,9 @@
 // The maximum is lazy: P refers to a column maximum that is only raised when a
 // score passes it by 2^6 (P stays under F16's top), so the usual tile has no
 // reduction over lanes at all; the same slow path raises the reference of the
-// value scales, which P carries.
+// value scales, which P carries.  A raise costs several tiles, so a reference
+// is set 2^3 above the maximum: with normally distributed scores that leaves
+// next to none but the first.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -75,6 +77,7 @@ constexpr int kThreads = 128 + kSoft + 256; // warps: 0 K copies, 1 scores, 2 V 
 constexpr int kRegsLaunch = 72, kRegsSoft = 88, kRegsOther = 48;
 static_assert(kSoft * kRegsSoft + (kThreads - kSoft) * kRegsOther <= kThreads * kRegsLaunch, "register shares");
 constexpr float kHead = 16.f;              // P of a weight of 1 under the reference scale
+constexpr float kMargin = 6.f;             // a reference is set this (log2) above the largest score there was
 constexpr float kRaise = 6.f;              // a score may pass the column's reference by this (log2) before it is raised
 constexpr float kCap = 8.f;                // scores are held under this until then
 constexpr float kScaleRaise = 16.f;        // ... and a value scale its reference by this factor: 16 * 2^6 * 16 < 2^15
@@ -827,8 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (tok < steps * 8) {
                         const int n = n0 + tok;
                         float m = max_nan(max_nan(s.red[grp][0][n], s.red[grp][1][n]), max_nan(s.red[grp][2][n], s.red[grp][3][n]));
-                        if (!fresh) m = max_nan(m, 0.f);
-                        if (m == -INFINITY) m = 0.f;
+                        if (!fresh && m <= kRaise) m = 0.f;
+                        else m = m == -INFINITY ? 0.f : m + kMargin;
                         s.delta[grp][n] = ex2(-m);
                         s.mneg[grp][n] -= m;
                     }
