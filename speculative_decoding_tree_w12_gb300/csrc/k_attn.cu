@@ -11,7 +11,10 @@
 // k_attn_ctx: the cached context.  The work is a list of tiles of 128 tokens
 // (request, key/value head, group of rows; tokens innermost), cut into equal
 // consecutive shares, one per CTA and one CTA per SM, so a long context of one
-// request and many short ones balance alike.  A share leaves, for every
+// request and many short ones balance alike.  Starting and ending a segment
+// costs as much as a handful of tiles, so every segment has a lead of as many
+// empty ones in the list (kLead; 256 rows of 32 requests: the slowest CTA was
+// 23% over the mean without).  A share leaves, for every
 // segment (request, head, group) that it meets, FP32 sums with their maximum
 // and normaliser; k_attn_join merges them with the root path's.
 //
@@ -94,7 +97,7 @@ struct AttnParams {
     RopeArgs rope;
     float scale2;                           // softmax scale * log2(e)
     uint16_t *out;
-    int32_t *plan;                          // [n_req + 1] first tile of every request
+    int32_t *plan;                          // [n_req + 1] first tile of every request in the list; tiles of a lead
     float *part;                            // [R * Hq + ctas * cols][kD] sums
     float2 *ml;                             // [R * Hq + ctas * cols] maximum (log2), normaliser
     int32_t *status;
@@ -225,6 +228,7 @@ struct Shape {
 };
 
 constexpr int kMaxStages = 6;
+constexpr int kLead = 8;                                     // a segment's start and end in tiles: 6 to 7 of 16 columns, 10 of 48 and 80
 
 struct Shared {
     uint64_t k_full[kMaxStages], k_empty[kMaxStages];  // K and V tiles loaded / consumed
@@ -233,7 +237,9 @@ struct Shared {
     uint64_t p_full[2], v16_full[2], pv_done[2];       // weights and widened values in shared memory / their product added
     uint64_t q_full, drain[2];
     int64_t wsum[kThreads / 32];
-    int32_t pre[kMaxReq + 1];                          // first tile of every request
+    int32_t wsegs[kThreads / 32];
+    int32_t pre[kMaxReq + 1];                          // first tile of every request, leads counted
+    int32_t lead;
     alignas(16) float cf[kMaxCols];                    // score factor of a column
     alignas(16) float mneg[2][kMaxCols];               // per group: minus its reference maximum,
     alignas(16) float delta[2][kMaxCols];              // the factor of its last raise; at the end, of the group's sums
@@ -262,26 +268,30 @@ struct Seg {
     int r, h, len, lo, rows, row0, nrows, t0, t1;
 };
 
-// the segment that tile `at` lies in, up to tile `end` of the whole list
-__device__ __forceinline__ Seg segment(const AttnParams &p, const Shared &sh, int32_t at, int32_t end)
+// the next segment with tiles in at .. end - 1 of the list, up to `end`; `at` moves behind it
+__device__ __forceinline__ bool next_segment(const AttnParams &p, const Shared &sh, int32_t &at, int32_t end, Seg &s)
 {
-    int a = 0;                              // pre[a] <= at < pre[a + 1]
-    for (int step = 512; step; step >>= 1)
-        if (a + step < p.n_req && sh.pre[a + step] <= at) a += step;
-    Seg s;
-    s.r = a;
-    s.lo = sh.lo[a];
-    s.rows = sh.rows[a];
-    s.len = sh.len[a];
-    const uint32_t nt = (uint32_t)(s.len + kTile - 1) / kTile;
-    const int g = group_count(s.rows, p.fit), per = (s.rows + g - 1) / g;
-    const uint32_t i = (uint32_t)(at - sh.pre[a]), seg = i / nt;
-    s.t0 = (int)(i - seg * nt);
-    s.t1 = min((int)nt, s.t0 + (end - at));
-    s.h = (int)(seg / (uint32_t)g);
-    s.row0 = (int)(seg % (uint32_t)g) * per;
-    s.nrows = min(per, s.rows - s.row0);
-    return s;
+    while (at < end) {
+        int a = 0;                          // pre[a] <= at < pre[a + 1]
+        for (int step = 512; step; step >>= 1)
+            if (a + step < p.n_req && sh.pre[a + step] <= at) a += step;
+        s.r = a;
+        s.lo = sh.lo[a];
+        s.rows = sh.rows[a];
+        s.len = sh.len[a];
+        const uint32_t n = (uint32_t)(s.len + kTile - 1) / kTile + sh.lead;
+        const int g = group_count(s.rows, p.fit), per = (s.rows + g - 1) / g;
+        const uint32_t i = (uint32_t)(at - sh.pre[a]), seg = i / n, u0 = i - seg * n;
+        const uint32_t u1 = min(n, u0 + (uint32_t)(end - at));
+        at += (int32_t)(u1 - u0);
+        s.t0 = max((int)u0 - sh.lead, 0);
+        s.t1 = (int)u1 - sh.lead;
+        s.h = (int)(seg / (uint32_t)g);
+        s.row0 = (int)(seg % (uint32_t)g) * per;
+        s.nrows = min(per, s.rows - s.row0);
+        if (s.t0 < s.t1) return true;
+    }
+    return false;
 }
 
 __device__ __forceinline__ bool bar_or(int id, int threads, bool x)
@@ -421,12 +431,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();                              // the join may start wherever there is room
     // ---- the tile list: tiles of every request, summed up
     int64_t mine = 0;
+    int32_t segs = 0;
     if (tid < p.n_req) {
         int lo, rows, len;
         if (request_ok(p, tid, lo, rows, len))
-            mine = rows ? (int64_t)((len + kTile - 1) / kTile) * p.H * group_count(rows, p.fit) : 0;
+            segs = len ? p.H * group_count(rows, p.fit) : 0;
         else
             fail(p.status);
+        mine = (int64_t)((len + kTile - 1) / kTile) * segs;
         s.lo[tid] = (uint16_t)lo;
         s.rows[tid] = (uint16_t)rows;
         s.len[tid] = len;
@@ -435,9 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int64_t t = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += t;
+        const int32_t n = __shfl_up_sync(0xffffffffu, segs, d);
+        if (lane >= d) incl += t, segs += n;
     }
-    if (lane == 31) s.wsum[warp] = incl;
+    if (lane == 31) s.wsum[warp] = incl, s.wsegs[warp] = segs;
     if (tid == 0) {
         s.abort = 0;
         for (int i = 0; i < kMaxStages; ++i) {
@@ -463,21 +476,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_alloc(smem_u32(&s.tmem), T::kTmCols);
     __syncthreads();
     int64_t all = 0;
+    int32_t all_segs = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) incl += s.wsum[w];
+        if (w < warp) incl += s.wsum[w], segs += s.wsegs[w];
         all += s.wsum[w];
+        all_segs += s.wsegs[w];
     }
+    // Every CTA starts one segment, whatever it does.  A lead counts where it
+    // goes on to another, and would only waste shares of a few tiles.
+    const int32_t lead = (int32_t)min((int64_t)kLead, all / p.ctas / 4);
+    incl += (int64_t)lead * segs;
+    all += (int64_t)lead * all_segs;
     const bool fits = all <= INT32_MAX;                   // else there is nothing to do but say so
     if (!fits && tid == 0) atomicCAS(p.status, 0, (int32_t)W12_E_UNSUPPORTED);
     if (tid < p.n_req) s.pre[tid + 1] = fits ? (int32_t)incl : 0;
-    if (tid == 0) s.pre[0] = 0;
+    if (tid == 0) s.pre[0] = 0, s.lead = lead;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     const int32_t total = s.pre[p.n_req];
     if (cta == 0)
-        for (int i = tid; i <= p.n_req; i += kThreads) p.plan[i] = s.pre[i];
+        for (int i = tid; i <= p.n_req + 1; i += kThreads) p.plan[i] = i <= p.n_req ? s.pre[i] : lead;
     const int64_t share = ((int64_t)total + p.ctas - 1) / p.ctas;
     const int32_t first = (int32_t)min((int64_t)total, cta * share), end = (int32_t)min((int64_t)total, first + share);
     const int bs = p.bt == 32 ? 5 : p.bt == 64 ? 6 : 7;   // log2 of a block's tokens
@@ -504,8 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tile0 = base + (is_k ? T::kOffK : T::kOffV), bytes = (uint32_t)(p.bt * kD);
         uint32_t j = 0, st = 0, par = 1;                      // tile, its stage, the parity its stage's last use left
         bool ok = true;
-        for (int32_t at = first; at < end && ok;) {
-            const Seg g = segment(p, s, at, end);
+        Seg g;
+        for (int32_t at = first; ok && next_segment(p, s, at, end, g);) {
             const int b0 = g.t0 * nb, b1 = min((g.len + p.bt - 1) >> bs, g.t1 * nb);
             const int32_t *table = p.table + (int64_t)g.r * p.max_blocks;
             int blk = 0;
@@ -553,7 +573,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 blk = blk2;
                 sc = sc2;
             }
-            at += g.t1 - g.t0;
         }
         if (!ok) {                                            // copies in flight land before the CTA leaves
             const uint64_t t0 = globaltimer();
@@ -568,8 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t j = 0, q = 0, st = 0, par = 0;
             bool ok = true;
             const uint64_t kd = smem_desc_sw128(base + T::kOffK), qd = smem_desc_sw128(base + T::kOffQ);
-            for (int32_t at = first; at < end && ok; ++q) {
-                const Seg g = segment(p, s, at, end);
+            Seg g;
+            for (int32_t at = first; ok && next_segment(p, s, at, end, g); ++q) {
                 const int n = (g.nrows * p.G + 15) & ~15;
                 const uint32_t idesc = idesc_e4m3_f32(kTile, T::kStacked ? 3 * kCols : n);
                 ok = wait_phase(bar(s.q_full), q & 1, to, p.status, abort);
@@ -589,7 +608,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_commit(bar(s.k_empty[st]));
                     if (++st == T::kStK) st = 0, par ^= 1;
                 }
-                at += g.t1 - g.t0;
             }
             if (!ok) drain(s.drain[0]);
         }
@@ -601,8 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t j = 0;
             bool ok = true;
             const uint64_t pd = smem_desc_mn_sw32(base + T::kOffP, kTile * 32);
-            for (int32_t at = first; at < end && ok;) {
-                const Seg g = segment(p, s, at, end);
+            Seg g;
+            for (int32_t at = first; ok && next_segment(p, s, at, end, g);) {
                 const uint32_t idesc = idesc_f16_f32_bmn(kD, (g.nrows * p.G + 15) & ~15);
                 for (int t = g.t0; t < g.t1 && ok; ++t, ++j) {
                     const int b = j & 1;
@@ -618,7 +636,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   idesc, keep | (k > 0));
                     tc_commit(bar(s.pv_done[b]));
                 }
-                at += g.t1 - g.t0;
             }
             if (!ok) drain(s.drain[1]);
         }
@@ -632,8 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + T::kTmV + wg * (kTile / 2);
         uint32_t j = 0;
         bool ok = true;
-        for (int32_t at = first; at < end && ok;) {
-            const Seg g = segment(p, s, at, end);
+        Seg g;
+        for (int32_t at = first; ok && next_segment(p, s, at, end, g);) {
             for (int t = g.t0; t < g.t1; ++t, ++j) {
                 if ((int)(j & 1) != wg) continue;
                 const int st = j % T::kStV;
@@ -671,7 +688,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(bar(s.v16_full[wg]));
                 }
             }
-            at += g.t1 - g.t0;
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax: group grp takes the tiles j with j % 2 == grp,
@@ -682,8 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
         uint32_t j = 0;
         bool ok = true;
-        for (int32_t at = first; at < end && ok;) {
-            const Seg g = segment(p, s, at, end);
+        Seg g;
+        for (int32_t at = first; ok && next_segment(p, s, at, end, g);) {
             const int ncol = g.nrows * p.G, npad = (ncol + 15) & ~15;
             const int col0 = g.lo * p.Hq + (g.h * g.rows + g.row0) * p.G + cta * kCols;   // its columns in the workspace
             // ---- Q: turned, scaled to E4M3's range by a power of two, in three pieces
@@ -933,7 +949,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dst[i * kD] = (has0 ? o0[i] * s.delta[0][c * 8 + i] : 0.f) + (has1 ? o1[i] * s.delta[1][c * 8 + i] : 0.f);
             }
             tc_fence_before();
-            at += g.t1 - g.t0;
         }
     }
     tc_fence_before();
@@ -1035,7 +1050,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const AttnParams p)
         // the shares that hold a part of this row's segment
         const int64_t total = __ldcg(p.plan + p.n_req), share = (total + p.ctas - 1) / p.ctas;
         const int nt = total ? (len + kTile - 1) / kTile : 0;
-        const int64_t a0 = __ldcg(p.plan + r) + (int64_t)(h * ng + grp) * nt;
+        const int lead = __ldcg(p.plan + p.n_req + 1);
+        const int64_t a0 = __ldcg(p.plan + r) + (int64_t)(h * ng + grp) * (nt + lead) + lead;
         const int cta0 = nt ? (int)(a0 / share) : 0, cta1 = nt ? (int)((a0 + nt - 1) / share) : -1;
         const int64_t col = (int64_t)lo * p.Hq + (int64_t)(h * rows + i0) * G + g;
         for (int c = cta0 + lane; c <= cta1; c += 32) m = fmaxf(m, __ldcg(p.ml + col + (int64_t)c * p.cols).x);
@@ -1089,7 +1105,7 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-size_t plan_bytes() { return (size_t)((kMaxReq + 1) * 4 + 255) / 256 * 256; }
+size_t plan_bytes() { return (size_t)((kMaxReq + 2) * 4 + 255) / 256 * 256; }
 size_t part_columns(int32_t R, int32_t Hq, int ctas) { return (size_t)R * Hq + (size_t)ctas * kMaxCols; }
 
 }  // namespace
