@@ -52,6 +52,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "w12_device.cuh"
@@ -963,22 +964,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // One CTA per row and key/value head; a warp takes a query head of the group at
 // a time, four dimensions to a lane.  It starts with the context's kernel (where
-// an SM has room) and waits for it after the path's keys are staged.
-constexpr int kJoinThreads = 256;
+// an SM has room) and waits for it after the path's scores.  Bound by the
+// latency of its loads: so many small CTAs to an SM, and a context's parts
+// fetched four at a time with their maxima.
+constexpr int kJoinWarps = 8;                           // at most; as many as the group has heads
+constexpr int kJoinKey = kD + 4;                        // stride of a key
+constexpr int kJoinParts = 4;
 
-__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const AttnParams p)
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const AttnParams p)
 {
-    extern __shared__ __align__(16) float smf[];
-    float *sv = smf;                                    // [kPath][kD], read four at a time
-    float *sq = sv + kPath * kD;                        // [8 warps][kD]
-    float *sk = sq + 8 * kD;                            // [kPath][kD + 1] keys of the path, turned
-    float *ss = sk + kPath * (kD + 1);                  // [8 warps][kPath] weights
+    __shared__ __align__(16) float sk[kPath * kJoinKey];      // keys of the path, turned
+    __shared__ __align__(16) uint2 sv[kPath][kD / 4];         // its values, as they come
+    __shared__ __align__(16) float sq[kJoinWarps][kD];
+    __shared__ float ss[kJoinWarps][kPath + 3];               // scores
     __shared__ int32_t s_parent[kMaxBudget], s_path[kPath + 1], s_n;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
     const int row = blockIdx.x, h = blockIdx.y, G = p.G;
     const int r = request_of(p, row);
     const int lo = r < 0 ? row : p.off[r];
-    for (int j = lo + tid; j <= row; j += kJoinThreads) s_parent[j - lo] = p.parent[j];
+    for (int j = lo + tid; j <= row; j += threads) s_parent[j - lo] = p.parent[j];
     __syncthreads();
     const int len = r < 0 ? 0 : p.len[r], rows = r < 0 ? 1 : p.off[r + 1] - lo;
     if (warp == 0) {
@@ -1005,45 +1009,64 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const AttnParams p)
     const int nA = s_n;
     uint16_t *o = p.out + ((int64_t)row * p.Hq + h * G) * kD;
     if (nA == 0) {                                      // malformed: zeros, and the status word says so
-        for (int i = tid; i < G * kD; i += kJoinThreads) o[i] = 0;
+        for (int i = tid; i < G * kD; i += threads) o[i] = 0;
         return;
     }
-    for (int a = warp; a < nA; a += 8) {
+    for (int a = warp; a < nA; a += warps) {
         const int64_t j = s_path[a];
         Raw4 rw;
         load4(rw, p.k + j * p.k_stride + h * kD, lane * 4, len + (int)p.depth[j], p.rope);
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.v + j * p.v_stride + h * kD + lane * 4));
-        const float4 x = turn4(rw);
-        float *dst = sk + a * (kD + 1) + lane * 4;
-        dst[0] = x.x, dst[1] = x.y, dst[2] = x.z, dst[3] = x.w;
-        *reinterpret_cast<float4 *>(sv + a * kD + lane * 4) = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+        sv[a][lane] = __ldg(reinterpret_cast<const uint2 *>(p.v + j * p.v_stride + h * kD + lane * 4));
+        *reinterpret_cast<float4 *>(sk + a * kJoinKey + lane * 4) = turn4(rw);
     }
     __syncthreads();
     const int ng = group_count(rows, p.fit), per = (rows + ng - 1) / ng, i0 = row - lo, grp = i0 / per;
     bool waited = false;
-    for (int g = warp; g < G; g += 8) {
+    for (int g = warp; g < G; g += warps) {
         Raw4 rw;
         load4(rw, p.q + row * p.q_stride + (int64_t)(h * G + g) * kD, lane * 4, len + (int)p.depth[row], p.rope);
         const float4 x = turn4(rw);
         __syncwarp();
-        *reinterpret_cast<float4 *>(sq + warp * kD + lane * 4) =
+        *reinterpret_cast<float4 *>(&sq[warp][lane * 4]) =
             make_float4(x.x * p.scale2, x.y * p.scale2, x.z * p.scale2, x.w * p.scale2);
         __syncwarp();
+        // scores: eight lanes to a row of the path, sixteen dimensions each
+        float4 q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4 *>(&sq[warp][(lane & 7) * 4 + i * 32]);
         float m = -INFINITY;
-        for (int a = lane; a < nA; a += 32) {
-            const float *k = sk + a * (kD + 1);
-            float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
-#pragma unroll 4
-            for (int d = 0; d < kD; d += 4) {
-                const float4 q = *reinterpret_cast<const float4 *>(sq + warp * kD + d);
-                d0 = fmaf(q.x, k[d], d0);
-                d1 = fmaf(q.y, k[d + 1], d1);
-                d2 = fmaf(q.z, k[d + 2], d2);
-                d3 = fmaf(q.w, k[d + 3], d3);
+        for (int a = lane >> 3; a < kPath + 3; a += 4) {
+            if (a - (lane >> 3) >= nA) break;
+            float y = 0.f;
+            if (a < nA) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 k = *reinterpret_cast<const float4 *>(sk + a * kJoinKey + (lane & 7) * 4 + i * 32);
+                    y = fmaf(q[i].x, k.x, fmaf(q[i].y, k.y, fmaf(q[i].z, k.z, fmaf(q[i].w, k.w, y))));
+                }
             }
-            const float y = (d0 + d1) + (d2 + d3);
-            ss[warp * kPath + a] = y;
-            m = fmaxf(m, y);
+#pragma unroll
+            for (int d = 4; d; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
+            if (a < nA) {
+                if ((lane & 7) == 0) ss[warp][a] = y;
+                m = fmaxf(m, y);
+            }
+        }
+#pragma unroll
+        for (int d = 16; d >= 8; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        m = fmaxf(m, -1e30f);                           // (nothing but NaN and -inf: the sums say so)
+        __syncwarp();
+        float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        auto add = [&](float e, float n, const float4 &v) {
+            l = fmaf(e, n, l);
+            acc[0] = fmaf(e, v.x, acc[0]);
+            acc[1] = fmaf(e, v.y, acc[1]);
+            acc[2] = fmaf(e, v.z, acc[2]);
+            acc[3] = fmaf(e, v.w, acc[3]);
+        };
+        for (int a = 0; a < nA; ++a) {
+            const uint2 v = sv[a][lane];
+            add(ex2(ss[warp][a] - m), 1.f, make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)));
         }
         if (!waited) pdl_wait();                        // the context's parts from here on
         waited = true;
@@ -1054,32 +1077,27 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const AttnParams p)
         const int64_t a0 = __ldcg(p.plan + r) + (int64_t)(h * ng + grp) * (nt + lead) + lead;
         const int cta0 = nt ? (int)(a0 / share) : 0, cta1 = nt ? (int)((a0 + nt - 1) / share) : -1;
         const int64_t col = (int64_t)lo * p.Hq + (int64_t)(h * rows + i0) * G + g;
-        for (int c = cta0 + lane; c <= cta1; c += 32) m = fmaxf(m, __ldcg(p.ml + col + (int64_t)c * p.cols).x);
+        for (int c = cta0; c <= cta1; c += kJoinParts) {
+            float2 w[kJoinParts];
+            float4 v[kJoinParts];
 #pragma unroll
-        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if (m == -INFINITY) m = 0.f;                    // nothing but NaN and -inf: the sums say so
-        __syncwarp();
-        float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int a = 0; a < nA; ++a) {
-            const float e = ex2(ss[warp * kPath + a] - m);
-            const float4 v = *reinterpret_cast<const float4 *>(sv + a * kD + lane * 4);
-            l += e;
-            acc[0] = fmaf(e, v.x, acc[0]);
-            acc[1] = fmaf(e, v.y, acc[1]);
-            acc[2] = fmaf(e, v.z, acc[2]);
-            acc[3] = fmaf(e, v.w, acc[3]);
-        }
-#pragma unroll 8
-        for (int c = cta0; c <= cta1; ++c) {
-            const float2 q = __ldcg(p.ml + col + (int64_t)c * p.cols);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (col + (int64_t)c * p.cols) * kD) + lane);
-            const float e = ex2(q.x - m);
-            l = fmaf(e, q.y, l);
-            acc[0] = fmaf(e, v.x, acc[0]);
-            acc[1] = fmaf(e, v.y, acc[1]);
-            acc[2] = fmaf(e, v.z, acc[2]);
-            acc[3] = fmaf(e, v.w, acc[3]);
+            for (int i = 0; i < kJoinParts; ++i)
+                if (c + i <= cta1) {
+                    const int64_t at = col + (int64_t)(c + i) * p.cols;
+                    w[i] = __ldcg(p.ml + at);
+                    v[i] = __ldcg(reinterpret_cast<const float4 *>(p.part + at * kD) + lane);
+                }
+            const float old = m;
+#pragma unroll
+            for (int i = 0; i < kJoinParts; ++i)
+                if (c + i <= cta1) m = fmaxf(m, w[i].x);
+            const float f = ex2(old - m);
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] *= f;
+#pragma unroll
+            for (int i = 0; i < kJoinParts; ++i)
+                if (c + i <= cta1) add(ex2(w[i].x - m), w[i].y, v[i]);
         }
         const float i = 1.f / l;
         *reinterpret_cast<uint2 *>(o + g * kD + lane * 4) =
@@ -1204,11 +1222,9 @@ int launch_attn(const AttnArgs &a, void *stream)
     else
         go(k_attn_ctx<80>, kThreads, smem_bytes<80>());
     if (e != cudaSuccess) return (int)e;
-    constexpr int smem = (kPath * (2 * kD + 1) + 8 * (kD + kPath)) * 4;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.R, (unsigned)a.H);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3((unsigned)std::min(p.G, kJoinWarps) * 32);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
