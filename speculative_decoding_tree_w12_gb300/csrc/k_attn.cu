@@ -706,22 +706,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- Q: turned, scaled to E4M3's range by a power of two, in three pieces
             named_bar(4, kSoft);                              // the last segment's columns are done with
             const int n_q = T::kStacked ? kCols : npad;       // stacked pieces are products of all their columns
-            // A column ahead: its loads are in flight while the last one is split.
+            // A column ahead, its depth two: their loads are in flight while a column is split.
+            constexpr int kStep = kSoft / 32;
             Raw4 rw;
-            auto fetch = [&](int n) {
-                const int i = min(n, ncol - 1), row = g.lo + g.row0 + i / p.G;
-                int pos = g.len + (int)__ldg(p.depth + row);
+            auto place = [&](int n, int &row, int &head) {
+                const int i = min(n, ncol - 1);
+                row = g.lo + g.row0 + i / p.G;
+                head = g.h * p.G + i % p.G;
+            };
+            auto fetch = [&](int row, int head, int depth) {
+                int pos = g.len + depth;
                 if (p.rope.rot && pos >= p.rope.max_pos) {
                     fail(p.status);
                     pos = 0;
                 }
-                load4(rw, p.q + (int64_t)row * p.q_stride + (int64_t)(g.h * p.G + i % p.G) * kD, lane * 4, pos, p.rope);
+                load4(rw, p.q + (int64_t)row * p.q_stride + (int64_t)head * kD, lane * 4, pos, p.rope);
             };
-            if (sw < n_q) fetch(sw);
+            int row, head, row2, head2;
+            place(sw, row, head);
+            place(sw + kStep, row2, head2);
+            int depth = __ldg(p.depth + row), depth2 = __ldg(p.depth + row2);
+            if (sw < n_q) fetch(row, head, depth);
 #pragma unroll 1
-            for (int n = sw; n < n_q; n += kSoft / 32) {
+            for (int n = sw; n < n_q; n += kStep) {
                 float4 x = turn4(rw);
-                if (n + kSoft / 32 < n_q) fetch(n + kSoft / 32);
+                if (n + kStep < n_q) {
+                    fetch(row2, head2, depth2);
+                    place(n + 2 * kStep, row2, head2);
+                    depth2 = __ldg(p.depth + row2);
+                }
                 float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
                 for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
