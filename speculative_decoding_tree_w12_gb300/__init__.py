@@ -736,13 +736,14 @@ class SampleRows:
         self.logits, self.u_sample, self.temperature, self.draft_p, self.u_accept = \
             logits, u_sample, temperature, draft_p, u_accept
         row = lambda t: t.stride(0) if R > 1 else max(t.stride(0), V)
-        nbytes = int(lib().w12_sample_scratch_bytes(R, V))
+        rows = min(R, 512)                       # of a tree at most
+        nbytes = int(lib().w12_sample_scratch_bytes(rows, V))
         if nbytes == 0:
             raise W12Error(W12_E_UNSUPPORTED, "w12_sample_scratch_bytes")
         self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=logits.device)
         self.c = SamplingC(logits.data_ptr(), int(logits.dtype == torch.float32), V, row(logits), _dp(temperature),
                            _dp(draft_p), row(draft_p) if draft_p is not None else 0, _dp(u_accept), _dp(u_sample),
-                           self.scratch.data_ptr(), R)
+                           self.scratch.data_ptr(), rows)
         self.ref = C.byref(self.c)
         self.rows = R
         self.requests = None if temperature is None else int(temperature.shape[0])

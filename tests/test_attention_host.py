@@ -223,3 +223,35 @@ def test_binding_refuses_tensors_it_cannot_pass(w12):
         w12.SampleRows(z(2, 8, dt=torch.float32), z(2, dt=torch.float32), draft_p=z(2, 8, dt=torch.float32))
     with pytest.raises(ValueError):
         w12.DeviceTree.from_arrays(z(3, dt=torch.int32), z(3, dt=torch.int32), z(3, dt=torch.int32), z(2, dt=torch.int32))
+
+
+def test_rope_refusals(w12):
+    L, n = w12.lib(), None
+    A = 1 << 20
+    nbytes = L.w12_workspace_bytes(1, 0, 0, 2)
+    cache = w12.KvCacheC(2, 128, 64, 8, 4, A, A, A, A, A, A)
+
+    def call(**kw):
+        r = dict(rot_dim=64, adjacent=0, max_pos=100, cos=A, sin=A)
+        r.update(kw)
+        return L.w12_kv_append(C.byref(cache), C.byref(w12.RopeC(*r.values())), 2, A, 256, A, 256, 4, A, A, A, nbytes, n)
+
+    for kw, want in ((dict(rot_dim=-8), INVAL), (dict(rot_dim=7), INVAL), (dict(max_pos=0), INVAL), (dict(cos=None), INVAL),
+                     (dict(sin=None), INVAL), (dict(cos=A + 4), INVAL), (dict(sin=A + 8), INVAL), (dict(rot_dim=12), UNSUPPORTED),
+                     (dict(rot_dim=136), UNSUPPORTED)):
+        assert call(**kw) == want, kw
+
+
+def test_sampling_scratch(w12):
+    L = w12.lib()
+    A = 1 << 20
+    nbytes = L.w12_workspace_bytes(1, 0, 0, 3)
+    top = L.w12_sample_max_vocab()
+    assert L.w12_sample_scratch_bytes(0, 10) == L.w12_sample_scratch_bytes(513, 10) == L.w12_sample_scratch_bytes(1, 0) == 0
+    assert L.w12_sample_scratch_bytes(1, top + 1) == 0
+    sizes = [L.w12_sample_scratch_bytes(r, v) for r, v in ((1, 1), (2, 1), (2, 5000), (512, 5000), (512, top))]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    tree = w12.TreeC(4, A, A, A, A, A, A, A)
+    for scratch, rows in ((None, 4), (A + 8, 4), (A, 3)):
+        d = w12.SamplingC(A, 1, 1000, 1000, None, None, 0, None, A, scratch, rows)
+        assert L.w12_tree_sample(C.byref(d), C.byref(tree), 3, A, None, A, nbytes, None) == WORKSPACE, (scratch, rows)
