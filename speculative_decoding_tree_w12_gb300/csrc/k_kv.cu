@@ -441,7 +441,7 @@ int launch_kv_write(const KvArgs &a, void *stream)
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     auto go = [&](auto kernel, int threads) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return;
         kernel<<<grid, threads, smem, st>>>(p);
         e = cudaGetLastError();
