@@ -221,39 +221,57 @@ struct Row {
     }
 };
 
-// The accepted path of request r: from the root to the first child in row order
-// that carries the row's token, as far as there is one.  One warp; a request's
-// first 32 rows are fetched at once.
-__device__ void accept_path(const SampleParams &p, int r, int lane)
+// The accepted paths of requests r0, r0 + step .. (four at most): from the root
+// to the first child in row order that carries the row's token, as far as there
+// is one.  One warp; the first 32 rows of all four are fetched at once.
+__device__ __forceinline__ void accept_paths(const SampleParams &p, int r0, int step, int lane)
 {
-    const int lo = p.off[r], hi = p.off[r + 1];
-    int32_t *out = p.acc_tok + (int64_t)r * (p.p_max + 1);
-    int n = 0, cur = -1;
-    if (lo >= 0 && hi <= p.R && lo < hi) {
-        const bool in = lo + lane < hi;
-        const int parent = in ? p.parent[lo + lane] : -1, token = in ? p.token[lo + lane] : -1;
-        const int drawn = in ? __ldcg(p.row_tok + lo + lane) : -1;
-        cur = lo;
-        for (;;) {
-            const int want = cur - lo < 32 ? __shfl_sync(0xffffffffu, drawn, cur - lo) : __ldcg(p.row_tok + cur);
-            if (lane == 0) out[n] = want;
-            ++n;
-            if (n > p.p_max) break;
-            unsigned b = __ballot_sync(0xffffffffu, in && lo + lane > cur && parent == cur && token == want);
-            int next = b ? lo + __ffs(b) - 1 : -1;
-            for (int j0 = max(cur + 1, lo + 32); j0 < hi && next < 0; j0 += 32) {
-                const int j = j0 + lane;
-                b = __ballot_sync(0xffffffffu, j < hi && p.parent[j] == cur && p.token[j] == want);
-                if (b) next = j0 + __ffs(b) - 1;
-            }
-            if (next < 0) break;
-            cur = next;
-        }
+    int lo[4], hi[4], parent[4], token[4], drawn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i * step;
+        lo[i] = r < p.n_req ? p.off[r] : 0;
+        hi[i] = r < p.n_req ? p.off[r + 1] : 0;
+        if (lo[i] < 0 || hi[i] > p.R) hi[i] = lo[i];
     }
-    for (int i = n + lane; i <= p.p_max; i += 32) out[i] = -1;
-    if (lane == 0) {
-        p.acc_len[r] = n;
-        if (p.acc_node) p.acc_node[r] = cur;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = lo[i] + lane;
+        const bool in = j < hi[i];
+        parent[i] = in ? p.parent[j] : -1;
+        token[i] = in ? p.token[j] : -1;
+        drawn[i] = in ? __ldcg(p.row_tok + j) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i * step;
+        if (r >= p.n_req) break;
+        int32_t *out = p.acc_tok + (int64_t)r * (p.p_max + 1);
+        int n = 0, cur = -1;
+        if (lo[i] < hi[i]) {
+            cur = lo[i];
+            for (;;) {
+                const int want = cur - lo[i] < 32 ? __shfl_sync(0xffffffffu, drawn[i], cur - lo[i]) : __ldcg(p.row_tok + cur);
+                if (lane == 0) out[n] = want;
+                ++n;
+                if (n > p.p_max) break;
+                const int j = lo[i] + lane;
+                unsigned b = __ballot_sync(0xffffffffu, j < hi[i] && j > cur && parent[i] == cur && token[i] == want);
+                int next = b ? lo[i] + __ffs(b) - 1 : -1;
+                for (int j0 = max(cur + 1, lo[i] + 32); j0 < hi[i] && next < 0; j0 += 32) {
+                    const int k = j0 + lane;
+                    b = __ballot_sync(0xffffffffu, k < hi[i] && p.parent[k] == cur && p.token[k] == want);
+                    if (b) next = j0 + __ffs(b) - 1;
+                }
+                if (next < 0) break;
+                cur = next;
+            }
+        }
+        for (int k = n + lane; k <= p.p_max; k += 32) out[k] = -1;
+        if (lane == 0) {
+            p.acc_len[r] = n;
+            if (p.acc_node) p.acc_node[r] = cur;
+        }
     }
 }
 
@@ -271,7 +289,8 @@ __device__ __forceinline__ void row_done(const SampleParams &p)
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    for (int r = threadIdx.x >> 5; r < p.n_req; r += blockDim.x >> 5) accept_path(p, r, threadIdx.x & 31);
+    const int warps = blockDim.x >> 5;
+    for (int r = threadIdx.x >> 5; r < p.n_req; r += 4 * warps) accept_paths(p, r, warps, threadIdx.x & 31);
 }
 
 // a greedy row's token: the lowest of the chunks' candidates.  One warp.
@@ -448,32 +467,61 @@ __device__ __forceinline__ void search(const SampleParams &p, int row, int first
     if (tok >= 0) write_row(p, row, tok, z, w, total);
 }
 
+// The sums of a row's stretches, a run of them to a thread.
+struct Scan {
+    u64 *sums;
+    int first, end;                            // this thread's
+    u64 before, mine, total;
+};
+
+__device__ __forceinline__ Scan scan_row(const SampleParams &p, int row, u64 *s_sum)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
+    const int n = p.chunks * kChunkWarps, run = (n + threads - 1) / threads;
+    Scan c;
+    c.sums = p.sums + (int64_t)row * n;
+    c.first = min(n, (int)threadIdx.x * run);
+    c.end = min(n, c.first + run);
+    c.mine = c.total = 0;
+    for (int i = c.first; i < c.end; ++i) c.mine += __ldcg(c.sums + i);
+    c.before = c.mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const u64 o = __shfl_up_sync(0xffffffffu, c.before, d);
+        if (lane >= d) c.before += o;
+    }
+    if (lane == 31) s_sum[warp] = c.before;
+    c.before -= c.mine;
+    __syncthreads();
+    for (int i = 0; i < threads / 32; ++i) {
+        if (i < warp) c.before += s_sum[i];
+        c.total += s_sum[i];
+    }
+    __syncthreads();
+    return c;
+}
+
 // A row without rejections, by one CTA: its token by the sums of the stretches.
 template <bool kF32>
-__device__ void draw(const SampleParams &p, int row, const Row<kF32> &z, const Weigher<kF32> &w, u64 total, u64 *s_sum)
+__device__ void draw(const SampleParams &p, int row, const Row<kF32> &z, const Weigher<kF32> &w, const Scan &c, u64 *s_sum)
 {
     constexpr int kPer = Row<kF32>::kPer;
-    const int lane = threadIdx.x & 31;
-    const u64 *sums = p.sums + (int64_t)row * p.chunks * kChunkWarps;
-    const int n = p.chunks * kChunkWarps;
-    u64 t = place(p.u_sample[row], total);
-    int at = -1;
-    for (int i0 = 0; i0 < n && at < 0; i0 += 32) {
-        u64 incl = i0 + lane < n ? __ldcg(sums + i0 + lane) : 0ull;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const u64 o = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += o;
+    __shared__ u64 s_rest;
+    __shared__ int32_t s_at;
+    u64 t = place(p.u_sample[row], c.total);
+    if (t >= c.before && t - c.before < c.mine) {
+        t -= c.before;
+        int at = c.first;
+        for (;; ++at) {
+            const u64 x = __ldcg(c.sums + at);
+            if (t < x) break;
+            t -= x;
         }
-        const unsigned b = __ballot_sync(0xffffffffu, incl > t);
-        if (b) {
-            at = i0 + __ffs(b) - 1;
-            t -= __ffs(b) > 1 ? __shfl_sync(0xffffffffu, incl, __ffs(b) - 2) : 0ull;
-        } else {
-            t -= __shfl_sync(0xffffffffu, incl, 31);
-        }
+        s_at = at;
+        s_rest = t;
     }
-    search(p, row, at * 32 * p.per, p.per, t, z, w, total, s_sum, [&](int v, u64 (&e)[kPer / 2]) { w.any_piece(z.piece(v), e); });
+    __syncthreads();
+    search(p, row, s_at * 32 * p.per, p.per, s_rest, z, w, c.total, s_sum, [&](int v, u64 (&e)[kPer / 2]) { w.any_piece(z.piece(v), e); });
 }
 
 // The row's next child after row j, of those whose token is one.  One warp.
@@ -598,19 +646,17 @@ __global__ void __launch_bounds__(kChunkThreads, 5) k_sample_sum(const SamplePar
     } else if (t.greedy) {
         if (warp == 0) draw_greedy(p, row, lane);
     } else {
-        u64 total = 0;
-        for (int i = lane; i < p.chunks * kChunkWarps; i += 32) total += __ldcg(p.sums + (int64_t)row * p.chunks * kChunkWarps + i);
-        total = warp_sum(total);
+        const Scan c = scan_row(p, row, s_sum);
         const int kid = kDraft ? next_child(p, row, row, lane) : -1;
         if (kid < 0) {
-            draw(p, row, z, w, total, s_sum);
+            draw(p, row, z, w, c, s_sum);
         } else {
-            const int c = p.token[kid];
-            if (!accepted(p.u_accept[kid], __ldg(p.draft_p + row * p.draft_stride + c), w.one(z.token(c)), total)) {
-                if (first) p.left[atomicAdd(p.n_left, 1)] = {row, top, total};
+            const int x = p.token[kid];
+            if (!accepted(p.u_accept[kid], __ldg(p.draft_p + row * p.draft_stride + x), w.one(z.token(x)), c.total)) {
+                if (first) p.left[atomicAdd(p.n_left, 1)] = {row, top, c.total};
                 return;
             }
-            if (first) write_row(p, row, c, z, w, total);
+            if (first) write_row(p, row, x, z, w, c.total);
         }
     }
     row_done(p);
@@ -770,7 +816,7 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
     if (took >= 0) {
         if (writes && tid == 0) write_row(p, row, p.token[took], z, w, job.total);
     } else if (rounds == 0) {                                       // p = q
-        if (writes) draw(p, row, z, w, total, s.wsum[buf ^ 1]);
+        if (writes) draw(p, row, z, w, scan_row(p, row, s.wsum[buf ^ 1]), s.wsum[buf ^ 1]);
     } else {
         const u64 at = place(p.u_sample[row], total);
         u64 before = 0;
