@@ -23,8 +23,9 @@
 // the rows whose first child was rejected are left to k_sample_draft: a cluster
 // to a row, which goes over it again for every rejection.
 // The CTA that completes the last row writes the accepted paths.
-// Many rows are bound by the issue rate of the sums' pass, some 15 instructions
-// a token, half of them expf; few rows by latency.
+// The second pass takes the rows in reverse, so that logits past the L2 cache's
+// size are found there as far as it reaches.  Many rows are bound by the issue
+// rate of the sums' pass, some ten instructions a token; few rows by latency.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -315,30 +316,43 @@ struct Temper {
     bool ok, greedy;
 };
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 __device__ __forceinline__ Temper temper(const SampleParams &p, int row)
 {
     const int r = p.req[row];
     Temper t;
     t.ok = r >= 0 && r < p.n_req;
     const float T = t.ok && p.temperature ? p.temperature[r] : 1.f;
-    t.greedy = !(T > 0.f);
-    t.inv_t = t.greedy ? 1.f : __fdiv_rn(1.f, T);
+    t.inv_t = __fdiv_rn(1.f, T);
+    t.greedy = !(T > 0.f) || !(t.inv_t * kLog2e < INFINITY);            // (1 / T over the numbers' range: next to nothing)
     return t;
 }
 
-// exp(z - m), z = logit / T
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// exp((x - m) / T) as 2^((x - m) c): the difference first, so that its rounding
+// and c's count by the distance from the largest logit, not by its size.  With
+// the machine's 2^x (2^-22) a weight is within 2^-22 (1 + 1.5 |x - m| / T) of
+// its value, and the sums' pass takes six instructions a token less than with
+// expf (192 rows of 151936 tokens: 40 -> 35 us).
 template <bool kF32>
 struct Weigher {
     static constexpr int kPer = Row<kF32>::kPer;
-    float inv_t, m;                            // m: the largest z
-    __device__ Weigher(float inv_t_, float top) : inv_t(inv_t_), m(top * inv_t_) {}   // (a positive factor keeps the order)
+    static constexpr float kLeast = -126.f;    // (also what a NaN becomes: a weight of nothing)
+    float inv_t, c, m;                         // m: the largest logit
+    __device__ Weigher(float inv_t_, float top) : inv_t(inv_t_), c(inv_t_ * kLog2e), m(top) {}
     __device__ __forceinline__ float one(float x) const
     {
-        const float z = __fmul_rn(x, inv_t);
-        if (m == INFINITY) return z == INFINITY ? 1.f : 0.f;            // nothing but the infinite ones counts
-        return expf(fmaxf(__fsub_rn(z, m), -128.f));                    // (a NaN becomes a weight of nothing)
+        if (m == INFINITY) return x == INFINITY ? 1.f : 0.f;            // nothing but the infinite ones counts
+        return ex2(fmaxf(__fmul_rn(__fsub_rn(x, m), c), kLeast));
     }
-    // of a piece's tokens, in pairs; kInf: there are infinite z
+    // of a piece's tokens, in pairs; kInf: there are infinite logits
     template <bool kInf = false>
     __device__ __forceinline__ void piece(const uint4 &x, u64 (&e)[kPer / 2]) const
     {
@@ -348,9 +362,9 @@ struct Weigher {
                 e[i / 2] = pair(one(Row<kF32>::get(x, i)), one(Row<kF32>::get(x, i + 1)));
                 continue;
             }
-            const u64 z = mul2(pair(Row<kF32>::get(x, i), Row<kF32>::get(x, i + 1)), pair(inv_t, inv_t));
-            const float2 d = unpair(add2(z, pair(-m, -m)));
-            e[i / 2] = pair(expf(fmaxf(d.x, -128.f)), expf(fmaxf(d.y, -128.f)));
+            const u64 d = add2(pair(Row<kF32>::get(x, i), Row<kF32>::get(x, i + 1)), pair(-m, -m));
+            const float2 t = unpair(mul2(d, pair(c, c)));
+            e[i / 2] = pair(ex2(fmaxf(t.x, kLeast)), ex2(fmaxf(t.y, kLeast)));
         }
     }
     __device__ __forceinline__ void any_piece(const uint4 &x, u64 (&e)[kPer / 2]) const
@@ -413,8 +427,8 @@ __device__ __forceinline__ void write_row(const SampleParams &p, int row, int to
     p.row_tok[row] = tok;
     if (p.row_logp) {
         // (a NaN can only be an accepted child's)
-        const float x = __fmul_rn(fmaxf(z.token(tok), -INFINITY), w.inv_t);
-        p.row_logp[row] = __fsub_rn(x == w.m ? 0.f : __fsub_rn(x, w.m), logf(weight_of(total)));
+        const float x = fmaxf(z.token(tok), -INFINITY);
+        p.row_logp[row] = __fsub_rn(x == w.m ? 0.f : __fmul_rn(__fsub_rn(x, w.m), w.inv_t), logf(weight_of(total)));
     }
 }
 
@@ -586,7 +600,7 @@ __global__ void __launch_bounds__(kChunkThreads, 5) k_sample_sum(const SamplePar
     constexpr int kPer = Row<kF32>::kPer;
     __shared__ int32_t s_last;
     __shared__ u64 s_sum[kChunkWarps];
-    const int row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = gridDim.y - 1 - blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Row<kF32> z(p.logits, row * p.stride, p.vocab);
     const int lo = (blockIdx.x * kChunkWarps + warp) * 32 * p.per;
     const Temper t = temper(p, row);
