@@ -70,11 +70,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+// a b + c d, every operation rounded on its own: the sums one at a time, since
+// a sum of two would be fused with a product of two before it
+__device__ __forceinline__ uint64_t mul2_add2(uint64_t a, uint64_t b, uint64_t c, uint64_t d)
 {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
+    const float2 x = unpair(mul2(a, b)), y = unpair(mul2(c, d));
+    return pair(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
 }
 
 // codes of two pairs of values, the first in the low byte.  `odd`: some may
@@ -293,8 +294,8 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
                             s[0] = pair(ss.x, ss.y), s[1] = pair(ss.z, ss.w);
                             y[0] = pair_bf16(o0), y[1] = pair_bf16(o1);
                         }
-                        x[i][0] = add2(mul2(x[i][0], c[0]), mul2(y[0], s[0]));
-                        x[i][1] = add2(mul2(x[i][1], c[1]), mul2(y[1], s[1]));
+                        x[i][0] = mul2_add2(x[i][0], c[0], y[0], s[0]);
+                        x[i][1] = mul2_add2(x[i][1], c[1], y[1], s[1]);
                     }
                     tk = top2(top2(tk, x[i][0], false), x[i][1], false);
                     vm = __vmaxu2(__vmaxu2(vm, vr[i].x & 0x7FFF7FFFu), vr[i].y & 0x7FFF7FFFu);

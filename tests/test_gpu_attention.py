@@ -133,6 +133,22 @@ def test_append(w12, lens, new, H, bt, rot, adjacent):
     assert s.ws.status() == 0
 
 
+@pytest.mark.parametrize("bt,rot,adjacent", [(32, 128, False), (64, 64, True), (128, 0, False), (128, 128, False)])
+def test_append_long(w12, bt, rot, adjacent):
+    """Enough tokens and heads that a CTA takes several heads of a block."""
+    lens, new, H = [5, 0, 77], [4001, 6000, 33], 16
+    s = World(w12, lens, H, bt, rot, adjacent, room=6001, seed=4)
+    x = rounded(s.g.standard_normal((sum(new), 2, H, D)) * np.exp(s.g.uniform(-3, 3, (sum(new), 1, H, 1))))
+    off = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    k, v = (bf16(x[:, i].reshape(-1, H * D)) for i in range(2))
+    w12.w12_kv_append(s.cache, s.rope, k, v, torch.from_numpy(off).cuda(), s.ws)
+    for r in range(len(lens)):
+        rows = x[off[r]:off[r + 1]]
+        ref.kv_write(s.host, r, rows[:, 0], rows[:, 1], s.cos, s.sin, adjacent)
+    s.same()
+    assert s.ws.status() == 0
+
+
 @pytest.mark.parametrize("bt", [32, 128])
 def test_growing_block(w12, bt):
     """One token at a time through a block, each larger than the ones before:
