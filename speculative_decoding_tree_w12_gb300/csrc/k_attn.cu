@@ -119,17 +119,6 @@ __device__ __forceinline__ bool request_ok(const AttnParams &p, int r, int &lo, 
     return lo >= 0 && hi <= p.R && rows >= 0 && len >= 0 && (int64_t)len <= (int64_t)p.max_blocks * p.bt;
 }
 
-// the request of a row, or -1
-__device__ __forceinline__ int request_of(const AttnParams &p, int row)
-{
-    const int r = p.req[row];
-    if (r < 0 || r >= p.n_req) return -1;
-    int lo, rows, len;
-    if (!request_ok(p, r, lo, rows, len) || row < lo || row >= lo + rows) return -1;
-    if (p.rope.rot && len + (int)p.depth[row] >= p.rope.max_pos) return -1;
-    return r;
-}
-
 // Four consecutive elements d0 .. d0 + 3 of a BF16 row and what turns them by
 // position pos; loaded apart from the arithmetic, so that the loads of several
 // rows are in flight together.  The rotated part is a multiple of 8 wide, so a
@@ -978,8 +967,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // One CTA per row and key/value head; a warp takes a query head of the group at
 // a time, four dimensions to a lane.  It starts with the context's kernel (where
 // an SM has room) and waits for it after the path's scores.  Bound by the
-// latency of its loads: so many small CTAs to an SM, and a context's parts
-// fetched four at a time with their maxima.
+// latency of its loads: so many small CTAs to an SM, everything asked for as
+// soon as its address is known (parents and depths of all rows up to this one
+// before its request is), and a context's parts fetched four at a time with
+// their maxima.
 constexpr int kJoinWarps = 8;                           // at most; as many as the group has heads
 constexpr int kJoinKey = kD + 4;                        // stride of a key
 constexpr int kJoinParts = 4;
@@ -991,27 +982,37 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const AttnPara
     __shared__ __align__(16) float sq[kJoinWarps][kD];
     __shared__ float ss[kJoinWarps][kPath + 3];               // scores
     __shared__ int32_t s_parent[kMaxBudget], s_path[kPath + 1], s_n;
+    __shared__ uint8_t s_depth[kMaxBudget];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
     const int row = blockIdx.x, h = blockIdx.y, G = p.G;
-    const int r = request_of(p, row);
-    const int lo = r < 0 ? row : p.off[r];
-    for (int j = lo + tid; j <= row; j += threads) s_parent[j - lo] = p.parent[j];
+    int r = p.req[row];
+    for (int j = tid; j <= row; j += threads) {
+        s_parent[j] = p.parent[j];
+        s_depth[j] = p.depth[j];
+    }
+    int lo = 0, rows = 1, len = 0;
+    if (r < 0 || r >= p.n_req || !request_ok(p, r, lo, rows, len) || row < lo || row >= lo + rows) r = -1;
     __syncthreads();
-    const int len = r < 0 ? 0 : p.len[r], rows = r < 0 ? 1 : p.off[r + 1] - lo;
+    // a position on the table (or none)
+    auto placed = [&](int j) { return p.rope.rot == 0 || len + (int)s_depth[j] < p.rope.max_pos; };
+    const bool served = r >= 0 && placed(row);
+    Raw4 rw;
+    if (served && warp < G)
+        load4(rw, p.q + row * p.q_stride + (int64_t)(h * G + warp) * kD, lane * 4, len + (int)s_depth[row], p.rope);
     if (warp == 0) {
         int n = 0, j = row;
-        while (r >= 0 && j >= lo && n <= kPath) {
+        while (served && j >= lo && n <= kPath) {
             if (lane == 0) s_path[n] = j;
             ++n;
-            const int q = s_parent[j - lo];
+            const int q = s_parent[j];
             if (q >= j) n = kPath + 1;                  // a parent after its child
             else j = q;
         }
-        const bool ok = r >= 0 && n <= kPath && j < 0;  // ... or outside the request
+        const bool ok = served && n <= kPath && j < 0;  // ... or outside the request
         bool off = false;                               // a position off the table
         __syncwarp();
-        if (ok && p.rope.rot)
-            for (int a = lane; a < n; a += 32) off |= len + (int)p.depth[s_path[a]] >= p.rope.max_pos;
+        if (ok)
+            for (int a = lane; a < n; a += 32) off |= !placed(s_path[a]);
         off = __any_sync(0xffffffffu, off);
         if (lane == 0) {
             s_n = ok && !off ? n : 0;
@@ -1027,17 +1028,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const AttnPara
     }
     for (int a = warp; a < nA; a += warps) {
         const int64_t j = s_path[a];
-        Raw4 rw;
-        load4(rw, p.k + j * p.k_stride + h * kD, lane * 4, len + (int)p.depth[j], p.rope);
+        Raw4 kw;
+        load4(kw, p.k + j * p.k_stride + h * kD, lane * 4, len + (int)s_depth[j], p.rope);
         sv[a][lane] = __ldg(reinterpret_cast<const uint2 *>(p.v + j * p.v_stride + h * kD + lane * 4));
-        *reinterpret_cast<float4 *>(sk + a * kJoinKey + lane * 4) = turn4(rw);
+        *reinterpret_cast<float4 *>(sk + a * kJoinKey + lane * 4) = turn4(kw);
     }
     __syncthreads();
     const int ng = group_count(rows, p.fit), per = (rows + ng - 1) / ng, i0 = row - lo, grp = i0 / per;
     bool waited = false;
     for (int g = warp; g < G; g += warps) {
-        Raw4 rw;
-        load4(rw, p.q + row * p.q_stride + (int64_t)(h * G + g) * kD, lane * 4, len + (int)p.depth[row], p.rope);
+        if (g >= warps)                                 // (the first is on its way)
+            load4(rw, p.q + row * p.q_stride + (int64_t)(h * G + g) * kD, lane * 4, len + (int)s_depth[row], p.rope);
         const float4 x = turn4(rw);
         __syncwarp();
         *reinterpret_cast<float4 *>(&sq[warp][lane * 4]) =
