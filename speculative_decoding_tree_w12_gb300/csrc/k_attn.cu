@@ -13,8 +13,9 @@
 // consecutive shares, one per CTA and one CTA per SM, so a long context of one
 // request and many short ones balance alike.  Starting and ending a segment
 // costs as much as a handful of tiles, so every segment has a lead of as many
-// empty ones in the list (kLead; 256 rows of 32 requests: the slowest CTA was
-// 23% over the mean without).  A share leaves, for every
+// empty ones in the list, and a tile counts by its columns (kLead and
+// tile_weight; 256 rows of 32 requests: the slowest CTA was 23% over the mean
+// without the leads, 10% without the weights).  A share leaves, for every
 // segment (request, head, group) that it meets, FP32 sums with their maximum
 // and normaliser; k_attn_join merges them with the root path's.
 //
@@ -98,7 +99,7 @@ struct AttnParams {
     RopeArgs rope;
     float scale2;                           // softmax scale * log2(e)
     uint16_t *out;
-    int32_t *plan;                          // [n_req + 1] first tile of every request in the list; tiles of a lead
+    int32_t *plan;                          // [n_req + 1] where every request starts in the list; tiles of a lead; whether tiles are weighted
     float *part;                            // [R * Hq + ctas * cols][kD] sums
     float2 *ml;                             // [R * Hq + ctas * cols] maximum (log2), normaliser
     int32_t *status;
@@ -109,6 +110,13 @@ __device__ __forceinline__ void fail(int32_t *status) { atomicCAS(status, 0, (in
 
 // rows of a request's groups: as many as fit the columns, evenly
 __device__ __forceinline__ int group_count(int rows, int fit) { return (rows + fit - 1) / fit; }
+// what a tile of such a request counts in the split: 0.35 us and 0.13 us for every 16 columns
+__device__ __forceinline__ int tile_weight(const AttnParams &p, int rows)
+{
+    const int g = group_count(rows, p.fit);
+    return 11 + 4 * (((rows + g - 1) / g * p.G + 15) >> 4);
+}
+
 // a request's rows and cached tokens; false where they contradict each other or the tables
 __device__ __forceinline__ bool request_ok(const AttnParams &p, int r, int &lo, int &rows, int &len)
 {
@@ -218,7 +226,8 @@ struct Shape {
 };
 
 constexpr int kMaxStages = 6;
-constexpr int kLead = 8;                                     // a segment's start and end in tiles: 6 to 7 of 16 columns, 10 of 48 and 80
+constexpr int kRowBits = 10;                                 // of a request's row count
+constexpr int kLead = 9;                                     // a segment's start and end in tiles: 7 of 16 columns, 10 of 48 and 80
 
 struct Shared {
     uint64_t k_full[kMaxStages], k_empty[kMaxStages];  // K and V tiles loaded / consumed
@@ -226,18 +235,22 @@ struct Shared {
     uint64_t s_full[2], s_empty[2];                    // scores in tensor memory / read
     uint64_t p_full[2], v16_full[2], pv_done[2];       // weights and widened values in shared memory / their product added
     uint64_t q_full, drain[2];
-    int64_t wsum[kThreads / 32];
-    int32_t wsegs[kThreads / 32];
-    int32_t pre[kMaxReq + 1];                          // first tile of every request, leads counted
-    int32_t lead;
+    int32_t pre[kMaxReq + 1];                          // where every request starts in the list
+    int32_t lead, weighted;
     alignas(16) float cf[kMaxCols];                    // score factor of a column
     alignas(16) float mneg[2][kMaxCols];               // per group: minus its reference maximum,
     alignas(16) float delta[2][kMaxCols];              // the factor of its last raise; at the end, of the group's sums
-    alignas(16) float red[2][4][kMaxCols];             // per warp
+    union {
+        alignas(16) float red[2][4][kMaxCols];         // per warp
+        struct {                                       // before: the list's sums, per warp
+            int64_t units[kThreads / 32], tiles[kThreads / 32];
+            int32_t segs[kThreads / 32];
+        } list;
+    };
     float lsum[2][kMaxCols];                           // normalisers
     float sref[2];
     int32_t len[kMaxReq];                              // of every request: cached tokens,
-    uint16_t lo[kMaxReq], rows[kMaxReq];               // first row, rows
+    uint16_t lo[kMaxReq], rows[kMaxReq];               // first row; rows, and above kRowBits the weight of its tiles
     float2 scale[kScaleRing][kTile / 32];              // K and V scale of a tile's blocks
     float top_v[kScaleRing];                           // the largest of the V scales
     uint32_t tmem;
@@ -269,13 +282,15 @@ __device__ __forceinline__ bool next_segment(const AttnParams &p, const Shared &
         s.lo = sh.lo[a];
         s.rows = sh.rows[a];
         s.len = sh.len[a];
-        const uint32_t n = (uint32_t)(s.len + kTile - 1) / kTile + sh.lead;
+        const uint32_t w = sh.weighted ? s.rows >> kRowBits : 1;
+        s.rows &= (1 << kRowBits) - 1;
+        const uint32_t n = ((uint32_t)(s.len + kTile - 1) / kTile + sh.lead) * w;
         const int g = group_count(s.rows, p.fit), per = (s.rows + g - 1) / g;
         const uint32_t i = (uint32_t)(at - sh.pre[a]), seg = i / n, u0 = i - seg * n;
         const uint32_t u1 = min(n, u0 + (uint32_t)(end - at));
         at += (int32_t)(u1 - u0);
-        s.t0 = max((int)u0 - sh.lead, 0);
-        s.t1 = (int)u1 - sh.lead;
+        s.t0 = max((int)((u0 + w - 1) / w) - sh.lead, 0);     // a tile is its first unit's
+        s.t1 = (int)((u1 + w - 1) / w) - sh.lead;
         s.h = (int)(seg / (uint32_t)g);
         s.row0 = (int)(seg % (uint32_t)g) * per;
         s.nrows = min(per, s.rows - s.row0);
@@ -420,27 +435,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     pdl_launch_dependents();                              // the join may start wherever there is room
     // ---- the tile list: tiles of every request, summed up
-    int64_t mine = 0;
-    int32_t segs = 0;
+    int64_t tiles = 0, incl = 0;                          // as they are; weighted
+    int32_t segs = 0;                                     // weighted
+    int w = 1;
     if (tid < p.n_req) {
         int lo, rows, len;
         if (request_ok(p, tid, lo, rows, len))
             segs = len ? p.H * group_count(rows, p.fit) : 0;
         else
             fail(p.status);
-        mine = (int64_t)((len + kTile - 1) / kTile) * segs;
+        if (segs) w = tile_weight(p, rows);
+        tiles = (int64_t)((len + kTile - 1) / kTile) * segs;
+        segs *= w;
+        incl = tiles * w;
         s.lo[tid] = (uint16_t)lo;
-        s.rows[tid] = (uint16_t)rows;
+        s.rows[tid] = (uint16_t)(rows | w << kRowBits);
         s.len[tid] = len;
     }
-    int64_t incl = mine;
+    auto scan = [&](int64_t &a, int64_t &b, int32_t &c) {  // over a warp
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t t = __shfl_up_sync(0xffffffffu, incl, d);
-        const int32_t n = __shfl_up_sync(0xffffffffu, segs, d);
-        if (lane >= d) incl += t, segs += n;
-    }
-    if (lane == 31) s.wsum[warp] = incl, s.wsegs[warp] = segs;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, b, d);
+            const int32_t z = __shfl_up_sync(0xffffffffu, c, d);
+            if (lane >= d) a += x, b += y, c += z;
+        }
+    };
+    if (warp * 32 < p.n_req) scan(incl, tiles, segs);
+    if (lane == 31) s.list.units[warp] = incl, s.list.tiles[warp] = tiles, s.list.segs[warp] = segs;
     if (tid == 0) {
         s.abort = 0;
         for (int i = 0; i < kMaxStages; ++i) {
@@ -465,29 +486,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 1) tmem_alloc(smem_u32(&s.tmem), T::kTmCols);
     __syncthreads();
-    int64_t all = 0;
-    int32_t all_segs = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) incl += s.wsum[w], segs += s.wsegs[w];
-        all += s.wsum[w];
-        all_segs += s.wsegs[w];
+    // what the warps before had, and all
+    static_assert(kThreads / 32 <= 32, "a warp's sums to a lane");
+    const int held = lane * 32 < p.n_req ? lane : -1;     // (a warp without requests has nothing)
+    int64_t all = held < 0 ? 0 : s.list.units[held], all_tiles = held < 0 ? 0 : s.list.tiles[held];
+    int32_t all_segs = held < 0 ? 0 : s.list.segs[held];
+    if (p.n_req > 32) {
+        scan(all, all_tiles, all_segs);
+        if (warp) {
+            incl += __shfl_sync(0xffffffffu, all, warp - 1);
+            tiles += __shfl_sync(0xffffffffu, all_tiles, warp - 1);
+            segs += __shfl_sync(0xffffffffu, all_segs, warp - 1);
+        }
     }
+    const int last = p.n_req > 32 ? 31 : 0;
+    all = __shfl_sync(0xffffffffu, all, last);
+    all_tiles = __shfl_sync(0xffffffffu, all_tiles, last);
+    all_segs = __shfl_sync(0xffffffffu, all_segs, last);
     // Every CTA starts one segment, whatever it does.  A lead counts where it
-    // goes on to another, and would only waste shares of a few tiles.
-    const int32_t lead = (int32_t)min((int64_t)kLead, all / p.ctas / 4);
-    incl += (int64_t)lead * segs;
-    all += (int64_t)lead * all_segs;
+    // goes on to another, and would only waste shares of a few tiles; those are
+    // also too small for weights (a share has to have a tile of every segment
+    // that it lies in).
+    int32_t lead = (int32_t)min((int64_t)kLead, all_tiles / p.ctas / 4);
+    const bool weighted = lead > 0 && all + (int64_t)lead * all_segs <= INT32_MAX;
+    if (weighted) {
+        incl += (int64_t)lead * segs;
+        all += (int64_t)lead * all_segs;
+    } else {
+        incl = tiles;
+        all = all_tiles;
+        lead = 0;
+    }
     const bool fits = all <= INT32_MAX;                   // else there is nothing to do but say so
     if (!fits && tid == 0) atomicCAS(p.status, 0, (int32_t)W12_E_UNSUPPORTED);
     if (tid < p.n_req) s.pre[tid + 1] = fits ? (int32_t)incl : 0;
-    if (tid == 0) s.pre[0] = 0, s.lead = lead;
+    if (tid == 0) s.pre[0] = 0, s.lead = lead, s.weighted = weighted;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     const int32_t total = s.pre[p.n_req];
     if (cta == 0)
-        for (int i = tid; i <= p.n_req + 1; i += kThreads) p.plan[i] = i <= p.n_req ? s.pre[i] : lead;
+        for (int i = tid; i <= p.n_req + 2; i += kThreads) p.plan[i] = i <= p.n_req ? s.pre[i] : i == p.n_req + 1 ? lead : weighted;
     const int64_t share = ((int64_t)total + p.ctas - 1) / p.ctas;
     const int32_t first = (int32_t)min((int64_t)total, cta * share), end = (int32_t)min((int64_t)total, first + share);
     const int bs = p.bt == 32 ? 5 : p.bt == 64 ? 6 : 7;   // log2 of a block's tokens
@@ -1087,31 +1127,31 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const AttnPara
         // the shares that hold a part of this row's segment
         const int64_t total = __ldcg(p.plan + p.n_req), share = (total + p.ctas - 1) / p.ctas;
         const int nt = total ? (len + kTile - 1) / kTile : 0;
-        const int lead = __ldcg(p.plan + p.n_req + 1);
-        const int64_t a0 = __ldcg(p.plan + r) + (int64_t)(h * ng + grp) * (nt + lead) + lead;
-        const int cta0 = nt ? (int)(a0 / share) : 0, cta1 = nt ? (int)((a0 + nt - 1) / share) : -1;
+        const int lead = __ldcg(p.plan + p.n_req + 1), w = __ldcg(p.plan + p.n_req + 2) ? tile_weight(p, rows) : 1;
+        const int64_t a0 = __ldcg(p.plan + r) + ((int64_t)(h * ng + grp) * (nt + lead) + lead) * w;
+        const int cta0 = nt ? (int)(a0 / share) : 0, cta1 = nt ? (int)((a0 + (int64_t)(nt - 1) * w) / share) : -1;
         const int64_t col = (int64_t)lo * p.Hq + (int64_t)(h * rows + i0) * G + g;
         for (int c = cta0; c <= cta1; c += kJoinParts) {
-            float2 w[kJoinParts];
+            float2 ml[kJoinParts];
             float4 v[kJoinParts];
 #pragma unroll
             for (int i = 0; i < kJoinParts; ++i)
                 if (c + i <= cta1) {
                     const int64_t at = col + (int64_t)(c + i) * p.cols;
-                    w[i] = __ldcg(p.ml + at);
+                    ml[i] = __ldcg(p.ml + at);
                     v[i] = __ldcg(reinterpret_cast<const float4 *>(p.part + at * kD) + lane);
                 }
             const float old = m;
 #pragma unroll
             for (int i = 0; i < kJoinParts; ++i)
-                if (c + i <= cta1) m = fmaxf(m, w[i].x);
+                if (c + i <= cta1) m = fmaxf(m, ml[i].x);
             const float f = ex2(old - m);
             l *= f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] *= f;
 #pragma unroll
             for (int i = 0; i < kJoinParts; ++i)
-                if (c + i <= cta1) add(ex2(w[i].x - m), w[i].y, v[i]);
+                if (c + i <= cta1) add(ex2(ml[i].x - m), ml[i].y, v[i]);
         }
         const float i = 1.f / l;
         *reinterpret_cast<uint2 *>(o + g * kD + lane * 4) =
@@ -1137,7 +1177,7 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-size_t plan_bytes() { return (size_t)((kMaxReq + 2) * 4 + 255) / 256 * 256; }
+size_t plan_bytes() { return (size_t)((kMaxReq + 3) * 4 + 255) / 256 * 256; }
 size_t part_columns(int32_t R, int32_t Hq, int ctas) { return (size_t)R * Hq + (size_t)ctas * kMaxCols; }
 
 }  // namespace
