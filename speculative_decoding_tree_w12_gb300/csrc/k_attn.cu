@@ -33,7 +33,7 @@
 //   O^T = V^T P  kind::f16: V's codes widened to F16 (exact) by warpgroups of
 //                their own, into tensor memory (through shared memory they
 //                would cost four times the bandwidth, which bounds the tile);
-//                P in F16, eleven significant bits down to 2^-15 of the
+//                P in F16, eleven significant bits down to 2^-12 of the
 //                largest weight there was when its reference was set.
 // Two groups of two softmax warpgroups take alternate tiles, each with its own
 // scores, P, maxima and sums, so that the latencies of one tile's chain
@@ -48,8 +48,17 @@
 // score passes it by 2^6 (P stays under F16's top), so the usual tile has no
 // reduction over lanes at all; the same slow path raises the reference of the
 // value scales, which P carries.  A raise costs several tiles, so a reference
-// is set 2^3 above the maximum: with normally distributed scores that leaves
-// next to none but the first.
+// is set 2^6 above the maximum: with normally distributed scores that leaves
+// next to none but the first (set at the maximum, 32 rows behind 32771 tokens
+// took 88 us; 2^6 above, 71).
+//
+// What bounds it.  One row behind a long context: memory (131072 tokens of 8
+// heads, 268 MB: 57.4 us, 4.7 TB/s, of which the tiles' loop 46 us at 5.8).
+// Many rows: the tensor cores' turn of a tile.  At M = 128 a product costs them
+// some 75 to 130 cycles however few its columns, so a tile takes 1280 cycles at
+// 16 columns, 1740 at 48 and 2250 at 80 (32 rows behind 32771 tokens: 61 to
+// 65 us; 256 rows of 32 requests behind up to 16384: 195.5 us, 3.8 TB/s), and a
+// segment's start and end some 8000 to 23000 more.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -1250,7 +1259,11 @@ int launch_attn(const AttnArgs &a, void *stream)
                 : a.bt == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                              : CU_TENSOR_MAP_SWIZZLE_128B))
         return (int)cudaErrorInvalidValue;
-    // columns of a segment: the least shape that holds an average request's rows and one row's heads
+    // Columns of a segment: the least shape that holds an average request's rows
+    // and one row's heads.  One row of 5 heads behind 200 tokens takes 12.3 us
+    // with 16 columns and 14.3 with 48 (the same behind 131072); 8 rows of 5
+    // heads to a request 195 us with 48, 231 with 80 and 348 with 16; 32 rows of
+    // 5 heads 64 us with 80, 71 with 48 and 117 with 16.
     const int64_t avg = (int64_t)((a.R + a.n_req - 1) / a.n_req) * p.G;
     p.cols = avg <= 16 ? 16 : avg <= 48 ? 48 : 80;
     p.fit = p.cols / p.G;

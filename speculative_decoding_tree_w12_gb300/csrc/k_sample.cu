@@ -24,8 +24,15 @@
 // to a row, which goes over it again for every rejection.
 // The CTA that completes the last row writes the accepted paths.
 // The second pass takes the rows in reverse, so that logits past the L2 cache's
-// size are found there as far as it reaches.  Many rows are bound by the issue
-// rate of the sums' pass, some ten instructions a token; few rows by latency.
+// size are found there as far as it reaches.
+//
+// What bounds it.  192 rows of 151936 BF16 tokens (58 MB) take 35 us: 7 for the
+// maxima, 19 for the sums, at the issue rate of some ten instructions a token,
+// 8 for the last rows' draws and the paths, each a chain of loads.  256 FP32
+// rows with a drafter's probabilities (156 MB, and as much of the drafter's for
+// the rows with a rejection) take 109 us: 25 and 30 for the two passes, both at
+// memory speed, 50 for some 40 rejected rows, which are few to spread over the
+// SMs and wait for their slowest.  One row takes 12 us, all of it latency.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -885,7 +892,8 @@ static int64_t chunk_count(int64_t vocab, bool f32, int per)
 
 // Pieces of a thread of the two passes: the most, of powers of two up to 16,
 // that leave every SM eight CTAs.  Few rows are spread over the SMs; many get
-// long stretches, over which a warp's sums and searches weigh less.
+// long stretches, over which a warp's sums and searches weigh less (256 FP32
+// rows: the sums' pass takes 40 us with 16 pieces, 56 with 4).
 static int pieces_per_thread(int64_t R, int64_t vocab, bool f32, int num_sms)
 {
     int per = 16;
@@ -964,8 +972,9 @@ int launch_sample(const SampleArgs &a, void *stream)
     const bool draft = a.draft_p != nullptr;
     const cudaError_t e = a.f32 ? passes_of<true>(cfg, pdl, p, draft) : passes_of<false>(cfg, pdl, p, draft);
     if (e != cudaSuccess || !draft) return (int)e;
-    // a rejection's pass is one row's own, so a row gets all the CTAs a cluster
-    // can have, down to 2048 tokens each
+    // A rejection's pass is one row's own, so a row gets all the CTAs a portable
+    // cluster can have, down to 2048 tokens each.  (Clusters of 16: 256 rows in
+    // 138 us against 121; fewer of them find room at a time.)
     int c = 1;
     while (c < kMaxCluster && a.vocab > 2048 * c) c *= 2;
     p.sub = (int32_t)((pieces_of(a.vocab, a.f32 != 0) + 32ll * c * kWarps - 1) / (32ll * c * kWarps) * 32);
@@ -977,10 +986,6 @@ int launch_sample(const SampleArgs &a, void *stream)
     both[1].val.clusterDim.y = both[1].val.clusterDim.z = 1;
     cfg.attrs = both;
     cfg.numAttrs = 2;
-    // (clusters of more than 8 are for the kernel to allow)
-    static const cudaError_t wide[2] = {cudaFuncSetAttribute(k_sample_draft<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
-                                        cudaFuncSetAttribute(k_sample_draft<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)};
-    if (wide[a.f32 != 0] != cudaSuccess) return (int)wide[a.f32 != 0];
     return (int)(a.f32 ? cudaLaunchKernelEx(&cfg, k_sample_draft<true>, p) : cudaLaunchKernelEx(&cfg, k_sample_draft<false>, p));
 }
 
