@@ -229,46 +229,60 @@ struct Row {
     }
 };
 
-// The accepted paths of requests r0, r0 + step .. (four at most): from the root
+// The accepted paths of requests r0, r0 + step .. (N at most): from the root
 // to the first child in row order that carries the row's token, as far as there
-// is one.  One warp; the first 32 rows of all four are fetched at once.
-__device__ __forceinline__ void accept_paths(const SampleParams &p, int r0, int step, int lane)
+// is one.  One warp; the first 32 rows of all N are fetched at once, and what
+// is in the tree before it is known whether all rows have their tokens.
+template <int N>
+struct Paths {
+    int lo[N], hi[N], parent[N], token[N];
+};
+
+template <int N>
+__device__ __forceinline__ Paths<N> fetch_paths(const SampleParams &p, int r0, int step, int lane)
 {
-    int lo[4], hi[4], parent[4], token[4], drawn[4];
+    Paths<N> t;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
         const int r = r0 + i * step;
-        lo[i] = r < p.n_req ? p.off[r] : 0;
-        hi[i] = r < p.n_req ? p.off[r + 1] : 0;
-        if (lo[i] < 0 || hi[i] > p.R) hi[i] = lo[i];
+        t.lo[i] = r < p.n_req ? p.off[r] : 0;
+        t.hi[i] = r < p.n_req ? p.off[r + 1] : 0;
+        if (t.lo[i] < 0 || t.hi[i] > p.R) t.hi[i] = t.lo[i];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int j = lo[i] + lane;
-        const bool in = j < hi[i];
-        parent[i] = in ? p.parent[j] : -1;
-        token[i] = in ? p.token[j] : -1;
-        drawn[i] = in ? __ldcg(p.row_tok + j) : -1;
+    for (int i = 0; i < N; ++i) {
+        const int j = t.lo[i] + lane;
+        t.parent[i] = j < t.hi[i] ? p.parent[j] : -1;
+        t.token[i] = j < t.hi[i] ? p.token[j] : -1;
     }
+    return t;
+}
+
+template <int N>
+__device__ __forceinline__ void accept_paths(const SampleParams &p, int r0, int step, int lane, const Paths<N> &t)
+{
+    int drawn[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = r0 + i * step;
+    for (int i = 0; i < N; ++i) drawn[i] = t.lo[i] + lane < t.hi[i] ? __ldcg(p.row_tok + t.lo[i] + lane) : -1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int r = r0 + i * step, lo = t.lo[i], hi = t.hi[i];
         if (r >= p.n_req) break;
         int32_t *out = p.acc_tok + (int64_t)r * (p.p_max + 1);
         int n = 0, cur = -1;
-        if (lo[i] < hi[i]) {
-            cur = lo[i];
+        if (lo < hi) {
+            cur = lo;
             for (;;) {
-                const int want = cur - lo[i] < 32 ? __shfl_sync(0xffffffffu, drawn[i], cur - lo[i]) : __ldcg(p.row_tok + cur);
+                const int want = cur - lo < 32 ? __shfl_sync(0xffffffffu, drawn[i], cur - lo) : __ldcg(p.row_tok + cur);
                 if (lane == 0) out[n] = want;
                 ++n;
                 if (n > p.p_max) break;
-                const int j = lo[i] + lane;
-                unsigned b = __ballot_sync(0xffffffffu, j < hi[i] && j > cur && parent[i] == cur && token[i] == want);
-                int next = b ? lo[i] + __ffs(b) - 1 : -1;
-                for (int j0 = max(cur + 1, lo[i] + 32); j0 < hi[i] && next < 0; j0 += 32) {
+                const int j = lo + lane;
+                unsigned b = __ballot_sync(0xffffffffu, j < hi && j > cur && t.parent[i] == cur && t.token[i] == want);
+                int next = b ? lo + __ffs(b) - 1 : -1;
+                for (int j0 = max(cur + 1, lo + 32); j0 < hi && next < 0; j0 += 32) {
                     const int k = j0 + lane;
-                    b = __ballot_sync(0xffffffffu, k < hi[i] && p.parent[k] == cur && p.token[k] == want);
+                    b = __ballot_sync(0xffffffffu, k < hi && p.parent[k] == cur && p.token[k] == want);
                     if (b) next = j0 + __ffs(b) - 1;
                 }
                 if (next < 0) break;
@@ -284,21 +298,31 @@ __device__ __forceinline__ void accept_paths(const SampleParams &p, int r0, int 
 }
 
 // After a CTA's thread has written the row's token: the CTA that writes the
-// last row's goes on to the accepted paths.
+// last row's goes on to the accepted paths, N of a warp at a time.
+template <int N>
 __device__ __forceinline__ void row_done(const SampleParams &p)
 {
     if (!p.acc_tok) return;
     __shared__ int32_t s_last;
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    int r = threadIdx.x >> 5;
+    Paths<N> t = fetch_paths<N>(p, r, warps, lane);
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (p.R > 1) {
+        if (threadIdx.x == 0) {
+            __threadfence();
+            s_last = atomicAdd(p.done, 1) == p.R - 1;
+        }
+        __syncthreads();
+        if (!s_last) return;
         __threadfence();
-        s_last = atomicAdd(p.done, 1) == p.R - 1;
     }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    const int warps = blockDim.x >> 5;
-    for (int r = threadIdx.x >> 5; r < p.n_req; r += 4 * warps) accept_paths(p, r, warps, threadIdx.x & 31);
+    for (;;) {
+        accept_paths(p, r, warps, lane, t);
+        r += N * warps;
+        if (r >= p.n_req) break;
+        t = fetch_paths<N>(p, r, warps, lane);
+    }
 }
 
 // a greedy row's token: the lowest of the chunks' candidates.  One warp.
@@ -429,12 +453,12 @@ __device__ __forceinline__ u64 place(float u, u64 total)
 }
 
 template <bool kF32>
-__device__ __forceinline__ void write_row(const SampleParams &p, int row, int tok, const Row<kF32> &z, const Weigher<kF32> &w, u64 total)
+__device__ __forceinline__ void write_row(const SampleParams &p, int row, int tok, float logit, const Weigher<kF32> &w, u64 total)
 {
     p.row_tok[row] = tok;
     if (p.row_logp) {
         // (a NaN can only be an accepted child's)
-        const float x = fmaxf(z.token(tok), -INFINITY);
+        const float x = fmaxf(logit, -INFINITY);
         p.row_logp[row] = __fsub_rn(x == w.m ? 0.f : __fmul_rn(__fsub_rn(x, w.m), w.inv_t), logf(weight_of(total)));
     }
 }
@@ -459,8 +483,13 @@ __device__ __forceinline__ float row_top(const SampleParams &p, int row, int lan
 // from `first` sum to more than t.  Every warp takes a part of the stretch.
 template <bool kF32, class Piece>
 __device__ __forceinline__ void search(const SampleParams &p, int row, int first, int n, u64 t, const Row<kF32> &z, const Weigher<kF32> &w,
-                                       u64 total, u64 *s_sum, Piece piece)
+                                       u64 total, u64 *s_sum, Piece weigh)
 {
+    uint4 x;                                   // the last piece
+    auto piece = [&](int v, auto &e) {
+        x = z.piece(v);
+        weigh(v, x, e);
+    };
     constexpr int kPer = Row<kF32>::kPer;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int sub = (n + warps - 1) / warps * 32;
@@ -485,7 +514,13 @@ __device__ __forceinline__ void search(const SampleParams &p, int row, int first
     }
     if (!mine) return;
     const int tok = find_token<kPer>(lo, hi, t, z.shift, lane, piece);
-    if (tok >= 0) write_row(p, row, tok, z, w, total);
+    if (tok >= 0) {
+        float logit = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (i == (tok + z.shift) % kPer) logit = Row<kF32>::get(x, i);
+        write_row(p, row, tok, logit, w, total);
+    }
 }
 
 // The sums of a row's stretches, a run of them to a thread.
@@ -542,7 +577,7 @@ __device__ void draw(const SampleParams &p, int row, const Row<kF32> &z, const W
         s_rest = t;
     }
     __syncthreads();
-    search(p, row, s_at * 32 * p.per, p.per, s_rest, z, w, c.total, s_sum, [&](int v, u64 (&e)[kPer / 2]) { w.any_piece(z.piece(v), e); });
+    search(p, row, s_at * 32 * p.per, p.per, s_rest, z, w, c.total, s_sum, [&](int, const uint4 &x, u64 (&e)[kPer / 2]) { w.any_piece(x, e); });
 }
 
 // The row's next child after row j, of those whose token is one.  One warp.
@@ -673,14 +708,15 @@ __global__ void __launch_bounds__(kChunkThreads, 5) k_sample_sum(const SamplePar
             draw(p, row, z, w, c, s_sum);
         } else {
             const int x = p.token[kid];
-            if (!accepted(p.u_accept[kid], __ldg(p.draft_p + row * p.draft_stride + x), w.one(z.token(x)), c.total)) {
+            const float logit = z.token(x);
+            if (!accepted(p.u_accept[kid], __ldg(p.draft_p + row * p.draft_stride + x), w.one(logit), c.total)) {
                 if (first) p.left[atomicAdd(p.n_left, 1)] = {row, top, c.total};
                 return;
             }
-            if (first) write_row(p, row, x, z, w, c.total);
+            if (first) write_row(p, row, x, logit, w, c.total);
         }
     }
-    row_done(p);
+    row_done<4>(p);
 }
 
 // ---------------------------------------------------------------------------
@@ -835,7 +871,7 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
     // ---- the row's token
     bool writes = rank == 0;                                        // this CTA has it
     if (took >= 0) {
-        if (writes && tid == 0) write_row(p, row, p.token[took], z, w, job.total);
+        if (writes && tid == 0) write_row(p, row, p.token[took], z.token(p.token[took]), w, job.total);
     } else if (rounds == 0) {                                       // p = q
         if (writes) draw(p, row, z, w, scan_row(p, row, s.wsum[buf ^ 1]), s.wsum[buf ^ 1]);
     } else {
@@ -848,10 +884,10 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
             int wi = 0;
             while (wi < kWarps - 1 && r >= s.wsum[buf][wi]) r -= s.wsum[buf][wi++];
             search(p, row, (rank * kWarps + wi) * p.sub, p.sub / 32, r, z, w, job.total, s.wsum[buf ^ 1],
-                   [&](int v, u64 (&e)[kPer / 2]) { weights(z.piece(v), drafts(v), e); });
+                   [&](int v, const uint4 &x, u64 (&e)[kPer / 2]) { weights(x, drafts(v), e); });
         }
     }
-    if (writes) row_done(p);
+    if (writes) row_done<1>(p);                                     // (a CTA of twice the warps)
 }
 
 template <bool kF32>
