@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (warp * 32 < p.n_req) scan(incl, tiles, segs);
     if (lane == 31) s.list.units[warp] = incl, s.list.tiles[warp] = tiles, s.list.segs[warp] = segs;
-    if (tid == 0) {
+    if (tid == 96) {                                      // (a warp that has nothing else to do here)
         s.abort = 0;
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(bar(s.k_full[i]), 1);
@@ -587,8 +587,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int blk2;
                 float2 sc2;
                 fetch(b + 32 + lane, blk2, sc2);
-                float top = sc.y;                             // the tile's largest V scale
-                for (int d = 1; d < nb; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                 const int row = is_k ? (blk * p.H + g.h) << bs : (blk * p.H + g.h) * kD;   // of the pool seen as rows
                 for (int l = 0; l < 32 && b + l < b1; l += nb, ++j) {
                     const int n = min(nb, b1 - (b + l));      // blocks of this tile that hold tokens
@@ -596,17 +594,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t f = full + st * 8;
                     ok = __all_sync(0xffffffffu, wait_phase(empty + st * 8, par, to, p.status, abort));
                     if (!ok) break;
-                    if (is_k) {
-                        if (in) s.scale[j % kScaleRing][lane - l] = sc;
-                        if (lane == l) s.top_v[j % kScaleRing] = top;
-                        __syncwarp();
-                    }
-                    if (lane == l) mbar_expect_tx(f, n * bytes);
-                    __syncwarp();
+                    // the copies first: a segment's first scales are still on their
+                    // way, and the phase stays open until this warp's arrival
                     if (in && lane < l + n) {
                         const uint32_t dst = tile0 + st * T::kKBytes + (uint32_t)(lane - l) * bytes;
                         tma_load_2d(dst, is_k ? &kmap : &vmap, 0, row, f);
                     }
+                    if (is_k) {
+                        float top = sc.y;                     // the tile's largest V scale
+                        for (int d = 1; d < nb; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        if (in) s.scale[j % kScaleRing][lane - l] = sc;
+                        if (lane == l) s.top_v[j % kScaleRing] = top;
+                    }
+                    __syncwarp();
+                    if (lane == l) mbar_expect_tx(f, n * bytes);
                     if (++st == (uint32_t)stages) st = 0, par ^= 1;
                 }
                 blk = blk2;
