@@ -81,6 +81,7 @@ constexpr int kStack = 48;                 // columns up to which Q's pieces are
 constexpr int kMaxCols = 80;               // query columns of a segment, see Shape
 constexpr int kScaleRing = 16;             // tiles whose block scales are kept (the copies run at most 8 ahead of their readers)
 constexpr int kMaxReq = kMaxBudget;
+constexpr int kLead = 9;                   // a segment's start and end in tiles: 7 of 16 columns, 10 of 48 and 80
 constexpr uint64_t kDrainNs = 1000000000;  // limit of the waits after a failed one
 constexpr int kSoft = 512;                 // softmax threads, in four warpgroups
 constexpr int kThreads = 128 + kSoft + 256; // warps: 0 K copies, 1 scores, 2 V copies, 3 sums, 4-19 softmax, 20-27 V to F16
@@ -108,7 +109,6 @@ struct AttnParams {
     RopeArgs rope;
     float scale2;                           // softmax scale * log2(e)
     uint16_t *out;
-    int32_t *plan;                          // [n_req + 1] where every request starts in the list; tiles of a lead; whether tiles are weighted
     float *part;                            // [R * Hq + ctas * cols][kD] sums
     float2 *ml;                             // [R * Hq + ctas * cols] maximum (log2), normaliser
     int32_t *status;
@@ -135,6 +135,42 @@ __device__ __forceinline__ bool request_ok(const AttnParams &p, int r, int &lo, 
     rows = hi - lo;
     return lo >= 0 && hi <= p.R && rows >= 0 && len >= 0 && (int64_t)len <= (int64_t)p.max_blocks * p.bt;
 }
+
+// What requests have in the list: tiles, the same weighted, weighted segments.
+struct List {
+    int64_t tiles, units;
+    int32_t segs;
+    __device__ __forceinline__ void add(const List &o) { tiles += o.tiles, units += o.units, segs += o.segs; }
+};
+
+__device__ __forceinline__ List list_of(const AttnParams &p, int rows, int len)
+{
+    List l{0, 0, 0};
+    if (rows > 0 && len > 0) {
+        const int w = tile_weight(p, rows), segs = p.H * group_count(rows, p.fit);
+        l.tiles = (int64_t)((len + kTile - 1) / kTile) * segs;
+        l.units = l.tiles * w;
+        l.segs = segs * w;
+    }
+    return l;
+}
+
+// How the whole list is cut: the lead of a segment, and whether tiles are
+// weighted.  Every CTA starts one segment, whatever it does.  A lead counts
+// where it goes on to another, and would only waste shares of a few tiles;
+// those are also too small for weights (a share has to have a tile of every
+// segment that it lies in).
+struct Cut {
+    int32_t lead;
+    bool weighted;
+    __device__ __forceinline__ Cut(const AttnParams &p, const List &all)
+    {
+        lead = (int32_t)min((int64_t)kLead, all.tiles / p.ctas / 4);
+        weighted = lead > 0 && all.units + (int64_t)lead * all.segs <= INT32_MAX;
+        if (!weighted) lead = 0;
+    }
+    __device__ __forceinline__ int64_t length(const List &l) const { return weighted ? l.units + (int64_t)lead * l.segs : l.tiles; }
+};
 
 // Four consecutive elements d0 .. d0 + 3 of a BF16 row and what turns them by
 // position pos; loaded apart from the arithmetic, so that the loads of several
@@ -236,7 +272,6 @@ struct Shape {
 
 constexpr int kMaxStages = 6;
 constexpr int kRowBits = 10;                                 // of a request's row count
-constexpr int kLead = 9;                                     // a segment's start and end in tiles: 7 of 16 columns, 10 of 48 and 80
 
 struct Shared {
     uint64_t k_full[kMaxStages], k_empty[kMaxStages];  // K and V tiles loaded / consumed
@@ -251,10 +286,7 @@ struct Shared {
     alignas(16) float delta[2][kMaxCols];              // the factor of its last raise; at the end, of the group's sums
     union {
         alignas(16) float red[2][4][kMaxCols];         // per warp
-        struct {                                       // before: the list's sums, per warp
-            int64_t units[kThreads / 32], tiles[kThreads / 32];
-            int32_t segs[kThreads / 32];
-        } list;
+        List list[kThreads / 32];                      // before: a warp's requests
     };
     float lsum[2][kMaxCols];                           // normalisers
     float sref[2];
@@ -444,33 +476,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     pdl_launch_dependents();                              // the join may start wherever there is room
     // ---- the tile list: tiles of every request, summed up
-    int64_t tiles = 0, incl = 0;                          // as they are; weighted
-    int32_t segs = 0;                                     // weighted
-    int w = 1;
+    List incl{0, 0, 0};
     if (tid < p.n_req) {
         int lo, rows, len;
-        if (request_ok(p, tid, lo, rows, len))
-            segs = len ? p.H * group_count(rows, p.fit) : 0;
-        else
+        if (!request_ok(p, tid, lo, rows, len)) {
+            rows = 0;
             fail(p.status);
-        if (segs) w = tile_weight(p, rows);
-        tiles = (int64_t)((len + kTile - 1) / kTile) * segs;
-        segs *= w;
-        incl = tiles * w;
+        }
+        incl = list_of(p, rows, len);
         s.lo[tid] = (uint16_t)lo;
-        s.rows[tid] = (uint16_t)(rows | w << kRowBits);
+        s.rows[tid] = (uint16_t)(rows | (rows ? tile_weight(p, rows) : 1) << kRowBits);
         s.len[tid] = len;
     }
-    auto scan = [&](int64_t &a, int64_t &b, int32_t &c) {  // over a warp
+    auto scan = [&](List &l) {                            // over a warp
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, b, d);
-            const int32_t z = __shfl_up_sync(0xffffffffu, c, d);
-            if (lane >= d) a += x, b += y, c += z;
+            const List o{__shfl_up_sync(0xffffffffu, l.tiles, d), __shfl_up_sync(0xffffffffu, l.units, d), __shfl_up_sync(0xffffffffu, l.segs, d)};
+            if (lane >= d) l.add(o);
         }
     };
-    if (warp * 32 < p.n_req) scan(incl, tiles, segs);
-    if (lane == 31) s.list.units[warp] = incl, s.list.tiles[warp] = tiles, s.list.segs[warp] = segs;
+    auto from = [&](const List &l, int i) -> List {
+        return {__shfl_sync(0xffffffffu, l.tiles, i), __shfl_sync(0xffffffffu, l.units, i), __shfl_sync(0xffffffffu, l.segs, i)};
+    };
+    if (warp * 32 < p.n_req) scan(incl);
+    if (lane == 31) s.list[warp] = incl;
     if (tid == 96) {                                      // (a warp that has nothing else to do here)
         s.abort = 0;
         for (int i = 0; i < kMaxStages; ++i) {
@@ -497,46 +526,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     // what the warps before had, and all
     static_assert(kThreads / 32 <= 32, "a warp's sums to a lane");
-    const int held = lane * 32 < p.n_req ? lane : -1;     // (a warp without requests has nothing)
-    int64_t all = held < 0 ? 0 : s.list.units[held], all_tiles = held < 0 ? 0 : s.list.tiles[held];
-    int32_t all_segs = held < 0 ? 0 : s.list.segs[held];
+    List all{0, 0, 0};
+    if (lane * 32 < p.n_req) all = s.list[lane];          // (a warp without requests has nothing)
     if (p.n_req > 32) {
-        scan(all, all_tiles, all_segs);
-        if (warp) {
-            incl += __shfl_sync(0xffffffffu, all, warp - 1);
-            tiles += __shfl_sync(0xffffffffu, all_tiles, warp - 1);
-            segs += __shfl_sync(0xffffffffu, all_segs, warp - 1);
-        }
+        scan(all);
+        if (warp) incl.add(from(all, warp - 1));
     }
-    const int last = p.n_req > 32 ? 31 : 0;
-    all = __shfl_sync(0xffffffffu, all, last);
-    all_tiles = __shfl_sync(0xffffffffu, all_tiles, last);
-    all_segs = __shfl_sync(0xffffffffu, all_segs, last);
-    // Every CTA starts one segment, whatever it does.  A lead counts where it
-    // goes on to another, and would only waste shares of a few tiles; those are
-    // also too small for weights (a share has to have a tile of every segment
-    // that it lies in).
-    int32_t lead = (int32_t)min((int64_t)kLead, all_tiles / p.ctas / 4);
-    const bool weighted = lead > 0 && all + (int64_t)lead * all_segs <= INT32_MAX;
-    if (weighted) {
-        incl += (int64_t)lead * segs;
-        all += (int64_t)lead * all_segs;
-    } else {
-        incl = tiles;
-        all = all_tiles;
-        lead = 0;
-    }
-    const bool fits = all <= INT32_MAX;                   // else there is nothing to do but say so
+    all = from(all, p.n_req > 32 ? 31 : 0);
+    const Cut cut(p, all);
+    const bool fits = cut.length(all) <= INT32_MAX;                   // else there is nothing to do but say so
     if (!fits && tid == 0) atomicCAS(p.status, 0, (int32_t)W12_E_UNSUPPORTED);
-    if (tid < p.n_req) s.pre[tid + 1] = fits ? (int32_t)incl : 0;
-    if (tid == 0) s.pre[0] = 0, s.lead = lead, s.weighted = weighted;
+    if (tid < p.n_req) s.pre[tid + 1] = fits ? (int32_t)cut.length(incl) : 0;
+    if (tid == 0) s.pre[0] = 0, s.lead = cut.lead, s.weighted = cut.weighted;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     const int32_t total = s.pre[p.n_req];
-    if (cta == 0)
-        for (int i = tid; i <= p.n_req + 2; i += kThreads) p.plan[i] = i <= p.n_req ? s.pre[i] : i == p.n_req + 1 ? lead : weighted;
     const int64_t share = ((int64_t)total + p.ctas - 1) / p.ctas;
     const int32_t first = (int32_t)min((int64_t)total, cta * share), end = (int32_t)min((int64_t)total, first + share);
     const int bs = p.bt == 32 ? 5 : p.bt == 64 ? 6 : 7;   // log2 of a block's tokens
@@ -1033,6 +1039,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const AttnPara
     __shared__ float ss[kJoinWarps][kPath + 3];               // scores
     __shared__ int32_t s_parent[kMaxBudget], s_path[kPath + 1], s_n;
     __shared__ uint8_t s_depth[kMaxBudget];
+    __shared__ int32_t s_cta0, s_cta1;                        // the shares that hold a part of this row's segment
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
     const int row = blockIdx.x, h = blockIdx.y, G = p.G;
     int r = p.req[row];
@@ -1041,7 +1048,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const AttnPara
         s_depth[j] = p.depth[j];
     }
     int lo = 0, rows = 1, len = 0;
-    if (r < 0 || r >= p.n_req || !request_ok(p, r, lo, rows, len) || row < lo || row >= lo + rows) r = -1;
+    if (r < 0 || r >= p.n_req || !request_ok(p, r, lo, rows, len) || row < lo || row >= lo + rows)
+        r = -1, lo = row, rows = 1, len = 0;
     __syncthreads();
     // a position on the table (or none)
     auto placed = [&](int j) { return p.rope.rot == 0 || len + (int)s_depth[j] < p.rope.max_pos; };
@@ -1069,6 +1077,32 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const AttnPara
             if (!ok || off) fail(p.status);
         }
     }
+    const int ng = group_count(rows, p.fit), per = (rows + ng - 1) / ng, i0 = row - lo, grp = i0 / per;
+    if (warp == warps - 1) {                            // the list again, as k_attn_ctx cuts it
+        List all{0, 0, 0}, before{0, 0, 0};
+        for (int i = lane; i < p.n_req; i += 32) {
+            int l, n, c;
+            if (!request_ok(p, i, l, n, c)) continue;
+            const List mine = list_of(p, n, c);
+            all.add(mine);
+            if (i < r) before.add(mine);
+        }
+        auto sum = [&](List &l) {
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                l.add({__shfl_xor_sync(0xffffffffu, l.tiles, d), __shfl_xor_sync(0xffffffffu, l.units, d), __shfl_xor_sync(0xffffffffu, l.segs, d)});
+        };
+        sum(all);
+        sum(before);
+        const Cut cut(p, all);
+        const int64_t total = cut.length(all), share = max((int64_t)1, (total + p.ctas - 1) / p.ctas);
+        const int nt = total <= INT32_MAX ? (len + kTile - 1) / kTile : 0, w = cut.weighted ? tile_weight(p, rows) : 1;
+        const int64_t a0 = cut.length(before) + ((int64_t)(h * ng + grp) * (nt + cut.lead) + cut.lead) * w;
+        if (lane == 0) {
+            s_cta0 = (int)(a0 / share);
+            s_cta1 = nt ? (int)((a0 + (int64_t)(nt - 1) * w) / share) : -1;
+        }
+    }
     __syncthreads();
     const int nA = s_n;
     uint16_t *o = p.out + ((int64_t)row * p.Hq + h * G) * kD;
@@ -1084,7 +1118,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const AttnPara
         *reinterpret_cast<float4 *>(sk + a * kJoinKey + lane * 4) = turn4(kw);
     }
     __syncthreads();
-    const int ng = group_count(rows, p.fit), per = (rows + ng - 1) / ng, i0 = row - lo, grp = i0 / per;
     bool waited = false;
     for (int g = warp; g < G; g += warps) {
         if (g >= warps)                                 // (the first is on its way)
@@ -1134,12 +1167,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const AttnPara
         }
         if (!waited) pdl_wait();                        // the context's parts from here on
         waited = true;
-        // the shares that hold a part of this row's segment
-        const int64_t total = __ldcg(p.plan + p.n_req), share = (total + p.ctas - 1) / p.ctas;
-        const int nt = total ? (len + kTile - 1) / kTile : 0;
-        const int lead = __ldcg(p.plan + p.n_req + 1), w = __ldcg(p.plan + p.n_req + 2) ? tile_weight(p, rows) : 1;
-        const int64_t a0 = __ldcg(p.plan + r) + ((int64_t)(h * ng + grp) * (nt + lead) + lead) * w;
-        const int cta0 = nt ? (int)(a0 / share) : 0, cta1 = nt ? (int)((a0 + (int64_t)(nt - 1) * w) / share) : -1;
+        const int cta0 = s_cta0, cta1 = s_cta1;
         const int64_t col = (int64_t)lo * p.Hq + (int64_t)(h * rows + i0) * G + g;
         for (int c = cta0; c <= cta1; c += kJoinParts) {
             float2 ml[kJoinParts];
@@ -1187,7 +1215,6 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-size_t plan_bytes() { return (size_t)((kMaxReq + 3) * 4 + 255) / 256 * 256; }
 size_t part_columns(int32_t R, int32_t Hq, int ctas) { return (size_t)R * Hq + (size_t)ctas * kMaxCols; }
 
 }  // namespace
@@ -1198,7 +1225,7 @@ size_t attn_ws_bytes(int32_t R, int32_t Hq, int32_t H, int32_t n_req, int num_sm
 {
     (void)H;
     (void)n_req;
-    return plan_bytes() + part_columns(R, Hq, num_sms) * (kD * 4 + 8);
+    return part_columns(R, Hq, num_sms) * (kD * 4 + 8);
 }
 
 int launch_attn(const AttnArgs &a, void *stream)
@@ -1234,9 +1261,8 @@ int launch_attn(const AttnArgs &a, void *stream)
     p.out = a.out;
     uint8_t *w = static_cast<uint8_t *>(a.work);
     const size_t cols = part_columns(a.R, a.Hq, p.ctas);
-    p.plan = reinterpret_cast<int32_t *>(w);
-    p.part = reinterpret_cast<float *>(w + plan_bytes());
-    p.ml = reinterpret_cast<float2 *>(w + plan_bytes() + cols * kD * 4);
+    p.part = reinterpret_cast<float *>(w);
+    p.ml = reinterpret_cast<float2 *>(w + cols * kD * 4);
     p.status = a.status;
     p.timeout_ns = a.timeout_ns;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
