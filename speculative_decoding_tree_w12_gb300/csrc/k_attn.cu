@@ -165,7 +165,7 @@ struct Cut {
     bool weighted;
     __device__ __forceinline__ Cut(const AttnParams &p, const List &all)
     {
-        lead = (int32_t)min((int64_t)kLead, all.tiles / p.ctas / 4);
+        lead = (int32_t)min((uint32_t)kLead, (uint32_t)min(all.tiles, (int64_t)INT32_MAX) / (4u * p.ctas));   // (no 64-bit division)
         weighted = lead > 0 && all.units + (int64_t)lead * all.segs <= INT32_MAX;
         if (!weighted) lead = 0;
     }
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     const int32_t total = s.pre[p.n_req];
-    const int64_t share = ((int64_t)total + p.ctas - 1) / p.ctas;
+    const int64_t share = ((uint32_t)total + p.ctas - 1) / p.ctas;
     const int32_t first = (int32_t)min((int64_t)total, cta * share), end = (int32_t)min((int64_t)total, first + share);
     const int bs = p.bt == 32 ? 5 : p.bt == 64 ? 6 : 7;   // log2 of a block's tokens
     const int nb = kTile >> bs;                           // blocks of a tile
