@@ -499,7 +499,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         return {__shfl_sync(0xffffffffu, l.tiles, i), __shfl_sync(0xffffffffu, l.units, i), __shfl_sync(0xffffffffu, l.segs, i)};
     };
     if (warp * 32 < p.n_req) scan(incl);
-    if (lane == 31) s.list[warp] = incl;
     if (tid == 96) {                                      // (a warp that has nothing else to do here)
         s.abort = 0;
         for (int i = 0; i < kMaxStages; ++i) {
@@ -523,21 +522,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&vmap);
     }
     if (warp == 1) tmem_alloc(smem_u32(&s.tmem), T::kTmCols);
-    __syncthreads();
-    // what the warps before had, and all
-    static_assert(kThreads / 32 <= 32, "a warp's sums to a lane");
-    List all{0, 0, 0};
-    if (lane * 32 < p.n_req) all = s.list[lane];          // (a warp without requests has nothing)
-    if (p.n_req > 32) {
+    List all;
+    const bool one = p.n_req <= 32;                       // one warp has all requests
+    if (one) {
+        all = from(incl, 31);
+    } else {                                              // what the warps before had, and all
+        static_assert(kThreads / 32 <= 32, "a warp's sums to a lane");
+        if (lane == 31) s.list[warp] = incl;
+        __syncthreads();
+        all = lane * 32 < p.n_req ? s.list[lane] : List{0, 0, 0};
         scan(all);
         if (warp) incl.add(from(all, warp - 1));
+        all = from(all, 31);
     }
-    all = from(all, p.n_req > 32 ? 31 : 0);
-    const Cut cut(p, all);
-    const bool fits = cut.length(all) <= INT32_MAX;                   // else there is nothing to do but say so
-    if (!fits && tid == 0) atomicCAS(p.status, 0, (int32_t)W12_E_UNSUPPORTED);
-    if (tid < p.n_req) s.pre[tid + 1] = fits ? (int32_t)cut.length(incl) : 0;
-    if (tid == 0) s.pre[0] = 0, s.lead = cut.lead, s.weighted = cut.weighted;
+    if (!one || warp == 0) {
+        const Cut cut(p, all);
+        const bool fits = cut.length(all) <= INT32_MAX;   // else there is nothing to do but say so
+        if (!fits && tid == 0) atomicCAS(p.status, 0, (int32_t)W12_E_UNSUPPORTED);
+        if (tid < p.n_req) s.pre[tid + 1] = fits ? (int32_t)cut.length(incl) : 0;
+        if (tid == 0) s.pre[0] = 0, s.lead = cut.lead, s.weighted = cut.weighted;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
