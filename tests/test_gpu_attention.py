@@ -288,6 +288,28 @@ def test_attention(w12, lens, rows, H, G, bt, rot, adjacent, chain):
     assert torch.equal(out, again)
 
 
+def _many(n, seed):
+    g = np.random.default_rng(seed)
+    return [int(x) for x in g.integers(0, 5000, n)], [int(x) for x in g.integers(1, 5, n)]
+
+
+# enough tiles that the split counts segments and columns: few long requests whose
+# rows need several groups, some without tokens; more requests than a warp has lanes
+LONG = [([9000, 3001, 0, 12345, 700], [8, 12, 2, 1, 30], 4, 5, 64), _many(40, 1) + (2, 4, 32), ([40000], [3], 2, 8, 128),
+        _many(70, 2) + (1, 8, 64)]
+
+
+@pytest.mark.parametrize("lens,rows,H,G,bt", LONG)
+def test_attention_long(w12, lens, rows, H, G, bt):
+    s = World(w12, lens, H, bt, 64, False, seed=16)
+    t = make_tree(s.g, rows)
+    q, k, v, dev = inputs(s.g, len(t[0]), H, G, s)
+    out = attend(w12, s, t, dev, H, G, len(lens))
+    assert s.ws.status() == 0
+    close(out, *ref.tree_attention(s.host, t[0], t[1], t[2], q, k, v, s.cos, s.sin, False, D ** -0.5))
+    assert torch.equal(out, attend(w12, s, t, dev, H, G, len(lens)))
+
+
 def test_attention_scales_and_sinks(w12):
     """Blocks whose scales differ by 2^20, a key every row attends to most, and a large softmax scale."""
     s = World(w12, [600], 1, 64, rot=0, seed=12)
