@@ -117,6 +117,19 @@ def test_sampled_verification(w12, rows, vocab, draft, chain, f32, temp):
         assert undecided <= 1 + len(t[0]) // 4
 
 
+# rows and vocabularies that give a thread 2, 4, 8 and 16 pieces of a row
+MANY = [([45], 60000, False, False, True, None), ([20] * 6, 70001, True, False, True, None),
+        ([10] * 24, 151936, False, False, False, None), ([1] * 260, 151936, False, True, True, None),
+        ([6] * 20, 140001, True, False, False, None)]
+
+
+@pytest.mark.parametrize("rows,vocab,draft,chain,f32,temp", MANY)
+def test_sampled_verification_of_many_rows(w12, rows, vocab, draft, chain, f32, temp):
+    g = np.random.default_rng(vocab + 1)
+    t, z, zt, q, token, u = draw(g, rows, vocab, draft, chain, f32)
+    check(w12, t, z, zt, q if draft else None, token, u, temp)
+
+
 def test_exact_boundaries(w12):
     """Equal logits: every weight is 2^40, so token floor(u V) is the answer without any rounding."""
     for V in (4, 1000, 4096, 150000):
