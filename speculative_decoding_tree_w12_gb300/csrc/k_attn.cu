@@ -113,6 +113,7 @@ struct AttnParams {
     float2 *ml;                             // [R * Hq + ctas * cols] maximum (log2), normaliser
     int32_t *status;
     uint64_t timeout_ns;                    // a wait's limit
+    int32_t debug_flags;                    // bit 0: CTA 0 never copies a key (test hook)
 };
 
 __device__ __forceinline__ void fail(int32_t *status) { atomicCAS(status, 0, (int32_t)W12_E_INVAL); }
@@ -574,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t j = 0, st = 0, par = 1;                      // tile, its stage, the parity its stage's last use left
         bool ok = true;
         Seg g;
-        for (int32_t at = first; ok && next_segment(p, s, at, end, g);) {
+        const bool withheld = is_k && cta == 0 && (p.debug_flags & 1);
+        for (int32_t at = withheld ? end : first; ok && next_segment(p, s, at, end, g);) {
             const int b0 = g.t0 * nb, b1 = min((g.len + p.bt - 1) >> bs, g.t1 * nb);
             const int32_t *table = p.table + (int64_t)g.r * p.max_blocks;
             int blk = 0;
@@ -1269,6 +1271,7 @@ int launch_attn(const AttnArgs &a, void *stream)
     p.ml = reinterpret_cast<float2 *>(w + cols * kD * 4);
     p.status = a.status;
     p.timeout_ns = a.timeout_ns;
+    p.debug_flags = a.debug_flags;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
 
     EncodeTiledFn fn = encode_fn();

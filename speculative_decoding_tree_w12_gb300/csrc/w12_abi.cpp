@@ -1064,6 +1064,7 @@ w12_status w12_tree_attention(const w12_kv_cache *cache, const w12_rope *rope, c
     a.work = aws;
     a.status = W.status();
     a.timeout_ns = g_timeout_ns;
+    a.debug_flags = g_debug_flags;
     return cuda_status(launch_attn(a, stream));
 }
 

@@ -212,6 +212,7 @@ struct AttnArgs {
     uint16_t *out;                  // [R][Hq][kKvDim] BF16
     void *work;                     // attn_ws_bytes
     int32_t *status;
+    int32_t debug_flags;
     uint64_t timeout_ns;
 };
 size_t attn_ws_bytes(int32_t R, int32_t Hq, int32_t H, int32_t n_req, int num_sms);

@@ -362,6 +362,26 @@ def test_zero_values_and_extreme_queries(w12):
     close(attend(w12, s, t, dev, 1, 2, 1), *ref.tree_attention(s.host, t[0], t[1], t[2], q, k, v, None, None, False, 0.1))
 
 
+@pytest.mark.parametrize("G", [1, 5, 16])
+def test_attention_wait_times_out_cleanly(w12, G):
+    """CTA 0 never copies a key (test hook): the scores' wait runs out after
+    50 ms, every warp stops, tensor memory is released, the status word reads
+    W12_E_TIMEOUT, and the same call without the hook matches the 64-bit form."""
+    s = World(w12, [3000], 1, 64, rot=0, seed=17)
+    t = make_tree(s.g, [4])
+    q, k, v, dev = inputs(s.g, 4, 1, G, s)
+    w12.debug_set(1, 50_000_000)
+    try:
+        attend(w12, s, t, dev, 1, G, 1)
+        torch.cuda.synchronize()
+        assert s.ws.status() == w12.W12_E_TIMEOUT
+    finally:
+        w12.debug_set(0, 0)
+    out = attend(w12, s, t, dev, 1, G, 1)
+    assert s.ws.status() == 0
+    close(out, *ref.tree_attention(s.host, t[0], t[1], t[2], q, k, v, None, None, False, D ** -0.5))
+
+
 def test_attention_device_checks(w12):
     def spoil_parent(s, t):
         t[0][4] = 5
