@@ -26,13 +26,14 @@
 // The second pass takes the rows in reverse, so that logits past the L2 cache's
 // size are found there as far as it reaches.
 //
-// What bounds it.  192 rows of 151936 BF16 tokens (58 MB) take 35 us: 7 for the
-// maxima, 19 for the sums, at the issue rate of some ten instructions a token,
-// 8 for the last rows' draws and the paths, each a chain of loads.  256 FP32
-// rows with a drafter's probabilities (156 MB, and as much of the drafter's for
-// the rows with a rejection) take 109 us: 25 and 30 for the two passes, both at
-// memory speed, 50 for some 40 rejected rows, which are few to spread over the
-// SMs and wait for their slowest.  One row takes 12 us, all of it latency.
+// What bounds it.  192 rows of 151936 BF16 tokens (58 MB) take 41 us: 7 for the
+// maxima, 25 for the sums, at the issue rate of some twenty instructions a
+// token, half of them expf, 8 for the last rows' draws and the paths, each a
+// chain of loads.  256 FP32 rows with a drafter's probabilities (156 MB, and as
+// much of the drafter's for the rows with a rejection) take 121 to 129 us: 25
+// and 38 for the two passes, 55 for some 40 rejected rows, which are few to
+// spread over the SMs and wait for their slowest.  One row takes 10 us, all of
+// it latency.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -347,8 +348,6 @@ struct Temper {
     bool ok, greedy;
 };
 
-constexpr float kLog2e = 1.4426950408889634f;
-
 __device__ __forceinline__ Temper temper(const SampleParams &p, int row)
 {
     const int r = p.req[row];
@@ -356,34 +355,28 @@ __device__ __forceinline__ Temper temper(const SampleParams &p, int row)
     t.ok = r >= 0 && r < p.n_req;
     const float T = t.ok && p.temperature ? p.temperature[r] : 1.f;
     t.inv_t = __fdiv_rn(1.f, T);
-    t.greedy = !(T > 0.f) || !(t.inv_t * kLog2e < INFINITY);            // (1 / T over the numbers' range: next to nothing)
+    t.greedy = !(T > 0.f) || t.inv_t == INFINITY;                       // (1 / T over the numbers' range: next to nothing)
     return t;
 }
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// exp((x - m) / T) as 2^((x - m) c): the difference first, so that its rounding
-// and c's count by the distance from the largest logit, not by its size.  With
-// the machine's 2^x (2^-22) a weight is within 2^-22 (1 + 1.5 |x - m| / T) of
-// its value, and the sums' pass takes six instructions a token less than with
-// expf (192 rows of 151936 tokens: 40 -> 35 us).
+// exp(z - m), z = logit / T.  With 10^5 tokens the next boundary of the CDF is
+// as near as 10^-6 of the mass, so the weights have to be as good as FP32 gives
+// them: expf, the largest part of the sums' pass.  (The machine's own 2^x would
+// take six instructions a token less, 192 rows 35 us instead of 40, and drew
+// another token than FP32's exponentials in one row of 200.)
 template <bool kF32>
 struct Weigher {
     static constexpr int kPer = Row<kF32>::kPer;
-    static constexpr float kLeast = -126.f;    // (also what a NaN becomes: a weight of nothing)
-    float inv_t, c, m;                         // m: the largest logit
-    __device__ Weigher(float inv_t_, float top) : inv_t(inv_t_), c(inv_t_ * kLog2e), m(top) {}
+    static constexpr float kLeast = -128.f;    // (also what a NaN becomes: a weight of nothing)
+    float inv_t, m;                            // m: the largest z
+    __device__ Weigher(float inv_t_, float top) : inv_t(inv_t_), m(top * inv_t_) {}   // (a positive factor keeps the order)
     __device__ __forceinline__ float one(float x) const
     {
-        if (m == INFINITY) return x == INFINITY ? 1.f : 0.f;            // nothing but the infinite ones counts
-        return ex2(fmaxf(__fmul_rn(__fsub_rn(x, m), c), kLeast));
+        const float z = __fmul_rn(x, inv_t);
+        if (m == INFINITY) return z == INFINITY ? 1.f : 0.f;            // nothing but the infinite ones counts
+        return expf(fmaxf(__fsub_rn(z, m), kLeast));
     }
-    // of a piece's tokens, in pairs; kInf: there are infinite logits
+    // of a piece's tokens, in pairs; kInf: there are infinite z
     template <bool kInf = false>
     __device__ __forceinline__ void piece(const uint4 &x, u64 (&e)[kPer / 2]) const
     {
@@ -393,9 +386,9 @@ struct Weigher {
                 e[i / 2] = pair(one(Row<kF32>::get(x, i)), one(Row<kF32>::get(x, i + 1)));
                 continue;
             }
-            const u64 d = add2(pair(Row<kF32>::get(x, i), Row<kF32>::get(x, i + 1)), pair(-m, -m));
-            const float2 t = unpair(mul2(d, pair(c, c)));
-            e[i / 2] = pair(ex2(fmaxf(t.x, kLeast)), ex2(fmaxf(t.y, kLeast)));
+            // (a product and a difference of two would be fused, and round once)
+            const float2 z = unpair(mul2(pair(Row<kF32>::get(x, i), Row<kF32>::get(x, i + 1)), pair(inv_t, inv_t)));
+            e[i / 2] = pair(expf(fmaxf(__fsub_rn(z.x, m), kLeast)), expf(fmaxf(__fsub_rn(z.y, m), kLeast)));
         }
     }
     __device__ __forceinline__ void any_piece(const uint4 &x, u64 (&e)[kPer / 2]) const
@@ -458,8 +451,8 @@ __device__ __forceinline__ void write_row(const SampleParams &p, int row, int to
     p.row_tok[row] = tok;
     if (p.row_logp) {
         // (a NaN can only be an accepted child's)
-        const float x = fmaxf(logit, -INFINITY);
-        p.row_logp[row] = __fsub_rn(x == w.m ? 0.f : __fmul_rn(__fsub_rn(x, w.m), w.inv_t), logf(weight_of(total)));
+        const float x = __fmul_rn(fmaxf(logit, -INFINITY), w.inv_t);
+        p.row_logp[row] = __fsub_rn(x == w.m ? 0.f : __fsub_rn(x, w.m), logf(weight_of(total)));
     }
 }
 
