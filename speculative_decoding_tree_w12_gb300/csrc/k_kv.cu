@@ -430,17 +430,20 @@ int launch_kv_write(const KvArgs &a, void *stream)
     p.len_out = a.len_out;
     p.arrive = a.arrive;
     p.status = a.status;
-    // Heads of a CTA: as many as leave every SM two rounds of its threads' worth
-    // of CTAs (each head more shares the staged tables and hides the next one's
-    // loads; fewer spread a short prompt).  16 prompts of up to 8192 tokens: all
-    // 8 heads to a CTA 125 us, half a round's worth (4 or 5) 138.
     const bool commit = a.acc_node != nullptr;
     // blocks that one request's new tokens can touch: n tokens reach over at
     // most (n - 1) / bt + 2 of them
     p.items = kMaxDepth / a.bt + 2;
     const int64_t x = commit ? (int64_t)a.n_req * p.items : (int64_t)a.n_rows / a.bt + 2ll * a.n_req;
-    const int64_t blocks = commit ? a.n_req : std::max<int64_t>(a.n_rows / a.bt, 1);
-    p.heads = (int32_t)std::min<int64_t>(a.H, std::max<int64_t>(1, blocks * a.H * a.bt / (256 * a.num_sms)));
+    // Heads of a CTA: so many that all touched blocks' CTAs fit the SMs at once
+    // (128 / bt of them an SM), since a CTA spends some 4 us on finding its
+    // block and staging the tables before its first head, and a head's loads
+    // hide behind the head before.  24 prompts of 700 tokens at most, blocks of
+    // 32: all 4 heads to a CTA 16.6 us, one 18.2; 16 of up to 8192 tokens: all
+    // 8 heads 125 us, 4 or 5 of them 138.
+    const int64_t blocks = (commit ? 0 : (int64_t)a.n_rows / a.bt) + a.n_req;
+    const int64_t parts = std::min<int64_t>(a.H, std::max<int64_t>(1, 128 / a.bt * a.num_sms / blocks));
+    p.heads = (int32_t)((a.H + parts - 1) / parts);
     const dim3 grid((unsigned)x, (unsigned)((a.H + p.heads - 1) / p.heads));
     const int smem = a.bt * (kKvDim + a.rope.rot * 4);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
