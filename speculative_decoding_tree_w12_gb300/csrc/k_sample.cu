@@ -822,7 +822,7 @@ __device__ __forceinline__ void reject(const SampleParams &p, Shared &s, const c
         __syncthreads();
         ++rounds;
         Sum40 left;
-        constexpr int kBatch = kF32 ? 4 : 2;                        // pieces in flight of a thread
+        constexpr int kBatch = kF32 ? 2 : 1;                        // pieces in flight of a thread
         for (int v0 = lo; v0 < hi; v0 += 32 * kBatch) {
             const int n = min(kBatch, (hi - v0) / 32);
             uint4 y[kBatch];
