@@ -605,7 +605,8 @@ typedef struct {
  * not depend on the batch or the machine's order; ties go to the lowest index.
  * row_tok (device [R]); row_logp (device [R], nullable): log p of it.  A row
  * whose logits are all -inf or NaN gets -1 and -inf; NaN counts as -inf.
- * vocab <= w12_sample_max_vocab().  ws: as for w12_tree_build.
+ * vocab <= w12_sample_max_vocab().  ws: as for w12_tree_build.  The scratch
+ * needs no initial contents and keeps none between calls.
  */
 int64_t w12_sample_max_vocab(void);
 size_t w12_sample_scratch_bytes(int32_t R, int64_t vocab);
