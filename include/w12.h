@@ -537,9 +537,9 @@ typedef struct {
  * a value that is not finite is stored as NaN and counts for no scale.
  * len_out[r] (device, may be cache->len) = the new length.  The blocks that the new
  * tokens fall into must be in the table, and no block may be in it twice.
- * Device checks: row offsets out of order, a length past the table or the
- * rotation tables, or a block outside the pool set W12_E_INVAL in the status
- * word and leave that request as it was.
+ * Device checks: a row offset below one before it, a length past the table or
+ * the rotation tables, or a block outside the pool set W12_E_INVAL in the
+ * status word and leave that request as it was.
  * ws: as for w12_tree_build.
  */
 w12_status w12_kv_append(const w12_kv_cache *cache, const w12_rope *rope, int32_t n_req, const uint16_t *k,

@@ -118,6 +118,12 @@ __device__ __forceinline__ uint4 xor_words(uint4 v, int x)
     return v;
 }
 
+// n tokens behind the length have their places in the table
+__device__ __forceinline__ bool fits(const KvParams &p, int bt, int len, int n)
+{
+    return len >= 0 && (int64_t)len + n <= (int64_t)p.max_blocks * bt;
+}
+
 // BT: tokens of a block.  kCommit: the new tokens are the root path of
 // acc_node[r], gathered by row; otherwise they are rows off[r] .. off[r + 1] - 1.
 template <int BT, bool kCommit>
@@ -162,12 +168,27 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
     } else if (warp == 0) {
         // items run over the requests' touched blocks in order
         int base = 0, found_r = -1, found_i = 0, found_n = 0, good = 1;
+        int top = INT32_MIN;                                         // the largest offset so far, once one was out of order
+        bool disorder = false;
         for (int r0 = 0; r0 < p.n_req && found_r < 0; r0 += 32) {
             const int r = r0 + lane;
-            int n = 0, nb = 0, ok = 1;
+            int n = 0, nb = 0, ok = 1, lo = 0, hi = 0, len = 0;
+            if (r < p.n_req) lo = p.off[r], hi = p.off[r + 1], len = p.len[r];
+            // the rows of the requests served lie one behind the other, so that the grid has a CTA for every block
+            disorder |= __any_sync(0xffffffffu, lo > hi);
+            if (disorder) {
+                int m = r < p.n_req ? lo : INT32_MIN;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int t = __shfl_up_sync(0xffffffffu, m, d);
+                    if (lane >= d) m = max(m, t);
+                }
+                top = max(top, m);
+                ok = lo >= top;
+                top = __shfl_sync(0xffffffffu, top, 31);
+            }
             if (r < p.n_req) {
-                const int lo = p.off[r], hi = p.off[r + 1], len = p.len[r];
-                ok = lo >= 0 && hi <= p.n_rows && lo <= hi && len >= 0;
+                ok = ok && lo >= 0 && hi <= p.n_rows && lo <= hi && fits(p, BT, len, hi - lo);
                 n = ok ? hi - lo : 0;
                 nb = n ? (len + n - 1) / BT - len / BT + 1 : 1;      // a request without tokens still reports its length
             }
@@ -198,11 +219,12 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
     __syncthreads();
     const int r = s_r;
     if (r < 0) return;
-    const int n_new = s_n, item = s_item, len = p.len[r];
+    const int item = s_item, len = p.len[r];
+    const bool room = fits(p, BT, len, s_n);
+    const int n_new = room ? s_n : 0;
     const int n_blk = n_new ? (len + n_new - 1) / BT - len / BT + 1 : 1;
     if (item >= n_blk) return;
-    bool ok = s_ok && len >= 0 && (int64_t)len + n_new <= (int64_t)p.max_blocks * BT &&
-              (p.rope.rot == 0 || n_new == 0 || len + n_new <= p.rope.max_pos);
+    bool ok = s_ok && room && (p.rope.rot == 0 || n_new == 0 || len + n_new <= p.rope.max_pos);
     const int bi = len / BT + item;
     // every CTA of the request looks at all of its blocks, so that they agree
     const int32_t *table = p.table + (int64_t)r * p.max_blocks;
