@@ -13,7 +13,7 @@
 // token.
 //
 // One CTA owns one block of tokens and a run of heads, so nothing is shared
-// between CTAs but the lengths (below).  It stages the positions' cosines and
+// between CTAs but the lengths (see the kernel's end).  It stages the positions' cosines and
 // sines once; then for each head a warp takes consecutive tokens, a lane four
 // dimensions, and everything stays in registers: rows, turned keys (a pair's
 // other half comes from the lane that has it), the two maxima, codes.  Keys
@@ -49,7 +49,7 @@ struct KvParams {
     const int32_t *parent, *acc_node;           // commit: the path ending on acc_node[r]
     const uint16_t *k, *v;
     RopeArgs rope;
-    int32_t *len_out, *arrive, *status;
+    int32_t *len_out, *arrive, *new_len, *status;
 };
 
 __device__ __forceinline__ void fail(int32_t *status) { atomicCAS(status, 0, (int32_t)W12_E_INVAL); }
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
     float *tab = reinterpret_cast<float *>(smem + BT * kKvDim);      // [tokens][rot / 2] cosines, then sines
     __shared__ int32_t s_path[kMaxDepth + 2];
     __shared__ int32_t s_parent[kMaxBudget];
-    __shared__ int32_t s_r, s_item, s_n, s_ok;
+    __shared__ int32_t s_r, s_item, s_n, s_ok, s_last;
     __shared__ uint2 s_top[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h0 = blockIdx.y * p.heads, h1 = min(p.H, h0 + p.heads);
@@ -218,16 +218,15 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
     }
     __syncthreads();
     const int r = s_r;
-    if (r < 0) return;
-    const int item = s_item, len = p.len[r];
+    const int item = s_item, len = r >= 0 ? p.len[r] : 0;
     const bool room = fits(p, BT, len, s_n);
     const int n_new = room ? s_n : 0;
     const int n_blk = n_new ? (len + n_new - 1) / BT - len / BT + 1 : 1;
-    if (item >= n_blk) return;
-    bool ok = s_ok && room && (p.rope.rot == 0 || n_new == 0 || len + n_new <= p.rope.max_pos);
+    const bool has = r >= 0 && item < n_blk;                         // the grid is the largest that the rows can need
+    bool ok = has && s_ok && room && (p.rope.rot == 0 || n_new == 0 || len + n_new <= p.rope.max_pos);
     const int bi = len / BT + item;
     // every CTA of the request looks at all of its blocks, so that they agree
-    const int32_t *table = p.table + (int64_t)r * p.max_blocks;
+    const int32_t *table = p.table + (int64_t)max(r, 0) * p.max_blocks;
     int bad = 0;
     if (ok && n_new)
         for (int i = tid; i < n_blk; i += kThreads) {
@@ -236,7 +235,7 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
         }
     if (__syncthreads_or(bad)) ok = false;
     const int blk = ok && n_new ? table[bi] : 0;
-    if (!ok && tid == 0) fail(p.status);
+    if (has && !ok && tid == 0) fail(p.status);
     if (ok && n_new) {
         const int first = max(len, bi * BT);                         // positions [first, last) go into this block
         const int last = min(len + n_new, (bi + 1) * BT);
@@ -409,18 +408,22 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
         if (held == 0 && end == BT) heads(std::true_type{});
         else heads(std::false_type{});
     }
-    // ---- the request's last CTA to get here writes its length (len_out may be
-    // the cache's own array: every CTA has read it by then).  The counter goes
-    // back to zero for the next launch.
+    // ---- The grid's last CTA writes all lengths, which each request's first CTA
+    // has left in the workspace: len_out may be the cache's own array, and any
+    // CTA that has not started yet still looks its block up in that.  So every
+    // CTA arrives, those without a block too.  The counter goes back to zero
+    // for the next launch.
     __syncthreads();
     if (tid == 0) {
-        const int total = n_blk * (int)gridDim.y;
+        if (has && item == 0 && blockIdx.y == 0) p.new_len[r] = ok ? len + n_new : len;
         __threadfence();
-        if (atomicAdd(p.arrive + r, 1) == total - 1) {
-            p.arrive[r] = 0;
-            p.len_out[r] = ok ? len + n_new : len;
-        }
+        s_last = atomicAdd(p.arrive, 1) == (int)(gridDim.x * gridDim.y) - 1;
     }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    for (int i = tid; i < p.n_req; i += kThreads) p.len_out[i] = __ldcg(p.new_len + i);
+    if (tid == 0) *p.arrive = 0;
 }
 
 }  // namespace
@@ -451,6 +454,7 @@ int launch_kv_write(const KvArgs &a, void *stream)
     p.rope = a.rope;
     p.len_out = a.len_out;
     p.arrive = a.arrive;
+    p.new_len = a.new_len;
     p.status = a.status;
     const bool commit = a.acc_node != nullptr;
     // blocks that one request's new tokens can touch: n tokens reach over at

@@ -149,6 +149,7 @@ struct Ws {
     WsLayout L;
     int32_t *status() const { return reinterpret_cast<int32_t *>(base + L.status); }
     int32_t *arrive() const { return reinterpret_cast<int32_t *>(base + L.arrive); }
+    int32_t *new_len() const { return reinterpret_cast<int32_t *>(base + L.new_len); }
     int64_t *mismatch() const { return reinterpret_cast<int64_t *>(base + L.status + 64); }
     int32_t *counters(int slot) const
     {
@@ -199,6 +200,8 @@ WsLayout layout_for(int32_t R, int64_t max_n, int64_t vocab, int32_t n_req)
     L.status = o;
     o += 256;
     L.arrive = o;
+    o += 256;
+    L.new_len = o;
     o += static_cast<size_t>(kMaxBudget) * 4;
     // the chain words end exactly where the counters start
     L.grid = o;
@@ -935,6 +938,7 @@ w12_status kv_entry(const w12_kv_cache *c, const w12_rope *rope, int32_t n_req, 
     a.v = v;
     a.len_out = len_out;
     a.arrive = W.arrive();
+    a.new_len = W.new_len();
     a.status = W.status();
     return cuda_status(launch_kv_write(a, stream));
 }

@@ -99,3 +99,79 @@ def test_lengths_out_of_range(w12, length, commit):
         ref.kv_write(s.host, r, x[off[r]:off[r + 1], 0], x[off[r]:off[r + 1], 1], s.cos, s.sin)
     s.same()
     assert s.ws.status() == w12.W12_E_INVAL
+
+
+def counters(s):
+    """The writer's words of the workspace: its arrivals."""
+    return s.ws.buf[256:512].view(torch.int32).tolist()
+
+
+@pytest.mark.parametrize("n,top,H,bt", [(70, 900, 1, 128), (48, 1400, 3, 128), (90, 700, 2, 32), (300, 150, 1, 64)])
+def test_in_place_over_several_waves(w12, n, top, H, bt):
+    """More CTAs than the SMs hold at once, the lengths written where they are read: two appends and a commit on one
+    workspace."""
+    g = np.random.default_rng(n)
+    s = World(w12, [int(x) for x in g.integers(0, 2 * bt, n)], H, bt, room=2 * top + 1, seed=n)
+    for _ in range(2):
+        cnt = g.integers(0, top, n)
+        off = np.concatenate([[0], np.cumsum(cnt)])
+        x = rows(s, int(off[-1]), H)
+        append(w12, s, x, off)
+        for r in range(n):
+            ref.kv_write(s.host, r, x[off[r]:off[r + 1], 0], x[off[r]:off[r + 1], 1], s.cos, s.sin)
+        s.same()
+        assert not any(counters(s))
+    t = chains(w12, n, 1)
+    x = rows(s, n, H)
+    w12.w12_kv_commit(s.cache, s.rope, t, n, ints(range(n)), bf16(x[:, 0].reshape(n, -1)), bf16(x[:, 1].reshape(n, -1)), s.ws)
+    for r in range(n):
+        ref.kv_write(s.host, r, x[r:r + 1, 0], x[r:r + 1, 1], s.cos, s.sin)
+    s.same()
+    assert not any(counters(s)) and s.ws.status() == 0
+
+
+def chains(w12, n, each):
+    """n requests of one chain of `each` rows."""
+    j = np.tile(np.arange(each), n)
+    parent = np.where(j == 0, -1, np.arange(n * each) - 1)
+    return w12.DeviceTree.from_arrays(ints(parent), torch.from_numpy(j.astype(np.uint8)).cuda(), ints(np.repeat(np.arange(n), each)),
+                                      ints(np.arange(n + 1) * each))
+
+
+@pytest.mark.parametrize("n,each,H,bt", [(500, 1, 4, 128), (60, 8, 8, 32), (15, 34, 16, 32), (128, 4, 8, 64)])
+def test_in_place_commits_of_many_requests(w12, n, each, H, bt):
+    """More CTAs without a block of their own than with one; many lengths change the number of blocks that the same rows
+    would touch behind them."""
+    g = np.random.default_rng(n)
+    s = World(w12, [int(x) for x in g.integers(0, 2 * bt, n)], H, bt, room=4 * each + 1, seed=23)
+    t = chains(w12, n, each)
+    for _ in range(3):
+        x = rows(s, n * each, H)
+        acc = np.arange(n) * each + g.integers(0, each, n)
+        k, v = (bf16(x[:, i].reshape(n * each, -1)) for i in range(2))
+        w12.w12_kv_commit(s.cache, s.rope, t, n, ints(acc), k, v, s.ws)
+        for r in range(n):
+            path = range(r * each, acc[r] + 1)
+            ref.kv_write(s.host, r, x[path, 0], x[path, 1], s.cos, s.sin)
+        s.same()
+        assert not any(counters(s)) and s.ws.status() == 0
+
+
+def test_in_place_is_as_apart(w12):
+    """A long append of many requests, the lengths in place and apart: the same caches."""
+    n, H, bt = 24, 8, 128
+    g = np.random.default_rng(24)
+    lens, cnt = g.integers(0, 300, n), g.integers(500, 4000, n)
+    off = np.concatenate([[0], np.cumsum(cnt)])
+    per = -(-int((lens + cnt).max()) // bt)
+    x = [torch.randn(int(off[-1]), H * D, device="cuda").bfloat16() for _ in range(2)]
+    table = torch.arange(n * per, dtype=torch.int32, device="cuda").view(n, per)
+    ws = w12.Workspace(1, 0, 0, n)
+    got = []
+    for apart in (True, False):
+        c = w12.KvCache.empty(n * per, H, bt, table)
+        c.len.copy_(ints(lens))
+        out = w12.w12_kv_append(c, None, x[0], x[1], ints(off), ws, len_out=torch.empty_like(c.len) if apart else None)
+        got.append((c.k, c.v, c.k_scale, c.v_scale, out))
+    assert got[0][4].tolist() == (lens + cnt).tolist() and all(torch.equal(a, b) for a, b in zip(*got))
+    assert ws.status() == 0
