@@ -585,7 +585,7 @@ typedef struct {
     const void *logits;          /* device [R][vocab], rows logits_stride elements apart */
     int32_t logits_f32;          /* 0: BF16, 1: FP32 */
     int64_t vocab, logits_stride;
-    const float *temperature;    /* device [n_req], or NULL (1); 0: greedy */
+    const float *temperature;    /* device [n_req], or NULL (1); 0, or so small that 1 / T overflows: greedy */
     const float *draft_p;        /* device [R][vocab]: the drafter's probabilities at each row, or NULL */
     int64_t draft_stride;
     const float *u_accept;       /* device [R] in [0, 1): decides on row j as a draft (needed with draft_p) */

@@ -368,21 +368,26 @@ template <bool kF32>
 struct Weigher {
     static constexpr int kPer = Row<kF32>::kPer;
     static constexpr float kLeast = -128.f;    // (also what a NaN becomes: a weight of nothing)
-    float inv_t, m;                            // m: the largest z
-    __device__ Weigher(float inv_t_, float top) : inv_t(inv_t_), m(top * inv_t_) {}   // (a positive factor keeps the order)
+    float inv_t, top, m;                       // m: the largest z
+    // The largest z may be no number: an infinite logit, or one of the type's
+    // lowest or highest over a T under 1.  Then the logits equal to the largest
+    // weigh 1 and all others nothing, as in the limit: two different ones of
+    // that size lie further apart than 2^100 T.  So a row's weights never sum
+    // to nothing.
+    bool flat;
+    __device__ Weigher(float inv_t_, float top_) : inv_t(inv_t_), top(top_), m(top_ * inv_t_), flat(!(fabsf(m) < INFINITY)) {}   // (a positive factor keeps the order)
     __device__ __forceinline__ float one(float x) const
     {
-        const float z = __fmul_rn(x, inv_t);
-        if (m == INFINITY) return z == INFINITY ? 1.f : 0.f;            // nothing but the infinite ones counts
-        return expf(fmaxf(__fsub_rn(z, m), kLeast));
+        if (flat) return x == top ? 1.f : 0.f;
+        return expf(fmaxf(__fsub_rn(__fmul_rn(x, inv_t), m), kLeast));
     }
-    // of a piece's tokens, in pairs; kInf: there are infinite z
-    template <bool kInf = false>
+    // of a piece's tokens, in pairs; kFlat: as above
+    template <bool kFlat = false>
     __device__ __forceinline__ void piece(const uint4 &x, u64 (&e)[kPer / 2]) const
     {
 #pragma unroll
         for (int i = 0; i < kPer; i += 2) {
-            if (kInf) {
+            if (kFlat) {
                 e[i / 2] = pair(one(Row<kF32>::get(x, i)), one(Row<kF32>::get(x, i + 1)));
                 continue;
             }
@@ -393,7 +398,7 @@ struct Weigher {
     }
     __device__ __forceinline__ void any_piece(const uint4 &x, u64 (&e)[kPer / 2]) const
     {
-        if (m == INFINITY) piece<true>(x, e);
+        if (flat) piece<true>(x, e);
         else piece(x, e);
     }
 };
@@ -452,7 +457,8 @@ __device__ __forceinline__ void write_row(const SampleParams &p, int row, int to
     if (p.row_logp) {
         // (a NaN can only be an accepted child's)
         const float x = __fmul_rn(fmaxf(logit, -INFINITY), w.inv_t);
-        p.row_logp[row] = __fsub_rn(x == w.m ? 0.f : __fsub_rn(x, w.m), logf(weight_of(total)));
+        const float z = w.flat ? (logit == w.top ? 0.f : -INFINITY) : __fsub_rn(x, w.m);
+        p.row_logp[row] = __fsub_rn(z, logf(weight_of(total)));
     }
 }
 
@@ -661,12 +667,12 @@ __global__ void __launch_bounds__(kChunkThreads, 5) k_sample_sum(const SamplePar
         if (lane == 0) *mine = (u64)tok;
     } else {
         Sum40 sum;
-        auto stretch = [&](auto inf) {
+        auto stretch = [&](auto flat) {
             for (int k = 0;;) {
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     u64 e[kPer / 2];
-                    w.template piece<decltype(inf)::value>(x[j], e);
+                    w.template piece<decltype(flat)::value>(x[j], e);
 #pragma unroll
                     for (int i = 0; i < kPer / 2; ++i) sum.add(e[i]);
                 }
@@ -674,7 +680,7 @@ __global__ void __launch_bounds__(kChunkThreads, 5) k_sample_sum(const SamplePar
                 z.load(lo + k * 32, lane, x);
             }
         };
-        if (w.m == INFINITY) stretch(std::true_type{});
+        if (w.flat) stretch(std::true_type{});
         else stretch(std::false_type{});
         const u64 all = warp_sum(sum.get());
         if (lane == 0) *mine = all;
