@@ -564,8 +564,15 @@ w12_status w12_kv_commit(const w12_kv_cache *cache, const w12_rope *rope, const 
  * q, k, v: the linears' rows before rotation (device BF16, rows *_stride
  * elements apart, 16-byte aligned; slices of one fused row are fine).
  * scale: the softmax scale.  out: device BF16 [R][n_heads][head_dim], 16-byte aligned.
- * The softmax statistics and all sums are FP32.  Rows off a root path and
- * cache slots past len[r] cannot reach an output, whatever they hold.
+ * Scores, softmax statistics and all sums are FP32.  Over the cached tokens two
+ * operands have fewer bits: a turned query is rounded to twelve significant
+ * bits (and to 2^-17 of the head's largest element), and a weight, where it
+ * meets its value, to eleven bits and to a multiple of 2^-26 of the largest
+ * among its neighbours (up to 16384 tokens): behind a token that outweighs them
+ * by 2^20 or more, a long flat stretch is off by 2^-13 of that token's weight
+ * at most.  A key that is not a number makes its head's outputs NaN, a value its
+ * own dimension, a query (an infinite one too) its row's head.  Rows off a root
+ * path and cache slots past len[r] cannot reach an output, whatever they hold.
  * aws: device, 256-byte aligned, w12_attn_workspace_bytes(...) bytes, no
  * initialisation; ws: as for w12_tree_build.  Device checks: tree arrays that
  * contradict each other, or lengths, positions or blocks out of range, set

@@ -33,8 +33,9 @@
 //   O^T = V^T P  kind::f16: V's codes widened to F16 (exact) by warpgroups of
 //                their own, into tensor memory (through shared memory they
 //                would cost four times the bandwidth, which bounds the tile);
-//                P in F16, eleven significant bits down to 2^-12 of the
-//                largest weight there was when its reference was set.
+//                P in F16, eleven significant bits down to 2^-16 of the
+//                largest weight there was when its reference was set, and
+//                multiples of 2^-26 of it below.
 // Two groups of two softmax warpgroups take alternate tiles, each with its own
 // scores, P, maxima and sums, so that the latencies of one tile's chain
 // (product, reads, exponentials, vote, product) hide behind the other's; the
@@ -50,7 +51,15 @@
 // value scales, which P carries.  A raise costs several tiles, so a reference
 // is set 2^6 above the maximum: with normally distributed scores that leaves
 // next to none but the first (set at the maximum, 32 rows behind 32771 tokens
-// took 88 us; 2^6 above, 71).
+// took 88 us; 2^6 above, 71).  What P can hold below the reference is F16's
+// range less those 2^12 and 2 for the value scales: every binade of margin less
+// keeps weights half as large, but 2^5 took 67 us where 2^6 takes 62, 2^4 74.
+// A token that outweighs the others by 2^20 and more would leave them few bits
+// or none, and if its own value is small they are the output.  So every 128
+// tiles of a group a column whose scores have all come to lie far below its
+// reference gets one of their own again: sums and normalisers are FP32 and can
+// be scaled up.  At most 128 tiles' weights are then rounded to multiples of
+// 2^-26 of a larger one: together 2^-13 of its weight at most.
 //
 // What bounds it.  One row behind a long context: memory (131072 tokens of 8
 // heads, 268 MB: 57.4 us, 4.7 TB/s, of which the tiles' loop 46 us at 5.8).
@@ -91,11 +100,15 @@ constexpr int kThreads = 128 + kSoft + 256; // warps: 0 K copies, 1 scores, 2 V 
 // is a read of L2, so the softmax warps must not spill.
 constexpr int kRegsLaunch = 72, kRegsSoft = 88, kRegsOther = 48;
 static_assert(kSoft * kRegsSoft + (kThreads - kSoft) * kRegsOther <= kThreads * kRegsLaunch, "register shares");
-constexpr float kHead = 16.f;              // P of a weight of 1 under the reference scale
+constexpr float kHead = 256.f;             // P of a weight of 1 under the reference scale
 constexpr float kMargin = 6.f;             // a reference is set this (log2) above the largest score there was
 constexpr float kRaise = 6.f;              // a score may pass the column's reference by this (log2) before it is raised
 constexpr float kCap = 8.f;                // scores are held under this until then
-constexpr float kScaleRaise = 16.f;        // ... and a value scale its reference by this factor: 16 * 2^6 * 16 < 2^15
+constexpr float kScaleRaise = 2.f;         // ... and a value scale its reference by this factor: 256 * 2^6 * 2 = 2^15 < F16's top
+// Every kSettle tiles of a group the references of columns whose scores have
+// all fallen kFar below come down again, to kLower under their highest at most.
+constexpr int kSettle = 128;
+constexpr float kFar = -12.f, kLower = 40.f;
 
 struct AttnParams {
     int32_t H, Hq, G, bt, n_blocks, max_blocks, n_req, R, ctas;
@@ -289,7 +302,10 @@ struct Shared {
         alignas(16) float red[2][4][kMaxCols];         // per warp
         List list[kThreads / 32];                      // before: a warp's requests
     };
-    float lsum[2][kMaxCols];                           // normalisers
+    union {
+        float mtop[2][kMaxCols];                       // the highest reference that a column ever had
+        float lsum[2][kMaxCols];                       // at the end: normalisers
+    };
     float sref[2];
     int32_t len[kMaxReq];                              // of every request: cached tokens,
     uint16_t lo[kMaxReq], rows[kMaxReq];               // first row; rows, and above kRowBits the weight of its tiles
@@ -805,6 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     s.cf[n] = n < ncol ? qs * p.scale2 : 0.f;
                     s.mneg[0][n] = 0.f;
                     s.mneg[1][n] = 0.f;
+                    s.mtop[0][n] = s.mtop[1][n] = -INFINITY;
                 }
             }
             fence_async_shared();
@@ -890,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Raise the references (first tile: set them).  A column with a
                 // NaN among its scores gets a NaN for its raise, and so carries
                 // it into its normaliser and sums.
-                auto raise = [&](bool must) -> bool {
+                auto raise = [&](bool must, bool settle) -> bool {
 #pragma unroll
                     for (int c = 0; c < T::kSteps; ++c)
                         if (c < steps) {
@@ -911,10 +928,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (tok < steps * 8) {
                         const int n = n0 + tok;
                         float m = max_nan(max_nan(s.red[grp][0][n], s.red[grp][1][n]), max_nan(s.red[grp][2][n], s.red[grp][3][n]));
-                        if (!fresh && m <= kRaise) m = 0.f;
-                        else m = m == -INFINITY ? 0.f : m + kMargin;
+                        float ref = -s.mneg[grp][n];
+                        if (m == -INFINITY || (!fresh && m <= kRaise && !(settle && m < kFar))) {
+                            m = 0.f;
+                        } else {
+                            m = max_nan(m + kMargin, s.mtop[grp][n] - kLower - ref);
+                            ref += m;
+                            s.mneg[grp][n] = -ref;
+                            s.mtop[grp][n] = fmaxf(s.mtop[grp][n], ref);
+                        }
                         s.delta[grp][n] = ex2(-m);
-                        s.mneg[grp][n] -= m;
                     }
                     named_bar(5 + wg, 128);
                     const float ref = must ? top_v : sref, fs = sref / ref;
@@ -944,8 +967,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // reference, once more to take the weights back, and again
                 // under raised references.  One copy of the pass serves all three.
                 const bool must = fresh || top_v > kScaleRaise * sref;          // the same for every thread
-                for (int turn = must ? 2 : 0;; ++turn) {
-                    if (turn == 2 && !raise(must)) {
+                const bool settle = (jj - j0) % (2 * kSettle) >= 2 * kSettle - 2;
+                for (int turn = must || settle ? 2 : 0;; ++turn) {
+                    if (turn == 2 && !raise(must, settle)) {
                         ok = false;
                         break;
                     }
