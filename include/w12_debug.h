@@ -64,6 +64,14 @@ int32_t w12_debug_last_cuda_error(char *buf, int32_t len);
 int32_t w12_debug_num_sms(void);
 
 /*
+ * Registers a thread of the attention kernel for segments of `cols` (16, 48,
+ * 80) query columns, as w12_tree_attention looks at them before a launch
+ * (0: another number of columns, or the query failed).  *wanted (may be NULL):
+ * what its warps' register shares need; with fewer it refuses.
+ */
+int32_t w12_debug_attn_registers(int32_t cols, int32_t *wanted);
+
+/*
  * Per-GEMM timing inside the verify step's GEMM chain (one persistent launch
  * for all linears and the LM head, split into w12_debug_chain_parts(n) launches
  * for n GEMMs).  While dev_words (device, n_words 64-bit words) is set, every

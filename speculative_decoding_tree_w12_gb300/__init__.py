@@ -121,6 +121,7 @@ def lib():
             "w12_tree_verify_sampled": ([p, p, i32, i32, p, p, p, p, p, p, sz, p], C.c_int),
             "w12_debug_set": ([i32, C.c_uint64], None),
             "w12_debug_num_sms": ([], i32),
+            "w12_debug_attn_registers": ([i32, p], i32),
             "w12_debug_profile": ([i32], None),
             "w12_debug_last_cuda_error": ([p, i32], i32),
             "w12_debug_profile_read": ([p, i32], i32),

@@ -72,6 +72,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "w12_device.cuh"
@@ -1245,6 +1246,31 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
+// Registers a thread of a shape's kernel, looked up once per shape; 0 if that
+// failed (and then looked up again).
+template <int kCols>
+int ctx_registers()
+{
+    static std::atomic<int> known{0};
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaFuncAttributes f{};
+        if (cudaFuncGetAttributes(&f, k_attn_ctx<kCols>) == cudaSuccess) known.store(n = f.numRegs, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+template <int kCols>
+cudaError_t launch_ctx(const CUtensorMap &kmap, const CUtensorMap &vmap, const AttnParams &p, cudaStream_t st)
+{
+    constexpr int bytes = smem_bytes<kCols>();
+    const cudaError_t e = cudaFuncSetAttribute(k_attn_ctx<kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    if (ctx_registers<kCols>() < kRegsLaunch) return cudaErrorInvalidConfiguration;   // the register shares need that many
+    k_attn_ctx<kCols><<<p.ctas, kThreads, bytes, st>>>(kmap, vmap, p);
+    return cudaGetLastError();
+}
+
 size_t part_columns(int32_t R, int32_t Hq, int ctas) { return (size_t)R * Hq + (size_t)ctas * kMaxCols; }
 
 }  // namespace
@@ -1256,6 +1282,12 @@ size_t attn_ws_bytes(int32_t R, int32_t Hq, int32_t H, int32_t n_req, int num_sm
     (void)H;
     (void)n_req;
     return part_columns(R, Hq, num_sms) * (kD * 4 + 8);
+}
+
+int attn_registers(int cols, int *wanted)
+{
+    *wanted = kRegsLaunch;
+    return cols == 16 ? ctx_registers<16>() : cols == 48 ? ctx_registers<48>() : cols == 80 ? ctx_registers<80>() : 0;
 }
 
 int launch_attn(const AttnArgs &a, void *stream)
@@ -1325,27 +1357,9 @@ int launch_attn(const AttnArgs &a, void *stream)
     const int64_t avg = (int64_t)((a.R + a.n_req - 1) / a.n_req) * p.G;
     p.cols = avg <= 16 ? 16 : avg <= 48 ? 48 : 80;
     p.fit = p.cols / p.G;
-    cudaError_t e;
-    auto go = [&](auto kernel, int threads, int bytes) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return;
-        static const int regs = [&] {       // the register shares need a launch with this many
-            cudaFuncAttributes f{};
-            return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
-        }();
-        if (regs < kRegsLaunch) {
-            e = cudaErrorInvalidConfiguration;
-            return;
-        }
-        kernel<<<p.ctas, threads, bytes, st>>>(kmap, vmap, p);
-        e = cudaGetLastError();
-    };
-    if (p.cols == 16)
-        go(k_attn_ctx<16>, kThreads, smem_bytes<16>());
-    else if (p.cols == 48)
-        go(k_attn_ctx<48>, kThreads, smem_bytes<48>());
-    else
-        go(k_attn_ctx<80>, kThreads, smem_bytes<80>());
+    const cudaError_t e = p.cols == 16   ? launch_ctx<16>(kmap, vmap, p, st)
+                          : p.cols == 48 ? launch_ctx<48>(kmap, vmap, p, st)
+                                         : launch_ctx<80>(kmap, vmap, p, st);
     if (e != cudaSuccess) return (int)e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.R, (unsigned)a.H);

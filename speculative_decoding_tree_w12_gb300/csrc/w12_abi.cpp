@@ -299,6 +299,14 @@ void w12_debug_set(int32_t flags, uint64_t timeout_ns)
 
 int32_t w12_debug_num_sms(void) { return num_sms(); }
 
+int32_t w12_debug_attn_registers(int32_t cols, int32_t *wanted)
+{
+    int w = 0;
+    const int n = attn_registers(cols, &w);
+    if (wanted) *wanted = w;
+    return n;
+}
+
 void w12_debug_chain_trace(void *dev_words, size_t n_words)
 {
     g_trace = static_cast<uint64_t *>(dev_words);

@@ -218,6 +218,7 @@ struct AttnArgs {
 };
 size_t attn_ws_bytes(int32_t R, int32_t Hq, int32_t H, int32_t n_req, int num_sms);
 int launch_attn(const AttnArgs &a, void *stream);
+int attn_registers(int cols, int *wanted);   // registers a thread of that shape's kernel
 
 // sampled verification (k_sample.cu)
 struct SampleArgs {
