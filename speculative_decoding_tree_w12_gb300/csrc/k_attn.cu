@@ -1139,6 +1139,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const AttnPara
     uint16_t *o = p.out + ((int64_t)row * p.Hq + h * G) * kD;
     if (nA == 0) {                                      // malformed: zeros, and the status word says so
         for (int i = tid; i < G * kD; i += threads) o[i] = 0;
+        pdl_wait();                                     // a call is over when its context's kernel is, whatever its rows
         return;
     }
     for (int a = warp; a < nA; a += warps) {
