@@ -251,7 +251,7 @@ class Workspace:
         if nbytes == 0:
             raise W12Error(W12_E_UNSUPPORTED, "w12_workspace_bytes")
         self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-        self.nbytes, self.addr = nbytes, self.buf.data_ptr()
+        self.nbytes, self.addr, self.dev = nbytes, self.buf.data_ptr(), self.buf.get_device()
         _check(lib().w12_workspace_init(self.ptr, nbytes, _stream()), "w12_workspace_init")
 
     @property
@@ -375,6 +375,7 @@ class DeviceTree:
         self.depth, self.rank = z(torch.uint8, budget), z(torch.uint8, budget)
         self.score = z(torch.float32, budget)
         self.req_row_off = z(torch.int32, n_req + 1)
+        self.n_req, self.dev = int(n_req), self.parent.get_device()
         self.c = TreeC(0, *(t.data_ptr() for t in (self.parent, self.token, self.depth, self.req, self.score,
                                                     self.rank, self.req_row_off)))
 
@@ -573,19 +574,42 @@ def _want(t, dtype, shape, what):
         raise ValueError(f"{what}: contiguous {dtype} {shape} wanted, got {t.dtype} {tuple(t.shape)}")
 
 
-def _ints(t, n, what) -> int:
+def _same_device(dev, what, *tensors):
+    """All of a handle's tensors lie where its first one does."""
+    if any(t is not None and t.get_device() != dev for t in tensors):
+        raise ValueError(f"{what}: tensors of one device wanted")
+
+
+def _on(dev, *handles):
+    """The GPU of a call: every handle's tensors lie there (a kernel gets their bare addresses)."""
+    if dev < 0:
+        raise ValueError("tensors of a CUDA device wanted")
+    for h in handles:
+        if h is not None and h.dev != dev:
+            raise ValueError(f"{type(h).__name__}: on cuda:{dev} wanted")
+    return dev
+
+
+def _tree(tree, n_req, dev):
+    if tree.n_req < n_req:
+        raise ValueError(f"tree: row offsets of {n_req} requests wanted, got {tree.n_req}")
+    return _on(dev, tree)
+
+
+def _ints(t, n, what, dev) -> int:
     """The address of n contiguous int32."""
-    if t.dtype is not _torch.int32 or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous int32 [{n}] wanted, got {t.dtype} {tuple(t.shape)}")
+    if t.dtype is not _torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{what}: contiguous int32 [{n}] on cuda:{dev} wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(t, rows, width, what):
+def _rows(t, rows, width, what, dev):
     """(address, elements between rows) of `rows` or more bfloat16 rows of `width` contiguous elements."""
     shape, stride = t.shape, t.stride()
-    if t.dtype is not _torch.bfloat16 or len(shape) != 2 or shape[1] != width or shape[0] < rows or stride[1] != 1:
-        raise ValueError(f"{what}: bfloat16 rows [>= {rows}][{width}] with contiguous elements wanted, got "
-                         f"{t.dtype} {tuple(shape)}")
+    if t.dtype is not _torch.bfloat16 or len(shape) != 2 or shape[1] != width or shape[0] < rows or stride[1] != 1 \
+            or t.get_device() != dev:
+        raise ValueError(f"{what}: bfloat16 rows [>= {rows}][{width}] with contiguous elements on cuda:{dev} wanted, got "
+                         f"{t.dtype} {tuple(shape)} on {t.device}")
     return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], width)
 
 
@@ -605,6 +629,8 @@ class KvCache:
         _want(v_scale, torch.float32, (n, H), "v_scale")
         _want(block_table, torch.int32, (None, None), "block_table")
         _want(length, torch.int32, (block_table.shape[0],), "length")
+        self.dev = k.get_device()
+        _same_device(self.dev, "cache", v, k_scale, v_scale, block_table, length)
         self.k, self.v, self.k_scale, self.v_scale, self.block_table, self.len = k, v, k_scale, v_scale, block_table, length
         self.n_req, self.H, self.bt, self.d = int(block_table.shape[0]), int(H), int(bt), int(d)
         self.c = KvCacheC(H, d, bt, n, block_table.shape[1], k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
@@ -629,7 +655,8 @@ class Rope:
         import torch
         _want(cos, torch.float32, (None, None), "cos")
         _want(sin, torch.float32, tuple(cos.shape), "sin")
-        self.cos, self.sin = cos, sin
+        self.cos, self.sin, self.dev = cos, sin, cos.get_device()
+        _same_device(self.dev, "position tables", sin)
         self.c = RopeC(2 * cos.shape[1], int(adjacent), cos.shape[0], cos.data_ptr(), sin.data_ptr())
         self.ref = C.byref(self.c)
 
@@ -643,7 +670,7 @@ class AttentionWorkspace:
         if self.nbytes == 0:
             raise W12Error(W12_E_UNSUPPORTED, "w12_attn_workspace_bytes")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
-        self.addr = self.buf.data_ptr()
+        self.addr, self.dev = self.buf.data_ptr(), self.buf.get_device()
 
 
 def w12_kv_append(cache: KvCache, rope: Optional[Rope], k, v, row_off, ws: Workspace, len_out=None, stream=None):
@@ -655,8 +682,10 @@ def w12_kv_append(cache: KvCache, rope: Optional[Rope], k, v, row_off, ws: Works
         raise ValueError("k and v: the same number of rows wanted")
     if len_out is None:
         len_out = cache.len
-    s = _lib.w12_kv_append(cache.ref, rope.ref if rope else None, n, *_rows(k, T, width, "k"), *_rows(v, T, width, "v"), T,
-                           _ints(row_off, n + 1, "row_off"), _ints(len_out, n, "len_out"), ws.addr, ws.nbytes, _st(stream))
+    dev = _on(cache.dev, rope, ws)
+    s = _lib.w12_kv_append(cache.ref, rope.ref if rope else None, n, *_rows(k, T, width, "k", dev), *_rows(v, T, width, "v", dev),
+                           T, _ints(row_off, n + 1, "row_off", dev), _ints(len_out, n, "len_out", dev), ws.addr, ws.nbytes,
+                           _st(stream))
     if s:
         raise W12Error(s, "w12_kv_append")
     return len_out
@@ -671,9 +700,10 @@ def w12_kv_commit(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n_req:
     if len_out is None:
         len_out = cache.len
     R, width = tree.c.R, cache.H * cache.d
-    s = _lib.w12_kv_commit(cache.ref, rope.ref if rope else None, C.byref(tree.c), n_req, _ints(acc_node, n_req, "acc_node"),
-                           *_rows(k, R, width, "k"), *_rows(v, R, width, "v"), _ints(len_out, n_req, "len_out"), ws.addr,
-                           ws.nbytes, _st(stream))
+    dev = _tree(tree, n_req, _on(cache.dev, rope, ws))
+    s = _lib.w12_kv_commit(cache.ref, rope.ref if rope else None, C.byref(tree.c), n_req, _ints(acc_node, n_req, "acc_node", dev),
+                           *_rows(k, R, width, "k", dev), *_rows(v, R, width, "v", dev), _ints(len_out, n_req, "len_out", dev),
+                           ws.addr, ws.nbytes, _st(stream))
     if s:
         raise W12Error(s, "w12_kv_commit")
     return len_out
@@ -689,13 +719,16 @@ def w12_tree_attention(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n
         raise ValueError("the cache's table and the tree: the same requests wanted")
     R, d, width, width_q = tree.c.R, cache.d, cache.H * cache.d, q.shape[-1]
     Hq = width_q // d
+    dev = _tree(tree, n_req, _on(cache.dev, rope, ws, aws))
     if out is None:
         out = _torch.empty((R, Hq, d), dtype=_torch.bfloat16, device=q.device)
-    elif out.shape[0] < R or out.shape[1:] != (Hq, d) or out.dtype is not _torch.bfloat16 or not out.is_contiguous():
-        raise ValueError(f"out: contiguous bfloat16 [{R}][{Hq}][{d}] wanted")
-    s = _lib.w12_tree_attention(cache.ref, rope.ref if rope else None, C.byref(tree.c), n_req, Hq, *_rows(q, R, Hq * d, "q"),
-                                *_rows(k, R, width, "k"), *_rows(v, R, width, "v"), d ** -0.5 if scale is None else scale,
-                                out.data_ptr(), ws.addr, ws.nbytes, aws.addr, aws.nbytes, _st(stream))
+    elif out.shape[0] < R or out.shape[1:] != (Hq, d) or out.dtype is not _torch.bfloat16 or not out.is_contiguous() \
+            or out.get_device() != dev:
+        raise ValueError(f"out: contiguous bfloat16 [{R}][{Hq}][{d}] on cuda:{dev} wanted")
+    s = _lib.w12_tree_attention(cache.ref, rope.ref if rope else None, C.byref(tree.c), n_req, Hq, *_rows(q, R, Hq * d, "q", dev),
+                                *_rows(k, R, width, "k", dev), *_rows(v, R, width, "v", dev),
+                                d ** -0.5 if scale is None else scale, out.data_ptr(), ws.addr, ws.nbytes, aws.addr, aws.nbytes,
+                                _st(stream))
     if s:
         raise W12Error(s, "w12_tree_attention")
     return out
@@ -734,6 +767,8 @@ class SampleRows:
                 raise ValueError("draft_p needs u_accept")
         if u_accept is not None:
             _want(u_accept, torch.float32, (R,), "u_accept")
+        self.dev = logits.get_device()
+        _same_device(self.dev, "logits and random numbers", u_sample, temperature, draft_p, u_accept)
         self.logits, self.u_sample, self.temperature, self.draft_p, self.u_accept = \
             logits, u_sample, temperature, draft_p, u_accept
         row = lambda t: t.stride(0) if R > 1 else max(t.stride(0), V)
@@ -749,31 +784,33 @@ class SampleRows:
         self.rows = R
         self.requests = None if temperature is None else int(temperature.shape[0])
 
-    def _fits(self, tree, n_req):
+    def _fits(self, tree, n_req, ws):
+        dev = _tree(tree, n_req, _on(self.dev, ws))
         if self.rows < tree.c.R or (self.requests is not None and self.requests < n_req):
             raise ValueError("logits: a row for every row of the tree wanted, and a temperature for every request")
+        return dev
 
 
 def w12_tree_sample(dist: SampleRows, tree: DeviceTree, n_req: int, ws: Workspace, row_tok=None, row_logp=None,
                     stream=None):
     """One token per tree row, distributed as the target's probabilities
     there -> int32 [R]; its log-probability to ``row_logp`` (float32 [R])."""
-    dist._fits(tree, n_req)
+    dev = dist._fits(tree, n_req, ws)
     R = tree.c.R
     if row_tok is None:
         row_tok = _torch.empty(R, dtype=_torch.int32, device=dist.logits.device)
-    s = _lib.w12_tree_sample(dist.ref, C.byref(tree.c), n_req, _ints(row_tok, R, "row_tok"), _floats(row_logp, R), ws.addr,
-                             ws.nbytes, _st(stream))
+    s = _lib.w12_tree_sample(dist.ref, C.byref(tree.c), n_req, _ints(row_tok, R, "row_tok", dev), _floats(row_logp, R, dev),
+                             ws.addr, ws.nbytes, _st(stream))
     if s:
         raise W12Error(s, "w12_tree_sample")
     return row_tok
 
 
-def _floats(t, n):
+def _floats(t, n, dev):
     if t is None:
         return None
-    if t.dtype is not _torch.float32 or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"row_logp: contiguous float32 [{n}] wanted")
+    if t.dtype is not _torch.float32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"row_logp: contiguous float32 [{n}] on cuda:{dev} wanted")
     return t.data_ptr()
 
 
@@ -781,7 +818,7 @@ def w12_tree_verify_sampled(dist: SampleRows, tree: DeviceTree, n_req: int, p_ma
                             row_logp=None, acc_tok=None, acc_len=None, acc_node=None, stream=None):
     """``w12_tree_sample`` and the acceptance of the children that carry their
     parent's token -> acc_tok, acc_len, acc_node."""
-    dist._fits(tree, n_req)
+    dev = dist._fits(tree, n_req, ws)
     R = tree.c.R
     if row_tok is None or acc_tok is None or acc_len is None or acc_node is None:
         new = lambda *s: _torch.empty(s, dtype=_torch.int32, device=dist.logits.device)
@@ -789,11 +826,12 @@ def w12_tree_verify_sampled(dist: SampleRows, tree: DeviceTree, n_req: int, p_ma
         acc_tok = acc_tok if acc_tok is not None else new(n_req, p_max + 1)
         acc_len = acc_len if acc_len is not None else new(n_req)
         acc_node = acc_node if acc_node is not None else new(n_req)
-    if acc_tok.shape != (n_req, p_max + 1) or acc_tok.dtype is not _torch.int32 or not acc_tok.is_contiguous():
-        raise ValueError(f"acc_tok: contiguous int32 [{n_req}][{p_max + 1}] wanted")
-    s = _lib.w12_tree_verify_sampled(dist.ref, C.byref(tree.c), n_req, p_max, _ints(row_tok, R, "row_tok"),
-                                     _floats(row_logp, R), acc_tok.data_ptr(), _ints(acc_len, n_req, "acc_len"),
-                                     _ints(acc_node, n_req, "acc_node"), ws.addr, ws.nbytes, _st(stream))
+    if acc_tok.shape != (n_req, p_max + 1) or acc_tok.dtype is not _torch.int32 or not acc_tok.is_contiguous() \
+            or acc_tok.get_device() != dev:
+        raise ValueError(f"acc_tok: contiguous int32 [{n_req}][{p_max + 1}] on cuda:{dev} wanted")
+    s = _lib.w12_tree_verify_sampled(dist.ref, C.byref(tree.c), n_req, p_max, _ints(row_tok, R, "row_tok", dev),
+                                     _floats(row_logp, R, dev), acc_tok.data_ptr(), _ints(acc_len, n_req, "acc_len", dev),
+                                     _ints(acc_node, n_req, "acc_node", dev), ws.addr, ws.nbytes, _st(stream))
     if s:
         raise W12Error(s, "w12_tree_verify_sampled")
     return acc_tok, acc_len, acc_node
