@@ -580,20 +580,14 @@ def _same_device(dev, what, *tensors):
         raise ValueError(f"{what}: tensors of one device wanted")
 
 
-def _on(dev, *handles):
-    """The GPU of a call: every handle's tensors lie there (a kernel gets their bare addresses)."""
+def _refuse(dev, n_req, tree, *handles):
+    """What a call turns away: a kernel gets bare addresses, so every handle's tensors have to lie on the call's GPU, and
+    a tree has to have row offsets for every request.  (The calls compare by themselves, which takes them 0.1 us.)"""
     if dev < 0:
         raise ValueError("tensors of a CUDA device wanted")
-    for h in handles:
-        if h is not None and h.dev != dev:
-            raise ValueError(f"{type(h).__name__}: on cuda:{dev} wanted")
-    return dev
-
-
-def _tree(tree, n_req, dev):
-    if tree.n_req < n_req:
+    if tree is not None and tree.n_req < n_req:
         raise ValueError(f"tree: row offsets of {n_req} requests wanted, got {tree.n_req}")
-    return _on(dev, tree)
+    raise ValueError(f"{', '.join(type(h).__name__ for h in (tree, *handles) if h is not None)}: on cuda:{dev} wanted")
 
 
 def _ints(t, n, what, dev) -> int:
@@ -682,7 +676,9 @@ def w12_kv_append(cache: KvCache, rope: Optional[Rope], k, v, row_off, ws: Works
         raise ValueError("k and v: the same number of rows wanted")
     if len_out is None:
         len_out = cache.len
-    dev = _on(cache.dev, rope, ws)
+    dev = cache.dev
+    if dev < 0 or ws.dev != dev or (rope is not None and rope.dev != dev):
+        _refuse(dev, n, None, rope, ws)
     s = _lib.w12_kv_append(cache.ref, rope.ref if rope else None, n, *_rows(k, T, width, "k", dev), *_rows(v, T, width, "v", dev),
                            T, _ints(row_off, n + 1, "row_off", dev), _ints(len_out, n, "len_out", dev), ws.addr, ws.nbytes,
                            _st(stream))
@@ -700,7 +696,9 @@ def w12_kv_commit(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n_req:
     if len_out is None:
         len_out = cache.len
     R, width = tree.c.R, cache.H * cache.d
-    dev = _tree(tree, n_req, _on(cache.dev, rope, ws))
+    dev = cache.dev
+    if dev < 0 or ws.dev != dev or tree.dev != dev or tree.n_req < n_req or (rope is not None and rope.dev != dev):
+        _refuse(dev, n_req, tree, rope, ws)
     s = _lib.w12_kv_commit(cache.ref, rope.ref if rope else None, C.byref(tree.c), n_req, _ints(acc_node, n_req, "acc_node", dev),
                            *_rows(k, R, width, "k", dev), *_rows(v, R, width, "v", dev), _ints(len_out, n_req, "len_out", dev),
                            ws.addr, ws.nbytes, _st(stream))
@@ -719,7 +717,10 @@ def w12_tree_attention(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n
         raise ValueError("the cache's table and the tree: the same requests wanted")
     R, d, width, width_q = tree.c.R, cache.d, cache.H * cache.d, q.shape[-1]
     Hq = width_q // d
-    dev = _tree(tree, n_req, _on(cache.dev, rope, ws, aws))
+    dev = cache.dev
+    if dev < 0 or ws.dev != dev or aws.dev != dev or tree.dev != dev or tree.n_req < n_req or \
+            (rope is not None and rope.dev != dev):
+        _refuse(dev, n_req, tree, rope, ws, aws)
     if out is None:
         out = _torch.empty((R, Hq, d), dtype=_torch.bfloat16, device=q.device)
     elif out.shape[0] < R or out.shape[1:] != (Hq, d) or out.dtype is not _torch.bfloat16 or not out.is_contiguous() \
@@ -785,7 +786,9 @@ class SampleRows:
         self.requests = None if temperature is None else int(temperature.shape[0])
 
     def _fits(self, tree, n_req, ws):
-        dev = _tree(tree, n_req, _on(self.dev, ws))
+        dev = self.dev
+        if dev < 0 or ws.dev != dev or tree.dev != dev or tree.n_req < n_req:
+            _refuse(dev, n_req, tree, ws)
         if self.rows < tree.c.R or (self.requests is not None and self.requests < n_req):
             raise ValueError("logits: a row for every row of the tree wanted, and a temperature for every request")
         return dev
