@@ -41,7 +41,7 @@ using namespace w12d;
 using namespace w12i;
 
 struct KvParams {
-    int32_t H, n_blocks, max_blocks, n_req, n_rows, items, heads;   // heads: of one CTA
+    int32_t H, n_blocks, max_blocks, n_req, n_rows, heads;          // heads: of one CTA
     int64_t k_stride, v_stride;
     uint8_t *kc, *vc;
     float *ks, *vs;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
 
     // ---- which request and which of its blocks
     if (kCommit) {
-        const int r = blockIdx.x / p.items;
+        const int r = blockIdx.x;
         const int lo = p.off[r], hi = p.off[r + 1], end = p.acc_node[r];
         const bool in = lo >= 0 && hi <= p.n_rows && lo <= hi && (lo == hi || (end >= lo && end < hi));
         if (in && lo < hi)
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
                 if (j >= 0 || n > kMaxDepth + 1) ok = 0;             // left the request, or too deep
             }
             s_r = r;
-            s_item = blockIdx.x % p.items;
+            s_item = blockIdx.z;
             s_n = ok ? n : 0;
             s_ok = ok;
         }
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
     const int n_new = room ? s_n : 0;
     const int n_blk = n_new ? (len + n_new - 1) / BT - len / BT + 1 : 1;
     const bool has = r >= 0 && item < n_blk;                         // the grid is the largest that the rows can need
-    bool ok = has && s_ok && room && (p.rope.rot == 0 || n_new == 0 || len + n_new <= p.rope.max_pos);
+    bool ok = r >= 0 && s_ok && room && (p.rope.rot == 0 || n_new == 0 || len + n_new <= p.rope.max_pos);
     const int bi = len / BT + item;
     // every CTA of the request looks at all of its blocks, so that they agree
     const int32_t *table = p.table + (int64_t)max(r, 0) * p.max_blocks;
@@ -234,22 +234,24 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
             bad |= b < 0 || b >= p.n_blocks;
         }
     if (__syncthreads_or(bad)) ok = false;
-    const int blk = ok && n_new ? table[bi] : 0;
-    // ---- The grid's last CTA writes all lengths, which each request's first CTA
-    // leaves in the workspace: len_out may be the cache's own array, and any CTA
-    // that has not started yet still looks its block up in that.  So every CTA
-    // arrives, those without a block too, and here, since all of its reads of
-    // the lengths are behind it: the answer is back by the time it is wanted
-    // (16 prompts of up to 8192 tokens: 123 us; arriving at the end 126, and
-    // 133 with all warps waiting for the answer).
+    const bool writes = ok && has && n_new;
+    const int blk = writes ? table[bi] : 0;
+    // ---- A length is written when every CTA that looks at it has done so: len_out
+    // may be the cache's own array, and a CTA that has not started yet still
+    // finds its block by it.  In an append that is any CTA of the grid, whose
+    // last one writes all lengths (each request's first CTA leaves them in the
+    // workspace); in a commit any CTA of the request.  So every CTA arrives,
+    // those without a block too, and here, right behind its reads: the answer is
+    // back by the time it is wanted (16 prompts of up to 8192 tokens: 123 us;
+    // arriving at the end 126, and 133 with all warps waiting for the answer).
     int arrived = 0;
     if (tid == 0) {
         if (has && !ok) fail(p.status);
-        if (has && item == 0 && blockIdx.y == 0) p.new_len[r] = ok ? len + n_new : len;
+        if (!kCommit && has && item == 0 && blockIdx.y == 0) p.new_len[r] = ok ? len + n_new : len;
         __threadfence();
-        arrived = atomicAdd(p.arrive, 1);
+        arrived = atomicAdd(p.arrive + (kCommit ? r : 0), 1);
     }
-    if (ok && n_new) {
+    if (writes) {
         const int first = max(len, bi * BT);                         // positions [first, last) go into this block
         const int last = min(len + n_new, (bi + 1) * BT);
         const int held = first - bi * BT, end = last - bi * BT;      // slots it holds already; the new ones' end
@@ -421,7 +423,14 @@ __global__ void __launch_bounds__(BT * 8, 128 / BT) k_kv_write(const KvParams p)
         if (held == 0 && end == BT) heads(std::true_type{});
         else heads(std::false_type{});
     }
-    // ---- all lengths are read: publish the new ones, and the counter goes back to zero for the next launch
+    // ---- the last one writes the new lengths, and the counter goes back to zero for the next launch
+    if (kCommit) {
+        if (tid == 0 && arrived == (int)(gridDim.y * gridDim.z) - 1) {
+            p.len_out[r] = ok ? len + n_new : len;
+            p.arrive[r] = 0;
+        }
+        return;
+    }
     if (warp) return;
     if (__shfl_sync(0xffffffffu, arrived, 0) != (int)(gridDim.x * gridDim.y) - 1) return;
     __threadfence();
@@ -461,9 +470,11 @@ int launch_kv_write(const KvArgs &a, void *stream)
     p.status = a.status;
     const bool commit = a.acc_node != nullptr;
     // blocks that one request's new tokens can touch: n tokens reach over at
-    // most (n - 1) / bt + 2 of them
-    p.items = kMaxDepth / a.bt + 2;
-    const int64_t x = commit ? (int64_t)a.n_req * p.items : (int64_t)a.n_rows / a.bt + 2ll * a.n_req;
+    // most (n - 1) / bt + 2 of them.  A path's further blocks come last: most
+    // of those CTAs have nothing to write (24 requests of 8 rows: 12.1 us with
+    // a request's CTAs side by side)
+    const unsigned items = commit ? kMaxDepth / a.bt + 2 : 1;
+    const int64_t x = commit ? a.n_req : (int64_t)a.n_rows / a.bt + 2ll * a.n_req;
     // Heads of a CTA: so many that all touched blocks' CTAs fit the SMs at once
     // (128 / bt of them an SM), since a CTA spends some 4 us on finding its
     // block and staging the tables before its first head, and a head's loads
@@ -473,7 +484,7 @@ int launch_kv_write(const KvArgs &a, void *stream)
     const int64_t blocks = (commit ? 0 : (int64_t)a.n_rows / a.bt) + a.n_req;
     const int64_t parts = std::min<int64_t>(a.H, std::max<int64_t>(1, 128 / a.bt * a.num_sms / blocks));
     p.heads = (int32_t)((a.H + parts - 1) / parts);
-    const dim3 grid((unsigned)x, (unsigned)((a.H + p.heads - 1) / p.heads));
+    const dim3 grid((unsigned)x, (unsigned)((a.H + p.heads - 1) / p.heads), items);
     const int smem = a.bt * (kKvDim + a.rope.rot * 4);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;

@@ -200,7 +200,7 @@ WsLayout layout_for(int32_t R, int64_t max_n, int64_t vocab, int32_t n_req)
     L.status = o;
     o += 256;
     L.arrive = o;
-    o += 256;
+    o += static_cast<size_t>(kMaxBudget) * 4;
     L.new_len = o;
     o += static_cast<size_t>(kMaxBudget) * 4;
     // the chain words end exactly where the counters start

@@ -26,8 +26,8 @@ constexpr int32_t kDevOk = 0;
 // Byte layout of the caller's workspace.  Every region is 256-byte aligned.
 struct WsLayout {
     size_t status;        // int32[64]: [0] status, [1] detail, [8] mismatch count (int64)
-    size_t arrive;        // int32[64]: [0] the KV cache writer's arrivals, zero between calls
-    size_t new_len;       // int32[kMaxBudget]: the lengths that its last CTA publishes
+    size_t arrive;        // int32[kMaxBudget], zero between calls: the KV cache writer's arrivals (append: [0]; commit: per request)
+    size_t new_len;       // int32[kMaxBudget]: the lengths that an append's last CTA writes
     size_t grid;          // uint32[kGridWords]: [0] abort word of a GEMM chain, [1 + j] CTAs done with GEMM j
     size_t counters;      // int32[kGemmSlots][max_tiles_n]: split-tile arrival counters
     size_t partial;       // float[kGemmSlots][max_ctas][2][rows8][128]

@@ -103,7 +103,7 @@ def test_lengths_out_of_range(w12, length, commit):
 
 def counters(s):
     """The writer's words of the workspace: its arrivals."""
-    return s.ws.buf[256:512].view(torch.int32).tolist()
+    return s.ws.buf[256:256 + 2048].view(torch.int32).tolist()
 
 
 @pytest.mark.parametrize("n,top,H,bt", [(70, 900, 1, 128), (48, 1400, 3, 128), (90, 700, 2, 32), (300, 150, 1, 64)])
