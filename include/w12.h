@@ -499,7 +499,8 @@ w12_status w12_tlv_splice(const w12_tree *t1, const int32_t *c_tok, const int32_
  *   accepted row (w12_tree_accept, w12_tree_verify_sampled) --w12_kv_commit--> cache
  *
  * Limits: head_dim 128; block_tokens 32, 64 or 128; at most 64 query heads to
- * a key/value head; n_req <= 512; anything else is W12_E_UNSUPPORTED.
+ * a key/value head; n_kv_heads <= 1024; n_req <= 512; n_blocks * n_kv_heads <
+ * 2^24; max_blocks * block_tokens < 2^31; anything else is W12_E_UNSUPPORTED.
  * ---------------------------------------------------------------------- */
 
 typedef struct {

@@ -50,10 +50,13 @@
 // reduction over lanes at all; the same slow path raises the reference of the
 // value scales, which P carries.  A raise costs several tiles, so a reference
 // is set 2^6 above the maximum: with normally distributed scores that leaves
-// next to none but the first (set at the maximum, 32 rows behind 32771 tokens
-// took 88 us; 2^6 above, 71).  What P can hold below the reference is F16's
+// next to none but the first.  What P can hold below the reference is F16's
 // range less those 2^12 and 2 for the value scales: every binade of margin less
-// keeps weights half as large, but 2^5 took 67 us where 2^6 takes 62, 2^4 74.
+// keeps weights half as large, but 32 rows behind 32771 tokens take 67 us with
+// 2^5, 74 with 2^4 and 97 with 2^2 where they take 60 to 62 with 2^6.  Scores
+// that rise along the context cost their raises: 152 rows of 64 heads behind
+// 40000 tokens take 363 us flat, 369 rising by 2^30 in all and 478 by 2^300; of
+// one head 224, 225 and 240; falling, nothing.
 // A token that outweighs the others by 2^20 and more would leave them few bits
 // or none, and if its own value is small they are the output.  So every 128
 // tiles of a group a column whose scores have all come to lie far below its
@@ -62,11 +65,11 @@
 // 2^-26 of a larger one: together 2^-13 of its weight at most.
 //
 // What bounds it.  One row behind a long context: memory (131072 tokens of 8
-// heads, 268 MB: 57.4 us, 4.7 TB/s, of which the tiles' loop 46 us at 5.8).
+// heads, 268 MB: 55.6 us, 4.8 TB/s, of which the tiles' loop 46 us at 5.8).
 // Many rows: the tensor cores' turn of a tile.  At M = 128 a product costs them
 // some 75 to 130 cycles however few its columns, so a tile takes 1280 cycles at
-// 16 columns, 1740 at 48 and 2250 at 80 (32 rows behind 32771 tokens: 61 to
-// 65 us; 256 rows of 32 requests behind up to 16384: 195.5 us, 3.8 TB/s), and a
+// 16 columns, 1740 at 48 and 2250 at 80 (32 rows behind 32771 tokens: 60 to
+// 62 us; 256 rows of 32 requests behind up to 16384: 198 us, 3.8 TB/s), and a
 // segment's start and end some 8000 to 23000 more.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -98,7 +101,8 @@ constexpr int kThreads = 128 + kSoft + 256; // warps: 0 K copies, 1 scores, 2 V 
 // Registers a thread: at launch, of the softmax warps, of the others.  The
 // shares add up to no more than the launch has (a larger one would wait for
 // ever).  Shared memory leaves the L1 cache so little that a spilled register
-// is a read of L2, so the softmax warps must not spill.
+// is a read of L2: the shapes of 16 and 48 columns spill none, that of 80 five
+// (20 bytes stored, 28 read).
 constexpr int kRegsLaunch = 72, kRegsSoft = 88, kRegsOther = 48;
 static_assert(kSoft * kRegsSoft + (kThreads - kSoft) * kRegsOther <= kThreads * kRegsLaunch, "register shares");
 constexpr float kHead = 256.f;             // P of a weight of 1 under the reference scale
@@ -368,6 +372,7 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool x)
     return r != 0;
 }
 
+// the machine's 2^x, within 2^-22 of it; results under 2^-126 are zero
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -1351,10 +1356,10 @@ int launch_attn(const AttnArgs &a, void *stream)
                              : CU_TENSOR_MAP_SWIZZLE_128B))
         return (int)cudaErrorInvalidValue;
     // Columns of a segment: the least shape that holds an average request's rows
-    // and one row's heads.  One row of 5 heads behind 200 tokens takes 12.3 us
-    // with 16 columns and 14.3 with 48 (the same behind 131072); 8 rows of 5
-    // heads to a request 195 us with 48, 231 with 80 and 348 with 16; 32 rows of
-    // 5 heads 64 us with 80, 71 with 48 and 117 with 16.
+    // and one row's heads.  One row of 5 heads behind 131072 tokens takes 55.7 us
+    // with 16 columns, 56.0 with 48 and 71 with 80 (behind 200: 11.3, 12.3, 12.3);
+    // 8 rows of 5 heads to a request 198 us with 48, 237 with 80 and 348 with 16;
+    // 32 rows of 5 heads 60 us with 80, 71.5 with 48 and 118 with 16.
     const int64_t avg = (int64_t)((a.R + a.n_req - 1) / a.n_req) * p.G;
     p.cols = avg <= 16 ? 16 : avg <= 48 ? 48 : 80;
     p.fit = p.cols / p.G;

@@ -15,8 +15,9 @@
 // One CTA owns one block of tokens and a run of heads, so nothing is shared
 // between CTAs but the lengths (see below).  It stages the positions' cosines and
 // sines once; then for each head a warp takes consecutive tokens, a lane four
-// dimensions, and everything stays in registers: rows, turned keys (a pair's
-// other half comes from the lane that has it), the two maxima, codes.  Keys
+// dimensions, and what it works on stays in registers: rows, turned keys (a
+// pair's other half comes from the lane that has it), the two maxima, codes (all
+// 64 registers, and 48 to 56 bytes a thread spilled).  Keys
 // leave token-major as they are; values are transposed through shared memory
 // under an exclusive-or of the token group with the dimension, which keeps both
 // sides free of most bank conflicts, and leave as whole rows of a dimension
@@ -24,8 +25,8 @@
 // transposition).  What bounds a long prompt is memory, 4 bytes read and 2
 // written for each pair of key and value elements, and next to it the issue of
 // some 13 instructions an element between two barriers a head: 16 prompts of up
-// to 8192 tokens with 8 heads (546 MB) take 125 us, 4.4 TB/s.  (Rows staged two
-// heads ahead in shared memory took 146 us.)
+// to 8192 tokens with 8 heads (546 MB) take 123 us, 4.4 TB/s.  (Rows staged two
+// heads ahead in shared memory took 20 us more.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -479,8 +480,9 @@ int launch_kv_write(const KvArgs &a, void *stream)
     // (128 / bt of them an SM), since a CTA spends some 4 us on finding its
     // block and staging the tables before its first head, and a head's loads
     // hide behind the head before.  24 prompts of 700 tokens at most, blocks of
-    // 32: all 4 heads to a CTA 16.6 us, one 18.2; 16 of up to 8192 tokens: all
-    // 8 heads 125 us, 4 or 5 of them 138.
+    // 32: all 4 heads to a CTA 16.4 us, one 18.4; 16 of up to 8192 tokens: all
+    // 8 heads 123 us, 4 of them 133, one 229; 24 paths of a tree of 192 rows with
+    // 8 heads: one 13 to 16 us, all 8 21.
     const int64_t blocks = (commit ? 0 : (int64_t)a.n_rows / a.bt) + a.n_req;
     const int64_t parts = std::min<int64_t>(a.H, std::max<int64_t>(1, 128 / a.bt * a.num_sms / blocks));
     p.heads = (int32_t)((a.H + parts - 1) / parts);

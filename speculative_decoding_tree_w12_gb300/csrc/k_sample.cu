@@ -30,7 +30,7 @@
 // maxima, 25 for the sums, at the issue rate of some twenty instructions a
 // token, half of them expf, 8 for the last rows' draws and the paths, each a
 // chain of loads.  256 FP32 rows with a drafter's probabilities (156 MB, and as
-// much of the drafter's for the rows with a rejection) take 118 to 126 us: 25
+// much of the drafter's for the rows with a rejection) take 115 to 123 us: 25
 // and 36 for the two passes, 50 for some 40 rejected rows, which are few to
 // spread over the SMs and wait for their slowest.  One row takes 10 us, all of
 // it latency.
