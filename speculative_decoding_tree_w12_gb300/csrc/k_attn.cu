@@ -943,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             s.mneg[grp][n] = -ref;
                             s.mtop[grp][n] = fmaxf(s.mtop[grp][n], ref);
                         }
-                        s.delta[grp][n] = ex2(-m);
+                        s.delta[grp][n] = fresh ? 1.f : ex2(-m);   // (nothing to scale yet, and 2^-m may be no number)
                     }
                     named_bar(5 + wg, 128);
                     const float ref = must ? top_v : sref, fs = sref / ref;

@@ -28,9 +28,10 @@ def w12():
 
 class Shared:
     """n requests of one row each that read one cached context of `tokens` tokens (one head, no rotation): as many
-    segments as that are not split over CTAs.  Keys: dimension 0 as given, small random codes in eight others."""
+    segments as that are not split over CTAs.  Keys: dimension 0 as given, small random codes in eight others; the rows'
+    own keys: own_k0 in dimension 0."""
 
-    def __init__(self, w12, n, G, k0, seed, v=None):
+    def __init__(self, w12, n, G, k0, seed, v=None, own_k0=0.0):
         g = np.random.default_rng(seed)
         tokens = len(k0)
         blocks = -(-tokens // BT)
@@ -53,7 +54,9 @@ class Shared:
         q = np.zeros((n, G, D))
         q[:, :, 0] = 1.0
         q[:, :, 1:9] = np.round(g.standard_normal((n, G, 8)) * 16) / 64
-        x = np.concatenate([q.reshape(n, -1), np.zeros((n, D)), np.round(g.standard_normal((n, D)) * 16) / 16], 1)
+        self.own_k0, own_k = own_k0, np.zeros((n, D))
+        own_k[:, 0] = own_k0
+        x = np.concatenate([q.reshape(n, -1), own_k, np.round(g.standard_normal((n, D)) * 16) / 16], 1)
         self.rows = c(x.astype(np.float32)).bfloat16()
         assert torch.equal(self.rows.double().cpu(), torch.from_numpy(x))
         self.ws = w12.Workspace(1, 0, 0, n)
@@ -76,7 +79,7 @@ class Shared:
         outs = []
         for at in range(0, len(q), 1024):
             Q, o = q[at:at + 1024], own[at:at + 1024]
-            s = torch.cat([Q @ K.T * scale, torch.zeros(len(Q), 1, dtype=torch.float64, device="cuda")], 1)
+            s = torch.cat([Q @ K.T * scale, Q[:, :1] * self.own_k0 * scale], 1)
             p = torch.softmax(s, 1)
             last = p[:, -1:]
             ds = scale * (Q.abs() @ K.abs().T * 2.0 ** -12 + 2.0 ** -17 * Q.abs().amax(1, keepdim=True) * K.abs().sum(1)).amax(1)
@@ -127,6 +130,18 @@ def test_scores_in_steps(w12, G):
     k0 = np.concatenate([np.full(n, x) + 0.0 for x, n in zip(levels, lengths)])
     k0[g.choice(len(k0), 20, replace=False)] = 224
     compare(w12, Shared(w12, 160, G, k0, 8), 60 * math.log(2) / 448, 128 * 128 * 20)
+
+
+@pytest.mark.parametrize("G", [1, 40, 64])
+@pytest.mark.parametrize("tokens", [1, 100, 300, 5000])
+@pytest.mark.parametrize("size", [100.0, 130.0, 1000.0, 20000.0])
+def test_scores_far_from_zero(w12, G, tokens, size):
+    """Every score is +- size (of log 2) and a little; the row's own key weighs as much as the cached ones, or all or
+    nothing next to them."""
+    for sign in (1, -1):
+        for own in (16.0 * sign, 0.0, -16.0 * sign):
+            s = Shared(w12, 3, G, np.full(tokens, 16.0 * sign), 9, own_k0=own)
+            compare(w12, s, size * math.log(2) / 16, tokens)
 
 
 @pytest.mark.parametrize("G", [2, 5, 16])
