@@ -491,7 +491,8 @@ int launch_kv_write(const KvArgs &a, void *stream)
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     auto go = [&](auto kernel, int threads) {
-        if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        // (static shared memory counts too: up to 2.4 KB)
+        if (smem > 44 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return;
         kernel<<<grid, threads, smem, st>>>(p);
         e = cudaGetLastError();

@@ -175,3 +175,23 @@ def test_in_place_is_as_apart(w12):
         got.append((c.k, c.v, c.k_scale, c.v_scale, out))
     assert got[0][4].tolist() == (lens + cnt).tolist() and all(torch.equal(a, b) for a, b in zip(*got))
     assert ws.status() == 0
+
+
+@pytest.mark.parametrize("bt", [32, 64, 128])
+def test_every_rotated_width(w12, bt):
+    """Append and commit at every number of rotated dimensions, whose tables lie in shared memory."""
+    for rot in range(0, 129, 8):
+        s = World(w12, [bt - 3, 5], 2, bt, rot, bool(rot & 8), room=2 * bt + 8, seed=rot)
+        off = [0, 7, 7 + bt]
+        x = rows(s, off[-1], 2)
+        append(w12, s, x, off)
+        for r in range(2):
+            ref.kv_write(s.host, r, x[off[r]:off[r + 1], 0], x[off[r]:off[r + 1], 1], s.cos, s.sin, bool(rot & 8))
+        s.same()
+        x = rows(s, 8, 2)
+        k, v = (bf16(x[:, i].reshape(8, -1)) for i in range(2))
+        w12.w12_kv_commit(s.cache, s.rope, chains(w12, 2, 4), 2, ints([3, 6]), k, v, s.ws)
+        for r, path in enumerate((range(4), range(4, 7))):
+            ref.kv_write(s.host, r, x[path, 0], x[path, 1], s.cos, s.sin, bool(rot & 8))
+        s.same()
+        assert s.ws.status() == 0
