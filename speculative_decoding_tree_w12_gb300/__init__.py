@@ -600,8 +600,8 @@ def _ints(t, n, what, dev) -> int:
 def _rows(t, rows, width, what, dev):
     """(address, elements between rows) of `rows` or more bfloat16 rows of `width` contiguous elements."""
     shape, stride = t.shape, t.stride()
-    if t.dtype is not _torch.bfloat16 or len(shape) != 2 or shape[1] != width or shape[0] < rows or stride[1] != 1 \
-            or t.get_device() != dev:
+    if t.dtype is not _torch.bfloat16 or len(shape) != 2 or shape[1] != width or shape[0] < rows \
+            or (stride[1] != 1 and shape[0]) or t.get_device() != dev:
         raise ValueError(f"{what}: bfloat16 rows [>= {rows}][{width}] with contiguous elements on cuda:{dev} wanted, got "
                          f"{t.dtype} {tuple(shape)} on {t.device}")
     return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], width)

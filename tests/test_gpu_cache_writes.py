@@ -195,3 +195,13 @@ def test_every_rotated_width(w12, bt):
             ref.kv_write(s.host, r, x[path, 0], x[path, 1], s.cos, s.sin, bool(rot & 8))
         s.same()
         assert s.ws.status() == 0
+
+
+def test_no_rows(w12):
+    """An append without rows, whatever strides an empty tensor has, reports the lengths as they are."""
+    s = World(w12, [5, 40], 2, 32, seed=25)
+    none = torch.empty(0, dtype=torch.bfloat16, device="cuda")
+    for k in (none.view(0, 2 * D), none.as_strided((0, 2 * D), (0, 0)), none.as_strided((0, 2 * D), (1, 7))):
+        out = w12.w12_kv_append(s.cache, s.rope, k, k, ints([0, 0, 0]), s.ws, len_out=torch.full_like(s.cache.len, -5))
+        s.same()
+        assert out.tolist() == [5, 40] and s.ws.status() == 0
