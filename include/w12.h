@@ -13,9 +13,11 @@
  * w12_lmhead_argmax_q, w12_verify_step_q), the certified LM head
  * (w12_head_cert_norms, w12_lmhead_argmax_certified), the TLV splice of two
  * trees (w12_tlv_chain, w12_tlv_splice), a recurrent (Gated DeltaNet)
- * layer over a tree (w12_gdn_tree_verify, w12_gdn_commit), attention over a
- * paged 8-bit KV cache (w12_kv_append, w12_tree_attention, w12_kv_commit) and
- * acceptance by sampling (w12_tree_verify_sampled).
+ * layer over a tree (w12_gdn_tree_verify, w12_gdn_commit), over prompts
+ * (w12_gdn_prefill) and single tokens (w12_gdn_step), the norms around a block
+ * (w12_gdn_norm, w12_block_norm), attention over a paged 8-bit KV cache
+ * (w12_kv_append, w12_tree_attention, w12_kv_commit) and acceptance by sampling
+ * (w12_tree_verify_sampled).
  *
  * Sources (SpecPilot explainer at jaehun.me, "SpecPilot: Autonomous Algorithm
  * Discovery and Systems Optimization for Speculative Decoding"; the summary
@@ -393,6 +395,98 @@ w12_status w12_gdn_wy_verify(const w12_gdn_layer *layer, const w12_tree *tree, i
  */
 w12_status w12_gdn_wy_commit(const w12_gdn_layer *layer, const w12_tree *tree, int32_t n_req, const int32_t *acc_node,
                              const float *u, float *state, void *ws, size_t ws_bytes, w12_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The same layer over prompts and single tokens
+ *
+ * Rows are tokens in order, as the linears leave them:
+ *
+ *   prompt rows --w12_gdn_prefill--> outputs, state --+-- w12_gdn_step --> ...
+ *                                                     +-- w12_gdn_tree_verify, w12_gdn_commit --> ...
+ *
+ * Limits: head_dim 128; n_heads a multiple of n_qk_heads, at most 65535; n_req <= 512; anything
+ * else is W12_E_UNSUPPORTED.
+ * ---------------------------------------------------------------------- */
+
+typedef struct {
+    int32_t n_heads;             /* value heads: a state, a gate and a strength each */
+    int32_t n_qk_heads;          /* query/key heads: value head h reads h / (n_heads / n_qk_heads) */
+    int32_t head_dim;
+    int32_t n_rows;
+    const uint16_t *q, *k;       /* device BF16 [n_rows][n_qk_heads][d], rows *_stride elements apart (a multiple of 8), 16-byte aligned */
+    const uint16_t *v;           /* device BF16 [n_rows][n_heads][d], the same */
+    int64_t q_stride, k_stride, v_stride;
+    const float *alpha, *beta;   /* device [n_rows][n_heads]: gates and write strengths */
+} w12_gdn_rows;
+
+/*
+ * Rows row_off[r] .. row_off[r+1]-1 (device [n_req + 1]) continue request r's
+ * state S0[r] (device FP32 [n_req][n_heads][d][d] as S[v][k], 16-byte aligned;
+ * NULL: zero): every row's output o (device FP32 [n_rows][n_heads][d]) and the
+ * state behind the last row (device, layout of S0, 16-byte aligned; may be S0
+ * itself, else the two do not overlap).  Any number of rows a request, none
+ * included: its state is then copied.  Rows outside every request are neither
+ * read nor written.  Requests' rows do not overlap.
+ * Outputs and states are those of the token-by-token form to FP32 rounding:
+ * FP32 operands enter the tensor cores as three BF16 pieces that add up to them, with
+ * FP32 accumulation.  Gates may be zero.  A value of a row that is not finite reaches the
+ * outputs of its own run of 64 rows (counted from row_off[r]) and all later
+ * ones of its request and head; other requests and heads never.
+ * ws: as for w12_tree_build.  Device checks: offsets that descend or leave
+ * [0, n_rows] set W12_E_INVAL in the status word, and that request is left as it was;
+ * a wait that runs out sets W12_E_TIMEOUT (outputs undefined).
+ */
+w12_status w12_gdn_prefill(const w12_gdn_rows *rows, int32_t n_req, const int32_t *row_off, const float *S0,
+                           float *state, float *o, void *ws, size_t ws_bytes, w12_stream_t stream);
+
+/*
+ * One token of every request: row r continues request r (n_rows requests, at
+ * most 65535 of them).  S0, state and o as above.
+ */
+w12_status w12_gdn_step(const w12_gdn_rows *rows, const float *S0, float *state, float *o, w12_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Norms around a block.  rms(x) = x / sqrt(mean(x^2) + eps), eps > 0; sums and
+ * products in FP32, each result rounded once.  Weights are BF16.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * The recurrent layer's outputs o (device FP32 [n_rows][n_heads][head_dim],
+ * 16-byte aligned) as the next linear reads them, BF16 rows x x_stride
+ * elements apart: per head x = rms(o) weight silu(z), with gate_first
+ * x = rms(o silu(z)) weight.  weight[head_dim]: shared by the heads.  z: the gate's rows
+ * (BF16 [n_rows][n_heads * head_dim], z_stride elements apart), or NULL: no gate.  BF16
+ * pointers 16-byte aligned, strides multiples of 8.  x may be z, with the same
+ * stride.  head_dim 128 (else W12_E_UNSUPPORTED).
+ */
+w12_status w12_gdn_norm(const float *o, int32_t n_rows, int32_t n_heads, int32_t head_dim, const uint16_t *z,
+                        int64_t z_stride, const uint16_t *weight, float eps, int32_t gate_first, uint16_t *x,
+                        int64_t x_stride, w12_stream_t stream);
+
+typedef struct {
+    int32_t n_rows;
+    int32_t h_f32;               /* the residual stream's type: 0 BF16, 1 FP32 */
+    int64_t n;                   /* row length: a multiple of 8, at most 16384 */
+    const void *h;               /* device [n_rows][n], rows h_stride elements apart */
+    int64_t h_stride;
+    void *h_out;                 /* h' (may be h, with the same stride); unused without y */
+    int64_t h_out_stride;
+    const uint16_t *y;           /* the block's output, BF16 rows, or NULL: h' = h */
+    int64_t y_stride;
+    const uint16_t *post;        /* [n]: norm behind the block, or NULL: none */
+    float scale;                 /* residual scale */
+    const uint16_t *pre;         /* [n]: norm in front of the next block, or NULL: no x */
+    float eps;
+    uint16_t *x;                 /* BF16 rows (may be y, with the same stride) */
+    int64_t x_stride;
+} w12_residual;
+
+/*
+ * Between two blocks: h' = h + scale t, t = y or rms(y) post; x = rms(h') pre,
+ * of the FP32 h' before it is rounded for storage.  Pointers 16-byte
+ * aligned, strides multiples of 8 (FP32 rows: of 4).  At least one of y and pre.
+ */
+w12_status w12_block_norm(const w12_residual *res, w12_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * The verify step

@@ -407,3 +407,32 @@ def gdn_commit(S0: np.ndarray, k: np.ndarray, v: np.ndarray, alpha: np.ndarray, 
                 + b64[i][:, None, None] * vf[i][:, :, None] * kf[i][:, None, :]
         out[r] = S
     return out
+
+
+def gdn_sequence(S0: Optional[np.ndarray], q: np.ndarray, k: np.ndarray, v: np.ndarray, alpha: np.ndarray, beta: np.ndarray,
+                 row_off: np.ndarray):
+    """The layer over token rows in order (FP64): rows row_off[r] ..
+    row_off[r+1]-1 continue request r's state S0[r] (None: zero) by the update of
+    gdn_tree_path; value head h reads query/key head h // (H / Hk).  q, k: BF16 bits
+    [T][Hk][d]; v: BF16 bits [T][H][d]; alpha, beta [T][H].  Returns o [T][H][d]
+    (NaN in rows outside every request), the states behind the last rows, and per request and head the largest
+    ||S[v]|| + |v| met, which bounds every value in between for keys of unit norm."""
+    qf, kf, vf = _bf16_to_f64(q), _bf16_to_f64(k), _bf16_to_f64(v)
+    a64, b64 = np.asarray(alpha, np.float64), np.asarray(beta, np.float64)
+    T, H, d = vf.shape
+    group = H // kf.shape[1]
+    qf, kf = np.repeat(qf, group, 1), np.repeat(kf, group, 1)
+    n = len(row_off) - 1
+    S = np.zeros((n, H, d, d)) if S0 is None else np.array(S0, np.float64)
+    o = np.full((T, H, d), np.nan)
+    top = np.zeros((n, H))
+    for r in range(n):
+        T_r = S[r]
+        for i in range(int(row_off[r]), int(row_off[r + 1])):
+            top[r] = np.maximum(top[r], np.sqrt((T_r ** 2).sum(-1)).max(-1) + np.abs(vf[i]).max(-1))
+            u = b64[i][:, None] * (vf[i] - a64[i][:, None] * np.matmul(T_r, kf[i][:, :, None])[..., 0])
+            T_r *= a64[i][:, None, None]
+            T_r += u[:, :, None] * kf[i][:, None, :]
+            o[i] = np.matmul(T_r, qf[i][:, :, None])[..., 0]
+        top[r] = np.maximum(top[r], np.sqrt((T_r ** 2).sum(-1)).max(-1))
+    return o, S, top

@@ -9,8 +9,10 @@ below raises -- there is no fallback.
 Entry points (same names as the C ABI): ``w12_pack``, ``w12_unpack``,
 ``w12_load_check``, ``w12_gemm``, ``w12_lmhead_argmax``, ``w12_tree_build``,
 ``w12_tree_accept``, ``w12_verify_step``, the TLV calls (``w12_verify_step_q``,
-``w12_tlv_chain``, ``w12_tlv_splice``), the attention layer's
-``w12_kv_append``, ``w12_tree_attention``, ``w12_kv_commit``, and
+``w12_tlv_chain``, ``w12_tlv_splice``), the recurrent layer's
+``w12_gdn_tree_verify``, ``w12_gdn_commit``, ``w12_gdn_prefill`` and
+``w12_gdn_step``, the norms ``w12_gdn_norm`` and ``w12_block_norm``, the attention
+layer's ``w12_kv_append``, ``w12_tree_attention``, ``w12_kv_commit``, and
 ``w12_tree_verify_sampled``, plus the workspace helpers.
 """
 from __future__ import annotations
@@ -110,6 +112,10 @@ def lib():
             "w12_gdn_commit": ([p, p, i32, p, p, p, sz, p], C.c_int),
             "w12_gdn_wy_verify": ([p, p, i32, p, p, p, sz, p], C.c_int),
             "w12_gdn_wy_commit": ([p, p, i32, p, p, p, p, sz, p], C.c_int),
+            "w12_gdn_prefill": ([p, i32, p, p, p, p, p, sz, p], C.c_int),
+            "w12_gdn_step": ([p, p, p, p, p], C.c_int),
+            "w12_gdn_norm": ([p, i32, i32, i32, p, i64, p, C.c_float, i32, p, i64, p], C.c_int),
+            "w12_block_norm": ([p, p], C.c_int),
             "w12_tlv_splice": ([p, p, p, p, i32, i32, p, p, p, p, sz, p], C.c_int),
             "w12_kv_append": ([p, p, i32, p, i64, p, i64, i32, p, p, p, sz, p], C.c_int),
             "w12_kv_commit": ([p, p, p, i32, p, p, i64, p, i64, p, p, sz, p], C.c_int),
@@ -733,6 +739,169 @@ def w12_tree_attention(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n
     if s:
         raise W12Error(s, "w12_tree_attention")
     return out
+
+
+# ---------------------------------------------------------------------------
+# the recurrent layer over prompts and single tokens, norms around a block
+# ---------------------------------------------------------------------------
+
+class GdnRowsC(C.Structure):
+    _fields_ = [("n_heads", C.c_int32), ("n_qk_heads", C.c_int32), ("head_dim", C.c_int32), ("n_rows", C.c_int32),
+                ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("q_stride", C.c_int64), ("k_stride", C.c_int64),
+                ("v_stride", C.c_int64), ("alpha", C.c_void_p), ("beta", C.c_void_p)]
+
+
+class GdnRows:
+    """A recurrent layer's token rows: q and k (bfloat16 [T][n_qk_heads * 128]),
+    v (bfloat16 [T][H * 128]; slices of a fused row are fine), gates alpha and
+    write strengths beta (float32 [T][H]).  Value head h reads query/key head
+    h // (H // n_qk_heads).  The tensors stay the caller's."""
+
+    def __init__(self, q, k, v, alpha, beta):
+        torch = _runtime()
+        lib()
+        _want(alpha, torch.float32, (None, None), "alpha")
+        T, H = alpha.shape
+        _want(beta, torch.float32, (T, H), "beta")
+        self.dev = alpha.get_device()
+        if q.dim() != 2 or q.shape[0] != T or k.shape[0] != T or v.shape[0] != T:
+            raise ValueError(f"q, k, v: {T} rows wanted, as alpha has")
+        if H < 1 or q.shape[1] < 128 or q.shape[1] % 128 or H % (q.shape[1] // 128):
+            raise ValueError(f"q: rows of whole heads of 128 wanted that {H} value heads share evenly, got {q.shape[1]}")
+        _same_device(self.dev, "rows", beta, q, k, v)
+        self.q, self.k, self.v, self.alpha, self.beta = q, k, v, alpha, beta
+        self.T, self.H, self.d = int(T), int(H), 128
+        (qa, qs), (ka, ks), (va, vs) = (_rows(t, T, w, n, self.dev) for t, w, n in
+                                        ((q, q.shape[1], "q"), (k, q.shape[1], "k"), (v, H * 128, "v")))
+        self.c = GdnRowsC(H, q.shape[1] // 128, 128, T, qa, ka, va, qs, ks, vs, alpha.data_ptr(), beta.data_ptr())
+        self.ref = C.byref(self.c)
+
+    def _buffers(self, n_req, S0, state, out):
+        """The calls' state and output tensors, made or checked."""
+        dev, shape = self.dev, (n_req, self.H, self.d, self.d)
+        if dev < 0:
+            _refuse(dev, n_req, None, self)
+        new = lambda *s: _torch.empty(s, dtype=_torch.float32, device=self.alpha.device)
+        state = new(*shape) if state is None else state
+        out = new(self.T, self.H, self.d) if out is None else out
+        for t, what, want in ((S0, "S0", shape), (state, "state", shape), (out, "out", (self.T, self.H, self.d))):
+            if t is not None and (t.dtype is not _torch.float32 or t.shape != want or not t.is_contiguous()
+                                  or t.get_device() != dev):
+                raise ValueError(f"{what}: contiguous float32 {tuple(want)} on cuda:{dev} wanted, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device}")
+        return state, out
+
+
+def w12_gdn_prefill(rows: GdnRows, row_off, ws: Workspace, S0=None, state=None, out=None, stream=None):
+    """Rows row_off[r]..row_off[r+1]-1 (int32 [n_req + 1]) continue request
+    r's state -> (out, state): every row's output (float32 [T][H][128]) and the
+    states behind the last rows (float32 [n_req][H][128][128] as S[v][k]).  S0: the
+    states in front (default: zero); state may be S0 itself."""
+    n = row_off.shape[0] - 1
+    state, out = rows._buffers(n, S0, state, out)
+    if ws.dev != rows.dev:
+        _refuse(rows.dev, n, None, ws)
+    s = _lib.w12_gdn_prefill(rows.ref, n, _ints(row_off, n + 1, "row_off", rows.dev), _dp(S0), state.data_ptr(),
+                             out.data_ptr(), ws.addr, ws.nbytes, _st(stream))
+    if s:
+        raise W12Error(s, "w12_gdn_prefill")
+    return out, state
+
+
+def w12_gdn_step(rows: GdnRows, S0=None, state=None, out=None, stream=None):
+    """One token of every request: row r continues request r's state -> (out,
+    state), as for ``w12_gdn_prefill``."""
+    state, out = rows._buffers(rows.T, S0, state, out)
+    s = _lib.w12_gdn_step(rows.ref, _dp(S0), state.data_ptr(), out.data_ptr(), _st(stream))
+    if s:
+        raise W12Error(s, "w12_gdn_step")
+    return out, state
+
+
+def w12_gdn_norm(o, weight, z=None, eps: float = 1e-6, gate_first: bool = False, out=None, stream=None):
+    """The recurrent layer's outputs o (float32 [R][H][128]) as the next linear
+    reads them -> bfloat16 [R][H * 128]: rms(o) * weight * silu(z) per head, with
+    ``gate_first`` rms(o * silu(z)) * weight.  weight: bfloat16 [128]; z:
+    bfloat16 rows [R][H * 128] (slices of a fused row are fine), optional."""
+    _runtime()
+    lib()
+    _want(o, _torch.float32, (None, None, 128), "o")
+    R, H, d = o.shape
+    _want(weight, _torch.bfloat16, (d,), "weight")
+    dev = o.get_device()
+    if dev < 0 or weight.get_device() != dev:
+        raise ValueError("o and weight: tensors of one CUDA device wanted")
+    if out is None:
+        out = _torch.empty((R, H * d), dtype=_torch.bfloat16, device=o.device)
+    za, zs = (None, 0) if z is None else _rows(z, R, H * d, "z", dev)
+    s = _lib.w12_gdn_norm(o.data_ptr(), R, H, d, za, zs, weight.data_ptr(), eps, int(gate_first),
+                          *_rows(out, R, H * d, "out", dev), _st(stream))
+    if s:
+        raise W12Error(s, "w12_gdn_norm")
+    return out
+
+
+class ResidualC(C.Structure):
+    _fields_ = [("n_rows", C.c_int32), ("h_f32", C.c_int32), ("n", C.c_int64), ("h", C.c_void_p), ("h_stride", C.c_int64),
+                ("h_out", C.c_void_p), ("h_out_stride", C.c_int64), ("y", C.c_void_p), ("y_stride", C.c_int64),
+                ("post", C.c_void_p), ("scale", C.c_float), ("pre", C.c_void_p), ("eps", C.c_float), ("x", C.c_void_p),
+                ("x_stride", C.c_int64)]
+
+
+def _stream_rows(t, rows, width, f32, what, dev):
+    """_rows of a residual stream, bfloat16 or float32."""
+    if not f32:
+        return _rows(t, rows, width, what, dev)
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not _torch.float32 or len(shape) != 2 or shape[1] != width or shape[0] < rows \
+            or (stride[1] != 1 and shape[0]) or t.get_device() != dev:
+        raise ValueError(f"{what}: float32 rows [>= {rows}][{width}] with contiguous elements on cuda:{dev} wanted, got "
+                         f"{t.dtype} {tuple(shape)} on {t.device}")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], width)
+
+
+def w12_block_norm(h, y=None, pre=None, post=None, scale: float = 1.0, eps: float = 1e-6, h_out=None, out=None, stream=None):
+    """Between two blocks -> (h', x): h' = h + scale * t with t = y, or
+    rms(y) * post; x = rms(h') * pre (bfloat16), of h' before it is rounded.
+    h: the residual stream, bfloat16 or float32 rows [R][n]; y: the block's
+    output, bfloat16 rows (None: h' = h); pre, post: bfloat16 [n] (None: no norm
+    there, and without pre no x).  h' goes to ``h_out`` (default: new rows; may
+    be h), x to ``out``."""
+    _runtime()
+    lib()
+    if h.dim() != 2:
+        raise ValueError("h: rows wanted")
+    R, n = h.shape
+    dev, f32 = h.get_device(), h.dtype is _torch.float32
+    if dev < 0:
+        raise ValueError("tensors of a CUDA device wanted")
+    for w, what in ((pre, "pre"), (post, "post")):
+        if w is not None:
+            _want(w, _torch.bfloat16, (n,), what)
+            if w.get_device() != dev:
+                raise ValueError(f"{what}: on cuda:{dev} wanted")
+    ha, hs = _stream_rows(h, R, n, f32, "h", dev)
+    ya = ys = oa = os_ = xa = xs = 0
+    if y is None:
+        if h_out is not None or post is not None:
+            raise ValueError("h_out and post: only with y")
+        h_out = h
+    else:
+        ya, ys = _rows(y, R, n, "y", dev)
+        if h_out is None:
+            h_out = _torch.empty((R, n), dtype=h.dtype, device=h.device)
+        oa, os_ = _stream_rows(h_out, R, n, f32, "h_out", dev)
+    if pre is not None:
+        if out is None:
+            out = _torch.empty((R, n), dtype=_torch.bfloat16, device=h.device)
+        xa, xs = _rows(out, R, n, "out", dev)
+    elif out is not None:
+        raise ValueError("out: only with pre")
+    s = _lib.w12_block_norm(C.byref(ResidualC(R, int(f32), n, ha, hs, oa, os_, ya, ys, _dp(post), scale, _dp(pre), eps, xa, xs)),
+                            _st(stream))
+    if s:
+        raise W12Error(s, "w12_block_norm")
+    return h_out, out
 
 
 # ---------------------------------------------------------------------------

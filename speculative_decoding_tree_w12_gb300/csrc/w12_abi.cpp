@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <vector>
 
@@ -700,6 +701,45 @@ w12_status w12_verify_step_q(const w12_step *step, const w12_tree *tree, int32_t
 
 namespace {
 
+// rows of `width` BF16 values: 16-byte aligned, `stride` elements apart
+bool rows_ok(const uint16_t *x, int64_t stride, int64_t width)
+{
+    return x && aligned(x, 16) && stride >= width && stride % 8 == 0;
+}
+
+w12_status gdn_seq_args(const w12_gdn_rows *L, const float *S0, float *state, float *o, GdnSeqArgs &a)
+{
+    if (!L || !aligned(state, 16) || !aligned(S0, 16)) return W12_E_INVAL;
+    if (L->n_heads < 1 || L->n_qk_heads < 1 || L->n_rows < 0) return W12_E_INVAL;
+    if (L->head_dim != kGdnDim || L->n_heads % L->n_qk_heads || L->n_heads > 65535) return W12_E_UNSUPPORTED;
+    if (L->n_rows > 0) {
+        const int64_t wk = (int64_t)L->n_qk_heads * kGdnDim, wv = (int64_t)L->n_heads * kGdnDim;
+        if (!rows_ok(L->q, L->q_stride, wk) || !rows_ok(L->k, L->k_stride, wk) || !rows_ok(L->v, L->v_stride, wv))
+            return W12_E_INVAL;
+        if (!L->alpha || !L->beta || !o || !aligned(L->alpha, 4) || !aligned(L->beta, 4) || !aligned(o, 16)) return W12_E_INVAL;
+        // the tensor maps' strides are 40-bit numbers of bytes
+        if (std::max({L->q_stride, L->k_stride, L->v_stride}) >= INT64_C(1) << 38) return W12_E_UNSUPPORTED;
+    }
+    a = GdnSeqArgs{};
+    a.H = L->n_heads;
+    a.Hk = L->n_qk_heads;
+    a.n_rows = L->n_rows;
+    a.q = L->q;
+    a.k = L->k;
+    a.v = L->v;
+    a.q_stride = L->q_stride;
+    a.k_stride = L->k_stride;
+    a.v_stride = L->v_stride;
+    a.alpha = L->alpha;
+    a.beta = L->beta;
+    a.S0 = S0;
+    a.state = state;
+    a.o = o;
+    a.timeout_ns = g_timeout_ns;
+    a.debug_flags = g_debug_flags;
+    return W12_OK;
+}
+
 w12_status gdn_args(const w12_gdn_layer *L, const w12_tree *tree, int32_t n_req, GdnArgs &a)
 {
     if (!L || !tree || !tree->parent || !tree->req_row_off || !L->S0 || !L->q || !L->k || !L->v || !L->alpha ||
@@ -793,6 +833,97 @@ w12_status w12_gdn_commit(const w12_gdn_layer *layer, const w12_tree *tree, int3
     a.out = state;
     a.status = W.status();
     return cuda_status(launch_gdn(a, kGdnCommit, stream));
+}
+
+w12_status w12_gdn_prefill(const w12_gdn_rows *rows, int32_t n_req, const int32_t *row_off, const float *S0,
+                           float *state, float *o, void *ws, size_t ws_bytes, w12_stream_t stream)
+{
+    GdnSeqArgs a;
+    w12_status s = gdn_seq_args(rows, S0, state, o, a);
+    if (s != W12_OK) return s;
+    if (n_req < 1 || !row_off || !state) return W12_E_INVAL;
+    if (n_req > kMaxBudget) return W12_E_UNSUPPORTED;
+    const WsLayout L = layout_for(1, 0, 0, n_req);
+    if ((s = ws_check(ws, ws_bytes, L)) != W12_OK) return s;
+    Ws W{static_cast<uint8_t *>(ws), L};
+    a.n_req = n_req;
+    a.off = row_off;
+    a.status = W.status();
+    return cuda_status(launch_gdn_prefill(a, stream));
+}
+
+w12_status w12_gdn_step(const w12_gdn_rows *rows, const float *S0, float *state, float *o, w12_stream_t stream)
+{
+    GdnSeqArgs a;
+    const w12_status s = gdn_seq_args(rows, S0, state, o, a);
+    if (s != W12_OK) return s;
+    if (a.n_rows == 0) return W12_OK;
+    if (!state) return W12_E_INVAL;
+    if (a.n_rows > 65535) return W12_E_UNSUPPORTED;
+    a.n_req = a.n_rows;
+    return cuda_status(launch_gdn_step(a, stream));
+}
+
+w12_status w12_gdn_norm(const float *o, int32_t n_rows, int32_t n_heads, int32_t head_dim, const uint16_t *z,
+                        int64_t z_stride, const uint16_t *weight, float eps, int32_t gate_first, uint16_t *x,
+                        int64_t x_stride, w12_stream_t stream)
+{
+    if (n_rows < 0 || n_heads < 1 || !(eps > 0.f) || !(eps < INFINITY)) return W12_E_INVAL;
+    if (head_dim != kGdnDim || (int64_t)n_rows * n_heads > INT32_MAX) return W12_E_UNSUPPORTED;
+    if (n_rows == 0) return W12_OK;
+    const int64_t width = (int64_t)n_heads * head_dim;
+    if (!o || !aligned(o, 16) || !weight || !aligned(weight, 16) || !rows_ok(x, x_stride, width)) return W12_E_INVAL;
+    if (z && (!rows_ok(z, z_stride, width) || (z == x && z_stride != x_stride))) return W12_E_INVAL;
+    GdnNormArgs a{};
+    a.o = o;
+    a.z = z;
+    a.w = weight;
+    a.x = x;
+    a.z_stride = z_stride;
+    a.x_stride = x_stride;
+    a.rows = n_rows;
+    a.H = n_heads;
+    a.gate_first = gate_first;
+    a.eps = eps;
+    return cuda_status(launch_gdn_norm(a, stream));
+}
+
+w12_status w12_block_norm(const w12_residual *r, w12_stream_t stream)
+{
+    if (!r || r->n_rows < 0 || r->n < 1 || (!r->y && !r->pre) || (r->post && !r->y)) return W12_E_INVAL;
+    if (!(r->eps > 0.f) || !(r->eps < INFINITY) || (r->y && !std::isfinite(r->scale))) return W12_E_INVAL;
+    if (r->n % 8 || r->n > kMaxNormRow) return W12_E_UNSUPPORTED;
+    if (r->n_rows == 0) return W12_OK;
+    const int64_t unit = r->h_f32 ? 4 : 8;
+    if (!r->h || !aligned(r->h, 16) || r->h_stride < r->n || r->h_stride % unit) return W12_E_INVAL;
+    if (r->y) {
+        if (!rows_ok(r->y, r->y_stride, r->n)) return W12_E_INVAL;
+        if (!r->h_out || !aligned(r->h_out, 16) || r->h_out_stride < r->n || r->h_out_stride % unit) return W12_E_INVAL;
+        if (r->h_out == r->h && r->h_out_stride != r->h_stride) return W12_E_INVAL;
+    }
+    if (r->post && !aligned(r->post, 16)) return W12_E_INVAL;
+    if (r->pre) {
+        if (!aligned(r->pre, 16) || !rows_ok(r->x, r->x_stride, r->n)) return W12_E_INVAL;
+        if (r->x == r->y && r->x_stride != r->y_stride) return W12_E_INVAL;
+        if (r->x == r->h || (r->y && r->x == r->h_out)) return W12_E_INVAL;
+    }
+    BlockNormArgs a{};
+    a.h = r->h;
+    a.h_out = r->h_out;
+    a.h_f32 = r->h_f32 != 0;
+    a.y = r->y;
+    a.post = r->post;
+    a.pre = r->pre;
+    a.x = r->x;
+    a.h_stride = r->h_stride;
+    a.ho_stride = r->h_out_stride;
+    a.y_stride = r->y_stride;
+    a.x_stride = r->x_stride;
+    a.rows = r->n_rows;
+    a.n = r->n;
+    a.scale = r->scale;
+    a.eps = r->eps;
+    return cuda_status(launch_block_norm(a, stream));
 }
 
 w12_status w12_tlv_chain(const int32_t *c_len, const int32_t *t1_row_off, int32_t n_req, int32_t budget, int32_t *m,
@@ -902,12 +1033,6 @@ w12_status rope_ok(const w12_rope *r, RopeArgs &a)
     a.adjacent = r->adjacent != 0;
     a.max_pos = r->max_pos;
     return W12_OK;
-}
-
-// rows of `width` BF16 values: 16-byte aligned, `stride` elements apart
-bool rows_ok(const uint16_t *x, int64_t stride, int64_t width)
-{
-    return x && aligned(x, 16) && stride >= width && stride % 8 == 0;
 }
 
 w12_status kv_entry(const w12_kv_cache *c, const w12_rope *rope, int32_t n_req, const uint16_t *k, int64_t k_stride,

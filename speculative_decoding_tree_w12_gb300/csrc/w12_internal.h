@@ -160,6 +160,47 @@ struct GdnArgs {
 };
 int launch_gdn(const GdnArgs &a, int mode, void *stream);
 
+// recurrent layer over prompts (k_gdn_prefill.cu) and single tokens (k_gdn_step.cu)
+struct GdnSeqArgs {
+    int32_t H, Hk, n_req, n_rows;   // value heads, query/key heads
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;   // elements between rows
+    const float *alpha, *beta;      // [n_rows][H]
+    const int32_t *off;             // prefill: [n_req + 1]
+    const float *S0;                // [n_req][H][d][d] or null (zero)
+    float *state, *o;
+    uint64_t timeout_ns;
+    int32_t *status;
+    int32_t debug_flags;
+};
+int launch_gdn_prefill(const GdnSeqArgs &a, void *stream);
+int launch_gdn_step(const GdnSeqArgs &a, void *stream);
+
+// norms around a block (k_norm.cu)
+struct GdnNormArgs {
+    const float *o;
+    const uint16_t *z, *w;          // z may be null
+    uint16_t *x;
+    int64_t z_stride, x_stride;
+    int32_t rows, H;
+    int32_t gate_first;
+    float eps;
+};
+int launch_gdn_norm(const GdnNormArgs &a, void *stream);
+struct BlockNormArgs {
+    const void *h;
+    void *h_out;
+    int32_t h_f32;
+    const uint16_t *y, *post, *pre; // each may be null
+    uint16_t *x;
+    int64_t h_stride, ho_stride, y_stride, x_stride;
+    int32_t rows;
+    int64_t n;
+    float scale, eps;
+};
+constexpr int64_t kMaxNormRow = 16384;
+int launch_block_norm(const BlockNormArgs &a, void *stream);
+
 // TLV splice (k_tlv.cu)
 struct SpliceArgs {
     int32_t n_req, p1_max, t1_R, t2_R, R;
