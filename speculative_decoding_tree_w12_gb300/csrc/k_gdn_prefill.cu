@@ -16,17 +16,17 @@
 // memory throughout, so that all its products take their left operand from
 // there and no operand but M and A is ever written to shared memory:
 //     D_K[c][j] = S k_j    D_Q[c][j] = S q_j    U[c][i] = X M^T    U A^T    S' += U K.
-// A product's FP32 side (S, X, U, M, A) is taken as three BF16 pieces that add up to
-// it exactly, keys and queries as they are, all with FP32 accumulation: two
-// pieces (2^-17) would be the largest error of the layer by far.  Products of
-// two FP32 sides take the six pairs of pieces above 2^-24.
+// Products with keys and queries take those as they are and the FP32 side (S, U) as three BF16
+// pieces that add up to it exactly: two (2^-17) would be the largest error of the layer by
+// far.  Products of two FP32 sides (X M^T, U A^T) take both as two F16 pieces (2^-22) under a power of two
+// for each row, and of their four pairs all but the smallest.  All accumulation is FP32.
 //
 // Sixteen warps:
 //  * state warps (0..7; two threads to a state row, each with half of the
 //    columns; S itself stays in their registers) turn accumulators into operands,
 //  * chunk warps (8..11) make M and A of the next chunk: k.k and q.k on the
-//    tensor cores, then the inverse of two 32 x 32 blocks by columns and of the
-//    block below them from those two,
+//    tensor cores, then the inverse, of four 16 x 16 blocks by columns and of the
+//    blocks below them from those,
 //  * warp 12 issues the state warps' products, warp 13 the copies by TMA.
 // Every wait is bounded: a wait that runs out sets s.abort, which ends every
 // other wait at once, so all roles run to their ends; the state is then left
@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstddef>
 
 #include "w12_device.cuh"
 
@@ -47,31 +48,41 @@ constexpr int kC = 64;              // tokens of a chunk
 constexpr int kThreads = 512;
 constexpr int kStateWarps = 8;
 constexpr int kChunkThreads = 128;
-constexpr int kRegsLaunch = 128, kRegsState = 176, kRegsChunk = 104, kRegsIssue = 40;
+constexpr int kRegsLaunch = 128, kRegsState = 176, kRegsChunk = 104, kRegsIssue = 56;
 static_assert(256 * kRegsState + 128 * kRegsChunk + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register shares");
 
 // tensor memory columns
-constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; later U's pieces, first scaled for S', then for A
+constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; later three of U for S' and two for A, 32 each
 constexpr uint32_t kColDQ = 192;    // S q
-constexpr uint32_t kColDK = 256;    // S k; then X's low piece; then, with the next 64 columns, U K
-constexpr uint32_t kColX = 320;     // X's high and middle pieces
+constexpr uint32_t kColDK = 256;    // S k; then, with the next 64 columns, U K
+constexpr uint32_t kColX = 320;     // X's two pieces
 constexpr uint32_t kColU = 384;     // U; then U A
 constexpr uint32_t kColKK = 448;    // k.k (lanes 0..63) and q.k (lanes 64..127) of the next chunk
 
 constexpr int kLS = 68;             // FP32 row stride of L and M (16-byte rows, 4 banks apart)
-constexpr int kTS = 36;
+constexpr int kTS = 36, kTS16 = 20; // and of products in between, of 32 and 16 columns
 constexpr int kBarChunk = 1;        // named barrier of the chunk warps
+constexpr int kBarRow = 2;          // and of the two warps of 32 state rows (2 .. 5)
+constexpr int kStages = 3;          // of keys and queries (their chunk is prepared while two others are in use)
 
 struct PrefillShared {
-    uint8_t KQ[2][2 * 128 * 128];   // [stage][feature half][key rows, query rows][64 BF16], 128-byte swizzle
-    uint8_t M[2][3][kC * 128];      // pieces of M and A, rows of 64 BF16, 128-byte swizzle
-    uint8_t A[2][3][kC * 128];
+    uint8_t KQ[kStages][2 * 128 * 128];   // [stage][feature half][key rows, query rows][64 BF16], 128-byte swizzle
+    uint8_t M[2][2][kC * 128];      // pieces of M and A, rows of 64 F16, 128-byte swizzle
+    uint8_t A[2][2][kC * 128];
     uint16_t V[2][kC * kD];
-    float L[kC * kLS];
-    float T[32 * kTS];
-    float a[kC];
-    float b[4][kC], G[4][kC], tail[4][kC];   // of chunk c in [c % 4]: strengths, G_i, D_Ci
-    unsigned long long full[2], empty[2], ready[2];
+    alignas(16) float L[kC * kLS];
+    alignas(16) float T[32 * kTS];
+    alignas(16) float next[kC];     // the gates of tokens 1 .. 63, then 1
+    alignas(16) float b[4][kC];     // of chunk c in [c % 4]: strengths, G_i, D_Ci
+    alignas(16) float G[4][kC];
+    alignas(16) float tail[4][kC];
+    alignas(16) float m_unit[4][kC];   // and the powers of two of the rows of M and of A
+    alignas(16) float a_unit[4][kC];
+    float top[2][2][kD];            // [X, U][half] largest magnitude of a state row's values
+    float first;                    // the gate of token 0
+    unsigned long long full[kStages], empty[kStages];   // keys and queries
+    unsigned long long vfull[2], vempty[2];             // values
+    unsigned long long ready[2], used[2];               // M, A and the gates' products; M and A have been read
     unsigned long long bar_kk;
     unsigned long long have_s, have_x, have_us, have_u, read_o;   // to the issuing warp: operands written, outputs read
     unsigned long long done_k, done_u, done_s, done_o;            // from it: products done
@@ -80,7 +91,9 @@ struct PrefillShared {
     int32_t abort;
 };
 static_assert(sizeof(PrefillShared) + 1024 <= 227 * 1024, "shared memory above the per-CTA limit");
-constexpr uint32_t kStageBytes = sizeof(PrefillShared::KQ) / 2 + sizeof(PrefillShared::V) / 2;
+static_assert(offsetof(PrefillShared, M) % 1024 == 0 && offsetof(PrefillShared, A) % 1024 == 0, "swizzled tiles");
+static_assert(offsetof(PrefillShared, V) % 128 == 0 && offsetof(PrefillShared, full) % 8 == 0, "copies and barriers");
+constexpr uint32_t kKqBytes = sizeof(PrefillShared::KQ) / kStages, kVBytes = sizeof(PrefillShared::V) / 2;
 
 struct PrefillParams {
     const float *S0;                // may be null: zero
@@ -140,6 +153,7 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
 }
 
 constexpr uint32_t kBMnMajor = 1u << 16;   // instruction descriptor: B's rows are its K index
+constexpr uint32_t kIdescF16 = (1u << 4) | ((uint32_t)(kC >> 3) << 17) | ((128u >> 4) << 24);   // F16 operands, both K-major, N = 64
 
 // The high, middle and low BF16 pieces of 2N values, N words each: `put(piece, words)`.  Every piece is
 // the upper half of what the ones before it left, so the three add up exactly.
@@ -164,6 +178,54 @@ __device__ __forceinline__ void pieces3(float (&x)[2 * N], F put)
     }
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t w)
+{
+    float2 r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(w));
+    return r;
+}
+
+// The power of two that brings magnitudes up to `top` into [2^13, 2^14), and its inverse.  F16's range below that
+// is 2^-38 of the top, far under what FP32 sums keep; magnitudes under 2^-113 count as that.
+struct Unit {
+    float scale, back;
+};
+__device__ __forceinline__ Unit unit_of(float top)
+{
+    const uint32_t e = min(max(__float_as_uint(top) >> 23, 14u), 253u);
+    return Unit{__uint_as_float((267u - e) << 23), __uint_as_float((e - 13u) << 23)};
+}
+
+__device__ __forceinline__ float top_of(const float (&x)[32], float top)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
+    return top;
+}
+
+// The two F16 pieces of 32 scaled values, rounded to nearest: what is left is 2^-22 of a value
+template <class F>
+__device__ __forceinline__ void pieces2(const float (&x)[32], float scale, F put)
+{
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 y = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(scale, scale));
+        hi[i] = pack_f16x2(y.x, y.y);
+        const float2 r = __ffma2_rn(unpack_f16x2(hi[i]), make_float2(-1.f, -1.f), y);
+        lo[i] = pack_f16x2(r.x, r.y);
+    }
+    put(0, hi);
+    put(1, lo);
+}
+
 // 32 lanes x 32 columns as floats, the load complete
 __device__ __forceinline__ void tmem_read(uint32_t taddr, float (&x)[32])
 {
@@ -172,6 +234,19 @@ __device__ __forceinline__ void tmem_read(uint32_t taddr, float (&x)[32])
     tmem_ld_wait();
 #pragma unroll
     for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(w[i]);
+}
+
+// 32 values of shared memory, the same ones for every lane
+__device__ __forceinline__ void read32(const float *src, float (&x)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 v = reinterpret_cast<const float4 *>(src)[i];
+        x[4 * i] = v.x;
+        x[4 * i + 1] = v.y;
+        x[4 * i + 2] = v.z;
+        x[4 * i + 3] = v.w;
+    }
 }
 
 // this warp's tensor-memory accesses are done: one arrival for the warp
@@ -231,27 +306,46 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
     }
     put_state(S, tm, hs);
     warp_arrive(smem_u32(&s.have_s), lane);
+    // the larger of `top` here and in the thread with the other half of the columns
+    auto row_top = [&](float (&at)[2][kD], float top) {
+        at[hs][c] = top;
+        named_bar(kBarRow + (warp & 3), 64);
+        return fmaxf(top, at[hs ^ 1][c]);
+    };
 #pragma unroll 1
     for (int ch = 0; ch < t.chunks; ++ch) {
         const int st = ch & 1, k4 = ch & 3;
         const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
         float x[32];
         // X = b (v - G S k): tokens 32 hs .. 32 hs + 31
-        wait(s.full[st], par2);
+        Unit ux;
+        wait(s.vfull[st], par2);
         wait(s.ready[st], par2);
-        wait(s.done_k, par);
-        tmem_read(tm + kColDK + 32 * hs, x);
         {
+            float bv[32], G[32];
+            read32(s.b[k4] + 32 * hs, bv);
+            read32(s.G[k4] + 32 * hs, G);
             const uint16_t *v = s.V[st] + 32 * hs * kD + c;
-            const float *b = s.b[k4] + 32 * hs, *G = s.G[k4] + 32 * hs;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                x[j] = b[j] * (__uint_as_float((uint32_t)v[j * kD] << 16) - G[j] * x[j]);
+            for (int j = 0; j < 32; ++j) {
+                G[j] *= -bv[j];
+                bv[j] *= __uint_as_float((uint32_t)v[j * kD] << 16);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.vempty[st]));
+            const int left = t.n - ch * kC - 32 * hs;
+            if (left < 32) {
+                // rows behind the request's end are another request's, or none: whatever they hold counts for nothing
+#pragma unroll
+                for (int j = 0; j < 32; ++j) bv[j] = j < left ? bv[j] : 0.f;
+            }
+            wait(s.done_k, par);
+            tmem_read(tm + kColDK + 32 * hs, x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = fmaf(G[j], x[j], bv[j]);
         }
-        // (the low piece goes where this thread has read S k: the other half's columns may not be read yet)
-        pieces3<16>(x, [&](int piece, const uint32_t (&w)[16]) {
-            tmem_st_x16(piece < 2 ? tm + kColX + 32 * piece + 16 * hs : tm + kColDK + 32 * hs, w);
-        });
+        ux = unit_of(row_top(s.top[0], top_of(x, 0.f)));
+        pieces2(x, ux.scale, [&](int piece, const uint32_t (&w)[16]) { tmem_st_x16(tm + kColX + 32 * piece + 16 * hs, w); });
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_x), lane);
 
@@ -260,14 +354,18 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
         tmem_read(tm + kColU + 32 * hs, x);
         {
             float y[32];
-            const float *tail = s.tail[k4] + 32 * hs;
+            read32(s.m_unit[k4] + 32 * hs, y);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] = x[j] * tail[j];
+            for (int j = 0; j < 32; ++j) x[j] *= ux.back * y[j];
+            read32(s.tail[k4] + 32 * hs, y);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] *= x[j];
             pieces3<16>(y, [&](int piece, const uint32_t (&w)[16]) { tmem_st_x16(tm + kColS + 32 * piece + 16 * hs, w); });
         }
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_us), lane);
-        pieces3<16>(x, [&](int piece, const uint32_t (&w)[16]) { tmem_st_x16(tm + kColS + 96 + 32 * piece + 16 * hs, w); });
+        const Unit uu = unit_of(row_top(s.top[1], top_of(x, 0.f)));
+        pieces2(x, uu.scale, [&](int piece, const uint32_t (&w)[16]) { tmem_st_x16(tm + kColS + 96 + 32 * piece + 16 * hs, w); });
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_u), lane);
 
@@ -286,17 +384,26 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
             warp_arrive(smem_u32(&s.have_s), lane);
         }
         // o = G S q + U A
-        float y[32];
-        tmem_read(tm + kColDQ + 32 * hs, x);
-        tmem_read(tm + kColU + 32 * hs, y);
-        warp_arrive(smem_u32(&s.read_o), lane);
+        {
+            float y[32], G[32];
+            tmem_read(tm + kColDQ + 32 * hs, x);
+            tmem_read(tm + kColU + 32 * hs, y);
+            warp_arrive(smem_u32(&s.read_o), lane);
+            read32(s.G[k4] + 32 * hs, G);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] *= G[j];
+            read32(s.a_unit[k4] + 32 * hs, G);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = fmaf(uu.back * G[j], y[j], x[j]);
+        }
         const int left = t.n - ch * kC - 32 * hs;
         float *dst = p.o + ((size_t)(t.row0 + ch * kC + 32 * hs) * p.H + h) * kD + c;
         const size_t step = (size_t)p.H * kD;
-        const float *G = s.G[k4] + 32 * hs;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < left) dst[j * step] = fmaf(G[j], x[j], y[j]);
+        for (int j = 0; j < 32; ++j) {
+            if (j < left) *dst = x[j];
+            dst += step;
+        }
     }
     if (!*(volatile int32_t *)&s.abort) {
 #pragma unroll
@@ -309,46 +416,68 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
 // chunk warps
 // ---------------------------------------------------------------------------
 
-// C (32 x 32) = -/+ X Y of three 32 x 32 blocks in shared memory: two rows and four columns to a thread
-template <bool kNeg>
-__device__ __forceinline__ void block_product(const float *X, int xs, const float *Y, int ys, float *Z, int zs, int t)
+// Z = -/+ X Y of kN x kN blocks in shared memory, kR rows and four columns to a thread: rows kR * rt ..,
+// columns 4 * ct ..
+template <int kN, int kR, bool kNeg>
+__device__ __forceinline__ void block_product(const float *X, int xs, const float *Y, int ys, float *Z, int zs, int rt, int ct)
 {
-    const int r0 = 2 * (t >> 3), c0 = 4 * (t & 7);
-    float acc[2][4] = {};
+    const int r0 = kR * rt, c0 = 4 * ct;
+    float2 acc[kR][2] = {};
 #pragma unroll
-    for (int l = 0; l < 32; l += 4) {
-        float xr[2][4];
+    for (int l = 0; l < kN; l += 4) {
+        float4 xr[kR], yr[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 v = *reinterpret_cast<const float4 *>(X + (r0 + i) * xs + l);
-            xr[i][0] = v.x;
-            xr[i][1] = v.y;
-            xr[i][2] = v.z;
-            xr[i][3] = v.w;
-        }
+        for (int i = 0; i < kR; ++i) xr[i] = *reinterpret_cast<const float4 *>(X + (r0 + i) * xs + l);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 v = *reinterpret_cast<const float4 *>(Y + (l + e) * ys + c0);
+        for (int e = 0; e < 4; ++e) yr[e] = *reinterpret_cast<const float4 *>(Y + (l + e) * ys + c0);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                acc[i][0] = fmaf(xr[i][e], v.x, acc[i][0]);
-                acc[i][1] = fmaf(xr[i][e], v.y, acc[i][1]);
-                acc[i][2] = fmaf(xr[i][e], v.z, acc[i][2]);
-                acc[i][3] = fmaf(xr[i][e], v.w, acc[i][3]);
+        for (int i = 0; i < kR; ++i) {
+            const float xe[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = make_float2(xe[e], xe[e]);
+                acc[i][0] = __ffma2_rn(f, make_float2(yr[e].x, yr[e].y), acc[i][0]);
+                acc[i][1] = __ffma2_rn(f, make_float2(yr[e].z, yr[e].w), acc[i][1]);
             }
         }
     }
     const float f = kNeg ? -1.f : 1.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < kR; ++i)
         *reinterpret_cast<float4 *>(Z + (r0 + i) * zs + c0) =
-            make_float4(f * acc[i][0], f * acc[i][1], f * acc[i][2], f * acc[i][3]);
+            make_float4(f * acc[i][0].x, f * acc[i][0].y, f * acc[i][1].x, f * acc[i][1].y);
 }
 
-// words of three pieces of 32 values into row `row` of three swizzled tiles, from column `col0` on (a multiple of 32)
-__device__ __forceinline__ void put_row(uint8_t (&tile)[3][kC * 128], int row, int col0, float (&x)[32])
+// A lower-triangular block with ones on its diagonal, inverted in place by one warp, a column to a lane
+// (both halves of the warp the same): x_i = [i = j] - sum over l < i of L_il x_l
+__device__ __forceinline__ void invert16(float *B, int lane)
 {
-    pieces3<16>(x, [&](int piece, const uint32_t (&w)[16]) {
+    const int col = lane & 15;
+    float x[16];
+#pragma unroll
+    for (int row = 0; row < 16; ++row) {
+        float acc[4] = {row == col ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int l = 0; l < row; l += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(B + row * kLS + l);
+            acc[0] = fmaf(-v.x, x[l], acc[0]);
+            if (l + 1 < row) acc[1] = fmaf(-v.y, x[l + 1], acc[1]);
+            if (l + 2 < row) acc[2] = fmaf(-v.z, x[l + 2], acc[2]);
+            if (l + 3 < row) acc[3] = fmaf(-v.w, x[l + 3], acc[3]);
+        }
+        x[row] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    }
+    __syncwarp();
+    if (lane < 16) {
+#pragma unroll
+        for (int row = 0; row < 16; ++row) B[row * kLS + col] = x[row];
+    }
+}
+
+// the two pieces of 32 values into row `row` of swizzled tiles, from column `col0` on (a multiple of 32)
+__device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, int col0, const float (&x)[32], float scale)
+{
+    pieces2(x, scale, [&](int piece, const uint32_t (&w)[16]) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             *reinterpret_cast<uint4 *>(tile[piece] + row * 128 + (((col0 / 8 + q) ^ (row & 7)) << 4)) =
@@ -367,95 +496,124 @@ __device__ __forceinline__ void chunk_warps(const PrefillParams &p, PrefillShare
         if (row >= t.n) return query ? 0.f : 1.f;
         return (query ? p.beta : p.alpha)[(size_t)(t.row0 + row) * p.H + h];
     };
-    float ab = gate(0);
-#pragma unroll 1
-    for (int ch = 0; ch < t.chunks; ++ch) {
-        const int st = ch & 1, k4 = ch & 3;
-        const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
-        mbar_wait(smem_u32(&s.full[st]), par2, p.timeout_ns, p.status, &s.abort);
-        const int valid = min(t.n - ch * kC, kC);
+    // warp 3: k.k and q.k of a chunk whose rows have arrived.  Rows behind the request's end are another
+    // request's, or none: whatever they hold becomes zero.
+    auto products = [&](int ch) {
+        const int st = ch % kStages, valid = min(t.n - ch * kC, kC);
         if (valid < kC) {
-            // rows behind the request's end are another request's, or none: whatever they hold becomes zero
-            for (int e = tid; e < (kC - valid) * 16; e += kChunkThreads) {
+            for (int e = lane; e < (kC - valid) * 16; e += 32) {
                 const int row = valid + (e >> 4), q = e & 15;
                 const uint4 z = make_uint4(0, 0, 0, 0);
                 uint8_t *half = s.KQ[st] + (q >> 3) * (128 * 128);
                 *reinterpret_cast<uint4 *>(half + row * 128 + (q & 7) * 16) = z;
                 *reinterpret_cast<uint4 *>(half + (kC + row) * 128 + (q & 7) * 16) = z;
-                *reinterpret_cast<uint4 *>(s.V[st] + row * kD + q * 8) = z;
             }
             fence_async_shared();
+            __syncwarp();
         }
+        tc_fence_after();
+        const uint32_t kq = smem_u32(s.KQ[st]);
+        const uint64_t x0 = smem_desc_sw128(kq), x1 = smem_desc_sw128(kq + 128 * 128);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            const uint64_t d = (ks < 4 ? x0 : x1) + (uint64_t)((ks & 3) * 2);
+            tc_mma_ss_elect(s.tmem + kColKK, d, d, idesc_bf16_f32(128, kC), ks ? 1u : 0u);
+        }
+        tc_commit_elect(smem_u32(&s.bar_kk));
+    };
+    auto arrived = [&](int ch) { mbar_wait(smem_u32(&s.full[ch % kStages]), (ch / kStages) & 1, p.timeout_ns, p.status, &s.abort); };
+    float ab = gate(0);
+    if (warp == 3) {
+        arrived(0);
+        __syncwarp();
+        products(0);
+    }
+#pragma unroll 1
+    for (int ch = 0; ch < t.chunks; ++ch) {
+        const int st = ch & 1, k4 = ch & 3;
         if (query)
             s.b[k4][i] = ab;
-        else
-            s.a[i] = ab;
-        tc_fence_before();
+        else if (i > 0)
+            s.next[i - 1] = ab;
+        else {
+            s.first = ab;
+            s.next[kC - 1] = 1.f;
+        }
         named_bar(kBarChunk, kChunkThreads);
         if (ch + 1 < t.chunks) ab = gate(ch + 1);
-        if (warp == 0) {
-            tc_fence_after();
-            const uint32_t kq = smem_u32(s.KQ[st]);
-            const uint64_t x0 = smem_desc_sw128(kq), x1 = smem_desc_sw128(kq + 128 * 128);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                const uint64_t d = (ks < 4 ? x0 : x1) + (uint64_t)((ks & 3) * 2);
-                tc_mma_ss_elect(s.tmem + kColKK, d, d, idesc_bf16_f32(128, kC), ks ? 1u : 0u);
-            }
-            tc_commit_elect(smem_u32(&s.bar_kk));
-        }
-        mbar_wait(smem_u32(&s.bar_kk), par, p.timeout_ns, p.status, &s.abort);
+        mbar_wait(smem_u32(&s.bar_kk), ch & 1, p.timeout_ns, p.status, &s.abort);
         tc_fence_after();
-        const float bi = s.b[k4][i];
-        float d = 1.f;                            // D_ij, from j = i down
+        {
+            float d = query ? 1.f : s.b[k4][i];       // D_ij (times b_i), from j = i down
+            const int last = query ? i : i - 1;       // the row's last entry
+            float x[2][32], top = 0.f;
 #pragma unroll
-        for (int half = 1; half >= 0; --half) {
-            float x[32];
-            tmem_read(tm + kColKK + 32 * half, x);
+            for (int half = 1; half >= 0; --half) {
+                tmem_read(tm + kColKK + 32 * half, x[half]);
 #pragma unroll
-            for (int jj = 31; jj >= 0; --jj) {
-                const int j = 32 * half + jj;
-                if (j + 1 <= kC - 1 && j < i) d *= s.a[j < kC - 1 ? j + 1 : j];
-                x[jj] = (query ? j <= i : j < i) ? x[jj] * (query ? d : d * bi) : 0.f;
-                if (tid == kC - 1) s.tail[k4][j] = d;
+                for (int g = 7; g >= 0; --g) {
+                    const float4 nx = *reinterpret_cast<const float4 *>(s.next + 32 * half + 4 * g);
+                    const float f[4] = {nx.x, nx.y, nx.z, nx.w};
+#pragma unroll
+                    for (int e = 3; e >= 0; --e) {
+                        const int j = 32 * half + 4 * g + e;
+                        d *= j < i ? f[e] : 1.f;
+                        x[half][4 * g + e] = j <= last ? x[half][4 * g + e] * d : 0.f;
+                    }
+                }
+                top = top_of(x[half], top);
             }
+            if (ch >= 2) mbar_wait(smem_u32(&s.used[st]), ((ch >> 1) & 1) ^ 1, p.timeout_ns, p.status, &s.abort);
             if (query) {
-                put_row(s.A[st], i, 32 * half, x);
+                const Unit u = unit_of(top);
+                s.a_unit[k4][i] = u.back;
+                put_row(s.A[st], i, 0, x[0], u.scale);
+                put_row(s.A[st], i, 32, x[1], u.scale);
             } else {
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    *reinterpret_cast<float4 *>(s.L + i * kLS + 32 * half + 4 * q) =
-                        make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                for (int q = 0; q < 16; ++q)
+                    *reinterpret_cast<float4 *>(s.L + i * kLS + 4 * q) =
+                        make_float4(x[q >> 3][4 * (q & 7)], x[q >> 3][4 * (q & 7) + 1], x[q >> 3][4 * (q & 7) + 2], x[q >> 3][4 * (q & 7) + 3]);
             }
         }
-        if (!query) s.G[k4][i] = d * s.a[0];
-        named_bar(kBarChunk, kChunkThreads);
-        // the inverse of the two diagonal blocks, a column to a thread: x_i = [i = j] - sum over l < i of L_il x_l
-        if (!query) {
-            float *B = s.L + warp * 32 * (kLS + 1);
-            float x[32];
+        if (warp == 0) {
+            // G_i and D_Ci by scans of the gates from both ends, two tokens to a lane
+            const float a1 = s.next[2 * lane], a0 = lane ? s.next[2 * lane - 1] : s.first;
+            float up = a0 * a1, down = up;
 #pragma unroll
-            for (int row = 0; row < 32; ++row) {
-                float acc[4] = {row == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int l = 0; l < row; l += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(B + row * kLS + l);
-                    acc[0] = fmaf(-v.x, x[l], acc[0]);
-                    if (l + 1 < row) acc[1] = fmaf(-v.y, x[l + 1], acc[1]);
-                    if (l + 2 < row) acc[2] = fmaf(-v.z, x[l + 2], acc[2]);
-                    if (l + 3 < row) acc[3] = fmaf(-v.w, x[l + 3], acc[3]);
-                }
-                x[row] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            for (int o = 1; o < 32; o <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, up, o), v = __shfl_down_sync(0xffffffffu, down, o);
+                if (lane >= o) up *= u;
+                if (lane + o < 32) down *= v;
             }
-            __syncwarp();
-#pragma unroll
-            for (int row = 0; row < 32; ++row) B[row * kLS + lane] = x[row];
+            float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 0) before = 1.f;
+            if (lane == 31) after = 1.f;
+            *reinterpret_cast<float2 *>(&s.G[k4][2 * lane]) = make_float2(before * a0, up);
+            *reinterpret_cast<float2 *>(&s.tail[k4][2 * lane]) = make_float2(a1 * after, after);
+        }
+        tc_fence_before();
+        named_bar(kBarChunk, kChunkThreads);
+        // the next chunk's products as soon as its rows are there
+        bool issued = false;
+        if (warp == 3 && ch + 1 < t.chunks) {
+            issued = __all_sync(0xffffffffu, mbar_test_wait(smem_u32(&s.full[(ch + 1) % kStages]), ((ch + 1) / kStages) & 1));
+            if (issued) products(ch + 1);
+        }
+        // M by blocks of 16, 32 and 64: M21 = -M22 (L21 M11)
+        invert16(s.L + warp * 16 * (kLS + 1), lane);
+        named_bar(kBarChunk, kChunkThreads);
+        {
+            float *B = s.L + (warp >> 1) * 32 * (kLS + 1), *T = s.T + (warp >> 1) * 16 * kTS16;
+            const int tt = tid & 63;
+            block_product<16, 1, false>(B + 16 * kLS, kLS, B, kLS, T, kTS16, tt >> 2, tt & 3);
+            named_bar(kBarChunk, kChunkThreads);
+            block_product<16, 1, true>(B + 16 * (kLS + 1), kLS, T, kTS16, B + 16 * kLS, kLS, tt >> 2, tt & 3);
         }
         named_bar(kBarChunk, kChunkThreads);
-        // and of the block below them: M21 = -M22 (L21 M11)
-        block_product<false>(s.L + 32 * kLS, kLS, s.L, kLS, s.T, kTS, tid);
+        block_product<32, 2, false>(s.L + 32 * kLS, kLS, s.L, kLS, s.T, kTS, tid >> 3, tid & 7);
         named_bar(kBarChunk, kChunkThreads);
-        block_product<true>(s.L + 32 * (kLS + 1), kLS, s.T, kTS, s.L + 32 * kLS, kLS, tid);
+        block_product<32, 2, true>(s.L + 32 * (kLS + 1), kLS, s.T, kTS, s.L + 32 * kLS, kLS, tid >> 3, tid & 7);
         named_bar(kBarChunk, kChunkThreads);
         {
             const int row = tid >> 1, c0 = (tid & 1) * 32;
@@ -468,12 +626,21 @@ __device__ __forceinline__ void chunk_warps(const PrefillParams &p, PrefillShare
                 x[4 * q + 2] = v.z;
                 x[4 * q + 3] = v.w;
             }
-            put_row(s.M[st], row, c0, x);
+            float top = top_of(x, 0.f);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            const Unit u = unit_of(top);
+            if (c0 == 0) s.m_unit[k4][row] = u.back;
+            put_row(s.M[st], row, c0, x, u.scale);
         }
         fence_async_shared();
         warp_arrive(smem_u32(&s.ready[st]), lane);
+        if (warp == 3 && ch + 1 < t.chunks && !issued) {
+            arrived(ch + 1);
+            __syncwarp();
+            products(ch + 1);
+        }
     }
-    if (warp == 0) {
+    if (warp == 3) {
         tc_commit_elect(smem_u32(&s.last_kk));
         drain(smem_u32(&s.last_kk), 0, p.timeout_ns);
     }
@@ -483,17 +650,17 @@ __device__ __forceinline__ void chunk_warps(const PrefillParams &p, PrefillShare
 // the issuing warps
 // ---------------------------------------------------------------------------
 
-// The six pairs of pieces of two FP32 operands, K = 64 tokens: piece columns a[piece] + step, tiles of `B`
+// Two FP32 operands of two F16 pieces each, K = 64 tokens: high times high, high times low, low times high.
+// a(piece, step): columns of the left one; B: the right one's tiles.
 template <class F>
 __device__ __forceinline__ void issue_pairs(uint32_t d, F a, const uint8_t (*B)[kC * 128])
 {
-    constexpr int pa[6] = {0, 0, 1, 1, 0, 2}, pb[6] = {0, 1, 0, 1, 2, 0};
 #pragma unroll
-    for (int q = 0; q < 6; ++q) {
-        const uint64_t b = smem_desc_sw128(smem_u32(B[pb[q]]));
+    for (int q = 0; q < 3; ++q) {
+        const uint64_t b = smem_desc_sw128(smem_u32(B[q == 1]));
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-            tc_mma_ts_elect(d, a(pa[q], ks), b + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC), (q | ks) ? 1u : 0u);
+            tc_mma_ts_elect(d, a(q == 2, ks), b + (uint64_t)(ks * 2), kIdescF16, (q | ks) ? 1u : 0u);
     }
 }
 
@@ -508,10 +675,10 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
     };
 #pragma unroll 1
     for (int ch = 0; ch < t.chunks; ++ch) {
-        const int st = ch & 1;
+        const int st = ch & 1, sk = ch % kStages;
         const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
-        const uint32_t kq = smem_u32(s.KQ[st]);
-        if (!wait(s.full[st], par2) || !wait(s.ready[st], par2) || !wait(s.have_s, par)) break;
+        const uint32_t kq = smem_u32(s.KQ[sk]);
+        if (!wait(s.full[sk], (ch / kStages) & 1) || !wait(s.ready[st], par2) || !wait(s.have_s, par)) break;
         // S k (rows 0..63 of the tile), then S q (rows 64..127) once the last chunk's outputs are read
         auto products = [&](uint32_t d, uint32_t row0) {
             const uint64_t b0 = smem_desc_sw128(kq + row0 * 128), b1 = smem_desc_sw128(kq + 128 * 128 + row0 * 128);
@@ -528,7 +695,7 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
         products(tm + kColDQ, kC);
         if (!wait(s.have_x, par)) break;
         issue_pairs(tm + kColU, [&](int piece, int ks) {
-            return piece < 2 ? tm + kColX + 32 * piece + 8 * ks : tm + kColDK + 8 * (ks & 2) + 8 * ks;
+            return tm + kColX + 32 * piece + 8 * ks;
         }, s.M[st]);
         tc_commit_elect(smem_u32(&s.done_u));
         if (!wait(s.have_us, par)) break;
@@ -540,10 +707,11 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
                                 smem_desc_mn_sw128(kq + ks * 16 * 128, 128 * 128), idesc_bf16_f32(128, kD) | kBMnMajor,
                                 (piece | ks) ? 1u : 0u);
         tc_commit_elect(smem_u32(&s.done_s));
+        tc_commit_elect(smem_u32(&s.empty[sk]));
         if (!wait(s.have_u, par)) break;
         issue_pairs(tm + kColU, [&](int piece, int ks) { return tm + kColS + 96 + 32 * piece + 8 * ks; }, s.A[st]);
         tc_commit_elect(smem_u32(&s.done_o));
-        tc_commit_elect(smem_u32(&s.empty[st]));
+        tc_commit_elect(smem_u32(&s.used[st]));
     }
     tc_commit_elect(smem_u32(&s.last));
     drain(smem_u32(&s.last), 0, p.timeout_ns);   // no product in flight when tensor memory is given back
@@ -553,24 +721,29 @@ __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShare
                                             const CUtensorMap &kmap, const CUtensorMap &vmap)
 {
     const int hk = h / p.group;
-    int issued = 0;
+    const bool withheld = (p.debug_flags & 1) && blockIdx.x == 0 && blockIdx.y == 0;
+    int kq_issued = 0, v_issued = 0;
     for (int ch = 0; ch < t.chunks; ++ch) {
-        const int st = ch & 1;
-        const uint32_t bar = smem_u32(&s.full[st]), kq = smem_u32(s.KQ[st]);
-        if (ch >= 2 && !mbar_wait(smem_u32(&s.empty[st]), ((ch >> 1) & 1) ^ 1, p.timeout_ns, p.status, &s.abort)) break;
-        mbar_expect_tx(bar, kStageBytes);
-        if ((p.debug_flags & 1) && blockIdx.x == 0 && blockIdx.y == 0) break;
-        const int row = t.row0 + ch * kC;
+        const int sk = ch % kStages, sv = ch & 1, row = t.row0 + ch * kC;
+        const uint32_t kq_bar = smem_u32(&s.full[sk]), v_bar = smem_u32(&s.vfull[sv]), kq = smem_u32(s.KQ[sk]);
+        if (ch >= kStages && !mbar_wait(smem_u32(&s.empty[sk]), ((ch / kStages) & 1) ^ 1, p.timeout_ns, p.status, &s.abort)) break;
+        mbar_expect_tx(kq_bar, kKqBytes);
+        if (withheld) break;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            tma_load_2d(kq + half * 128 * 128, &kmap, hk * kD + 64 * half, row, bar);
-            tma_load_2d(kq + half * 128 * 128 + kC * 128, &qmap, hk * kD + 64 * half, row, bar);
+            tma_load_2d(kq + half * 128 * 128, &kmap, hk * kD + 64 * half, row, kq_bar);
+            tma_load_2d(kq + half * 128 * 128 + kC * 128, &qmap, hk * kD + 64 * half, row, kq_bar);
         }
-        tma_load_2d(smem_u32(s.V[st]), &vmap, h * kD, row, bar);
-        issued = ch + 1;
+        kq_issued = ch + 1;
+        if (ch >= 2 && !mbar_wait(smem_u32(&s.vempty[sv]), ((ch >> 1) & 1) ^ 1, p.timeout_ns, p.status, &s.abort)) break;
+        mbar_expect_tx(v_bar, kVBytes);
+        tma_load_2d(smem_u32(s.V[sv]), &vmap, h * kD, row, v_bar);
+        v_issued = ch + 1;
     }
     // no copy into shared memory in flight at the end
-    for (int ch = max(issued - 2, 0); ch < issued; ++ch) drain(smem_u32(&s.full[ch & 1]), (ch >> 1) & 1, p.timeout_ns);
+    for (int ch = max(kq_issued - kStages, 0); ch < kq_issued; ++ch)
+        drain(smem_u32(&s.full[ch % kStages]), (ch / kStages) & 1, p.timeout_ns);
+    for (int ch = max(v_issued - 2, 0); ch < v_issued; ++ch) drain(smem_u32(&s.vfull[ch & 1]), (ch >> 1) & 1, p.timeout_ns);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -597,10 +770,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (tid == 0) {
-        for (int st = 0; st < 2; ++st) {
+        for (int st = 0; st < kStages; ++st) {
             mbar_init(smem_u32(&s.full[st]), 1);
             mbar_init(smem_u32(&s.empty[st]), 1);
+        }
+        for (int st = 0; st < 2; ++st) {
+            mbar_init(smem_u32(&s.vfull[st]), 1);
+            mbar_init(smem_u32(&s.vempty[st]), kStateWarps);
             mbar_init(smem_u32(&s.ready[st]), kChunkThreads / 32);
+            mbar_init(smem_u32(&s.used[st]), 1);
         }
         for (unsigned long long *b : {&s.bar_kk, &s.done_k, &s.done_u, &s.done_s, &s.done_o, &s.last, &s.last_kk}) mbar_init(smem_u32(b), 1);
         for (unsigned long long *b : {&s.have_s, &s.have_x, &s.have_us, &s.have_u, &s.read_o}) mbar_init(smem_u32(b), kStateWarps);
