@@ -21,19 +21,21 @@
 // far.  Products of two FP32 sides (X M^T, U A^T) take both as two F16 pieces (2^-22) under a power of two
 // for each row, and of their four pairs all but the smallest.  All accumulation is FP32.
 //
-// Sixteen warps:
-//  * state warps (0..7; two threads to a state row, each with half of the
+// Twenty-eight warps (many, with few columns each: a chunk runs through every role's code once, and
+// the time goes into fetching that code, which warps in step share):
+//  * state warps (0..15; four threads to a state row, each with a quarter of the
 //    columns; S itself stays in their registers) turn accumulators into operands,
-//  * chunk warps (8..11) make M and A of the next chunk: k.k and q.k on the
-//    tensor cores, then the inverse, of four 16 x 16 blocks by columns and of the
+//  * chunk warps (16..23; two threads to a row of k.k or q.k) make M and A of the next chunk: k.k and q.k on
+//    the tensor cores, then the inverse, of four 16 x 16 blocks by columns and of the
 //    blocks below them from those,
-//  * warp 12 issues the state warps' products, warp 13 the copies by TMA.
+//  * warp 24 issues the state warps' products, warp 25 the copies by TMA.
 // Every wait is bounded: a wait that runs out sets s.abort, which ends every
 // other wait at once, so all roles run to their ends; the state is then left
 // unwritten.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstddef>
 
@@ -45,14 +47,16 @@ namespace {
 
 constexpr int kD = 128;             // head dimension
 constexpr int kC = 64;              // tokens of a chunk
-constexpr int kThreads = 512;
-constexpr int kStateWarps = 8;
-constexpr int kChunkThreads = 128;
-constexpr int kRegsLaunch = 128, kRegsState = 176, kRegsChunk = 104, kRegsIssue = 56;
-static_assert(256 * kRegsState + 128 * kRegsChunk + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register shares");
+constexpr int kStateWarps = 16, kChunkWarps = 8;
+constexpr int kChunkThreads = 32 * kChunkWarps;
+constexpr int kThreads = 32 * (kStateWarps + kChunkWarps + 4);
+constexpr int kChunk0 = 32 * kStateWarps, kIssue0 = kChunk0 + kChunkThreads;   // the roles' first threads
+constexpr int kRegsLaunch = 72, kRegsState = 80, kRegsIssue = 40;             // (chunk warps keep the launch's)
+static_assert(kChunk0 * kRegsState + kChunkThreads * kRegsLaunch + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register shares");
 
-// tensor memory columns
-constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; later three of U for S' and two for A, 32 each
+// tensor memory columns: all 512 are one CTA's, from column 0 on
+constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; later three of U for S', 32 each,
+constexpr uint32_t kColUA = 128;    // and, on the last of them, two of U for A
 constexpr uint32_t kColDQ = 192;    // S q
 constexpr uint32_t kColDK = 256;    // S k; then, with the next 64 columns, U K
 constexpr uint32_t kColX = 320;     // X's two pieces
@@ -62,7 +66,8 @@ constexpr uint32_t kColKK = 448;    // k.k (lanes 0..63) and q.k (lanes 64..127)
 constexpr int kLS = 68;             // FP32 row stride of L and M (16-byte rows, 4 banks apart)
 constexpr int kTS = 36, kTS16 = 20; // and of products in between, of 32 and 16 columns
 constexpr int kBarChunk = 1;        // named barrier of the chunk warps
-constexpr int kBarRow = 2;          // and of the two warps of 32 state rows (2 .. 5)
+constexpr int kBarRow = 2;          // of the four warps of 32 state rows (2 .. 5)
+constexpr int kBarKey = 6;          // and of the four chunk warps with key rows
 constexpr int kStages = 3;          // of keys and queries (their chunk is prepared while two others are in use)
 
 struct PrefillShared {
@@ -73,13 +78,15 @@ struct PrefillShared {
     alignas(16) float L[kC * kLS];
     alignas(16) float T[32 * kTS];
     alignas(16) float next[kC];     // the gates of tokens 1 .. 63, then 1
-    alignas(16) float b[4][kC];     // of chunk c in [c % 4]: strengths, G_i, D_Ci
+    alignas(16) float b[4][kC];     // of chunk c in [c % 4]: strengths, -b_i G_i, G_i, D_Ci
+    alignas(16) float bG[4][kC];
     alignas(16) float G[4][kC];
     alignas(16) float tail[4][kC];
     alignas(16) float m_unit[4][kC];   // and the powers of two of the rows of M and of A
     alignas(16) float a_unit[4][kC];
-    float top[2][2][kD];            // [X, U][half] largest magnitude of a state row's values
-    float first;                    // the gate of token 0
+    float top[2][kStateWarps / 4][kD];   // [X, U][part] largest magnitude of a state row's values
+    float a_top[2][kC];             // and of a row of A, by halves
+    float gates[2];                 // products of the gates of tokens 0 .. 31 and 32 .. 63
     unsigned long long full[kStages], empty[kStages];   // keys and queries
     unsigned long long vfull[2], vempty[2];             // values
     unsigned long long ready[2], used[2];               // M, A and the gates' products; M and A have been read
@@ -101,7 +108,7 @@ struct PrefillParams {
     const float *alpha, *beta;
     const int32_t *off;
     int32_t H, group, n_rows;
-    uint64_t timeout_ns;
+    uint32_t polls;                 // of a wait, before it gives up
     int32_t *status;
     int32_t debug_flags;            // bit 0: CTA (0, 0) announces its first copies and leaves them out (test hook)
 };
@@ -127,16 +134,21 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
         : "memory");
 }
 
-// D[tmem] (+)= A[smem] * B[smem], one elected lane of a converged warp (a product issued from a
-// diverged thread takes 124 cycles to issue on GB300, an elected one none beyond its own time)
-__device__ __forceinline__ void tc_mma_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                uint32_t accumulate)
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
 
 // BF16 operand whose rows (of 64 features, 128-byte swizzle) are its K index: 8-row groups 1024 bytes
@@ -203,20 +215,22 @@ __device__ __forceinline__ Unit unit_of(float top)
     return Unit{__uint_as_float((267u - e) << 23), __uint_as_float((e - 13u) << 23)};
 }
 
-__device__ __forceinline__ float top_of(const float (&x)[32], float top)
+template <int N>
+__device__ __forceinline__ float top_of(const float (&x)[N])
 {
+    float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
+    for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(x[i]));
     return top;
 }
 
-// The two F16 pieces of 32 scaled values, rounded to nearest: what is left is 2^-22 of a value
-template <class F>
-__device__ __forceinline__ void pieces2(const float (&x)[32], float scale, F put)
+// The two F16 pieces of scaled values, rounded to nearest: what is left is 2^-22 of a value
+template <int N, class F>
+__device__ __forceinline__ void pieces2(const float (&x)[N], float scale, F put)
 {
-    uint32_t hi[16], lo[16];
+    uint32_t hi[N / 2], lo[N / 2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < N / 2; ++i) {
         const float2 y = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(scale, scale));
         hi[i] = pack_f16x2(y.x, y.y);
         const float2 r = __ffma2_rn(unpack_f16x2(hi[i]), make_float2(-1.f, -1.f), y);
@@ -226,26 +240,81 @@ __device__ __forceinline__ void pieces2(const float (&x)[32], float scale, F put
     put(1, lo);
 }
 
-// 32 lanes x 32 columns as floats, the load complete
-__device__ __forceinline__ void tmem_read(uint32_t taddr, float (&x)[32])
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8])
 {
-    uint32_t w[32];
-    tmem_ld_x32(taddr, w);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(w[i]);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
-// 32 values of shared memory, the same ones for every lane
-__device__ __forceinline__ void read32(const float *src, float (&x)[32])
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N])
+{
+    if constexpr (N == 8)
+        tmem_st_x8(taddr, r);
+    else
+        tmem_st_x16(taddr, r);
+}
+
+// 32 lanes x N columns as floats (complete after tmem_ld_wait)
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&x)[N])
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < N; i += 16)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+            "%15}, [%16];"
+            : "=f"(x[i]), "=f"(x[i + 1]), "=f"(x[i + 2]), "=f"(x[i + 3]), "=f"(x[i + 4]), "=f"(x[i + 5]), "=f"(x[i + 6]),
+              "=f"(x[i + 7]), "=f"(x[i + 8]), "=f"(x[i + 9]), "=f"(x[i + 10]), "=f"(x[i + 11]), "=f"(x[i + 12]),
+              "=f"(x[i + 13]), "=f"(x[i + 14]), "=f"(x[i + 15])
+            : "r"(taddr + i)
+            : "memory");
+}
+
+// N values of shared memory, the same ones for every lane
+template <int N>
+__device__ __forceinline__ void read_n(const float *src, float (&x)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
         const float4 v = reinterpret_cast<const float4 *>(src)[i];
         x[4 * i] = v.x;
         x[4 * i + 1] = v.y;
         x[4 * i + 2] = v.z;
         x[4 * i + 3] = v.w;
+    }
+}
+
+// x *= y; x *= f; z += x y, two at a time
+template <int N>
+__device__ __forceinline__ void mul_n(float (&x)[N], const float (&y)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 r = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]));
+        x[i] = r.x;
+        x[i + 1] = r.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void scale_n(float (&x)[N], float f)
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 r = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(f, f));
+        x[i] = r.x;
+        x[i + 1] = r.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void fma_n(const float (&x)[N], const float (&y)[N], float (&z)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 r = __ffma2_rn(make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]), make_float2(z[i], z[i + 1]));
+        z[i] = r.x;
+        z[i + 1] = r.y;
     }
 }
 
@@ -257,11 +326,28 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane)
     if (lane == 0) mbar_arrive(bar);
 }
 
-// a wait that nothing ends early: for what is in flight at the end
-__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint64_t timeout_ns)
+// A bounded wait in few instructions (there are two dozen of it): polls that sleep up to kWaitSleepNs each.
+// One that runs out, or finds s.abort set, sets it; the kernel's end reports it.
+__device__ __forceinline__ bool wait_for(unsigned long long &bar, uint32_t parity, const PrefillParams &p, PrefillShared &s)
 {
-    const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < timeout_ns) {
+    const uint32_t at = smem_u32(&bar);
+    uint32_t left = p.polls;
+#pragma unroll 1
+    while (!mbar_try_wait_sleep(at, parity, kWaitSleepNs)) {
+        if (--left == 0 || *(volatile int32_t *)&s.abort) {
+            *(volatile int32_t *)&s.abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// a wait that s.abort does not end: for what is in flight at the end
+__device__ __forceinline__ void drain(unsigned long long &bar, uint32_t parity, const PrefillParams &p)
+{
+    uint32_t left = p.polls;
+#pragma unroll 1
+    while (!mbar_try_wait_sleep(smem_u32(&bar), parity, kWaitSleepNs) && --left) {
     }
 }
 
@@ -273,141 +359,149 @@ struct Tile {
 // state warps
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void put_state(float (&S)[64], uint32_t tm, int hs)
-{
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        float x[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = S[32 * q + i];
-        pieces3<16>(x, [&](int piece, const uint32_t (&w)[16]) { tmem_st_x16(tm + kColS + 64 * piece + 32 * hs + 16 * q, w); });
-    }
-    tmem_st_wait();
-}
+constexpr int kParts = kStateWarps / 4;   // threads of a state row
+constexpr int kT = kC / kParts;           // tokens of a thread
+constexpr int kF = kD / kParts;           // features of a thread
 
 __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShared &s, const Tile &t, int r, int h)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hs = warp >> 2;
-    const int c = (warp & 3) * 32 + lane;                                 // state row
-    const uint32_t tm = s.tmem + ((uint32_t)((warp & 3) * 32) << 16);     // this warp's lanes
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 2;
+    const int c = (warp & 3) * 32 + lane, t0 = kT * part;                 // state row, first token
+    const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;                // this warp's lanes
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
-        mbar_wait(smem_u32(&bar), parity, p.timeout_ns, p.status, &s.abort);
+        wait_for(bar, parity, p, s);
         tc_fence_after();
     };
-    const size_t at = (((size_t)r * p.H + h) * kD + c) * kD + 64 * hs;    // this thread's half row
-    float S[64];
+    // the largest of `top` here and in the threads with the other parts of the columns
+    auto row_top = [&](float (&at)[kParts][kD], float top) {
+        at[part][c] = top;
+        named_bar(kBarRow + (warp & 3), 32 * kParts);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < kParts; ++i) top = fmaxf(top, at[i][c]);
+        return top;
+    };
+    const size_t at = (((size_t)r * p.H + h) * kD + c) * kD + kF * part;  // this thread's part of the row
+    float S[kF];
+#pragma unroll
+    for (int i = 0; i < kF / 4; ++i) {
         const float4 x = p.S0 ? *reinterpret_cast<const float4 *>(p.S0 + at + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
         S[4 * i] = x.x;
         S[4 * i + 1] = x.y;
         S[4 * i + 2] = x.z;
         S[4 * i + 3] = x.w;
     }
-    put_state(S, tm, hs);
-    warp_arrive(smem_u32(&s.have_s), lane);
-    // the larger of `top` here and in the thread with the other half of the columns
-    auto row_top = [&](float (&at)[2][kD], float top) {
-        at[hs][c] = top;
-        named_bar(kBarRow + (warp & 3), 64);
-        return fmaxf(top, at[hs ^ 1][c]);
-    };
+    float u_back = 0.f;
+    // (one pass more than there are chunks: the last chunk's outputs come in the pass behind it)
 #pragma unroll 1
-    for (int ch = 0; ch < t.chunks; ++ch) {
+    for (int ch = 0;; ++ch) {
         const int st = ch & 1, k4 = ch & 3;
         const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
-        float x[32];
-        // X = b (v - G S k): tokens 32 hs .. 32 hs + 31
-        Unit ux;
+        float x[kT], y[kT];
+        if (ch < t.chunks) {
+            // S's pieces; the last one's columns may still hold U's pieces for A
+#pragma unroll
+            for (int q = 0; q < kF / 32; ++q) {
+                float z[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = S[32 * q + i];
+                pieces3<16>(z, [&](int piece, const uint32_t (&w)[16]) {
+                    if (piece == 2 && q == 0 && ch > 0) wait(s.done_o, par ^ 1u);
+                    tmem_st<16>(tm + kColS + 64 * piece + kF / 2 * part + 16 * q, w);
+                });
+            }
+            tmem_st_wait();
+            warp_arrive(smem_u32(&s.have_s), lane);
+        } else {
+            wait(s.done_o, par ^ 1u);
+        }
+        if (ch > 0) {
+            // the last chunk's outputs: o = G S q + U A
+            const int ko = (ch - 1) & 3, left = t.n - (ch - 1) * kC - t0;
+            tmem_ld<kT>(tm + kColDQ + t0, x);
+            tmem_ld<kT>(tm + kColU + t0, y);
+            tmem_ld_wait();
+            warp_arrive(smem_u32(&s.read_o), lane);
+            float f[kT];
+            read_n(s.G[ko] + t0, f);
+            mul_n(x, f);
+            read_n(s.a_unit[ko] + t0, f);
+            scale_n(f, u_back);
+            fma_n(f, y, x);              // x += f y
+            float *dst = p.o + ((size_t)(t.row0 + (ch - 1) * kC + t0) * p.H + h) * kD + c;
+            const size_t step = (size_t)p.H * kD;
+#pragma unroll
+            for (int j = 0; j < kT; ++j) {
+                if (j < left) *dst = x[j];
+                dst += step;
+            }
+        }
+        if (ch == t.chunks) break;
+        // X = b (v - G S k)
         wait(s.vfull[st], par2);
         wait(s.ready[st], par2);
         {
-            float bv[32], G[32];
-            read32(s.b[k4] + 32 * hs, bv);
-            read32(s.G[k4] + 32 * hs, G);
-            const uint16_t *v = s.V[st] + 32 * hs * kD + c;
+            const int left = t.n - ch * kC - t0;
+            const uint16_t *v = s.V[st] + t0 * kD + c;
+            float f[kT];
+            read_n(s.b[k4] + t0, f);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                G[j] *= -bv[j];
-                bv[j] *= __uint_as_float((uint32_t)v[j * kD] << 16);
-            }
+            for (int j = 0; j < kT; ++j) y[j] = __uint_as_float((uint32_t)v[j * kD] << 16);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s.vempty[st]));
-            const int left = t.n - ch * kC - 32 * hs;
-            if (left < 32) {
+            if (left < kT) {
                 // rows behind the request's end are another request's, or none: whatever they hold counts for nothing
 #pragma unroll
-                for (int j = 0; j < 32; ++j) bv[j] = j < left ? bv[j] : 0.f;
+                for (int j = 0; j < kT; ++j) y[j] = j < left ? y[j] : 0.f;
             }
+            mul_n(y, f);
+            read_n(s.bG[k4] + t0, f);
             wait(s.done_k, par);
-            tmem_read(tm + kColDK + 32 * hs, x);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = fmaf(G[j], x[j], bv[j]);
+            tmem_ld<kT>(tm + kColDK + t0, x);
+            tmem_ld_wait();
+            fma_n(f, x, y);              // y += f x
         }
-        ux = unit_of(row_top(s.top[0], top_of(x, 0.f)));
-        pieces2(x, ux.scale, [&](int piece, const uint32_t (&w)[16]) { tmem_st_x16(tm + kColX + 32 * piece + 16 * hs, w); });
+        const Unit ux = unit_of(row_top(s.top[0], top_of(y)));
+        pieces2(y, ux.scale, [&](int piece, const uint32_t (&w)[kT / 2]) { tmem_st<kT / 2>(tm + kColX + 32 * piece + kT / 2 * part, w); });
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_x), lane);
 
         // U, scaled for S' (S's pieces have been read: S q came before U), then for A
+        read_n(s.m_unit[k4] + t0, y);
+        scale_n(y, ux.back);
         wait(s.done_u, par);
-        tmem_read(tm + kColU + 32 * hs, x);
-        {
-            float y[32];
-            read32(s.m_unit[k4] + 32 * hs, y);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] *= ux.back * y[j];
-            read32(s.tail[k4] + 32 * hs, y);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] *= x[j];
-            pieces3<16>(y, [&](int piece, const uint32_t (&w)[16]) { tmem_st_x16(tm + kColS + 32 * piece + 16 * hs, w); });
-        }
+        tmem_ld<kT>(tm + kColU + t0, x);
+        tmem_ld_wait();
+        mul_n(x, y);
+        read_n(s.tail[k4] + t0, y);
+        mul_n(y, x);
+        pieces3<kT / 2>(y, [&](int piece, const uint32_t (&w)[kT / 2]) { tmem_st<kT / 2>(tm + kColS + 32 * piece + kT / 2 * part, w); });
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_us), lane);
-        const Unit uu = unit_of(row_top(s.top[1], top_of(x, 0.f)));
-        pieces2(x, uu.scale, [&](int piece, const uint32_t (&w)[16]) { tmem_st_x16(tm + kColS + 96 + 32 * piece + 16 * hs, w); });
+        const Unit uu = unit_of(row_top(s.top[1], top_of(x)));
+        u_back = uu.back;
+        pieces2(x, uu.scale, [&](int piece, const uint32_t (&w)[kT / 2]) { tmem_st<kT / 2>(tm + kColUA + 32 * piece + kT / 2 * part, w); });
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_u), lane);
 
-        // S' = G_C S + U K: features 64 hs .. 64 hs + 63
+        // S' = G_C S + U K
         const float gc = s.G[k4][kC - 1];
         wait(s.done_s, par);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            tmem_read(tm + kColDK + 64 * hs + 32 * q, x);
+        for (int q = 0; q < kF / 32; ++q) {
+            float z[32];
+            tmem_ld<32>(tm + kColDK + kF * part + 32 * q, z);
+            tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) S[32 * q + i] = fmaf(gc, S[32 * q + i], x[i]);
-        }
-        wait(s.done_o, par);
-        if (ch + 1 < t.chunks) {
-            put_state(S, tm, hs);
-            warp_arrive(smem_u32(&s.have_s), lane);
-        }
-        // o = G S q + U A
-        {
-            float y[32], G[32];
-            tmem_read(tm + kColDQ + 32 * hs, x);
-            tmem_read(tm + kColU + 32 * hs, y);
-            warp_arrive(smem_u32(&s.read_o), lane);
-            read32(s.G[k4] + 32 * hs, G);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] *= G[j];
-            read32(s.a_unit[k4] + 32 * hs, G);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = fmaf(uu.back * G[j], y[j], x[j]);
-        }
-        const int left = t.n - ch * kC - 32 * hs;
-        float *dst = p.o + ((size_t)(t.row0 + ch * kC + 32 * hs) * p.H + h) * kD + c;
-        const size_t step = (size_t)p.H * kD;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (j < left) *dst = x[j];
-            dst += step;
+            for (int i = 0; i < 32; i += 2) {
+                const float2 n = __ffma2_rn(make_float2(gc, gc), make_float2(S[32 * q + i], S[32 * q + i + 1]), make_float2(z[i], z[i + 1]));
+                S[32 * q + i] = n.x;
+                S[32 * q + i + 1] = n.y;
+            }
         }
     }
     if (!*(volatile int32_t *)&s.abort) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < kF / 4; ++i)
             *reinterpret_cast<float4 *>(p.state + at + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
     }
 }
@@ -423,7 +517,7 @@ __device__ __forceinline__ void block_product(const float *X, int xs, const floa
 {
     const int r0 = kR * rt, c0 = 4 * ct;
     float2 acc[kR][2] = {};
-#pragma unroll
+#pragma unroll 2
     for (int l = 0; l < kN; l += 4) {
         float4 xr[kR], yr[4];
 #pragma unroll
@@ -474,12 +568,12 @@ __device__ __forceinline__ void invert16(float *B, int lane)
     }
 }
 
-// the two pieces of 32 values into row `row` of swizzled tiles, from column `col0` on (a multiple of 32)
-__device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, int col0, const float (&x)[32], float scale)
+// the two pieces of 16 values into row `row` of swizzled tiles, from column `col0` on (a multiple of 16)
+__device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, int col0, const float (&x)[16], float scale)
 {
-    pieces2(x, scale, [&](int piece, const uint32_t (&w)[16]) {
+    pieces2(x, scale, [&](int piece, const uint32_t (&w)[8]) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 2; ++q)
             *reinterpret_cast<uint4 *>(tile[piece] + row * 128 + (((col0 / 8 + q) ^ (row & 7)) << 4)) =
                 make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
     });
@@ -487,42 +581,52 @@ __device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, i
 
 __device__ __forceinline__ void chunk_warps(const PrefillParams &p, PrefillShared &s, const Tile &t, int h)
 {
-    const int tid = threadIdx.x - 256, lane = tid & 31, warp = tid >> 5;
-    const int i = tid & 63;                       // token of the chunk
-    const bool query = tid >= 64;                 // this thread's row of k.k / q.k
-    const uint32_t tm = s.tmem + ((uint32_t)(warp * 32) << 16);
-    auto gate = [&](int ch) {                     // threads 0..63: the gate of their token, others its strength; 1 and 0 behind the end
-        const int row = ch * kC + i;
-        if (row >= t.n) return query ? 0.f : 1.f;
-        return (query ? p.beta : p.alpha)[(size_t)(t.row0 + row) * p.H + h];
-    };
+    const int tid = threadIdx.x - kChunk0, lane = tid & 31, warp = tid >> 5;
+    const int half = warp >> 2;                   // of the columns of k.k and q.k
+    const int i = (warp & 1) * 32 + lane;         // token of the chunk
+    const bool query = warp & 2;                  // this thread's row: k_i.k or q_i.k
+    const int key = (warp & 1) + 2 * half;        // number of a warp of key rows among those
+    const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;
     // warp 3: k.k and q.k of a chunk whose rows have arrived.  Rows behind the request's end are another
     // request's, or none: whatever they hold becomes zero.
     auto products = [&](int ch) {
         const int st = ch % kStages, valid = min(t.n - ch * kC, kC);
         if (valid < kC) {
+#pragma unroll 1
             for (int e = lane; e < (kC - valid) * 16; e += 32) {
                 const int row = valid + (e >> 4), q = e & 15;
                 const uint4 z = make_uint4(0, 0, 0, 0);
-                uint8_t *half = s.KQ[st] + (q >> 3) * (128 * 128);
-                *reinterpret_cast<uint4 *>(half + row * 128 + (q & 7) * 16) = z;
-                *reinterpret_cast<uint4 *>(half + (kC + row) * 128 + (q & 7) * 16) = z;
+                uint8_t *part = s.KQ[st] + (q >> 3) * (128 * 128);
+                *reinterpret_cast<uint4 *>(part + row * 128 + (q & 7) * 16) = z;
+                *reinterpret_cast<uint4 *>(part + (kC + row) * 128 + (q & 7) * 16) = z;
             }
             fence_async_shared();
             __syncwarp();
         }
         tc_fence_after();
         const uint32_t kq = smem_u32(s.KQ[st]);
-        const uint64_t x0 = smem_desc_sw128(kq), x1 = smem_desc_sw128(kq + 128 * 128);
+        if (elect_lane()) {
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const uint64_t x = smem_desc_sw128(kq + half * 128 * 128);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-            const uint64_t d = (ks < 4 ? x0 : x1) + (uint64_t)((ks & 3) * 2);
-            tc_mma_ss_elect(s.tmem + kColKK, d, d, idesc_bf16_f32(128, kC), ks ? 1u : 0u);
+                for (int ks = 0; ks < 4; ++ks)
+                    tc_mma_ss(kColKK, x + (uint64_t)(ks * 2), x + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC), (uint32_t)(half | ks));
+            }
+            tc_commit(smem_u32(&s.bar_kk));
         }
-        tc_commit_elect(smem_u32(&s.bar_kk));
+        __syncwarp();
     };
-    auto arrived = [&](int ch) { mbar_wait(smem_u32(&s.full[ch % kStages]), (ch / kStages) & 1, p.timeout_ns, p.status, &s.abort); };
-    float ab = gate(0);
+    auto arrived = [&](int ch) { wait_for(s.full[ch % kStages], (ch / kStages) & 1, p, s); };
+    // the gate and the strength of this thread's token; 1 and 0 behind the end
+    float a, b;
+    auto gate = [&](int ch) {
+        const int row = ch * kC + i;
+        const size_t at = (size_t)(t.row0 + row) * p.H + h;
+        a = row < t.n ? p.alpha[at] : 1.f;
+        b = row < t.n ? p.beta[at] : 0.f;
+    };
+    gate(0);
     if (warp == 3) {
         arrived(0);
         __syncwarp();
@@ -531,118 +635,109 @@ __device__ __forceinline__ void chunk_warps(const PrefillParams &p, PrefillShare
 #pragma unroll 1
     for (int ch = 0; ch < t.chunks; ++ch) {
         const int st = ch & 1, k4 = ch & 3;
-        if (query)
-            s.b[k4][i] = ab;
-        else if (i > 0)
-            s.next[i - 1] = ab;
-        else {
-            s.first = ab;
-            s.next[kC - 1] = 1.f;
+        // products of the gates from this block of 32 tokens' start to token i, and from behind it to the block's end
+        float up = a, down = a;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, up, o), v = __shfl_down_sync(0xffffffffu, down, o);
+            if (lane >= o) up *= u;
+            if (lane + o < 32) down *= v;
+        }
+        down = __shfl_down_sync(0xffffffffu, down, 1);
+        if (lane == 31) down = 1.f;
+        const bool writes = !query && half == 0;  // of the four threads of token i
+        if (writes) {
+            s.next[(i + kC - 1) & (kC - 1)] = i ? a : 1.f;
+            if (lane == 31) s.gates[warp] = up;
         }
         named_bar(kBarChunk, kChunkThreads);
-        if (ch + 1 < t.chunks) ab = gate(ch + 1);
-        mbar_wait(smem_u32(&s.bar_kk), ch & 1, p.timeout_ns, p.status, &s.abort);
+        if (writes) {
+            const float g = i < 32 ? up : up * s.gates[0];
+            s.b[k4][i] = b;
+            s.G[k4][i] = g;
+            s.bG[k4][i] = -b * g;
+            s.tail[k4][i] = i < 32 ? down * s.gates[1] : down;
+        }
+        float d = query ? 1.f : b;                // D_ij (times b_i), from j = i down
+        if (half == 0 && i >= 32) d *= up;        // (from j = 31)
+        if (ch + 1 < t.chunks) gate(ch + 1);
+        wait_for(s.bar_kk, ch & 1, p, s);
         tc_fence_after();
+        float x[2][16];
+        tmem_ld<16>(tm + kColKK + 32 * half, x[0]);
+        tmem_ld<16>(tm + kColKK + 32 * half + 16, x[1]);
+        tmem_ld_wait();
         {
-            float d = query ? 1.f : s.b[k4][i];       // D_ij (times b_i), from j = i down
-            const int last = query ? i : i - 1;       // the row's last entry
-            float x[2][32], top = 0.f;
+            const int last = (query ? i : i - 1) - 32 * half, row = i - 32 * half;   // the row's last entry in this half
 #pragma unroll
-            for (int half = 1; half >= 0; --half) {
-                tmem_read(tm + kColKK + 32 * half, x[half]);
+            for (int g = 7; g >= 0; --g) {
+                const float4 nx = *reinterpret_cast<const float4 *>(s.next + 32 * half + 4 * g);
+                const float f[4] = {nx.x, nx.y, nx.z, nx.w};
 #pragma unroll
-                for (int g = 7; g >= 0; --g) {
-                    const float4 nx = *reinterpret_cast<const float4 *>(s.next + 32 * half + 4 * g);
-                    const float f[4] = {nx.x, nx.y, nx.z, nx.w};
-#pragma unroll
-                    for (int e = 3; e >= 0; --e) {
-                        const int j = 32 * half + 4 * g + e;
-                        d *= j < i ? f[e] : 1.f;
-                        x[half][4 * g + e] = j <= last ? x[half][4 * g + e] * d : 0.f;
-                    }
+                for (int e = 3; e >= 0; --e) {
+                    const int j = 4 * g + e;
+                    if (j < 31) d *= j < row ? f[e] : 1.f;   // (j = 31: this half's first, or behind the block that d has)
+                    float &v = x[j >> 4][j & 15];
+                    v = j <= last ? v * d : 0.f;
                 }
-                top = top_of(x[half], top);
-            }
-            if (ch >= 2) mbar_wait(smem_u32(&s.used[st]), ((ch >> 1) & 1) ^ 1, p.timeout_ns, p.status, &s.abort);
-            if (query) {
-                const Unit u = unit_of(top);
-                s.a_unit[k4][i] = u.back;
-                put_row(s.A[st], i, 0, x[0], u.scale);
-                put_row(s.A[st], i, 32, x[1], u.scale);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    *reinterpret_cast<float4 *>(s.L + i * kLS + 4 * q) =
-                        make_float4(x[q >> 3][4 * (q & 7)], x[q >> 3][4 * (q & 7) + 1], x[q >> 3][4 * (q & 7) + 2], x[q >> 3][4 * (q & 7) + 3]);
             }
         }
-        if (warp == 0) {
-            // G_i and D_Ci by scans of the gates from both ends, two tokens to a lane
-            const float a1 = s.next[2 * lane], a0 = lane ? s.next[2 * lane - 1] : s.first;
-            float up = a0 * a1, down = up;
+        float top = 0.f;
+        if (query) {
+            top = fmaxf(top_of(x[0]), top_of(x[1]));
+            s.a_top[half][i] = top;
+        } else {
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float u = __shfl_up_sync(0xffffffffu, up, o), v = __shfl_down_sync(0xffffffffu, down, o);
-                if (lane >= o) up *= u;
-                if (lane + o < 32) down *= v;
-            }
-            float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
-            if (lane == 0) before = 1.f;
-            if (lane == 31) after = 1.f;
-            *reinterpret_cast<float2 *>(&s.G[k4][2 * lane]) = make_float2(before * a0, up);
-            *reinterpret_cast<float2 *>(&s.tail[k4][2 * lane]) = make_float2(a1 * after, after);
+            for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<float4 *>(s.L + i * kLS + 32 * half + 4 * q) =
+                    make_float4(x[q >> 2][4 * (q & 3)], x[q >> 2][4 * (q & 3) + 1], x[q >> 2][4 * (q & 3) + 2], x[q >> 2][4 * (q & 3) + 3]);
         }
+        if (ch >= 2) wait_for(s.used[st], ((ch >> 1) & 1) ^ 1, p, s);
         tc_fence_before();
         named_bar(kBarChunk, kChunkThreads);
-        // the next chunk's products as soon as its rows are there
-        bool issued = false;
+        // the next chunk's products: its rows have mostly arrived, and the warps of the query rows have time
         if (warp == 3 && ch + 1 < t.chunks) {
-            issued = __all_sync(0xffffffffu, mbar_test_wait(smem_u32(&s.full[(ch + 1) % kStages]), ((ch + 1) / kStages) & 1));
-            if (issued) products(ch + 1);
-        }
-        // M by blocks of 16, 32 and 64: M21 = -M22 (L21 M11)
-        invert16(s.L + warp * 16 * (kLS + 1), lane);
-        named_bar(kBarChunk, kChunkThreads);
-        {
-            float *B = s.L + (warp >> 1) * 32 * (kLS + 1), *T = s.T + (warp >> 1) * 16 * kTS16;
-            const int tt = tid & 63;
-            block_product<16, 1, false>(B + 16 * kLS, kLS, B, kLS, T, kTS16, tt >> 2, tt & 3);
-            named_bar(kBarChunk, kChunkThreads);
-            block_product<16, 1, true>(B + 16 * (kLS + 1), kLS, T, kTS16, B + 16 * kLS, kLS, tt >> 2, tt & 3);
-        }
-        named_bar(kBarChunk, kChunkThreads);
-        block_product<32, 2, false>(s.L + 32 * kLS, kLS, s.L, kLS, s.T, kTS, tid >> 3, tid & 7);
-        named_bar(kBarChunk, kChunkThreads);
-        block_product<32, 2, true>(s.L + 32 * (kLS + 1), kLS, s.T, kTS, s.L + 32 * kLS, kLS, tid >> 3, tid & 7);
-        named_bar(kBarChunk, kChunkThreads);
-        {
-            const int row = tid >> 1, c0 = (tid & 1) * 32;
-            float x[32];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float4 v = *reinterpret_cast<const float4 *>(s.L + row * kLS + c0 + 4 * q);
-                x[4 * q] = v.x;
-                x[4 * q + 1] = v.y;
-                x[4 * q + 2] = v.z;
-                x[4 * q + 3] = v.w;
-            }
-            float top = top_of(x, 0.f);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            const Unit u = unit_of(top);
-            if (c0 == 0) s.m_unit[k4][row] = u.back;
-            put_row(s.M[st], row, c0, x, u.scale);
-        }
-        fence_async_shared();
-        warp_arrive(smem_u32(&s.ready[st]), lane);
-        if (warp == 3 && ch + 1 < t.chunks && !issued) {
             arrived(ch + 1);
             __syncwarp();
             products(ch + 1);
         }
+        if (query) {
+            const Unit u = unit_of(fmaxf(top, s.a_top[half ^ 1][i]));
+            if (half == 0) s.a_unit[k4][i] = u.back;
+            put_row(s.A[st], i, 32 * half, x[0], u.scale);
+            put_row(s.A[st], i, 32 * half + 16, x[1], u.scale);
+        } else {
+            // M by blocks of 16, 32 and 64: M21 = -M22 (L21 M11)
+            invert16(s.L + key * 16 * (kLS + 1), lane);
+            named_bar(kBarKey, 128);
+            float *B = s.L + (key >> 1) * 32 * (kLS + 1), *T = s.T + (key >> 1) * 16 * kTS16;
+            const int tt = (key & 1) * 32 + lane;
+            block_product<16, 1, false>(B + 16 * kLS, kLS, B, kLS, T, kTS16, tt >> 2, tt & 3);
+            named_bar(kBarKey, 128);
+            block_product<16, 1, true>(B + 16 * (kLS + 1), kLS, T, kTS16, B + 16 * kLS, kLS, tt >> 2, tt & 3);
+        }
+        named_bar(kBarChunk, kChunkThreads);
+        block_product<32, 1, false>(s.L + 32 * kLS, kLS, s.L, kLS, s.T, kTS, tid >> 3, tid & 7);
+        named_bar(kBarChunk, kChunkThreads);
+        block_product<32, 1, true>(s.L + 32 * (kLS + 1), kLS, s.T, kTS, s.L + 32 * kLS, kLS, tid >> 3, tid & 7);
+        named_bar(kBarChunk, kChunkThreads);
+        {
+            const int row = tid >> 2, c0 = (tid & 3) * 16;
+            float m[16];
+            read_n(s.L + row * kLS + c0, m);
+            float mt = top_of(m);
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+            const Unit u = unit_of(mt);
+            if (c0 == 0) s.m_unit[k4][row] = u.back;
+            put_row(s.M[st], row, c0, m, u.scale);
+        }
+        fence_async_shared();
+        warp_arrive(smem_u32(&s.ready[st]), lane);
     }
     if (warp == 3) {
-        tc_commit_elect(smem_u32(&s.last_kk));
-        drain(smem_u32(&s.last_kk), 0, p.timeout_ns);
+        if (elect_lane()) tc_commit(smem_u32(&s.last_kk));
+        drain(s.last_kk, 0, p);
     }
 }
 
@@ -650,28 +745,26 @@ __device__ __forceinline__ void chunk_warps(const PrefillParams &p, PrefillShare
 // the issuing warps
 // ---------------------------------------------------------------------------
 
-// Two FP32 operands of two F16 pieces each, K = 64 tokens: high times high, high times low, low times high.
-// a(piece, step): columns of the left one; B: the right one's tiles.
-template <class F>
-__device__ __forceinline__ void issue_pairs(uint32_t d, F a, const uint8_t (*B)[kC * 128])
-{
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-        const uint64_t b = smem_desc_sw128(smem_u32(B[q == 1]));
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-            tc_mma_ts_elect(d, a(q == 2, ks), b + (uint64_t)(ks * 2), kIdescF16, (q | ks) ? 1u : 0u);
-    }
-}
-
+// The loops stay rolled: a product's few instructions are fetched once and run from the instruction
+// buffer, where straight-line code waits longer for its next line than for the tensor cores.
 __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared &s, const Tile &t)
 {
-    const uint32_t tm = s.tmem;
     bool ok = true;
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, p.timeout_ns, p.status, &s.abort));
+        ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, p, s));
         tc_fence_after();
         return ok;
+    };
+    // two FP32 operands of two F16 pieces each, K = 64 tokens: high times high, high times low, low times high
+    auto pairs = [&](uint32_t a, const uint8_t *B) {
+        const uint64_t b0 = smem_desc_sw128(smem_u32(B));
+#pragma unroll 1
+        for (int q = 0; q < 3; ++q) {
+            const uint64_t b = b0 + (q == 1 ? kC * 128 / 16 : 0);
+            const uint32_t aq = a + (q == 2 ? 32 : 0);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) tc_mma_ts(kColU, aq + 8 * ks, b + (uint64_t)(ks * 2), kIdescF16, (uint32_t)(q | ks));
+        }
     };
 #pragma unroll 1
     for (int ch = 0; ch < t.chunks; ++ch) {
@@ -680,41 +773,52 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
         const uint32_t kq = smem_u32(s.KQ[sk]);
         if (!wait(s.full[sk], (ch / kStages) & 1) || !wait(s.ready[st], par2) || !wait(s.have_s, par)) break;
         // S k (rows 0..63 of the tile), then S q (rows 64..127) once the last chunk's outputs are read
-        auto products = [&](uint32_t d, uint32_t row0) {
-            const uint64_t b0 = smem_desc_sw128(kq + row0 * 128), b1 = smem_desc_sw128(kq + 128 * 128 + row0 * 128);
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+            if (q && ch > 0 && !wait(s.read_o, par ^ 1u)) break;
+            if (elect_lane()) {
+                const uint32_t d = q ? kColDQ : kColDK;
+                const uint64_t b0 = smem_desc_sw128(kq + q * kC * 128);
+#pragma unroll 1
+                for (int half = 0; half < 6; ++half) {      // halves of the features, piece by piece
+                    const uint64_t b = b0 + (half & 1 ? 128 * 128 / 16 : 0);
 #pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        tc_mma_ts(d, kColS + 32 * half + 8 * ks, b + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC), (uint32_t)(half | ks));
+                }
+                if (q == 0) tc_commit(smem_u32(&s.done_k));
+            }
+            __syncwarp();
+        }
+        if (!wait(s.have_x, par)) break;
+        if (elect_lane()) {
+            pairs(kColX, s.M[st][0]);
+            tc_commit(smem_u32(&s.done_u));
+        }
+        __syncwarp();
+        if (!wait(s.have_us, par)) break;
+        if (elect_lane()) {
+            const uint64_t b = smem_desc_mn_sw128(kq, 128 * 128);
+#pragma unroll 1
             for (int piece = 0; piece < 3; ++piece)
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    tc_mma_ts_elect(d, tm + kColS + 64 * piece + 8 * ks, (ks < 4 ? b0 : b1) + (uint64_t)((ks & 3) * 2),
-                                    idesc_bf16_f32(128, kC), (piece | ks) ? 1u : 0u);
-        };
-        products(tm + kColDK, 0);
-        tc_commit_elect(smem_u32(&s.done_k));
-        if (ch > 0 && !wait(s.read_o, par ^ 1u)) break;
-        products(tm + kColDQ, kC);
-        if (!wait(s.have_x, par)) break;
-        issue_pairs(tm + kColU, [&](int piece, int ks) {
-            return tm + kColX + 32 * piece + 8 * ks;
-        }, s.M[st]);
-        tc_commit_elect(smem_u32(&s.done_u));
-        if (!wait(s.have_us, par)) break;
-#pragma unroll
-        for (int piece = 0; piece < 3; ++piece)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                tc_mma_ts_elect(tm + kColDK, tm + kColS + 32 * piece + 8 * ks,
-                                smem_desc_mn_sw128(kq + ks * 16 * 128, 128 * 128), idesc_bf16_f32(128, kD) | kBMnMajor,
-                                (piece | ks) ? 1u : 0u);
-        tc_commit_elect(smem_u32(&s.done_s));
-        tc_commit_elect(smem_u32(&s.empty[sk]));
+                for (int ks = 0; ks < 4; ++ks)
+                    tc_mma_ts(kColDK, kColS + 32 * piece + 8 * ks, b + (uint64_t)(ks * 16 * 128 / 16),
+                              idesc_bf16_f32(128, kD) | kBMnMajor, (uint32_t)(piece | ks));
+            tc_commit(smem_u32(&s.done_s));
+            tc_commit(smem_u32(&s.empty[sk]));
+        }
+        __syncwarp();
         if (!wait(s.have_u, par)) break;
-        issue_pairs(tm + kColU, [&](int piece, int ks) { return tm + kColS + 96 + 32 * piece + 8 * ks; }, s.A[st]);
-        tc_commit_elect(smem_u32(&s.done_o));
-        tc_commit_elect(smem_u32(&s.used[st]));
+        if (elect_lane()) {
+            pairs(kColUA, s.A[st][0]);
+            tc_commit(smem_u32(&s.done_o));
+            tc_commit(smem_u32(&s.used[st]));
+        }
+        __syncwarp();
     }
-    tc_commit_elect(smem_u32(&s.last));
-    drain(smem_u32(&s.last), 0, p.timeout_ns);   // no product in flight when tensor memory is given back
+    if (elect_lane()) tc_commit(smem_u32(&s.last));
+    drain(s.last, 0, p);   // no product in flight when tensor memory is given back
 }
 
 __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShared &s, const Tile &t, int h, const CUtensorMap &qmap,
@@ -726,7 +830,7 @@ __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShare
     for (int ch = 0; ch < t.chunks; ++ch) {
         const int sk = ch % kStages, sv = ch & 1, row = t.row0 + ch * kC;
         const uint32_t kq_bar = smem_u32(&s.full[sk]), v_bar = smem_u32(&s.vfull[sv]), kq = smem_u32(s.KQ[sk]);
-        if (ch >= kStages && !mbar_wait(smem_u32(&s.empty[sk]), ((ch / kStages) & 1) ^ 1, p.timeout_ns, p.status, &s.abort)) break;
+        if (ch >= kStages && !wait_for(s.empty[sk], ((ch / kStages) & 1) ^ 1, p, s)) break;
         mbar_expect_tx(kq_bar, kKqBytes);
         if (withheld) break;
 #pragma unroll
@@ -735,15 +839,15 @@ __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShare
             tma_load_2d(kq + half * 128 * 128 + kC * 128, &qmap, hk * kD + 64 * half, row, kq_bar);
         }
         kq_issued = ch + 1;
-        if (ch >= 2 && !mbar_wait(smem_u32(&s.vempty[sv]), ((ch >> 1) & 1) ^ 1, p.timeout_ns, p.status, &s.abort)) break;
+        if (ch >= 2 && !wait_for(s.vempty[sv], ((ch >> 1) & 1) ^ 1, p, s)) break;
         mbar_expect_tx(v_bar, kVBytes);
         tma_load_2d(smem_u32(s.V[sv]), &vmap, h * kD, row, v_bar);
         v_issued = ch + 1;
     }
     // no copy into shared memory in flight at the end
     for (int ch = max(kq_issued - kStages, 0); ch < kq_issued; ++ch)
-        drain(smem_u32(&s.full[ch % kStages]), (ch / kStages) & 1, p.timeout_ns);
-    for (int ch = max(v_issued - 2, 0); ch < v_issued; ++ch) drain(smem_u32(&s.vfull[ch & 1]), (ch >> 1) & 1, p.timeout_ns);
+        drain(s.full[ch % kStages], (ch / kStages) & 1, p);
+    for (int ch = max(v_issued - 2, 0); ch < v_issued; ++ch) drain(s.vfull[ch & 1], (ch >> 1) & 1, p);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -777,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int st = 0; st < 2; ++st) {
             mbar_init(smem_u32(&s.vfull[st]), 1);
             mbar_init(smem_u32(&s.vempty[st]), kStateWarps);
-            mbar_init(smem_u32(&s.ready[st]), kChunkThreads / 32);
+            mbar_init(smem_u32(&s.ready[st]), kChunkWarps);
             mbar_init(smem_u32(&s.used[st]), 1);
         }
         for (unsigned long long *b : {&s.bar_kk, &s.done_k, &s.done_u, &s.done_s, &s.done_o, &s.last, &s.last_kk}) mbar_init(smem_u32(b), 1);
@@ -792,20 +896,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp < 8) {
+    if (tid < kChunk0) {
         regs_inc<kRegsState>();
         state_warps(p, s, t, r, h);
-    } else if (warp < 12) {
-        regs_dec<kRegsChunk>();
+    } else if (tid < kIssue0) {
         chunk_warps(p, s, t, h);
     } else {
         regs_dec<kRegsIssue>();
-        if (warp == 12) issue_warp(p, s, t);
-        if (tid == 13 * 32) copy_thread(p, s, t, h, qmap, kmap, vmap);
+        if (warp == kIssue0 / 32) issue_warp(p, s, t);
+        if (tid == kIssue0 + 32) copy_thread(p, s, t, h, qmap, kmap, vmap);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && s.abort) atomicCAS(p.status, 0, (int32_t)W12_E_TIMEOUT);
     if (warp == 0) tmem_dealloc(s.tmem, 512);
 }
 
@@ -867,7 +971,7 @@ int launch_gdn_prefill(const GdnSeqArgs &a, void *stream)
     p.H = a.H;
     p.group = a.H / a.Hk;
     p.n_rows = a.n_rows;
-    p.timeout_ns = a.timeout_ns;
+    p.polls = (uint32_t)std::min<uint64_t>(a.timeout_ns / kWaitSleepNs + 1, 1u << 31);
     p.status = a.status;
     p.debug_flags = a.debug_flags;
     cudaLaunchConfig_t cfg{};

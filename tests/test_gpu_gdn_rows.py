@@ -201,7 +201,9 @@ def test_offsets_that_make_no_sense(w12):
             if r in bad:
                 assert (state[r] == 9.0).all()
             elif (off[r], off[r + 1]) == (c.off[r], c.off[r + 1]):
-                assert torch.equal(state[r], gs[r]) and torch.equal(out[off[r]:off[r + 1]], good[off[r]:off[r + 1]])
+                end = min(off[r + 1], off[2])              # (rows that another request's offsets take in as well are anyone's)
+                assert torch.equal(state[r], gs[r]) and (r >= 2 or torch.equal(out[off[r]:end], good[off[r]:end]))
+                assert r < 2 or torch.equal(out[off[r]:off[r + 1]], good[off[r]:off[r + 1]])
     out, state = c.run(w12)
     assert torch.equal(out, good) and torch.equal(state, gs)
 

@@ -1,0 +1,950 @@
+// Recurrent (Gated DeltaNet) layer over whole prompts (sm_103a).
+//
+// A head's state S (d_v x d_k) follows S <- a S (I - b k k^T) + b v k^T, and a
+// token's output is o = S q of the new state.  64 tokens are taken at once.
+// With G_i the product of the gates from the chunk's start to token i and D_ij
+// that of the gates j + 1 .. i, the vectors u_i = b_i (v_i - a_i S_{i-1} k_i)
+// solve
+//     (I + L) U = X,   L_ij = b_i D_ij k_i.k_j (j < i),   x_i = b_i (v_i - G_i S k_i),
+// with S the state in front of the chunk, and
+//     o_i = G_i S q_i + sum over j <= i of A_ij u_j,   A_ij = D_ij q_i.k_j,
+//     S'  = G_C S + sum over j of D_Cj u_j k_j^T.
+// M = (I + L)^-1 and A need no state, so they are made a chunk ahead.  The D_ij
+// are running products, never quotients: a gate of zero forgets, as it should.
+//
+// One CTA to a (request, head); the state rows c lie on the 128 lanes of tensor
+// memory throughout, so that all its products take their left operand from
+// there and no operand but M and A is ever written to shared memory:
+//     D_K[c][j] = S k_j    D_Q[c][j] = S q_j    U[c][i] = X M^T    U A^T    S' += U K.
+// Products with keys and queries take those as they are and the FP32 side (S, U) as three BF16
+// pieces that add up to it exactly: two (2^-17) would be the largest error of the layer by
+// far.  Products of two FP32 sides (X M^T, U A^T) take both as two F16 pieces (2^-22) under a power of two
+// for each row, and of their four pairs all but the smallest.  All accumulation is FP32.
+//
+// Twenty-eight warps (many, with few columns each: a chunk runs through every role's code once, and
+// the time goes into fetching that code, which warps in step share):
+//  * state warps (0..15; four threads to a state row, each with a quarter of the
+//    columns; S itself stays in their registers) turn accumulators into operands,
+//  * chunk warps (16..23; two threads to a row of k.k or q.k) make M and A of the next chunk: k.k and q.k on
+//    the tensor cores, then the inverse, of four 16 x 16 blocks by columns and of the
+//    blocks below them from those,
+//  * warp 24 issues the state warps' products, warp 25 the copies by TMA.
+// Every wait is bounded: a wait that runs out sets s.abort, which ends every
+// other wait at once, so all roles run to their ends; the state is then left
+// unwritten.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstddef>
+
+#include "w12_device.cuh"
+
+using namespace w12d;
+
+namespace {
+
+constexpr int kD = 128;             // head dimension
+constexpr int kC = 64;              // tokens of a chunk
+constexpr int kStateWarps = 16, kChunkWarps = 8;
+constexpr int kChunkThreads = 32 * kChunkWarps;
+constexpr int kThreads = 32 * (kStateWarps + kChunkWarps + 4);
+constexpr int kChunk0 = 32 * kStateWarps, kIssue0 = kChunk0 + kChunkThreads;   // the roles' first threads
+constexpr int kRegsLaunch = 72, kRegsState = 80, kRegsIssue = 40;             // (chunk warps keep the launch's)
+static_assert(kChunk0 * kRegsState + kChunkThreads * kRegsLaunch + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register shares");
+
+// tensor memory columns: all 512 are one CTA's, from column 0 on
+constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; later three of U for S', 32 each,
+constexpr uint32_t kColUA = 128;    // and, on the last of them, two of U for A
+constexpr uint32_t kColDQ = 192;    // S q
+constexpr uint32_t kColDK = 256;    // S k; then, with the next 64 columns, U K
+constexpr uint32_t kColX = 320;     // X's two pieces
+constexpr uint32_t kColU = 384;     // U; then U A
+constexpr uint32_t kColKK = 448;    // k.k (lanes 0..63) and q.k (lanes 64..127) of the next chunk
+
+constexpr int kLS = 68;             // FP32 row stride of L and M (16-byte rows, 4 banks apart)
+constexpr int kTS = 36, kTS16 = 20; // and of products in between, of 32 and 16 columns
+constexpr int kBarChunk = 1;        // named barrier of the chunk warps
+constexpr int kBarRow = 2;          // of the four warps of 32 state rows (2 .. 5)
+constexpr int kBarKey = 6;          // and of the four chunk warps with key rows
+constexpr int kStages = 3;          // of keys and queries (their chunk is prepared while two others are in use)
+
+struct PrefillShared {
+    uint8_t KQ[kStages][2 * 128 * 128];   // [stage][feature half][key rows, query rows][64 BF16], 128-byte swizzle
+    uint8_t M[2][2][kC * 128];      // pieces of M and A, rows of 64 F16, 128-byte swizzle
+    uint8_t A[2][2][kC * 128];
+    uint16_t V[2][kC * kD];
+    alignas(16) float L[kC * kLS];
+    alignas(16) float T[32 * kTS];
+    alignas(16) float next[kC];     // the gates of tokens 1 .. 63, then 1
+    alignas(16) float b[4][kC];     // of chunk c in [c % 4]: strengths, -b_i G_i, G_i, D_Ci
+    alignas(16) float bG[4][kC];
+    alignas(16) float G[4][kC];
+    alignas(16) float tail[4][kC];
+    alignas(16) float m_unit[4][kC];   // and the powers of two of the rows of M and of A
+    alignas(16) float a_unit[4][kC];
+    float top[2][4][kD];            // [X, U][quarter] largest magnitude of a state row's values
+    float a_top[2][kC];             // and of a row of A, by halves
+    float gates[2];                 // products of the gates of tokens 0 .. 31 and 32 .. 63
+    unsigned long long full[kStages], empty[kStages];   // keys and queries
+    unsigned long long vfull[2], vempty[2];             // values
+    unsigned long long ready[2], used[2];               // M, A and the gates' products; M and A have been read
+    unsigned long long bar_kk;
+    unsigned long long have_s, have_x, have_us, have_u, read_o;   // to the issuing warp: operands written, outputs read
+    unsigned long long done_k, done_u, done_s, done_o;            // from it: products done
+    unsigned long long last, last_kk;
+    uint32_t tmem;
+    int32_t abort;
+};
+static_assert(sizeof(PrefillShared) + 1024 <= 227 * 1024, "shared memory above the per-CTA limit");
+static_assert(offsetof(PrefillShared, M) % 1024 == 0 && offsetof(PrefillShared, A) % 1024 == 0, "swizzled tiles");
+static_assert(offsetof(PrefillShared, V) % 128 == 0 && offsetof(PrefillShared, full) % 8 == 0, "copies and barriers");
+constexpr uint32_t kKqBytes = sizeof(PrefillShared::KQ) / kStages, kVBytes = sizeof(PrefillShared::V) / 2;
+
+struct PrefillParams {
+    const float *S0;                // may be null: zero
+    float *state, *o;
+    const float *alpha, *beta;
+    const int32_t *off;
+    int32_t H, group, n_rows;
+    uint32_t timeout_ns;
+    int32_t *status;
+    int32_t debug_flags;            // bit 0: CTA (0, 0) announces its first copies and leaves them out (test hook)
+};
+
+template <int N>
+__device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+// BF16 operand whose rows (of 64 features, 128-byte swizzle) are its K index: 8-row groups 1024 bytes
+// apart, the next 64 features `half` bytes on
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t half)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(half >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+constexpr uint32_t kBMnMajor = 1u << 16;   // instruction descriptor: B's rows are its K index
+constexpr uint32_t kIdescF16 = (1u << 4) | ((uint32_t)(kC >> 3) << 17) | ((128u >> 4) << 24);   // F16 operands, both K-major, N = 64
+
+// The high, middle and low BF16 pieces of 2N values, N words each: `put(piece, words)`.  Every piece is
+// the upper half of what the ones before it left, so the three add up exactly.
+template <int N, class F>
+__device__ __forceinline__ void pieces3(float (&x)[2 * N], F put)
+{
+#pragma unroll
+    for (int piece = 0; piece < 3; ++piece) {
+        uint32_t w[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t b0 = __float_as_uint(x[2 * i]), b1 = __float_as_uint(x[2 * i + 1]);
+            w[i] = __byte_perm(b0, b1, 0x7632);
+            if (piece < 2) {
+                const float2 r = __ffma2_rn(make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u)),
+                                            make_float2(-1.f, -1.f), make_float2(x[2 * i], x[2 * i + 1]));
+                x[2 * i] = r.x;
+                x[2 * i + 1] = r.y;
+            }
+        }
+        put(piece, w);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t w)
+{
+    float2 r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(w));
+    return r;
+}
+
+// The power of two that brings magnitudes up to `top` into [2^13, 2^14), and its inverse.  F16's range below that
+// is 2^-38 of the top, far under what FP32 sums keep; magnitudes under 2^-113 count as that.
+struct Unit {
+    float scale, back;
+};
+__device__ __forceinline__ Unit unit_of(float top)
+{
+    const uint32_t e = min(max(__float_as_uint(top) >> 23, 14u), 253u);
+    return Unit{__uint_as_float((267u - e) << 23), __uint_as_float((e - 13u) << 23)};
+}
+
+template <int N>
+__device__ __forceinline__ float top_of(const float (&x)[N])
+{
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(x[i]));
+    return top;
+}
+
+// The two F16 pieces of 16 scaled values, rounded to nearest: what is left is 2^-22 of a value
+template <class F>
+__device__ __forceinline__ void pieces2(const float (&x)[16], float scale, F put)
+{
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 y = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(scale, scale));
+        hi[i] = pack_f16x2(y.x, y.y);
+        const float2 r = __ffma2_rn(unpack_f16x2(hi[i]), make_float2(-1.f, -1.f), y);
+        lo[i] = pack_f16x2(r.x, r.y);
+    }
+    put(0, hi);
+    put(1, lo);
+}
+
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// 32 lanes x 16 columns as floats (complete after tmem_ld_wait)
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&x)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]),
+          "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// 32 lanes x 32 columns as floats, the load complete
+__device__ __forceinline__ void tmem_read(uint32_t taddr, float (&x)[32])
+{
+    uint32_t w[32];
+    tmem_ld_x32(taddr, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(w[i]);
+}
+
+// 16 values of shared memory, the same ones for every lane
+__device__ __forceinline__ void read16(const float *src, float (&x)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = reinterpret_cast<const float4 *>(src)[i];
+        x[4 * i] = v.x;
+        x[4 * i + 1] = v.y;
+        x[4 * i + 2] = v.z;
+        x[4 * i + 3] = v.w;
+    }
+}
+
+// this warp's tensor-memory accesses are done: one arrival for the warp
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane)
+{
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+// mbar_wait in fewer instructions (there are two dozen of it): the clock's lower word, limits up to 2^31 ns
+__device__ __forceinline__ uint32_t timer_low()
+{
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+
+__device__ __forceinline__ bool wait_for(unsigned long long &bar, uint32_t parity, const PrefillParams &p, PrefillShared &s)
+{
+    const uint32_t at = smem_u32(&bar);
+    if (mbar_try_wait(at, parity)) return true;
+    const uint32_t t0 = timer_low();
+#pragma unroll 1
+    while (!mbar_try_wait_sleep(at, parity, kWaitSleepNs)) {
+        if (*(volatile int32_t *)&s.abort) return false;
+        if (timer_low() - t0 > p.timeout_ns) {
+            atomicCAS(p.status, 0, (int32_t)W12_E_TIMEOUT);
+            *(volatile int32_t *)&s.abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// a wait that nothing ends early: for what is in flight at the end
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint64_t timeout_ns)
+{
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < timeout_ns) {
+    }
+}
+
+struct Tile {
+    int32_t row0, n, chunks;        // the request's first row, its rows, chunks
+};
+
+// ---------------------------------------------------------------------------
+// state warps
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShared &s, const Tile &t, int r, int h)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, qt = warp >> 2;   // qt: quarter of the columns
+    const int c = (warp & 3) * 32 + lane;                                 // state row
+    const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;     // this warp's lanes
+    auto wait = [&](unsigned long long &bar, uint32_t parity) {
+        wait_for(bar, parity, p, s);
+        tc_fence_after();
+    };
+    // S's pieces; `before_last` comes in front of the last one, whose columns U's pieces for A may still hold
+    auto put_state = [&](const float (&S)[32], auto before_last) {
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = S[i];
+        pieces3<16>(x, [&](int piece, const uint32_t (&w)[16]) {
+            if (piece == 2) before_last();
+            tmem_st_x16(tm + kColS + 64 * piece + 16 * qt, w);
+        });
+        tmem_st_wait();
+        warp_arrive(smem_u32(&s.have_s), lane);
+    };
+    // the largest of `top` here and in the threads with the other quarters of the columns
+    auto row_top = [&](float (&at)[4][kD], float top) {
+        at[qt][c] = top;
+        named_bar(kBarRow + (warp & 3), 128);
+        return fmaxf(fmaxf(at[0][c], at[1][c]), fmaxf(at[2][c], at[3][c]));
+    };
+    const size_t at = (((size_t)r * p.H + h) * kD + c) * kD + 32 * qt;    // this thread's quarter row
+    float S[32];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 x = p.S0 ? *reinterpret_cast<const float4 *>(p.S0 + at + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        S[4 * i] = x.x;
+        S[4 * i + 1] = x.y;
+        S[4 * i + 2] = x.z;
+        S[4 * i + 3] = x.w;
+    }
+    put_state(S, [] {});
+#pragma unroll 1
+    for (int ch = 0; ch < t.chunks; ++ch) {
+        const int st = ch & 1, k4 = ch & 3, t0 = 16 * qt;                 // t0: this thread's first token
+        const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
+        const int left = t.n - ch * kC - t0;
+        float x[16], y[16];
+        // X = b (v - G S k)
+        wait(s.vfull[st], par2);
+        wait(s.ready[st], par2);
+        {
+            const uint16_t *v = s.V[st] + t0 * kD + c;
+            read16(s.b[k4] + t0, y);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] *= __uint_as_float((uint32_t)v[j * kD] << 16);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.vempty[st]));
+            if (left < 16) {
+                // rows behind the request's end are another request's, or none: whatever they hold counts for nothing
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = j < left ? y[j] : 0.f;
+            }
+            float f[16];
+            read16(s.bG[k4] + t0, f);
+            wait(s.done_k, par);
+            tmem_ld16(tm + kColDK + t0, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = fmaf(f[j], x[j], y[j]);
+        }
+        const Unit ux = unit_of(row_top(s.top[0], top_of(x)));
+        pieces2(x, ux.scale, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColX + 32 * piece + 8 * qt, w); });
+        tmem_st_wait();
+        warp_arrive(smem_u32(&s.have_x), lane);
+
+        // U, scaled for S' (S's pieces have been read: S q came before U), then for A
+        read16(s.m_unit[k4] + t0, y);
+        wait(s.done_u, par);
+        tmem_ld16(tm + kColU + t0, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] *= ux.back * y[j];
+        read16(s.tail[k4] + t0, y);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] *= x[j];
+        pieces3<8>(y, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColS + 32 * piece + 8 * qt, w); });
+        tmem_st_wait();
+        warp_arrive(smem_u32(&s.have_us), lane);
+        const Unit uu = unit_of(row_top(s.top[1], top_of(x)));
+        pieces2(x, uu.scale, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColUA + 32 * piece + 8 * qt, w); });
+        tmem_st_wait();
+        warp_arrive(smem_u32(&s.have_u), lane);
+
+        // S' = G_C S + U K
+        {
+            const float gc = s.G[k4][kC - 1];
+            wait(s.done_s, par);
+            float z[32];
+            tmem_read(tm + kColDK + 32 * qt, z);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[i] = fmaf(gc, S[i], z[i]);
+        }
+        if (ch + 1 < t.chunks)
+            put_state(S, [&] { wait(s.done_o, par); });
+        else
+            wait(s.done_o, par);
+        // o = G S q + U A
+        tmem_ld16(tm + kColDQ + t0, x);
+        tmem_ld16(tm + kColU + t0, y);
+        tmem_ld_wait();
+        warp_arrive(smem_u32(&s.read_o), lane);
+        {
+            float f[16];
+            read16(s.G[k4] + t0, f);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] *= f[j];
+            read16(s.a_unit[k4] + t0, f);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = fmaf(uu.back * f[j], y[j], x[j]);
+        }
+        float *dst = p.o + ((size_t)(t.row0 + ch * kC + t0) * p.H + h) * kD + c;
+        const size_t step = (size_t)p.H * kD;
+        if (left >= 16) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) dst[j * step] = x[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (j < left) dst[j * step] = x[j];
+        }
+    }
+    if (!*(volatile int32_t *)&s.abort) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4 *>(p.state + at + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// chunk warps
+// ---------------------------------------------------------------------------
+
+// Z = -/+ X Y of kN x kN blocks in shared memory, kR rows and four columns to a thread: rows kR * rt ..,
+// columns 4 * ct ..
+template <int kN, int kR, bool kNeg>
+__device__ __forceinline__ void block_product(const float *X, int xs, const float *Y, int ys, float *Z, int zs, int rt, int ct)
+{
+    const int r0 = kR * rt, c0 = 4 * ct;
+    float2 acc[kR][2] = {};
+#pragma unroll 2
+    for (int l = 0; l < kN; l += 4) {
+        float4 xr[kR], yr[4];
+#pragma unroll
+        for (int i = 0; i < kR; ++i) xr[i] = *reinterpret_cast<const float4 *>(X + (r0 + i) * xs + l);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) yr[e] = *reinterpret_cast<const float4 *>(Y + (l + e) * ys + c0);
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            const float xe[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = make_float2(xe[e], xe[e]);
+                acc[i][0] = __ffma2_rn(f, make_float2(yr[e].x, yr[e].y), acc[i][0]);
+                acc[i][1] = __ffma2_rn(f, make_float2(yr[e].z, yr[e].w), acc[i][1]);
+            }
+        }
+    }
+    const float f = kNeg ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < kR; ++i)
+        *reinterpret_cast<float4 *>(Z + (r0 + i) * zs + c0) =
+            make_float4(f * acc[i][0].x, f * acc[i][0].y, f * acc[i][1].x, f * acc[i][1].y);
+}
+
+// A lower-triangular block with ones on its diagonal, inverted in place by one warp, a column to a lane
+// (both halves of the warp the same): x_i = [i = j] - sum over l < i of L_il x_l
+__device__ __forceinline__ void invert16(float *B, int lane)
+{
+    const int col = lane & 15;
+    float x[16];
+#pragma unroll
+    for (int row = 0; row < 16; ++row) {
+        float acc[4] = {row == col ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int l = 0; l < row; l += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(B + row * kLS + l);
+            acc[0] = fmaf(-v.x, x[l], acc[0]);
+            if (l + 1 < row) acc[1] = fmaf(-v.y, x[l + 1], acc[1]);
+            if (l + 2 < row) acc[2] = fmaf(-v.z, x[l + 2], acc[2]);
+            if (l + 3 < row) acc[3] = fmaf(-v.w, x[l + 3], acc[3]);
+        }
+        x[row] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    }
+    __syncwarp();
+    if (lane < 16) {
+#pragma unroll
+        for (int row = 0; row < 16; ++row) B[row * kLS + col] = x[row];
+    }
+}
+
+// the two pieces of 16 values into row `row` of swizzled tiles, from column `col0` on (a multiple of 16)
+__device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, int col0, const float (&x)[16], float scale)
+{
+    pieces2(x, scale, [&](int piece, const uint32_t (&w)[8]) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<uint4 *>(tile[piece] + row * 128 + (((col0 / 8 + q) ^ (row & 7)) << 4)) =
+                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    });
+}
+
+__device__ __forceinline__ void chunk_warps(const PrefillParams &p, PrefillShared &s, const Tile &t, int h)
+{
+    const int tid = threadIdx.x - kChunk0, lane = tid & 31, warp = tid >> 5;
+    const int half = warp >> 2;                   // of the columns of k.k and q.k
+    const int i = (warp & 1) * 32 + lane;         // token of the chunk
+    const bool query = warp & 2;                  // this thread's row: k_i.k or q_i.k
+    const int key = (warp & 1) + 2 * half;        // number of a warp of key rows among those
+    const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;
+    // warp 3: k.k and q.k of a chunk whose rows have arrived.  Rows behind the request's end are another
+    // request's, or none: whatever they hold becomes zero.
+    auto products = [&](int ch) {
+        const int st = ch % kStages, valid = min(t.n - ch * kC, kC);
+        if (valid < kC) {
+            for (int e = lane; e < (kC - valid) * 16; e += 32) {
+                const int row = valid + (e >> 4), q = e & 15;
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                uint8_t *part = s.KQ[st] + (q >> 3) * (128 * 128);
+                *reinterpret_cast<uint4 *>(part + row * 128 + (q & 7) * 16) = z;
+                *reinterpret_cast<uint4 *>(part + (kC + row) * 128 + (q & 7) * 16) = z;
+            }
+            fence_async_shared();
+            __syncwarp();
+        }
+        tc_fence_after();
+        const uint32_t kq = smem_u32(s.KQ[st]);
+        if (elect_lane()) {
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const uint64_t x = smem_desc_sw128(kq + half * 128 * 128);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    tc_mma_ss(kColKK, x + (uint64_t)(ks * 2), x + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC), (uint32_t)(half | ks));
+            }
+            tc_commit(smem_u32(&s.bar_kk));
+        }
+        __syncwarp();
+    };
+    auto arrived = [&](int ch) { wait_for(s.full[ch % kStages], (ch / kStages) & 1, p, s); };
+    // the gate and the strength of this thread's token; 1 and 0 behind the end
+    float a, b;
+    auto gate = [&](int ch) {
+        const int row = ch * kC + i;
+        const size_t at = (size_t)(t.row0 + row) * p.H + h;
+        a = row < t.n ? p.alpha[at] : 1.f;
+        b = row < t.n ? p.beta[at] : 0.f;
+    };
+    gate(0);
+    if (warp == 3) {
+        arrived(0);
+        __syncwarp();
+        products(0);
+    }
+#pragma unroll 1
+    for (int ch = 0; ch < t.chunks; ++ch) {
+        const int st = ch & 1, k4 = ch & 3;
+        // products of the gates from this block of 32 tokens' start to token i, and from behind it to the block's end
+        float up = a, down = a;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, up, o), v = __shfl_down_sync(0xffffffffu, down, o);
+            if (lane >= o) up *= u;
+            if (lane + o < 32) down *= v;
+        }
+        down = __shfl_down_sync(0xffffffffu, down, 1);
+        if (lane == 31) down = 1.f;
+        const bool writes = !query && half == 0;  // of the four threads of token i
+        if (writes) {
+            s.next[(i + kC - 1) & (kC - 1)] = i ? a : 1.f;
+            if (lane == 31) s.gates[warp] = up;
+        }
+        named_bar(kBarChunk, kChunkThreads);
+        if (writes) {
+            const float g = i < 32 ? up : up * s.gates[0];
+            s.b[k4][i] = b;
+            s.G[k4][i] = g;
+            s.bG[k4][i] = -b * g;
+            s.tail[k4][i] = i < 32 ? down * s.gates[1] : down;
+        }
+        float d = query ? 1.f : b;                // D_ij (times b_i), from j = i down
+        if (half == 0 && i >= 32) d *= up;        // (from j = 31)
+        if (ch + 1 < t.chunks) gate(ch + 1);
+        wait_for(s.bar_kk, ch & 1, p, s);
+        tc_fence_after();
+        float x[2][16];
+        tmem_ld16(tm + kColKK + 32 * half, x[0]);
+        tmem_ld16(tm + kColKK + 32 * half + 16, x[1]);
+        tmem_ld_wait();
+        {
+            const int last = (query ? i : i - 1) - 32 * half, row = i - 32 * half;   // the row's last entry in this half
+#pragma unroll
+            for (int g = 7; g >= 0; --g) {
+                const float4 nx = *reinterpret_cast<const float4 *>(s.next + 32 * half + 4 * g);
+                const float f[4] = {nx.x, nx.y, nx.z, nx.w};
+#pragma unroll
+                for (int e = 3; e >= 0; --e) {
+                    const int j = 4 * g + e;
+                    if (j < 31) d *= j < row ? f[e] : 1.f;   // (j = 31: this half's first, or behind the block that d has)
+                    float &v = x[j >> 4][j & 15];
+                    v = j <= last ? v * d : 0.f;
+                }
+            }
+        }
+        float top = 0.f;
+        if (query) {
+            top = fmaxf(top_of(x[0]), top_of(x[1]));
+            s.a_top[half][i] = top;
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<float4 *>(s.L + i * kLS + 32 * half + 4 * q) =
+                    make_float4(x[q >> 2][4 * (q & 3)], x[q >> 2][4 * (q & 3) + 1], x[q >> 2][4 * (q & 3) + 2], x[q >> 2][4 * (q & 3) + 3]);
+        }
+        if (ch >= 2) wait_for(s.used[st], ((ch >> 1) & 1) ^ 1, p, s);
+        tc_fence_before();
+        named_bar(kBarChunk, kChunkThreads);
+        bool issued = false;
+        if (query) {
+            // the next chunk's products as soon as its rows are there
+            if (warp == 3 && ch + 1 < t.chunks) {
+                issued = __all_sync(0xffffffffu, mbar_test_wait(smem_u32(&s.full[(ch + 1) % kStages]), ((ch + 1) / kStages) & 1));
+                if (issued) products(ch + 1);
+            }
+            const Unit u = unit_of(fmaxf(top, s.a_top[half ^ 1][i]));
+            if (half == 0) s.a_unit[k4][i] = u.back;
+            put_row(s.A[st], i, 32 * half, x[0], u.scale);
+            put_row(s.A[st], i, 32 * half + 16, x[1], u.scale);
+        } else {
+            // M by blocks of 16, 32 and 64: M21 = -M22 (L21 M11)
+            invert16(s.L + key * 16 * (kLS + 1), lane);
+            named_bar(kBarKey, 128);
+            float *B = s.L + (key >> 1) * 32 * (kLS + 1), *T = s.T + (key >> 1) * 16 * kTS16;
+            const int tt = (key & 1) * 32 + lane;
+            block_product<16, 1, false>(B + 16 * kLS, kLS, B, kLS, T, kTS16, tt >> 2, tt & 3);
+            named_bar(kBarKey, 128);
+            block_product<16, 1, true>(B + 16 * (kLS + 1), kLS, T, kTS16, B + 16 * kLS, kLS, tt >> 2, tt & 3);
+        }
+        named_bar(kBarChunk, kChunkThreads);
+        block_product<32, 1, false>(s.L + 32 * kLS, kLS, s.L, kLS, s.T, kTS, tid >> 3, tid & 7);
+        named_bar(kBarChunk, kChunkThreads);
+        block_product<32, 1, true>(s.L + 32 * (kLS + 1), kLS, s.T, kTS, s.L + 32 * kLS, kLS, tid >> 3, tid & 7);
+        named_bar(kBarChunk, kChunkThreads);
+        {
+            const int row = tid >> 2, c0 = (tid & 3) * 16;
+            float m[16];
+            read16(s.L + row * kLS + c0, m);
+            float mt = top_of(m);
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+            const Unit u = unit_of(mt);
+            if (c0 == 0) s.m_unit[k4][row] = u.back;
+            put_row(s.M[st], row, c0, m, u.scale);
+        }
+        fence_async_shared();
+        warp_arrive(smem_u32(&s.ready[st]), lane);
+        if (warp == 3 && ch + 1 < t.chunks && !issued) {
+            arrived(ch + 1);
+            __syncwarp();
+            products(ch + 1);
+        }
+    }
+    if (warp == 3) {
+        if (elect_lane()) tc_commit(smem_u32(&s.last_kk));
+        drain(smem_u32(&s.last_kk), 0, p.timeout_ns);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the issuing warps
+// ---------------------------------------------------------------------------
+
+// The loops stay rolled: a product's few instructions are fetched once and run from the instruction
+// buffer, where straight-line code waits longer for its next line than for the tensor cores.
+__device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared &s, const Tile &t)
+{
+    bool ok = true;
+    auto wait = [&](unsigned long long &bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, p, s));
+        tc_fence_after();
+        return ok;
+    };
+    // two FP32 operands of two F16 pieces each, K = 64 tokens: high times high, high times low, low times high
+    auto pairs = [&](uint32_t a, const uint8_t *B) {
+        const uint64_t b0 = smem_desc_sw128(smem_u32(B));
+#pragma unroll 1
+        for (int q = 0; q < 3; ++q) {
+            const uint64_t b = b0 + (q == 1 ? kC * 128 / 16 : 0);
+            const uint32_t aq = a + (q == 2 ? 32 : 0);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) tc_mma_ts(kColU, aq + 8 * ks, b + (uint64_t)(ks * 2), kIdescF16, (uint32_t)(q | ks));
+        }
+    };
+#pragma unroll 1
+    for (int ch = 0; ch < t.chunks; ++ch) {
+        const int st = ch & 1, sk = ch % kStages;
+        const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
+        const uint32_t kq = smem_u32(s.KQ[sk]);
+        if (!wait(s.full[sk], (ch / kStages) & 1) || !wait(s.ready[st], par2) || !wait(s.have_s, par)) break;
+        // S k (rows 0..63 of the tile), then S q (rows 64..127) once the last chunk's outputs are read
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+            if (q && ch > 0 && !wait(s.read_o, par ^ 1u)) break;
+            if (elect_lane()) {
+                const uint32_t d = q ? kColDQ : kColDK;
+                const uint64_t b0 = smem_desc_sw128(kq + q * kC * 128);
+#pragma unroll 1
+                for (int half = 0; half < 6; ++half) {      // halves of the features, piece by piece
+                    const uint64_t b = b0 + (half & 1 ? 128 * 128 / 16 : 0);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        tc_mma_ts(d, kColS + 32 * half + 8 * ks, b + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC), (uint32_t)(half | ks));
+                }
+                if (q == 0) tc_commit(smem_u32(&s.done_k));
+            }
+            __syncwarp();
+        }
+        if (!wait(s.have_x, par)) break;
+        if (elect_lane()) {
+            pairs(kColX, s.M[st][0]);
+            tc_commit(smem_u32(&s.done_u));
+        }
+        __syncwarp();
+        if (!wait(s.have_us, par)) break;
+        if (elect_lane()) {
+            const uint64_t b = smem_desc_mn_sw128(kq, 128 * 128);
+#pragma unroll 1
+            for (int piece = 0; piece < 3; ++piece)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    tc_mma_ts(kColDK, kColS + 32 * piece + 8 * ks, b + (uint64_t)(ks * 16 * 128 / 16),
+                              idesc_bf16_f32(128, kD) | kBMnMajor, (uint32_t)(piece | ks));
+            tc_commit(smem_u32(&s.done_s));
+            tc_commit(smem_u32(&s.empty[sk]));
+        }
+        __syncwarp();
+        if (!wait(s.have_u, par)) break;
+        if (elect_lane()) {
+            pairs(kColUA, s.A[st][0]);
+            tc_commit(smem_u32(&s.done_o));
+            tc_commit(smem_u32(&s.used[st]));
+        }
+        __syncwarp();
+    }
+    if (elect_lane()) tc_commit(smem_u32(&s.last));
+    drain(smem_u32(&s.last), 0, p.timeout_ns);   // no product in flight when tensor memory is given back
+}
+
+__device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShared &s, const Tile &t, int h, const CUtensorMap &qmap,
+                                            const CUtensorMap &kmap, const CUtensorMap &vmap)
+{
+    const int hk = h / p.group;
+    const bool withheld = (p.debug_flags & 1) && blockIdx.x == 0 && blockIdx.y == 0;
+    int kq_issued = 0, v_issued = 0;
+    for (int ch = 0; ch < t.chunks; ++ch) {
+        const int sk = ch % kStages, sv = ch & 1, row = t.row0 + ch * kC;
+        const uint32_t kq_bar = smem_u32(&s.full[sk]), v_bar = smem_u32(&s.vfull[sv]), kq = smem_u32(s.KQ[sk]);
+        if (ch >= kStages && !wait_for(s.empty[sk], ((ch / kStages) & 1) ^ 1, p, s)) break;
+        mbar_expect_tx(kq_bar, kKqBytes);
+        if (withheld) break;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            tma_load_2d(kq + half * 128 * 128, &kmap, hk * kD + 64 * half, row, kq_bar);
+            tma_load_2d(kq + half * 128 * 128 + kC * 128, &qmap, hk * kD + 64 * half, row, kq_bar);
+        }
+        kq_issued = ch + 1;
+        if (ch >= 2 && !wait_for(s.vempty[sv], ((ch >> 1) & 1) ^ 1, p, s)) break;
+        mbar_expect_tx(v_bar, kVBytes);
+        tma_load_2d(smem_u32(s.V[sv]), &vmap, h * kD, row, v_bar);
+        v_issued = ch + 1;
+    }
+    // no copy into shared memory in flight at the end
+    for (int ch = max(kq_issued - kStages, 0); ch < kq_issued; ++ch)
+        drain(smem_u32(&s.full[ch % kStages]), (ch / kStages) & 1, p.timeout_ns);
+    for (int ch = max(v_issued - 2, 0); ch < v_issued; ++ch) drain(smem_u32(&s.vfull[ch & 1]), (ch >> 1) & 1, p.timeout_ns);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    k_gdn_prefill(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const PrefillParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    PrefillShared &s = *reinterpret_cast<PrefillShared *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int h = blockIdx.x, r = blockIdx.y;
+    const int o0 = p.off[r], o1 = p.off[r + 1];
+    if (o0 < 0 || o1 < o0 || o1 > p.n_rows) {
+        if (tid == 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
+        return;
+    }
+    const Tile t{o0, o1 - o0, (o1 - o0 + kC - 1) / kC};
+    if (t.n == 0) {
+        // no token: the state stays what it was
+        const size_t at = ((size_t)r * p.H + h) * kD * kD;
+        if (p.state != p.S0)
+            for (int e = tid; e < kD * kD / 4; e += kThreads)
+                reinterpret_cast<float4 *>(p.state + at)[e] =
+                    p.S0 ? reinterpret_cast<const float4 *>(p.S0 + at)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+        return;
+    }
+    if (tid == 0) {
+        for (int st = 0; st < kStages; ++st) {
+            mbar_init(smem_u32(&s.full[st]), 1);
+            mbar_init(smem_u32(&s.empty[st]), 1);
+        }
+        for (int st = 0; st < 2; ++st) {
+            mbar_init(smem_u32(&s.vfull[st]), 1);
+            mbar_init(smem_u32(&s.vempty[st]), kStateWarps);
+            mbar_init(smem_u32(&s.ready[st]), kChunkWarps);
+            mbar_init(smem_u32(&s.used[st]), 1);
+        }
+        for (unsigned long long *b : {&s.bar_kk, &s.done_k, &s.done_u, &s.done_s, &s.done_o, &s.last, &s.last_kk}) mbar_init(smem_u32(b), 1);
+        for (unsigned long long *b : {&s.have_s, &s.have_x, &s.have_us, &s.have_u, &s.read_o}) mbar_init(smem_u32(b), kStateWarps);
+        s.abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&qmap);
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
+    if (warp == 0) tmem_alloc(smem_u32(&s.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid < kChunk0) {
+        regs_inc<kRegsState>();
+
+    } else if (tid < kIssue0) {
+
+    } else {
+        regs_dec<kRegsIssue>();
+        if (warp == kIssue0 / 32) issue_warp(p, s, t);
+        
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(s.tmem, 512);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    if (!fn) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(f);
+    }
+    return fn;
+}
+
+}  // namespace
+
+namespace w12i {
+
+int launch_gdn_prefill(const GdnSeqArgs &a, void *stream)
+{
+    CUtensorMap maps[3] = {};
+    if (a.n_rows > 0) {
+        EncodeTiledFn enc = encode_fn();
+        if (!enc) return (int)cudaErrorNotSupported;
+        const uint16_t *src[3] = {a.q, a.k, a.v};
+        const int64_t stride[3] = {a.q_stride, a.k_stride, a.v_stride};
+        for (int i = 0; i < 3; ++i) {
+            const cuuint64_t dims[2] = {(cuuint64_t)(i < 2 ? a.Hk : a.H) * kD, (cuuint64_t)a.n_rows};
+            const cuuint64_t strides[1] = {(cuuint64_t)stride[i] * 2};
+            const cuuint32_t box[2] = {i < 2 ? 64u : (cuuint32_t)kD, (cuuint32_t)kC}, estr[2] = {1, 1};
+            if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(src[i]), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, i < 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return (int)cudaErrorInvalidValue;
+        }
+    }
+    static std::atomic<int> known{0};
+    int regs = known.load(std::memory_order_relaxed);
+    if (regs == 0) {
+        cudaFuncAttributes attr{};
+        const cudaError_t e = cudaFuncGetAttributes(&attr, k_gdn_prefill);
+        if (e != cudaSuccess) return (int)e;
+        known.store(regs = attr.numRegs, std::memory_order_relaxed);
+    }
+    if (regs < kRegsLaunch) return (int)cudaErrorInvalidConfiguration;   // the register shares need that many
+    PrefillParams p{};
+    p.S0 = a.S0;
+    p.state = a.state;
+    p.o = a.o;
+    p.alpha = a.alpha;
+    p.beta = a.beta;
+    p.off = a.off;
+    p.H = a.H;
+    p.group = a.H / a.Hk;
+    p.n_rows = a.n_rows;
+    p.timeout_ns = (uint32_t)std::min<uint64_t>(a.timeout_ns, 1u << 31);
+    p.status = a.status;
+    p.debug_flags = a.debug_flags;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.H, a.n_req);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(PrefillShared) + 1024;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = cudaFuncSetAttribute(k_gdn_prefill, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return (int)e;
+    return (int)cudaLaunchKernelEx(&cfg, k_gdn_prefill, maps[0], maps[1], maps[2], p);
+}
+
+}  // namespace w12i
