@@ -15,20 +15,23 @@
 // One CTA to a (request, head); the state rows c lie on the 128 lanes of tensor
 // memory throughout, so that all its products take their left operand from
 // there and no operand but M and A is ever written to shared memory:
-//     D_K[c][j] = S k_j    D_Q[c][j] = S q_j    U[c][i] = X M^T    U A^T    S' += U K.
+//     D_K[c][j] = S k_j    D_Q[c][j] = S q_j    U[c][i] = X M^T    U A^T    S' = U K.
 // Products with keys and queries take those as they are and the FP32 side (S, U) as three BF16
 // pieces that add up to it exactly: two (2^-17) would be the largest error of the layer by
 // far.  Products of two FP32 sides (X M^T, U A^T) take both as two F16 pieces (2^-22) under a power of two
 // for each row, and of their four pairs all but the smallest.  All accumulation is FP32.
 //
-// Twenty-eight warps (many, with few columns each: a chunk runs through every role's code once, and
-// the time goes into fetching that code, which warps in step share):
-//  * state warps (0..15; four threads to a state row, each with a quarter of the
-//    columns; S itself stays in their registers) turn accumulators into operands,
-//  * chunk warps (16..23; two threads to a row of k.k or q.k) make M and A of the next chunk: k.k and q.k on
-//    the tensor cores, then the inverse, of four 16 x 16 blocks by columns and of the
-//    blocks below them from those,
-//  * warp 24 issues the state warps' products, warp 25 the copies by TMA.
+// A chunk runs through S's pieces -> S k -> X -> U -> U's pieces -> U K -> S', each step of which waits for the one before
+// it; the rest (A, M, U A^T and the outputs) is other warps' work, a chunk ahead or beside it:
+//  * state warps (0..7; two threads to a state row): S, which stays in their registers, and U scaled for S',
+//  * token warps (8..15; two threads to a state row): X, U for A, and the outputs,
+//  * gate warps (16..19; a thread to a row of k.k or q.k): the gates' products, L and A,
+//  * inverse warps (20..23): M from L, by four 16 x 16 blocks whose columns are solved in registers and
+//    the blocks below them from those,
+//  * warp 24 issues the products with the state, warp 25 the copies by TMA.
+// What a chunk takes is the warps' instructions, not the products (a quarter of its time): of those the cutting into
+// pieces, three BF16 pieces 11 cycles of a scheduler for two values of 32 lanes, two F16 pieces 5.  The products are issued
+// in rolled loops and the code is kept short: straight-line code of a few times this length spent half its time on its own way in.
 // Every wait is bounded: a wait that runs out sets s.abort, which ends every
 // other wait at once, so all roles run to their ends; the state is then left
 // unwritten.
@@ -47,35 +50,33 @@ namespace {
 
 constexpr int kD = 128;             // head dimension
 constexpr int kC = 64;              // tokens of a chunk
-constexpr int kStateWarps = 16, kChunkWarps = 8;
-constexpr int kChunkThreads = 32 * kChunkWarps;
-constexpr int kThreads = 32 * (kStateWarps + kChunkWarps + 4);
-constexpr int kChunk0 = 32 * kStateWarps, kIssue0 = kChunk0 + kChunkThreads;   // the roles' first threads
-constexpr int kRegsLaunch = 72, kRegsState = 80, kRegsIssue = 40;             // (chunk warps keep the launch's)
-static_assert(kChunk0 * kRegsState + kChunkThreads * kRegsLaunch + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register shares");
+constexpr int kThreads = 32 * 28;
+// the roles' first threads, and their registers (the launch's where they are equal to it)
+constexpr int kToken0 = 256, kGate0 = 512, kInv0 = 640, kIssue0 = 768;
+constexpr int kRegsLaunch = 72, kRegsState = 104, kRegsGate = 64, kRegsInv = 56, kRegsIssue = 32;
+static_assert(256 * (kRegsState + kRegsLaunch) + 128 * (kRegsGate + kRegsInv + kRegsIssue) <= kThreads * kRegsLaunch, "register shares");
 
 // tensor memory columns: all 512 are one CTA's, from column 0 on
-constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; later three of U for S', 32 each,
-constexpr uint32_t kColUA = 128;    // and, on the last of them, two of U for A
+constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; then three of U for S', 32 each,
+constexpr uint32_t kColUA = 128;    // and U A, over the last piece
 constexpr uint32_t kColDQ = 192;    // S q
 constexpr uint32_t kColDK = 256;    // S k; then, with the next 64 columns, U K
-constexpr uint32_t kColX = 320;     // X's two pieces
-constexpr uint32_t kColU = 384;     // U; then U A
+constexpr uint32_t kColU = 320;     // U
+constexpr uint32_t kColX = 384;     // X's two pieces, then U's two for A
 constexpr uint32_t kColKK = 448;    // k.k (lanes 0..63) and q.k (lanes 64..127) of the next chunk
 
 constexpr int kLS = 68;             // FP32 row stride of L and M (16-byte rows, 4 banks apart)
 constexpr int kTS = 36, kTS16 = 20; // and of products in between, of 32 and 16 columns
-constexpr int kBarChunk = 1;        // named barrier of the chunk warps
-constexpr int kBarRow = 2;          // of the four warps of 32 state rows (2 .. 5)
-constexpr int kBarKey = 6;          // and of the four chunk warps with key rows
+constexpr int kBarGate = 1, kBarInv = 6;   // named barriers of the gate and of the inverse warps
+constexpr int kBarRow = 2;                 // and of the two token warps of 32 state rows (2 .. 5)
 constexpr int kStages = 3;          // of keys and queries (their chunk is prepared while two others are in use)
 
 struct PrefillShared {
     uint8_t KQ[kStages][2 * 128 * 128];   // [stage][feature half][key rows, query rows][64 BF16], 128-byte swizzle
-    uint8_t M[2][2][kC * 128];      // pieces of M and A, rows of 64 F16, 128-byte swizzle
-    uint8_t A[2][2][kC * 128];
+    uint8_t A[2][2][kC * 128];      // pieces of A and M, rows of 64 F16, 128-byte swizzle
+    uint8_t M[2][kC * 128];
     uint16_t V[2][kC * kD];
-    alignas(16) float L[kC * kLS];
+    alignas(16) float L[2][kC * kLS];   // then, in place, M
     alignas(16) float T[32 * kTS];
     alignas(16) float next[kC];     // the gates of tokens 1 .. 63, then 1
     alignas(16) float b[4][kC];     // of chunk c in [c % 4]: strengths, -b_i G_i, G_i, D_Ci
@@ -84,19 +85,22 @@ struct PrefillShared {
     alignas(16) float tail[4][kC];
     alignas(16) float m_unit[4][kC];   // and the powers of two of the rows of M and of A
     alignas(16) float a_unit[4][kC];
-    float top[2][kStateWarps / 4][kD];   // [X, U][part] largest magnitude of a state row's values
-    float a_top[2][kC];             // and of a row of A, by halves
-    float gates[2];                 // products of the gates of tokens 0 .. 31 and 32 .. 63
+    float top[2][2][kD];            // [X, U][half of the tokens] largest magnitude of a state row's values
+    float x_back[kD];               // powers of two of X's rows
+    float gates[2], grow[2];        // products of the gates of tokens 0 .. 31 and 32 .. 63, and of those above 1
     unsigned long long full[kStages], empty[kStages];   // keys and queries
     unsigned long long vfull[2], vempty[2];             // values
-    unsigned long long ready[2], used[2];               // M, A and the gates' products; M and A have been read
+    unsigned long long gready[2], gused[2];             // A and the gates' products are there; A has been read
+    unsigned long long lready[2], lfree[2];             // L is there; M has been taken from it
+    unsigned long long mready[2];                       // M is there (two barriers for one M: a waiter may be a phase late)
     unsigned long long bar_kk;
-    unsigned long long have_s, have_x, have_us, have_u, read_o;   // to the issuing warp: operands written, outputs read
-    unsigned long long done_k, done_u, done_s, done_o;            // from it: products done
+    unsigned long long have_s, have_x, have_us, have_u, read_u, read_o;   // operands written, U and the outputs read
+    unsigned long long done_k, done_u, done_s, done_o;  // products done
     unsigned long long last, last_kk;
     uint32_t tmem;
     int32_t abort;
 };
+static_assert(offsetof(PrefillShared, L) % 16 == 0 && sizeof(PrefillShared::L) % 32 == 0, "rows of four floats");
 static_assert(sizeof(PrefillShared) + 1024 <= 227 * 1024, "shared memory above the per-CTA limit");
 static_assert(offsetof(PrefillShared, M) % 1024 == 0 && offsetof(PrefillShared, A) % 1024 == 0, "swizzled tiles");
 static_assert(offsetof(PrefillShared, V) % 128 == 0 && offsetof(PrefillShared, full) % 8 == 0, "copies and barriers");
@@ -122,16 +126,6 @@ template <int N>
 __device__ __forceinline__ void regs_dec()
 {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
 }
 
 // D[tmem] (+)= A[smem] * B[smem]
@@ -177,10 +171,10 @@ __device__ __forceinline__ void pieces3(float (&x)[2 * N], F put)
         uint32_t w[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const uint32_t b0 = __float_as_uint(x[2 * i]), b1 = __float_as_uint(x[2 * i + 1]);
-            w[i] = __byte_perm(b0, b1, 0x7632);
+            w[i] = __byte_perm(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]), 0x7632);
             if (piece < 2) {
-                const float2 r = __ffma2_rn(make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u)),
+                // (the shift runs beside the logic operations, so taking both halves from the word is a fifth faster)
+                const float2 r = __ffma2_rn(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)),
                                             make_float2(-1.f, -1.f), make_float2(x[2 * i], x[2 * i + 1]));
                 x[2 * i] = r.x;
                 x[2 * i + 1] = r.y;
@@ -247,15 +241,6 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8
                  : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N])
-{
-    if constexpr (N == 8)
-        tmem_st_x8(taddr, r);
-    else
-        tmem_st_x16(taddr, r);
-}
-
 // 32 lanes x N columns as floats (complete after tmem_ld_wait)
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&x)[N])
@@ -270,6 +255,14 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&x)[N])
               "=f"(x[i + 13]), "=f"(x[i + 14]), "=f"(x[i + 15])
             : "r"(taddr + i)
             : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&x)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "r"(taddr)
+                 : "memory");
 }
 
 // N values of shared memory, the same ones for every lane
@@ -359,155 +352,385 @@ struct Tile {
 // state warps
 // ---------------------------------------------------------------------------
 
-constexpr int kParts = kStateWarps / 4;   // threads of a state row
-constexpr int kT = kC / kParts;           // tokens of a thread
-constexpr int kF = kD / kParts;           // features of a thread
-
 __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShared &s, const Tile &t, int r, int h)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 2;
-    const int c = (warp & 3) * 32 + lane, t0 = kT * part;                 // state row, first token
+    const int c = (warp & 3) * 32 + lane;                                 // state row
     const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;                // this warp's lanes
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
         wait_for(bar, parity, p, s);
         tc_fence_after();
     };
-    // the largest of `top` here and in the threads with the other parts of the columns
-    auto row_top = [&](float (&at)[kParts][kD], float top) {
-        at[part][c] = top;
-        named_bar(kBarRow + (warp & 3), 32 * kParts);
+    const size_t at = (((size_t)r * p.H + h) * kD + c) * kD + 64 * part;  // this thread's half of the row
+    float S[64];
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) top = fmaxf(top, at[i][c]);
-        return top;
-    };
-    const size_t at = (((size_t)r * p.H + h) * kD + c) * kD + kF * part;  // this thread's part of the row
-    float S[kF];
-#pragma unroll
-    for (int i = 0; i < kF / 4; ++i) {
+    for (int i = 0; i < 16; ++i) {
         const float4 x = p.S0 ? *reinterpret_cast<const float4 *>(p.S0 + at + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
         S[4 * i] = x.x;
         S[4 * i + 1] = x.y;
         S[4 * i + 2] = x.z;
         S[4 * i + 3] = x.w;
     }
-    float u_back = 0.f;
-    // (one pass more than there are chunks: the last chunk's outputs come in the pass behind it)
 #pragma unroll 1
-    for (int ch = 0;; ++ch) {
-        const int st = ch & 1, k4 = ch & 3;
+    for (int ch = 0; ch < t.chunks; ++ch) {
+        const int k4 = ch & 3;
         const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
-        float x[kT], y[kT];
-        if (ch < t.chunks) {
-            // S's pieces; the last one's columns may still hold U's pieces for A
+        // S's pieces; the last one's columns may still hold the last chunk's U A
+        if (ch > 0) wait(s.read_o, par ^ 1u);
 #pragma unroll
-            for (int q = 0; q < kF / 32; ++q) {
-                float z[32];
+        for (int q = 0; q < 4; ++q) {
+            float z[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = S[32 * q + i];
-                pieces3<16>(z, [&](int piece, const uint32_t (&w)[16]) {
-                    if (piece == 2 && q == 0 && ch > 0) wait(s.done_o, par ^ 1u);
-                    tmem_st<16>(tm + kColS + 64 * piece + kF / 2 * part + 16 * q, w);
-                });
-            }
-            tmem_st_wait();
-            warp_arrive(smem_u32(&s.have_s), lane);
-        } else {
-            wait(s.done_o, par ^ 1u);
+            for (int i = 0; i < 16; ++i) z[i] = S[16 * q + i];
+            pieces3<8>(z, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColS + 64 * piece + 32 * part + 8 * q, w); });
         }
-        if (ch > 0) {
-            // the last chunk's outputs: o = G S q + U A
-            const int ko = (ch - 1) & 3, left = t.n - (ch - 1) * kC - t0;
-            tmem_ld<kT>(tm + kColDQ + t0, x);
-            tmem_ld<kT>(tm + kColU + t0, y);
-            tmem_ld_wait();
-            warp_arrive(smem_u32(&s.read_o), lane);
-            float f[kT];
-            read_n(s.G[ko] + t0, f);
-            mul_n(x, f);
-            read_n(s.a_unit[ko] + t0, f);
-            scale_n(f, u_back);
-            fma_n(f, y, x);              // x += f y
-            float *dst = p.o + ((size_t)(t.row0 + (ch - 1) * kC + t0) * p.H + h) * kD + c;
-            const size_t step = (size_t)p.H * kD;
-#pragma unroll
-            for (int j = 0; j < kT; ++j) {
-                if (j < left) *dst = x[j];
-                dst += step;
-            }
-        }
-        if (ch == t.chunks) break;
-        // X = b (v - G S k)
-        wait(s.vfull[st], par2);
-        wait(s.ready[st], par2);
-        {
-            const int left = t.n - ch * kC - t0;
-            const uint16_t *v = s.V[st] + t0 * kD + c;
-            float f[kT];
-            read_n(s.b[k4] + t0, f);
-#pragma unroll
-            for (int j = 0; j < kT; ++j) y[j] = __uint_as_float((uint32_t)v[j * kD] << 16);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s.vempty[st]));
-            if (left < kT) {
-                // rows behind the request's end are another request's, or none: whatever they hold counts for nothing
-#pragma unroll
-                for (int j = 0; j < kT; ++j) y[j] = j < left ? y[j] : 0.f;
-            }
-            mul_n(y, f);
-            read_n(s.bG[k4] + t0, f);
-            wait(s.done_k, par);
-            tmem_ld<kT>(tm + kColDK + t0, x);
-            tmem_ld_wait();
-            fma_n(f, x, y);              // y += f x
-        }
-        const Unit ux = unit_of(row_top(s.top[0], top_of(y)));
-        pieces2(y, ux.scale, [&](int piece, const uint32_t (&w)[kT / 2]) { tmem_st<kT / 2>(tm + kColX + 32 * piece + kT / 2 * part, w); });
         tmem_st_wait();
-        warp_arrive(smem_u32(&s.have_x), lane);
+        warp_arrive(smem_u32(&s.have_s), lane);
 
-        // U, scaled for S' (S's pieces have been read: S q came before U), then for A
-        read_n(s.m_unit[k4] + t0, y);
-        scale_n(y, ux.back);
+        // U scaled for S', over S's pieces (which have been read: S q came before U)
+        wait(s.gready[ch & 1], par2);
+        wait(s.mready[ch & 1], par2);
+        wait(s.have_x, par);
+        const float back = s.x_back[c];
         wait(s.done_u, par);
-        tmem_ld<kT>(tm + kColU + t0, x);
-        tmem_ld_wait();
-        mul_n(x, y);
-        read_n(s.tail[k4] + t0, y);
-        mul_n(y, x);
-        pieces3<kT / 2>(y, [&](int piece, const uint32_t (&w)[kT / 2]) { tmem_st<kT / 2>(tm + kColS + 32 * piece + kT / 2 * part, w); });
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int t0 = 32 * part + 16 * q;
+            float x[16], f[16];
+            tmem_ld<16>(tm + kColU + t0, x);
+            read_n(s.m_unit[k4] + t0, f);
+            scale_n(f, back);
+            tmem_ld_wait();
+            mul_n(x, f);
+            read_n(s.tail[k4] + t0, f);
+            mul_n(x, f);
+            pieces3<8>(x, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColS + 32 * piece + t0 / 2, w); });
+        }
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_us), lane);
-        const Unit uu = unit_of(row_top(s.top[1], top_of(x)));
-        u_back = uu.back;
-        pieces2(x, uu.scale, [&](int piece, const uint32_t (&w)[kT / 2]) { tmem_st<kT / 2>(tm + kColUA + 32 * piece + kT / 2 * part, w); });
-        tmem_st_wait();
-        warp_arrive(smem_u32(&s.have_u), lane);
 
         // S' = G_C S + U K
         const float gc = s.G[k4][kC - 1];
         wait(s.done_s, par);
 #pragma unroll
-        for (int q = 0; q < kF / 32; ++q) {
-            float z[32];
-            tmem_ld<32>(tm + kColDK + kF * part + 32 * q, z);
+        for (int q = 0; q < 4; ++q) {
+            float z[16];
+            tmem_ld<16>(tm + kColDK + 64 * part + 16 * q, z);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                const float2 n = __ffma2_rn(make_float2(gc, gc), make_float2(S[32 * q + i], S[32 * q + i + 1]), make_float2(z[i], z[i + 1]));
-                S[32 * q + i] = n.x;
-                S[32 * q + i + 1] = n.y;
+            for (int i = 0; i < 16; i += 2) {
+                const float2 n = __ffma2_rn(make_float2(gc, gc), make_float2(S[16 * q + i], S[16 * q + i + 1]), make_float2(z[i], z[i + 1]));
+                S[16 * q + i] = n.x;
+                S[16 * q + i + 1] = n.y;
             }
         }
     }
     if (!*(volatile int32_t *)&s.abort) {
 #pragma unroll
-        for (int i = 0; i < kF / 4; ++i)
+        for (int i = 0; i < 16; ++i)
             *reinterpret_cast<float4 *>(p.state + at + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
     }
 }
 
 // ---------------------------------------------------------------------------
-// chunk warps
+// token warps
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShared &s, const Tile &t, int h)
+{
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x - kToken0) >> 5, part = warp >> 2;
+    const int c = (warp & 3) * 32 + lane, t0 = 32 * part;                 // state row, first token
+    const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;
+    auto wait = [&](unsigned long long &bar, uint32_t parity) {
+        wait_for(bar, parity, p, s);
+        tc_fence_after();
+    };
+    // the unit for the larger of `top` here and in the thread with the other half of the tokens
+    auto row_unit = [&](float (&at)[2][kD], float top) {
+        at[part][c] = top;
+        named_bar(kBarRow + (warp & 3), 64);
+        return unit_of(fmaxf(top, at[part ^ 1][c]));
+    };
+    // two pieces of 32 values, for X or for U
+    auto put = [&](const float (&x)[32], float scale) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float z[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] = x[16 * q + i];
+            pieces2(z, scale, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColX + 32 * piece + 16 * part + 8 * q, w); });
+        }
+        tmem_st_wait();
+    };
+#pragma unroll 1
+    for (int ch = 0; ch < t.chunks; ++ch) {
+        const int st = ch & 1, k4 = ch & 3, left = t.n - ch * kC - t0;
+        const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
+        float x[32];
+        // X = b (v - G S k)
+        wait(s.vfull[st], par2);
+        wait(s.gready[st], par2);
+        {
+            const uint16_t *v = s.V[st] + t0 * kD + c;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float((uint32_t)v[j * kD] << 16);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.vempty[st]));
+            if (left < 32) {
+                // rows behind the request's end are another request's, or none: whatever they hold counts for nothing
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = j < left ? x[j] : 0.f;
+            }
+            float f[32];
+            read_n(s.b[k4] + t0, f);
+            mul_n(x, f);
+        }
+        wait(s.done_k, par);
+        float top = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float d[8], f[8];
+            tmem_ld8(tm + kColDK + t0 + 8 * q, d);
+            read_n(s.bG[k4] + t0 + 8 * q, f);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const int i = 8 * q + j;
+                const float2 y = __ffma2_rn(make_float2(f[j], f[j + 1]), make_float2(d[j], d[j + 1]), make_float2(x[i], x[i + 1]));
+                x[i] = y.x;
+                x[i + 1] = y.y;
+                top = fmaxf(fmaxf(top, fabsf(y.x)), fabsf(y.y));
+            }
+        }
+        const Unit ux = row_unit(s.top[0], top);
+        if (part == 0) s.x_back[c] = ux.back;
+        put(x, ux.scale);
+        warp_arrive(smem_u32(&s.have_x), lane);
+
+        // U's pieces for A, over X's
+        wait(s.mready[st], par2);
+        wait(s.done_u, par);
+        tmem_ld<32>(tm + kColU + t0, x);
+        tmem_ld_wait();
+        warp_arrive(smem_u32(&s.read_u), lane);
+        top = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float f[8];
+            read_n(s.m_unit[k4] + t0 + 8 * q, f);
+            scale_n(f, ux.back);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const int i = 8 * q + j;
+                const float2 y = __fmul2_rn(make_float2(f[j], f[j + 1]), make_float2(x[i], x[i + 1]));
+                x[i] = y.x;
+                x[i + 1] = y.y;
+                top = fmaxf(fmaxf(top, fabsf(y.x)), fabsf(y.y));
+            }
+        }
+        const Unit uu = row_unit(s.top[1], top);
+        put(x, uu.scale);
+        warp_arrive(smem_u32(&s.have_u), lane);
+
+        // o = G S q + U A
+        wait(s.done_o, par);
+        tmem_ld<32>(tm + kColDQ + t0, x);
+        tmem_ld_wait();
+        float *dst = p.o + ((size_t)(t.row0 + ch * kC + t0) * p.H + h) * kD + c;
+        const size_t step = (size_t)p.H * kD;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float d[8], f[8], g[8];
+            tmem_ld8(tm + kColUA + t0 + 8 * q, d);
+            read_n(s.G[k4] + t0 + 8 * q, f);
+            read_n(s.a_unit[k4] + t0 + 8 * q, g);
+            scale_n(g, uu.back);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[8 * q + j] = fmaf(f[j], x[8 * q + j], g[j] * d[j]);
+        }
+        warp_arrive(smem_u32(&s.read_o), lane);
+        if (left >= 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                *dst = x[j];
+                dst += step;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                if (j < left) *dst = x[j];
+                dst += step;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gate warps
+// ---------------------------------------------------------------------------
+
+// the two pieces of 16 values into row `row` of swizzled tiles, from column `col0` on (a multiple of 16)
+__device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, int col0, const float (&x)[16], float scale)
+{
+    pieces2(x, scale, [&](int piece, const uint32_t (&w)[8]) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<uint4 *>(tile[piece] + row * 128 + (((col0 / 8 + q) ^ (row & 7)) << 4)) =
+                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    });
+}
+
+__device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared &s, const Tile &t, int h)
+{
+    const int tid = threadIdx.x - kGate0, lane = tid & 31, warp = tid >> 5;
+    const int i = tid & 63;                       // token of the chunk
+    const bool query = warp >= 2;                 // this thread's row: k_i.k or q_i.k
+    const int blocks = (warp & 1) ? 4 : 2;        // of 16 columns that its warp's rows reach into
+    const uint32_t tm = (uint32_t)(warp * 32) << 16;
+    // warp 3: k.k and q.k of a chunk whose rows have arrived.  Rows behind the request's end are another
+    // request's, or none: whatever they hold becomes zero.
+    auto products = [&](int ch) {
+        const int st = ch % kStages, valid = min(t.n - ch * kC, kC);
+        wait_for(s.full[st], (ch / kStages) & 1, p, s);
+        __syncwarp();
+        if (valid < kC) {
+#pragma unroll 1
+            for (int e = lane; e < (kC - valid) * 16; e += 32) {
+                const int row = valid + (e >> 4), q = e & 15;
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                uint8_t *half = s.KQ[st] + (q >> 3) * (128 * 128);
+                *reinterpret_cast<uint4 *>(half + row * 128 + (q & 7) * 16) = z;
+                *reinterpret_cast<uint4 *>(half + (kC + row) * 128 + (q & 7) * 16) = z;
+            }
+            fence_async_shared();
+            __syncwarp();
+        }
+        tc_fence_after();
+        const uint32_t kq = smem_u32(s.KQ[st]);
+        if (elect_lane()) {
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const uint64_t x = smem_desc_sw128(kq + half * 128 * 128);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    tc_mma_ss(kColKK, x + (uint64_t)(ks * 2), x + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC), (uint32_t)(half | ks));
+            }
+            tc_commit(smem_u32(&s.bar_kk));
+        }
+        __syncwarp();
+    };
+    // the gate and the strength of this thread's token; 1 and 0 behind the end
+    float a, b;
+    auto gate = [&](int ch) {
+        const int row = ch * kC + i;
+        const size_t at = (size_t)(t.row0 + row) * p.H + h;
+        a = row < t.n ? p.alpha[at] : 1.f;
+        b = row < t.n ? p.beta[at] : 0.f;
+    };
+    gate(0);
+    if (warp == 3) products(0);
+#pragma unroll 1
+    for (int ch = 0; ch < t.chunks; ++ch) {
+        const int st = ch & 1, k4 = ch & 3;
+        const uint32_t par2 = (ch >> 1) & 1;
+        const float strength = b;
+        float up = a, down = a, grow = fmaxf(a, 1.f);
+        if (!query) {
+            // products of the gates from this block of 32 tokens' start to token i, and from behind it to the block's
+            // end; and of those above 1, which bound the D_ij
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, up, o), v = __shfl_down_sync(0xffffffffu, down, o);
+                grow *= __shfl_xor_sync(0xffffffffu, grow, o);
+                if (lane >= o) up *= u;
+                if (lane + o < 32) down *= v;
+            }
+            down = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 31) down = 1.f;
+            s.next[(i + kC - 1) & (kC - 1)] = i ? a : 1.f;
+            if (lane == 31) {
+                s.gates[warp] = up;
+                s.grow[warp] = grow;
+            }
+        }
+        named_bar(kBarGate, 128);
+        if (ch + 1 < t.chunks) gate(ch + 1);
+        if (!query) {
+            const float g = i < 32 ? up : up * s.gates[0];
+            s.b[k4][i] = strength;
+            s.G[k4][i] = g;
+            s.bG[k4][i] = -strength * g;
+            s.tail[k4][i] = i < 32 ? down * s.gates[1] : down;
+        }
+        wait_for(s.bar_kk, ch & 1, p, s);
+        tc_fence_after();
+        Unit u{1.f, 1.f};
+        if (query) {
+            // A's unit, from a bound of the row: |q_i.k_j| times what the gates can add
+            float top = 0.f;
+#pragma unroll 1
+            for (int J = 0; J < blocks; ++J) {
+                float x[16];
+                tmem_ld<16>(tm + kColKK + 16 * J, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) top = fmaxf(top, 16 * J + j <= i ? fabsf(x[j]) : 0.f);
+            }
+            u = unit_of(top * s.grow[0] * s.grow[1]);
+            if (ch >= 2) wait_for(s.gused[st], par2 ^ 1u, p, s);
+            s.a_unit[k4][i] = u.back;
+        } else if (ch >= 2) {
+            wait_for(s.lfree[st], par2 ^ 1u, p, s);
+        }
+        float d = query ? 1.f : strength;         // D_ij (times b_i), from j = i down
+        const int last = query ? i : i - 1;       // the row's last entry
+#pragma unroll 1
+        for (int J = blocks - 1; J >= 0; --J) {
+            float x[16], f[16];
+            tmem_ld<16>(tm + kColKK + 16 * J, x);
+            read_n(s.next + 16 * J, f);
+            tmem_ld_wait();
+            if (J >= blocks - 2) {                // columns among which this warp's diagonals lie
+#pragma unroll
+                for (int j = 15; j >= 0; --j) {
+                    d *= 16 * J + j < i ? f[j] : 1.f;
+                    x[j] = 16 * J + j <= last ? x[j] * d : 0.f;
+                }
+            } else {
+#pragma unroll
+                for (int j = 15; j >= 0; --j) {
+                    d *= f[j];
+                    x[j] *= d;
+                }
+            }
+            if (query) {
+                put_row(s.A[st], i, 16 * J, x, u.scale);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<float4 *>(s.L[st] + i * kLS + 16 * J + 4 * q) =
+                        make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            }
+        }
+        if (query) {
+            fence_async_shared();
+        } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.lready[st]));
+        }
+        warp_arrive(smem_u32(&s.gready[st]), lane);
+        named_bar(kBarGate, 128);                 // k.k and q.k have been read
+        if (warp == 3 && ch + 1 < t.chunks) products(ch + 1);
+    }
+    if (warp == 3) {
+        if (elect_lane()) tc_commit(smem_u32(&s.last_kk));
+        drain(s.last_kk, 0, p);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// inverse warps
 // ---------------------------------------------------------------------------
 
 // Z = -/+ X Y of kN x kN blocks in shared memory, kR rows and four columns to a thread: rows kR * rt ..,
@@ -568,176 +791,54 @@ __device__ __forceinline__ void invert16(float *B, int lane)
     }
 }
 
-// the two pieces of 16 values into row `row` of swizzled tiles, from column `col0` on (a multiple of 16)
-__device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, int col0, const float (&x)[16], float scale)
+__device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillShared &s, const Tile &t)
 {
-    pieces2(x, scale, [&](int piece, const uint32_t (&w)[8]) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-            *reinterpret_cast<uint4 *>(tile[piece] + row * 128 + (((col0 / 8 + q) ^ (row & 7)) << 4)) =
-                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-    });
-}
-
-__device__ __forceinline__ void chunk_warps(const PrefillParams &p, PrefillShared &s, const Tile &t, int h)
-{
-    const int tid = threadIdx.x - kChunk0, lane = tid & 31, warp = tid >> 5;
-    const int half = warp >> 2;                   // of the columns of k.k and q.k
-    const int i = (warp & 1) * 32 + lane;         // token of the chunk
-    const bool query = warp & 2;                  // this thread's row: k_i.k or q_i.k
-    const int key = (warp & 1) + 2 * half;        // number of a warp of key rows among those
-    const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;
-    // warp 3: k.k and q.k of a chunk whose rows have arrived.  Rows behind the request's end are another
-    // request's, or none: whatever they hold becomes zero.
-    auto products = [&](int ch) {
-        const int st = ch % kStages, valid = min(t.n - ch * kC, kC);
-        if (valid < kC) {
-#pragma unroll 1
-            for (int e = lane; e < (kC - valid) * 16; e += 32) {
-                const int row = valid + (e >> 4), q = e & 15;
-                const uint4 z = make_uint4(0, 0, 0, 0);
-                uint8_t *part = s.KQ[st] + (q >> 3) * (128 * 128);
-                *reinterpret_cast<uint4 *>(part + row * 128 + (q & 7) * 16) = z;
-                *reinterpret_cast<uint4 *>(part + (kC + row) * 128 + (q & 7) * 16) = z;
-            }
-            fence_async_shared();
-            __syncwarp();
-        }
-        tc_fence_after();
-        const uint32_t kq = smem_u32(s.KQ[st]);
-        if (elect_lane()) {
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                const uint64_t x = smem_desc_sw128(kq + half * 128 * 128);
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    tc_mma_ss(kColKK, x + (uint64_t)(ks * 2), x + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC), (uint32_t)(half | ks));
-            }
-            tc_commit(smem_u32(&s.bar_kk));
-        }
-        __syncwarp();
-    };
-    auto arrived = [&](int ch) { wait_for(s.full[ch % kStages], (ch / kStages) & 1, p, s); };
-    // the gate and the strength of this thread's token; 1 and 0 behind the end
-    float a, b;
-    auto gate = [&](int ch) {
-        const int row = ch * kC + i;
-        const size_t at = (size_t)(t.row0 + row) * p.H + h;
-        a = row < t.n ? p.alpha[at] : 1.f;
-        b = row < t.n ? p.beta[at] : 0.f;
-    };
-    gate(0);
-    if (warp == 3) {
-        arrived(0);
-        __syncwarp();
-        products(0);
-    }
+    const int tid = threadIdx.x - kInv0, lane = tid & 31, warp = tid >> 5;
 #pragma unroll 1
     for (int ch = 0; ch < t.chunks; ++ch) {
         const int st = ch & 1, k4 = ch & 3;
-        // products of the gates from this block of 32 tokens' start to token i, and from behind it to the block's end
-        float up = a, down = a;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float u = __shfl_up_sync(0xffffffffu, up, o), v = __shfl_down_sync(0xffffffffu, down, o);
-            if (lane >= o) up *= u;
-            if (lane + o < 32) down *= v;
-        }
-        down = __shfl_down_sync(0xffffffffu, down, 1);
-        if (lane == 31) down = 1.f;
-        const bool writes = !query && half == 0;  // of the four threads of token i
-        if (writes) {
-            s.next[(i + kC - 1) & (kC - 1)] = i ? a : 1.f;
-            if (lane == 31) s.gates[warp] = up;
-        }
-        named_bar(kBarChunk, kChunkThreads);
-        if (writes) {
-            const float g = i < 32 ? up : up * s.gates[0];
-            s.b[k4][i] = b;
-            s.G[k4][i] = g;
-            s.bG[k4][i] = -b * g;
-            s.tail[k4][i] = i < 32 ? down * s.gates[1] : down;
-        }
-        float d = query ? 1.f : b;                // D_ij (times b_i), from j = i down
-        if (half == 0 && i >= 32) d *= up;        // (from j = 31)
-        if (ch + 1 < t.chunks) gate(ch + 1);
-        wait_for(s.bar_kk, ch & 1, p, s);
-        tc_fence_after();
-        float x[2][16];
-        tmem_ld<16>(tm + kColKK + 32 * half, x[0]);
-        tmem_ld<16>(tm + kColKK + 32 * half + 16, x[1]);
-        tmem_ld_wait();
+        float *L = s.L[st];
+        wait_for(s.lready[st], (ch >> 1) & 1, p, s);
+        // M by blocks of 16, 32 and 64: M21 = -M22 (L21 M11)
+        invert16(L + warp * 16 * (kLS + 1), lane);
+        named_bar(kBarInv, 128);
         {
-            const int last = (query ? i : i - 1) - 32 * half, row = i - 32 * half;   // the row's last entry in this half
-#pragma unroll
-            for (int g = 7; g >= 0; --g) {
-                const float4 nx = *reinterpret_cast<const float4 *>(s.next + 32 * half + 4 * g);
-                const float f[4] = {nx.x, nx.y, nx.z, nx.w};
-#pragma unroll
-                for (int e = 3; e >= 0; --e) {
-                    const int j = 4 * g + e;
-                    if (j < 31) d *= j < row ? f[e] : 1.f;   // (j = 31: this half's first, or behind the block that d has)
-                    float &v = x[j >> 4][j & 15];
-                    v = j <= last ? v * d : 0.f;
-                }
-            }
-        }
-        float top = 0.f;
-        if (query) {
-            top = fmaxf(top_of(x[0]), top_of(x[1]));
-            s.a_top[half][i] = top;
-        } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                *reinterpret_cast<float4 *>(s.L + i * kLS + 32 * half + 4 * q) =
-                    make_float4(x[q >> 2][4 * (q & 3)], x[q >> 2][4 * (q & 3) + 1], x[q >> 2][4 * (q & 3) + 2], x[q >> 2][4 * (q & 3) + 3]);
-        }
-        if (ch >= 2) wait_for(s.used[st], ((ch >> 1) & 1) ^ 1, p, s);
-        tc_fence_before();
-        named_bar(kBarChunk, kChunkThreads);
-        // the next chunk's products: its rows have mostly arrived, and the warps of the query rows have time
-        if (warp == 3 && ch + 1 < t.chunks) {
-            arrived(ch + 1);
-            __syncwarp();
-            products(ch + 1);
-        }
-        if (query) {
-            const Unit u = unit_of(fmaxf(top, s.a_top[half ^ 1][i]));
-            if (half == 0) s.a_unit[k4][i] = u.back;
-            put_row(s.A[st], i, 32 * half, x[0], u.scale);
-            put_row(s.A[st], i, 32 * half + 16, x[1], u.scale);
-        } else {
-            // M by blocks of 16, 32 and 64: M21 = -M22 (L21 M11)
-            invert16(s.L + key * 16 * (kLS + 1), lane);
-            named_bar(kBarKey, 128);
-            float *B = s.L + (key >> 1) * 32 * (kLS + 1), *T = s.T + (key >> 1) * 16 * kTS16;
-            const int tt = (key & 1) * 32 + lane;
+            float *B = L + (warp >> 1) * 32 * (kLS + 1), *T = s.T + (warp >> 1) * 16 * kTS16;
+            const int tt = tid & 63;
             block_product<16, 1, false>(B + 16 * kLS, kLS, B, kLS, T, kTS16, tt >> 2, tt & 3);
-            named_bar(kBarKey, 128);
+            named_bar(kBarInv, 128);
             block_product<16, 1, true>(B + 16 * (kLS + 1), kLS, T, kTS16, B + 16 * kLS, kLS, tt >> 2, tt & 3);
         }
-        named_bar(kBarChunk, kChunkThreads);
-        block_product<32, 1, false>(s.L + 32 * kLS, kLS, s.L, kLS, s.T, kTS, tid >> 3, tid & 7);
-        named_bar(kBarChunk, kChunkThreads);
-        block_product<32, 1, true>(s.L + 32 * (kLS + 1), kLS, s.T, kTS, s.L + 32 * kLS, kLS, tid >> 3, tid & 7);
-        named_bar(kBarChunk, kChunkThreads);
-        {
-            const int row = tid >> 2, c0 = (tid & 3) * 16;
-            float m[16];
-            read_n(s.L + row * kLS + c0, m);
-            float mt = top_of(m);
-            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-            const Unit u = unit_of(mt);
-            if (c0 == 0) s.m_unit[k4][row] = u.back;
-            put_row(s.M[st], row, c0, m, u.scale);
+        named_bar(kBarInv, 128);
+        block_product<32, 2, false>(L + 32 * kLS, kLS, L, kLS, s.T, kTS, tid >> 3, tid & 7);
+        named_bar(kBarInv, 128);
+        block_product<32, 2, true>(L + 32 * (kLS + 1), kLS, s.T, kTS, L + 32 * kLS, kLS, tid >> 3, tid & 7);
+        named_bar(kBarInv, 128);
+        // the last chunk's M has been read
+        if (ch > 0) wait_for(s.done_u, (ch & 1) ^ 1u, p, s);
+        // M's pieces, eight columns to a thread and turn: the upper rows' left half, then 16 lower rows at a time
+#pragma unroll 1
+        for (int q = 0; q < 3; ++q) {
+            const int row = q == 0 ? tid >> 2 : 16 + 16 * q + (tid >> 3), col = (q == 0 ? tid & 3 : tid & 7) * 8;
+            float x[8];
+            read_n(L + row * kLS + col, x);
+            float top = top_of(x);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float other = __shfl_xor_sync(0xffffffffu, top, 4);
+            if (q) top = fmaxf(top, other);
+            const Unit u = unit_of(top);
+            if (col == 0) s.m_unit[k4][row] = u.back;
+            pieces2(x, u.scale, [&](int piece, const uint32_t (&w)[4]) {
+                *reinterpret_cast<uint4 *>(s.M[piece] + row * 128 + (((col >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            });
         }
         fence_async_shared();
-        warp_arrive(smem_u32(&s.ready[st]), lane);
-    }
-    if (warp == 3) {
-        if (elect_lane()) tc_commit(smem_u32(&s.last_kk));
-        drain(s.last_kk, 0, p);
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&s.mready[st]));
+            mbar_arrive(smem_u32(&s.lfree[st]));
+        }
     }
 }
 
@@ -756,14 +857,14 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
         return ok;
     };
     // two FP32 operands of two F16 pieces each, K = 64 tokens: high times high, high times low, low times high
-    auto pairs = [&](uint32_t a, const uint8_t *B) {
+    auto pairs = [&](uint32_t d, const uint8_t *B) {
         const uint64_t b0 = smem_desc_sw128(smem_u32(B));
 #pragma unroll 1
         for (int q = 0; q < 3; ++q) {
             const uint64_t b = b0 + (q == 1 ? kC * 128 / 16 : 0);
-            const uint32_t aq = a + (q == 2 ? 32 : 0);
+            const uint32_t a = kColX + (q == 2 ? 32 : 0);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) tc_mma_ts(kColU, aq + 8 * ks, b + (uint64_t)(ks * 2), kIdescF16, (uint32_t)(q | ks));
+            for (int ks = 0; ks < 4; ++ks) tc_mma_ts(d, a + 8 * ks, b + (uint64_t)(ks * 2), kIdescF16, (uint32_t)(q | ks));
         }
     };
 #pragma unroll 1
@@ -771,7 +872,7 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
         const int st = ch & 1, sk = ch % kStages;
         const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
         const uint32_t kq = smem_u32(s.KQ[sk]);
-        if (!wait(s.full[sk], (ch / kStages) & 1) || !wait(s.ready[st], par2) || !wait(s.have_s, par)) break;
+        if (!wait(s.full[sk], (ch / kStages) & 1) || !wait(s.gready[st], par2) || !wait(s.have_s, par)) break;
         // S k (rows 0..63 of the tile), then S q (rows 64..127) once the last chunk's outputs are read
 #pragma unroll 1
         for (int q = 0; q < 2; ++q) {
@@ -790,13 +891,13 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
             }
             __syncwarp();
         }
-        if (!wait(s.have_x, par)) break;
+        if (!wait(s.mready[st], par2) || !wait(s.have_x, par)) break;
         if (elect_lane()) {
-            pairs(kColX, s.M[st][0]);
+            pairs(kColU, s.M[0]);
             tc_commit(smem_u32(&s.done_u));
         }
         __syncwarp();
-        if (!wait(s.have_us, par)) break;
+        if (!wait(s.read_u, par) || !wait(s.have_us, par)) break;
         if (elect_lane()) {
             const uint64_t b = smem_desc_mn_sw128(kq, 128 * 128);
 #pragma unroll 1
@@ -813,7 +914,7 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
         if (elect_lane()) {
             pairs(kColUA, s.A[st][0]);
             tc_commit(smem_u32(&s.done_o));
-            tc_commit(smem_u32(&s.used[st]));
+            tc_commit(smem_u32(&s.gused[st]));
         }
         __syncwarp();
     }
@@ -880,12 +981,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int st = 0; st < 2; ++st) {
             mbar_init(smem_u32(&s.vfull[st]), 1);
-            mbar_init(smem_u32(&s.vempty[st]), kStateWarps);
-            mbar_init(smem_u32(&s.ready[st]), kChunkWarps);
-            mbar_init(smem_u32(&s.used[st]), 1);
+            mbar_init(smem_u32(&s.vempty[st]), 8);
+            mbar_init(smem_u32(&s.gready[st]), 4);
+            mbar_init(smem_u32(&s.gused[st]), 1);
+            mbar_init(smem_u32(&s.lready[st]), 2);
+            mbar_init(smem_u32(&s.lfree[st]), 4);
+            mbar_init(smem_u32(&s.mready[st]), 4);
         }
         for (unsigned long long *b : {&s.bar_kk, &s.done_k, &s.done_u, &s.done_s, &s.done_o, &s.last, &s.last_kk}) mbar_init(smem_u32(b), 1);
-        for (unsigned long long *b : {&s.have_s, &s.have_x, &s.have_us, &s.have_u, &s.read_o}) mbar_init(smem_u32(b), kStateWarps);
+        for (unsigned long long *b : {&s.have_s, &s.have_x, &s.have_us, &s.have_u, &s.read_u, &s.read_o}) mbar_init(smem_u32(b), 8);
         s.abort = 0;
         fence_mbar_init();
         prefetch_tmap(&qmap);
@@ -893,14 +997,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&vmap);
     }
     if (warp == 0) tmem_alloc(smem_u32(&s.tmem), 512);
+    // what no chunk writes and every chunk reads: the entries above the diagonal blocks of 32
+    for (int e = tid; e < 32 * 8; e += kThreads) {
+        const int row = e >> 3, q = e & 7;
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        for (int st = 0; st < 2; ++st) *reinterpret_cast<uint4 *>(s.L[st] + row * kLS + 32 + 4 * q) = z;
+        if (q < 4) {
+            const int at = row * 128 + (((4 + q) ^ (row & 7)) << 4);
+            for (int piece = 0; piece < 2; ++piece) {
+                *reinterpret_cast<uint4 *>(s.M[piece] + at) = z;
+                for (int st = 0; st < 2; ++st) *reinterpret_cast<uint4 *>(s.A[st][piece] + at) = z;
+            }
+        }
+    }
+    fence_async_shared();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid < kChunk0) {
+    if (tid < kToken0) {
         regs_inc<kRegsState>();
         state_warps(p, s, t, r, h);
+    } else if (tid < kGate0) {
+        token_warps(p, s, t, h);
+    } else if (tid < kInv0) {
+        regs_dec<kRegsGate>();
+        gate_warps(p, s, t, h);
     } else if (tid < kIssue0) {
-        chunk_warps(p, s, t, h);
+        regs_dec<kRegsInv>();
+        inverse_warps(p, s, t);
     } else {
         regs_dec<kRegsIssue>();
         if (warp == kIssue0 / 32) issue_warp(p, s, t);
