@@ -57,9 +57,8 @@ constexpr int kRegsLaunch = 72, kRegsState = 104, kRegsGate = 64, kRegsInv = 56,
 static_assert(256 * (kRegsState + kRegsLaunch) + 128 * (kRegsGate + kRegsInv + kRegsIssue) <= kThreads * kRegsLaunch, "register shares");
 
 // tensor memory columns: all 512 are one CTA's, from column 0 on
-constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; then three of U for S', 32 each,
-constexpr uint32_t kColUA = 128;    // and U A, over the last piece
-constexpr uint32_t kColDQ = 192;    // S q
+constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; then three of U for S', 32 each
+constexpr uint32_t kColDQ = 192;    // S q; then, scaled and with U A added, the outputs
 constexpr uint32_t kColDK = 256;    // S k; then, with the next 64 columns, U K
 constexpr uint32_t kColU = 320;     // U
 constexpr uint32_t kColX = 384;     // X's two pieces, then U's two for A
@@ -67,7 +66,7 @@ constexpr uint32_t kColKK = 448;    // k.k (lanes 0..63) and q.k (lanes 64..127)
 
 constexpr int kLS = 68;             // FP32 row stride of L and M (16-byte rows, 4 banks apart)
 constexpr int kTS = 36, kTS16 = 20; // and of products in between, of 32 and 16 columns
-constexpr int kBarGate = 1, kBarInv = 6;   // named barriers of the gate and of the inverse warps
+constexpr int kBarGate = 1, kBarInv = 6, kBarQuery = 7;   // named barriers of the gate and of the inverse warps, of the gate warps' latter two
 constexpr int kBarRow = 2;                 // and of the two token warps of 32 state rows (2 .. 5)
 constexpr int kStages = 3;          // of keys and queries (their chunk is prepared while two others are in use)
 
@@ -83,10 +82,12 @@ struct PrefillShared {
     alignas(16) float bG[4][kC];
     alignas(16) float G[4][kC];
     alignas(16) float tail[4][kC];
-    alignas(16) float m_unit[4][kC];   // and the powers of two of the rows of M and of A
-    alignas(16) float a_unit[4][kC];
-    float top[2][2][kD];            // [X, U][half of the tokens] largest magnitude of a state row's values
+    alignas(16) float m_unit[4][kC];   // the powers of two of M's rows, and D_Ci times them
+    alignas(16) float m_tail[4][kC];
+    float top[2][2][kD];            // [X, S q][half of the tokens] largest magnitude of a state row's values
     float x_back[kD];               // powers of two of X's rows
+    float a_top[2], a_back[4];      // largest magnitude of A's rows by halves, its power of two
+    uint32_t m_top[4];              // largest magnitude in M, as its bits
     float gates[2], grow[2];        // products of the gates of tokens 0 .. 31 and 32 .. 63, and of those above 1
     unsigned long long full[kStages], empty[kStages];   // keys and queries
     unsigned long long vfull[2], vempty[2];             // values
@@ -94,8 +95,9 @@ struct PrefillShared {
     unsigned long long lready[2], lfree[2];             // L is there; M has been taken from it
     unsigned long long mready[2];                       // M is there (two barriers for one M: a waiter may be a phase late)
     unsigned long long bar_kk;
-    unsigned long long have_s, have_x, have_us, have_u, read_u, read_o;   // operands written, U and the outputs read
-    unsigned long long done_k, done_u, done_s, done_o;  // products done
+    unsigned long long have_s[2], have_us[2], have_x, have_u;   // operands written (S and U for S' by halves)
+    unsigned long long read_u, read_o;                  // U and the outputs have been read
+    unsigned long long done_k, done_q, done_u, done_s, done_o;  // products done
     unsigned long long last, last_kk;
     uint32_t tmem;
     int32_t abort;
@@ -218,16 +220,15 @@ __device__ __forceinline__ float top_of(const float (&x)[N])
     return top;
 }
 
-// The two F16 pieces of scaled values, rounded to nearest: what is left is 2^-22 of a value
+// The two F16 pieces of values below 2^15, rounded to nearest: what is left is 2^-22 of a value
 template <int N, class F>
-__device__ __forceinline__ void pieces2(const float (&x)[N], float scale, F put)
+__device__ __forceinline__ void pieces2(const float (&x)[N], F put)
 {
     uint32_t hi[N / 2], lo[N / 2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-        const float2 y = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(scale, scale));
-        hi[i] = pack_f16x2(y.x, y.y);
-        const float2 r = __ffma2_rn(unpack_f16x2(hi[i]), make_float2(-1.f, -1.f), y);
+        hi[i] = pack_f16x2(x[2 * i], x[2 * i + 1]);
+        const float2 r = __ffma2_rn(unpack_f16x2(hi[i]), make_float2(-1.f, -1.f), make_float2(x[2 * i], x[2 * i + 1]));
         lo[i] = pack_f16x2(r.x, r.y);
     }
     put(0, hi);
@@ -375,17 +376,18 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
     for (int ch = 0; ch < t.chunks; ++ch) {
         const int k4 = ch & 3;
         const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
-        // S's pieces; the last one's columns may still hold the last chunk's U A
-        if (ch > 0) wait(s.read_o, par ^ 1u);
+        // S's pieces, a half of this thread's features at a time
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             float z[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) z[i] = S[16 * q + i];
             pieces3<8>(z, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColS + 64 * piece + 32 * part + 8 * q, w); });
+            if (q & 1) {
+                tmem_st_wait();
+                warp_arrive(smem_u32(&s.have_s[q >> 1]), lane);
+            }
         }
-        tmem_st_wait();
-        warp_arrive(smem_u32(&s.have_s), lane);
 
         // U scaled for S', over S's pieces (which have been read: S q came before U)
         wait(s.gready[ch & 1], par2);
@@ -398,16 +400,14 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
             const int t0 = 32 * part + 16 * q;
             float x[16], f[16];
             tmem_ld<16>(tm + kColU + t0, x);
-            read_n(s.m_unit[k4] + t0, f);
+            read_n(s.m_tail[k4] + t0, f);
             scale_n(f, back);
             tmem_ld_wait();
             mul_n(x, f);
-            read_n(s.tail[k4] + t0, f);
-            mul_n(x, f);
             pieces3<8>(x, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColS + 32 * piece + t0 / 2, w); });
+            tmem_st_wait();
+            warp_arrive(smem_u32(&s.have_us[q]), lane);
         }
-        tmem_st_wait();
-        warp_arrive(smem_u32(&s.have_us), lane);
 
         // S' = G_C S + U K
         const float gc = s.G[k4][kC - 1];
@@ -445,20 +445,20 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         wait_for(bar, parity, p, s);
         tc_fence_after();
     };
-    // the unit for the larger of `top` here and in the thread with the other half of the tokens
-    auto row_unit = [&](float (&at)[2][kD], float top) {
+    // the larger of `top` here and in the thread with the other half of the tokens
+    auto row_top = [&](float (&at)[2][kD], float top) {
         at[part][c] = top;
         named_bar(kBarRow + (warp & 3), 64);
-        return unit_of(fmaxf(top, at[part ^ 1][c]));
+        return fmaxf(top, at[part ^ 1][c]);
     };
     // two pieces of 32 values, for X or for U
-    auto put = [&](const float (&x)[32], float scale) {
+    auto put = [&](const float (&x)[32]) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             float z[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) z[i] = x[16 * q + i];
-            pieces2(z, scale, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColX + 32 * piece + 16 * part + 8 * q, w); });
+            pieces2(z, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColX + 32 * piece + 16 * part + 8 * q, w); });
         }
         tmem_st_wait();
     };
@@ -502,23 +502,22 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
                 top = fmaxf(fmaxf(top, fabsf(y.x)), fabsf(y.y));
             }
         }
-        const Unit ux = row_unit(s.top[0], top);
+        const Unit ux = unit_of(row_top(s.top[0], top));
         if (part == 0) s.x_back[c] = ux.back;
-        put(x, ux.scale);
+        scale_n(x, ux.scale);
+        put(x);
         warp_arrive(smem_u32(&s.have_x), lane);
 
-        // U's pieces for A, over X's
-        wait(s.mready[st], par2);
-        wait(s.done_u, par);
-        tmem_ld<32>(tm + kColU + t0, x);
-        tmem_ld_wait();
-        warp_arrive(smem_u32(&s.read_u), lane);
+        // S q to where U A is added to it: G S q in the units of U and A.  U's unit is a bound, at most 64 |M| |X|
+        // (F16 has 16 bits to spare under the largest value), and one under which S q keeps finite.
+        wait(s.done_q, par);
+        tmem_ld<32>(tm + kColDQ + t0, x);
         top = 0.f;
+        tmem_ld_wait();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             float f[8];
-            read_n(s.m_unit[k4] + t0 + 8 * q, f);
-            scale_n(f, ux.back);
+            read_n(s.G[k4] + t0 + 8 * q, f);
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
                 const int i = 8 * q + j;
@@ -528,28 +527,52 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
                 top = fmaxf(fmaxf(top, fabsf(y.x)), fabsf(y.y));
             }
         }
-        const Unit uu = row_unit(s.top[1], top);
-        put(x, uu.scale);
+        const float a_back = s.a_back[k4];
+        const float a_scale = __uint_as_float(0x7F000000u - __float_as_uint(a_back));   // 1 / a_back
+        top = row_top(s.top[1], top) * 0x1p-60f * a_scale;
+        wait(s.mready[st], par2);
+        const Unit uu = unit_of(fmaxf(top, ux.back * 0x1p20f * __uint_as_float(s.m_top[k4])));
+        scale_n(x, uu.scale);
+        scale_n(x, a_scale);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[8 * q + j]);
+            tmem_st_x8(tm + kColDQ + t0 + 8 * q, w);
+        }
+
+        // U's pieces for A, over X's
+        wait(s.done_u, par);
+        tmem_ld<32>(tm + kColU + t0, x);
+        tmem_ld_wait();
+        warp_arrive(smem_u32(&s.read_u), lane);
+        const float unit = ux.back * uu.scale;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float f[8];
+            read_n(s.m_unit[k4] + t0 + 8 * q, f);
+            scale_n(f, unit);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const int i = 8 * q + j;
+                const float2 y = __fmul2_rn(make_float2(f[j], f[j + 1]), make_float2(x[i], x[i + 1]));
+                x[i] = y.x;
+                x[i + 1] = y.y;
+            }
+        }
+        put(x);
         warp_arrive(smem_u32(&s.have_u), lane);
 
         // o = G S q + U A
         wait(s.done_o, par);
         tmem_ld<32>(tm + kColDQ + t0, x);
         tmem_ld_wait();
+        warp_arrive(smem_u32(&s.read_o), lane);
+        scale_n(x, uu.back);
+        scale_n(x, a_back);
         float *dst = p.o + ((size_t)(t.row0 + ch * kC + t0) * p.H + h) * kD + c;
         const size_t step = (size_t)p.H * kD;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float d[8], f[8], g[8];
-            tmem_ld8(tm + kColUA + t0 + 8 * q, d);
-            read_n(s.G[k4] + t0 + 8 * q, f);
-            read_n(s.a_unit[k4] + t0 + 8 * q, g);
-            scale_n(g, uu.back);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[8 * q + j] = fmaf(f[j], x[8 * q + j], g[j] * d[j]);
-        }
-        warp_arrive(smem_u32(&s.read_o), lane);
         if (left >= 32) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -571,9 +594,9 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
 // ---------------------------------------------------------------------------
 
 // the two pieces of 16 values into row `row` of swizzled tiles, from column `col0` on (a multiple of 16)
-__device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, int col0, const float (&x)[16], float scale)
+__device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, int col0, const float (&x)[16])
 {
-    pieces2(x, scale, [&](int piece, const uint32_t (&w)[8]) {
+    pieces2(x, [&](int piece, const uint32_t (&w)[8]) {
 #pragma unroll
         for (int q = 0; q < 2; ++q)
             *reinterpret_cast<uint4 *>(tile[piece] + row * 128 + (((col0 / 8 + q) ^ (row & 7)) << 4)) =
@@ -667,7 +690,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         tc_fence_after();
         Unit u{1.f, 1.f};
         if (query) {
-            // A's unit, from a bound of the row: |q_i.k_j| times what the gates can add
+            // A's unit, from a bound: |q_i.k_j| times what the gates can add
             float top = 0.f;
 #pragma unroll 1
             for (int J = 0; J < blocks; ++J) {
@@ -677,13 +700,16 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
 #pragma unroll
                 for (int j = 0; j < 16; ++j) top = fmaxf(top, 16 * J + j <= i ? fabsf(x[j]) : 0.f);
             }
-            u = unit_of(top * s.grow[0] * s.grow[1]);
+            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+            if (lane == 0) s.a_top[warp & 1] = __uint_as_float(most);
+            named_bar(kBarQuery, 64);
+            u = unit_of(fmaxf(s.a_top[0], s.a_top[1]) * s.grow[0] * s.grow[1]);
             if (ch >= 2) wait_for(s.gused[st], par2 ^ 1u, p, s);
-            s.a_unit[k4][i] = u.back;
+            if (tid == 64) s.a_back[k4] = u.back;
         } else if (ch >= 2) {
             wait_for(s.lfree[st], par2 ^ 1u, p, s);
         }
-        float d = query ? 1.f : strength;         // D_ij (times b_i), from j = i down
+        float d = query ? u.scale : strength;     // D_ij (in A's unit, or times b_i), from j = i down
         const int last = query ? i : i - 1;       // the row's last entry
 #pragma unroll 1
         for (int J = blocks - 1; J >= 0; --J) {
@@ -705,7 +731,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
                 }
             }
             if (query) {
-                put_row(s.A[st], i, 16 * J, x, u.scale);
+                put_row(s.A[st], i, 16 * J, x);
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -816,6 +842,7 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
         named_bar(kBarInv, 128);
         // the last chunk's M has been read
         if (ch > 0) wait_for(s.done_u, (ch & 1) ^ 1u, p, s);
+        if (tid == 0) s.m_top[(ch + 1) & 3] = 0;
         // M's pieces, eight columns to a thread and turn: the upper rows' left half, then 16 lower rows at a time
 #pragma unroll 1
         for (int q = 0; q < 3; ++q) {
@@ -828,8 +855,14 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
             const float other = __shfl_xor_sync(0xffffffffu, top, 4);
             if (q) top = fmaxf(top, other);
             const Unit u = unit_of(top);
-            if (col == 0) s.m_unit[k4][row] = u.back;
-            pieces2(x, u.scale, [&](int piece, const uint32_t (&w)[4]) {
+            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+            if (lane == 0) atomicMax(&s.m_top[k4], most);
+            if (col == 0) {
+                s.m_unit[k4][row] = u.back;
+                s.m_tail[k4][row] = u.back * s.tail[k4][row];
+            }
+            scale_n(x, u.scale);
+            pieces2(x, [&](int piece, const uint32_t (&w)[4]) {
                 *reinterpret_cast<uint4 *>(s.M[piece] + row * 128 + (((col >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             });
         }
@@ -857,14 +890,14 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
         return ok;
     };
     // two FP32 operands of two F16 pieces each, K = 64 tokens: high times high, high times low, low times high
-    auto pairs = [&](uint32_t d, const uint8_t *B) {
+    auto pairs = [&](uint32_t d, const uint8_t *B, uint32_t add) {
         const uint64_t b0 = smem_desc_sw128(smem_u32(B));
 #pragma unroll 1
         for (int q = 0; q < 3; ++q) {
             const uint64_t b = b0 + (q == 1 ? kC * 128 / 16 : 0);
             const uint32_t a = kColX + (q == 2 ? 32 : 0);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) tc_mma_ts(d, a + 8 * ks, b + (uint64_t)(ks * 2), kIdescF16, (uint32_t)(q | ks));
+            for (int ks = 0; ks < 4; ++ks) tc_mma_ts(d, a + 8 * ks, b + (uint64_t)(ks * 2), kIdescF16, add | (uint32_t)(q | ks));
         }
     };
 #pragma unroll 1
@@ -872,47 +905,65 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
         const int st = ch & 1, sk = ch % kStages;
         const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
         const uint32_t kq = smem_u32(s.KQ[sk]);
-        if (!wait(s.full[sk], (ch / kStages) & 1) || !wait(s.gready[st], par2) || !wait(s.have_s, par)) break;
-        // S k (rows 0..63 of the tile), then S q (rows 64..127) once the last chunk's outputs are read
+        if (!wait(s.full[sk], (ch / kStages) & 1) || !wait(s.gready[st], par2)) break;
+        // S times the keys (rows 0..63 of the tile) or the queries (64..127), 32 features and a piece of S at a time: both
+        // threads' first half of the features, then the second
+        auto product = [&](uint32_t d, uint32_t row0, int half) {
+            const uint64_t b0 = smem_desc_sw128(kq + row0 * 128) + (uint64_t)(half * 4);
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-            if (q && ch > 0 && !wait(s.read_o, par ^ 1u)) break;
-            if (elect_lane()) {
-                const uint32_t d = q ? kColDQ : kColDK;
-                const uint64_t b0 = smem_desc_sw128(kq + q * kC * 128);
-#pragma unroll 1
-                for (int half = 0; half < 6; ++half) {      // halves of the features, piece by piece
-                    const uint64_t b = b0 + (half & 1 ? 128 * 128 / 16 : 0);
+            for (int q = 0; q < 6; ++q) {
+                const int piece = q >> 1, part = q & 1;
+                const uint64_t b = b0 + (part ? 128 * 128 / 16 : 0);
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        tc_mma_ts(d, kColS + 32 * half + 8 * ks, b + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC), (uint32_t)(half | ks));
-                }
-                if (q == 0) tc_commit(smem_u32(&s.done_k));
+                for (int ks = 0; ks < 2; ++ks)
+                    tc_mma_ts(d, kColS + 64 * piece + 32 * part + 16 * half + 8 * ks, b + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC),
+                              (uint32_t)(half | q | ks));
             }
-            __syncwarp();
+        };
+        if (!wait(s.have_s[0], par)) break;
+        if (elect_lane()) product(kColDK, 0, 0);
+        __syncwarp();
+        if (!wait(s.have_s[1], par)) break;
+        if (elect_lane()) {
+            product(kColDK, 0, 1);
+            tc_commit(smem_u32(&s.done_k));
         }
+        __syncwarp();
+        if (ch > 0 && !wait(s.read_o, par ^ 1u)) break;
+        if (elect_lane()) {
+            product(kColDQ, kC, 0);
+            product(kColDQ, kC, 1);
+            tc_commit(smem_u32(&s.done_q));
+        }
+        __syncwarp();
         if (!wait(s.mready[st], par2) || !wait(s.have_x, par)) break;
         if (elect_lane()) {
-            pairs(kColU, s.M[0]);
+            pairs(kColU, s.M[0], 0);
             tc_commit(smem_u32(&s.done_u));
         }
         __syncwarp();
-        if (!wait(s.read_u, par) || !wait(s.have_us, par)) break;
-        if (elect_lane()) {
-            const uint64_t b = smem_desc_mn_sw128(kq, 128 * 128);
+        if (!wait(s.read_u, par)) break;
 #pragma unroll 1
-            for (int piece = 0; piece < 3; ++piece)
+        for (int half = 0; half < 2; ++half) {
+            if (!wait(s.have_us[half], par)) break;
+            if (elect_lane()) {
+                const uint64_t b = smem_desc_mn_sw128(kq, 128 * 128) + (uint64_t)(half * 16 * 128 / 16);
+#pragma unroll 1
+                for (int piece = 0; piece < 3; ++piece)
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    tc_mma_ts(kColDK, kColS + 32 * piece + 8 * ks, b + (uint64_t)(ks * 16 * 128 / 16),
-                              idesc_bf16_f32(128, kD) | kBMnMajor, (uint32_t)(piece | ks));
-            tc_commit(smem_u32(&s.done_s));
-            tc_commit(smem_u32(&s.empty[sk]));
+                    for (int ks = 0; ks < 2; ++ks)
+                        tc_mma_ts(kColDK, kColS + 32 * piece + 8 * half + 16 * ks, b + (uint64_t)(ks * 32 * 128 / 16),
+                                  idesc_bf16_f32(128, kD) | kBMnMajor, (uint32_t)(half | piece | ks));
+                if (half) {
+                    tc_commit(smem_u32(&s.done_s));
+                    tc_commit(smem_u32(&s.empty[sk]));
+                }
+            }
+            __syncwarp();
         }
-        __syncwarp();
         if (!wait(s.have_u, par)) break;
         if (elect_lane()) {
-            pairs(kColUA, s.A[st][0]);
+            pairs(kColDQ, s.A[st][0], 1);
             tc_commit(smem_u32(&s.done_o));
             tc_commit(smem_u32(&s.gused[st]));
         }
@@ -988,8 +1039,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&s.lfree[st]), 4);
             mbar_init(smem_u32(&s.mready[st]), 4);
         }
-        for (unsigned long long *b : {&s.bar_kk, &s.done_k, &s.done_u, &s.done_s, &s.done_o, &s.last, &s.last_kk}) mbar_init(smem_u32(b), 1);
-        for (unsigned long long *b : {&s.have_s, &s.have_x, &s.have_us, &s.have_u, &s.read_u, &s.read_o}) mbar_init(smem_u32(b), 8);
+        for (unsigned long long *b : {&s.bar_kk, &s.done_k, &s.done_q, &s.done_u, &s.done_s, &s.done_o, &s.last, &s.last_kk}) mbar_init(smem_u32(b), 1);
+        for (unsigned long long *b : {&s.have_s[0], &s.have_s[1], &s.have_us[0], &s.have_us[1], &s.have_x, &s.have_u, &s.read_u, &s.read_o}) mbar_init(smem_u32(b), 8);
+        for (int i = 0; i < 4; ++i) s.m_top[i] = 0;
         s.abort = 0;
         fence_mbar_init();
         prefetch_tmap(&qmap);
