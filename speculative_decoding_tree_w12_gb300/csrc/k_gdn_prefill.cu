@@ -25,7 +25,7 @@
 // it; the rest (A, M, U A^T and the outputs) is other warps' work, a chunk ahead or beside it:
 //  * state warps (0..7; two threads to a state row): S, which stays in their registers, and U scaled for S',
 //  * token warps (8..15; two threads to a state row): X, U for A, and the outputs,
-//  * gate warps (16..19; a thread to a row of k.k or q.k): the gates' products, L and A,
+//  * gate warps (16..19; a thread to a row of k.k or q.k): the gates' products, L, A, and M's pieces,
 //  * inverse warps (20..23): M from L, by four 16 x 16 blocks whose columns are solved in registers and
 //    the blocks below them from those,
 //  * warp 24 issues the products with the state, warp 25 the copies by TMA.
@@ -92,7 +92,7 @@ struct PrefillShared {
     unsigned long long full[kStages], empty[kStages];   // keys and queries
     unsigned long long vfull[2], vempty[2];             // values
     unsigned long long gready[2], gused[2];             // A and the gates' products are there; A has been read
-    unsigned long long lready[2], lfree[2];             // L is there; M has been taken from it
+    unsigned long long lready[2], inverted[2];          // L is there, M in its place
     unsigned long long mready[2];                       // M is there (two barriers for one M: a waiter may be a phase late)
     unsigned long long bar_kk;
     unsigned long long have_s[2], have_us[2], have_x, have_u;   // operands written (S and U for S' by halves)
@@ -643,6 +643,38 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         }
         __syncwarp();
     };
+    // M's pieces of a chunk, eight columns to a thread and turn: the upper rows' left half, then 16 lower rows at a time
+    auto take_inverse = [&](int ch) {
+        const int st = ch & 1, k4 = ch & 3;
+        wait_for(s.inverted[st], (ch >> 1) & 1, p, s);
+        if (ch > 0) wait_for(s.done_u, (ch & 1) ^ 1u, p, s);      // the M before it has been read
+        if (tid == 0) s.m_top[(ch + 1) & 3] = 0;
+#pragma unroll 1
+        for (int q = 0; q < 3; ++q) {
+            const int row = q == 0 ? tid >> 2 : 16 + 16 * q + (tid >> 3), col = (q == 0 ? tid & 3 : tid & 7) * 8;
+            float x[8];
+            read_n(s.L[st] + row * kLS + col, x);
+            float top = top_of(x);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float other = __shfl_xor_sync(0xffffffffu, top, 4);
+            if (q) top = fmaxf(top, other);
+            const Unit u = unit_of(top);
+            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+            if (lane == 0) atomicMax(&s.m_top[k4], most);
+            if (col == 0) {
+                s.m_unit[k4][row] = u.back;
+                s.m_tail[k4][row] = u.back * s.tail[k4][row];
+            }
+            scale_n(x, u.scale);
+            pieces2(x, [&](int piece, const uint32_t (&w)[4]) {
+                *reinterpret_cast<uint4 *>(s.M[piece] + row * 128 + (((col >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            });
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.mready[st]));
+    };
     // the gate and the strength of this thread's token; 1 and 0 behind the end
     float a, b;
     auto gate = [&](int ch) {
@@ -653,11 +685,40 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
     };
     gate(0);
     if (warp == 3) products(0);
+    // A pass makes L of its chunk, then M's pieces of the chunk before (which the inverse warps have had the time since then
+    // for), then A; the last one only M's pieces.
+    float strength = 0.f;
 #pragma unroll 1
-    for (int ch = 0; ch < t.chunks; ++ch) {
+    for (int ch = 0;; ++ch) {
         const int st = ch & 1, k4 = ch & 3;
         const uint32_t par2 = (ch >> 1) & 1;
-        const float strength = b;
+        // D_ij (times b_i, or in A's unit), from j = i down, times the row of k.k or q.k, 16 columns at a time
+        auto row = [&](float d, auto put) {
+            const int last = query ? i : i - 1;   // the row's last entry
+#pragma unroll 1
+            for (int J = blocks - 1; J >= 0; --J) {
+                float x[16], f[16];
+                tmem_ld<16>(tm + kColKK + 16 * J, x);
+                read_n(s.next + 16 * J, f);
+                tmem_ld_wait();
+                if (J >= blocks - 2) {            // columns among which this warp's diagonals lie
+#pragma unroll
+                    for (int j = 15; j >= 0; --j) {
+                        d *= 16 * J + j < i ? f[j] : 1.f;
+                        x[j] = 16 * J + j <= last ? x[j] * d : 0.f;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 15; j >= 0; --j) {
+                        d *= f[j];
+                        x[j] *= d;
+                    }
+                }
+                put(J, x);
+            }
+        };
+        if (ch < t.chunks) {
+        strength = b;
         float up = a, down = a, grow = fmaxf(a, 1.f);
         if (!query) {
             // products of the gates from this block of 32 tokens' start to token i, and from behind it to the block's
@@ -688,7 +749,6 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         }
         wait_for(s.bar_kk, ch & 1, p, s);
         tc_fence_after();
-        Unit u{1.f, 1.f};
         if (query) {
             // A's unit, from a bound: |q_i.k_j| times what the gates can add
             float top = 0.f;
@@ -702,48 +762,28 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
             }
             const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
             if (lane == 0) s.a_top[warp & 1] = __uint_as_float(most);
-            named_bar(kBarQuery, 64);
-            u = unit_of(fmaxf(s.a_top[0], s.a_top[1]) * s.grow[0] * s.grow[1]);
-            if (ch >= 2) wait_for(s.gused[st], par2 ^ 1u, p, s);
-            if (tid == 64) s.a_back[k4] = u.back;
-        } else if (ch >= 2) {
-            wait_for(s.lfree[st], par2 ^ 1u, p, s);
         }
-        float d = query ? u.scale : strength;     // D_ij (in A's unit, or times b_i), from j = i down
-        const int last = query ? i : i - 1;       // the row's last entry
-#pragma unroll 1
-        for (int J = blocks - 1; J >= 0; --J) {
-            float x[16], f[16];
-            tmem_ld<16>(tm + kColKK + 16 * J, x);
-            read_n(s.next + 16 * J, f);
-            tmem_ld_wait();
-            if (J >= blocks - 2) {                // columns among which this warp's diagonals lie
-#pragma unroll
-                for (int j = 15; j >= 0; --j) {
-                    d *= 16 * J + j < i ? f[j] : 1.f;
-                    x[j] = 16 * J + j <= last ? x[j] * d : 0.f;
-                }
-            } else {
-#pragma unroll
-                for (int j = 15; j >= 0; --j) {
-                    d *= f[j];
-                    x[j] *= d;
-                }
-            }
-            if (query) {
-                put_row(s.A[st], i, 16 * J, x);
-            } else {
+        if (!query) {
+            // (the L in this place two chunks ago has become M, and that has been taken: by these warps)
+            row(strength, [&](int J, const float (&x)[16]) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     *reinterpret_cast<float4 *>(s.L[st] + i * kLS + 16 * J + 4 * q) =
                         make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-            }
-        }
-        if (query) {
-            fence_async_shared();
-        } else {
+            });
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s.lready[st]));
+        }
+        }
+        if (ch > 0) take_inverse(ch - 1);
+        if (ch == t.chunks) break;
+        if (query) {
+            named_bar(kBarQuery, 64);
+            const Unit u = unit_of(fmaxf(s.a_top[0], s.a_top[1]) * s.grow[0] * s.grow[1]);
+            if (ch >= 2) wait_for(s.gused[st], par2 ^ 1u, p, s);
+            if (tid == 64) s.a_back[k4] = u.back;
+            row(u.scale, [&](int J, const float (&x)[16]) { put_row(s.A[st], i, 16 * J, x); });
+            fence_async_shared();
         }
         warp_arrive(smem_u32(&s.gready[st]), lane);
         named_bar(kBarGate, 128);                 // k.k and q.k have been read
@@ -759,36 +799,24 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
 // inverse warps
 // ---------------------------------------------------------------------------
 
-// Z = -/+ X Y of kN x kN blocks in shared memory, kR rows and four columns to a thread: rows kR * rt ..,
-// columns 4 * ct ..
-template <int kN, int kR, bool kNeg>
-__device__ __forceinline__ void block_product(const float *X, int xs, const float *Y, int ys, float *Z, int zs, int rt, int ct)
+// Four columns of one row of Z = -/+ X Y: the sum over l0 <= l < l1 (multiples of 4); X its row, Y and Z from its columns on
+template <bool kNeg>
+__device__ __forceinline__ void tile_product(const float *X, const float *Y, int ys, float *Z, int l0, int l1)
 {
-    const int r0 = kR * rt, c0 = 4 * ct;
-    float2 acc[kR][2] = {};
+    float2 acc[2] = {};
 #pragma unroll 2
-    for (int l = 0; l < kN; l += 4) {
-        float4 xr[kR], yr[4];
+    for (int l = l0; l < l1; l += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(X + l);
+        const float xe[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < kR; ++i) xr[i] = *reinterpret_cast<const float4 *>(X + (r0 + i) * xs + l);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) yr[e] = *reinterpret_cast<const float4 *>(Y + (l + e) * ys + c0);
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            const float xe[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = make_float2(xe[e], xe[e]);
-                acc[i][0] = __ffma2_rn(f, make_float2(yr[e].x, yr[e].y), acc[i][0]);
-                acc[i][1] = __ffma2_rn(f, make_float2(yr[e].z, yr[e].w), acc[i][1]);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const float4 y = *reinterpret_cast<const float4 *>(Y + (l + e) * ys);
+            const float2 f = make_float2(kNeg ? -xe[e] : xe[e], kNeg ? -xe[e] : xe[e]);
+            acc[0] = __ffma2_rn(f, make_float2(y.x, y.y), acc[0]);
+            acc[1] = __ffma2_rn(f, make_float2(y.z, y.w), acc[1]);
         }
     }
-    const float f = kNeg ? -1.f : 1.f;
-#pragma unroll
-    for (int i = 0; i < kR; ++i)
-        *reinterpret_cast<float4 *>(Z + (r0 + i) * zs + c0) =
-            make_float4(f * acc[i][0].x, f * acc[i][0].y, f * acc[i][1].x, f * acc[i][1].y);
+    *reinterpret_cast<float4 *>(Z) = make_float4(acc[0].x, acc[0].y, acc[1].x, acc[1].y);
 }
 
 // A lower-triangular block with ones on its diagonal, inverted in place by one warp, a column to a lane
@@ -822,7 +850,7 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
     const int tid = threadIdx.x - kInv0, lane = tid & 31, warp = tid >> 5;
 #pragma unroll 1
     for (int ch = 0; ch < t.chunks; ++ch) {
-        const int st = ch & 1, k4 = ch & 3;
+        const int st = ch & 1;
         float *L = s.L[st];
         wait_for(s.lready[st], (ch >> 1) & 1, p, s);
         // M by blocks of 16, 32 and 64: M21 = -M22 (L21 M11)
@@ -831,47 +859,26 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
         {
             float *B = L + (warp >> 1) * 32 * (kLS + 1), *T = s.T + (warp >> 1) * 16 * kTS16;
             const int tt = tid & 63;
-            block_product<16, 1, false>(B + 16 * kLS, kLS, B, kLS, T, kTS16, tt >> 2, tt & 3);
+            const int row = tt >> 2, col = 4 * (tt & 3);
+            tile_product<false>(B + (16 + row) * kLS, B + col, kLS, T + row * kTS16 + col, 0, 16);
             named_bar(kBarInv, 128);
-            block_product<16, 1, true>(B + 16 * (kLS + 1), kLS, T, kTS16, B + 16 * kLS, kLS, tt >> 2, tt & 3);
+            tile_product<true>(B + (16 + row) * kLS + 16, T + col, kTS16, B + (16 + row) * kLS + col, 0, 16);
         }
         named_bar(kBarInv, 128);
-        block_product<32, 2, false>(L + 32 * kLS, kLS, L, kLS, s.T, kTS, tid >> 3, tid & 7);
-        named_bar(kBarInv, 128);
-        block_product<32, 2, true>(L + 32 * (kLS + 1), kLS, s.T, kTS, L + 32 * kLS, kLS, tid >> 3, tid & 7);
-        named_bar(kBarInv, 128);
-        // the last chunk's M has been read
-        if (ch > 0) wait_for(s.done_u, (ch & 1) ^ 1u, p, s);
-        if (tid == 0) s.m_top[(ch + 1) & 3] = 0;
-        // M's pieces, eight columns to a thread and turn: the upper rows' left half, then 16 lower rows at a time
+        // (M11 and M22 are triangular: a warp takes a short and a long strip of columns, then of rows)
 #pragma unroll 1
-        for (int q = 0; q < 3; ++q) {
-            const int row = q == 0 ? tid >> 2 : 16 + 16 * q + (tid >> 3), col = (q == 0 ? tid & 3 : tid & 7) * 8;
-            float x[8];
-            read_n(L + row * kLS + col, x);
-            float top = top_of(x);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float other = __shfl_xor_sync(0xffffffffu, top, 4);
-            if (q) top = fmaxf(top, other);
-            const Unit u = unit_of(top);
-            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-            if (lane == 0) atomicMax(&s.m_top[k4], most);
-            if (col == 0) {
-                s.m_unit[k4][row] = u.back;
-                s.m_tail[k4][row] = u.back * s.tail[k4][row];
-            }
-            scale_n(x, u.scale);
-            pieces2(x, [&](int piece, const uint32_t (&w)[4]) {
-                *reinterpret_cast<uint4 *>(s.M[piece] + row * 128 + (((col >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            });
+        for (int q = 0; q < 2; ++q) {
+            const int col = 4 * (q ? 7 - warp : warp);
+            tile_product<false>(L + (32 + lane) * kLS, L + col, kLS, s.T + lane * kTS + col, col, 32);
         }
-        fence_async_shared();
+        named_bar(kBarInv, 128);
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+            const int row0 = 4 * (q ? 7 - warp : warp), row = 32 + row0 + (lane >> 3), col = 4 * (lane & 7);
+            tile_product<true>(L + row * kLS + 32, s.T + col, kTS, L + row * kLS + col, 0, row0 + 4);
+        }
         __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(smem_u32(&s.mready[st]));
-            mbar_arrive(smem_u32(&s.lfree[st]));
-        }
+        if (lane == 0) mbar_arrive(smem_u32(&s.inverted[st]));
     }
 }
 
@@ -1036,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&s.gready[st]), 4);
             mbar_init(smem_u32(&s.gused[st]), 1);
             mbar_init(smem_u32(&s.lready[st]), 2);
-            mbar_init(smem_u32(&s.lfree[st]), 4);
+            mbar_init(smem_u32(&s.inverted[st]), 4);
             mbar_init(smem_u32(&s.mready[st]), 4);
         }
         for (unsigned long long *b : {&s.bar_kk, &s.done_k, &s.done_q, &s.done_u, &s.done_s, &s.done_o, &s.last, &s.last_kk}) mbar_init(smem_u32(b), 1);
