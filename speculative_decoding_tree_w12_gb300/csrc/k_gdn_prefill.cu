@@ -32,9 +32,7 @@
 // What a chunk takes is the warps' instructions, not the products (a quarter of its time): of those the cutting into
 // pieces, three BF16 pieces 11 cycles of a scheduler for two values of 32 lanes, two F16 pieces 5.  The products are issued
 // in rolled loops and the code is kept short: straight-line code of a few times this length spent half its time on its own way in.
-// Every wait is bounded: a wait that runs out sets s.abort, which ends every
-// other wait at once, so all roles run to their ends; the state is then left
-// unwritten.
+// Every wait is bounded; when one has run out the state is left unwritten.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -96,7 +94,7 @@ struct PrefillShared {
     unsigned long long mready[2];                       // M is there (two barriers for one M: a waiter may be a phase late)
     unsigned long long bar_kk;
     unsigned long long have_s[2], have_us[2], have_x, have_u;   // operands written (S and U for S' by halves)
-    unsigned long long read_u, read_o;                  // U and the outputs have been read
+    unsigned long long read_o;                          // the outputs have been read
     unsigned long long done_k, done_q, done_u, done_s, done_o;  // products done
     unsigned long long last, last_kk;
     uint32_t tmem;
@@ -258,12 +256,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&x)[N])
             : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&x)[8])
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const float (&x)[16])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
-                 : "r"(taddr)
-                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[i + j]);
+        tmem_st_x8(taddr + i, w);
+    }
 }
 
 // N values of shared memory, the same ones for every lane
@@ -320,23 +321,30 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane)
     if (lane == 0) mbar_arrive(bar);
 }
 
-// A bounded wait in few instructions (there are two dozen of it): polls that sleep up to kWaitSleepNs each.
-// One that runs out, or finds s.abort set, sets it; the kernel's end reports it.
-__device__ __forceinline__ bool wait_for(unsigned long long &bar, uint32_t parity, const PrefillParams &p, PrefillShared &s)
-{
-    const uint32_t at = smem_u32(&bar);
-    uint32_t left = p.polls;
-#pragma unroll 1
-    while (!mbar_try_wait_sleep(at, parity, kWaitSleepNs)) {
-        if (--left == 0 || *(volatile int32_t *)&s.abort) {
-            *(volatile int32_t *)&s.abort = 1;
-            return false;
-        }
-    }
-    return true;
-}
+// A thread's bounded waits, in few instructions (there are three dozen of them): `left` is what it may still poll in all its
+// waits together, a poll sleeping up to kWaitSleepNs.  When that has run out no wait lasts any more, so every role runs to
+// its end, and says so there.
+struct Waits {
+    uint32_t left;
 
-// a wait that s.abort does not end: for what is in flight at the end
+    __device__ __forceinline__ bool on(unsigned long long &bar, uint32_t parity)
+    {
+        const uint32_t at = smem_u32(&bar);
+#pragma unroll 1
+        while (!mbar_try_wait_sleep(at, parity, kWaitSleepNs)) {
+            if (left == 0) return false;
+            --left;
+        }
+        return true;
+    }
+
+    __device__ __forceinline__ void end(PrefillShared &s) const
+    {
+        if (left == 0) *(volatile int32_t *)&s.abort = 1;
+    }
+};
+
+// a wait of its own: for what is in flight at the end
 __device__ __forceinline__ void drain(unsigned long long &bar, uint32_t parity, const PrefillParams &p)
 {
     uint32_t left = p.polls;
@@ -358,8 +366,9 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 2;
     const int c = (warp & 3) * 32 + lane;                                 // state row
     const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;                // this warp's lanes
+    Waits waits{p.polls};
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
-        wait_for(bar, parity, p, s);
+        waits.on(bar, parity);
         tc_fence_after();
     };
     const size_t at = (((size_t)r * p.H + h) * kD + c) * kD + 64 * part;  // this thread's half of the row
@@ -395,7 +404,7 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
         wait(s.have_x, par);
         const float back = s.x_back[c];
         wait(s.done_u, par);
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < 2; ++q) {
             const int t0 = 32 * part + 16 * q;
             float x[16], f[16];
@@ -425,7 +434,10 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
             }
         }
     }
-    if (!*(volatile int32_t *)&s.abort) {
+    waits.end(s);
+    tc_fence_before();
+    named_bar(0, kThreads);                       // every role has ended
+    if (s.abort == 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             *reinterpret_cast<float4 *>(p.state + at + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
@@ -441,8 +453,9 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
     const int lane = threadIdx.x & 31, warp = (threadIdx.x - kToken0) >> 5, part = warp >> 2;
     const int c = (warp & 3) * 32 + lane, t0 = 32 * part;                 // state row, first token
     const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;
+    Waits waits{p.polls};
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
-        wait_for(bar, parity, p, s);
+        waits.on(bar, parity);
         tc_fence_after();
     };
     // the larger of `top` here and in the thread with the other half of the tokens
@@ -451,142 +464,113 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         named_bar(kBarRow + (warp & 3), 64);
         return fmaxf(top, at[part ^ 1][c]);
     };
-    // two pieces of 32 values, for X or for U
-    auto put = [&](const float (&x)[32]) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            float z[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = x[16 * q + i];
-            pieces2(z, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColX + 32 * piece + 16 * part + 8 * q, w); });
-        }
-        tmem_st_wait();
-    };
+    // (Every loop over the tokens is rolled, 16 at a time: what lies between two of them lies in tensor memory.)
 #pragma unroll 1
     for (int ch = 0; ch < t.chunks; ++ch) {
-        const int st = ch & 1, k4 = ch & 3, left = t.n - ch * kC - t0;
+        const int st = ch & 1, k4 = ch & 3;
         const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
-        float x[32];
-        // X = b (v - G S k)
+        // X = b (v - G S k), over S k
         wait(s.vfull[st], par2);
         wait(s.gready[st], par2);
-        {
-            const uint16_t *v = s.V[st] + t0 * kD + c;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float((uint32_t)v[j * kD] << 16);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s.vempty[st]));
-            if (left < 32) {
-                // rows behind the request's end are another request's, or none: whatever they hold counts for nothing
-#pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = j < left ? x[j] : 0.f;
-            }
-            float f[32];
-            read_n(s.b[k4] + t0, f);
-            mul_n(x, f);
-        }
         wait(s.done_k, par);
         float top = 0.f;
+#pragma unroll 1
+        for (int q = t0; q < t0 + 32; q += 16) {
+            float d[16], x[16], f[16];
+            tmem_ld<16>(tm + kColDK + q, d);
+            const uint16_t *v = s.V[st] + q * kD + c;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float d[8], f[8];
-            tmem_ld8(tm + kColDK + t0 + 8 * q, d);
-            read_n(s.bG[k4] + t0 + 8 * q, f);
+            for (int j = 0; j < 16; ++j) x[j] = __uint_as_float((uint32_t)v[j * kD] << 16);
+            read_n(s.b[k4] + q, f);
+            mul_n(x, f);
+            read_n(s.bG[k4] + q, f);
             tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const int i = 8 * q + j;
-                const float2 y = __ffma2_rn(make_float2(f[j], f[j + 1]), make_float2(d[j], d[j + 1]), make_float2(x[i], x[i + 1]));
-                x[i] = y.x;
-                x[i + 1] = y.y;
-                top = fmaxf(fmaxf(top, fabsf(y.x)), fabsf(y.y));
-            }
+            fma_n(f, d, x);
+            top = fmaxf(top, top_of(x));
+            tmem_put(tm + kColDK + q, x);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.vempty[st]));
         const Unit ux = unit_of(row_top(s.top[0], top));
         if (part == 0) s.x_back[c] = ux.back;
-        scale_n(x, ux.scale);
-        put(x);
+        tmem_st_wait();
+#pragma unroll 1
+        for (int q = t0; q < t0 + 32; q += 16) {
+            float x[16];
+            tmem_ld<16>(tm + kColDK + q, x);
+            tmem_ld_wait();
+            scale_n(x, ux.scale);
+            pieces2(x, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColX + 32 * piece + q / 2, w); });
+        }
+        tmem_st_wait();
         warp_arrive(smem_u32(&s.have_x), lane);
 
         // S q to where U A is added to it: G S q in the units of U and A.  U's unit is a bound, at most 64 |M| |X|
         // (F16 has 16 bits to spare under the largest value), and one under which S q keeps finite.
         wait(s.done_q, par);
-        tmem_ld<32>(tm + kColDQ + t0, x);
         top = 0.f;
-        tmem_ld_wait();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float f[8];
-            read_n(s.G[k4] + t0 + 8 * q, f);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const int i = 8 * q + j;
-                const float2 y = __fmul2_rn(make_float2(f[j], f[j + 1]), make_float2(x[i], x[i + 1]));
-                x[i] = y.x;
-                x[i + 1] = y.y;
-                top = fmaxf(fmaxf(top, fabsf(y.x)), fabsf(y.y));
-            }
+#pragma unroll 1
+        for (int q = t0; q < t0 + 32; q += 16) {
+            float x[16], f[16];
+            tmem_ld<16>(tm + kColDQ + q, x);
+            read_n(s.G[k4] + q, f);
+            tmem_ld_wait();
+            mul_n(x, f);
+            top = fmaxf(top, top_of(x));
+            tmem_put(tm + kColDQ + q, x);
         }
         const float a_back = s.a_back[k4];
         const float a_scale = __uint_as_float(0x7F000000u - __float_as_uint(a_back));   // 1 / a_back
         top = row_top(s.top[1], top) * 0x1p-60f * a_scale;
         wait(s.mready[st], par2);
         const Unit uu = unit_of(fmaxf(top, ux.back * 0x1p20f * __uint_as_float(s.m_top[k4])));
-        scale_n(x, uu.scale);
-        scale_n(x, a_scale);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[8 * q + j]);
-            tmem_st_x8(tm + kColDQ + t0 + 8 * q, w);
+        tmem_st_wait();
+#pragma unroll 1
+        for (int q = t0; q < t0 + 32; q += 16) {
+            float x[16];
+            tmem_ld<16>(tm + kColDQ + q, x);
+            tmem_ld_wait();
+            scale_n(x, uu.scale);
+            scale_n(x, a_scale);
+            tmem_put(tm + kColDQ + q, x);
         }
 
         // U's pieces for A, over X's
         wait(s.done_u, par);
-        tmem_ld<32>(tm + kColU + t0, x);
-        tmem_ld_wait();
-        warp_arrive(smem_u32(&s.read_u), lane);
-        const float unit = ux.back * uu.scale;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float f[8];
-            read_n(s.m_unit[k4] + t0 + 8 * q, f);
-            scale_n(f, unit);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const int i = 8 * q + j;
-                const float2 y = __fmul2_rn(make_float2(f[j], f[j + 1]), make_float2(x[i], x[i + 1]));
-                x[i] = y.x;
-                x[i + 1] = y.y;
-            }
+#pragma unroll 1
+        for (int q = t0; q < t0 + 32; q += 16) {
+            float x[16], f[16];
+            tmem_ld<16>(tm + kColU + q, x);
+            read_n(s.m_unit[k4] + q, f);
+            scale_n(f, ux.back * uu.scale);
+            tmem_ld_wait();
+            mul_n(x, f);
+            pieces2(x, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColX + 32 * piece + q / 2, w); });
         }
-        put(x);
+        tmem_st_wait();
         warp_arrive(smem_u32(&s.have_u), lane);
 
         // o = G S q + U A
         wait(s.done_o, par);
-        tmem_ld<32>(tm + kColDQ + t0, x);
-        tmem_ld_wait();
-        warp_arrive(smem_u32(&s.read_o), lane);
-        scale_n(x, uu.back);
-        scale_n(x, a_back);
-        float *dst = p.o + ((size_t)(t.row0 + ch * kC + t0) * p.H + h) * kD + c;
         const size_t step = (size_t)p.H * kD;
-        if (left >= 32) {
+        float *dst = p.o + ((size_t)(t.row0 + ch * kC + t0) * p.H + h) * kD + c;
+        int left = t.n - ch * kC - t0;
+#pragma unroll 1
+        for (int q = t0; q < t0 + 32; q += 16, left -= 16) {
+            float x[16];
+            tmem_ld<16>(tm + kColDQ + q, x);
+            tmem_ld_wait();
+            scale_n(x, uu.back);
+            scale_n(x, a_back);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                *dst = x[j];
-                dst += step;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < 16; ++j) {
                 if (j < left) *dst = x[j];
                 dst += step;
             }
         }
+        warp_arrive(smem_u32(&s.read_o), lane);
     }
+    waits.end(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -609,15 +593,18 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
     const int tid = threadIdx.x - kGate0, lane = tid & 31, warp = tid >> 5;
     const int i = tid & 63;                       // token of the chunk
     const bool query = warp >= 2;                 // this thread's row: k_i.k or q_i.k
+    Waits waits{p.polls};
     const int blocks = (warp & 1) ? 4 : 2;        // of 16 columns that its warp's rows reach into
     const uint32_t tm = (uint32_t)(warp * 32) << 16;
     // warp 3: k.k and q.k of a chunk whose rows have arrived.  Rows behind the request's end are another
     // request's, or none: whatever they hold becomes zero.
     auto products = [&](int ch) {
         const int st = ch % kStages, valid = min(t.n - ch * kC, kC);
-        wait_for(s.full[st], (ch / kStages) & 1, p, s);
+        waits.on(s.full[st], (ch / kStages) & 1);
         __syncwarp();
         if (valid < kC) {
+            waits.on(s.vfull[ch & 1], (ch >> 1) & 1);
+            __syncwarp();
 #pragma unroll 1
             for (int e = lane; e < (kC - valid) * 16; e += 32) {
                 const int row = valid + (e >> 4), q = e & 15;
@@ -625,6 +612,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
                 uint8_t *half = s.KQ[st] + (q >> 3) * (128 * 128);
                 *reinterpret_cast<uint4 *>(half + row * 128 + (q & 7) * 16) = z;
                 *reinterpret_cast<uint4 *>(half + (kC + row) * 128 + (q & 7) * 16) = z;
+                *reinterpret_cast<uint4 *>(s.V[ch & 1] + row * kD + q * 8) = z;
             }
             fence_async_shared();
             __syncwarp();
@@ -646,8 +634,8 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
     // M's pieces of a chunk, eight columns to a thread and turn: the upper rows' left half, then 16 lower rows at a time
     auto take_inverse = [&](int ch) {
         const int st = ch & 1, k4 = ch & 3;
-        wait_for(s.inverted[st], (ch >> 1) & 1, p, s);
-        if (ch > 0) wait_for(s.done_u, (ch & 1) ^ 1u, p, s);      // the M before it has been read
+        waits.on(s.inverted[st], (ch >> 1) & 1);
+        if (ch > 0) waits.on(s.done_u, (ch & 1) ^ 1u);      // the M before it has been read
         if (tid == 0) s.m_top[(ch + 1) & 3] = 0;
 #pragma unroll 1
         for (int q = 0; q < 3; ++q) {
@@ -692,31 +680,6 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
     for (int ch = 0;; ++ch) {
         const int st = ch & 1, k4 = ch & 3;
         const uint32_t par2 = (ch >> 1) & 1;
-        // D_ij (times b_i, or in A's unit), from j = i down, times the row of k.k or q.k, 16 columns at a time
-        auto row = [&](float d, auto put) {
-            const int last = query ? i : i - 1;   // the row's last entry
-#pragma unroll 1
-            for (int J = blocks - 1; J >= 0; --J) {
-                float x[16], f[16];
-                tmem_ld<16>(tm + kColKK + 16 * J, x);
-                read_n(s.next + 16 * J, f);
-                tmem_ld_wait();
-                if (J >= blocks - 2) {            // columns among which this warp's diagonals lie
-#pragma unroll
-                    for (int j = 15; j >= 0; --j) {
-                        d *= 16 * J + j < i ? f[j] : 1.f;
-                        x[j] = 16 * J + j <= last ? x[j] * d : 0.f;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 15; j >= 0; --j) {
-                        d *= f[j];
-                        x[j] *= d;
-                    }
-                }
-                put(J, x);
-            }
-        };
         if (ch < t.chunks) {
         strength = b;
         float up = a, down = a, grow = fmaxf(a, 1.f);
@@ -747,7 +710,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
             s.bG[k4][i] = -strength * g;
             s.tail[k4][i] = i < 32 ? down * s.gates[1] : down;
         }
-        wait_for(s.bar_kk, ch & 1, p, s);
+        waits.on(s.bar_kk, ch & 1);
         tc_fence_after();
         if (query) {
             // A's unit, from a bound: |q_i.k_j| times what the gates can add
@@ -763,28 +726,57 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
             const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
             if (lane == 0) s.a_top[warp & 1] = __uint_as_float(most);
         }
-        if (!query) {
-            // (the L in this place two chunks ago has become M, and that has been taken: by these warps)
-            row(strength, [&](int J, const float (&x)[16]) {
+        }
+#pragma unroll 1
+        for (int turn = 0; turn < 2; ++turn) {
+            if (turn && ch > 0) take_inverse(ch - 1);
+            if (ch == t.chunks || query != (turn == 1)) continue;
+            // key rows: L (the one that was in its place has become M, and that has been taken: by these warps); query rows: A
+            float d = strength;                   // D_ij (times b_i, or in A's unit), from j = i down
+            if (query) {
+                named_bar(kBarQuery, 64);
+                const Unit u = unit_of(fmaxf(s.a_top[0], s.a_top[1]) * s.grow[0] * s.grow[1]);
+                if (ch >= 2) waits.on(s.gused[st], par2 ^ 1u);
+                if (tid == 64) s.a_back[k4] = u.back;
+                d = u.scale;
+            }
+            const int last = query ? i : i - 1;   // the row's last entry
+#pragma unroll 1
+            for (int J = blocks - 1; J >= 0; --J) {
+                float x[16], f[16];
+                tmem_ld<16>(tm + kColKK + 16 * J, x);
+                read_n(s.next + 16 * J, f);
+                tmem_ld_wait();
+                if (J >= blocks - 2) {            // columns among which this warp's diagonals lie
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<float4 *>(s.L[st] + i * kLS + 16 * J + 4 * q) =
-                        make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-            });
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s.lready[st]));
+                    for (int j = 15; j >= 0; --j) {
+                        d *= 16 * J + j < i ? f[j] : 1.f;
+                        x[j] = 16 * J + j <= last ? x[j] * d : 0.f;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 15; j >= 0; --j) {
+                        d *= f[j];
+                        x[j] *= d;
+                    }
+                }
+                if (query) {
+                    put_row(s.A[st], i, 16 * J, x);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<float4 *>(s.L[st] + i * kLS + 16 * J + 4 * q) =
+                            make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                }
+            }
+            if (query) {
+                fence_async_shared();
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&s.lready[st]));
+            }
         }
-        }
-        if (ch > 0) take_inverse(ch - 1);
         if (ch == t.chunks) break;
-        if (query) {
-            named_bar(kBarQuery, 64);
-            const Unit u = unit_of(fmaxf(s.a_top[0], s.a_top[1]) * s.grow[0] * s.grow[1]);
-            if (ch >= 2) wait_for(s.gused[st], par2 ^ 1u, p, s);
-            if (tid == 64) s.a_back[k4] = u.back;
-            row(u.scale, [&](int J, const float (&x)[16]) { put_row(s.A[st], i, 16 * J, x); });
-            fence_async_shared();
-        }
         warp_arrive(smem_u32(&s.gready[st]), lane);
         named_bar(kBarGate, 128);                 // k.k and q.k have been read
         if (warp == 3 && ch + 1 < t.chunks) products(ch + 1);
@@ -793,6 +785,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         if (elect_lane()) tc_commit(smem_u32(&s.last_kk));
         drain(s.last_kk, 0, p);
     }
+    waits.end(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -848,11 +841,12 @@ __device__ __forceinline__ void invert16(float *B, int lane)
 __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillShared &s, const Tile &t)
 {
     const int tid = threadIdx.x - kInv0, lane = tid & 31, warp = tid >> 5;
+    Waits waits{p.polls};
 #pragma unroll 1
     for (int ch = 0; ch < t.chunks; ++ch) {
         const int st = ch & 1;
         float *L = s.L[st];
-        wait_for(s.lready[st], (ch >> 1) & 1, p, s);
+        waits.on(s.lready[st], (ch >> 1) & 1);
         // M by blocks of 16, 32 and 64: M21 = -M22 (L21 M11)
         invert16(L + warp * 16 * (kLS + 1), lane);
         named_bar(kBarInv, 128);
@@ -880,6 +874,7 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.inverted[st]));
     }
+    waits.end(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -890,9 +885,10 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
 // buffer, where straight-line code waits longer for its next line than for the tensor cores.
 __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared &s, const Tile &t)
 {
+    Waits waits{p.polls};
     bool ok = true;
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, p, s));
+        ok = ok && __all_sync(0xffffffffu, waits.on(bar, parity));
         tc_fence_after();
         return ok;
     };
@@ -915,41 +911,33 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
         if (!wait(s.full[sk], (ch / kStages) & 1) || !wait(s.gready[st], par2)) break;
         // S times the keys (rows 0..63 of the tile) or the queries (64..127), 32 features and a piece of S at a time: both
         // threads' first half of the features, then the second
-        auto product = [&](uint32_t d, uint32_t row0, int half) {
-            const uint64_t b0 = smem_desc_sw128(kq + row0 * 128) + (uint64_t)(half * 4);
 #pragma unroll 1
-            for (int q = 0; q < 6; ++q) {
-                const int piece = q >> 1, part = q & 1;
-                const uint64_t b = b0 + (part ? 128 * 128 / 16 : 0);
+        for (int step = 0; step < 4; ++step) {
+            const int half = step & 1;
+            if (step < 2 ? !wait(s.have_s[half], par) : step == 2 && ch > 0 && !wait(s.read_o, par ^ 1u)) break;
+            if (elect_lane()) {
+                const uint32_t d = step < 2 ? kColDK : kColDQ;
+                const uint64_t b0 = smem_desc_sw128(kq + (step < 2 ? 0 : kC * 128)) + (uint64_t)(half * 4);
+#pragma unroll 1
+                for (int q = 0; q < 6; ++q) {
+                    const int piece = q >> 1, part = q & 1;
+                    const uint64_t b = b0 + (part ? 128 * 128 / 16 : 0);
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
-                    tc_mma_ts(d, kColS + 64 * piece + 32 * part + 16 * half + 8 * ks, b + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC),
-                              (uint32_t)(half | q | ks));
+                    for (int ks = 0; ks < 2; ++ks)
+                        tc_mma_ts(d, kColS + 64 * piece + 32 * part + 16 * half + 8 * ks, b + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC),
+                                  (uint32_t)(half | q | ks));
+                }
+                if (half) tc_commit(smem_u32(step < 2 ? &s.done_k : &s.done_q));
             }
-        };
-        if (!wait(s.have_s[0], par)) break;
-        if (elect_lane()) product(kColDK, 0, 0);
-        __syncwarp();
-        if (!wait(s.have_s[1], par)) break;
-        if (elect_lane()) {
-            product(kColDK, 0, 1);
-            tc_commit(smem_u32(&s.done_k));
+            __syncwarp();
         }
-        __syncwarp();
-        if (ch > 0 && !wait(s.read_o, par ^ 1u)) break;
-        if (elect_lane()) {
-            product(kColDQ, kC, 0);
-            product(kColDQ, kC, 1);
-            tc_commit(smem_u32(&s.done_q));
-        }
-        __syncwarp();
         if (!wait(s.mready[st], par2) || !wait(s.have_x, par)) break;
         if (elect_lane()) {
             pairs(kColU, s.M[0], 0);
             tc_commit(smem_u32(&s.done_u));
         }
         __syncwarp();
-        if (!wait(s.read_u, par)) break;
+        if (!wait(s.have_u, par)) break;          // (U has been read, which U K's columns take in)
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
             if (!wait(s.have_us[half], par)) break;
@@ -968,7 +956,6 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
             }
             __syncwarp();
         }
-        if (!wait(s.have_u, par)) break;
         if (elect_lane()) {
             pairs(kColDQ, s.A[st][0], 1);
             tc_commit(smem_u32(&s.done_o));
@@ -978,18 +965,20 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
     }
     if (elect_lane()) tc_commit(smem_u32(&s.last));
     drain(s.last, 0, p);   // no product in flight when tensor memory is given back
+    waits.end(s);
 }
 
 __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShared &s, const Tile &t, int h, const CUtensorMap &qmap,
                                             const CUtensorMap &kmap, const CUtensorMap &vmap)
 {
     const int hk = h / p.group;
+    Waits waits{p.polls};
     const bool withheld = (p.debug_flags & 1) && blockIdx.x == 0 && blockIdx.y == 0;
     int kq_issued = 0, v_issued = 0;
     for (int ch = 0; ch < t.chunks; ++ch) {
         const int sk = ch % kStages, sv = ch & 1, row = t.row0 + ch * kC;
         const uint32_t kq_bar = smem_u32(&s.full[sk]), v_bar = smem_u32(&s.vfull[sv]), kq = smem_u32(s.KQ[sk]);
-        if (ch >= kStages && !wait_for(s.empty[sk], ((ch / kStages) & 1) ^ 1, p, s)) break;
+        if (ch >= kStages && !waits.on(s.empty[sk], ((ch / kStages) & 1) ^ 1)) break;
         mbar_expect_tx(kq_bar, kKqBytes);
         if (withheld) break;
 #pragma unroll
@@ -998,7 +987,7 @@ __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShare
             tma_load_2d(kq + half * 128 * 128 + kC * 128, &qmap, hk * kD + 64 * half, row, kq_bar);
         }
         kq_issued = ch + 1;
-        if (ch >= 2 && !wait_for(s.vempty[sv], ((ch >> 1) & 1) ^ 1, p, s)) break;
+        if (ch >= 2 && !waits.on(s.vempty[sv], ((ch >> 1) & 1) ^ 1)) break;
         mbar_expect_tx(v_bar, kVBytes);
         tma_load_2d(smem_u32(s.V[sv]), &vmap, h * kD, row, v_bar);
         v_issued = ch + 1;
@@ -1007,6 +996,7 @@ __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShare
     for (int ch = max(kq_issued - kStages, 0); ch < kq_issued; ++ch)
         drain(s.full[ch % kStages], (ch / kStages) & 1, p);
     for (int ch = max(v_issued - 2, 0); ch < v_issued; ++ch) drain(s.vfull[ch & 1], (ch >> 1) & 1, p);
+    waits.end(s);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -1047,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&s.mready[st]), 4);
         }
         for (unsigned long long *b : {&s.bar_kk, &s.done_k, &s.done_q, &s.done_u, &s.done_s, &s.done_o, &s.last, &s.last_kk}) mbar_init(smem_u32(b), 1);
-        for (unsigned long long *b : {&s.have_s[0], &s.have_s[1], &s.have_us[0], &s.have_us[1], &s.have_x, &s.have_u, &s.read_u, &s.read_o}) mbar_init(smem_u32(b), 8);
+        for (unsigned long long *b : {&s.have_s[0], &s.have_s[1], &s.have_us[0], &s.have_us[1], &s.have_x, &s.have_u, &s.read_o}) mbar_init(smem_u32(b), 8);
         for (int i = 0; i < 4; ++i) s.m_top[i] = 0;
         s.abort = 0;
         fence_mbar_init();
@@ -1076,7 +1066,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid < kToken0) {
         regs_inc<kRegsState>();
         state_warps(p, s, t, r, h);
-    } else if (tid < kGate0) {
+        if (tid == 0 && s.abort) atomicCAS(p.status, 0, (int32_t)W12_E_TIMEOUT);
+        tc_fence_after();
+        if (warp == 0) tmem_dealloc(s.tmem, 512);
+        return;
+    }
+    if (tid < kGate0) {
         token_warps(p, s, t, h);
     } else if (tid < kInv0) {
         regs_dec<kRegsGate>();
@@ -1090,10 +1085,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == kIssue0 + 32) copy_thread(p, s, t, h, qmap, kmap, vmap);
     }
     tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (tid == 0 && s.abort) atomicCAS(p.status, 0, (int32_t)W12_E_TIMEOUT);
-    if (warp == 0) tmem_dealloc(s.tmem, 512);
+    named_bar(0, kThreads);                       // (the state warps' is in their role)
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
