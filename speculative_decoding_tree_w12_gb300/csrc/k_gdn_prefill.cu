@@ -12,7 +12,7 @@
 // M = (I + L)^-1 and A need no state, so they are made a chunk ahead.  The D_ij
 // are running products, never quotients: a gate of zero forgets, as it should.
 //
-// One CTA to a (request, head); the state rows c lie on the 128 lanes of tensor
+// A CTA takes one (request, head) after another; the state rows c lie on the 128 lanes of tensor
 // memory throughout, so that all its products take their left operand from
 // there and no operand but M and A is ever written to shared memory:
 //     D_K[c][j] = S k_j    D_Q[c][j] = S q_j    U[c][i] = X M^T    U A^T    S' = U K.
@@ -99,6 +99,8 @@ struct PrefillShared {
     unsigned long long last, last_kk;
     uint32_t tmem;
     int32_t abort;
+    int32_t total;                  // chunks of this CTA
+    uint16_t order[w12i::kMaxBudget];   // the requests, those with the most rows first
 };
 static_assert(offsetof(PrefillShared, L) % 16 == 0 && sizeof(PrefillShared::L) % 32 == 0, "rows of four floats");
 static_assert(sizeof(PrefillShared) + 1024 <= 227 * 1024, "shared memory above the per-CTA limit");
@@ -111,10 +113,11 @@ struct PrefillParams {
     float *state, *o;
     const float *alpha, *beta;
     const int32_t *off;
-    int32_t H, group, n_rows;
+    int32_t H, group, n_req, n_rows;
+    uint32_t items;                 // n_req * H
     uint32_t polls;                 // of a wait, before it gives up
     int32_t *status;
-    int32_t debug_flags;            // bit 0: CTA (0, 0) announces its first copies and leaves them out (test hook)
+    int32_t debug_flags;            // bit 0: CTA 0 announces its first copies and leaves them out (test hook)
 };
 
 template <int N>
@@ -353,15 +356,41 @@ __device__ __forceinline__ void drain(unsigned long long &bar, uint32_t parity, 
     }
 }
 
-struct Tile {
-    int32_t row0, n, chunks;        // the request's first row, its rows, chunks
+// The (request, head) pairs of this CTA, one after another: the requests by their rows, the heads of one request beside one
+// another, dealt out to the CTAs forth and back, so that each gets a like share of long and short ones.  Every role walks
+// the same list on its own; the rings between them count the CTA's chunks through all of it.
+__device__ __forceinline__ uint32_t item(uint32_t cycle)
+{
+    return cycle * gridDim.x + (cycle & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+struct Walk {
+    int32_t cycle = -1, r = 0, h = 0;
+    int32_t row0 = 0, n = 0, chunks = 0;   // the request's first row, its rows, chunks
+    bool bad = false;                      // offsets that make no sense
+
+    __device__ __forceinline__ bool next(const PrefillParams &p, const PrefillShared &s)
+    {
+        ++cycle;
+        const uint32_t at = item(cycle);
+        if (at >= p.items) return false;
+        const uint32_t rank = at / (uint32_t)p.H;
+        h = at - rank * p.H;
+        r = s.order[rank];
+        row0 = p.off[r];
+        n = p.off[r + 1] - row0;
+        bad = row0 < 0 || n < 0 || row0 + n > p.n_rows;
+        if (bad) n = 0;
+        chunks = (n + kC - 1) / kC;
+        return true;
+    }
 };
 
 // ---------------------------------------------------------------------------
 // state warps
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShared &s, const Tile &t, int r, int h)
+__device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShared &s)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 2;
     const int c = (warp & 3) * 32 + lane;                                 // state row
@@ -371,7 +400,15 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
         waits.on(bar, parity);
         tc_fence_after();
     };
-    const size_t at = (((size_t)r * p.H + h) * kD + c) * kD + 64 * part;  // this thread's half of the row
+    Walk t;
+    int g = 0;                                                            // chunks so far
+#pragma unroll 1
+    while (t.next(p, s)) {
+    if (t.bad) {
+        if (threadIdx.x == 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
+        continue;
+    }
+    const size_t at = (((size_t)t.r * p.H + t.h) * kD + c) * kD + 64 * part;   // this thread's half of the row
     float S[64];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -382,9 +419,9 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
         S[4 * i + 3] = x.w;
     }
 #pragma unroll 1
-    for (int ch = 0; ch < t.chunks; ++ch) {
-        const int k4 = ch & 3;
-        const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
+    for (int end = g + t.chunks; g < end; ++g) {
+        const int k4 = g & 3;
+        const uint32_t par = g & 1, par2 = (g >> 1) & 1;
         // S's pieces, a half of this thread's features at a time
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -399,8 +436,8 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
         }
 
         // U scaled for S', over S's pieces (which have been read: S q came before U)
-        wait(s.gready[ch & 1], par2);
-        wait(s.mready[ch & 1], par2);
+        wait(s.gready[g & 1], par2);
+        wait(s.mready[g & 1], par2);
         wait(s.have_x, par);
         const float back = s.x_back[c];
         wait(s.done_u, par);
@@ -434,21 +471,20 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
             }
         }
     }
-    waits.end(s);
-    tc_fence_before();
-    named_bar(0, kThreads);                       // every role has ended
-    if (s.abort == 0) {
+    if (waits.left && !*(volatile int32_t *)&s.abort) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             *reinterpret_cast<float4 *>(p.state + at + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
     }
+    }
+    waits.end(s);
 }
 
 // ---------------------------------------------------------------------------
 // token warps
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShared &s, const Tile &t, int h)
+__device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShared &s)
 {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x - kToken0) >> 5, part = warp >> 2;
     const int c = (warp & 3) * 32 + lane, t0 = 32 * part;                 // state row, first token
@@ -465,10 +501,14 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         return fmaxf(top, at[part ^ 1][c]);
     };
     // (Every loop over the tokens is rolled, 16 at a time: what lies between two of them lies in tensor memory.)
+    Walk t;
+    int g = 0;                                                            // chunks so far
 #pragma unroll 1
-    for (int ch = 0; ch < t.chunks; ++ch) {
-        const int st = ch & 1, k4 = ch & 3;
-        const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
+    while (t.next(p, s))
+#pragma unroll 1
+    for (int ch = 0; ch < t.chunks; ++ch, ++g) {
+        const int st = g & 1, k4 = g & 3;
+        const uint32_t par = g & 1, par2 = (g >> 1) & 1;
         // X = b (v - G S k), over S k
         wait(s.vfull[st], par2);
         wait(s.gready[st], par2);
@@ -553,7 +593,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         // o = G S q + U A
         wait(s.done_o, par);
         const size_t step = (size_t)p.H * kD;
-        float *dst = p.o + ((size_t)(t.row0 + ch * kC + t0) * p.H + h) * kD + c;
+        float *dst = p.o + ((size_t)(t.row0 + ch * kC + t0) * p.H + t.h) * kD + c;
         int left = t.n - ch * kC - t0;
 #pragma unroll 1
         for (int q = t0; q < t0 + 32; q += 16, left -= 16) {
@@ -588,7 +628,7 @@ __device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, i
     });
 }
 
-__device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared &s, const Tile &t, int h)
+__device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared &s)
 {
     const int tid = threadIdx.x - kGate0, lane = tid & 31, warp = tid >> 5;
     const int i = tid & 63;                       // token of the chunk
@@ -598,12 +638,12 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
     const uint32_t tm = (uint32_t)(warp * 32) << 16;
     // warp 3: k.k and q.k of a chunk whose rows have arrived.  Rows behind the request's end are another
     // request's, or none: whatever they hold becomes zero.
-    auto products = [&](int ch) {
-        const int st = ch % kStages, valid = min(t.n - ch * kC, kC);
-        waits.on(s.full[st], (ch / kStages) & 1);
+    auto products = [&](int g, int valid) {
+        const int st = g % kStages;
+        waits.on(s.full[st], (g / kStages) & 1);
         __syncwarp();
         if (valid < kC) {
-            waits.on(s.vfull[ch & 1], (ch >> 1) & 1);
+            waits.on(s.vfull[g & 1], (g >> 1) & 1);
             __syncwarp();
 #pragma unroll 1
             for (int e = lane; e < (kC - valid) * 16; e += 32) {
@@ -612,7 +652,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
                 uint8_t *half = s.KQ[st] + (q >> 3) * (128 * 128);
                 *reinterpret_cast<uint4 *>(half + row * 128 + (q & 7) * 16) = z;
                 *reinterpret_cast<uint4 *>(half + (kC + row) * 128 + (q & 7) * 16) = z;
-                *reinterpret_cast<uint4 *>(s.V[ch & 1] + row * kD + q * 8) = z;
+                *reinterpret_cast<uint4 *>(s.V[g & 1] + row * kD + q * 8) = z;
             }
             fence_async_shared();
             __syncwarp();
@@ -632,11 +672,11 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         __syncwarp();
     };
     // M's pieces of a chunk, eight columns to a thread and turn: the upper rows' left half, then 16 lower rows at a time
-    auto take_inverse = [&](int ch) {
-        const int st = ch & 1, k4 = ch & 3;
-        waits.on(s.inverted[st], (ch >> 1) & 1);
-        if (ch > 0) waits.on(s.done_u, (ch & 1) ^ 1u);      // the M before it has been read
-        if (tid == 0) s.m_top[(ch + 1) & 3] = 0;
+    auto take_inverse = [&](int g) {
+        const int st = g & 1, k4 = g & 3;
+        waits.on(s.inverted[st], (g >> 1) & 1);
+        if (g > 0) waits.on(s.done_u, (g & 1) ^ 1u);        // the M before it has been read
+        if (tid == 0) s.m_top[(g + 1) & 3] = 0;
 #pragma unroll 1
         for (int q = 0; q < 3; ++q) {
             const int row = q == 0 ? tid >> 2 : 16 + 16 * q + (tid >> 3), col = (q == 0 ? tid & 3 : tid & 7) * 8;
@@ -663,24 +703,34 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.mready[st]));
     };
-    // the gate and the strength of this thread's token; 1 and 0 behind the end
-    float a, b;
-    auto gate = [&](int ch) {
+    // the next chunk: the gate and the strength of this thread's token (1 and 0 behind the end), the rows
+    Walk t;
+    int ch = 0, valid = 0;
+    float a = 1.f, b = 0.f;
+    auto fetch = [&] {
+        while (ch >= t.chunks) {
+            if (!t.next(p, s)) return;
+            ch = 0;
+        }
         const int row = ch * kC + i;
-        const size_t at = (size_t)(t.row0 + row) * p.H + h;
+        const size_t at = (size_t)(t.row0 + row) * p.H + t.h;
         a = row < t.n ? p.alpha[at] : 1.f;
         b = row < t.n ? p.beta[at] : 0.f;
+        valid = min(t.n - ch * kC, kC);
+        ++ch;
     };
-    gate(0);
-    if (warp == 3) products(0);
+    const int total = s.total;
+    if (total == 0) return;
+    fetch();
+    if (warp == 3) products(0, valid);
     // A pass makes L of its chunk, then M's pieces of the chunk before (which the inverse warps have had the time since then
     // for), then A; the last one only M's pieces.
     float strength = 0.f;
 #pragma unroll 1
-    for (int ch = 0;; ++ch) {
-        const int st = ch & 1, k4 = ch & 3;
-        const uint32_t par2 = (ch >> 1) & 1;
-        if (ch < t.chunks) {
+    for (int g = 0;; ++g) {
+        const int st = g & 1, k4 = g & 3;
+        const uint32_t par2 = (g >> 1) & 1;
+        if (g < total) {
         strength = b;
         float up = a, down = a, grow = fmaxf(a, 1.f);
         if (!query) {
@@ -702,15 +752,15 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
             }
         }
         named_bar(kBarGate, 128);
-        if (ch + 1 < t.chunks) gate(ch + 1);
+        if (g + 1 < total) fetch();
         if (!query) {
-            const float g = i < 32 ? up : up * s.gates[0];
+            const float G = i < 32 ? up : up * s.gates[0];
             s.b[k4][i] = strength;
-            s.G[k4][i] = g;
-            s.bG[k4][i] = -strength * g;
+            s.G[k4][i] = G;
+            s.bG[k4][i] = -strength * G;
             s.tail[k4][i] = i < 32 ? down * s.gates[1] : down;
         }
-        waits.on(s.bar_kk, ch & 1);
+        waits.on(s.bar_kk, g & 1);
         tc_fence_after();
         if (query) {
             // A's unit, from a bound: |q_i.k_j| times what the gates can add
@@ -729,14 +779,14 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         }
 #pragma unroll 1
         for (int turn = 0; turn < 2; ++turn) {
-            if (turn && ch > 0) take_inverse(ch - 1);
-            if (ch == t.chunks || query != (turn == 1)) continue;
+            if (turn && g > 0) take_inverse(g - 1);
+            if (g == total || query != (turn == 1)) continue;
             // key rows: L (the one that was in its place has become M, and that has been taken: by these warps); query rows: A
             float d = strength;                   // D_ij (times b_i, or in A's unit), from j = i down
             if (query) {
                 named_bar(kBarQuery, 64);
                 const Unit u = unit_of(fmaxf(s.a_top[0], s.a_top[1]) * s.grow[0] * s.grow[1]);
-                if (ch >= 2) waits.on(s.gused[st], par2 ^ 1u);
+                if (g >= 2) waits.on(s.gused[st], par2 ^ 1u);
                 if (tid == 64) s.a_back[k4] = u.back;
                 d = u.scale;
             }
@@ -776,10 +826,10 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
                 if (lane == 0) mbar_arrive(smem_u32(&s.lready[st]));
             }
         }
-        if (ch == t.chunks) break;
+        if (g == total) break;
         warp_arrive(smem_u32(&s.gready[st]), lane);
         named_bar(kBarGate, 128);                 // k.k and q.k have been read
-        if (warp == 3 && ch + 1 < t.chunks) products(ch + 1);
+        if (warp == 3 && g + 1 < total) products(g + 1, valid);
     }
     if (warp == 3) {
         if (elect_lane()) tc_commit(smem_u32(&s.last_kk));
@@ -838,15 +888,15 @@ __device__ __forceinline__ void invert16(float *B, int lane)
     }
 }
 
-__device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillShared &s, const Tile &t)
+__device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillShared &s)
 {
     const int tid = threadIdx.x - kInv0, lane = tid & 31, warp = tid >> 5;
     Waits waits{p.polls};
 #pragma unroll 1
-    for (int ch = 0; ch < t.chunks; ++ch) {
-        const int st = ch & 1;
+    for (int g = 0; g < s.total; ++g) {
+        const int st = g & 1;
         float *L = s.L[st];
-        waits.on(s.lready[st], (ch >> 1) & 1);
+        waits.on(s.lready[st], (g >> 1) & 1);
         // M by blocks of 16, 32 and 64: M21 = -M22 (L21 M11)
         invert16(L + warp * 16 * (kLS + 1), lane);
         named_bar(kBarInv, 128);
@@ -883,9 +933,10 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
 
 // The loops stay rolled: a product's few instructions are fetched once and run from the instruction
 // buffer, where straight-line code waits longer for its next line than for the tensor cores.
-__device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared &s, const Tile &t)
+__device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared &s)
 {
     Waits waits{p.polls};
+    const int total = s.total;
     bool ok = true;
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
         ok = ok && __all_sync(0xffffffffu, waits.on(bar, parity));
@@ -904,17 +955,17 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
         }
     };
 #pragma unroll 1
-    for (int ch = 0; ch < t.chunks; ++ch) {
-        const int st = ch & 1, sk = ch % kStages;
-        const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
+    for (int g = 0; g < total; ++g) {
+        const int st = g & 1, sk = g % kStages;
+        const uint32_t par = g & 1, par2 = (g >> 1) & 1;
         const uint32_t kq = smem_u32(s.KQ[sk]);
-        if (!wait(s.full[sk], (ch / kStages) & 1) || !wait(s.gready[st], par2)) break;
+        if (!wait(s.full[sk], (g / kStages) & 1) || !wait(s.gready[st], par2)) break;
         // S times the keys (rows 0..63 of the tile) or the queries (64..127), 32 features and a piece of S at a time: both
         // threads' first half of the features, then the second
 #pragma unroll 1
         for (int step = 0; step < 4; ++step) {
             const int half = step & 1;
-            if (step < 2 ? !wait(s.have_s[half], par) : step == 2 && ch > 0 && !wait(s.read_o, par ^ 1u)) break;
+            if (step < 2 ? !wait(s.have_s[half], par) : step == 2 && g > 0 && !wait(s.read_o, par ^ 1u)) break;
             if (elect_lane()) {
                 const uint32_t d = step < 2 ? kColDK : kColDQ;
                 const uint64_t b0 = smem_desc_sw128(kq + (step < 2 ? 0 : kC * 128)) + (uint64_t)(half * 4);
@@ -968,34 +1019,46 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
     waits.end(s);
 }
 
-__device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShared &s, const Tile &t, int h, const CUtensorMap &qmap,
-                                            const CUtensorMap &kmap, const CUtensorMap &vmap)
+__device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShared &s, const CUtensorMap &qmap, const CUtensorMap &kmap,
+                                            const CUtensorMap &vmap)
 {
-    const int hk = h / p.group;
     Waits waits{p.polls};
-    const bool withheld = (p.debug_flags & 1) && blockIdx.x == 0 && blockIdx.y == 0;
-    int kq_issued = 0, v_issued = 0;
-    for (int ch = 0; ch < t.chunks; ++ch) {
-        const int sk = ch % kStages, sv = ch & 1, row = t.row0 + ch * kC;
-        const uint32_t kq_bar = smem_u32(&s.full[sk]), v_bar = smem_u32(&s.vfull[sv]), kq = smem_u32(s.KQ[sk]);
-        if (ch >= kStages && !waits.on(s.empty[sk], ((ch / kStages) & 1) ^ 1)) break;
-        mbar_expect_tx(kq_bar, kKqBytes);
-        if (withheld) break;
+    const bool withheld = (p.debug_flags & 1) && blockIdx.x == 0;
+    int g = 0, kq_issued = 0, v_issued = 0;
+    bool go = true;
+    Walk t;
+#pragma unroll 1
+    while (go && t.next(p, s)) {
+        if (p.S0 && t.chunks)                     // the state, for when its turn comes
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.S0 + ((size_t)t.r * p.H + t.h) * kD * kD),
+                         "r"((uint32_t)(kD * kD * sizeof(float)))
+                         : "memory");
+        const int hk = t.h / p.group;
+#pragma unroll 1
+        for (int ch = 0; go && ch < t.chunks; ++ch, ++g) {
+            const int sk = g % kStages, sv = g & 1, row = t.row0 + ch * kC;
+            const uint32_t kq_bar = smem_u32(&s.full[sk]), v_bar = smem_u32(&s.vfull[sv]), kq = smem_u32(s.KQ[sk]);
+            go = g < kStages || waits.on(s.empty[sk], ((g / kStages) & 1) ^ 1u);
+            if (!go) break;
+            mbar_expect_tx(kq_bar, kKqBytes);
+            go = !withheld;
+            if (!go) break;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            tma_load_2d(kq + half * 128 * 128, &kmap, hk * kD + 64 * half, row, kq_bar);
-            tma_load_2d(kq + half * 128 * 128 + kC * 128, &qmap, hk * kD + 64 * half, row, kq_bar);
+            for (int half = 0; half < 2; ++half) {
+                tma_load_2d(kq + half * 128 * 128, &kmap, hk * kD + 64 * half, row, kq_bar);
+                tma_load_2d(kq + half * 128 * 128 + kC * 128, &qmap, hk * kD + 64 * half, row, kq_bar);
+            }
+            kq_issued = g + 1;
+            go = g < 2 || waits.on(s.vempty[sv], ((g >> 1) & 1) ^ 1u);
+            if (!go) break;
+            mbar_expect_tx(v_bar, kVBytes);
+            tma_load_2d(smem_u32(s.V[sv]), &vmap, t.h * kD, row, v_bar);
+            v_issued = g + 1;
         }
-        kq_issued = ch + 1;
-        if (ch >= 2 && !waits.on(s.vempty[sv], ((ch >> 1) & 1) ^ 1)) break;
-        mbar_expect_tx(v_bar, kVBytes);
-        tma_load_2d(smem_u32(s.V[sv]), &vmap, h * kD, row, v_bar);
-        v_issued = ch + 1;
     }
     // no copy into shared memory in flight at the end
-    for (int ch = max(kq_issued - kStages, 0); ch < kq_issued; ++ch)
-        drain(s.full[ch % kStages], (ch / kStages) & 1, p);
-    for (int ch = max(v_issued - 2, 0); ch < v_issued; ++ch) drain(s.vfull[ch & 1], (ch >> 1) & 1, p);
+    for (int i = max(kq_issued - kStages, 0); i < kq_issued; ++i) drain(s.full[i % kStages], (i / kStages) & 1, p);
+    for (int i = max(v_issued - 2, 0); i < v_issued; ++i) drain(s.vfull[i & 1], (i >> 1) & 1, p);
     waits.end(s);
 }
 
@@ -1006,21 +1069,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     PrefillShared &s = *reinterpret_cast<PrefillShared *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int h = blockIdx.x, r = blockIdx.y;
-    const int o0 = p.off[r], o1 = p.off[r + 1];
-    if (o0 < 0 || o1 < o0 || o1 > p.n_rows) {
-        if (tid == 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
-        return;
-    }
-    const Tile t{o0, o1 - o0, (o1 - o0 + kC - 1) / kC};
-    if (t.n == 0) {
-        // no token: the state stays what it was
-        const size_t at = ((size_t)r * p.H + h) * kD * kD;
-        if (p.state != p.S0)
-            for (int e = tid; e < kD * kD / 4; e += kThreads)
-                reinterpret_cast<float4 *>(p.state + at)[e] =
-                    p.S0 ? reinterpret_cast<const float4 *>(p.S0 + at)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
-        return;
+    {
+        // the requests by their rows, and this CTA's chunks
+        int32_t *rows = reinterpret_cast<int32_t *>(s.KQ[0]);
+        for (int r = tid; r < p.n_req; r += kThreads) {
+            const int o0 = p.off[r], o1 = p.off[r + 1];
+            rows[r] = o0 < 0 || o1 < o0 || o1 > p.n_rows ? 0 : o1 - o0;
+        }
+        if (tid == 0) s.total = 0;
+        __syncthreads();
+        for (int r = tid; r < p.n_req; r += kThreads) {
+            const int mine = rows[r];
+            int rank = 0;
+            for (int j = 0; j < p.n_req; ++j) rank += rows[j] > mine || (rows[j] == mine && j < r);
+            s.order[rank] = (uint16_t)r;
+        }
+        __syncthreads();
+        int chunks = 0;
+        for (uint32_t cycle = tid, at; (at = item(cycle)) < p.items; cycle += kThreads)
+            chunks += (rows[s.order[at / (uint32_t)p.H]] + kC - 1) / kC;
+        if (chunks) atomicAdd(&s.total, chunks);
     }
     if (tid == 0) {
         for (int st = 0; st < kStages; ++st) {
@@ -1065,27 +1133,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if (tid < kToken0) {
         regs_inc<kRegsState>();
-        state_warps(p, s, t, r, h);
-        if (tid == 0 && s.abort) atomicCAS(p.status, 0, (int32_t)W12_E_TIMEOUT);
-        tc_fence_after();
-        if (warp == 0) tmem_dealloc(s.tmem, 512);
-        return;
-    }
-    if (tid < kGate0) {
-        token_warps(p, s, t, h);
+        state_warps(p, s);
+    } else if (tid < kGate0) {
+        token_warps(p, s);
     } else if (tid < kInv0) {
         regs_dec<kRegsGate>();
-        gate_warps(p, s, t, h);
+        gate_warps(p, s);
     } else if (tid < kIssue0) {
         regs_dec<kRegsInv>();
-        inverse_warps(p, s, t);
+        inverse_warps(p, s);
     } else {
         regs_dec<kRegsIssue>();
-        if (warp == kIssue0 / 32) issue_warp(p, s, t);
-        if (tid == kIssue0 + 32) copy_thread(p, s, t, h, qmap, kmap, vmap);
+        if (warp == kIssue0 / 32) issue_warp(p, s);
+        if (tid == kIssue0 + 32) copy_thread(p, s, qmap, kmap, vmap);
     }
     tc_fence_before();
-    named_bar(0, kThreads);                       // (the state warps' is in their role)
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && s.abort) atomicCAS(p.status, 0, (int32_t)W12_E_TIMEOUT);
+    if (warp == 0) tmem_dealloc(s.tmem, 512);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -1145,12 +1211,14 @@ int launch_gdn_prefill(const GdnSeqArgs &a, void *stream)
     p.off = a.off;
     p.H = a.H;
     p.group = a.H / a.Hk;
+    p.n_req = a.n_req;
+    p.items = (uint32_t)a.n_req * (uint32_t)a.H;
     p.n_rows = a.n_rows;
     p.polls = (uint32_t)std::min<uint64_t>(a.timeout_ns / kWaitSleepNs + 1, 1u << 31);
     p.status = a.status;
     p.debug_flags = a.debug_flags;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(a.H, a.n_req);
+    cfg.gridDim = dim3((uint32_t)std::min<int64_t>((int64_t)a.H * a.n_req, a.num_sms));   // one CTA fills an SM
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(PrefillShared) + 1024;
     cfg.stream = static_cast<cudaStream_t>(stream);

@@ -721,6 +721,7 @@ w12_status gdn_seq_args(const w12_gdn_rows *L, const float *S0, float *state, fl
         if (std::max({L->q_stride, L->k_stride, L->v_stride}) >= INT64_C(1) << 38) return W12_E_UNSUPPORTED;
     }
     a = GdnSeqArgs{};
+    a.num_sms = num_sms();
     a.H = L->n_heads;
     a.Hk = L->n_qk_heads;
     a.n_rows = L->n_rows;

@@ -163,6 +163,7 @@ int launch_gdn(const GdnArgs &a, int mode, void *stream);
 // recurrent layer over prompts (k_gdn_prefill.cu) and single tokens (k_gdn_step.cu)
 struct GdnSeqArgs {
     int32_t H, Hk, n_req, n_rows;   // value heads, query/key heads
+    int num_sms;
     const uint16_t *q, *k, *v;
     int64_t q_stride, k_stride, v_stride;   // elements between rows
     const float *alpha, *beta;      // [n_rows][H]
