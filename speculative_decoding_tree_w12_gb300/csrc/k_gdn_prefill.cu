@@ -25,10 +25,10 @@
 // it; the rest (A, M, U A^T and the outputs) is other warps' work, a chunk ahead or beside it:
 //  * state warps (0..7; two threads to a state row): S, which stays in their registers, and U scaled for S',
 //  * token warps (8..15; two threads to a state row): X, U for A, and the outputs,
-//  * gate warps (16..19; a thread to a row of k.k or q.k): the gates' products, L, A, and M's pieces,
+//  * gate warps (16..19; a thread to a row of k.k or q.k): the gates' products, L and A,
 //  * inverse warps (20..23): M from L, by four 16 x 16 blocks whose columns are solved in registers and
 //    the blocks below them from those,
-//  * warp 24 issues the products with the state, warp 25 the copies by TMA.
+//  * warp 24 issues the products with the state, warp 25 the copies by TMA, warps 26 and 27 make M's pieces.
 // What a chunk takes is the warps' instructions, not the products (a quarter of its time): of those the cutting into
 // pieces, three BF16 pieces 11 cycles of a scheduler for two values of 32 lanes, two F16 pieces 5.  The products are issued
 // in rolled loops and the code is kept short: straight-line code of a few times this length spent half its time on its own way in.
@@ -51,7 +51,7 @@ constexpr int kC = 64;              // tokens of a chunk
 constexpr int kThreads = 32 * 28;
 // the roles' first threads, and their registers (the launch's where they are equal to it)
 constexpr int kToken0 = 256, kGate0 = 512, kInv0 = 640, kIssue0 = 768;
-constexpr int kRegsLaunch = 72, kRegsState = 104, kRegsGate = 64, kRegsInv = 56, kRegsIssue = 32;
+constexpr int kRegsLaunch = 72, kRegsState = 104, kRegsGate = 56, kRegsInv = 56, kRegsIssue = 40;
 static_assert(256 * (kRegsState + kRegsLaunch) + 128 * (kRegsGate + kRegsInv + kRegsIssue) <= kThreads * kRegsLaunch, "register shares");
 
 // tensor memory columns: all 512 are one CTA's, from column 0 on
@@ -64,7 +64,7 @@ constexpr uint32_t kColKK = 448;    // k.k (lanes 0..63) and q.k (lanes 64..127)
 
 constexpr int kLS = 68;             // FP32 row stride of L and M (16-byte rows, 4 banks apart)
 constexpr int kTS = 36, kTS16 = 20; // and of products in between, of 32 and 16 columns
-constexpr int kBarGate = 1, kBarInv = 6, kBarQuery = 7;   // named barriers of the gate and of the inverse warps, of the gate warps' latter two
+constexpr int kBarGate = 1, kBarInv = 6, kBarQuery = 7, kBarPiece = 8;   // named barriers of the gate and of the inverse warps, of the gate warps' latter two
 constexpr int kBarRow = 2;                 // and of the two token warps of 32 state rows (2 .. 5)
 constexpr int kStages = 3;          // of keys and queries (their chunk is prepared while two others are in use)
 
@@ -90,7 +90,7 @@ struct PrefillShared {
     unsigned long long full[kStages], empty[kStages];   // keys and queries
     unsigned long long vfull[2], vempty[2];             // values
     unsigned long long gready[2], gused[2];             // A and the gates' products are there; A has been read
-    unsigned long long lready[2], inverted[2];          // L is there, M in its place
+    unsigned long long lready[2], inverted[2], lfree[2];   // L is there, M in its place, M taken from there
     unsigned long long mready[2];                       // M is there (two barriers for one M: a waiter may be a phase late)
     unsigned long long bar_kk;
     unsigned long long have_s[2], have_us[2], have_x, have_u;   // operands written (S and U for S' by halves)
@@ -257,6 +257,14 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&x)[N])
               "=f"(x[i + 13]), "=f"(x[i + 14]), "=f"(x[i + 15])
             : "r"(taddr + i)
             : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&x)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "r"(taddr)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_put(uint32_t taddr, const float (&x)[16])
@@ -509,38 +517,37 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
     for (int ch = 0; ch < t.chunks; ++ch, ++g) {
         const int st = g & 1, k4 = g & 3;
         const uint32_t par = g & 1, par2 = (g >> 1) & 1;
-        // X = b (v - G S k), over S k
+        // X = b (v - G S k)
         wait(s.vfull[st], par2);
         wait(s.gready[st], par2);
         wait(s.done_k, par);
-        float top = 0.f;
-#pragma unroll 1
-        for (int q = t0; q < t0 + 32; q += 16) {
-            float d[16], x[16], f[16];
-            tmem_ld<16>(tm + kColDK + q, d);
-            const uint16_t *v = s.V[st] + q * kD + c;
+        float x[32], top = 0.f;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = __uint_as_float((uint32_t)v[j * kD] << 16);
-            read_n(s.b[k4] + q, f);
-            mul_n(x, f);
-            read_n(s.bG[k4] + q, f);
+        for (int q = 0; q < 32; q += 8) {
+            float d[8], f[8], e[8];
+            const uint16_t *v = s.V[st] + (t0 + q) * kD + c;
+            tmem_ld8(tm + kColDK + t0 + q, d);
+            read_n(s.b[k4] + t0 + q, e);
+            read_n(s.bG[k4] + t0 + q, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] *= __uint_as_float((uint32_t)v[j * kD] << 16);
             tmem_ld_wait();
-            fma_n(f, d, x);
-            top = fmaxf(top, top_of(x));
-            tmem_put(tm + kColDK + q, x);
+            fma_n(f, d, e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[q + j] = e[j];
+            top = fmaxf(top, top_of(e));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.vempty[st]));
         const Unit ux = unit_of(row_top(s.top[0], top));
         if (part == 0) s.x_back[c] = ux.back;
-        tmem_st_wait();
-#pragma unroll 1
-        for (int q = t0; q < t0 + 32; q += 16) {
-            float x[16];
-            tmem_ld<16>(tm + kColDK + q, x);
-            tmem_ld_wait();
-            scale_n(x, ux.scale);
-            pieces2(x, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColX + 32 * piece + q / 2, w); });
+        scale_n(x, ux.scale);
+#pragma unroll
+        for (int q = 0; q < 32; q += 16) {
+            float z[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z[j] = x[q + j];
+            pieces2(z, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColX + 32 * piece + (t0 + q) / 2, w); });
         }
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_x), lane);
@@ -671,38 +678,6 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         }
         __syncwarp();
     };
-    // M's pieces of a chunk, eight columns to a thread and turn: the upper rows' left half, then 16 lower rows at a time
-    auto take_inverse = [&](int g) {
-        const int st = g & 1, k4 = g & 3;
-        waits.on(s.inverted[st], (g >> 1) & 1);
-        if (g > 0) waits.on(s.done_u, (g & 1) ^ 1u);        // the M before it has been read
-        if (tid == 0) s.m_top[(g + 1) & 3] = 0;
-#pragma unroll 1
-        for (int q = 0; q < 3; ++q) {
-            const int row = q == 0 ? tid >> 2 : 16 + 16 * q + (tid >> 3), col = (q == 0 ? tid & 3 : tid & 7) * 8;
-            float x[8];
-            read_n(s.L[st] + row * kLS + col, x);
-            float top = top_of(x);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float other = __shfl_xor_sync(0xffffffffu, top, 4);
-            if (q) top = fmaxf(top, other);
-            const Unit u = unit_of(top);
-            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-            if (lane == 0) atomicMax(&s.m_top[k4], most);
-            if (col == 0) {
-                s.m_unit[k4][row] = u.back;
-                s.m_tail[k4][row] = u.back * s.tail[k4][row];
-            }
-            scale_n(x, u.scale);
-            pieces2(x, [&](int piece, const uint32_t (&w)[4]) {
-                *reinterpret_cast<uint4 *>(s.M[piece] + row * 128 + (((col >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            });
-        }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.mready[st]));
-    };
     // the next chunk: the gate and the strength of this thread's token (1 and 0 behind the end), the rows
     Walk t;
     int ch = 0, valid = 0;
@@ -723,15 +698,11 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
     if (total == 0) return;
     fetch();
     if (warp == 3) products(0, valid);
-    // A pass makes L of its chunk, then M's pieces of the chunk before (which the inverse warps have had the time since then
-    // for), then A; the last one only M's pieces.
-    float strength = 0.f;
 #pragma unroll 1
-    for (int g = 0;; ++g) {
+    for (int g = 0; g < total; ++g) {
         const int st = g & 1, k4 = g & 3;
         const uint32_t par2 = (g >> 1) & 1;
-        if (g < total) {
-        strength = b;
+        const float strength = b;
         float up = a, down = a, grow = fmaxf(a, 1.f);
         if (!query) {
             // products of the gates from this block of 32 tokens' start to token i, and from behind it to the block's
@@ -776,19 +747,17 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
             const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
             if (lane == 0) s.a_top[warp & 1] = __uint_as_float(most);
         }
-        }
-#pragma unroll 1
-        for (int turn = 0; turn < 2; ++turn) {
-            if (turn && g > 0) take_inverse(g - 1);
-            if (g == total || query != (turn == 1)) continue;
-            // key rows: L (the one that was in its place has become M, and that has been taken: by these warps); query rows: A
-            float d = strength;                   // D_ij (times b_i, or in A's unit), from j = i down
+        // D_ij (times b_i, or in A's unit), from j = i down, times the row of k.k or q.k
+        {
+            float d = strength;
             if (query) {
                 named_bar(kBarQuery, 64);
                 const Unit u = unit_of(fmaxf(s.a_top[0], s.a_top[1]) * s.grow[0] * s.grow[1]);
                 if (g >= 2) waits.on(s.gused[st], par2 ^ 1u);
                 if (tid == 64) s.a_back[k4] = u.back;
                 d = u.scale;
+            } else if (g >= 2) {
+                waits.on(s.lfree[st], par2 ^ 1u);
             }
             const int last = query ? i : i - 1;   // the row's last entry
 #pragma unroll 1
@@ -826,7 +795,6 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
                 if (lane == 0) mbar_arrive(smem_u32(&s.lready[st]));
             }
         }
-        if (g == total) break;
         warp_arrive(smem_u32(&s.gready[st]), lane);
         named_bar(kBarGate, 128);                 // k.k and q.k have been read
         if (warp == 3 && g + 1 < total) products(g + 1, valid);
@@ -1019,6 +987,52 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
     waits.end(s);
 }
 
+// M's pieces, eight columns to a thread and turn: the upper rows' left half (four threads to a row), then the lower rows (eight)
+__device__ __forceinline__ void piece_warps(const PrefillParams &p, PrefillShared &s)
+{
+    const int tid = threadIdx.x - kIssue0 - 64, lane = tid & 31;
+    Waits waits{p.polls};
+#pragma unroll 1
+    for (int g = 0; g < s.total; ++g) {
+        const int st = g & 1, k4 = g & 3;
+        waits.on(s.inverted[st], (g >> 1) & 1);
+        if (g > 0) waits.on(s.done_u, (g & 1) ^ 1u);          // the M before it has been read
+        if (tid == 0) s.m_top[(g + 1) & 3] = 0;
+        named_bar(kBarPiece, 64);
+        uint32_t most = 0;
+#pragma unroll 1
+        for (int q = 0; q < 6; ++q) {
+            const int row = q < 2 ? 16 * q + (tid >> 2) : 16 + 8 * q + (tid >> 3), col = (q < 2 ? tid & 3 : tid & 7) * 8;
+            float x[8];
+            read_n(s.L[st] + row * kLS + col, x);
+            float top = top_of(x);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float other = __shfl_xor_sync(0xffffffffu, top, 4);
+            if (q >= 2) top = fmaxf(top, other);
+            const Unit u = unit_of(top);
+            most = max(most, __float_as_uint(top));
+            if (col == 0) {
+                s.m_unit[k4][row] = u.back;
+                s.m_tail[k4][row] = u.back * s.tail[k4][row];
+            }
+            scale_n(x, u.scale);
+            pieces2(x, [&](int piece, const uint32_t (&w)[4]) {
+                *reinterpret_cast<uint4 *>(s.M[piece] + row * 128 + (((col >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            });
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) atomicMax(&s.m_top[k4], most);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&s.mready[st]));
+            mbar_arrive(smem_u32(&s.lfree[st]));
+        }
+    }
+    waits.end(s);
+}
+
 __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShared &s, const CUtensorMap &qmap, const CUtensorMap &kmap,
                                             const CUtensorMap &vmap)
 {
@@ -1102,7 +1116,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&s.gused[st]), 1);
             mbar_init(smem_u32(&s.lready[st]), 2);
             mbar_init(smem_u32(&s.inverted[st]), 4);
-            mbar_init(smem_u32(&s.mready[st]), 4);
+            mbar_init(smem_u32(&s.lfree[st]), 2);
+            mbar_init(smem_u32(&s.mready[st]), 2);
         }
         for (unsigned long long *b : {&s.bar_kk, &s.done_k, &s.done_q, &s.done_u, &s.done_s, &s.done_o, &s.last, &s.last_kk}) mbar_init(smem_u32(b), 1);
         for (unsigned long long *b : {&s.have_s[0], &s.have_s[1], &s.have_us[0], &s.have_us[1], &s.have_x, &s.have_u, &s.read_o}) mbar_init(smem_u32(b), 8);
@@ -1145,6 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         regs_dec<kRegsIssue>();
         if (warp == kIssue0 / 32) issue_warp(p, s);
+        if (tid >= kIssue0 + 64) piece_warps(p, s);
         if (tid == kIssue0 + 32) copy_thread(p, s, qmap, kmap, vmap);
     }
     tc_fence_before();
