@@ -55,11 +55,12 @@ constexpr int kRegsLaunch = 72, kRegsState = 104, kRegsGate = 56, kRegsInv = 56,
 static_assert(256 * (kRegsState + kRegsLaunch) + 128 * (kRegsGate + kRegsInv + kRegsIssue) <= kThreads * kRegsLaunch, "register shares");
 
 // tensor memory columns: all 512 are one CTA's, from column 0 on
-constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; then three of U for S', 32 each
+constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; then three of U for S', 32 each,
+constexpr uint32_t kColUA = 128;    // and, over S's last, two of U for A
 constexpr uint32_t kColDQ = 192;    // S q; then, scaled and with U A added, the outputs
 constexpr uint32_t kColDK = 256;    // S k; then, with the next 64 columns, U K
-constexpr uint32_t kColU = 320;     // U
-constexpr uint32_t kColX = 384;     // X's two pieces, then U's two for A
+constexpr uint32_t kColX = 320;     // X's two pieces
+constexpr uint32_t kColU = 384;     // U
 constexpr uint32_t kColKK = 448;    // k.k (lanes 0..63) and q.k (lanes 64..127) of the next chunk
 
 constexpr int kLS = 68;             // FP32 row stride of L and M (16-byte rows, 4 banks apart)
@@ -148,18 +149,19 @@ __device__ __forceinline__ bool elect_lane()
     return e != 0;
 }
 
-// BF16 operand whose rows (of 64 features, 128-byte swizzle) are its K index: 8-row groups 1024 bytes
-// apart, the next 64 features `half` bytes on
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t half)
+// Matrix descriptors from their lower word (address and leading offset): rows of 64 values under the 128-byte swizzle, eight
+// rows 1024 bytes on.  desc_k: the rows are the operand's own; desc_mn: they are its K index, the next 64 values
+// 128 rows of 128 bytes further on.
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr) { return (saddr >> 4) & 0x3FFFu; }
+__device__ __forceinline__ uint64_t desc_of(uint32_t low)
 {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(half >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
+    constexpr uint32_t high = (1024u >> 4) | (1u << 14) | (2u << 29);   // stride, version 1, swizzle
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "n"(high));
     return d;
 }
+__device__ __forceinline__ uint64_t desc_k(uint32_t low) { return desc_of(low | (1u << 16)); }
+__device__ __forceinline__ uint64_t desc_mn(uint32_t low) { return desc_of(low | ((128u * 128u / 16u) << 16)); }
 
 constexpr uint32_t kBMnMajor = 1u << 16;   // instruction descriptor: B's rows are its K index
 constexpr uint32_t kIdescF16 = (1u << 4) | ((uint32_t)(kC >> 3) << 17) | ((128u >> 4) << 24);   // F16 operands, both K-major, N = 64
@@ -430,7 +432,8 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
     for (int end = g + t.chunks; g < end; ++g) {
         const int k4 = g & 3;
         const uint32_t par = g & 1, par2 = (g >> 1) & 1;
-        // S's pieces, a half of this thread's features at a time
+        // S's pieces, a half of this thread's features at a time (over the last chunk's U, which A has been multiplied by)
+        if (g > 0) wait(s.done_o, par ^ 1u);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             float z[16];
@@ -449,33 +452,38 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
         wait(s.have_x, par);
         const float back = s.x_back[c];
         wait(s.done_u, par);
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-            const int t0 = 32 * part + 16 * q;
-            float x[16], f[16];
-            tmem_ld<16>(tm + kColU + t0, x);
-            read_n(s.m_tail[k4] + t0, f);
-            scale_n(f, back);
+        {
+            float x[32];
+            tmem_ld<32>(tm + kColU + 32 * part, x);
             tmem_ld_wait();
-            mul_n(x, f);
-            pieces3<8>(x, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColS + 32 * piece + t0 / 2, w); });
-            tmem_st_wait();
-            warp_arrive(smem_u32(&s.have_us[q]), lane);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int t0 = 32 * part + 16 * q;
+                float y[16], f[16];
+                read_n(s.m_tail[k4] + t0, f);
+                scale_n(f, back);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = x[16 * q + j];
+                mul_n(y, f);
+                pieces3<8>(y, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColS + 32 * piece + t0 / 2, w); });
+                tmem_st_wait();
+                warp_arrive(smem_u32(&s.have_us[q]), lane);
+            }
         }
 
         // S' = G_C S + U K
         const float gc = s.G[k4][kC - 1];
         wait(s.done_s, par);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float z[16];
-            tmem_ld<16>(tm + kColDK + 64 * part + 16 * q, z);
+        for (int q = 0; q < 2; ++q) {
+            float z[32];
+            tmem_ld<32>(tm + kColDK + 64 * part + 32 * q, z);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const float2 n = __ffma2_rn(make_float2(gc, gc), make_float2(S[16 * q + i], S[16 * q + i + 1]), make_float2(z[i], z[i + 1]));
-                S[16 * q + i] = n.x;
-                S[16 * q + i + 1] = n.y;
+            for (int i = 0; i < 32; i += 2) {
+                const float2 n = __ffma2_rn(make_float2(gc, gc), make_float2(S[32 * q + i], S[32 * q + i + 1]), make_float2(z[i], z[i + 1]));
+                S[32 * q + i] = n.x;
+                S[32 * q + i + 1] = n.y;
             }
         }
     }
@@ -582,7 +590,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
             tmem_put(tm + kColDQ + q, x);
         }
 
-        // U's pieces for A, over X's
+        // U's pieces for A, over S's last (S q is there)
         wait(s.done_u, par);
 #pragma unroll 1
         for (int q = t0; q < t0 + 32; q += 16) {
@@ -592,7 +600,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
             scale_n(f, ux.back * uu.scale);
             tmem_ld_wait();
             mul_n(x, f);
-            pieces2(x, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColX + 32 * piece + q / 2, w); });
+            pieces2(x, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColUA + 32 * piece + q / 2, w); });
         }
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_u), lane);
@@ -669,10 +677,10 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         if (elect_lane()) {
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-                const uint64_t x = smem_desc_sw128(kq + half * 128 * 128);
+                const uint32_t x = desc_low(kq + half * 128 * 128);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    tc_mma_ss(kColKK, x + (uint64_t)(ks * 2), x + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC), (uint32_t)(half | ks));
+                    tc_mma_ss(kColKK, desc_k(x + ks * 2), desc_k(x + ks * 2), idesc_bf16_f32(128, kC), (uint32_t)(half | ks));
             }
             tc_commit(smem_u32(&s.bar_kk));
         }
@@ -911,15 +919,26 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
         tc_fence_after();
         return ok;
     };
-    // two FP32 operands of two F16 pieces each, K = 64 tokens: high times high, high times low, low times high
-    auto pairs = [&](uint32_t d, const uint8_t *B, uint32_t add) {
-        const uint64_t b0 = smem_desc_sw128(smem_u32(B));
+    // U or U A: two FP32 operands of two F16 pieces each, K = 64 tokens: high times high, high times low, low times high
+    auto pairs = [&](uint32_t d, uint32_t a, const uint8_t *B, uint32_t add) {
+        const uint32_t b0 = desc_low(smem_u32(B));
 #pragma unroll 1
         for (int q = 0; q < 3; ++q) {
-            const uint64_t b = b0 + (q == 1 ? kC * 128 / 16 : 0);
-            const uint32_t a = kColX + (q == 2 ? 32 : 0);
+            const uint32_t b = b0 + (q == 1 ? kC * 128 / 16 : 0), aq = a + (q == 2 ? 32 : 0);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) tc_mma_ts(d, a + 8 * ks, b + (uint64_t)(ks * 2), kIdescF16, add | (uint32_t)(q | ks));
+            for (int ks = 0; ks < 4; ++ks) tc_mma_ts(d, aq + 8 * ks, desc_k(b + ks * 2), kIdescF16, add | (uint32_t)(q | ks));
+        }
+    };
+    // a half of both threads' features of S times the keys (rows 0..63 of the tile) or the queries (64..127)
+    auto product = [&](uint32_t d, uint32_t tile, int half) {
+        const uint32_t b = desc_low(tile) + half * 4;
+#pragma unroll 1
+        for (int piece = 0; piece < 3; ++piece) {
+            const uint32_t a = kColS + 64 * piece + 16 * half;
+            tc_mma_ts(d, a, desc_k(b), idesc_bf16_f32(128, kC), (uint32_t)(half | piece));
+            tc_mma_ts(d, a + 8, desc_k(b + 2), idesc_bf16_f32(128, kC), 1);
+            tc_mma_ts(d, a + 32, desc_k(b + 128 * 128 / 16), idesc_bf16_f32(128, kC), 1);
+            tc_mma_ts(d, a + 40, desc_k(b + 128 * 128 / 16 + 2), idesc_bf16_f32(128, kC), 1);
         }
     };
 #pragma unroll 1
@@ -928,46 +947,39 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
         const uint32_t par = g & 1, par2 = (g >> 1) & 1;
         const uint32_t kq = smem_u32(s.KQ[sk]);
         if (!wait(s.full[sk], (g / kStages) & 1) || !wait(s.gready[st], par2)) break;
-        // S times the keys (rows 0..63 of the tile) or the queries (64..127), 32 features and a piece of S at a time: both
-        // threads' first half of the features, then the second
 #pragma unroll 1
-        for (int step = 0; step < 4; ++step) {
-            const int half = step & 1;
-            if (step < 2 ? !wait(s.have_s[half], par) : step == 2 && g > 0 && !wait(s.read_o, par ^ 1u)) break;
+        for (int half = 0; half < 2; ++half) {
+            if (!wait(s.have_s[half], par)) break;
             if (elect_lane()) {
-                const uint32_t d = step < 2 ? kColDK : kColDQ;
-                const uint64_t b0 = smem_desc_sw128(kq + (step < 2 ? 0 : kC * 128)) + (uint64_t)(half * 4);
-#pragma unroll 1
-                for (int q = 0; q < 6; ++q) {
-                    const int piece = q >> 1, part = q & 1;
-                    const uint64_t b = b0 + (part ? 128 * 128 / 16 : 0);
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks)
-                        tc_mma_ts(d, kColS + 64 * piece + 32 * part + 16 * half + 8 * ks, b + (uint64_t)(ks * 2), idesc_bf16_f32(128, kC),
-                                  (uint32_t)(half | q | ks));
-                }
-                if (half) tc_commit(smem_u32(step < 2 ? &s.done_k : &s.done_q));
+                product(kColDK, kq, half);
+                if (half) tc_commit(smem_u32(&s.done_k));
             }
             __syncwarp();
         }
+        if (g > 0 && !wait(s.read_o, par ^ 1u)) break;
+        if (elect_lane()) {
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) product(kColDQ, kq + kC * 128, half);
+            tc_commit(smem_u32(&s.done_q));
+        }
+        __syncwarp();
         if (!wait(s.mready[st], par2) || !wait(s.have_x, par)) break;
         if (elect_lane()) {
-            pairs(kColU, s.M[0], 0);
+            pairs(kColU, kColX, s.M[0], 0);
             tc_commit(smem_u32(&s.done_u));
         }
         __syncwarp();
-        if (!wait(s.have_u, par)) break;          // (U has been read, which U K's columns take in)
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
             if (!wait(s.have_us[half], par)) break;
             if (elect_lane()) {
-                const uint64_t b = smem_desc_mn_sw128(kq, 128 * 128) + (uint64_t)(half * 16 * 128 / 16);
-#pragma unroll 1
-                for (int piece = 0; piece < 3; ++piece)
+                const uint32_t b = desc_low(kq) + half * (16 * 128 / 16);
 #pragma unroll
-                    for (int ks = 0; ks < 2; ++ks)
-                        tc_mma_ts(kColDK, kColS + 32 * piece + 8 * half + 16 * ks, b + (uint64_t)(ks * 32 * 128 / 16),
-                                  idesc_bf16_f32(128, kD) | kBMnMajor, (uint32_t)(half | piece | ks));
+                for (int piece = 0; piece < 3; ++piece) {
+                    const uint32_t a = kColS + 32 * piece + 8 * half;
+                    tc_mma_ts(kColDK, a, desc_mn(b), idesc_bf16_f32(128, kD) | kBMnMajor, (uint32_t)(half | piece));
+                    tc_mma_ts(kColDK, a + 16, desc_mn(b + 32 * 128 / 16), idesc_bf16_f32(128, kD) | kBMnMajor, 1);
+                }
                 if (half) {
                     tc_commit(smem_u32(&s.done_s));
                     tc_commit(smem_u32(&s.empty[sk]));
@@ -975,8 +987,9 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
             }
             __syncwarp();
         }
+        if (!wait(s.have_u, par)) break;
         if (elect_lane()) {
-            pairs(kColDQ, s.A[st][0], 1);
+            pairs(kColDQ, kColUA, s.A[st][0], 1);
             tc_commit(smem_u32(&s.done_o));
             tc_commit(smem_u32(&s.gused[st]));
         }
