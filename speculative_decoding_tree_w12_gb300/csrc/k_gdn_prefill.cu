@@ -25,9 +25,9 @@
 // it; the rest (A, M, U A^T and the outputs) is other warps' work, a chunk ahead or beside it:
 //  * state warps (0..7; two threads to a state row): S, which stays in their registers, and U scaled for S',
 //  * token warps (8..15; two threads to a state row): X, U for A, and the outputs,
-//  * gate warps (16..19; a thread to a row of k.k or q.k): the gates' products, L and A,
-//  * inverse warps (20..23): M from L, by four 16 x 16 blocks whose columns are solved in registers and
-//    the blocks below them from those,
+//  * gate warps (16..19; a thread to a row of k.k or q.k): the gates' products, L with the inverses of its four diagonal
+//    blocks of 16, whose columns are solved in registers, and A,
+//  * inverse warps (20..23): M, the blocks below those from them,
 //  * warp 24 issues the products with the state, warp 25 the copies by TMA, warps 26 and 27 make M's pieces.
 // What a chunk takes is the warps' instructions, not the products (a quarter of its time): of those the cutting into
 // pieces, three BF16 pieces 11 cycles of a scheduler for two values of 32 lanes, two F16 pieces 5.  The products are issued
@@ -63,19 +63,29 @@ constexpr uint32_t kColX = 320;     // X's two pieces
 constexpr uint32_t kColU = 384;     // U
 constexpr uint32_t kColKK = 448;    // k.k (lanes 0..63) and q.k (lanes 64..127) of the next chunk
 
-constexpr int kLS = 68;             // FP32 row stride of L and M (16-byte rows, 4 banks apart)
-constexpr int kTS = 36, kTS16 = 20; // and of products in between, of 32 and 16 columns
+// L, then M: three blocks of 32 x 32 (the one above the diagonal is zero), their FP32 rows 16-byte aligned and 4 banks apart
+constexpr int kLS = 36;
+constexpr int kL11 = 0, kL22 = 32 * kLS, kL21 = 2 * 32 * kLS, kLFloats = 3 * 32 * kLS;
 constexpr int kBarGate = 1, kBarInv = 6, kBarQuery = 7, kBarPiece = 8;   // named barriers of the gate and of the inverse warps, of the gate warps' latter two
 constexpr int kBarRow = 2;                 // and of the two token warps of 32 state rows (2 .. 5)
 constexpr int kStages = 3;          // of keys and queries (their chunk is prepared while two others are in use)
+
+// what a chunk is of
+struct Chunk {
+    int32_t row0, n;                // first row, rows
+    int32_t h;
+    int32_t pair;                   // r * H + h
+    int32_t first, last;            // whether it is its request's first or last
+};
+constexpr int kChunks = 8;          // descriptions kept
 
 struct PrefillShared {
     uint8_t KQ[kStages][2 * 128 * 128];   // [stage][feature half][key rows, query rows][64 BF16], 128-byte swizzle
     uint8_t A[2][2][kC * 128];      // pieces of A and M, rows of 64 F16, 128-byte swizzle
     uint8_t M[2][kC * 128];
     uint16_t V[2][kC * kD];
-    alignas(16) float L[2][kC * kLS];   // then, in place, M
-    alignas(16) float T[32 * kTS];
+    alignas(16) float L[2][kLFloats];   // then, in place, M
+    alignas(16) float T[32 * kLS];      // products in between
     alignas(16) float next[kC];     // the gates of tokens 1 .. 63, then 1
     alignas(16) float b[4][kC];     // of chunk c in [c % 4]: strengths, -b_i G_i, G_i, D_Ci
     alignas(16) float bG[4][kC];
@@ -88,6 +98,8 @@ struct PrefillShared {
     float a_top[2], a_back[4];      // largest magnitude of A's rows by halves, its power of two
     uint32_t m_top[4];              // largest magnitude in M, as its bits
     float gates[2], grow[2];        // products of the gates of tokens 0 .. 31 and 32 .. 63, and of those above 1
+    Chunk chunk[kChunks];           // of chunk c in [c % 8], by the thread that issues the copies
+    unsigned long long told[4];                         // it is there
     unsigned long long full[kStages], empty[kStages];   // keys and queries
     unsigned long long vfull[2], vempty[2];             // values
     unsigned long long gready[2], gused[2];             // A and the gates' products are there; A has been read
@@ -103,7 +115,8 @@ struct PrefillShared {
     int32_t total;                  // chunks of this CTA
     uint16_t order[w12i::kMaxBudget];   // the requests, those with the most rows first
 };
-static_assert(offsetof(PrefillShared, L) % 16 == 0 && sizeof(PrefillShared::L) % 32 == 0, "rows of four floats");
+static_assert(offsetof(PrefillShared, L) % 16 == 0 && kLFloats % 4 == 0, "rows of four floats");
+static_assert(offsetof(PrefillShared, T) == offsetof(PrefillShared, L) + sizeof(PrefillShared::L), "T behind L");
 static_assert(sizeof(PrefillShared) + 1024 <= 227 * 1024, "shared memory above the per-CTA limit");
 static_assert(offsetof(PrefillShared, M) % 1024 == 0 && offsetof(PrefillShared, A) % 1024 == 0, "swizzled tiles");
 static_assert(offsetof(PrefillShared, V) % 128 == 0 && offsetof(PrefillShared, full) % 8 == 0, "copies and barriers");
@@ -367,34 +380,19 @@ __device__ __forceinline__ void drain(unsigned long long &bar, uint32_t parity, 
 }
 
 // The (request, head) pairs of this CTA, one after another: the requests by their rows, the heads of one request beside one
-// another, dealt out to the CTAs forth and back, so that each gets a like share of long and short ones.  Every role walks
-// the same list on its own; the rings between them count the CTA's chunks through all of it.
+// another, dealt out to the CTAs forth and back, so that each gets a like share of long and short ones.  The rings count
+// the CTA's chunks through all of them.
+// a request's rows, or -1 where its offsets make no sense
+__device__ __forceinline__ int request_rows(const PrefillParams &p, int r)
+{
+    const int o0 = p.off[r], o1 = p.off[r + 1];
+    return o0 < 0 || o1 < o0 || o1 > p.n_rows ? -1 : o1 - o0;
+}
+
 __device__ __forceinline__ uint32_t item(uint32_t cycle)
 {
     return cycle * gridDim.x + (cycle & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
-
-struct Walk {
-    int32_t cycle = -1, r = 0, h = 0;
-    int32_t row0 = 0, n = 0, chunks = 0;   // the request's first row, its rows, chunks
-    bool bad = false;                      // offsets that make no sense
-
-    __device__ __forceinline__ bool next(const PrefillParams &p, const PrefillShared &s)
-    {
-        ++cycle;
-        const uint32_t at = item(cycle);
-        if (at >= p.items) return false;
-        const uint32_t rank = at / (uint32_t)p.H;
-        h = at - rank * p.H;
-        r = s.order[rank];
-        row0 = p.off[r];
-        n = p.off[r + 1] - row0;
-        bad = row0 < 0 || n < 0 || row0 + n > p.n_rows;
-        if (bad) n = 0;
-        chunks = (n + kC - 1) / kC;
-        return true;
-    }
-};
 
 // ---------------------------------------------------------------------------
 // state warps
@@ -410,26 +408,23 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
         waits.on(bar, parity);
         tc_fence_after();
     };
-    Walk t;
-    int g = 0;                                                            // chunks so far
-#pragma unroll 1
-    while (t.next(p, s)) {
-    if (t.bad) {
-        if (threadIdx.x == 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
-        continue;
-    }
-    const size_t at = (((size_t)t.r * p.H + t.h) * kD + c) * kD + 64 * part;   // this thread's half of the row
+    const int total = s.total;
     float S[64];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float4 x = p.S0 ? *reinterpret_cast<const float4 *>(p.S0 + at + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-        S[4 * i] = x.x;
-        S[4 * i + 1] = x.y;
-        S[4 * i + 2] = x.z;
-        S[4 * i + 3] = x.w;
-    }
 #pragma unroll 1
-    for (int end = g + t.chunks; g < end; ++g) {
+    for (int g = 0; g < total; ++g) {
+        wait(s.told[g & 3], (g >> 2) & 1);
+        const Chunk &t = s.chunk[g % kChunks];
+        const size_t at = ((size_t)t.pair * kD + c) * kD + 64 * part;     // this thread's half of the row
+        if (t.first) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float4 x = p.S0 ? *reinterpret_cast<const float4 *>(p.S0 + at + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                S[4 * i] = x.x;
+                S[4 * i + 1] = x.y;
+                S[4 * i + 2] = x.z;
+                S[4 * i + 3] = x.w;
+            }
+        }
         const int k4 = g & 3;
         const uint32_t par = g & 1, par2 = (g >> 1) & 1;
         // S's pieces, a half of this thread's features at a time (over the last chunk's U, which A has been multiplied by)
@@ -452,23 +447,18 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
         wait(s.have_x, par);
         const float back = s.x_back[c];
         wait(s.done_u, par);
-        {
-            float x[32];
-            tmem_ld<32>(tm + kColU + 32 * part, x);
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+            const int t0 = 32 * part + 16 * q;
+            float x[16], f[16];
+            tmem_ld<16>(tm + kColU + t0, x);
+            read_n(s.m_tail[k4] + t0, f);
+            scale_n(f, back);
             tmem_ld_wait();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int t0 = 32 * part + 16 * q;
-                float y[16], f[16];
-                read_n(s.m_tail[k4] + t0, f);
-                scale_n(f, back);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = x[16 * q + j];
-                mul_n(y, f);
-                pieces3<8>(y, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColS + 32 * piece + t0 / 2, w); });
-                tmem_st_wait();
-                warp_arrive(smem_u32(&s.have_us[q]), lane);
-            }
+            mul_n(x, f);
+            pieces3<8>(x, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColS + 32 * piece + t0 / 2, w); });
+            tmem_st_wait();
+            warp_arrive(smem_u32(&s.have_us[q]), lane);
         }
 
         // S' = G_C S + U K
@@ -486,12 +476,11 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
                 S[32 * q + i + 1] = n.y;
             }
         }
-    }
-    if (waits.left && !*(volatile int32_t *)&s.abort) {
+        if (t.last && waits.left && !*(volatile int32_t *)&s.abort) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            *reinterpret_cast<float4 *>(p.state + at + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-    }
+            for (int i = 0; i < 16; ++i)
+                *reinterpret_cast<float4 *>(p.state + at + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        }
     }
     waits.end(s);
 }
@@ -517,12 +506,9 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         return fmaxf(top, at[part ^ 1][c]);
     };
     // (Every loop over the tokens is rolled, 16 at a time: what lies between two of them lies in tensor memory.)
-    Walk t;
-    int g = 0;                                                            // chunks so far
+    const int total = s.total;
 #pragma unroll 1
-    while (t.next(p, s))
-#pragma unroll 1
-    for (int ch = 0; ch < t.chunks; ++ch, ++g) {
+    for (int g = 0; g < total; ++g) {
         const int st = g & 1, k4 = g & 3;
         const uint32_t par = g & 1, par2 = (g >> 1) & 1;
         // X = b (v - G S k)
@@ -608,8 +594,9 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         // o = G S q + U A
         wait(s.done_o, par);
         const size_t step = (size_t)p.H * kD;
-        float *dst = p.o + ((size_t)(t.row0 + ch * kC + t0) * p.H + t.h) * kD + c;
-        int left = t.n - ch * kC - t0;
+        const Chunk &t = s.chunk[g % kChunks];
+        float *dst = p.o + ((size_t)(t.row0 + t0) * p.H + t.h) * kD + c;
+        int left = t.n - t0;
 #pragma unroll 1
         for (int q = t0; q < t0 + 32; q += 16, left -= 16) {
             float x[16];
@@ -641,6 +628,42 @@ __device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, i
             *reinterpret_cast<uint4 *>(tile[piece] + row * 128 + (((col0 / 8 + q) ^ (row & 7)) << 4)) =
                 make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
     });
+}
+
+// Two lower-triangular 16 x 16 blocks with ones on their diagonals, one below the other's corner, inverted in place by one
+// warp, a column to a lane and four rows at a time: x_i = [i = j] - sum over l < i of L_il x_l.  A lane reads back only
+// what it wrote itself.
+__device__ __forceinline__ void invert16(float *L, int lane)
+{
+    float *B = L + (lane >> 4) * 16 * (kLS + 1);
+    const int col = lane & 15;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 16; r0 += 4) {
+        float *R = B + r0 * kLS;
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = r0 + i == col ? 1.f : 0.f;
+#pragma unroll 1
+        for (int l = 0; l < r0; l += 4) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = B[(l + e) * kLS + col];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = *reinterpret_cast<const float4 *>(R + i * kLS + l);
+                x[i] = fmaf(-v.x, y[0], fmaf(-v.y, y[1], fmaf(-v.z, y[2], fmaf(-v.w, y[3], x[i]))));
+            }
+        }
+        const float l10 = R[kLS + r0];
+        const float2 l2 = *reinterpret_cast<const float2 *>(R + 2 * kLS + r0);
+        const float4 l3 = *reinterpret_cast<const float4 *>(R + 3 * kLS + r0);
+        x[1] = fmaf(-l10, x[0], x[1]);
+        x[2] = fmaf(-l2.x, x[0], fmaf(-l2.y, x[1], x[2]));
+        x[3] = fmaf(-l3.x, x[0], fmaf(-l3.y, x[1], fmaf(-l3.z, x[2], x[3])));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) R[i * kLS + col] = x[i];
+    }
 }
 
 __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared &s)
@@ -686,30 +709,24 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         }
         __syncwarp();
     };
-    // the next chunk: the gate and the strength of this thread's token (1 and 0 behind the end), the rows
-    Walk t;
-    int ch = 0, valid = 0;
+    // the next chunk: the gate and the strength of this thread's token (1 and 0 behind the end), its rows
+    int valid = 0;
     float a = 1.f, b = 0.f;
-    auto fetch = [&] {
-        while (ch >= t.chunks) {
-            if (!t.next(p, s)) return;
-            ch = 0;
-        }
-        const int row = ch * kC + i;
-        const size_t at = (size_t)(t.row0 + row) * p.H + t.h;
-        a = row < t.n ? p.alpha[at] : 1.f;
-        b = row < t.n ? p.beta[at] : 0.f;
-        valid = min(t.n - ch * kC, kC);
-        ++ch;
+    auto fetch = [&](int g) {
+        waits.on(s.told[g & 3], (g >> 2) & 1);
+        const Chunk &t = s.chunk[g % kChunks];
+        const size_t at = (size_t)(t.row0 + i) * p.H + t.h;
+        valid = t.n;
+        a = i < valid ? p.alpha[at] : 1.f;
+        b = i < valid ? p.beta[at] : 0.f;
     };
     const int total = s.total;
-    if (total == 0) return;
-    fetch();
-    if (warp == 3) products(0, valid);
+    if (total > 0) fetch(0);
 #pragma unroll 1
     for (int g = 0; g < total; ++g) {
         const int st = g & 1, k4 = g & 3;
         const uint32_t par2 = (g >> 1) & 1;
+        if (warp == 3) products(g, valid);
         const float strength = b;
         float up = a, down = a, grow = fmaxf(a, 1.f);
         if (!query) {
@@ -731,7 +748,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
             }
         }
         named_bar(kBarGate, 128);
-        if (g + 1 < total) fetch();
+        if (g + 1 < total) fetch(g + 1);
         if (!query) {
             const float G = i < 32 ? up : up * s.gates[0];
             s.b[k4][i] = strength;
@@ -792,20 +809,22 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<float4 *>(s.L[st] + i * kLS + 16 * J + 4 * q) =
+                        *reinterpret_cast<float4 *>(s.L[st] + (i < 32 ? kL11 : J < 2 ? kL21 : kL22) + (i & 31) * kLS + 16 * (J & 1) + 4 * q) =
                             make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
                 }
             }
             if (query) {
                 fence_async_shared();
             } else {
+                // the diagonal blocks of 16 of this warp's rows are its own: it inverts them at once
+                __syncwarp();
+                invert16(s.L[st] + (warp ? kL22 : kL11), lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&s.lready[st]));
             }
         }
         warp_arrive(smem_u32(&s.gready[st]), lane);
         named_bar(kBarGate, 128);                 // k.k and q.k have been read
-        if (warp == 3 && g + 1 < total) products(g + 1, valid);
     }
     if (warp == 3) {
         if (elect_lane()) tc_commit(smem_u32(&s.last_kk));
@@ -818,52 +837,6 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
 // inverse warps
 // ---------------------------------------------------------------------------
 
-// Four columns of one row of Z = -/+ X Y: the sum over l0 <= l < l1 (multiples of 4); X its row, Y and Z from its columns on
-template <bool kNeg>
-__device__ __forceinline__ void tile_product(const float *X, const float *Y, int ys, float *Z, int l0, int l1)
-{
-    float2 acc[2] = {};
-#pragma unroll 2
-    for (int l = l0; l < l1; l += 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(X + l);
-        const float xe[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 y = *reinterpret_cast<const float4 *>(Y + (l + e) * ys);
-            const float2 f = make_float2(kNeg ? -xe[e] : xe[e], kNeg ? -xe[e] : xe[e]);
-            acc[0] = __ffma2_rn(f, make_float2(y.x, y.y), acc[0]);
-            acc[1] = __ffma2_rn(f, make_float2(y.z, y.w), acc[1]);
-        }
-    }
-    *reinterpret_cast<float4 *>(Z) = make_float4(acc[0].x, acc[0].y, acc[1].x, acc[1].y);
-}
-
-// A lower-triangular block with ones on its diagonal, inverted in place by one warp, a column to a lane
-// (both halves of the warp the same): x_i = [i = j] - sum over l < i of L_il x_l
-__device__ __forceinline__ void invert16(float *B, int lane)
-{
-    const int col = lane & 15;
-    float x[16];
-#pragma unroll
-    for (int row = 0; row < 16; ++row) {
-        float acc[4] = {row == col ? 1.f : 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int l = 0; l < row; l += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(B + row * kLS + l);
-            acc[0] = fmaf(-v.x, x[l], acc[0]);
-            if (l + 1 < row) acc[1] = fmaf(-v.y, x[l + 1], acc[1]);
-            if (l + 2 < row) acc[2] = fmaf(-v.z, x[l + 2], acc[2]);
-            if (l + 3 < row) acc[3] = fmaf(-v.w, x[l + 3], acc[3]);
-        }
-        x[row] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-    }
-    __syncwarp();
-    if (lane < 16) {
-#pragma unroll
-        for (int row = 0; row < 16; ++row) B[row * kLS + col] = x[row];
-    }
-}
-
 __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillShared &s)
 {
     const int tid = threadIdx.x - kInv0, lane = tid & 31, warp = tid >> 5;
@@ -871,31 +844,53 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
 #pragma unroll 1
     for (int g = 0; g < s.total; ++g) {
         const int st = g & 1;
-        float *L = s.L[st];
         waits.on(s.lready[st], (g >> 1) & 1);
-        // M by blocks of 16, 32 and 64: M21 = -M22 (L21 M11)
-        invert16(L + warp * 16 * (kLS + 1), lane);
-        named_bar(kBarInv, 128);
-        {
-            float *B = L + (warp >> 1) * 32 * (kLS + 1), *T = s.T + (warp >> 1) * 16 * kTS16;
-            const int tt = tid & 63;
-            const int row = tt >> 2, col = 4 * (tt & 3);
-            tile_product<false>(B + (16 + row) * kLS, B + col, kLS, T + row * kTS16 + col, 0, 16);
-            named_bar(kBarInv, 128);
-            tile_product<true>(B + (16 + row) * kLS + 16, T + col, kTS16, B + (16 + row) * kLS + col, 0, 16);
-        }
-        named_bar(kBarInv, 128);
-        // (M11 and M22 are triangular: a warp takes a short and a long strip of columns, then of rows)
+        // M by blocks of 32 (two of them, half the warps each: steps 0 and 1) and 64 (steps 2, 3 and 4, 5): M21 = -M22 (L21 M11).
+        // Every step makes four columns of a row of Z = X Y to a thread, from the l in [l0, l1) that a triangle leaves; a warp
+        // takes a short and a long strip of M11's columns, then of M22's rows.  X, Y, Z: places from s.L on.
+        float *F = &s.L[0][0];
+        const int L = st * kLFloats, B = L + (warp >> 1 ? kL22 : kL11), T = 2 * kLFloats, T16 = T + (warp >> 1) * 16 * kLS;
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-            const int col = 4 * (q ? 7 - warp : warp);
-            tile_product<false>(L + (32 + lane) * kLS, L + col, kLS, s.T + lane * kTS + col, col, 32);
-        }
-        named_bar(kBarInv, 128);
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-            const int row0 = 4 * (q ? 7 - warp : warp), row = 32 + row0 + (lane >> 3), col = 4 * (lane & 7);
-            tile_product<true>(L + row * kLS + 32, s.T + col, kTS, L + row * kLS + col, 0, row0 + 4);
+        for (int step = 0; step < 6; ++step) {
+            const int strip = 4 * (step & 1 ? 7 - warp : warp);
+            int X, Y, Z, l0 = 0, l1 = 32;
+            if (step < 2) {
+                const int row = (tid & 63) >> 2, col = 4 * (tid & 3), below = B + (16 + row) * kLS;
+                X = below + (step ? 16 : 0);
+                Y = (step ? T16 : B) + col;
+                Z = (step ? below : T16 + row * kLS) + col;
+                l1 = 16;
+            } else if (step < 4) {
+                X = L + kL21 + lane * kLS;
+                Y = L + kL11 + strip;
+                Z = T + lane * kLS + strip;
+                l0 = strip;
+            } else {
+                const int row = strip + (lane >> 3), col = 4 * (lane & 7);
+                X = L + kL22 + row * kLS;
+                Y = T + col;
+                Z = L + kL21 + row * kLS + col;
+                l1 = strip + 4;
+            }
+            float acc[4] = {};
+#pragma unroll 2
+            for (int l = l0; l < l1; l += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(F + X + l);
+                const float xe[4] = {x.x, x.y, x.z, x.w};
+                float4 y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const float4 *>(F + Y + (l + e) * kLS);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[0] = fmaf(xe[e], y[e].x, acc[0]);
+                    acc[1] = fmaf(xe[e], y[e].y, acc[1]);
+                    acc[2] = fmaf(xe[e], y[e].z, acc[2]);
+                    acc[3] = fmaf(xe[e], y[e].w, acc[3]);
+                }
+            }
+            const float f = step == 1 || step >= 4 ? -1.f : 1.f;
+            *reinterpret_cast<float4 *>(F + Z) = make_float4(f * acc[0], f * acc[1], f * acc[2], f * acc[3]);
+            if (step < 2 || step == 3) named_bar(kBarInv, 128);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.inverted[st]));
@@ -909,13 +904,13 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
 
 // The loops stay rolled: a product's few instructions are fetched once and run from the instruction
 // buffer, where straight-line code waits longer for its next line than for the tensor cores.
-__device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared &s)
+__device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShared &s)
 {
     Waits waits{p.polls};
     const int total = s.total;
     bool ok = true;
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, waits.on(bar, parity));
+        ok = ok && waits.on(bar, parity);
         tc_fence_after();
         return ok;
     };
@@ -950,29 +945,20 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
             if (!wait(s.have_s[half], par)) break;
-            if (elect_lane()) {
-                product(kColDK, kq, half);
-                if (half) tc_commit(smem_u32(&s.done_k));
-            }
-            __syncwarp();
+            product(kColDK, kq, half);
+            if (half) tc_commit(smem_u32(&s.done_k));
         }
         if (g > 0 && !wait(s.read_o, par ^ 1u)) break;
-        if (elect_lane()) {
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) product(kColDQ, kq + kC * 128, half);
-            tc_commit(smem_u32(&s.done_q));
-        }
-        __syncwarp();
+        for (int half = 0; half < 2; ++half) product(kColDQ, kq + kC * 128, half);
+        tc_commit(smem_u32(&s.done_q));
         if (!wait(s.mready[st], par2) || !wait(s.have_x, par)) break;
-        if (elect_lane()) {
-            pairs(kColU, kColX, s.M[0], 0);
-            tc_commit(smem_u32(&s.done_u));
-        }
-        __syncwarp();
+        pairs(kColU, kColX, s.M[0], 0);
+        tc_commit(smem_u32(&s.done_u));
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
             if (!wait(s.have_us[half], par)) break;
-            if (elect_lane()) {
+            {
                 const uint32_t b = desc_low(kq) + half * (16 * 128 / 16);
 #pragma unroll
                 for (int piece = 0; piece < 3; ++piece) {
@@ -985,17 +971,13 @@ __device__ __forceinline__ void issue_warp(const PrefillParams &p, PrefillShared
                     tc_commit(smem_u32(&s.empty[sk]));
                 }
             }
-            __syncwarp();
         }
         if (!wait(s.have_u, par)) break;
-        if (elect_lane()) {
-            pairs(kColDQ, kColUA, s.A[st][0], 1);
-            tc_commit(smem_u32(&s.done_o));
-            tc_commit(smem_u32(&s.gused[st]));
-        }
-        __syncwarp();
+        pairs(kColDQ, kColUA, s.A[st][0], 1);
+        tc_commit(smem_u32(&s.done_o));
+        tc_commit(smem_u32(&s.gused[st]));
     }
-    if (elect_lane()) tc_commit(smem_u32(&s.last));
+    tc_commit(smem_u32(&s.last));
     drain(s.last, 0, p);   // no product in flight when tensor memory is given back
     waits.end(s);
 }
@@ -1017,7 +999,7 @@ __device__ __forceinline__ void piece_warps(const PrefillParams &p, PrefillShare
         for (int q = 0; q < 6; ++q) {
             const int row = q < 2 ? 16 * q + (tid >> 2) : 16 + 8 * q + (tid >> 3), col = (q < 2 ? tid & 3 : tid & 7) * 8;
             float x[8];
-            read_n(s.L[st] + row * kLS + col, x);
+            read_n(s.L[st] + (row < 32 ? kL11 : col < 32 ? kL21 : kL22) + (row & 31) * kLS + (col & 31), x);
             float top = top_of(x);
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -1053,18 +1035,21 @@ __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShare
     const bool withheld = (p.debug_flags & 1) && blockIdx.x == 0;
     int g = 0, kq_issued = 0, v_issued = 0;
     bool go = true;
-    Walk t;
 #pragma unroll 1
-    while (go && t.next(p, s)) {
-        if (p.S0 && t.chunks)                     // the state, for when its turn comes
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.S0 + ((size_t)t.r * p.H + t.h) * kD * kD),
+    for (uint32_t cycle = 0, at; go && (at = item(cycle)) < p.items; ++cycle) {
+        const int rank = at / (uint32_t)p.H, h = at - rank * p.H, r = s.order[rank], pair = r * p.H + h, hk = h / p.group;
+        const int row0 = p.off[r], end = row0 + max(request_rows(p, r), 0);
+        if (p.S0 && end > row0)                   // the state, for when its turn comes
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.S0 + (size_t)pair * kD * kD),
                          "r"((uint32_t)(kD * kD * sizeof(float)))
                          : "memory");
-        const int hk = t.h / p.group;
 #pragma unroll 1
-        for (int ch = 0; go && ch < t.chunks; ++ch, ++g) {
-            const int sk = g % kStages, sv = g & 1, row = t.row0 + ch * kC;
+        for (int row = row0; go && row < end; row += kC, ++g) {
+            const int sk = g % kStages, sv = g & 1;
             const uint32_t kq_bar = smem_u32(&s.full[sk]), v_bar = smem_u32(&s.vfull[sv]), kq = smem_u32(s.KQ[sk]);
+            // (told ahead of the wait for room: the gates are asked for a chunk before their keys)
+            s.chunk[g % kChunks] = Chunk{row, min(end - row, kC), h, pair, row == row0, row + kC >= end};
+            mbar_arrive(smem_u32(&s.told[g & 3]));
             go = g < kStages || waits.on(s.empty[sk], ((g / kStages) & 1) ^ 1u);
             if (!go) break;
             mbar_expect_tx(kq_bar, kKqBytes);
@@ -1079,7 +1064,7 @@ __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShare
             go = g < 2 || waits.on(s.vempty[sv], ((g >> 1) & 1) ^ 1u);
             if (!go) break;
             mbar_expect_tx(v_bar, kVBytes);
-            tma_load_2d(smem_u32(s.V[sv]), &vmap, t.h * kD, row, v_bar);
+            tma_load_2d(smem_u32(s.V[sv]), &vmap, h * kD, row, v_bar);
             v_issued = g + 1;
         }
     }
@@ -1100,24 +1085,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the requests by their rows, and this CTA's chunks
         int32_t *rows = reinterpret_cast<int32_t *>(s.KQ[0]);
         for (int r = tid; r < p.n_req; r += kThreads) {
-            const int o0 = p.off[r], o1 = p.off[r + 1];
-            rows[r] = o0 < 0 || o1 < o0 || o1 > p.n_rows ? 0 : o1 - o0;
+            rows[r] = request_rows(p, r);
+            if (rows[r] < 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
         }
         if (tid == 0) s.total = 0;
         __syncthreads();
         for (int r = tid; r < p.n_req; r += kThreads) {
             const int mine = rows[r];
             int rank = 0;
+#pragma unroll 1
             for (int j = 0; j < p.n_req; ++j) rank += rows[j] > mine || (rows[j] == mine && j < r);
             s.order[rank] = (uint16_t)r;
         }
         __syncthreads();
         int chunks = 0;
+#pragma unroll 1
         for (uint32_t cycle = tid, at; (at = item(cycle)) < p.items; cycle += kThreads)
-            chunks += (rows[s.order[at / (uint32_t)p.H]] + kC - 1) / kC;
+            chunks += (max(rows[s.order[at / (uint32_t)p.H]], 0) + kC - 1) / kC;
         if (chunks) atomicAdd(&s.total, chunks);
+        // where there is no token the state stays what it was (those pairs come last)
+#pragma unroll 1
+        for (uint32_t cycle = 0, at; p.state != p.S0 && (at = item(cycle)) < p.items; ++cycle) {
+            const int rank = at / (uint32_t)p.H, r = s.order[rank];
+            if (rows[r] != 0) continue;
+            const size_t to = ((size_t)r * p.H + (at - rank * p.H)) * kD * kD;
+#pragma unroll 1
+            for (int e = tid; e < kD * kD / 4; e += kThreads)
+                reinterpret_cast<float4 *>(p.state + to)[e] =
+                    p.S0 ? reinterpret_cast<const float4 *>(p.S0 + to)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     }
     if (tid == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.told[i]), 1);
         for (int st = 0; st < kStages; ++st) {
             mbar_init(smem_u32(&s.full[st]), 1);
             mbar_init(smem_u32(&s.empty[st]), 1);
@@ -1142,17 +1141,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&vmap);
     }
     if (warp == 0) tmem_alloc(smem_u32(&s.tmem), 512);
-    // what no chunk writes and every chunk reads: the entries above the diagonal blocks of 32
-    for (int e = tid; e < 32 * 8; e += kThreads) {
-        const int row = e >> 3, q = e & 7;
+    // what no chunk writes and every chunk reads: M and A above the diagonal blocks of 32
+    for (int e = tid; e < 32 * 4; e += kThreads) {
+        const int row = e >> 2, at = row * 128 + (((4 + (e & 3)) ^ (row & 7)) << 4);
         const uint4 z = make_uint4(0, 0, 0, 0);
-        for (int st = 0; st < 2; ++st) *reinterpret_cast<uint4 *>(s.L[st] + row * kLS + 32 + 4 * q) = z;
-        if (q < 4) {
-            const int at = row * 128 + (((4 + q) ^ (row & 7)) << 4);
-            for (int piece = 0; piece < 2; ++piece) {
-                *reinterpret_cast<uint4 *>(s.M[piece] + at) = z;
-                for (int st = 0; st < 2; ++st) *reinterpret_cast<uint4 *>(s.A[st][piece] + at) = z;
-            }
+#pragma unroll
+        for (int piece = 0; piece < 2; ++piece) {
+            *reinterpret_cast<uint4 *>(s.M[piece] + at) = z;
+            for (int st = 0; st < 2; ++st) *reinterpret_cast<uint4 *>(s.A[st][piece] + at) = z;
         }
     }
     fence_async_shared();
@@ -1172,7 +1168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         inverse_warps(p, s);
     } else {
         regs_dec<kRegsIssue>();
-        if (warp == kIssue0 / 32) issue_warp(p, s);
+        if (warp == kIssue0 / 32 && elect_lane()) issue_thread(p, s);
         if (tid >= kIssue0 + 64) piece_warps(p, s);
         if (tid == kIssue0 + 32) copy_thread(p, s, qmap, kmap, vmap);
     }
