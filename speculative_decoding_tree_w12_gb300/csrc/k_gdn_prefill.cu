@@ -914,27 +914,26 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
         tc_fence_after();
         return ok;
     };
-    // U or U A: two FP32 operands of two F16 pieces each, K = 64 tokens: high times high, high times low, low times high
+    // (Each product adds to its sum with a rounding of some 2^-24 of that sum, towards zero: so the small pieces come first,
+    // and few products meet a sum of full size.)
+    // U or U A: two FP32 operands of two F16 pieces each, K = 64 tokens: low times high, high times low, high times high
     auto pairs = [&](uint32_t d, uint32_t a, const uint8_t *B, uint32_t add) {
         const uint32_t b0 = desc_low(smem_u32(B));
 #pragma unroll 1
         for (int q = 0; q < 3; ++q) {
-            const uint32_t b = b0 + (q == 1 ? kC * 128 / 16 : 0), aq = a + (q == 2 ? 32 : 0);
+            const uint32_t b = b0 + (q == 1 ? kC * 128 / 16 : 0), aq = a + (q == 0 ? 32 : 0);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) tc_mma_ts(d, aq + 8 * ks, desc_k(b + ks * 2), kIdescF16, add | (uint32_t)(q | ks));
         }
     };
-    // a half of both threads' features of S times the keys (rows 0..63 of the tile) or the queries (64..127)
-    auto product = [&](uint32_t d, uint32_t tile, int half) {
-        const uint32_t b = desc_low(tile) + half * 4;
-#pragma unroll 1
-        for (int piece = 0; piece < 3; ++piece) {
-            const uint32_t a = kColS + 64 * piece + 16 * half;
-            tc_mma_ts(d, a, desc_k(b), idesc_bf16_f32(128, kC), (uint32_t)(half | piece));
-            tc_mma_ts(d, a + 8, desc_k(b + 2), idesc_bf16_f32(128, kC), 1);
-            tc_mma_ts(d, a + 32, desc_k(b + 128 * 128 / 16), idesc_bf16_f32(128, kC), 1);
-            tc_mma_ts(d, a + 40, desc_k(b + 128 * 128 / 16 + 2), idesc_bf16_f32(128, kC), 1);
-        }
+    // a piece (0 high, 2 low) of a half of both threads' features of S times the keys (rows 0..63 of the tile) or the queries
+    // (64..127)
+    auto product = [&](uint32_t d, uint32_t tile, int half, int piece, bool first) {
+        const uint32_t b = desc_low(tile) + half * 4, a = kColS + 64 * piece + 16 * half;
+        tc_mma_ts(d, a, desc_k(b), idesc_bf16_f32(128, kC), first ? 0u : 1u);
+        tc_mma_ts(d, a + 8, desc_k(b + 2), idesc_bf16_f32(128, kC), 1);
+        tc_mma_ts(d, a + 32, desc_k(b + 128 * 128 / 16), idesc_bf16_f32(128, kC), 1);
+        tc_mma_ts(d, a + 40, desc_k(b + 128 * 128 / 16 + 2), idesc_bf16_f32(128, kC), 1);
     };
 #pragma unroll 1
     for (int g = 0; g < total; ++g) {
@@ -945,12 +944,13 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
             if (!wait(s.have_s[half], par)) break;
-            product(kColDK, kq, half);
+#pragma unroll 1
+            for (int piece = 2; piece >= 0; --piece) product(kColDK, kq, half, piece, half == 0 && piece == 2);
             if (half) tc_commit(smem_u32(&s.done_k));
         }
         if (g > 0 && !wait(s.read_o, par ^ 1u)) break;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) product(kColDQ, kq + kC * 128, half);
+        for (int q = 0; q < 6; ++q) product(kColDQ, kq + kC * 128, q & 1, 2 - (q >> 1), q == 0);
         tc_commit(smem_u32(&s.done_q));
         if (!wait(s.mready[st], par2) || !wait(s.have_x, par)) break;
         pairs(kColU, kColX, s.M[0], 0);
@@ -961,9 +961,9 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
             {
                 const uint32_t b = desc_low(kq) + half * (16 * 128 / 16);
 #pragma unroll
-                for (int piece = 0; piece < 3; ++piece) {
+                for (int piece = 2; piece >= 0; --piece) {
                     const uint32_t a = kColS + 32 * piece + 8 * half;
-                    tc_mma_ts(kColDK, a, desc_mn(b), idesc_bf16_f32(128, kD) | kBMnMajor, (uint32_t)(half | piece));
+                    tc_mma_ts(kColDK, a, desc_mn(b), idesc_bf16_f32(128, kD) | kBMnMajor, (uint32_t)(half | (piece < 2)));
                     tc_mma_ts(kColDK, a + 16, desc_mn(b + 32 * 128 / 16), idesc_bf16_f32(128, kD) | kBMnMajor, 1);
                 }
                 if (half) {
