@@ -417,7 +417,13 @@ typedef struct {
     const uint16_t *v;           /* device BF16 [n_rows][n_heads][d], the same */
     int64_t q_stride, k_stride, v_stride;
     const float *alpha, *beta;   /* device [n_rows][n_heads]: gates and write strengths */
+    void *scratch;               /* w12_gdn_prefill: device, 16-byte aligned, one call's at a time; or NULL: a request's head
+                                    is then one SM's, however long it is */
+    size_t scratch_bytes;        /* w12_gdn_scratch_bytes(n_heads, n_rows) at least (else W12_E_WORKSPACE) */
 } w12_gdn_rows;
+
+/* Scratch for so many heads and rows on the current device (20 MB at most); 0 where none is used. */
+size_t w12_gdn_scratch_bytes(int32_t n_heads, int32_t n_rows);
 
 /*
  * Rows row_off[r] .. row_off[r+1]-1 (device [n_req + 1]) continue request r's

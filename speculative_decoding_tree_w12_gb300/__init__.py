@@ -113,6 +113,7 @@ def lib():
             "w12_gdn_wy_verify": ([p, p, i32, p, p, p, sz, p], C.c_int),
             "w12_gdn_wy_commit": ([p, p, i32, p, p, p, p, sz, p], C.c_int),
             "w12_gdn_prefill": ([p, i32, p, p, p, p, p, sz, p], C.c_int),
+            "w12_gdn_scratch_bytes": ([i32, i32], sz),
             "w12_gdn_step": ([p, p, p, p, p], C.c_int),
             "w12_gdn_norm": ([p, i32, i32, i32, p, i64, p, C.c_float, i32, p, i64, p], C.c_int),
             "w12_block_norm": ([p, p], C.c_int),
@@ -748,14 +749,16 @@ def w12_tree_attention(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n
 class GdnRowsC(C.Structure):
     _fields_ = [("n_heads", C.c_int32), ("n_qk_heads", C.c_int32), ("head_dim", C.c_int32), ("n_rows", C.c_int32),
                 ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("q_stride", C.c_int64), ("k_stride", C.c_int64),
-                ("v_stride", C.c_int64), ("alpha", C.c_void_p), ("beta", C.c_void_p)]
+                ("v_stride", C.c_int64), ("alpha", C.c_void_p), ("beta", C.c_void_p), ("scratch", C.c_void_p),
+                ("scratch_bytes", C.c_size_t)]
 
 
 class GdnRows:
     """A recurrent layer's token rows: q and k (bfloat16 [T][n_qk_heads * 128]),
     v (bfloat16 [T][H * 128]; slices of a fused row are fine), gates alpha and
     write strengths beta (float32 [T][H]).  Value head h reads query/key head
-    h // (H // n_qk_heads).  The tensors stay the caller's."""
+    h // (H // n_qk_heads).  The tensors stay the caller's.
+    Holds the scratch of ``w12_gdn_prefill``; one object's calls of it run in order."""
 
     def __init__(self, q, k, v, alpha, beta):
         torch = _runtime()
@@ -773,8 +776,15 @@ class GdnRows:
         self.T, self.H, self.d = int(T), int(H), 128
         (qa, qs), (ka, ks), (va, vs) = (_rows(t, T, w, n, self.dev) for t, w, n in
                                         ((q, q.shape[1], "q"), (k, q.shape[1], "k"), (v, H * 128, "v")))
-        self.c = GdnRowsC(H, q.shape[1] // 128, 128, T, qa, ka, va, qs, ks, vs, alpha.data_ptr(), beta.data_ptr())
+        self.c = GdnRowsC(H, q.shape[1] // 128, 128, T, qa, ka, va, qs, ks, vs, alpha.data_ptr(), beta.data_ptr(), None, 0)
+        self.scratch = None                      # for w12_gdn_prefill, made by its first call
         self.ref = C.byref(self.c)
+
+    def _make_scratch(self):
+        nbytes = int(_lib.w12_gdn_scratch_bytes(self.H, self.T))
+        self.scratch = _torch.empty(nbytes, dtype=_torch.uint8, device=self.alpha.device)
+        if nbytes:
+            self.c.scratch, self.c.scratch_bytes = self.scratch.data_ptr(), nbytes
 
     def _buffers(self, n_req, S0, state, out):
         """The calls' state and output tensors, made or checked."""
@@ -801,6 +811,8 @@ def w12_gdn_prefill(rows: GdnRows, row_off, ws: Workspace, S0=None, state=None, 
     state, out = rows._buffers(n, S0, state, out)
     if ws.dev != rows.dev:
         _refuse(rows.dev, n, None, ws)
+    if rows.scratch is None:
+        rows._make_scratch()
     s = _lib.w12_gdn_prefill(rows.ref, n, _ints(row_off, n + 1, "row_off", rows.dev), _dp(S0), state.data_ptr(),
                              out.data_ptr(), ws.addr, ws.nbytes, _st(stream))
     if s:

@@ -71,11 +71,14 @@ constexpr int kBarRow = 2;                 // and of the two token warps of 32 s
 constexpr int kStages = 3;          // of keys and queries (their chunk is prepared while two others are in use)
 
 // what a chunk is of
+enum Start : int32_t { kGoesOn, kFromState, kFromZero, kFromOne };
 struct Chunk {
+    const float *from;              // the state in front, where one is loaded
+    float *to;                      // where the state behind it goes, or null
     int32_t row0, n;                // first row, rows
+    int32_t out;                    // rows whose outputs are wanted: all of them or none
     int32_t h;
-    int32_t pair;                   // r * H + h
-    int32_t first, last;            // whether it is its request's first or last
+    Start start;                    // where the state in front comes from
 };
 constexpr int kChunks = 8;          // descriptions kept
 
@@ -97,7 +100,7 @@ struct PrefillShared {
     float x_back[kD];               // powers of two of X's rows
     float a_top[2], a_back[4];      // largest magnitude of A's rows by halves, its power of two
     uint32_t m_top[4];              // largest magnitude in M, as its bits
-    float gates[2], grow[2];        // products of the gates of tokens 0 .. 31 and 32 .. 63, and of those above 1
+    float gates[2], grow[2];        // products of the gates of tokens 0 .. 31 and 32 .. 63, and of the magnitudes above 1
     Chunk chunk[kChunks];           // of chunk c in [c % 8], by the thread that issues the copies
     unsigned long long told[4];                         // it is there
     unsigned long long full[kStages], empty[kStages];   // keys and queries
@@ -122,13 +125,42 @@ static_assert(offsetof(PrefillShared, M) % 1024 == 0 && offsetof(PrefillShared, 
 static_assert(offsetof(PrefillShared, V) % 128 == 0 && offsetof(PrefillShared, full) % 8 == 0, "copies and barriers");
 constexpr uint32_t kKqBytes = sizeof(PrefillShared::KQ) / kStages, kVBytes = sizeof(PrefillShared::V) / 2;
 
+// Few long requests leave most SMs without one.  The state behind a part of a request is S P + Q in that in front: Q what the
+// part makes of a state of zero, P what it makes of the unit matrix without values.  So each is cut into n = (j + 1) w + 1 like
+// pieces, and two launches run them, one CTA to an item:
+//  * kAhead: the first w pieces as they are, and Q and P of the j segments of w pieces behind them, noted after every piece,
+//  * k_gdn_join: the states in front of every piece but the first w from those,
+//  * kPieces: those pieces, now with their outputs.
+// That takes w + 1 pieces' time of n, and (2 j + 1) and (j w + 1) CTAs a pair (one of 4096 tokens, 4 heads: 299 us in one
+// part a head, 94 cut; of 32768 tokens, 32 heads: 2346 and 1412).  The launches overlap: each begins where SMs are left, and waits for the
+// one before it only for what that wrote (3 to 6 us of those).  All three as one launch whose CTAs wait for one another's
+// counts were slower (4096 tokens, 4 heads: 130 us), the join being short of registers and of shared memory there.
+enum Mode : int32_t { kWhole, kAhead, kPieces };
+
+struct SplitParams {
+    Mode mode;
+    int32_t j, w;                   // at most; pieces of a segment
+    float *states;                  // [pair][j w + 1][Q or the state in front, P][kD][kD]
+    int32_t *failed;                // [pair][2 j + 1]: whether an item of kAhead has given up
+};
+
+// Segments of a request of nc chunks.  The join takes a product of 1.1 us for each piece of them, so no more than pay for theirs; and it and
+// two more launches some 35 us, eight chunks' time (4.6 us each), which the j w pieces not waited for have to save.  (One request
+// of 32 heads, j = 1: 16 chunks 87 us whole, 94 cut, 24 chunks 124 and 112; of 16 heads, j = 4: 10 chunks 60 and 62, 12 chunks 69 and 67.)
+__host__ __device__ inline int split_segments(int nc, int j, int w)
+{
+    while (j > 0 && (j * j > 2 * nc || (j + 1) * w + 1 > nc)) --j;
+    return (int64_t)nc * j * w < 8 * ((j + 1) * w + 1) ? 0 : j;
+}
+
 struct PrefillParams {
     const float *S0;                // may be null: zero
     float *state, *o;
     const float *alpha, *beta;
     const int32_t *off;
     int32_t H, group, n_req, n_rows;
-    uint32_t items;                 // n_req * H
+    SplitParams split;
+    uint32_t subs, items;           // items of a pair; n_req * H of them each
     uint32_t polls;                 // of a wait, before it gives up
     int32_t *status;
     int32_t debug_flags;            // bit 0: CTA 0 announces its first copies and leaves them out (test hook)
@@ -394,6 +426,38 @@ __device__ __forceinline__ uint32_t item(uint32_t cycle)
     return cycle * gridDim.x + (cycle & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
+__device__ __forceinline__ int chunks_of(int rows) { return rows > 0 ? (rows - 1) / kC + 1 : 0; }
+
+// the chunks of item `sub` of a request of nc of them
+struct Part {
+    int first, end;
+    int j;                          // the request's segments
+    int slot;                       // kAhead: of the first state that is noted; kPieces: of the one in front
+};
+__device__ __forceinline__ int piece_start(const PrefillParams &p, int nc, int j, uint32_t i)
+{
+    const uint32_t n = (j + 1) * p.split.w + 1, like = (uint32_t)nc / n;
+    return (int)(i * like + i * (nc - n * like) / n);
+}
+__device__ __forceinline__ Part part_of(const PrefillParams &p, int nc, int sub)
+{
+    if (p.split.mode == kWhole) return Part{0, nc, 0, 0};
+    const int j = split_segments(nc, p.split.j, p.split.w), w = p.split.w;
+    if (p.split.mode == kAhead) {
+        const int seg = (sub + 1) >> 1;
+        if (seg == 0) return Part{0, j ? piece_start(p, nc, j, w) : nc, j, 0};
+        if (seg > j) return Part{0, 0, j, 0};
+        return Part{piece_start(p, nc, j, seg * w), piece_start(p, nc, j, (seg + 1) * w), j, (seg - 1) * w + 1};
+    }
+    if (j == 0 || sub > j * w) return Part{0, 0, j, 0};
+    return Part{piece_start(p, nc, j, w + sub), piece_start(p, nc, j, w + sub + 1), j, sub};
+}
+// the state (or Q) in front of piece w + slot, P with `which` 1
+__device__ __forceinline__ float *split_state(const SplitParams &s, int pair, int slot, int which)
+{
+    return s.states + (((size_t)pair * (s.j * s.w + 1) + slot) * 2 + which) * (kD * kD);
+}
+
 // ---------------------------------------------------------------------------
 // state warps
 // ---------------------------------------------------------------------------
@@ -403,26 +467,40 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 2;
     const int c = (warp & 3) * 32 + lane;                                 // state row
     const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;                // this warp's lanes
-    Waits waits{p.polls};
+    Waits waits{p.polls + s.total};
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
         waits.on(bar, parity);
         tc_fence_after();
     };
     const int total = s.total;
+    if (p.split.mode == kPieces) {
+        pdl_wait();                               // the states in front come from the launches before
+        const uint32_t a_rank = p.subs * p.H, pair = s.order[blockIdx.x / a_rank] * p.H + blockIdx.x % a_rank % p.H;
+        const int all = 2 * p.split.j + 1;
+        int failed = 0;
+#pragma unroll 1
+        for (int e = lane; e < all; e += 32) failed |= __ldcg(p.split.failed + pair * all + e);
+        if (__any_sync(0xffffffffu, failed)) waits.left = 0;   // (nothing is made of what did not come about)
+    }
     float S[64];
 #pragma unroll 1
     for (int g = 0; g < total; ++g) {
         wait(s.told[g & 3], (g >> 2) & 1);
         const Chunk &t = s.chunk[g % kChunks];
-        const size_t at = ((size_t)t.pair * kD + c) * kD + 64 * part;     // this thread's half of the row
-        if (t.first) {
+        const int at = c * kD + 64 * part;                                // this thread's half of the row
+        if (t.start != kGoesOn) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float4 x = p.S0 ? *reinterpret_cast<const float4 *>(p.S0 + at + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 x = t.start == kFromState ? *reinterpret_cast<const float4 *>(t.from + at + 4 * i)
+                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
                 S[4 * i] = x.x;
                 S[4 * i + 1] = x.y;
                 S[4 * i + 2] = x.z;
                 S[4 * i + 3] = x.w;
+            }
+            if (t.start == kFromOne) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) S[i] = 64 * part + i == c ? 1.f : 0.f;
             }
         }
         const int k4 = g & 3;
@@ -476,10 +554,10 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
                 S[32 * q + i + 1] = n.y;
             }
         }
-        if (t.last && waits.left && !*(volatile int32_t *)&s.abort) {
+        if (t.to && waits.left && !*(volatile int32_t *)&s.abort) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                *reinterpret_cast<float4 *>(p.state + at + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+                *reinterpret_cast<float4 *>(t.to + at + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
         }
     }
     waits.end(s);
@@ -494,7 +572,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
     const int lane = threadIdx.x & 31, warp = (threadIdx.x - kToken0) >> 5, part = warp >> 2;
     const int c = (warp & 3) * 32 + lane, t0 = 32 * part;                 // state row, first token
     const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;
-    Waits waits{p.polls};
+    Waits waits{p.polls + s.total};
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
         waits.on(bar, parity);
         tc_fence_after();
@@ -596,7 +674,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         const size_t step = (size_t)p.H * kD;
         const Chunk &t = s.chunk[g % kChunks];
         float *dst = p.o + ((size_t)(t.row0 + t0) * p.H + t.h) * kD + c;
-        int left = t.n - t0;
+        int left = t.out - t0;
 #pragma unroll 1
         for (int q = t0; q < t0 + 32; q += 16, left -= 16) {
             float x[16];
@@ -671,7 +749,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
     const int tid = threadIdx.x - kGate0, lane = tid & 31, warp = tid >> 5;
     const int i = tid & 63;                       // token of the chunk
     const bool query = warp >= 2;                 // this thread's row: k_i.k or q_i.k
-    Waits waits{p.polls};
+    Waits waits{p.polls + s.total};
     const int blocks = (warp & 1) ? 4 : 2;        // of 16 columns that its warp's rows reach into
     const uint32_t tm = (uint32_t)(warp * 32) << 16;
     // warp 3: k.k and q.k of a chunk whose rows have arrived.  Rows behind the request's end are another
@@ -728,10 +806,10 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         const uint32_t par2 = (g >> 1) & 1;
         if (warp == 3) products(g, valid);
         const float strength = b;
-        float up = a, down = a, grow = fmaxf(a, 1.f);
+        float up = a, down = a, grow = fmaxf(fabsf(a), 1.f);
         if (!query) {
             // products of the gates from this block of 32 tokens' start to token i, and from behind it to the block's
-            // end; and of those above 1, which bound the D_ij
+            // end; and of the magnitudes above 1, which bound the D_ij
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const float u = __shfl_up_sync(0xffffffffu, up, o), v = __shfl_down_sync(0xffffffffu, down, o);
@@ -840,7 +918,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
 __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillShared &s)
 {
     const int tid = threadIdx.x - kInv0, lane = tid & 31, warp = tid >> 5;
-    Waits waits{p.polls};
+    Waits waits{p.polls + s.total};
 #pragma unroll 1
     for (int g = 0; g < s.total; ++g) {
         const int st = g & 1;
@@ -906,7 +984,7 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
 // buffer, where straight-line code waits longer for its next line than for the tensor cores.
 __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShared &s)
 {
-    Waits waits{p.polls};
+    Waits waits{p.polls + s.total};
     const int total = s.total;
     bool ok = true;
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
@@ -986,7 +1064,7 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
 __device__ __forceinline__ void piece_warps(const PrefillParams &p, PrefillShared &s)
 {
     const int tid = threadIdx.x - kIssue0 - 64, lane = tid & 31;
-    Waits waits{p.polls};
+    Waits waits{p.polls + s.total};
 #pragma unroll 1
     for (int g = 0; g < s.total; ++g) {
         const int st = g & 1, k4 = g & 3;
@@ -1031,25 +1109,40 @@ __device__ __forceinline__ void piece_warps(const PrefillParams &p, PrefillShare
 __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShared &s, const CUtensorMap &qmap, const CUtensorMap &kmap,
                                             const CUtensorMap &vmap)
 {
-    Waits waits{p.polls};
-    const bool withheld = (p.debug_flags & 1) && blockIdx.x == 0;
+    Waits waits{p.polls + s.total};
+    const bool withheld = (p.debug_flags & 1) && blockIdx.x == 0 && p.split.mode != kPieces;
     int g = 0, kq_issued = 0, v_issued = 0;
     bool go = true;
 #pragma unroll 1
     for (uint32_t cycle = 0, at; go && (at = item(cycle)) < p.items; ++cycle) {
-        const int rank = at / (uint32_t)p.H, h = at - rank * p.H, r = s.order[rank], pair = r * p.H + h, hk = h / p.group;
-        const int row0 = p.off[r], end = row0 + max(request_rows(p, r), 0);
-        if (p.S0 && end > row0)                   // the state, for when its turn comes
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.S0 + (size_t)pair * kD * kD),
-                         "r"((uint32_t)(kD * kD * sizeof(float)))
-                         : "memory");
+        const int rank = at / (p.subs * p.H), left = at - rank * p.subs * p.H, sub = left / p.H, h = left - sub * p.H;
+        const int r = s.order[rank], pair = r * p.H + h, hk = h / p.group;
+        const int row0 = p.off[r], rows = max(request_rows(p, r), 0);
+        const Part part = part_of(p, chunks_of(rows), sub);
+        const bool affine = p.split.mode == kAhead && sub > 0, unit = affine && !(sub & 1);
+        const size_t whole = (size_t)pair * kD * kD;
+        const float *from = affine ? nullptr : p.split.mode == kPieces ? split_state(p.split, pair, part.slot, 0) : p.S0 ? p.S0 + whole : nullptr;
+        Start start = unit ? kFromOne : from ? kFromState : kFromZero;
+        // the states to be noted: behind every piece of a segment; of the first w pieces; behind the last piece
+        float *to = affine ? split_state(p.split, pair, part.slot, unit)
+                    : p.split.mode == kAhead && part.j ? split_state(p.split, pair, 0, 0)
+                    : p.split.mode == kPieces && part.slot < part.j * p.split.w ? nullptr : p.state + whole;
+        int piece = affine ? p.split.w + part.slot : 0, note = affine ? piece_start(p, chunks_of(rows), part.j, piece) : part.end;
+        if (from && part.end > part.first)        // the state, for when its turn comes
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(kD * kD * sizeof(float))) : "memory");
 #pragma unroll 1
-        for (int row = row0; go && row < end; row += kC, ++g) {
+        for (int chunk = part.first; go && chunk < part.end; ++chunk, ++g) {
+            const int row = row0 + chunk * kC, n = min(rows - chunk * kC, kC);
             const int sk = g % kStages, sv = g & 1;
             const uint32_t kq_bar = smem_u32(&s.full[sk]), v_bar = smem_u32(&s.vfull[sv]), kq = smem_u32(s.KQ[sk]);
             // (told ahead of the wait for room: the gates are asked for a chunk before their keys)
-            s.chunk[g % kChunks] = Chunk{row, min(end - row, kC), h, pair, row == row0, row + kC >= end};
+            s.chunk[g % kChunks] = Chunk{from, chunk + 1 == note ? to : nullptr, row, n, affine ? 0 : n, h, start};
             mbar_arrive(smem_u32(&s.told[g & 3]));
+            start = kGoesOn;
+            if (affine && chunk + 1 == note) {
+                note = piece_start(p, chunks_of(rows), part.j, ++piece);
+                to += 2 * kD * kD;
+            }
             go = g < kStages || waits.on(s.empty[sk], ((g / kStages) & 1) ^ 1u);
             if (!go) break;
             mbar_expect_tx(kq_bar, kKqBytes);
@@ -1063,6 +1156,10 @@ __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShare
             kq_issued = g + 1;
             go = g < 2 || waits.on(s.vempty[sv], ((g >> 1) & 1) ^ 1u);
             if (!go) break;
+            if (unit) {                           // no values: zeros lie there
+                mbar_arrive(v_bar);
+                continue;
+            }
             mbar_expect_tx(v_bar, kVBytes);
             tma_load_2d(smem_u32(s.V[sv]), &vmap, h * kD, row, v_bar);
             v_issued = g + 1;
@@ -1074,6 +1171,16 @@ __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShare
     waits.end(s);
 }
 
+__device__ __forceinline__ void keep_state(const PrefillParams &p, int pair)
+{
+    if (p.state == p.S0) return;
+    const size_t to = (size_t)pair * kD * kD;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < kD * kD / 4; e += kThreads)
+        reinterpret_cast<float4 *>(p.state + to)[e] =
+            p.S0 ? reinterpret_cast<const float4 *>(p.S0 + to)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     k_gdn_prefill(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const PrefillParams p)
@@ -1081,6 +1188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     PrefillShared &s = *reinterpret_cast<PrefillShared *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, warp = tid >> 5;
+    if (p.split.mode == kAhead) pdl_launch_dependents();   // (the join waits for this launch's end, in the SMs that are left)
     {
         // the requests by their rows, and this CTA's chunks
         int32_t *rows = reinterpret_cast<int32_t *>(s.KQ[0]);
@@ -1100,19 +1208,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         int chunks = 0;
 #pragma unroll 1
-        for (uint32_t cycle = tid, at; (at = item(cycle)) < p.items; cycle += kThreads)
-            chunks += (max(rows[s.order[at / (uint32_t)p.H]], 0) + kC - 1) / kC;
+        for (uint32_t cycle = tid, at; (at = item(cycle)) < p.items; cycle += kThreads) {
+            const int rank = at / (p.subs * p.H);
+            const Part part = part_of(p, chunks_of(rows[s.order[rank]]), (at - rank * p.subs * p.H) / p.H);
+            chunks += part.end - part.first;
+        }
         if (chunks) atomicAdd(&s.total, chunks);
-        // where there is no token the state stays what it was (those pairs come last)
+        if (p.split.mode == kWhole) {
+            // where there is no token the state stays what it was (those pairs come last)
 #pragma unroll 1
-        for (uint32_t cycle = 0, at; p.state != p.S0 && (at = item(cycle)) < p.items; ++cycle) {
-            const int rank = at / (uint32_t)p.H, r = s.order[rank];
-            if (rows[r] != 0) continue;
-            const size_t to = ((size_t)r * p.H + (at - rank * p.H)) * kD * kD;
+            for (uint32_t cycle = 0, at; (at = item(cycle)) < p.items; ++cycle) {
+                const int rank = at / (uint32_t)p.H, r = s.order[rank];
+                if (rows[r] == 0) keep_state(p, r * p.H + (at - rank * p.H));
+            }
+        } else if (blockIdx.x < p.items) {        // one item: see above
+            const uint32_t at = blockIdx.x;
+            const int rank = at / (p.subs * p.H), left = at - rank * p.subs * p.H, sub = left / p.H, h = left - sub * p.H;
+            const int r = s.order[rank];
+            if (p.split.mode == kAhead) {
+                if (sub == 0 && rows[r] == 0) keep_state(p, r * p.H + h);
+                if (sub && !(sub & 1)) {          // P has no values
 #pragma unroll 1
-            for (int e = tid; e < kD * kD / 4; e += kThreads)
-                reinterpret_cast<float4 *>(p.state + to)[e] =
-                    p.S0 ? reinterpret_cast<const float4 *>(p.S0 + to)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int e = tid; e < (int)(sizeof(s.V) / 16); e += kThreads) reinterpret_cast<uint4 *>(s.V)[e] = make_uint4(0, 0, 0, 0);
+                }
+            }
         }
     }
     if (tid == 0) {
@@ -1176,7 +1295,112 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && s.abort) atomicCAS(p.status, 0, (int32_t)W12_E_TIMEOUT);
+    if (tid == 0 && p.split.mode == kAhead) {
+        const uint32_t a_rank = p.subs * p.H, left = blockIdx.x % a_rank;
+        p.split.failed[(s.order[blockIdx.x / a_rank] * p.H + left % p.H) * p.subs + left / p.H] = s.abort;
+    }
     if (warp == 0) tmem_dealloc(s.tmem, 512);
+}
+
+// The states in front of the pieces, segment after segment: S P + Q over Q.  A CTA takes 8 rows of a pair's states for each of its
+// groups of 8 warps (rows are each other's business in no product), so P, which the copy engine brings a product ahead, is
+// read once for all of them.  A warp takes 16 of a product's 128 features; its sums join those of the group's other warps
+// in shared memory.  8 rows' 131,072 multiplications take 0.55 us of an SM, as long as P's way from L2.
+constexpr int kJoinRows = 8, kJoinWarps = 8;      // of a group
+template <int kGroups>
+struct JoinShared {
+    float P[2][kD][kD];
+    float S[kGroups][kD][kJoinRows + 4];          // the state in front, by features, 12 banks apart
+    float sums[kGroups][kJoinWarps][kJoinRows][kD];
+    unsigned long long full[2];
+};
+
+// a plain copy into shared memory, addresses and size multiples of 16 bytes
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+                 "r"(bar)
+                 : "memory");
+}
+
+template <int kGroups>
+__global__ void __launch_bounds__(32 * kJoinWarps * kGroups, 1) k_gdn_join(const PrefillParams p)
+{
+    pdl_wait();                                   // first of all: the launch behind this one counts on it
+    pdl_launch_dependents();
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    JoinShared<kGroups> &s = *reinterpret_cast<JoinShared<kGroups> *>(smem_raw);
+    constexpr int kOwn = kD / kJoinWarps;         // features of a warp
+    const int tid = threadIdx.x & 255, lane = tid & 31, warp = tid >> 5, group = threadIdx.x >> 8;
+    const int pair = blockIdx.y, row0 = (blockIdx.x * kGroups + group) * kJoinRows, w = p.split.w;
+    const int last = split_segments(chunks_of(request_rows(p, pair / p.H)), p.split.j, w) * w;
+    if (last == 0) return;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&s.full[0]), 1);
+        mbar_init(smem_u32(&s.full[1]), 1);
+        fence_mbar_init();
+    }
+    auto fetch = [&](int slot) {                  // thread 0
+        const uint32_t bar = smem_u32(&s.full[slot & 1]);
+        mbar_expect_tx(bar, kD * kD * 4);
+        bulk_load(smem_u32(s.P[slot & 1]), split_state(p.split, pair, slot, 1), kD * kD * 4, bar);
+    };
+    const int row = 4 * (tid >> 7), col = tid & 127;   // of this thread's four sums
+    float *Q = split_state(p.split, pair, 0, 0) + (row0 + row) * kD + col;
+    auto read_q = [&]() { return make_float4(Q[0], Q[kD], Q[2 * kD], Q[3 * kD]); };
+    float(&S)[kD][kJoinRows + 4] = s.S[group];
+    *reinterpret_cast<float4 *>(&S[col][row]) = read_q();
+    if (threadIdx.x == 0) fetch(1);
+    __syncthreads();
+    Waits waits{p.polls};
+#pragma unroll 1
+    for (int slot = 1, piece = 1; slot <= last; ++slot, ++piece) {
+        if (threadIdx.x == 0 && slot < last) fetch(slot + 1);
+        Q += 2 * kD * kD;                         // (a piece's states lie behind those of the one before)
+        float4 sum = read_q();
+        float2 acc[kJoinRows][2] = {};
+        waits.on(s.full[slot & 1], ((slot - 1) >> 1) & 1);
+#pragma unroll
+        for (int l = 0; l < kOwn; ++l) {
+            float x[kJoinRows];
+            read_n(S[warp * kOwn + l], x);
+            const float4 y = *reinterpret_cast<const float4 *>(&s.P[slot & 1][warp * kOwn + l][4 * lane]);
+#pragma unroll
+            for (int r = 0; r < kJoinRows; ++r) {
+                acc[r][0] = __ffma2_rn(make_float2(x[r], x[r]), make_float2(y.x, y.y), acc[r][0]);
+                acc[r][1] = __ffma2_rn(make_float2(x[r], x[r]), make_float2(y.z, y.w), acc[r][1]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r)
+            *reinterpret_cast<float4 *>(&s.sums[group][warp][r][4 * lane]) = make_float4(acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y);
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < kJoinWarps; ++v) {
+            sum.x += s.sums[group][v][row][col];
+            sum.y += s.sums[group][v][row + 1][col];
+            sum.z += s.sums[group][v][row + 2][col];
+            sum.w += s.sums[group][v][row + 3][col];
+        }
+        Q[0] = sum.x;
+        Q[kD] = sum.y;
+        Q[2 * kD] = sum.z;
+        Q[3 * kD] = sum.w;
+        if (piece == w) {                         // the state in front of the next segment
+            *reinterpret_cast<float4 *>(&S[col][row]) = sum;
+            piece = 0;
+        }
+        __syncthreads();
+    }
+    if (waits.left == 0) {                        // (a copy did not come: no piece of the pair is run)
+        atomicCAS(p.status, 0, (int32_t)W12_E_TIMEOUT);
+        p.split.failed[pair * (2 * p.split.j + 1)] = 1;
+        if (threadIdx.x == 0) {
+            drain(s.full[0], ((last >> 1) + 1) & 1, p);
+            drain(s.full[1], (((last + 1) >> 1) + 1) & 1, p);
+        }
+        __syncwarp();
+    }
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -1194,6 +1418,16 @@ EncodeTiledFn encode_fn()
             fn = reinterpret_cast<EncodeTiledFn>(f);
     }
     return fn;
+}
+
+// Segments and their pieces for so many pairs of a call's rows: what the SMs take of both launches' items.
+constexpr size_t kSplitHeader = 4096;             // a word for each item of kAhead
+void split_of(int num_sms, int64_t pairs, int32_t n_rows, int32_t &j, int32_t &w)
+{
+    const int most = (int)std::min<int64_t>(std::min<int64_t>(num_sms, kSplitHeader / sizeof(int32_t)) / pairs, 64);   // CTAs a pair
+    j = (most - 1) / 2;
+    w = j > 0 ? std::min((most - 1) / j, 3) : 0;
+    if (j > 0) j = split_segments((int)(((int64_t)n_rows + kC - 1) / kC), j, w);
 }
 
 }  // namespace
@@ -1237,19 +1471,57 @@ int launch_gdn_prefill(const GdnSeqArgs &a, void *stream)
     p.H = a.H;
     p.group = a.H / a.Hk;
     p.n_req = a.n_req;
-    p.items = (uint32_t)a.n_req * (uint32_t)a.H;
     p.n_rows = a.n_rows;
-    p.polls = (uint32_t)std::min<uint64_t>(a.timeout_ns / kWaitSleepNs + 1, 1u << 31);
+    p.polls = (uint32_t)std::min<uint64_t>(a.timeout_ns / kWaitSleepNs + 1, 1u << 30);
     p.status = a.status;
     p.debug_flags = a.debug_flags;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((uint32_t)std::min<int64_t>((int64_t)a.H * a.n_req, a.num_sms));   // one CTA fills an SM
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(PrefillShared) + 1024;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = cudaFuncSetAttribute(k_gdn_prefill, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(k_gdn_prefill, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return (int)e;
-    return (int)cudaLaunchKernelEx(&cfg, k_gdn_prefill, maps[0], maps[1], maps[2], p);
+    const int64_t pairs = (int64_t)a.n_req * a.H;
+    cudaLaunchAttribute behind{};                 // a launch that begins while the one before it ends, and waits for that
+    behind.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    behind.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &behind;
+    auto run = [&](Mode mode, int subs) {
+        p.split.mode = mode;
+        p.subs = (uint32_t)subs;
+        p.items = (uint32_t)(pairs * subs);
+        cfg.gridDim = dim3((uint32_t)std::min<int64_t>(p.items, a.num_sms));   // one CTA fills an SM
+        cfg.numAttrs = mode == kPieces;
+        return cudaLaunchKernelEx(&cfg, k_gdn_prefill, maps[0], maps[1], maps[2], p);
+    };
+    if (a.scratch) split_of(a.num_sms, pairs, a.n_rows, p.split.j, p.split.w);
+    if (p.split.j == 0) return (int)run(kWhole, 1);
+    p.split.failed = static_cast<int32_t *>(a.scratch);
+    p.split.states = reinterpret_cast<float *>(static_cast<uint8_t *>(a.scratch) + kSplitHeader);
+    if ((e = run(kAhead, 2 * p.split.j + 1)) != cudaSuccess) return (int)e;
+    // (two groups halve P's ways from L2, which bound it where there are many rows; one is the faster where SMs are left)
+    auto join = [&](auto kernel, int groups, size_t bytes) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3(kD / kJoinRows / groups, (uint32_t)pairs);
+        c.blockDim = dim3(32 * kJoinWarps * groups);
+        c.dynamicSmemBytes = bytes;
+        c.stream = cfg.stream;
+        c.attrs = &behind;
+        c.numAttrs = 1;
+        return cudaLaunchKernelEx(&c, kernel, p);
+    };
+    e = pairs * (kD / kJoinRows) > a.num_sms ? join(k_gdn_join<2>, 2, sizeof(JoinShared<2>)) : join(k_gdn_join<1>, 1, sizeof(JoinShared<1>));
+    if (e != cudaSuccess) return (int)e;
+    return (int)run(kPieces, p.split.j * p.split.w + 1);
+}
+
+size_t gdn_scratch_bytes(int num_sms, int32_t H, int32_t n_rows)
+{
+    int j = 0, w;
+    for (int64_t pairs = H; j == 0 && pairs <= num_sms; pairs += H) split_of(num_sms, pairs, n_rows, j, w);
+    return j ? kSplitHeader + (size_t)num_sms * 2 * kD * kD * sizeof(float) : 0;
 }
 
 }  // namespace w12i

@@ -847,10 +847,20 @@ w12_status w12_gdn_prefill(const w12_gdn_rows *rows, int32_t n_req, const int32_
     const WsLayout L = layout_for(1, 0, 0, n_req);
     if ((s = ws_check(ws, ws_bytes, L)) != W12_OK) return s;
     Ws W{static_cast<uint8_t *>(ws), L};
+    if (rows->scratch) {
+        if (!aligned(rows->scratch, 16)) return W12_E_INVAL;
+        if (rows->scratch_bytes < gdn_scratch_bytes(a.num_sms, a.H, a.n_rows)) return W12_E_WORKSPACE;
+    }
     a.n_req = n_req;
     a.off = row_off;
+    a.scratch = rows->scratch;
     a.status = W.status();
     return cuda_status(launch_gdn_prefill(a, stream));
+}
+
+size_t w12_gdn_scratch_bytes(int32_t n_heads, int32_t n_rows)
+{
+    return n_heads < 1 || n_heads > 65535 || n_rows < 1 ? 0 : gdn_scratch_bytes(num_sms(), n_heads, n_rows);
 }
 
 w12_status w12_gdn_step(const w12_gdn_rows *rows, const float *S0, float *state, float *o, w12_stream_t stream)

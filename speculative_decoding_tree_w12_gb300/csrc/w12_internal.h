@@ -171,9 +171,11 @@ struct GdnSeqArgs {
     const float *S0;                // [n_req][H][d][d] or null (zero)
     float *state, *o;
     uint64_t timeout_ns;
+    void *scratch;                  // gdn_scratch_bytes(num_sms, H, n_rows) bytes, or null
     int32_t *status;
     int32_t debug_flags;
 };
+size_t gdn_scratch_bytes(int num_sms, int32_t H, int32_t n_rows);
 int launch_gdn_prefill(const GdnSeqArgs &a, void *stream);
 int launch_gdn_step(const GdnSeqArgs &a, void *stream);
 

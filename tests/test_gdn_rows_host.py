@@ -61,7 +61,8 @@ INVAL, UNSUPPORTED, WORKSPACE = -1, -2, -6
 
 
 def rows(w12, **kw):
-    f = dict(n_heads=4, n_qk_heads=2, head_dim=128, n_rows=10, q=A, k=A, v=A, q_stride=256, k_stride=256, v_stride=512, alpha=A, beta=A)
+    f = dict(n_heads=4, n_qk_heads=2, head_dim=128, n_rows=10, q=A, k=A, v=A, q_stride=256, k_stride=256, v_stride=512, alpha=A, beta=A,
+             scratch=0, scratch_bytes=0)
     f.update(kw)
     return w12.GdnRowsC(*(f[n] for n, _ in w12.GdnRowsC._fields_))
 
@@ -90,6 +91,18 @@ def test_prefill_refused(w12):
                      (dict(S0=A + 8), INVAL), (dict(state=A + 4), INVAL), (dict(o=A + 4), INVAL), (dict(ws=None), WORKSPACE),
                      (dict(ws=A + 16), WORKSPACE), (dict(nb=C.c_size_t(64)), WORKSPACE), (dict(rr=None), INVAL)):
         assert call(**kw) == want, kw
+
+
+def test_scratch_refused(w12):
+    """Scratch is checked where one is given: its alignment, and its size where a call of such rows would use it."""
+    L, big = w12.lib(), C.c_size_t(1 << 30)
+    call = lambda **kw: L.w12_gdn_prefill(C.byref(rows(w12, **kw)), 1, A, A, A, A, A, big, None)
+    need = L.w12_gdn_scratch_bytes(4, 5000)
+    assert need > 0 and L.w12_gdn_scratch_bytes(4, 100) == 0
+    assert L.w12_gdn_scratch_bytes(0, 5000) == 0 and L.w12_gdn_scratch_bytes(4, 0) == 0 and L.w12_gdn_scratch_bytes(65536, 5000) == 0
+    assert call(n_rows=5000, scratch=A + 8, scratch_bytes=need) == INVAL
+    assert call(n_rows=5000, scratch=A, scratch_bytes=need - 1) == WORKSPACE
+    assert call(n_rows=5000, scratch=A, scratch_bytes=0) == WORKSPACE
 
 
 def test_step_refused(w12):
