@@ -835,22 +835,29 @@ def w12_gdn_norm(o, weight, z=None, eps: float = 1e-6, gate_first: bool = False,
     reads them -> bfloat16 [R][H * 128]: rms(o) * weight * silu(z) per head, with
     ``gate_first`` rms(o * silu(z)) * weight.  weight: bfloat16 [128]; z:
     bfloat16 rows [R][H * 128] (slices of a fused row are fine), optional."""
-    _runtime()
-    lib()
-    _want(o, _torch.float32, (None, None, 128), "o")
-    R, H, d = o.shape
-    _want(weight, _torch.bfloat16, (d,), "weight")
-    dev = o.get_device()
-    if dev < 0 or weight.get_device() != dev:
-        raise ValueError("o and weight: tensors of one CUDA device wanted")
+    if _torch is None:
+        _runtime()
+        lib()
+    shape, dev = o.shape, o.get_device()
+    if len(shape) != 3 or shape[2] != 128 or o.dtype is not _torch.float32 or dev < 0 or not o.is_contiguous():
+        raise ValueError(f"o: contiguous float32 [rows][heads][128] of a CUDA device wanted, got {o.dtype} {tuple(shape)} on {o.device}")
+    R, H, _ = shape
+    width = H * 128
     if out is None:
-        out = _torch.empty((R, H * d), dtype=_torch.bfloat16, device=o.device)
-    za, zs = (None, 0) if z is None else _rows(z, R, H * d, "z", dev)
-    s = _lib.w12_gdn_norm(o.data_ptr(), R, H, d, za, zs, weight.data_ptr(), eps, int(gate_first),
-                          *_rows(out, R, H * d, "out", dev), _st(stream))
+        out = _torch.empty((R, width), dtype=_torch.bfloat16, device=o.device)
+    za, zs = (None, 0) if z is None else _rows(z, R, width, "z", dev)
+    oa, os_ = _rows(out, R, width, "out", dev)
+    s = _lib.w12_gdn_norm(o.data_ptr(), R, H, 128, za, zs, _vector(weight, 128, "weight", dev), eps, gate_first, oa, os_, _st(stream))
     if s:
         raise W12Error(s, "w12_gdn_norm")
     return out
+
+
+def _vector(t, n, what, dev):
+    """The address of n contiguous bfloat16."""
+    if t.dtype is not _torch.bfloat16 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous bfloat16 [{n}] on cuda:{dev} wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 class ResidualC(C.Structure):
@@ -879,27 +886,23 @@ def w12_block_norm(h, y=None, pre=None, post=None, scale: float = 1.0, eps: floa
     output, bfloat16 rows (None: h' = h); pre, post: bfloat16 [n] (None: no norm
     there, and without pre no x).  h' goes to ``h_out`` (default: new rows; may
     be h), x to ``out``."""
-    _runtime()
-    lib()
-    if h.dim() != 2:
-        raise ValueError("h: rows wanted")
-    R, n = h.shape
-    dev, f32 = h.get_device(), h.dtype is _torch.float32
-    if dev < 0:
-        raise ValueError("tensors of a CUDA device wanted")
-    for w, what in ((pre, "pre"), (post, "post")):
-        if w is not None:
-            _want(w, _torch.bfloat16, (n,), what)
-            if w.get_device() != dev:
-                raise ValueError(f"{what}: on cuda:{dev} wanted")
+    if _torch is None:
+        _runtime()
+        lib()
+    shape, dev, f32 = h.shape, h.get_device(), h.dtype is _torch.float32
+    if len(shape) != 2 or dev < 0:
+        raise ValueError("h: rows of a CUDA device wanted")
+    R, n = shape
     ha, hs = _stream_rows(h, R, n, f32, "h", dev)
-    ya = ys = oa = os_ = xa = xs = 0
+    ya = ys = oa = os_ = xa = xs = posta = prea = 0
     if y is None:
         if h_out is not None or post is not None:
             raise ValueError("h_out and post: only with y")
         h_out = h
     else:
         ya, ys = _rows(y, R, n, "y", dev)
+        if post is not None:
+            posta = _vector(post, n, "post", dev)
         if h_out is None:
             h_out = _torch.empty((R, n), dtype=h.dtype, device=h.device)
         oa, os_ = _stream_rows(h_out, R, n, f32, "h_out", dev)
@@ -907,10 +910,10 @@ def w12_block_norm(h, y=None, pre=None, post=None, scale: float = 1.0, eps: floa
         if out is None:
             out = _torch.empty((R, n), dtype=_torch.bfloat16, device=h.device)
         xa, xs = _rows(out, R, n, "out", dev)
+        prea = _vector(pre, n, "pre", dev)
     elif out is not None:
         raise ValueError("out: only with pre")
-    s = _lib.w12_block_norm(C.byref(ResidualC(R, int(f32), n, ha, hs, oa, os_, ya, ys, _dp(post), scale, _dp(pre), eps, xa, xs)),
-                            _st(stream))
+    s = _lib.w12_block_norm(C.byref(ResidualC(R, f32, n, ha, hs, oa, os_, ya, ys, posta, scale, prea, eps, xa, xs)), _st(stream))
     if s:
         raise W12Error(s, "w12_block_norm")
     return h_out, out
