@@ -1358,7 +1358,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps * kGroups, 1) k_gdn_join(const
         if (threadIdx.x == 0 && slot < last) fetch(slot + 1);
         Q += 2 * kD * kD;                         // (a piece's states lie behind those of the one before)
         float4 sum = read_q();
-        float2 acc[kJoinRows][2] = {};
+        float2 acc[kJoinRows / 2][4] = {};        // of two rows (which lie beside one another: four values doubled a feature, not eight)
         waits.on(s.full[slot & 1], ((slot - 1) >> 1) & 1);
 #pragma unroll
         for (int l = 0; l < kOwn; ++l) {
@@ -1366,14 +1366,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps * kGroups, 1) k_gdn_join(const
             read_n(S[warp * kOwn + l], x);
             const float4 y = *reinterpret_cast<const float4 *>(&s.P[slot & 1][warp * kOwn + l][4 * lane]);
 #pragma unroll
-            for (int r = 0; r < kJoinRows; ++r) {
-                acc[r][0] = __ffma2_rn(make_float2(x[r], x[r]), make_float2(y.x, y.y), acc[r][0]);
-                acc[r][1] = __ffma2_rn(make_float2(x[r], x[r]), make_float2(y.z, y.w), acc[r][1]);
+            for (int r = 0; r < kJoinRows / 2; ++r) {
+                const float2 rows = make_float2(x[2 * r], x[2 * r + 1]);
+                acc[r][0] = __ffma2_rn(rows, make_float2(y.x, y.x), acc[r][0]);
+                acc[r][1] = __ffma2_rn(rows, make_float2(y.y, y.y), acc[r][1]);
+                acc[r][2] = __ffma2_rn(rows, make_float2(y.z, y.z), acc[r][2]);
+                acc[r][3] = __ffma2_rn(rows, make_float2(y.w, y.w), acc[r][3]);
             }
         }
 #pragma unroll
-        for (int r = 0; r < kJoinRows; ++r)
-            *reinterpret_cast<float4 *>(&s.sums[group][warp][r][4 * lane]) = make_float4(acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y);
+        for (int r = 0; r < kJoinRows / 2; ++r) {
+            float(*sums)[kD] = &s.sums[group][warp][2 * r];
+            *reinterpret_cast<float4 *>(&sums[0][4 * lane]) = make_float4(acc[r][0].x, acc[r][1].x, acc[r][2].x, acc[r][3].x);
+            *reinterpret_cast<float4 *>(&sums[1][4 * lane]) = make_float4(acc[r][0].y, acc[r][1].y, acc[r][2].y, acc[r][3].y);
+        }
         __syncthreads();
 #pragma unroll
         for (int v = 0; v < kJoinWarps; ++v) {
