@@ -417,7 +417,7 @@ typedef struct {
     const uint16_t *v;           /* device BF16 [n_rows][n_heads][d], the same */
     int64_t q_stride, k_stride, v_stride;
     const float *alpha, *beta;   /* device [n_rows][n_heads]: gates and write strengths */
-    void *scratch;               /* w12_gdn_prefill: device, 16-byte aligned, one call's at a time; or NULL: a request's head
+    void *scratch;               /* w12_gdn_prefill: device, 32-byte aligned, one call's at a time; or NULL: a request's head
                                     is then one SM's, however long it is */
     size_t scratch_bytes;        /* w12_gdn_scratch_bytes(n_heads, n_rows) at least (else W12_E_WORKSPACE) */
 } w12_gdn_rows;
@@ -427,27 +427,29 @@ size_t w12_gdn_scratch_bytes(int32_t n_heads, int32_t n_rows);
 
 /*
  * Rows row_off[r] .. row_off[r+1]-1 (device [n_req + 1]) continue request r's
- * state S0[r] (device FP32 [n_req][n_heads][d][d] as S[v][k], 16-byte aligned;
- * NULL: zero): every row's output o (device FP32 [n_rows][n_heads][d]) and the
- * state behind the last row (device, layout of S0, 16-byte aligned; may be S0
+ * state S0[r] (device FP32 [n_req][n_heads][d][d] as S[v][k], 32-byte aligned;
+ * NULL: zero): every row's output o (device FP32 [n_rows][n_heads][d], 16-byte aligned) and the
+ * state behind the last row (device, layout of S0, 32-byte aligned; may be S0
  * itself, else the two do not overlap).  Any number of rows a request, none
  * included: its state is then copied.  Rows outside every request are neither
  * read nor written.  Requests' rows do not overlap.
- * Outputs and states are those of the token-by-token form to FP32 rounding:
- * FP32 operands enter the tensor cores as three BF16 pieces that add up to them, with
- * FP32 accumulation.  Gates may be zero.  A value of a row that is not finite reaches the
- * outputs of its own run of 64 rows (counted from row_off[r]) and all later
- * ones of its request and head; other requests and heads never.
+ * Outputs and states are those of the token-by-token form to FP32 rounding: next to BF16 operands, FP32 ones enter the
+ * tensor cores as three BF16 pieces that add up to them; two FP32 operands both enter as two F16 pieces of 22 bits; sums
+ * are FP32.  Runs of 64 rows (counted from row_off[r]) are taken at once, and with scratch few long requests are cut into parts
+ * that run beside one another: where they are cut depends on n_req, n_rows and the request's rows, so the last bits of a
+ * request's results may depend on the call it is in, but not from one such call to the next.  Gates may be zero or negative.
+ * A value of a row that is not finite may reach every output of its own run of 64 rows and of all later rows of its request and
+ * head; other requests and heads never.
  * ws: as for w12_tree_build.  Device checks: offsets that descend or leave
  * [0, n_rows] set W12_E_INVAL in the status word, and that request is left as it was;
- * a wait that runs out sets W12_E_TIMEOUT (outputs undefined).
+ * a wait that runs out sets W12_E_TIMEOUT (outputs undefined, the states of the requests and heads concerned not written).
  */
 w12_status w12_gdn_prefill(const w12_gdn_rows *rows, int32_t n_req, const int32_t *row_off, const float *S0,
                            float *state, float *o, void *ws, size_t ws_bytes, w12_stream_t stream);
 
 /*
  * One token of every request: row r continues request r (n_rows requests, at
- * most 65535 of them).  S0, state and o as above.
+ * most 65535 of them).  S0, state and o as above, all of them 16-byte aligned.
  */
 w12_status w12_gdn_step(const w12_gdn_rows *rows, const float *S0, float *state, float *o, w12_stream_t stream);
 

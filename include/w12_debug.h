@@ -24,8 +24,8 @@ extern "C" {
  *                several requests), CTA (0, 0) never copies its first
  *                request's state: its splitters' wait runs out, both warp
  *                roles stop, W12_E_TIMEOUT is recorded and tensor memory is
- *                released.  w12_tree_attention: CTA 0 never copies a key, with
- *                the same end.
+ *                released.  w12_tree_attention, w12_gdn_prefill: CTA 0 never
+ *                copies a key, with the same end.
  *   flags bit 1: run every GEMM on the tensor-memory (tcgen05) kernel.
  *   flags bit 2: run every GEMM on the warp-MMA kernel (64 rows per pass).
  *                Without either bit the library picks by row count.

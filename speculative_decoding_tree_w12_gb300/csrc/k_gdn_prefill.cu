@@ -339,6 +339,22 @@ __device__ __forceinline__ void read_n(const float *src, float (&x)[N])
     }
 }
 
+// eight values of global memory, a whole 32-byte sector a lane (half of one at a time, as four values are, takes the load and store
+// units twice as long where every lane has a row of its own)
+__device__ __forceinline__ void load8(const float *src, float *x)
+{
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void store8(float *dst, const float *x)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]),
+                 "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+
 // x *= y; x *= f; z += x y, two at a time
 template <int N>
 __device__ __forceinline__ void mul_n(float (&x)[N], const float (&y)[N])
@@ -489,14 +505,12 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
         const Chunk &t = s.chunk[g % kChunks];
         const int at = c * kD + 64 * part;                                // this thread's half of the row
         if (t.start != kGoesOn) {
+            if (t.start == kFromState) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float4 x = t.start == kFromState ? *reinterpret_cast<const float4 *>(t.from + at + 4 * i)
-                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-                S[4 * i] = x.x;
-                S[4 * i + 1] = x.y;
-                S[4 * i + 2] = x.z;
-                S[4 * i + 3] = x.w;
+                for (int i = 0; i < 64; i += 8) load8(t.from + at + i, S + i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) S[i] = 0.f;
             }
             if (t.start == kFromOne) {
 #pragma unroll
@@ -556,8 +570,7 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
         }
         if (t.to && waits.left && !*(volatile int32_t *)&s.abort) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                *reinterpret_cast<float4 *>(t.to + at + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+            for (int i = 0; i < 64; i += 8) store8(t.to + at + i, S + i);
         }
     }
     waits.end(s);

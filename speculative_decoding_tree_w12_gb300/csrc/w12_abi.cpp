@@ -842,13 +842,13 @@ w12_status w12_gdn_prefill(const w12_gdn_rows *rows, int32_t n_req, const int32_
     GdnSeqArgs a;
     w12_status s = gdn_seq_args(rows, S0, state, o, a);
     if (s != W12_OK) return s;
-    if (n_req < 1 || !row_off || !state) return W12_E_INVAL;
+    if (n_req < 1 || !row_off || !state || !aligned(state, 32) || !aligned(S0, 32)) return W12_E_INVAL;
     if (n_req > kMaxBudget) return W12_E_UNSUPPORTED;
     const WsLayout L = layout_for(1, 0, 0, n_req);
     if ((s = ws_check(ws, ws_bytes, L)) != W12_OK) return s;
     Ws W{static_cast<uint8_t *>(ws), L};
     if (rows->scratch) {
-        if (!aligned(rows->scratch, 16)) return W12_E_INVAL;
+        if (!aligned(rows->scratch, 32)) return W12_E_INVAL;
         if (rows->scratch_bytes < gdn_scratch_bytes(a.num_sms, a.H, a.n_rows)) return W12_E_WORKSPACE;
     }
     a.n_req = n_req;

@@ -88,7 +88,7 @@ def test_prefill_refused(w12):
     r, big = rows(w12), C.c_size_t(1 << 30)
     call = lambda n=2, off=A, S0=A, state=A, o=A, ws=A, nb=big, rr=C.byref(r): w12.lib().w12_gdn_prefill(rr, n, off, S0, state, o, ws, nb, None)
     for kw, want in ((dict(n=0), INVAL), (dict(n=513), UNSUPPORTED), (dict(off=None), INVAL), (dict(state=None), INVAL), (dict(o=None), INVAL),
-                     (dict(S0=A + 8), INVAL), (dict(state=A + 4), INVAL), (dict(o=A + 4), INVAL), (dict(ws=None), WORKSPACE),
+                     (dict(S0=A + 8), INVAL), (dict(S0=A + 16), INVAL), (dict(state=A + 4), INVAL), (dict(state=A + 16), INVAL), (dict(o=A + 4), INVAL), (dict(ws=None), WORKSPACE),
                      (dict(ws=A + 16), WORKSPACE), (dict(nb=C.c_size_t(64)), WORKSPACE), (dict(rr=None), INVAL)):
         assert call(**kw) == want, kw
 
@@ -100,7 +100,7 @@ def test_scratch_refused(w12):
     need = L.w12_gdn_scratch_bytes(4, 5000)
     assert need > 0 and L.w12_gdn_scratch_bytes(4, 100) == 0
     assert L.w12_gdn_scratch_bytes(0, 5000) == 0 and L.w12_gdn_scratch_bytes(4, 0) == 0 and L.w12_gdn_scratch_bytes(65536, 5000) == 0
-    assert call(n_rows=5000, scratch=A + 8, scratch_bytes=need) == INVAL
+    assert call(n_rows=5000, scratch=A + 16, scratch_bytes=need) == INVAL
     assert call(n_rows=5000, scratch=A, scratch_bytes=need - 1) == WORKSPACE
     assert call(n_rows=5000, scratch=A, scratch_bytes=0) == WORKSPACE
 
