@@ -116,6 +116,7 @@ struct PrefillShared {
     uint32_t tmem;
     int32_t abort;
     int32_t total;                  // chunks of this CTA
+    int32_t silent;                 // whose outputs nobody wants (Q and P)
     uint16_t order[w12i::kMaxBudget];   // the requests, those with the most rows first
 };
 static_assert(offsetof(PrefillShared, L) % 16 == 0 && kLFloats % 4 == 0, "rows of four floats");
@@ -452,8 +453,9 @@ struct Part {
 };
 __device__ __forceinline__ int piece_start(const PrefillParams &p, int nc, int j, uint32_t i)
 {
-    const uint32_t n = (j + 1) * p.split.w + 1, like = (uint32_t)nc / n;
-    return (int)(i * like + i * (nc - n * like) / n);
+    // (in eighths of a piece: the first w pieces are shorter by one, since a chunk with its outputs takes that much longer than Q's and P's)
+    const uint32_t w = p.split.w, n = 8 * (j * w + 1) + 7 * w, like = (uint32_t)nc / n, at = i < w ? 7 * i : 8 * i - w;
+    return (int)(at * like + at * (nc - n * like) / n);
 }
 __device__ __forceinline__ Part part_of(const PrefillParams &p, int nc, int sub)
 {
@@ -636,6 +638,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         }
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_x), lane);
+        if (s.silent) continue;
 
         // S q to where U A is added to it: G S q in the units of U and A.  U's unit is a bound, at most 64 |M| |X|
         // (F16 has 16 bits to spare under the largest value), and one under which S q keeps finite.
@@ -999,6 +1002,7 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
 {
     Waits waits{p.polls + s.total};
     const int total = s.total;
+    const bool silent = s.silent;
     bool ok = true;
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
         ok = ok && waits.on(bar, parity);
@@ -1039,9 +1043,9 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
             for (int piece = 2; piece >= 0; --piece) product(kColDK, kq, half, piece, half == 0 && piece == 2);
             if (half) tc_commit(smem_u32(&s.done_k));
         }
-        if (g > 0 && !wait(s.read_o, par ^ 1u)) break;
+        if (!silent && g > 0 && !wait(s.read_o, par ^ 1u)) break;
 #pragma unroll 1
-        for (int q = 0; q < 6; ++q) product(kColDQ, kq + kC * 128, q & 1, 2 - (q >> 1), q == 0);
+        for (int q = silent ? 6 : 0; q < 6; ++q) product(kColDQ, kq + kC * 128, q & 1, 2 - (q >> 1), q == 0);
         tc_commit(smem_u32(&s.done_q));
         if (!wait(s.mready[st], par2) || !wait(s.have_x, par)) break;
         pairs(kColU, kColX, s.M[0], 0);
@@ -1063,8 +1067,10 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
                 }
             }
         }
-        if (!wait(s.have_u, par)) break;
-        pairs(kColDQ, kColUA, s.A[st][0], 1);
+        if (!silent) {
+            if (!wait(s.have_u, par)) break;
+            pairs(kColDQ, kColUA, s.A[st][0], 1);
+        }
         tc_commit(smem_u32(&s.done_o));
         tc_commit(smem_u32(&s.gused[st]));
     }
@@ -1209,7 +1215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             rows[r] = request_rows(p, r);
             if (rows[r] < 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
         }
-        if (tid == 0) s.total = 0;
+        if (tid == 0) s.total = s.silent = 0;
         __syncthreads();
         for (int r = tid; r < p.n_req; r += kThreads) {
             const int mine = rows[r];
@@ -1240,6 +1246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = s.order[rank];
             if (p.split.mode == kAhead) {
                 if (sub == 0 && rows[r] == 0) keep_state(p, r * p.H + h);
+                if (tid == 0 && sub) s.silent = 1;
                 if (sub && !(sub & 1)) {          // P has no values
 #pragma unroll 1
                     for (int e = tid; e < (int)(sizeof(s.V) / 16); e += kThreads) reinterpret_cast<uint4 *>(s.V)[e] = make_uint4(0, 0, 0, 0);
