@@ -1208,52 +1208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     PrefillShared &s = *reinterpret_cast<PrefillShared *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, warp = tid >> 5;
     if (p.split.mode == kAhead) pdl_launch_dependents();   // (the join waits for this launch's end, in the SMs that are left)
-    {
-        // the requests by their rows, and this CTA's chunks
-        int32_t *rows = reinterpret_cast<int32_t *>(s.KQ[0]);
-        for (int r = tid; r < p.n_req; r += kThreads) {
-            rows[r] = request_rows(p, r);
-            if (rows[r] < 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
-        }
-        if (tid == 0) s.total = s.silent = 0;
-        __syncthreads();
-        for (int r = tid; r < p.n_req; r += kThreads) {
-            const int mine = rows[r];
-            int rank = 0;
-#pragma unroll 1
-            for (int j = 0; j < p.n_req; ++j) rank += rows[j] > mine || (rows[j] == mine && j < r);
-            s.order[rank] = (uint16_t)r;
-        }
-        __syncthreads();
-        int chunks = 0;
-#pragma unroll 1
-        for (uint32_t cycle = tid, at; (at = item(cycle)) < p.items; cycle += kThreads) {
-            const int rank = at / (p.subs * p.H);
-            const Part part = part_of(p, chunks_of(rows[s.order[rank]]), (at - rank * p.subs * p.H) / p.H);
-            chunks += part.end - part.first;
-        }
-        if (chunks) atomicAdd(&s.total, chunks);
-        if (p.split.mode == kWhole) {
-            // where there is no token the state stays what it was (those pairs come last)
-#pragma unroll 1
-            for (uint32_t cycle = 0, at; (at = item(cycle)) < p.items; ++cycle) {
-                const int rank = at / (uint32_t)p.H, r = s.order[rank];
-                if (rows[r] == 0) keep_state(p, r * p.H + (at - rank * p.H));
-            }
-        } else if (blockIdx.x < p.items) {        // one item: see above
-            const uint32_t at = blockIdx.x;
-            const int rank = at / (p.subs * p.H), left = at - rank * p.subs * p.H, sub = left / p.H, h = left - sub * p.H;
-            const int r = s.order[rank];
-            if (p.split.mode == kAhead) {
-                if (sub == 0 && rows[r] == 0) keep_state(p, r * p.H + h);
-                if (tid == 0 && sub) s.silent = 1;
-                if (sub && !(sub & 1)) {          // P has no values
-#pragma unroll 1
-                    for (int e = tid; e < (int)(sizeof(s.V) / 16); e += kThreads) reinterpret_cast<uint4 *>(s.V)[e] = make_uint4(0, 0, 0, 0);
-                }
-            }
-        }
-    }
+    static_assert(w12i::kMaxBudget <= kThreads, "a request to a thread");
+    const int mine = tid < p.n_req ? request_rows(p, tid) : 0;   // (on its way while the rest is set up)
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.told[i]), 1);
         for (int st = 0; st < kStages; ++st) {
@@ -1288,6 +1244,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int piece = 0; piece < 2; ++piece) {
             *reinterpret_cast<uint4 *>(s.M[piece] + at) = z;
             for (int st = 0; st < 2; ++st) *reinterpret_cast<uint4 *>(s.A[st][piece] + at) = z;
+        }
+    }
+    {
+        // the requests by their rows, and this CTA's chunks
+        int32_t *rows = reinterpret_cast<int32_t *>(s.KQ[0]);
+        if (tid < p.n_req) {
+            rows[tid] = mine;
+            if (mine < 0) atomicCAS(p.status, 0, (int32_t)W12_E_INVAL);
+        }
+        if (tid == 0) s.total = s.silent = 0;
+        __syncthreads();
+        if (tid < p.n_req) {
+            int rank = 0;
+#pragma unroll 1
+            for (int j = 0; j < p.n_req; ++j) rank += rows[j] > mine || (rows[j] == mine && j < tid);
+            s.order[rank] = (uint16_t)tid;
+        }
+        __syncthreads();
+        int chunks = 0;
+#pragma unroll 1
+        for (uint32_t cycle = tid, at; (at = item(cycle)) < p.items; cycle += kThreads) {
+            const int rank = at / (p.subs * p.H);
+            const Part part = part_of(p, chunks_of(rows[s.order[rank]]), (at - rank * p.subs * p.H) / p.H);
+            chunks += part.end - part.first;
+        }
+        if (chunks) atomicAdd(&s.total, chunks);
+        if (p.split.mode == kWhole) {
+            // where there is no token the state stays what it was (those pairs come last)
+#pragma unroll 1
+            for (uint32_t cycle = 0, at; (at = item(cycle)) < p.items; ++cycle) {
+                const int rank = at / (uint32_t)p.H, r = s.order[rank];
+                if (rows[r] == 0) keep_state(p, r * p.H + (at - rank * p.H));
+            }
+        } else if (blockIdx.x < p.items) {        // one item: see above
+            const uint32_t at = blockIdx.x;
+            const int rank = at / (p.subs * p.H), left = at - rank * p.subs * p.H, sub = left / p.H, h = left - sub * p.H;
+            const int r = s.order[rank];
+            if (p.split.mode == kAhead) {
+                if (sub == 0 && rows[r] == 0) keep_state(p, r * p.H + h);
+                if (tid == 0 && sub) s.silent = 1;
+                if (sub && !(sub & 1)) {          // P has no values
+#pragma unroll 1
+                    for (int e = tid; e < (int)(sizeof(s.V) / 16); e += kThreads) reinterpret_cast<uint4 *>(s.V)[e] = make_uint4(0, 0, 0, 0);
+                }
+            }
         }
     }
     fence_async_shared();
