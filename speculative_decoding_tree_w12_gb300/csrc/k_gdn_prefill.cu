@@ -12,14 +12,12 @@
 // M = (I + L)^-1 and A need no state, so they are made a chunk ahead.  The D_ij
 // are running products, never quotients: a gate of zero forgets, as it should.
 //
-// A CTA takes one (request, head) after another; the state rows c lie on the 128 lanes of tensor
-// memory throughout, so that all its products take their left operand from
-// there and no operand but M and A is ever written to shared memory:
+// A CTA takes one (request, head) after another; the state rows c lie on the 128 lanes of tensor memory throughout, so that
+// all its products take their left operand from there and no operand but M and A is ever written to shared memory:
 //     D_K[c][j] = S k_j    D_Q[c][j] = S q_j    U[c][i] = X M^T    U A^T    S' = U K.
-// Products with keys and queries take those as they are and the FP32 side (S, U) as three BF16
-// pieces that add up to it exactly: two (2^-17) would be the largest error of the layer by
-// far.  Products of two FP32 sides (X M^T, U A^T) take both as two F16 pieces (2^-22) under a power of two
-// for each row, and of their four pairs all but the smallest.  All accumulation is FP32.
+// Products with keys and queries take those as they are and the FP32 side (S, U) as three BF16 pieces that add up to it exactly:
+// two (2^-17) would be the largest error of the layer by far.  Products of two FP32 sides (X M^T, U A^T) take both as two F16
+// pieces (2^-22) under a power of two for each row, and of their four pairs all but the smallest.  All accumulation is FP32.
 //
 // A chunk runs through S's pieces -> S k -> X -> U -> U's pieces -> U K -> S', each step of which waits for the one before
 // it; the rest (A, M, U A^T and the outputs) is other warps' work, a chunk ahead or beside it:
@@ -29,9 +27,13 @@
 //    blocks of 16, whose columns are solved in registers, and A,
 //  * inverse warps (20..23): M, the blocks below those from them,
 //  * warp 24 issues the products with the state, warp 25 the copies by TMA, warps 26 and 27 make M's pieces.
-// What a chunk takes is the warps' instructions, not the products (a quarter of its time): of those the cutting into
-// pieces, three BF16 pieces 11 cycles of a scheduler for two values of 32 lanes, two F16 pieces 5.  The products are issued
-// in rolled loops and the code is kept short: straight-line code of a few times this length spent half its time on its own way in.
+// A chunk takes 4.4 to 4.7 us (8,400 to 9,000 cycles) however many there are: sixteen prompts of up to 8192 tokens x 32 heads
+// 1481 us, 2.7 times what their bytes take at the measured copy bandwidth.  That is the way through the steps above, whose longest
+// are the cutting into pieces (S 1,800 cycles, X and U 1,500 each: three BF16 pieces take 11 cycles of a scheduler for two
+// values of 32 lanes, two F16 pieces 5), M X 600, U K 800 and some 200 for each hand-over between warps; the schedulers issue in 58 %
+// of the cycles, the tensor cores work in 32 %.  With fewer warps of more columns each it took 1.6 times as long.
+// The products are issued in rolled loops and the code is kept short: straight-line code of a few times this length spent half
+// its time on its own way in.  A new pair costs 3 us more than its chunks, 5 where a state is read.
 // Every wait is bounded; when one has run out the state is left unwritten.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -133,7 +135,7 @@ constexpr uint32_t kKqBytes = sizeof(PrefillShared::KQ) / kStages, kVBytes = siz
 //  * k_gdn_join: the states in front of every piece but the first w from those,
 //  * kPieces: those pieces, now with their outputs.
 // That takes w + 1 pieces' time of n, and (2 j + 1) and (j w + 1) CTAs a pair (one of 4096 tokens, 4 heads: 299 us in one
-// part a head, 94 cut; of 32768 tokens, 32 heads: 2346 and 1412).  The launches overlap: each begins where SMs are left, and waits for the
+// part a head, 87 cut; of 32768 tokens, 32 heads: 2346 and 1322).  The launches overlap: each begins where SMs are left, and waits for the
 // one before it only for what that wrote (3 to 6 us of those).  All three as one launch whose CTAs wait for one another's
 // counts were slower (4096 tokens, 4 heads: 130 us), the join being short of registers and of shared memory there.
 enum Mode : int32_t { kWhole, kAhead, kPieces };

@@ -10,6 +10,9 @@
 // lines and each sum takes three shuffles; a warp takes eight rows, every load
 // of which is asked for before the first is used.  Four CTAs of 32 rows to a
 // head: one request of 32 heads puts 128 CTAs on the machine.
+//
+// 256 requests of 32 heads (1.08 GB): 163 us by itself, 6.6 TB/s; 24 requests 14.7 us, 6.9 TB/s; one request 4.1 us, which
+// is the launch and one way to memory and back.
 #include <cuda_runtime.h>
 
 #include "w12_internal.h"

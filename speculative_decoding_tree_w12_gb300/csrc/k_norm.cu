@@ -11,6 +11,9 @@
 // Both are bound by memory: one pass, each input read once and each output
 // written once, sums in FP32 in registers.  x is taken from the FP32 h', not
 // from the value that is stored: one rounding less in every layer.
+//
+// 16384 rows of 32 heads with their gate (537 MB): 76 us, 7.0 TB/s.  Between two blocks of 5120 values, 16384 rows: 99.8 us BF16
+// (6.7 TB/s), 149.7 us FP32 with a norm behind the block (6.7); 192 rows take 4 us, the launch and one way to memory and back.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -269,7 +272,8 @@ int launch_block_norm(const BlockNormArgs &a, void *stream)
     p.scale = a.scale;
     p.eps = a.eps;
     p.inv_n = 1.f / (float)a.n;
-    // as many threads as leave one piece to each, two beyond 1024 threads
+    // As many threads as leave one piece to each, two beyond 1024 threads.  (16384 BF16 rows of 5120 values: one piece 99.8 us,
+    // two 115.0; of 2560: 49.1 and 54.9; 192 rows of 8192: 3.5 and 3.3.  Rows of 16384, which only go with two: 393 us, 5.5 TB/s.)
     const int v = p.pieces <= 1024 ? 1 : 2;
     const int threads = ((p.pieces + v - 1) / v + 31) / 32 * 32;
     const auto k16 = v == 1 ? k_block_norm<false, 1> : k_block_norm<false, 2>;
