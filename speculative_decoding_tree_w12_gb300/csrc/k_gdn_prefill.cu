@@ -31,7 +31,7 @@
 // 1481 us, 2.7 times what their bytes take at the measured copy bandwidth.  That is the way through the steps above, whose longest
 // are the cutting into pieces (S 1,800 cycles, X and U 1,500 each: three BF16 pieces take 11 cycles of a scheduler for two
 // values of 32 lanes, two F16 pieces 5), M X 600, U K 800 and some 200 for each hand-over between warps; the schedulers issue in 58 %
-// of the cycles, the tensor cores work in 32 %.  With fewer warps of more columns each it took 1.6 times as long.
+// of the cycles, the tensor cores work in 32 %.  With fewer warps of more columns each it took 1.2 times as long.
 // The products are issued in rolled loops and the code is kept short: straight-line code of a few times this length spent half
 // its time on its own way in.  A new pair costs 3 us more than its chunks, 5 where a state is read.
 // Every wait is bounded; when one has run out the state is left unwritten.
