@@ -2,7 +2,7 @@
 
 Every step drafts a tree per request, runs the layers over all rows of all
 trees at once (``w12_gemm`` for the linears, ``w12_tree_attention`` over the
-paged cache), verifies the drafts against the model's own distribution
+paged cache, ``w12_block_norm`` between them), verifies the drafts against the model's own distribution
 (``w12_tree_verify_sampled``) and moves the accepted paths into the cache
 (``w12_kv_commit``).  Prompts enter through the same layers in chunks, which
 ``w12_kv_append`` appends.
@@ -43,6 +43,7 @@ class Decoder:
             self.qkv.append(linear((heads + 2 * kv_heads) * D, hidden))
             self.o.append(linear(hidden, heads * D))
         self.head = linear(vocab, hidden, 3.0)
+        self.one = torch.ones(hidden, dtype=torch.bfloat16, device=device)     # the norms' weights
         self.embed = torch.from_numpy(rng.standard_normal((vocab, hidden)).astype(np.float32)).bfloat16().to(device)
         # the drafter: every token's two likeliest successors with no context but itself
         self.draft = (norm(self.embed).float() @ self.dense[-1].to(device).float().T).topk(2).indices.cpu()
@@ -72,15 +73,16 @@ class Session:
 
     def forward(self, tree, tokens):
         """Logits of the tree's rows, and every layer's fused rows (its keys and values among them)."""
-        m, x, rows = self.m, self.m.embed[tokens.long()], []
+        m, rows = self.m, []
+        x, n = w12.w12_block_norm(m.embed[tokens.long()], pre=m.one)
         wq, wk = m.heads * D, m.kv_heads * D
         for qkv, o, cache in zip(m.qkv, m.o, self.caches):
-            r = w12.w12_gemm(qkv, norm(x), self.ws)
+            r = w12.w12_gemm(qkv, n, self.ws)
             a = w12.w12_tree_attention(cache, self.rope, tree, self.n, r[:, :wq], r[:, wq:wq + wk], r[:, wq + wk:], self.ws,
                                        self.aws)
-            x = x + w12.w12_gemm(o, a.view(len(tokens), wq), self.ws)
+            x, n = w12.w12_block_norm(x, w12.w12_gemm(o, a.view(len(tokens), wq), self.ws), pre=m.one)
             rows.append((r[:, wq:wq + wk], r[:, wq + wk:]))
-        return w12.w12_gemm(m.head, norm(x), self.ws), rows
+        return w12.w12_gemm(m.head, n, self.ws), rows
 
     def prefill(self, prompts):
         """All prompt tokens but the last of each request into the caches."""

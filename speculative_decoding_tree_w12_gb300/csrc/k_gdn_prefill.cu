@@ -68,8 +68,9 @@ constexpr uint32_t kColKK = 448;    // k.k (lanes 0..63) and q.k (lanes 64..127)
 // L, then M: three blocks of 32 x 32 (the one above the diagonal is zero), their FP32 rows 16-byte aligned and 4 banks apart
 constexpr int kLS = 36;
 constexpr int kL11 = 0, kL22 = 32 * kLS, kL21 = 2 * 32 * kLS, kLFloats = 3 * 32 * kLS;
-constexpr int kBarGate = 1, kBarInv = 6, kBarQuery = 7, kBarPiece = 8;   // named barriers of the gate and of the inverse warps, of the gate warps' latter two
-constexpr int kBarRow = 2;                 // and of the two token warps of 32 state rows (2 .. 5)
+// named barriers: of the gate warps, of the inverse warps, of the gate warps' latter two, of the piece warps, and of the two
+// token warps of 32 state rows (2 .. 5)
+constexpr int kBarGate = 1, kBarInv = 6, kBarQuery = 7, kBarPiece = 8, kBarRow = 2;
 constexpr int kStages = 3;          // of keys and queries (their chunk is prepared while two others are in use)
 
 // what a chunk is of
@@ -147,9 +148,10 @@ struct SplitParams {
     int32_t *failed;                // [pair][2 j + 1]: whether an item of kAhead has given up
 };
 
-// Segments of a request of nc chunks.  The join takes a product of 1.1 us for each piece of them, so no more than pay for theirs; and it and
-// two more launches some 35 us, eight chunks' time (4.6 us each), which the j w pieces not waited for have to save.  (One request
-// of 32 heads, j = 1: 16 chunks 87 us whole, 94 cut, 24 chunks 124 and 112; of 16 heads, j = 4: 10 chunks 60 and 62, 12 chunks 69 and 67.)
+// Segments of a request of nc chunks.  The join takes a product of 1.1 us for each piece of them, so no more than pay for
+// theirs; and it and one more launch some 35 us, eight chunks' time (4.6 us each), which the j w pieces that run beside the others
+// have to save.  (One request of 32 heads, j = 1: 16 chunks 87 us whole, 94 cut, 24 chunks 124 and 112; of 16 heads, j = 4: 10 chunks
+// 60 and 62, 12 chunks 69 and 67.)
 __host__ __device__ inline int split_segments(int nc, int j, int w)
 {
     while (j > 0 && (j * j > 2 * nc || (j + 1) * w + 1 > nc)) --j;
@@ -430,9 +432,6 @@ __device__ __forceinline__ void drain(unsigned long long &bar, uint32_t parity, 
     }
 }
 
-// The (request, head) pairs of this CTA, one after another: the requests by their rows, the heads of one request beside one
-// another, dealt out to the CTAs forth and back, so that each gets a like share of long and short ones.  The rings count
-// the CTA's chunks through all of them.
 // a request's rows, or -1 where its offsets make no sense
 __device__ __forceinline__ int request_rows(const PrefillParams &p, int r)
 {
@@ -440,6 +439,9 @@ __device__ __forceinline__ int request_rows(const PrefillParams &p, int r)
     return o0 < 0 || o1 < o0 || o1 > p.n_rows ? -1 : o1 - o0;
 }
 
+// The (request, head) pairs of this CTA, one after another: the requests by their rows, the heads of one request beside one
+// another, dealt out to the CTAs forth and back, so that each gets a like share of long and short ones.  The rings count
+// the CTA's chunks through all of them.
 __device__ __forceinline__ uint32_t item(uint32_t cycle)
 {
     return cycle * gridDim.x + (cycle & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -455,7 +457,8 @@ struct Part {
 };
 __device__ __forceinline__ int piece_start(const PrefillParams &p, int nc, int j, uint32_t i)
 {
-    // (in eighths of a piece: the first w pieces are shorter by one, since a chunk with its outputs takes that much longer than Q's and P's)
+    // In eighths of a piece: the first w pieces are shorter by one, since a chunk with its outputs takes longer than one of Q's or P's (one
+    // request of 32768 tokens, 32 heads: 1388 us with like pieces, 1332 so, 1390 with two eighths).
     const uint32_t w = p.split.w, n = 8 * (j * w + 1) + 7 * w, like = (uint32_t)nc / n, at = i < w ? 7 * i : 8 * i - w;
     return (int)(at * like + at * (nc - n * like) / n);
 }
@@ -1528,7 +1531,8 @@ int launch_gdn_prefill(const GdnSeqArgs &a, void *stream)
     p.split.failed = static_cast<int32_t *>(a.scratch);
     p.split.states = reinterpret_cast<float *>(static_cast<uint8_t *>(a.scratch) + kSplitHeader);
     if ((e = run(kAhead, 2 * p.split.j + 1)) != cudaSuccess) return (int)e;
-    // (two groups halve P's ways from L2, which bound it where there are many rows; one is the faster where SMs are left)
+    // Two groups halve P's ways from L2, which bound it where there are many rows; one is the faster where SMs are left.  (Four
+    // requests of 4096 tokens, 4 heads: 130.2 us a call with one group, 128.4 with two; one such request: 93.8 and 107.4.)
     auto join = [&](auto kernel, int groups, size_t bytes) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != cudaSuccess) return e;
