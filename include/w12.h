@@ -465,7 +465,7 @@ w12_status w12_gdn_step(const w12_gdn_rows *rows, const float *S0, float *state,
  * x = rms(o silu(z)) weight.  weight[head_dim]: shared by the heads.  z: the gate's rows
  * (BF16 [n_rows][n_heads * head_dim], z_stride elements apart), or NULL: no gate.  BF16
  * pointers 16-byte aligned, strides multiples of 8.  x may be z, with the same
- * stride.  head_dim 128 (else W12_E_UNSUPPORTED).
+ * stride, and is otherwise not to overlap what is read.  head_dim 128 (else W12_E_UNSUPPORTED).
  */
 w12_status w12_gdn_norm(const float *o, int32_t n_rows, int32_t n_heads, int32_t head_dim, const uint16_t *z,
                         int64_t z_stride, const uint16_t *weight, float eps, int32_t gate_first, uint16_t *x,
@@ -493,6 +493,7 @@ typedef struct {
  * Between two blocks: h' = h + scale t, t = y or rms(y) post; x = rms(h') pre,
  * of the FP32 h' before it is rounded for storage.  Pointers 16-byte
  * aligned, strides multiples of 8 (FP32 rows: of 4).  At least one of y and pre.
+ * h_out and x do not overlap one another nor, but as said above, what is read.
  */
 w12_status w12_block_norm(const w12_residual *res, w12_stream_t stream);
 

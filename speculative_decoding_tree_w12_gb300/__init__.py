@@ -161,11 +161,11 @@ def _stream(stream=None):
 # What the calls of a decode loop look up once: the types they accept and the
 # runtime's own query of the current stream (a call of some 0.2 us; building a
 # torch.cuda.Stream object takes fifteen times that).
-_torch = _raw_stream = None
+_torch = _raw_stream = _device = None
 
 
 def _runtime():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _device
     if _torch is None:
         import torch
         current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -174,11 +174,19 @@ def _runtime():
             _raw_stream = lambda: current(device())
         else:
             _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+        _device = device if device is not None else torch.cuda.current_device
         _torch = torch
     return _torch
 
 
 def _st(stream) -> int:
+    return _raw_stream() if stream is None else stream.cuda_stream
+
+
+def _st_on(dev, stream) -> int:
+    """_st of a call whose tensors are on cuda:dev: it has to be the current device, on which the library launches."""
+    if _device() != dev:
+        raise ValueError(f"tensors on cuda:{dev}: it has to be the current device")
     return _raw_stream() if stream is None else stream.cuda_stream
 
 
@@ -808,13 +816,16 @@ def w12_gdn_prefill(rows: GdnRows, row_off, ws: Workspace, S0=None, state=None, 
     states behind the last rows (float32 [n_req][H][128][128] as S[v][k]).  S0: the
     states in front (default: zero); state may be S0 itself."""
     n = row_off.shape[0] - 1
+    if n < 1:
+        raise ValueError("row_off: int32 [n_req + 1] wanted")
     state, out = rows._buffers(n, S0, state, out)
     if ws.dev != rows.dev:
         _refuse(rows.dev, n, None, ws)
+    st = _st_on(rows.dev, stream)
     if rows.scratch is None:
         rows._make_scratch()
     s = _lib.w12_gdn_prefill(rows.ref, n, _ints(row_off, n + 1, "row_off", rows.dev), _dp(S0), state.data_ptr(),
-                             out.data_ptr(), ws.addr, ws.nbytes, _st(stream))
+                             out.data_ptr(), ws.addr, ws.nbytes, st)
     if s:
         raise W12Error(s, "w12_gdn_prefill")
     return out, state
@@ -824,7 +835,7 @@ def w12_gdn_step(rows: GdnRows, S0=None, state=None, out=None, stream=None):
     """One token of every request: row r continues request r's state -> (out,
     state), as for ``w12_gdn_prefill``."""
     state, out = rows._buffers(rows.T, S0, state, out)
-    s = _lib.w12_gdn_step(rows.ref, _dp(S0), state.data_ptr(), out.data_ptr(), _st(stream))
+    s = _lib.w12_gdn_step(rows.ref, _dp(S0), state.data_ptr(), out.data_ptr(), _st_on(rows.dev, stream))
     if s:
         raise W12Error(s, "w12_gdn_step")
     return out, state
@@ -847,7 +858,8 @@ def w12_gdn_norm(o, weight, z=None, eps: float = 1e-6, gate_first: bool = False,
         out = _torch.empty((R, width), dtype=_torch.bfloat16, device=o.device)
     za, zs = (None, 0) if z is None else _rows(z, R, width, "z", dev)
     oa, os_ = _rows(out, R, width, "out", dev)
-    s = _lib.w12_gdn_norm(o.data_ptr(), R, H, 128, za, zs, _vector(weight, 128, "weight", dev), eps, gate_first, oa, os_, _st(stream))
+    s = _lib.w12_gdn_norm(o.data_ptr(), R, H, 128, za, zs, _vector(weight, 128, "weight", dev), eps, gate_first, oa, os_,
+                          _st_on(dev, stream))
     if s:
         raise W12Error(s, "w12_gdn_norm")
     return out
@@ -913,7 +925,7 @@ def w12_block_norm(h, y=None, pre=None, post=None, scale: float = 1.0, eps: floa
         prea = _vector(pre, n, "pre", dev)
     elif out is not None:
         raise ValueError("out: only with pre")
-    s = _lib.w12_block_norm(C.byref(ResidualC(R, f32, n, ha, hs, oa, os_, ya, ys, posta, scale, prea, eps, xa, xs)), _st(stream))
+    s = _lib.w12_block_norm(C.byref(ResidualC(R, f32, n, ha, hs, oa, os_, ya, ys, posta, scale, prea, eps, xa, xs)), _st_on(dev, stream))
     if s:
         raise W12Error(s, "w12_block_norm")
     return h_out, out

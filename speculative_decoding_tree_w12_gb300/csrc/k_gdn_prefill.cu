@@ -401,8 +401,9 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane)
 }
 
 // A thread's bounded waits, in few instructions (there are three dozen of them): `left` is what it may still poll in all its
-// waits together, a poll sleeping up to kWaitSleepNs.  When that has run out no wait lasts any more, so every role runs to
-// its end, and says so there.
+// waits together (the time limit and 16 polls for every chunk), a poll sleeping up to kWaitSleepNs.  When that has run out no wait
+// lasts any more, so every role runs to its end, and says so there.  What it reads on the way may be old or half written: so no
+// address is made of it that is not checked where it is used.
 struct Waits {
     uint32_t left;
 
@@ -490,7 +491,7 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 2;
     const int c = (warp & 3) * 32 + lane;                                 // state row
     const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;                // this warp's lanes
-    Waits waits{p.polls + s.total};
+    Waits waits{p.polls + 16u * s.total};
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
         waits.on(bar, parity);
         tc_fence_after();
@@ -512,9 +513,10 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
         const Chunk &t = s.chunk[g % kChunks];
         const int at = c * kD + 64 * part;                                // this thread's half of the row
         if (t.start != kGoesOn) {
-            if (t.start == kFromState) {
+            const float *from = *(const float *const volatile *)&t.from;   // (null behind a wait that has run out, maybe)
+            if (t.start == kFromState && from) {
 #pragma unroll
-                for (int i = 0; i < 64; i += 8) load8(t.from + at + i, S + i);
+                for (int i = 0; i < 64; i += 8) load8(from + at + i, S + i);
             } else {
 #pragma unroll
                 for (int i = 0; i < 64; ++i) S[i] = 0.f;
@@ -592,7 +594,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
     const int lane = threadIdx.x & 31, warp = (threadIdx.x - kToken0) >> 5, part = warp >> 2;
     const int c = (warp & 3) * 32 + lane, t0 = 32 * part;                 // state row, first token
     const uint32_t tm = (uint32_t)((warp & 3) * 32) << 16;
-    Waits waits{p.polls + s.total};
+    Waits waits{p.polls + 16u * s.total};
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
         waits.on(bar, parity);
         tc_fence_after();
@@ -695,7 +697,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         const size_t step = (size_t)p.H * kD;
         const Chunk &t = s.chunk[g % kChunks];
         float *dst = p.o + ((size_t)(t.row0 + t0) * p.H + t.h) * kD + c;
-        int left = t.out - t0;
+        int left = min(t.out, p.n_rows - t.row0) - t0;
 #pragma unroll 1
         for (int q = t0; q < t0 + 32; q += 16, left -= 16) {
             float x[16];
@@ -770,7 +772,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
     const int tid = threadIdx.x - kGate0, lane = tid & 31, warp = tid >> 5;
     const int i = tid & 63;                       // token of the chunk
     const bool query = warp >= 2;                 // this thread's row: k_i.k or q_i.k
-    Waits waits{p.polls + s.total};
+    Waits waits{p.polls + 16u * s.total};
     const int blocks = (warp & 1) ? 4 : 2;        // of 16 columns that its warp's rows reach into
     const uint32_t tm = (uint32_t)(warp * 32) << 16;
     // warp 3: k.k and q.k of a chunk whose rows have arrived.  Rows behind the request's end are another
@@ -815,7 +817,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         waits.on(s.told[g & 3], (g >> 2) & 1);
         const Chunk &t = s.chunk[g % kChunks];
         const size_t at = (size_t)(t.row0 + i) * p.H + t.h;
-        valid = t.n;
+        valid = min(t.n, p.n_rows - t.row0);      // (less only behind a wait that has run out)
         a = i < valid ? p.alpha[at] : 1.f;
         b = i < valid ? p.beta[at] : 0.f;
     };
@@ -939,7 +941,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
 __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillShared &s)
 {
     const int tid = threadIdx.x - kInv0, lane = tid & 31, warp = tid >> 5;
-    Waits waits{p.polls + s.total};
+    Waits waits{p.polls + 16u * s.total};
 #pragma unroll 1
     for (int g = 0; g < s.total; ++g) {
         const int st = g & 1;
@@ -1005,7 +1007,7 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
 // buffer, where straight-line code waits longer for its next line than for the tensor cores.
 __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShared &s)
 {
-    Waits waits{p.polls + s.total};
+    Waits waits{p.polls + 16u * s.total};
     const int total = s.total;
     const bool silent = s.silent;
     bool ok = true;
@@ -1088,7 +1090,7 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
 __device__ __forceinline__ void piece_warps(const PrefillParams &p, PrefillShared &s)
 {
     const int tid = threadIdx.x - kIssue0 - 64, lane = tid & 31;
-    Waits waits{p.polls + s.total};
+    Waits waits{p.polls + 16u * s.total};
 #pragma unroll 1
     for (int g = 0; g < s.total; ++g) {
         const int st = g & 1, k4 = g & 3;
@@ -1133,7 +1135,7 @@ __device__ __forceinline__ void piece_warps(const PrefillParams &p, PrefillShare
 __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShared &s, const CUtensorMap &qmap, const CUtensorMap &kmap,
                                             const CUtensorMap &vmap)
 {
-    Waits waits{p.polls + s.total};
+    Waits waits{p.polls + 16u * s.total};
     const bool withheld = (p.debug_flags & 1) && blockIdx.x == 0 && p.split.mode != kPieces;
     int g = 0, kq_issued = 0, v_issued = 0;
     bool go = true;
@@ -1241,6 +1243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&vmap);
     }
     if (warp == 0) tmem_alloc(smem_u32(&s.tmem), 512);
+    if (tid >= 32 && tid < 32 + kChunks) s.chunk[tid - 32] = Chunk{};   // (what is read of it where a wait has run out)
     // what no chunk writes and every chunk reads: M and A above the diagonal blocks of 32
     for (int e = tid; e < 32 * 4; e += kThreads) {
         const int row = e >> 2, at = row * 128 + (((4 + (e & 3)) ^ (row & 7)) << 4);
@@ -1431,7 +1434,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps * kGroups, 1) k_gdn_join(const
             drain(s.full[0], ((last >> 1) + 1) & 1, p);
             drain(s.full[1], (((last + 1) >> 1) + 1) & 1, p);
         }
-        __syncwarp();
     }
 }
 

@@ -885,6 +885,7 @@ w12_status w12_gdn_norm(const float *o, int32_t n_rows, int32_t n_heads, int32_t
     const int64_t width = (int64_t)n_heads * head_dim;
     if (!o || !aligned(o, 16) || !weight || !aligned(weight, 16) || !rows_ok(x, x_stride, width)) return W12_E_INVAL;
     if (z && (!rows_ok(z, z_stride, width) || (z == x && z_stride != x_stride))) return W12_E_INVAL;
+    if (static_cast<const void *>(x) == o) return W12_E_INVAL;
     GdnNormArgs a{};
     a.o = o;
     a.z = z;
@@ -911,6 +912,7 @@ w12_status w12_block_norm(const w12_residual *r, w12_stream_t stream)
         if (!rows_ok(r->y, r->y_stride, r->n)) return W12_E_INVAL;
         if (!r->h_out || !aligned(r->h_out, 16) || r->h_out_stride < r->n || r->h_out_stride % unit) return W12_E_INVAL;
         if (r->h_out == r->h && r->h_out_stride != r->h_stride) return W12_E_INVAL;
+        if (r->h_out == r->y) return W12_E_INVAL;
     }
     if (r->post && !aligned(r->post, 16)) return W12_E_INVAL;
     if (r->pre) {

@@ -121,7 +121,7 @@ def test_gdn_norm_refused(w12):
                      (dict(R=1 << 30, H=4, zs=512, xs=512), UNSUPPORTED), (dict(z=A + 8), INVAL), (dict(zs=248), INVAL), (dict(zs=260), INVAL),
                      (dict(w=None), INVAL), (dict(w=A + 4), INVAL), (dict(eps=0.0), INVAL), (dict(eps=float("nan")), INVAL),
                      (dict(eps=float("inf")), INVAL), (dict(x=None), INVAL), (dict(x=A + 8), INVAL), (dict(xs=128), INVAL),
-                     (dict(x=A, zs=264), INVAL)):
+                     (dict(x=A, zs=264), INVAL), (dict(o=A + 4096), INVAL)):
         assert call(**kw) == want, kw
     assert call(R=0, o=None, x=None) == 0
 
@@ -138,7 +138,7 @@ def test_block_norm_refused(w12):
                      (dict(h_out=None), INVAL), (dict(h_out=A + 2), INVAL), (dict(h_out_stride=0), INVAL), (dict(h_out=A, h_out_stride=264), INVAL),
                      (dict(y=A + 2), INVAL), (dict(y_stride=128), INVAL), (dict(post=A + 2), INVAL), (dict(pre=A + 2), INVAL), (dict(x=None), INVAL),
                      (dict(x=A + 2), INVAL), (dict(x_stride=250), INVAL), (dict(x=3 * A, x_stride=264), INVAL), (dict(x=A), INVAL),
-                     (dict(x=2 * A), INVAL), (dict(eps=0.0), INVAL), (dict(scale=float("nan")), INVAL), (dict(scale=float("inf")), INVAL),
+                     (dict(x=2 * A), INVAL), (dict(y=2 * A), INVAL), (dict(eps=0.0), INVAL), (dict(scale=float("nan")), INVAL), (dict(scale=float("inf")), INVAL),
                      (dict(y=None, pre=None, post=None), INVAL), (dict(y=None), INVAL)):
         assert call(**kw) == want, kw
     assert call(n_rows=0) == 0
@@ -156,8 +156,9 @@ def test_binding_turns_host_and_misshapen_tensors_away(w12):
         with pytest.raises(ValueError):
             w12.GdnRows(*good[:i], t, *good[i + 1:])
     off = torch.zeros(2, dtype=torch.int32)
-    with pytest.raises(ValueError):
-        w12.w12_gdn_prefill(layer, off, None)
+    for offsets in (off, off[:1], off[:0]):
+        with pytest.raises(ValueError):
+            w12.w12_gdn_prefill(layer, offsets, None)
     with pytest.raises(ValueError):
         w12.w12_gdn_step(layer)
     with pytest.raises(ValueError):

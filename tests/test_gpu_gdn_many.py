@@ -92,6 +92,23 @@ def test_two_calls_at_once(w12):
             assert torch.equal(outs[k][i], want[k][0]) and torch.equal(states[k][i], want[k][1])
 
 
+def test_on_another_device_than_the_current_one(w12, monkeypatch):
+    """The library launches on the current device: with tensors elsewhere the calls are refused (the current device here
+    is made another one by its name only)."""
+    c = Case(w12, [10], 2, 2, seed=6)
+    o, w = torch.zeros(10, 2, D, device="cuda"), torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    h = torch.zeros(10, 64, dtype=torch.bfloat16, device="cuda")
+    calls = [lambda: w12.w12_gdn_prefill(c.rows, c.row_off, c.ws), lambda: w12.w12_gdn_step(c.rows), lambda: w12.w12_gdn_norm(o, w),
+             lambda: w12.w12_block_norm(h, h)]
+    for call in calls:
+        call()
+    monkeypatch.setattr(w12, "_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("post,f32", [(False, False), (True, True)])
 def test_a_layer_of_prompts_and_tokens(w12, post, f32):
     """norm - linear - recurrent layer - norm with gate - linear - residual and norm, over a prompt and over two tokens behind it,
