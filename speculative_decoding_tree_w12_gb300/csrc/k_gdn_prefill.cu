@@ -611,28 +611,35 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
     for (int g = 0; g < total; ++g) {
         const int st = g & 1, k4 = g & 3;
         const uint32_t par = g & 1, par2 = (g >> 1) & 1;
-        // X = b (v - G S k)
+        // X = b (v - G S k); b v while S k is being made
         wait(s.vfull[st], par2);
         wait(s.gready[st], par2);
-        wait(s.done_k, par);
         float x[32], top = 0.f;
 #pragma unroll
         for (int q = 0; q < 32; q += 8) {
-            float d[8], f[8], e[8];
+            float e[8];
             const uint16_t *v = s.V[st] + (t0 + q) * kD + c;
-            tmem_ld8(tm + kColDK + t0 + q, d);
             read_n(s.b[k4] + t0 + q, e);
-            read_n(s.bG[k4] + t0 + q, f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] *= __uint_as_float((uint32_t)v[j * kD] << 16);
-            tmem_ld_wait();
-            fma_n(f, d, e);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[q + j] = e[j];
-            top = fmaxf(top, top_of(e));
+            for (int j = 0; j < 8; ++j) x[q + j] = e[j] * __uint_as_float((uint32_t)v[j * kD] << 16);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.vempty[st]));
+        wait(s.done_k, par);
+#pragma unroll
+        for (int q = 0; q < 32; q += 16) {
+            float d[16], f[16];
+            tmem_ld<16>(tm + kColDK + t0 + q, d);
+            read_n(s.bG[k4] + t0 + q, f);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                const float2 r = __ffma2_rn(make_float2(f[j], f[j + 1]), make_float2(d[j], d[j + 1]), make_float2(x[q + j], x[q + j + 1]));
+                x[q + j] = r.x;
+                x[q + j + 1] = r.y;
+                top = fmaxf(top, fmaxf(fabsf(r.x), fabsf(r.y)));
+            }
+        }
         const Unit ux = unit_of(row_top(s.top[0], top));
         if (part == 0) s.x_back[c] = ux.back;
         scale_n(x, ux.scale);
@@ -651,34 +658,35 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         // (F16 has 16 bits to spare under the largest value), and one under which S q keeps finite.
         wait(s.done_q, par);
         top = 0.f;
-#pragma unroll 1
-        for (int q = t0; q < t0 + 32; q += 16) {
-            float x[16], f[16];
-            tmem_ld<16>(tm + kColDQ + q, x);
-            read_n(s.G[k4] + q, f);
+#pragma unroll
+        for (int q = 0; q < 32; q += 16) {
+            float z[16], f[16];
+            tmem_ld<16>(tm + kColDQ + t0 + q, z);
+            read_n(s.G[k4] + t0 + q, f);
             tmem_ld_wait();
-            mul_n(x, f);
-            top = fmaxf(top, top_of(x));
-            tmem_put(tm + kColDQ + q, x);
+            mul_n(z, f);
+            top = fmaxf(top, top_of(z));
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[q + j] = z[j];
         }
         const float a_back = s.a_back[k4];
         const float a_scale = __uint_as_float(0x7F000000u - __float_as_uint(a_back));   // 1 / a_back
         top = row_top(s.top[1], top) * 0x1p-60f * a_scale;
         wait(s.mready[st], par2);
         const Unit uu = unit_of(fmaxf(top, ux.back * 0x1p20f * __uint_as_float(s.m_top[k4])));
-        tmem_st_wait();
-#pragma unroll 1
-        for (int q = t0; q < t0 + 32; q += 16) {
-            float x[16];
-            tmem_ld<16>(tm + kColDQ + q, x);
-            tmem_ld_wait();
-            scale_n(x, uu.scale);
-            scale_n(x, a_scale);
-            tmem_put(tm + kColDQ + q, x);
+        scale_n(x, uu.scale);
+        scale_n(x, a_scale);
+#pragma unroll
+        for (int q = 0; q < 32; q += 16) {
+            float z[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z[j] = x[q + j];
+            tmem_put(tm + kColDQ + t0 + q, z);
         }
 
         // U's pieces for A, over S's last (S q is there)
         wait(s.done_u, par);
+        wait(s.have_us[0], par);                  // (the state warps' way goes first: 735 -> 728 us for sixteen prompts of 4096 tokens)
 #pragma unroll 1
         for (int q = t0; q < t0 + 32; q += 16) {
             float x[16], f[16];
