@@ -27,11 +27,11 @@
 //    blocks of 16, whose columns are solved in registers, and A,
 //  * inverse warps (20..23): M, the blocks below those from them,
 //  * warp 24 issues the products with the state, warp 25 the copies by TMA, warps 26 and 27 make M's pieces.
-// A chunk takes 4.4 to 4.7 us (8,400 to 9,000 cycles) however many there are: sixteen prompts of up to 8192 tokens x 32 heads
-// 1481 us, 2.7 times what their bytes take at the measured copy bandwidth.  That is the way through the steps above, whose longest
-// are the cutting into pieces (S 1,800 cycles, X and U 1,500 each: three BF16 pieces take 11 cycles of a scheduler for two
-// values of 32 lanes, two F16 pieces 5), M X 600, U K 800 and some 200 for each hand-over between warps; the schedulers issue in 58 %
-// of the cycles, the tensor cores work in 32 %.  With fewer warps of more columns each it took 1.2 times as long.
+// A chunk takes 4.2 to 4.4 us (8,000 to 8,500 cycles) however many there are: sixteen prompts of up to 8192 tokens x 32 heads
+// 1417 us, 2.5 times what their bytes take at the measured copy bandwidth.  That is the way through the steps above, on a full
+// machine: S's pieces 2,200 cycles (three BF16 pieces take 11 cycles of a scheduler for two values of 32 lanes, two F16 pieces 5),
+// what of S k is left then 950, X 1,150, M X 800, U's pieces 1,450, U K 700, S' 700; each with some 200 for its hand-over between
+// warps.  The schedulers issue in 58 % of the cycles, the tensor cores work in 32 %.  With fewer warps of more columns each it took 1.2 times as long.
 // The products are issued in rolled loops and the code is kept short: straight-line code of a few times this length spent half
 // its time on its own way in.  A new pair costs 3 us more than its chunks, 5 where a state is read.
 // Every wait is bounded; when one has run out the state is left unwritten.
@@ -136,9 +136,9 @@ constexpr uint32_t kKqBytes = sizeof(PrefillShared::KQ) / kStages, kVBytes = siz
 //  * k_gdn_join: the states in front of every piece but the first w from those,
 //  * kPieces: those pieces, now with their outputs.
 // That takes w + 1 pieces' time of n, and (2 j + 1) and (j w + 1) CTAs a pair (one of 4096 tokens, 4 heads: 299 us in one
-// part a head, 87 cut; of 32768 tokens, 32 heads: 2346 and 1322).  The launches overlap: each begins where SMs are left, and waits for the
+// part a head, 87 cut; of 32768 tokens, 32 heads: 2250 and 1281).  The launches overlap: each begins where SMs are left, and waits for the
 // one before it only for what that wrote (3 to 6 us of those).  All three as one launch whose CTAs wait for one another's
-// counts were slower (4096 tokens, 4 heads: 130 us), the join being short of registers and of shared memory there.
+// counts were slower (4096 tokens, 4 heads: 120 to 130 us), the join being short of registers and of shared memory there.
 enum Mode : int32_t { kWhole, kAhead, kPieces };
 
 struct SplitParams {
@@ -311,14 +311,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&x)[N])
             : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&x)[8])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
-                 : "r"(taddr)
-                 : "memory");
-}
-
 __device__ __forceinline__ void tmem_put(uint32_t taddr, const float (&x)[16])
 {
 #pragma unroll
@@ -360,7 +352,7 @@ __device__ __forceinline__ void store8(float *dst, const float *x)
                  : "memory");
 }
 
-// x *= y; x *= f; z += x y, two at a time
+// x *= y; x *= f, two at a time
 template <int N>
 __device__ __forceinline__ void mul_n(float (&x)[N], const float (&y)[N])
 {
@@ -381,17 +373,6 @@ __device__ __forceinline__ void scale_n(float (&x)[N], float f)
         x[i + 1] = r.y;
     }
 }
-template <int N>
-__device__ __forceinline__ void fma_n(const float (&x)[N], const float (&y)[N], float (&z)[N])
-{
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float2 r = __ffma2_rn(make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]), make_float2(z[i], z[i + 1]));
-        z[i] = r.x;
-        z[i + 1] = r.y;
-    }
-}
-
 // this warp's tensor-memory accesses are done: one arrival for the warp
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane)
 {
@@ -605,7 +586,6 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         named_bar(kBarRow + (warp & 3), 64);
         return fmaxf(top, at[part ^ 1][c]);
     };
-    // (Every loop over the tokens is rolled, 16 at a time: what lies between two of them lies in tensor memory.)
     const int total = s.total;
 #pragma unroll 1
     for (int g = 0; g < total; ++g) {
@@ -686,7 +666,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
 
         // U's pieces for A, over S's last (S q is there)
         wait(s.done_u, par);
-        wait(s.have_us[0], par);                  // (the state warps' way goes first: 735 -> 728 us for sixteen prompts of 4096 tokens)
+        wait(s.have_us[0], par);                  // (the state warps' way goes first: sixteen prompts of 4096 tokens 736 us without, 728 with)
 #pragma unroll 1
         for (int q = t0; q < t0 + 32; q += 16) {
             float x[16], f[16];
@@ -1365,7 +1345,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps * kGroups, 1) k_gdn_join(const
 {
     pdl_wait();                                   // first of all: the launch behind this one counts on it
     pdl_launch_dependents();
-    extern __shared__ __align__(128) uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     JoinShared<kGroups> &s = *reinterpret_cast<JoinShared<kGroups> *>(smem_raw);
     constexpr int kOwn = kD / kJoinWarps;         // features of a warp
     const int tid = threadIdx.x & 255, lane = tid & 31, warp = tid >> 5, group = threadIdx.x >> 8;
