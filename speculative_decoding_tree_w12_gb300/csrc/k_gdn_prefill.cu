@@ -135,8 +135,8 @@ constexpr uint32_t kKqBytes = sizeof(PrefillShared::KQ) / kStages, kVBytes = siz
 //  * kAhead: the first w pieces as they are, and Q and P of the j segments of w pieces behind them, noted after every piece,
 //  * k_gdn_join: the states in front of every piece but the first w from those,
 //  * kPieces: those pieces, now with their outputs.
-// That takes w + 1 pieces' time of n, and (2 j + 1) and (j w + 1) CTAs a pair (one of 4096 tokens, 4 heads: 299 us in one
-// part a head, 87 cut; of 32768 tokens, 32 heads: 2250 and 1281).  The launches overlap: each begins where SMs are left, and waits for the
+// That takes w + 1 pieces' time of n, and (2 j + 1) and (j w + 1) CTAs a pair (one of 4096 tokens, 4 heads: 286 us in one
+// part a head, 85 cut; of 32768 tokens, 32 heads: 2281 and 1280).  The launches overlap: each begins where SMs are left, and waits for the
 // one before it only for what that wrote (3 to 6 us of those).  All three as one launch whose CTAs wait for one another's
 // counts were slower (4096 tokens, 4 heads: 120 to 130 us), the join being short of registers and of shared memory there.
 enum Mode : int32_t { kWhole, kAhead, kPieces };
@@ -149,13 +149,13 @@ struct SplitParams {
 };
 
 // Segments of a request of nc chunks.  The join takes a product of 1.1 us for each piece of them, so no more than pay for
-// theirs; and it and one more launch some 35 us, eight chunks' time (4.6 us each), which the j w pieces that run beside the others
-// have to save.  (One request of 32 heads, j = 1: 16 chunks 87 us whole, 94 cut, 24 chunks 124 and 112; of 16 heads, j = 4: 10 chunks
-// 60 and 62, 12 chunks 69 and 67.)
+// theirs; and it and one more launch some 30 us, seven chunks' time, which the j w pieces that run beside the others have to
+// save.  (One request of 32 heads, j = 1: 14 chunks 74 us whole, 79 cut, 16 chunks 83 and 83, 20 chunks 99 and 95; of 16 heads: 8 chunks
+// 48 and 52, 10 chunks 56 and 56, 12 chunks 65 and 64.)
 __host__ __device__ inline int split_segments(int nc, int j, int w)
 {
     while (j > 0 && (j * j > 2 * nc || (j + 1) * w + 1 > nc)) --j;
-    return (int64_t)nc * j * w < 8 * ((j + 1) * w + 1) ? 0 : j;
+    return (int64_t)nc * j * w < 7 * ((j + 1) * w + 1) ? 0 : j;
 }
 
 struct PrefillParams {
