@@ -15,6 +15,7 @@
 // is the launch and one way to memory and back.
 #include <cuda_runtime.h>
 
+#include "w12_device.cuh"
 #include "w12_internal.h"
 
 namespace {
@@ -55,6 +56,8 @@ __device__ __forceinline__ float sum8(float x)
 
 __global__ void __launch_bounds__(kStepThreads) k_gdn_step(const GdnStepParams p)
 {
+    w12d::pdl_wait();
+    w12d::pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c0 = (lane & 7) * 4, h = blockIdx.y;
     const size_t r = blockIdx.x;
@@ -127,6 +130,11 @@ int launch_gdn_step(const GdnSeqArgs &a, void *stream)
     cfg.gridDim = dim3(a.n_req, a.H, kD / kStepRows);
     cfg.blockDim = dim3(kStepThreads);
     cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute behind{};                 // begins while the launch before it ends, and waits for that first of all
+    behind.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    behind.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &behind;
+    cfg.numAttrs = 1;
     return (int)cudaLaunchKernelEx(&cfg, k_gdn_step, p);
 }
 

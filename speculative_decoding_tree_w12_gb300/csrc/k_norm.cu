@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "w12_device.cuh"
 #include "w12_internal.h"
 
 namespace {
@@ -71,6 +72,8 @@ struct GdnNormParams {
 template <bool kGate, bool kFirst>
 __global__ void __launch_bounds__(kNormThreads) k_gdn_norm(const GdnNormParams p)
 {
+    w12d::pdl_wait();
+    w12d::pdl_launch_dependents();
     const uint32_t item = blockIdx.x * (uint32_t)(kNormThreads / 16) + (threadIdx.x >> 4);
     const int c = (threadIdx.x & 15) * 8;
     const bool live = item < p.items;      // (the other half of the warp takes part in the shuffles)
@@ -146,6 +149,8 @@ __device__ __forceinline__ float row_sum(float v, float *part, int warps)
 template <bool kF32, int kV>
 __global__ void __launch_bounds__(1024) k_block_norm(const BlockNormParams p)
 {
+    w12d::pdl_wait();
+    w12d::pdl_launch_dependents();
     __shared__ float part[2][32];
     const size_t row = blockIdx.x;
     const int warps = blockDim.x >> 5;
@@ -231,6 +236,11 @@ int launch(void (*kern)(P), uint32_t grid, int threads, const P &p, void *stream
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute behind{};                 // begins while the launch before it ends, and waits for that first of all
+    behind.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    behind.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &behind;
+    cfg.numAttrs = 1;
     return (int)cudaLaunchKernelEx(&cfg, kern, p);
 }
 
