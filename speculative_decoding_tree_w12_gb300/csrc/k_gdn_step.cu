@@ -11,8 +11,8 @@
 // of which is asked for before the first is used.  Four CTAs of 32 rows to a
 // head: one request of 32 heads puts 128 CTAs on the machine.
 //
-// 256 requests of 32 heads (1.08 GB): 163 us by itself, 6.6 TB/s; 24 requests 14.7 us, 6.9 TB/s; one request 4.1 us, which
-// is the launch and one way to memory and back.
+// 256 requests of 32 heads (1.08 GB), call after call: 172.6 us, 6.3 TB/s; 24 requests 17.1 us, 5.9 TB/s (18.8 if a launch waits for
+// the one before it to end before it begins); one request 4.1 us by itself, which is the launch and one way to memory and back.
 #include <cuda_runtime.h>
 
 #include "w12_device.cuh"

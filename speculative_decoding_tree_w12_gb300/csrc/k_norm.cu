@@ -12,8 +12,9 @@
 // written once, sums in FP32 in registers.  x is taken from the FP32 h', not
 // from the value that is stored: one rounding less in every layer.
 //
-// 16384 rows of 32 heads with their gate (537 MB): 76 us, 7.0 TB/s.  Between two blocks of 5120 values, 16384 rows: 99.8 us BF16
-// (6.7 TB/s), 149.7 us FP32 with a norm behind the block (6.7); 192 rows take 4 us, the launch and one way to memory and back.
+// 16384 rows of 32 heads with their gate (537 MB): 74.6 us, 7.2 TB/s.  Between two blocks of 5120 values, 16384 rows: 98.9 us BF16
+// (6.8 TB/s), 148.4 us FP32 with a norm behind the block (6.8); 192 rows 2.4 and 3.8 us, call after call.  (76.7, 99.8, 149.6, 2.75
+// and 4.2 if a launch waits for the one before it to end before it begins.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -282,8 +283,9 @@ int launch_block_norm(const BlockNormArgs &a, void *stream)
     p.scale = a.scale;
     p.eps = a.eps;
     p.inv_n = 1.f / (float)a.n;
-    // As many threads as leave one piece to each, two beyond 1024 threads.  (16384 BF16 rows of 5120 values: one piece 99.8 us,
-    // two 115.0; of 2560: 49.1 and 54.9; 192 rows of 8192: 3.5 and 3.3.  Rows of 16384, which only go with two: 393 us, 5.5 TB/s.)
+    // As many threads as leave one piece to each, two beyond 1024 threads.  (16384 BF16 rows of 5120 values, without overlap: one
+    // piece 99.8 us, two 115.0; of 2560: 49.1 and 54.9; 192 rows of 8192: 3.5 and 3.3.  Rows of 16384, which only go with two: 391 us,
+    // 5.5 TB/s.)
     const int v = p.pieces <= 1024 ? 1 : 2;
     const int threads = ((p.pieces + v - 1) / v + 31) / 32 * 32;
     const auto k16 = v == 1 ? k_block_norm<false, 1> : k_block_norm<false, 2>;
