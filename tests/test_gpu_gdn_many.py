@@ -195,3 +195,72 @@ def test_a_layer_of_prompts_and_tokens(w12, post, f32):
     assert prompt.ws.status() == 0 and token.ws.status() == 0
     prompt.check(S0, counts, last[0])
     token.check(last[1], [1, 1, 1], last[2])                 # (its buffers hold the second token's)
+
+
+@pytest.mark.parametrize("long", [False, True])
+def test_replayed_with_other_offsets(w12, long):
+    """A graph's call reads its offsets when it is replayed: where requests are cut follows them."""
+    T, H = (2600, 2) if long else (300, 3)
+    c = Case(w12, [T // 2, T - T // 2], H, 1, seed=7)
+    S0, off = c.S0.cuda(), c.row_off.clone()
+    out, state = torch.empty(T, H, D, device="cuda"), torch.empty_like(S0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w12.w12_gdn_prefill(c.rows, off, c.ws, S0=S0, state=state, out=out)
+    for cut in (T // 2, 1, T, 0, 65, T - 700 if long else 64):
+        off.copy_(torch.tensor([0, cut, T], dtype=torch.int32))
+        out.fill_(7.0)
+        graph.replay()
+        want, ws_ = w12.w12_gdn_prefill(c.rows, off, c.ws, S0=S0)
+        torch.cuda.synchronize()
+        assert c.ws.status() == 0 and torch.equal(out, want) and torch.equal(state, ws_)
+        c.counts, c.off = [cut, T - cut], np.asarray([0, cut, T], np.int32)
+        if not long or cut in (1, T - 700):
+            c.check(out, state)
+
+
+def test_calls_overlap_only_where_nothing_depends(w12):
+    """Kernels begin while the ones before them end.  Forty tokens through a layer whose rows are small and whose calls
+    feed one another, in one go, give what they give with a pause behind every call."""
+    n, H, R = 256, 4, 5
+    g = torch.Generator().manual_seed(8)
+    bits = lambda t: t.contiguous().view(torch.int16).numpy().view(np.uint16)
+    weight = lambda a, b: w12.DeviceWeight(w12.w12_pack(bits((torch.randn(a, b, generator=g) / b ** 0.5).bfloat16())))
+    wi, wo = weight(3 * H * D, n), weight(n, H * D)
+    one = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    head = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    h0 = torch.randn(R, n, generator=g).cuda()
+    S0 = (torch.randn(R, H, D, D, generator=g) * 0.05).cuda()
+    alpha, beta = (torch.rand(R, H, generator=g).cuda() for _ in range(2))
+    ws = w12.Workspace(R, 3 * H * D, 0, R)
+    off = torch.arange(R + 1, dtype=torch.int32, device="cuda")
+    new = lambda *s, t=torch.bfloat16: torch.empty(s, dtype=t, device="cuda")
+
+    def run(pause):
+        h, state, x, r, a, y = h0.clone(), S0.clone(), new(R, n), new(R, 3 * H * D), new(R, H * D), new(R, n)
+        o = new(R, H, D, t=torch.float32)
+        rows = w12.GdnRows(r[:, :H * D], r[:, H * D:2 * H * D], r[:, 2 * H * D:], alpha, beta)
+        w12.w12_block_norm(h, pre=one, out=x)
+        for i in range(40):
+            calls = [lambda: w12.w12_gemm(wi, x, ws, y=r),
+                     # unit keys and queries
+                     lambda: w12.w12_gdn_norm(r[:, :2 * H * D].float().view(R, 2 * H, D), head, out=r[:, :2 * H * D]),
+                     lambda: r[:, :2 * H * D].mul_(D ** -0.5),
+                     (lambda: w12.w12_gdn_step(rows, S0=state, state=state, out=o)) if i % 3 else
+                     (lambda: w12.w12_gdn_prefill(rows, off, ws, S0=state, state=state, out=o)),
+                     lambda: w12.w12_gdn_norm(o, head, out=a),
+                     lambda: w12.w12_gemm(wo, a, ws, y=y),
+                     lambda: w12.w12_block_norm(h, y, pre=one, scale=0.5, h_out=h, out=x)]
+            for call in calls:
+                call()
+                if pause:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert ws.status() == 0
+        return h, state, x
+
+    want = run(True)
+    assert all(torch.isfinite(t.float()).all() for t in want)
+    for _ in range(3):
+        for got, ref in zip(run(False), want):
+            assert torch.equal(got, ref)
