@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import List, Optional, Sequence
 
 import numpy as np
@@ -879,6 +880,9 @@ class ResidualC(C.Structure):
                 ("x_stride", C.c_int64)]
 
 
+_residual = struct.Struct("@iiqPqPqPqPfPfPq").pack      # ResidualC's bytes (a third of the time that filling one takes)
+
+
 def _stream_rows(t, rows, width, f32, what, dev):
     """_rows of a residual stream, bfloat16 or float32."""
     if not f32:
@@ -925,7 +929,7 @@ def w12_block_norm(h, y=None, pre=None, post=None, scale: float = 1.0, eps: floa
         prea = _vector(pre, n, "pre", dev)
     elif out is not None:
         raise ValueError("out: only with pre")
-    s = _lib.w12_block_norm(C.byref(ResidualC(R, f32, n, ha, hs, oa, os_, ya, ys, posta, scale, prea, eps, xa, xs)), _st_on(dev, stream))
+    s = _lib.w12_block_norm(_residual(R, f32, n, ha, hs, oa, os_, ya, ys, posta, scale, prea, eps, xa, xs), _st_on(dev, stream))
     if s:
         raise W12Error(s, "w12_block_norm")
     return h_out, out

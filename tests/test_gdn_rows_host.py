@@ -145,6 +145,16 @@ def test_block_norm_refused(w12):
     assert w12.lib().w12_block_norm(None, None) == INVAL
 
 
+def test_residual_bytes(w12):
+    """The binding's packed arguments are the C structure's bytes."""
+    values = (3, 1, 256, A, 264, 2 * A, 272, 3 * A, 280, 4 * A, 0.5, 5 * A, 1e-6, 6 * A, 288)
+    packed = w12._residual(*values)
+    assert len(packed) == C.sizeof(w12.ResidualC)
+    r = w12.ResidualC.from_buffer_copy(packed)
+    for (name, _), v in zip(w12.ResidualC._fields_, values):
+        assert getattr(r, name) == (pytest.approx(v) if isinstance(v, float) else v), name
+
+
 def test_binding_turns_host_and_misshapen_tensors_away(w12):
     torch = pytest.importorskip("torch")
     b = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
