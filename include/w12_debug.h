@@ -72,6 +72,13 @@ int32_t w12_debug_num_sms(void);
 int32_t w12_debug_attn_registers(int32_t cols, int32_t *wanted);
 
 /*
+ * w12_gdn_prefill's inverse, looked at on the host: the words of shared memory
+ * that two of its warps touch, at least one of them writing, with no barrier
+ * in between (from the index formulas and barriers that the kernel runs by).
+ */
+int32_t w12_debug_gdn_inverse_conflicts(void);
+
+/*
  * Per-GEMM timing inside the verify step's GEMM chain (one persistent launch
  * for all linears and the LM head, split into w12_debug_chain_parts(n) launches
  * for n GEMMs).  While dev_words (device, n_words 64-bit words) is set, every

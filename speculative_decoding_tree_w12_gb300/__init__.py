@@ -130,6 +130,7 @@ def lib():
             "w12_debug_set": ([i32, C.c_uint64], None),
             "w12_debug_num_sms": ([], i32),
             "w12_debug_attn_registers": ([i32, p], i32),
+            "w12_debug_gdn_inverse_conflicts": ([], i32),
             "w12_debug_profile": ([i32], None),
             "w12_debug_last_cuda_error": ([p, i32], i32),
             "w12_debug_profile_read": ([p, i32], i32),

@@ -41,6 +41,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstddef>
+#include <vector>
 
 #include "w12_device.cuh"
 
@@ -926,6 +927,28 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
 // inverse warps
 // ---------------------------------------------------------------------------
 
+// M by blocks of 32 (two of them, half the warps each: steps 0 and 1) and 64 (steps 2, 3 and 4, 5): M21 = -M22 (L21 M11).
+// Every step makes four columns of a row of Z = X Y to a thread, from the l in [l0, l1) that a triangle leaves; a warp
+// takes a short and a long strip of M11's columns, then of M22's rows.  X, Y, Z: places from s.L on.
+constexpr int kInvSteps = 6, kInvWarps = 4;
+struct InverseStep {
+    int X, Y, Z, l0, l1;
+};
+__host__ __device__ __forceinline__ InverseStep inverse_step(int step, int L, int warp, int lane)
+{
+    const int B = L + (warp >> 1 ? kL22 : kL11), T = 2 * kLFloats, T16 = T + (warp >> 1) * 16 * kLS;
+    const int strip = 4 * (step & 1 ? 7 - warp : warp);
+    if (step < 2) {
+        const int in_half = (warp & 1) * 32 + lane, row = in_half >> 2, col = 4 * (in_half & 3), below = B + (16 + row) * kLS;
+        return {below + (step ? 16 : 0), (step ? T16 : B) + col, (step ? below : T16 + row * kLS) + col, 0, 16};
+    }
+    if (step < 4) return {L + kL21 + lane * kLS, L + kL11 + strip, T + lane * kLS + strip, strip, 32};
+    const int row = strip + (lane >> 3), col = 4 * (lane & 7);
+    return {L + kL22 + row * kLS, T + col, L + kL21 + row * kLS + col, 0, strip + 4};
+}
+// whether the warps meet behind a step (the last: the next chunk's first products go where the slowest warp still reads these)
+__host__ __device__ __forceinline__ bool inverse_joins(int step) { return step < 2 || step == 3 || step == kInvSteps - 1; }
+
 __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillShared &s)
 {
     const int tid = threadIdx.x - kInv0, lane = tid & 31, warp = tid >> 5;
@@ -934,41 +957,18 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
     for (int g = 0; g < s.total; ++g) {
         const int st = g & 1;
         waits.on(s.lready[st], (g >> 1) & 1);
-        // M by blocks of 32 (two of them, half the warps each: steps 0 and 1) and 64 (steps 2, 3 and 4, 5): M21 = -M22 (L21 M11).
-        // Every step makes four columns of a row of Z = X Y to a thread, from the l in [l0, l1) that a triangle leaves; a warp
-        // takes a short and a long strip of M11's columns, then of M22's rows.  X, Y, Z: places from s.L on.
         float *F = &s.L[0][0];
-        const int L = st * kLFloats, B = L + (warp >> 1 ? kL22 : kL11), T = 2 * kLFloats, T16 = T + (warp >> 1) * 16 * kLS;
 #pragma unroll 1
-        for (int step = 0; step < 6; ++step) {
-            const int strip = 4 * (step & 1 ? 7 - warp : warp);
-            int X, Y, Z, l0 = 0, l1 = 32;
-            if (step < 2) {
-                const int row = (tid & 63) >> 2, col = 4 * (tid & 3), below = B + (16 + row) * kLS;
-                X = below + (step ? 16 : 0);
-                Y = (step ? T16 : B) + col;
-                Z = (step ? below : T16 + row * kLS) + col;
-                l1 = 16;
-            } else if (step < 4) {
-                X = L + kL21 + lane * kLS;
-                Y = L + kL11 + strip;
-                Z = T + lane * kLS + strip;
-                l0 = strip;
-            } else {
-                const int row = strip + (lane >> 3), col = 4 * (lane & 7);
-                X = L + kL22 + row * kLS;
-                Y = T + col;
-                Z = L + kL21 + row * kLS + col;
-                l1 = strip + 4;
-            }
+        for (int step = 0; step < kInvSteps; ++step) {
+            const InverseStep at = inverse_step(step, st * kLFloats, warp, lane);
             float acc[4] = {};
 #pragma unroll 2
-            for (int l = l0; l < l1; l += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(F + X + l);
+            for (int l = at.l0; l < at.l1; l += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(F + at.X + l);
                 const float xe[4] = {x.x, x.y, x.z, x.w};
                 float4 y[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const float4 *>(F + Y + (l + e) * kLS);
+                for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const float4 *>(F + at.Y + (l + e) * kLS);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     acc[0] = fmaf(xe[e], y[e].x, acc[0]);
@@ -978,11 +978,13 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
                 }
             }
             const float f = step == 1 || step >= 4 ? -1.f : 1.f;
-            *reinterpret_cast<float4 *>(F + Z) = make_float4(f * acc[0], f * acc[1], f * acc[2], f * acc[3]);
-            if (step < 2 || step == 3) named_bar(kBarInv, 128);
+            *reinterpret_cast<float4 *>(F + at.Z) = make_float4(f * acc[0], f * acc[1], f * acc[2], f * acc[3]);
+            if (step == kInvSteps - 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&s.inverted[st]));
+            }
+            if (inverse_joins(step)) named_bar(kBarInv, 32 * kInvWarps);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.inverted[st]));
     }
     waits.end(s);
 }
@@ -1551,6 +1553,35 @@ size_t gdn_scratch_bytes(int num_sms, int32_t H, int32_t n_rows)
     int j = 0, w;
     for (int64_t pairs = H; j == 0 && pairs <= num_sms; pairs += H) split_of(num_sms, pairs, n_rows, j, w);
     return j ? kSplitHeader + (size_t)num_sms * 2 * kD * kD * sizeof(float) : 0;
+}
+
+// Words that two of the inverse's warps touch, one of them writing, with no meeting in between: two chunks' steps on end, as the
+// warps take them.  (What is not theirs waits for barriers of its own.)
+int gdn_inverse_conflicts()
+{
+    constexpr int kWords = 2 * kLFloats + 32 * kLS;
+    std::vector<uint8_t> read(kWords), written(kWords);        // a bit for each warp, since the last meeting
+    int conflicts = 0;
+    for (int chunk = 0; chunk < 2; ++chunk)
+        for (int step = 0; step < kInvSteps; ++step) {
+            for (int warp = 0; warp < kInvWarps; ++warp)
+                for (int lane = 0; lane < 32; ++lane) {
+                    const InverseStep at = inverse_step(step, chunk * kLFloats, warp, lane);
+                    const uint8_t own = (uint8_t)(1 << warp);
+                    for (int e = 0; e < 4; ++e) {
+                        for (int l = at.l0; l < at.l1; ++l) read[at.Y + l * kLS + e] |= own;
+                        written[at.Z + e] |= own;
+                    }
+                    for (int l = at.l0; l < at.l1; ++l) read[at.X + l] |= own;
+                }
+            if (!inverse_joins(step) && !(chunk && step == kInvSteps - 1)) continue;
+            for (int w = 0; w < kWords; ++w) {
+                const int writers = written[w], all = writers | read[w];
+                conflicts += writers && (all & (all - 1));
+                written[w] = read[w] = 0;
+            }
+        }
+    return conflicts;
 }
 
 }  // namespace w12i

@@ -300,6 +300,8 @@ void w12_debug_set(int32_t flags, uint64_t timeout_ns)
 
 int32_t w12_debug_num_sms(void) { return num_sms(); }
 
+int32_t w12_debug_gdn_inverse_conflicts(void) { return gdn_inverse_conflicts(); }
+
 int32_t w12_debug_attn_registers(int32_t cols, int32_t *wanted)
 {
     int w = 0;

@@ -177,6 +177,7 @@ struct GdnSeqArgs {
 };
 size_t gdn_scratch_bytes(int num_sms, int32_t H, int32_t n_rows);
 int launch_gdn_prefill(const GdnSeqArgs &a, void *stream);
+int gdn_inverse_conflicts();          // see w12_debug_gdn_inverse_conflicts
 int launch_gdn_step(const GdnSeqArgs &a, void *stream);
 
 // norms around a block (k_norm.cu)
