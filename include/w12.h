@@ -433,13 +433,16 @@ size_t w12_gdn_scratch_bytes(int32_t n_heads, int32_t n_rows);
  * itself, else the two do not overlap).  Any number of rows a request, none
  * included: its state is then copied.  Rows outside every request are neither
  * read nor written.  Requests' rows do not overlap.
- * Outputs and states are those of the token-by-token form to FP32 rounding: next to BF16 operands, FP32 ones enter the
- * tensor cores as three BF16 pieces that add up to them; two FP32 operands both enter as two F16 pieces of 22 bits; sums
- * are FP32.  Runs of 64 rows (counted from row_off[r]) are taken at once, and with scratch few long requests are cut into parts
+ * Outputs and states are those of the token-by-token form to FP32 rounding: FP32 operands enter the tensor cores as three
+ * BF16 pieces that add up to them (of two such operands' products what is below 2^-21 is left out); sums are FP32.  A row's
+ * rounding is relative to what the state in front of its run and the values of the run's rows up to it leave under their
+ * gates: rows behind it, and what a gate has forgotten, do not enter; what writes of the same run replace does.
+ * Runs of 64 rows (counted from row_off[r]) are taken at once, and with scratch few long requests are cut into parts
  * that run beside one another: where they are cut depends on n_req, n_rows and the request's rows, so the last bits of a
- * request's results may depend on the call it is in, but not from one such call to the next.  Gates may be zero or negative.
- * A value of a row that is not finite may reach every output of its own run of 64 rows and of all later rows of its request and
- * head; other requests and heads never.
+ * request's results may depend on the call it is in, but not from one such call to the next.
+ * Gates may be zero, negative or above 1; their products within a run, and those times the state, are FP32 values too.
+ * A value of a row that is not finite, or a product that FP32 does not hold, may reach every output of its own run of 64 rows
+ * and of all later rows of its request and head; other requests and heads never.
  * ws: as for w12_tree_build.  Device checks: offsets that descend or leave
  * [0, n_rows] set W12_E_INVAL in the status word, and that request is left as it was;
  * a wait that runs out sets W12_E_TIMEOUT (outputs undefined, the states of the requests and heads concerned not written).

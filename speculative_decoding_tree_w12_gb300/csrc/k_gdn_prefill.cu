@@ -15,9 +15,10 @@
 // A CTA takes one (request, head) after another; the state rows c lie on the 128 lanes of tensor memory throughout, so that
 // all its products take their left operand from there and no operand but M and A is ever written to shared memory:
 //     D_K[c][j] = S k_j    D_Q[c][j] = S q_j    U[c][i] = X M^T    U A^T    S' = U K.
-// Products with keys and queries take those as they are and the FP32 side (S, U) as three BF16 pieces that add up to it exactly:
-// two (2^-17) would be the largest error of the layer by far.  Products of two FP32 sides (X M^T, U A^T) take both as two F16
-// pieces (2^-22) under a power of two for each row, and of their four pairs all but the smallest.  All accumulation is FP32.
+// An FP32 operand (S, U, X, M, A) is three BF16 pieces that add up to it exactly: two (2^-17) would be the largest error of the
+// layer by far, and F16 pieces need a unit, under which small values are lost beside large ones (a row's 64 tokens differ by what
+// their gates forget or raise).  Keys and queries are BF16 as they are; of two FP32 operands' nine pairs of pieces (X M^T, U A^T) the
+// three smallest are left out: 2^-21 of a product at most, 2^-24 in the mean.  All accumulation is FP32.
 //
 // A chunk runs through S's pieces -> S k -> X -> U -> U's pieces -> U K -> S', each step of which waits for the one before
 // it; the rest (A, M, U A^T and the outputs) is other warps' work, a chunk ahead or beside it:
@@ -29,9 +30,8 @@
 //  * warp 24 issues the products with the state, warp 25 the copies by TMA, warps 26 and 27 make M's pieces.
 // A chunk takes 4.2 to 4.4 us (8,000 to 8,500 cycles) however many there are: sixteen prompts of up to 8192 tokens x 32 heads
 // 1417 us, 2.5 times what their bytes take at the measured copy bandwidth.  That is the way through the steps above, on a full
-// machine: S's pieces 2,200 cycles (three BF16 pieces take 11 cycles of a scheduler for two values of 32 lanes, two F16 pieces 5),
-// what of S k is left then 950, X 1,150, M X 800, U's pieces 1,450, U K 700, S' 700; each with some 200 for its hand-over between
-// warps.  The schedulers issue in 58 % of the cycles, the tensor cores work in 32 %.  With fewer warps of more columns each it took 1.2 times as long.
+// machine: S's pieces 2,200 cycles (three BF16 pieces take 11 cycles of a scheduler for two values of 32 lanes), what of
+// S k is left then 950, X 1,150, M X 800, U's pieces 1,450, U K 700, S' 700; each with some 200 for its hand-over between warps.  The schedulers issue in 58 % of the cycles, the tensor cores work in 32 %.  With fewer warps of more columns each it took 1.2 times as long.
 // The products are issued in rolled loops and the code is kept short: straight-line code of a few times this length spent half
 // its time on its own way in.  A new pair costs 3 us more than its chunks, 5 where a state is read.
 // Every wait is bounded; when one has run out the state is left unwritten.
@@ -59,19 +59,28 @@ static_assert(256 * (kRegsState + kRegsLaunch) + 128 * (kRegsGate + kRegsInv + k
 
 // tensor memory columns: all 512 are one CTA's, from column 0 on
 constexpr uint32_t kColS = 0;       // S: three pieces of 64 columns; then three of U for S', 32 each,
-constexpr uint32_t kColUA = 128;    // and, over S's last, two of U for A
+constexpr uint32_t kColUA = 96;     // and three of U for A, by token_piece
 constexpr uint32_t kColDQ = 192;    // S q; then, scaled and with U A added, the outputs
 constexpr uint32_t kColDK = 256;    // S k; then, with the next 64 columns, U K
-constexpr uint32_t kColX = 320;     // X's two pieces
+constexpr uint32_t kColX = 256;     // X's three pieces, by token_piece: a thread's lie over the S k that it alone has read
 constexpr uint32_t kColU = 384;     // U
 constexpr uint32_t kColKK = 448;    // k.k (lanes 0..63) and q.k (lanes 64..127) of the next chunk
+
+// where 32 tokens' (half 0 or 1) high, middle and low pieces (0 .. 2) are, 16 columns each: the first two beside one another
+__host__ __device__ constexpr uint32_t token_piece(int piece, int half) { return piece < 2 ? 32 * half + 16 * piece : 64 + 16 * half; }
+
+// A piece of M or A in shared memory, rows of 32 BF16 under the 64-byte swizzle: all rows' first half, then the lower rows' second
+// (the upper rows have none)
+constexpr int kTriBytes = (kC + kC / 2) * 64, kTriRight = kC * 64;
+__host__ __device__ constexpr int tri_at(int row, int col)
+{
+    return (col < 32 ? row * 64 : kTriRight + (row - 32) * 64) + ((((col & 31) >> 3) ^ ((row >> 1) & 3)) << 4);
+}
 
 // L, then M: three blocks of 32 x 32 (the one above the diagonal is zero), their FP32 rows 16-byte aligned and 4 banks apart
 constexpr int kLS = 36;
 constexpr int kL11 = 0, kL22 = 32 * kLS, kL21 = 2 * 32 * kLS, kLFloats = 3 * 32 * kLS;
-// named barriers: of the gate warps, of the inverse warps, of the gate warps' latter two, of the piece warps, and of the two
-// token warps of 32 state rows (2 .. 5)
-constexpr int kBarGate = 1, kBarInv = 6, kBarQuery = 7, kBarPiece = 8, kBarRow = 2;
+constexpr int kBarGate = 1, kBarInv = 2;   // named barriers: of the gate warps, of the inverse warps
 constexpr int kStages = 3;          // of keys and queries (their chunk is prepared while two others are in use)
 
 // what a chunk is of
@@ -88,8 +97,8 @@ constexpr int kChunks = 8;          // descriptions kept
 
 struct PrefillShared {
     uint8_t KQ[kStages][2 * 128 * 128];   // [stage][feature half][key rows, query rows][64 BF16], 128-byte swizzle
-    uint8_t A[2][2][kC * 128];      // pieces of A and M, rows of 64 F16, 128-byte swizzle
-    uint8_t M[2][kC * 128];
+    uint8_t A[2][3][kTriBytes];     // pieces of A and M
+    uint8_t M[3][kTriBytes];
     uint16_t V[2][kC * kD];
     alignas(16) float L[2][kLFloats];   // then, in place, M
     alignas(16) float T[32 * kLS];      // products in between
@@ -98,13 +107,7 @@ struct PrefillShared {
     alignas(16) float bG[4][kC];
     alignas(16) float G[4][kC];
     alignas(16) float tail[4][kC];
-    alignas(16) float m_unit[4][kC];   // the powers of two of M's rows, and D_Ci times them
-    alignas(16) float m_tail[4][kC];
-    float top[2][2][kD];            // [X, S q][half of the tokens] largest magnitude of a state row's values
-    float x_back[kD];               // powers of two of X's rows
-    float a_top[2], a_back[4];      // largest magnitude of A's rows by halves, its power of two
-    uint32_t m_top[4];              // largest magnitude in M, as its bits
-    float gates[2], grow[2];        // products of the gates of tokens 0 .. 31 and 32 .. 63, and of the magnitudes above 1
+    float gates[2];                 // products of the gates of tokens 0 .. 31 and 32 .. 63
     Chunk chunk[kChunks];           // of chunk c in [c % 8], by the thread that issues the copies
     unsigned long long told[4];                         // it is there
     unsigned long long full[kStages], empty[kStages];   // keys and queries
@@ -212,10 +215,17 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t low)
     return d;
 }
 __device__ __forceinline__ uint64_t desc_k(uint32_t low) { return desc_of(low | (1u << 16)); }
+// ... rows of 32 values under the 64-byte swizzle, eight rows 512 bytes on
+__device__ __forceinline__ uint64_t desc_tri(uint32_t low)
+{
+    constexpr uint32_t high = (512u >> 4) | (1u << 14) | (4u << 29);
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low | (1u << 16)), "n"(high));
+    return d;
+}
 __device__ __forceinline__ uint64_t desc_mn(uint32_t low) { return desc_of(low | ((128u * 128u / 16u) << 16)); }
 
 constexpr uint32_t kBMnMajor = 1u << 16;   // instruction descriptor: B's rows are its K index
-constexpr uint32_t kIdescF16 = (1u << 4) | ((uint32_t)(kC >> 3) << 17) | ((128u >> 4) << 24);   // F16 operands, both K-major, N = 64
 
 // The high, middle and low BF16 pieces of 2N values, N words each: `put(piece, words)`.  Every piece is
 // the upper half of what the ones before it left, so the three add up exactly.
@@ -238,55 +248,6 @@ __device__ __forceinline__ void pieces3(float (&x)[2 * N], F put)
         }
         put(piece, w);
     }
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
-__device__ __forceinline__ float2 unpack_f16x2(uint32_t w)
-{
-    float2 r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(w));
-    return r;
-}
-
-// The power of two that brings magnitudes up to `top` into [2^13, 2^14), and its inverse.  F16's range below that
-// is 2^-38 of the top, far under what FP32 sums keep; magnitudes under 2^-113 count as that.
-struct Unit {
-    float scale, back;
-};
-__device__ __forceinline__ Unit unit_of(float top)
-{
-    const uint32_t e = min(max(__float_as_uint(top) >> 23, 14u), 253u);
-    return Unit{__uint_as_float((267u - e) << 23), __uint_as_float((e - 13u) << 23)};
-}
-
-template <int N>
-__device__ __forceinline__ float top_of(const float (&x)[N])
-{
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(x[i]));
-    return top;
-}
-
-// The two F16 pieces of values below 2^15, rounded to nearest: what is left is 2^-22 of a value
-template <int N, class F>
-__device__ __forceinline__ void pieces2(const float (&x)[N], F put)
-{
-    uint32_t hi[N / 2], lo[N / 2];
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        hi[i] = pack_f16x2(x[2 * i], x[2 * i + 1]);
-        const float2 r = __ffma2_rn(unpack_f16x2(hi[i]), make_float2(-1.f, -1.f), make_float2(x[2 * i], x[2 * i + 1]));
-        lo[i] = pack_f16x2(r.x, r.y);
-    }
-    put(0, hi);
-    put(1, lo);
 }
 
 __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8])
@@ -353,23 +314,13 @@ __device__ __forceinline__ void store8(float *dst, const float *x)
                  : "memory");
 }
 
-// x *= y; x *= f, two at a time
+// x *= y, two at a time
 template <int N>
 __device__ __forceinline__ void mul_n(float (&x)[N], const float (&y)[N])
 {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
         const float2 r = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]));
-        x[i] = r.x;
-        x[i + 1] = r.y;
-    }
-}
-template <int N>
-__device__ __forceinline__ void scale_n(float (&x)[N], float f)
-{
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float2 r = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(f, f));
         x[i] = r.x;
         x[i + 1] = r.y;
     }
@@ -526,17 +477,13 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
 
         // U scaled for S', over S's pieces (which have been read: S q came before U)
         wait(s.gready[g & 1], par2);
-        wait(s.mready[g & 1], par2);
-        wait(s.have_x, par);
-        const float back = s.x_back[c];
         wait(s.done_u, par);
 #pragma unroll 1
         for (int q = 0; q < 2; ++q) {
             const int t0 = 32 * part + 16 * q;
             float x[16], f[16];
             tmem_ld<16>(tm + kColU + t0, x);
-            read_n(s.m_tail[k4] + t0, f);
-            scale_n(f, back);
+            read_n(s.tail[k4] + t0, f);
             tmem_ld_wait();
             mul_n(x, f);
             pieces3<8>(x, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColS + 32 * piece + t0 / 2, w); });
@@ -581,11 +528,9 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         waits.on(bar, parity);
         tc_fence_after();
     };
-    // the larger of `top` here and in the thread with the other half of the tokens
-    auto row_top = [&](float (&at)[2][kD], float top) {
-        at[part][c] = top;
-        named_bar(kBarRow + (warp & 3), 64);
-        return fmaxf(top, at[part ^ 1][c]);
+    // the pieces of 16 tokens' values, from the first or the second of this thread's sixteens
+    auto put = [&](uint32_t col, int sixteen, float (&z)[16]) {
+        pieces3<8>(z, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + col + token_piece(piece, part) + 8 * sixteen, w); });
     };
     const int total = s.total;
 #pragma unroll 1
@@ -595,7 +540,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         // X = b (v - G S k); b v while S k is being made
         wait(s.vfull[st], par2);
         wait(s.gready[st], par2);
-        float x[32], top = 0.f;
+        float x[32];
 #pragma unroll
         for (int q = 0; q < 32; q += 8) {
             float e[8];
@@ -618,27 +563,21 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
                 const float2 r = __ffma2_rn(make_float2(f[j], f[j + 1]), make_float2(d[j], d[j + 1]), make_float2(x[q + j], x[q + j + 1]));
                 x[q + j] = r.x;
                 x[q + j + 1] = r.y;
-                top = fmaxf(top, fmaxf(fabsf(r.x), fabsf(r.y)));
             }
         }
-        const Unit ux = unit_of(row_top(s.top[0], top));
-        if (part == 0) s.x_back[c] = ux.back;
-        scale_n(x, ux.scale);
 #pragma unroll
         for (int q = 0; q < 32; q += 16) {
             float z[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) z[j] = x[q + j];
-            pieces2(z, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColX + 32 * piece + (t0 + q) / 2, w); });
+            put(kColX, q >> 4, z);
         }
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_x), lane);
         if (s.silent) continue;
 
-        // S q to where U A is added to it: G S q in the units of U and A.  U's unit is a bound, at most 64 |M| |X|
-        // (F16 has 16 bits to spare under the largest value), and one under which S q keeps finite.
+        // G S q, to which U A is added
         wait(s.done_q, par);
-        top = 0.f;
 #pragma unroll
         for (int q = 0; q < 32; q += 16) {
             float z[16], f[16];
@@ -646,22 +585,6 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
             read_n(s.G[k4] + t0 + q, f);
             tmem_ld_wait();
             mul_n(z, f);
-            top = fmaxf(top, top_of(z));
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[q + j] = z[j];
-        }
-        const float a_back = s.a_back[k4];
-        const float a_scale = __uint_as_float(0x7F000000u - __float_as_uint(a_back));   // 1 / a_back
-        top = row_top(s.top[1], top) * 0x1p-60f * a_scale;
-        wait(s.mready[st], par2);
-        const Unit uu = unit_of(fmaxf(top, ux.back * 0x1p20f * __uint_as_float(s.m_top[k4])));
-        scale_n(x, uu.scale);
-        scale_n(x, a_scale);
-#pragma unroll
-        for (int q = 0; q < 32; q += 16) {
-            float z[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) z[j] = x[q + j];
             tmem_put(tm + kColDQ + t0 + q, z);
         }
 
@@ -669,14 +592,11 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         wait(s.done_u, par);
         wait(s.have_us[0], par);                  // (the state warps' way goes first: sixteen prompts of 4096 tokens 736 us without, 728 with)
 #pragma unroll 1
-        for (int q = t0; q < t0 + 32; q += 16) {
-            float x[16], f[16];
-            tmem_ld<16>(tm + kColU + q, x);
-            read_n(s.m_unit[k4] + q, f);
-            scale_n(f, ux.back * uu.scale);
+        for (int q = 0; q < 2; ++q) {
+            float z[16];
+            tmem_ld<16>(tm + kColU + t0 + 16 * q, z);
             tmem_ld_wait();
-            mul_n(x, f);
-            pieces2(x, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + kColUA + 32 * piece + q / 2, w); });
+            put(kColUA, q, z);
         }
         tmem_st_wait();
         warp_arrive(smem_u32(&s.have_u), lane);
@@ -692,8 +612,6 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
             float x[16];
             tmem_ld<16>(tm + kColDQ + q, x);
             tmem_ld_wait();
-            scale_n(x, uu.back);
-            scale_n(x, a_back);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 if (j < left) *dst = x[j];
@@ -709,14 +627,13 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
 // gate warps
 // ---------------------------------------------------------------------------
 
-// the two pieces of 16 values into row `row` of swizzled tiles, from column `col0` on (a multiple of 16)
-__device__ __forceinline__ void put_row(uint8_t (&tile)[2][kC * 128], int row, int col0, const float (&x)[16])
+// the pieces of 16 values into row `row` of tiles, from column `col0` on (a multiple of 16)
+__device__ __forceinline__ void put_row(uint8_t (&tile)[3][kTriBytes], int row, int col0, float (&x)[16])
 {
-    pieces2(x, [&](int piece, const uint32_t (&w)[8]) {
+    pieces3<8>(x, [&](int piece, const uint32_t (&w)[8]) {
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-            *reinterpret_cast<uint4 *>(tile[piece] + row * 128 + (((col0 / 8 + q) ^ (row & 7)) << 4)) =
-                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+            *reinterpret_cast<uint4 *>(tile[piece] + tri_at(row, col0 + 8 * q)) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
     });
 }
 
@@ -818,24 +735,19 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         const uint32_t par2 = (g >> 1) & 1;
         if (warp == 3) products(g, valid);
         const float strength = b;
-        float up = a, down = a, grow = fmaxf(fabsf(a), 1.f);
+        float up = a, down = a;
         if (!query) {
-            // products of the gates from this block of 32 tokens' start to token i, and from behind it to the block's
-            // end; and of the magnitudes above 1, which bound the D_ij
+            // products of the gates from this block of 32 tokens' start to token i, and from behind it to the block's end
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const float u = __shfl_up_sync(0xffffffffu, up, o), v = __shfl_down_sync(0xffffffffu, down, o);
-                grow *= __shfl_xor_sync(0xffffffffu, grow, o);
                 if (lane >= o) up *= u;
                 if (lane + o < 32) down *= v;
             }
             down = __shfl_down_sync(0xffffffffu, down, 1);
             if (lane == 31) down = 1.f;
             s.next[(i + kC - 1) & (kC - 1)] = i ? a : 1.f;
-            if (lane == 31) {
-                s.gates[warp] = up;
-                s.grow[warp] = grow;
-            }
+            if (lane == 31) s.gates[warp] = up;
         }
         named_bar(kBarGate, 128);
         if (g + 1 < total) fetch(g + 1);
@@ -848,32 +760,10 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         }
         waits.on(s.bar_kk, g & 1);
         tc_fence_after();
-        if (query) {
-            // A's unit, from a bound: |q_i.k_j| times what the gates can add
-            float top = 0.f;
-#pragma unroll 1
-            for (int J = 0; J < blocks; ++J) {
-                float x[16];
-                tmem_ld<16>(tm + kColKK + 16 * J, x);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) top = fmaxf(top, 16 * J + j <= i ? fabsf(x[j]) : 0.f);
-            }
-            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-            if (lane == 0) s.a_top[warp & 1] = __uint_as_float(most);
-        }
-        // D_ij (times b_i, or in A's unit), from j = i down, times the row of k.k or q.k
+        // D_ij (for L times b_i), from j = i down, times the row of k.k or q.k
         {
-            float d = strength;
-            if (query) {
-                named_bar(kBarQuery, 64);
-                const Unit u = unit_of(fmaxf(s.a_top[0], s.a_top[1]) * s.grow[0] * s.grow[1]);
-                if (g >= 2) waits.on(s.gused[st], par2 ^ 1u);
-                if (tid == 64) s.a_back[k4] = u.back;
-                d = u.scale;
-            } else if (g >= 2) {
-                waits.on(s.lfree[st], par2 ^ 1u);
-            }
+            float d = query ? 1.f : strength;
+            if (g >= 2) waits.on(query ? s.gused[st] : s.lfree[st], par2 ^ 1u);
             const int last = query ? i : i - 1;   // the row's last entry
 #pragma unroll 1
             for (int J = blocks - 1; J >= 0; --J) {
@@ -1008,16 +898,22 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
     };
     // (Each product adds to its sum with a rounding of some 2^-24 of that sum, towards zero: so the small pieces come first,
     // and few products meet a sum of full size.)
-    // U or U A: two FP32 operands of two F16 pieces each, K = 64 tokens: low times high, high times low, high times high
-    auto pairs = [&](uint32_t d, uint32_t a, const uint8_t *B, uint32_t add) {
-        const uint32_t b0 = desc_low(smem_u32(B));
-#pragma unroll 1
-        for (int q = 0; q < 3; ++q) {
-            const uint32_t b = b0 + (q == 1 ? kC * 128 / 16 : 0), aq = a + (q == 0 ? 32 : 0);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) tc_mma_ts(d, aq + 8 * ks, desc_k(b + ks * 2), kIdescF16, add | (uint32_t)(q | ks));
-        }
+    // U or U A: two FP32 operands of three BF16 pieces each, one pair of which this adds; pair q of six is low times high, high times
+    // low, middle times middle, middle times high, high times middle, high times high.  The
+    // columns of tokens 0 .. 31 are sums over those tokens alone, and an accumulator of their own: products of one shape on one
+    // accumulator keep their order.
+    auto pair = [&](uint32_t d, uint32_t a, uint32_t b, int pa, int pb, uint32_t add) {
+        constexpr uint32_t lower = 32 * 64 / 16, right = kTriRight / 16, idesc = idesc_bf16_f32(128, kC / 2);
+        b += pb * (kTriBytes / 16);
+        const uint32_t a0 = a + token_piece(pa, 0), a1 = a + token_piece(pa, 1);
+        tc_mma_ts(d, a0, desc_tri(b), idesc, add);
+        tc_mma_ts(d, a0 + 8, desc_tri(b + 2), idesc, 1);
+        tc_mma_ts(d + kC / 2, a0, desc_tri(b + lower), idesc, add);
+        tc_mma_ts(d + kC / 2, a0 + 8, desc_tri(b + lower + 2), idesc, 1);
+        tc_mma_ts(d + kC / 2, a1, desc_tri(b + right), idesc, 1);
+        tc_mma_ts(d + kC / 2, a1 + 8, desc_tri(b + right + 2), idesc, 1);
     };
+    constexpr int kPairA[6] = {2, 0, 1, 1, 0, 0}, kPairB[6] = {0, 2, 1, 0, 1, 0};
     // a piece (0 high, 2 low) of a half of both threads' features of S times the keys (rows 0..63 of the tile) or the queries
     // (64..127)
     auto product = [&](uint32_t d, uint32_t tile, int half, int piece, bool first) {
@@ -1045,7 +941,13 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
         for (int q = silent ? 6 : 0; q < 6; ++q) product(kColDQ, kq + kC * 128, q & 1, 2 - (q >> 1), q == 0);
         tc_commit(smem_u32(&s.done_q));
         if (!wait(s.mready[st], par2) || !wait(s.have_x, par)) break;
-        pairs(kColU, kColX, s.M[0], 0);
+        {
+            const uint32_t b = desc_low(smem_u32(s.M[0]));
+            // (Straight-line: the state waits for it, and a rolled loop issues a product in 20 cycles, this in 16, as long as it takes.
+            // One prompt of 32768 tokens, 32 heads: 1349 us rolled, 1293 with U A unrolled as well, 1270 so.)
+#pragma unroll
+            for (int q = 0; q < 6; ++q) pair(kColU, kColX, b, kPairA[q], kPairB[q], (uint32_t)q);
+        }
         tc_commit(smem_u32(&s.done_u));
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -1066,7 +968,9 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
         }
         if (!silent) {
             if (!wait(s.have_u, par)) break;
-            pairs(kColDQ, kColUA, s.A[st][0], 1);
+            const uint32_t b = desc_low(smem_u32(s.A[st][0]));
+#pragma unroll 1
+            for (int q = 0; q < 6; ++q) pair(kColDQ, kColUA, b, (0x052 >> (2 * q)) & 3, (0x118 >> (2 * q)) & 3, 1);   // (kPairA, kPairB)
         }
         tc_commit(smem_u32(&s.done_o));
         tc_commit(smem_u32(&s.gused[st]));
@@ -1076,42 +980,25 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
     waits.end(s);
 }
 
-// M's pieces, eight columns to a thread and turn: the upper rows' left half (four threads to a row), then the lower rows (eight)
+// M's pieces, eight columns to a thread and turn, two turns to a block of 32 x 32
 __device__ __forceinline__ void piece_warps(const PrefillParams &p, PrefillShared &s)
 {
     const int tid = threadIdx.x - kIssue0 - 64, lane = tid & 31;
     Waits waits{p.polls + 16u * s.total};
 #pragma unroll 1
     for (int g = 0; g < s.total; ++g) {
-        const int st = g & 1, k4 = g & 3;
+        const int st = g & 1;
         waits.on(s.inverted[st], (g >> 1) & 1);
         if (g > 0) waits.on(s.done_u, (g & 1) ^ 1u);          // the M before it has been read
-        if (tid == 0) s.m_top[(g + 1) & 3] = 0;
-        named_bar(kBarPiece, 64);
-        uint32_t most = 0;
 #pragma unroll 1
         for (int q = 0; q < 6; ++q) {
-            const int row = q < 2 ? 16 * q + (tid >> 2) : 16 + 8 * q + (tid >> 3), col = (q < 2 ? tid & 3 : tid & 7) * 8;
+            const int row = 16 * (q & 1) + (tid >> 2), col = 8 * (tid & 3);   // in the block
             float x[8];
-            read_n(s.L[st] + (row < 32 ? kL11 : col < 32 ? kL21 : kL22) + (row & 31) * kLS + (col & 31), x);
-            float top = top_of(x);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float other = __shfl_xor_sync(0xffffffffu, top, 4);
-            if (q >= 2) top = fmaxf(top, other);
-            const Unit u = unit_of(top);
-            most = max(most, __float_as_uint(top));
-            if (col == 0) {
-                s.m_unit[k4][row] = u.back;
-                s.m_tail[k4][row] = u.back * s.tail[k4][row];
-            }
-            scale_n(x, u.scale);
-            pieces2(x, [&](int piece, const uint32_t (&w)[4]) {
-                *reinterpret_cast<uint4 *>(s.M[piece] + row * 128 + (((col >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            read_n(s.L[st] + (q < 2 ? kL11 : q < 4 ? kL21 : kL22) + row * kLS + col, x);
+            pieces3<4>(x, [&](int piece, const uint32_t (&w)[4]) {
+                *reinterpret_cast<uint4 *>(s.M[piece] + tri_at(row + (q < 2 ? 0 : 32), col + (q < 4 ? 0 : 32))) = make_uint4(w[0], w[1], w[2], w[3]);
             });
         }
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) atomicMax(&s.m_top[k4], most);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) {
@@ -1231,7 +1118,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (unsigned long long *b : {&s.bar_kk, &s.done_k, &s.done_q, &s.done_u, &s.done_s, &s.done_o, &s.last, &s.last_kk}) mbar_init(smem_u32(b), 1);
         for (unsigned long long *b : {&s.have_s[0], &s.have_s[1], &s.have_us[0], &s.have_us[1], &s.have_x, &s.have_u, &s.read_o}) mbar_init(smem_u32(b), 8);
-        for (int i = 0; i < 4; ++i) s.m_top[i] = 0;
         s.abort = 0;
         fence_mbar_init();
         prefetch_tmap(&qmap);
@@ -1240,16 +1126,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 0) tmem_alloc(smem_u32(&s.tmem), 512);
     if (tid >= 32 && tid < 32 + kChunks) s.chunk[tid - 32] = Chunk{};   // (what is read of it where a wait has run out)
-    // what no chunk writes and every chunk reads: M and A above the diagonal blocks of 32
-    for (int e = tid; e < 32 * 4; e += kThreads) {
-        const int row = e >> 2, at = row * 128 + (((4 + (e & 3)) ^ (row & 7)) << 4);
-        const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int piece = 0; piece < 2; ++piece) {
-            *reinterpret_cast<uint4 *>(s.M[piece] + at) = z;
-            for (int st = 0; st < 2; ++st) *reinterpret_cast<uint4 *>(s.A[st][piece] + at) = z;
-        }
-    }
     {
         // the requests by their rows, and this CTA's chunks
         int32_t *rows = reinterpret_cast<int32_t *>(s.KQ[0]);
