@@ -445,7 +445,8 @@ size_t w12_gdn_scratch_bytes(int32_t n_heads, int32_t n_rows);
  * and of all later rows of its request and head; other requests and heads never.
  * ws: as for w12_tree_build.  Device checks: offsets that descend or leave
  * [0, n_rows] set W12_E_INVAL in the status word, and that request is left as it was;
- * a wait that runs out sets W12_E_TIMEOUT (outputs undefined, the states of the requests and heads concerned not written).
+ * a wait that runs out sets W12_E_TIMEOUT (outputs undefined; the states of the requests and heads concerned, and of those that
+ * the same SM takes after them, are not written, each other state whole).
  */
 w12_status w12_gdn_prefill(const w12_gdn_rows *rows, int32_t n_req, const int32_t *row_off, const float *S0,
                            float *state, float *o, void *ws, size_t ws_bytes, w12_stream_t stream);

@@ -35,6 +35,10 @@ extern "C" {
  *                launch per up to 144 GEMMs, each GEMM's activations read
  *                once every CTA has finished the previous GEMM.  Bits 2 and
  *                3 take precedence.
+ *   flags bit 5: w12_gdn_prefill: in CTA 0 the warps that make the updates'
+ *                right side have used their time up when the last chunk's
+ *                products reach them, the other roles theirs not:
+ *                W12_E_TIMEOUT, and that chunk's state is not written.
  *   timeout_ns:  limit of every bounded wait inside the kernels
  *                (0 restores the default of 2 seconds).
  * Not thread-safe; meant to be set between launches by a test.

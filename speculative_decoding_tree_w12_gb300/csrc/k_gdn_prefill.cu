@@ -34,7 +34,7 @@
 // S k is left then 950, X 1,150, M X 800, U's pieces 1,450, U K 700, S' 700; each with some 200 for its hand-over between warps.  The schedulers issue in 58 % of the cycles, the tensor cores work in 32 %.  With fewer warps of more columns each it took 1.2 times as long.
 // The products are issued in rolled loops and the code is kept short: straight-line code of a few times this length spent half
 // its time on its own way in.  A new pair costs 3 us more than its chunks, 5 where a state is read.
-// Every wait is bounded; when one has run out the state is left unwritten.
+// Every wait is bounded; when one has run out no state that what did not come is part of is written.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -80,7 +80,7 @@ __host__ __device__ constexpr int tri_at(int row, int col)
 // L, then M: three blocks of 32 x 32 (the one above the diagonal is zero), their FP32 rows 16-byte aligned and 4 banks apart
 constexpr int kLS = 36;
 constexpr int kL11 = 0, kL22 = 32 * kLS, kL21 = 2 * 32 * kLS, kLFloats = 3 * 32 * kLS;
-constexpr int kBarGate = 1, kBarInv = 2;   // named barriers: of the gate warps, of the inverse warps
+constexpr int kBarGate = 1, kBarInv = 2, kBarState = 3;   // named barriers: of the gate warps, the inverse warps, the state warps
 constexpr int kStages = 3;          // of keys and queries (their chunk is prepared while two others are in use)
 
 // what a chunk is of
@@ -172,7 +172,8 @@ struct PrefillParams {
     uint32_t subs, items;           // items of a pair; n_req * H of them each
     uint32_t polls;                 // of a wait, before it gives up
     int32_t *status;
-    int32_t debug_flags;            // bit 0: CTA 0 announces its first copies and leaves them out (test hook)
+    int32_t debug_flags;            // test hooks, bit 0: CTA 0 announces its first copies and leaves them out; bit 5: its token
+                                    // warps' budget ends at its last chunk's S k
 };
 
 template <int N>
@@ -335,8 +336,9 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane)
 
 // A thread's bounded waits, in few instructions (there are three dozen of them): `left` is what it may still poll in all its
 // waits together (the time limit and 16 polls for every chunk), a poll sleeping up to kWaitSleepNs.  When that has run out no wait
-// lasts any more, so every role runs to its end, and says so there.  What it reads on the way may be old or half written: so no
-// address is made of it that is not checked where it is used.
+// lasts any more, so every role runs to its end.  What is made of what did not come is marked before it is signalled, so nothing
+// that it is part of is stored.  What is read on the way may be old or half written: so no address is made of it that is not checked
+// where it is used.  (Marked at once, in every wait: sixteen prompts of 1024 tokens x 32 heads 201 us, 190 so.)
 struct Waits {
     uint32_t left;
 
@@ -351,11 +353,23 @@ struct Waits {
         return true;
     }
 
-    __device__ __forceinline__ void end(PrefillShared &s) const
+    // in front of a signal to another role, and at a role's end
+    __device__ __forceinline__ void mark(PrefillShared &s) const
     {
         if (left == 0) *(volatile int32_t *)&s.abort = 1;
     }
 };
+
+// whether `ok` holds in every one of so many threads, the same answer in all of them
+__device__ __forceinline__ bool all_of(int id, int threads, bool ok)
+{
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all)
+                 : "r"(id), "r"(threads), "r"((uint32_t)ok)
+                 : "memory");
+    return all != 0;
+}
 
 // a wait of its own: for what is in flight at the end
 __device__ __forceinline__ void drain(unsigned long long &bar, uint32_t parity, const PrefillParams &p)
@@ -493,11 +507,15 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
 
         // S' = G_C S + U K
         const float gc = s.G[k4][kC - 1];
+        bool good = true;
         wait(s.done_s, par);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             float z[32];
             tmem_ld<32>(tm + kColDK + 64 * part + 32 * q, z);
+            // Whether a wait has run out for what this state is made of: one answer for all its rows, given in every chunk (where
+            // there is a state to write is no longer the same to all of them when one of their own has run out).
+            if (q == 0) good = all_of(kBarState, 256, waits.left && !*(volatile int32_t *)&s.abort);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
@@ -506,12 +524,12 @@ __device__ __forceinline__ void state_warps(const PrefillParams &p, PrefillShare
                 S[32 * q + i + 1] = n.y;
             }
         }
-        if (t.to && waits.left && !*(volatile int32_t *)&s.abort) {
+        if (good && t.to) {
 #pragma unroll
             for (int i = 0; i < 64; i += 8) store8(t.to + at + i, S + i);
         }
     }
-    waits.end(s);
+    waits.mark(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -533,6 +551,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         pieces3<8>(z, [&](int piece, const uint32_t (&w)[8]) { tmem_st_x8(tm + col + token_piece(piece, part) + 8 * sixteen, w); });
     };
     const int total = s.total;
+    const int impatient = (p.debug_flags & 32) && blockIdx.x == 0 && p.split.mode != kPieces ? total - 1 : -1;   // (test hook)
 #pragma unroll 1
     for (int g = 0; g < total; ++g) {
         const int st = g & 1, k4 = g & 3;
@@ -552,6 +571,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.vempty[st]));
         wait(s.done_k, par);
+        if (g == impatient) waits.left = 0;
 #pragma unroll
         for (int q = 0; q < 32; q += 16) {
             float d[16], f[16];
@@ -573,6 +593,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
             put(kColX, q >> 4, z);
         }
         tmem_st_wait();
+        waits.mark(s);
         warp_arrive(smem_u32(&s.have_x), lane);
         if (s.silent) continue;
 
@@ -620,7 +641,7 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
         }
         warp_arrive(smem_u32(&s.read_o), lane);
     }
-    waits.end(s);
+    waits.mark(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -799,10 +820,12 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
                 // the diagonal blocks of 16 of this warp's rows are its own: it inverts them at once
                 __syncwarp();
                 invert16(s.L[st] + (warp ? kL22 : kL11), lane);
+                waits.mark(s);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&s.lready[st]));
             }
         }
+        waits.mark(s);
         warp_arrive(smem_u32(&s.gready[st]), lane);
         named_bar(kBarGate, 128);                 // k.k and q.k have been read
     }
@@ -810,7 +833,7 @@ __device__ __forceinline__ void gate_warps(const PrefillParams &p, PrefillShared
         if (elect_lane()) tc_commit(smem_u32(&s.last_kk));
         drain(s.last_kk, 0, p);
     }
-    waits.end(s);
+    waits.mark(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -870,13 +893,14 @@ __device__ __forceinline__ void inverse_warps(const PrefillParams &p, PrefillSha
             const float f = step == 1 || step >= 4 ? -1.f : 1.f;
             *reinterpret_cast<float4 *>(F + at.Z) = make_float4(f * acc[0], f * acc[1], f * acc[2], f * acc[3]);
             if (step == kInvSteps - 1) {
+                waits.mark(s);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&s.inverted[st]));
             }
             if (inverse_joins(step)) named_bar(kBarInv, 32 * kInvWarps);
         }
     }
-    waits.end(s);
+    waits.mark(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -977,7 +1001,7 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
     }
     tc_commit(smem_u32(&s.last));
     drain(s.last, 0, p);   // no product in flight when tensor memory is given back
-    waits.end(s);
+    waits.mark(s);
 }
 
 // M's pieces, eight columns to a thread and turn, two turns to a block of 32 x 32
@@ -1000,13 +1024,14 @@ __device__ __forceinline__ void piece_warps(const PrefillParams &p, PrefillShare
             });
         }
         fence_async_shared();
+        waits.mark(s);
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(smem_u32(&s.mready[st]));
             mbar_arrive(smem_u32(&s.lfree[st]));
         }
     }
-    waits.end(s);
+    waits.mark(s);
 }
 
 __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShared &s, const CUtensorMap &qmap, const CUtensorMap &kmap,
@@ -1071,7 +1096,7 @@ __device__ __forceinline__ void copy_thread(const PrefillParams &p, PrefillShare
     // no copy into shared memory in flight at the end
     for (int i = max(kq_issued - kStages, 0); i < kq_issued; ++i) drain(s.full[i % kStages], (i / kStages) & 1, p);
     for (int i = max(v_issued - 2, 0); i < v_issued; ++i) drain(s.vfull[i & 1], (i >> 1) & 1, p);
-    waits.end(s);
+    waits.mark(s);
 }
 
 __device__ __forceinline__ void keep_state(const PrefillParams &p, int pair)
