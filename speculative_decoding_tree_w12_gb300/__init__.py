@@ -192,6 +192,18 @@ def _st_on(dev, stream) -> int:
     return _raw_stream() if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call on `stream` (None: the current one).  Memory of the current stream may still be in use there
+    when another stream's kernel writes it, so it is that stream's own; and since its reader may be on the current one,
+    it is nobody else's before both have passed its end."""
+    if stream is None or stream.cuda_stream == _raw_stream():
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        t = _torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(_torch.cuda.current_stream(t.device))
+    return t
+
+
 def _dp(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -768,7 +780,8 @@ class GdnRows:
     v (bfloat16 [T][H * 128]; slices of a fused row are fine), gates alpha and
     write strengths beta (float32 [T][H]).  Value head h reads query/key head
     h // (H // n_qk_heads).  The tensors stay the caller's.
-    Holds the scratch of ``w12_gdn_prefill``; one object's calls of it run in order."""
+    Holds the scratch of ``w12_gdn_prefill``; one object's calls of it run in order, and a captured one needs the object
+    for as long as its graph is replayed."""
 
     def __init__(self, q, k, v, alpha, beta):
         torch = _runtime()
@@ -788,20 +801,27 @@ class GdnRows:
                                         ((q, q.shape[1], "q"), (k, q.shape[1], "k"), (v, H * 128, "v")))
         self.c = GdnRowsC(H, q.shape[1] // 128, 128, T, qa, ka, va, qs, ks, vs, alpha.data_ptr(), beta.data_ptr(), None, 0)
         self.scratch = None                      # for w12_gdn_prefill, made by its first call
+        self._streams = set()                    # on which it has been used
         self.ref = C.byref(self.c)
 
-    def _make_scratch(self):
-        nbytes = int(_lib.w12_gdn_scratch_bytes(self.H, self.T))
-        self.scratch = _torch.empty(nbytes, dtype=_torch.uint8, device=self.alpha.device)
-        if nbytes:
-            self.c.scratch, self.c.scratch_bytes = self.scratch.data_ptr(), nbytes
+    def _scratch_on(self, st, stream):
+        """The scratch, made by the first call.  The allocator learns of every stream that uses it, so that it becomes nobody
+        else's while a call still runs."""
+        if self.scratch is None:
+            nbytes = int(_lib.w12_gdn_scratch_bytes(self.H, self.T))
+            self.scratch = _empty((nbytes,), _torch.uint8, self.alpha.device, stream)
+            if nbytes:
+                self.c.scratch, self.c.scratch_bytes = self.scratch.data_ptr(), nbytes
+        elif self.scratch.numel():
+            self.scratch.record_stream(_torch.cuda.current_stream() if stream is None else stream)
+        self._streams.add(st)
 
-    def _buffers(self, n_req, S0, state, out):
+    def _buffers(self, n_req, S0, state, out, stream):
         """The calls' state and output tensors, made or checked."""
         dev, shape = self.dev, (n_req, self.H, self.d, self.d)
         if dev < 0:
             _refuse(dev, n_req, None, self)
-        new = lambda *s: _torch.empty(s, dtype=_torch.float32, device=self.alpha.device)
+        new = lambda *s: _empty(s, _torch.float32, self.alpha.device, stream)
         state = new(*shape) if state is None else state
         out = new(self.T, self.H, self.d) if out is None else out
         for t, what, want in ((S0, "S0", shape), (state, "state", shape), (out, "out", (self.T, self.H, self.d))):
@@ -820,12 +840,12 @@ def w12_gdn_prefill(rows: GdnRows, row_off, ws: Workspace, S0=None, state=None, 
     n = row_off.shape[0] - 1
     if n < 1:
         raise ValueError("row_off: int32 [n_req + 1] wanted")
-    state, out = rows._buffers(n, S0, state, out)
+    state, out = rows._buffers(n, S0, state, out, stream)
     if ws.dev != rows.dev:
         _refuse(rows.dev, n, None, ws)
     st = _st_on(rows.dev, stream)
-    if rows.scratch is None:
-        rows._make_scratch()
+    if st not in rows._streams:
+        rows._scratch_on(st, stream)
     s = _lib.w12_gdn_prefill(rows.ref, n, _ints(row_off, n + 1, "row_off", rows.dev), _dp(S0), state.data_ptr(),
                              out.data_ptr(), ws.addr, ws.nbytes, st)
     if s:
@@ -836,7 +856,7 @@ def w12_gdn_prefill(rows: GdnRows, row_off, ws: Workspace, S0=None, state=None, 
 def w12_gdn_step(rows: GdnRows, S0=None, state=None, out=None, stream=None):
     """One token of every request: row r continues request r's state -> (out,
     state), as for ``w12_gdn_prefill``."""
-    state, out = rows._buffers(rows.T, S0, state, out)
+    state, out = rows._buffers(rows.T, S0, state, out, stream)
     s = _lib.w12_gdn_step(rows.ref, _dp(S0), state.data_ptr(), out.data_ptr(), _st_on(rows.dev, stream))
     if s:
         raise W12Error(s, "w12_gdn_step")
@@ -857,7 +877,7 @@ def w12_gdn_norm(o, weight, z=None, eps: float = 1e-6, gate_first: bool = False,
     R, H, _ = shape
     width = H * 128
     if out is None:
-        out = _torch.empty((R, width), dtype=_torch.bfloat16, device=o.device)
+        out = _empty((R, width), _torch.bfloat16, o.device, stream)
     za, zs = (None, 0) if z is None else _rows(z, R, width, "z", dev)
     oa, os_ = _rows(out, R, width, "out", dev)
     s = _lib.w12_gdn_norm(o.data_ptr(), R, H, 128, za, zs, _vector(weight, 128, "weight", dev), eps, gate_first, oa, os_,
@@ -921,11 +941,11 @@ def w12_block_norm(h, y=None, pre=None, post=None, scale: float = 1.0, eps: floa
         if post is not None:
             posta = _vector(post, n, "post", dev)
         if h_out is None:
-            h_out = _torch.empty((R, n), dtype=h.dtype, device=h.device)
+            h_out = _empty((R, n), h.dtype, h.device, stream)
         oa, os_ = _stream_rows(h_out, R, n, f32, "h_out", dev)
     if pre is not None:
         if out is None:
-            out = _torch.empty((R, n), dtype=_torch.bfloat16, device=h.device)
+            out = _empty((R, n), _torch.bfloat16, h.device, stream)
         xa, xs = _rows(out, R, n, "out", dev)
         prea = _vector(pre, n, "pre", dev)
     elif out is not None:

@@ -1,0 +1,145 @@
+"""Memory that a call makes for itself, where it runs on another stream than the current one: neither memory that the current
+stream may still use, nor memory that the current stream gets back while the call still uses it.  (What a torch allocation
+returns is what the stream under which it is made last freed: so a block that has just been freed shows whose memory it was.)"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from test_gpu_gdn_rows import Case, D
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def w12():
+    from speculative_decoding_tree_w12_gb300 import build
+    build.build()
+    import speculative_decoding_tree_w12_gb300 as m
+    m.lib()
+    return m
+
+
+def busy(stream):
+    """Some milliseconds' work in front of what comes next there."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(20_000_000)
+
+
+def freed(nbytes):
+    """The address of a block of the current stream's that has just become free."""
+    t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    at = t.data_ptr()
+    del t
+    again = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    assert again.data_ptr() == at          # (the next one would get it)
+    del again
+    return at
+
+
+def overlap(t, at, nbytes):
+    return t.data_ptr() < at + nbytes and at < t.data_ptr() + t.numel() * t.element_size()
+
+
+@pytest.fixture
+def side():
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    s = torch.cuda.Stream()
+    yield s
+    torch.cuda.synchronize()
+
+
+def case(w12):
+    c = Case(w12, [1500], 4, 4, seed=1)
+    need = int(w12.lib().w12_gdn_scratch_bytes(4, c.T))
+    assert need > 1 << 20
+    return c, need
+
+
+def test_scratch_is_not_the_current_streams(w12, side):
+    c, need = case(w12)
+    want, state = c.run(w12)
+    c.rows = w12.GdnRows(c.rows.q, c.rows.k, c.rows.v, c.rows.alpha, c.rows.beta)
+    S0, out, mine = c.S0.cuda(), torch.empty_like(want), torch.empty_like(state)
+    side.wait_stream(torch.cuda.current_stream())
+    at = freed(need)
+    w12.w12_gdn_prefill(c.rows, c.row_off, c.ws, S0=S0, state=mine, out=out, stream=side)
+    assert not overlap(c.rows.scratch, at, need)
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(mine, state)
+
+
+@pytest.mark.parametrize("first_on_current", [False, True])
+def test_scratch_outlives_its_rows(w12, side, first_on_current):
+    c, need = case(w12)
+    want, state = c.run(w12)
+    S0, out, mine = c.S0.cuda(), torch.empty_like(want), torch.empty_like(state)
+    if not first_on_current:
+        c.rows = w12.GdnRows(c.rows.q, c.rows.k, c.rows.v, c.rows.alpha, c.rows.beta)
+    side.wait_stream(torch.cuda.current_stream())
+    busy(side)
+    rows, kept = c.rows, (c.rows.q, c.rows.k, c.rows.v, c.rows.alpha, c.rows.beta)
+    c.rows = None
+    w12.w12_gdn_prefill(rows, c.row_off, c.ws, S0=S0, state=mine, out=out, stream=side)
+    at = rows.scratch.data_ptr()
+    del rows
+    other = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert not any(overlap(t, at, need) for t in other)
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(mine, state) and c.ws.status() == 0
+    del kept
+
+
+def norms(w12, stream):
+    g = torch.Generator().manual_seed(2)
+    new = lambda *s: torch.randn(s, generator=g)
+    o, w, h, y = new(300, 4, D).cuda(), new(D).bfloat16().cuda(), new(300, 512).cuda(), new(300, 512).bfloat16().cuda()
+    pre = new(512).bfloat16().cuda()
+    torch.cuda.synchronize()
+    return o, w, h, y, pre
+
+
+def test_outputs_are_not_the_current_streams(w12, side):
+    """What the calls make where the caller passes no output, while blocks of the same sizes have just been freed on the current
+    stream; and it is not the current stream's again while the call still runs."""
+    c, _ = case(w12)
+    o, w, h, y, pre = norms(w12, side)
+    step = Case(w12, [1] * 40, 4, 4, seed=3)
+    S0, S1 = c.S0.cuda(), step.S0.cuda()
+    torch.cuda.synchronize()
+    calls = [lambda **k: w12.w12_gdn_prefill(c.rows, c.row_off, c.ws, S0=S0, **k), lambda **k: w12.w12_gdn_step(step.rows, S0=S1, **k),
+             lambda **k: (w12.w12_gdn_norm(o, w, **k),), lambda **k: w12.w12_block_norm(h, y, pre=pre, **k)]
+    for call in calls:
+        want = [t.clone() for t in call()]
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        sizes = [t.numel() * t.element_size() for t in want]
+        blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+        at = [b.data_ptr() for b in blocks]
+        del blocks
+        busy(side)
+        got = call(stream=side)
+        for t in got:
+            assert not any(overlap(t, a, n) for a, n in zip(at, sizes))
+        for t, ref in zip(got, want):
+            torch.cuda.current_stream().wait_stream(side)
+            assert torch.equal(t, ref)
+        busy(side)
+        got = call(stream=side)
+        where = [(t.data_ptr(), n) for t, n in zip(got, sizes)]
+        del got, t
+        other = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+        assert not any(overlap(t, *w_) for t in other for w_ in where)
+        del other
+        torch.cuda.synchronize()
+
+
+def test_the_current_stream_named(w12, side):
+    """stream= the current one is as no stream."""
+    c, _ = case(w12)
+    want, state = c.run(w12)
+    with torch.cuda.stream(side):
+        out, mine = w12.w12_gdn_prefill(c.rows, c.row_off, c.ws, S0=c.S0.cuda(), stream=torch.cuda.current_stream())
+        assert torch.equal(out, want) and torch.equal(mine, state)
