@@ -775,15 +775,26 @@ class GdnRowsC(C.Structure):
                 ("scratch_bytes", C.c_size_t)]
 
 
+class GdnScratch:
+    """Device buffer for ``w12_gdn_prefill`` on rows of up to n_rows tokens and n_heads heads (20 MB at most), for several
+    layers' ``GdnRows`` whose calls run in order."""
+
+    def __init__(self, n_heads: int, n_rows: int, device="cuda"):
+        torch = _runtime()
+        self.nbytes = int(lib().w12_gdn_scratch_bytes(int(n_heads), int(n_rows)))
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.streams = set()                     # on which it has been used
+
+
 class GdnRows:
     """A recurrent layer's token rows: q and k (bfloat16 [T][n_qk_heads * 128]),
     v (bfloat16 [T][H * 128]; slices of a fused row are fine), gates alpha and
     write strengths beta (float32 [T][H]).  Value head h reads query/key head
     h // (H // n_qk_heads).  The tensors stay the caller's.
-    Holds the scratch of ``w12_gdn_prefill``; one object's calls of it run in order, and a captured one needs the object
-    for as long as its graph is replayed."""
+    Holds the scratch of ``w12_gdn_prefill``, its own or one that other layers' rows share; the calls that use one
+    run in order, and a captured call needs the object for as long as its graph is replayed."""
 
-    def __init__(self, q, k, v, alpha, beta):
+    def __init__(self, q, k, v, alpha, beta, scratch: Optional[GdnScratch] = None):
         torch = _runtime()
         lib()
         _want(alpha, torch.float32, (None, None), "alpha")
@@ -800,8 +811,14 @@ class GdnRows:
         (qa, qs), (ka, ks), (va, vs) = (_rows(t, T, w, n, self.dev) for t, w, n in
                                         ((q, q.shape[1], "q"), (k, q.shape[1], "k"), (v, H * 128, "v")))
         self.c = GdnRowsC(H, q.shape[1] // 128, 128, T, qa, ka, va, qs, ks, vs, alpha.data_ptr(), beta.data_ptr(), None, 0)
-        self.scratch = None                      # for w12_gdn_prefill, made by its first call
-        self._streams = set()                    # on which it has been used
+        self.scratch, self._streams = None, set()   # for w12_gdn_prefill, made by its first call; on which it has been used
+        if scratch is not None:
+            need = int(_lib.w12_gdn_scratch_bytes(self.H, self.T))
+            if scratch.nbytes < need or scratch.buf.get_device() != self.dev:
+                raise ValueError(f"scratch: {need} bytes on cuda:{self.dev} wanted, got {scratch.nbytes} on {scratch.buf.device}")
+            self.scratch, self._streams = scratch.buf, scratch.streams
+            if scratch.nbytes:
+                self.c.scratch, self.c.scratch_bytes = scratch.buf.data_ptr(), scratch.nbytes
         self.ref = C.byref(self.c)
 
     def _scratch_on(self, st, stream):

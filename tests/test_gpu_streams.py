@@ -143,3 +143,20 @@ def test_the_current_stream_named(w12, side):
     with torch.cuda.stream(side):
         out, mine = w12.w12_gdn_prefill(c.rows, c.row_off, c.ws, S0=c.S0.cuda(), stream=torch.cuda.current_stream())
         assert torch.equal(out, want) and torch.equal(mine, state)
+
+
+def test_layers_share_a_scratch(w12, side):
+    """Two layers' calls in a row, several times over, with one scratch between them."""
+    cases = [case(w12)[0], Case(w12, [1100, 1300], 2, 1, seed=5)]
+    want = [c.run(w12) for c in cases]
+    scratch = w12.GdnScratch(4, 2400)
+    for c in cases:
+        c.rows = w12.GdnRows(c.rows.q, c.rows.k, c.rows.v, c.rows.alpha, c.rows.beta, scratch=scratch)
+    S0 = [c.S0.cuda() for c in cases]
+    torch.cuda.synchronize()
+    got = [[w12.w12_gdn_prefill(c.rows, c.row_off, c.ws, S0=s, stream=side) for c, s in zip(cases, S0)] for _ in range(3)]
+    side.synchronize()
+    for pair in got:
+        for (o, s), (o_ref, s_ref), c in zip(pair, want, cases):
+            assert c.ws.status() == 0 and c.rows.scratch is scratch.buf
+            assert torch.equal(o[c.off[0]:c.off[-1]], o_ref[c.off[0]:c.off[-1]]) and torch.equal(s, s_ref)
