@@ -192,16 +192,32 @@ def _st_on(dev, stream) -> int:
     return _raw_stream() if stream is None else stream.cuda_stream
 
 
-def _empty(shape, dtype, device, stream):
-    """torch.empty for a call on `stream` (None: the current one).  Memory of the current stream may still be in use there
-    when another stream's kernel writes it, so it is that stream's own; and since its reader may be on the current one,
-    it is nobody else's before both have passed its end."""
+def _under(stream, make):
+    """make() -> tensors for a call on `stream` (None: the current one).  Memory of the current stream may still be in use there
+    when another stream's kernel writes it, so it is that stream's own (what fills it runs there too); and since its
+    reader may be on the current one, it is nobody else's before both have passed its end."""
+    torch = _runtime()
     if stream is None or stream.cuda_stream == _raw_stream():
-        return _torch.empty(shape, dtype=dtype, device=device)
-    with _torch.cuda.stream(stream):
-        t = _torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(_torch.cuda.current_stream(t.device))
-    return t
+        return make()
+    with torch.cuda.stream(stream):
+        made = make()
+    for t in made.tensors() if isinstance(made, DeviceTree) else (made,):
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return made
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call on `stream`."""
+    if stream is None:
+        return _runtime().empty(shape, dtype=dtype, device=device)
+    return _under(stream, lambda: _torch.empty(shape, dtype=dtype, device=device))
+
+
+def _used_on(streams, st, stream, scratch):
+    """A call on `stream` (its handle: st) uses scratch that its object holds: the allocator learns of every such stream."""
+    if scratch.numel() and scratch.is_cuda:
+        scratch.record_stream(_torch.cuda.current_stream() if stream is None else stream)
+    streams.add(st)
 
 
 def _dp(t) -> Optional[int]:
@@ -294,7 +310,7 @@ class Workspace:
 def w12_unpack(w: DeviceWeight, out=None, stream=None):
     import torch
     if out is None:
-        out = torch.empty((w.n, w.k), dtype=torch.bfloat16, device=w.rec.device)
+        out = _empty((w.n, w.k), torch.bfloat16, w.rec.device, stream)
     _check(lib().w12_unpack(C.byref(w.c), C.c_void_p(out.data_ptr()), _stream(stream)), "w12_unpack")
     return out
 
@@ -316,7 +332,7 @@ def w12_gemm(w: DeviceWeight, x, ws: Workspace, y=None, stream=None, quick: bool
     import torch
     R = x.shape[0]
     if y is None:
-        y = torch.empty((R, w.n), dtype=torch.bfloat16, device=x.device)
+        y = _empty((R, w.n), torch.bfloat16, x.device, stream)
     fn, name = (lib().w12_gemm_q, "w12_gemm_q") if quick else (lib().w12_gemm, "w12_gemm")
     _check(fn(C.byref(w.c), C.c_void_p(x.data_ptr()), R, C.c_void_p(y.data_ptr()), ws.ptr, ws.nbytes,
               _stream(stream)), name)
@@ -330,7 +346,7 @@ def w12_lmhead_argmax(head: DeviceWeight, h, ws: Workspace, argmax=None, maxlogi
     import torch
     R = h.shape[0]
     if argmax is None:
-        argmax = torch.empty(R, dtype=torch.int32, device=h.device)
+        argmax = _empty((R,), torch.int32, h.device, stream)
     fn, name = (lib().w12_lmhead_argmax_q, "w12_lmhead_argmax_q") if quick else \
         (lib().w12_lmhead_argmax, "w12_lmhead_argmax")
     _check(fn(C.byref(head.c), C.c_void_p(h.data_ptr()), R, C.c_void_p(argmax.data_ptr()),
@@ -344,7 +360,7 @@ def w12_head_cert_norms(head: DeviceWeight, out=None, stream=None):
     [2][n] on the device (load time, for the certified head)."""
     import torch
     if out is None:
-        out = torch.empty((2, head.n), dtype=torch.float32, device="cuda")
+        out = _empty((2, head.n), torch.float32, "cuda", stream)
     _check(lib().w12_head_cert_norms(C.byref(head.c), C.c_void_p(out.data_ptr()), _stream(stream)),
            "w12_head_cert_norms")
     return out
@@ -373,7 +389,7 @@ def w12_lmhead_argmax_certified(head: DeviceWeight, norms, h, ws: Workspace, cws
     import torch
     R = h.shape[0]
     if argmax is None:
-        argmax = torch.empty(R, dtype=torch.int32, device=h.device)
+        argmax = _empty((R,), torch.int32, h.device, stream)
     _check(lib().w12_lmhead_argmax_certified(C.byref(head.c), C.c_void_p(norms.data_ptr()), C.c_void_p(h.data_ptr()),
                                              R, C.c_void_p(argmax.data_ptr()),
                                              C.c_void_p(_dp(maxlogit)) if maxlogit is not None else None,
@@ -405,8 +421,10 @@ class DeviceTree:
         self.score = z(torch.float32, budget)
         self.req_row_off = z(torch.int32, n_req + 1)
         self.n_req, self.dev = int(n_req), self.parent.get_device()
-        self.c = TreeC(0, *(t.data_ptr() for t in (self.parent, self.token, self.depth, self.req, self.score,
-                                                    self.rank, self.req_row_off)))
+        self.c = TreeC(0, *(t.data_ptr() for t in self.tensors()))
+
+    def tensors(self):
+        return self.parent, self.token, self.depth, self.req, self.score, self.rank, self.req_row_off
 
     @classmethod
     def from_arrays(cls, parent, depth, req, req_row_off, token=None):
@@ -441,7 +459,7 @@ class DeviceTree:
 def w12_tree_build(lat: DeviceLattice, budget: int, ws: Workspace, tree: Optional[DeviceTree] = None,
                    stream=None) -> DeviceTree:
     if tree is None:
-        tree = DeviceTree(budget, lat.n_req, device=lat.root_tok.device)
+        tree = _under(stream, lambda: DeviceTree(budget, lat.n_req, device=lat.root_tok.device))
     _check(lib().w12_tree_build(C.byref(lat.c), int(budget), C.byref(tree.c), ws.ptr, ws.nbytes, _stream(stream)),
            "w12_tree_build")
     return tree
@@ -451,9 +469,9 @@ def w12_tree_accept(tree: DeviceTree, n_req: int, p_max: int, argmax, acc_tok=No
                     stream=None):
     import torch
     dev = argmax.device
-    acc_tok = acc_tok if acc_tok is not None else torch.empty((n_req, p_max + 1), dtype=torch.int32, device=dev)
-    acc_len = acc_len if acc_len is not None else torch.empty(n_req, dtype=torch.int32, device=dev)
-    acc_node = acc_node if acc_node is not None else torch.empty(n_req, dtype=torch.int32, device=dev)
+    acc_tok = acc_tok if acc_tok is not None else _empty((n_req, p_max + 1), torch.int32, dev, stream)
+    acc_len = acc_len if acc_len is not None else _empty((n_req,), torch.int32, dev, stream)
+    acc_node = acc_node if acc_node is not None else _empty((n_req,), torch.int32, dev, stream)
     _check(lib().w12_tree_accept(C.byref(tree.c), n_req, p_max, C.c_void_p(argmax.data_ptr()),
                                  C.c_void_p(acc_tok.data_ptr()), C.c_void_p(acc_len.data_ptr()),
                                  C.c_void_p(acc_node.data_ptr()), _stream(stream)), "w12_tree_accept")
@@ -510,7 +528,7 @@ def w12_tlv_splice(t1: DeviceTree, c_tok, c_len, c_node, m_host, t2: DeviceTree,
     n_req = len(m)
     p1_max = int(c_tok.shape[1]) - 1
     if out is None:
-        out = DeviceTree(max(1, int(m.sum()) + t2.R), n_req, device=c_tok.device)
+        out = _under(stream, lambda: DeviceTree(max(1, int(m.sum()) + t2.R), n_req, device=c_tok.device))
     _check(lib().w12_tlv_splice(C.byref(t1.c), C.c_void_p(c_tok.data_ptr()), C.c_void_p(c_len.data_ptr()),
                                 C.c_void_p(c_node.data_ptr()), n_req, p1_max, _np(m), C.byref(t2.c),
                                 C.byref(out.c), ws.ptr, ws.nbytes, _stream(stream)), "w12_tlv_splice")
@@ -541,7 +559,7 @@ def w12_gdn_tree_verify(layer: GdnLayer, tree: DeviceTree, n_req: int, ws: Works
                         out=None, stream=None):
     import torch
     if out is None:
-        out = torch.empty((tree.R, layer.H, layer.d), dtype=torch.float32, device=layer.q.device)
+        out = _empty((tree.R, layer.H, layer.d), torch.float32, layer.q.device, stream)
     _check(lib().w12_gdn_tree_verify(C.byref(layer.c), C.byref(tree.c), int(n_req), int(method),
                                      C.c_void_p(out.data_ptr()), ws.ptr, ws.nbytes, _stream(stream)),
            "w12_gdn_tree_verify")
@@ -551,7 +569,7 @@ def w12_gdn_tree_verify(layer: GdnLayer, tree: DeviceTree, n_req: int, ws: Works
 def w12_gdn_commit(layer: GdnLayer, tree: DeviceTree, n_req: int, acc_node, ws: Workspace, state=None, stream=None):
     import torch
     if state is None:
-        state = torch.empty_like(layer.S0)
+        state = _empty(layer.S0.shape, torch.float32, layer.S0.device, stream)
     _check(lib().w12_gdn_commit(C.byref(layer.c), C.byref(tree.c), int(n_req), C.c_void_p(acc_node.data_ptr()),
                                 C.c_void_p(state.data_ptr()), ws.ptr, ws.nbytes, _stream(stream)), "w12_gdn_commit")
     return state
@@ -561,9 +579,9 @@ def w12_gdn_wy_verify(layer: GdnLayer, tree: DeviceTree, n_req: int, ws: Workspa
     """WY-form outputs and the WY vectors u (both float32 [R][H][d])."""
     import torch
     if out is None:
-        out = torch.empty((tree.R, layer.H, layer.d), dtype=torch.float32, device=layer.q.device)
+        out = _empty((tree.R, layer.H, layer.d), torch.float32, layer.q.device, stream)
     if u is None:
-        u = torch.empty((tree.R, layer.H, layer.d), dtype=torch.float32, device=layer.q.device)
+        u = _empty((tree.R, layer.H, layer.d), torch.float32, layer.q.device, stream)
     _check(lib().w12_gdn_wy_verify(C.byref(layer.c), C.byref(tree.c), int(n_req), C.c_void_p(out.data_ptr()),
                                    C.c_void_p(u.data_ptr()), ws.ptr, ws.nbytes, _stream(stream)), "w12_gdn_wy_verify")
     return out, u
@@ -574,7 +592,7 @@ def w12_gdn_wy_commit(layer: GdnLayer, tree: DeviceTree, n_req: int, acc_node, u
     """The committed states from the WY vectors u of w12_gdn_wy_verify."""
     import torch
     if state is None:
-        state = torch.empty_like(layer.S0)
+        state = _empty(layer.S0.shape, torch.float32, layer.S0.device, stream)
     _check(lib().w12_gdn_wy_commit(C.byref(layer.c), C.byref(tree.c), int(n_req), C.c_void_p(acc_node.data_ptr()),
                                    C.c_void_p(u.data_ptr()), C.c_void_p(state.data_ptr()), ws.ptr, ws.nbytes,
                                    _stream(stream)), "w12_gdn_wy_commit")
@@ -751,7 +769,7 @@ def w12_tree_attention(cache: KvCache, rope: Optional[Rope], tree: DeviceTree, n
             (rope is not None and rope.dev != dev):
         _refuse(dev, n_req, tree, rope, ws, aws)
     if out is None:
-        out = _torch.empty((R, Hq, d), dtype=_torch.bfloat16, device=q.device)
+        out = _empty((R, Hq, d), _torch.bfloat16, q.device, stream)
     elif out.shape[0] < R or out.shape[1:] != (Hq, d) or out.dtype is not _torch.bfloat16 or not out.is_contiguous() \
             or out.get_device() != dev:
         raise ValueError(f"out: contiguous bfloat16 [{R}][{Hq}][{d}] on cuda:{dev} wanted")
@@ -829,9 +847,7 @@ class GdnRows:
             self.scratch = _empty((nbytes,), _torch.uint8, self.alpha.device, stream)
             if nbytes:
                 self.c.scratch, self.c.scratch_bytes = self.scratch.data_ptr(), nbytes
-        elif self.scratch.numel():
-            self.scratch.record_stream(_torch.cuda.current_stream() if stream is None else stream)
-        self._streams.add(st)
+        _used_on(self._streams, st, stream, self.scratch)
 
     def _buffers(self, n_req, S0, state, out, stream):
         """The calls' state and output tensors, made or checked."""
@@ -1015,7 +1031,7 @@ class SampleRows:
         nbytes = int(lib().w12_sample_scratch_bytes(rows, V))
         if nbytes == 0:
             raise W12Error(W12_E_UNSUPPORTED, "w12_sample_scratch_bytes")
-        self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=logits.device)
+        self.scratch, self._streams = torch.empty(nbytes, dtype=torch.uint8, device=logits.device), set()
         self.c = SamplingC(logits.data_ptr(), int(logits.dtype == torch.float32), V, row(logits), _dp(temperature),
                            _dp(draft_p), row(draft_p) if draft_p is not None else 0, _dp(u_accept), _dp(u_sample),
                            self.scratch.data_ptr(), rows)
@@ -1039,9 +1055,12 @@ def w12_tree_sample(dist: SampleRows, tree: DeviceTree, n_req: int, ws: Workspac
     dev = dist._fits(tree, n_req, ws)
     R = tree.c.R
     if row_tok is None:
-        row_tok = _torch.empty(R, dtype=_torch.int32, device=dist.logits.device)
+        row_tok = _empty((R,), _torch.int32, dist.logits.device, stream)
+    st = _st(stream)
+    if st not in dist._streams:
+        _used_on(dist._streams, st, stream, dist.scratch)
     s = _lib.w12_tree_sample(dist.ref, C.byref(tree.c), n_req, _ints(row_tok, R, "row_tok", dev), _floats(row_logp, R, dev),
-                             ws.addr, ws.nbytes, _st(stream))
+                             ws.addr, ws.nbytes, st)
     if s:
         raise W12Error(s, "w12_tree_sample")
     return row_tok
@@ -1062,7 +1081,7 @@ def w12_tree_verify_sampled(dist: SampleRows, tree: DeviceTree, n_req: int, p_ma
     dev = dist._fits(tree, n_req, ws)
     R = tree.c.R
     if row_tok is None or acc_tok is None or acc_len is None or acc_node is None:
-        new = lambda *s: _torch.empty(s, dtype=_torch.int32, device=dist.logits.device)
+        new = lambda *s: _empty(s, _torch.int32, dist.logits.device, stream)
         row_tok = row_tok if row_tok is not None else new(R)
         acc_tok = acc_tok if acc_tok is not None else new(n_req, p_max + 1)
         acc_len = acc_len if acc_len is not None else new(n_req)
@@ -1070,9 +1089,12 @@ def w12_tree_verify_sampled(dist: SampleRows, tree: DeviceTree, n_req: int, p_ma
     if acc_tok.shape != (n_req, p_max + 1) or acc_tok.dtype is not _torch.int32 or not acc_tok.is_contiguous() \
             or acc_tok.get_device() != dev:
         raise ValueError(f"acc_tok: contiguous int32 [{n_req}][{p_max + 1}] on cuda:{dev} wanted")
+    st = _st(stream)
+    if st not in dist._streams:
+        _used_on(dist._streams, st, stream, dist.scratch)
     s = _lib.w12_tree_verify_sampled(dist.ref, C.byref(tree.c), n_req, p_max, _ints(row_tok, R, "row_tok", dev),
                                      _floats(row_logp, R, dev), acc_tok.data_ptr(), _ints(acc_len, n_req, "acc_len", dev),
-                                     _ints(acc_node, n_req, "acc_node", dev), ws.addr, ws.nbytes, _st(stream))
+                                     _ints(acc_node, n_req, "acc_node", dev), ws.addr, ws.nbytes, st)
     if s:
         raise W12Error(s, "w12_tree_verify_sampled")
     return acc_tok, acc_len, acc_node

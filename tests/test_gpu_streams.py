@@ -160,3 +160,84 @@ def test_layers_share_a_scratch(w12, side):
         for (o, s), (o_ref, s_ref), c in zip(pair, want, cases):
             assert c.ws.status() == 0 and c.rows.scratch is scratch.buf
             assert torch.equal(o[c.off[0]:c.off[-1]], o_ref[c.off[0]:c.off[-1]]) and torch.equal(s, s_ref)
+
+
+def older_calls(w12):
+    """The other calls that make their outputs, on small inputs: name -> (call, its outputs' tensors)."""
+    from speculative_decoding_tree_w12_gb300 import synth
+    from test_binding_devices import parts
+
+    w = synth.scaled(synth.WORKLOADS["tiny"], n_req=3, positions=(2, 4, 6), budget=12, n_cand=16, hit_rate=0.9)
+    lat = w12.DeviceLattice(synth.lattice(w, 3))
+    ws = w12.Workspace(12, 1024, 1024, 3)
+    tree = w12.w12_tree_build(lat, w.budget, ws)
+    R = tree.R
+    g = torch.Generator().manual_seed(4)
+    bits = lambda *s: torch.randn(s, generator=g).bfloat16().view(torch.int16).numpy().view(np.uint16)
+    lin, head = (w12.DeviceWeight(w12.w12_pack(bits(1024, 512))) for _ in range(2))
+    x = torch.randn(R, 512, generator=g).bfloat16().cuda()
+    argmax = torch.randint(0, 16, (R,), generator=g, dtype=torch.int32).cuda()
+    norms = w12.w12_head_cert_norms(head)
+    cws = w12.CertWorkspace(R, 1024)
+    xg = synth.gdn_inputs(R, 3, 2, 128, seed=4)
+    dev = lambda a: torch.from_numpy(a.view(np.int16)).view(torch.bfloat16).cuda()
+    layer = w12.GdnLayer(torch.from_numpy(xg.S0).cuda(), dev(xg.q), dev(xg.k), dev(xg.v), torch.from_numpy(xg.alpha).cuda(),
+                         torch.from_numpy(xg.beta).cuda())
+    node = (tree.req_row_off[1:] - 1).contiguous()
+    _, u = w12.w12_gdn_wy_verify(layer, tree, 3, ws)
+    a = parts(w12, "cuda")
+    fields = lambda t: (t.parent[:R], t.token[:R], t.depth[:R], t.req[:R], t.score[:R], t.rank[:R], t.req_row_off)
+    torch.cuda.synchronize()
+    return {
+        "unpack": lambda **k: (w12.w12_unpack(lin, **k),),
+        "gemm": lambda **k: (w12.w12_gemm(lin, x, ws, **k),),
+        "argmax": lambda **k: (w12.w12_lmhead_argmax(head, x, ws, **k),),
+        "norms": lambda **k: (w12.w12_head_cert_norms(head, **k),),
+        "certified": lambda **k: (w12.w12_lmhead_argmax_certified(head, norms, x, ws, cws, **k),),
+        "tree": lambda **k: fields(w12.w12_tree_build(lat, w.budget, ws, **k)),
+        "accept": lambda **k: w12.w12_tree_accept(tree, 3, w.p_max, argmax, **k)[1:],
+        "gdn verify": lambda **k: (w12.w12_gdn_tree_verify(layer, tree, 3, ws, **k),),
+        "gdn commit": lambda **k: (w12.w12_gdn_commit(layer, tree, 3, node, ws, **k),),
+        "wy verify": lambda **k: w12.w12_gdn_wy_verify(layer, tree, 3, ws, **k),
+        "wy commit": lambda **k: (w12.w12_gdn_wy_commit(layer, tree, 3, node, u, ws, **k),),
+        "attention": lambda **k: (w12.w12_tree_attention(a["cache"], a["rope"], a["tree"], 2, a["q"], a["k"], a["v"], a["ws"], a["aws"], **k),),
+        "sample": lambda **k: (w12.w12_tree_sample(a["dist"], a["tree"], 2, a["ws"], **k),),
+        "verify sampled": lambda **k: w12.w12_tree_verify_sampled(a["dist"], a["tree"], 2, 2, a["ws"], **k)[1:],
+    }
+
+
+def test_outputs_of_the_other_calls(w12, side):
+    for name, call in older_calls(w12).items():
+        want = [t.clone() for t in call()]
+        torch.cuda.synchronize()
+        sizes = [t.untyped_storage().nbytes() for t in want]
+        blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+        at = [(b.data_ptr(), b.numel()) for b in blocks]
+        del blocks
+        # the current stream is behind: what it does to memory of its own comes after the call
+        busy(torch.cuda.current_stream())
+        got = call(stream=side)
+        for t in got:
+            assert not any(overlap(t, *b) for b in at), name
+        torch.cuda.synchronize()
+        for t, ref in zip(got, want):
+            assert torch.equal(t, ref), name
+
+
+def test_sampling_scratch_outlives_its_rows(w12, side):
+    from test_binding_devices import parts
+    a = parts(w12, "cuda")
+    logits, u = torch.randn(4, 70000, device="cuda"), torch.rand(4, device="cuda")
+    make = lambda: w12.SampleRows(logits, u)
+    want = w12.w12_tree_sample(make(), a["tree"], 2, a["ws"]).clone()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    dist = make()
+    at, n = dist.scratch.data_ptr(), dist.scratch.numel()
+    busy(side)
+    tok = w12.w12_tree_sample(dist, a["tree"], 2, a["ws"], stream=side)
+    del dist
+    other = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert not any(overlap(t, at, n) for t in other)
+    side.synchronize()
+    assert torch.equal(tok, want)
