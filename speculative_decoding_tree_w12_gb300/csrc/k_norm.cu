@@ -52,6 +52,19 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
     return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
 }
 
+// z / (1 + exp(-z)), for z < 0 as z exp(z) / (1 + exp(z)): 1 + exp(-z) leaves FP32's range at z = -88.7.  exp(-|z|) is held 2^32 times
+// as large until the last product, so that it has all its bits where the result has.  Off by (8 + 0.45 |z|) 2^-23 at most: 2^x by 2
+// units, the reciprocal by 1, log2(e) by 0.12 |z|, the exponent by half its last place (4 units up to 16, 22 up to 128), products by 2.
+// That is 2^-17 of a result where the gate closes, in front of a rounding of 2^-9.  (16384 rows of 32 heads 74.9 us; 78.5 with the gate behind
+// the norm and 82.4 in front of it with an exponential that is right to a bit or two.)
+__device__ __forceinline__ float silu(float z)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(fabsf(z), -1.44269504f, 32.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, 0x1p-32f, 1.f)));
+    return z < 0.f ? (z * e) * (r * 0x1p-32f) : z * r;
+}
+
 // ---------------------------------------------------------------------------
 // outputs of a recurrent layer
 // ---------------------------------------------------------------------------
@@ -95,9 +108,8 @@ __global__ void __launch_bounds__(kNormThreads) k_gdn_norm(const GdnNormParams p
     if (kGate) unpack8(*reinterpret_cast<const uint4 *>(p.z + row * p.z_stride + head * kHead + c), g);
     unpack8(*reinterpret_cast<const uint4 *>(p.w + c), w);
     if (kGate) {
-        // the machine's 2^x and reciprocal (some 2^-21 off) in front of a result of 2^-9
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = __fdividef(g[i], 1.f + __expf(-g[i]));
+        for (int i = 0; i < 8; ++i) g[i] = silu(g[i]);
     }
     float sum = 0.f;
 #pragma unroll
