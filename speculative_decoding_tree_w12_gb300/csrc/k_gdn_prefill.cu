@@ -611,7 +611,6 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
 
         // U's pieces for A, over S's last (S q is there)
         wait(s.done_u, par);
-        wait(s.have_us[0], par);                  // (the state warps' way goes first: sixteen prompts of 4096 tokens 736 us without, 728 with)
 #pragma unroll 1
         for (int q = 0; q < 2; ++q) {
             float z[16];
