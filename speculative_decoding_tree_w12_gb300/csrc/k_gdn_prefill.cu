@@ -28,12 +28,13 @@
 //    blocks of 16, whose columns are solved in registers, and A,
 //  * inverse warps (20..23): M, the blocks below those from them,
 //  * warp 24 issues the products with the state, warp 25 the copies by TMA, warps 26 and 27 make M's pieces.
-// A chunk takes 4.2 to 4.4 us (8,000 to 8,500 cycles) however many there are: sixteen prompts of up to 8192 tokens x 32 heads
-// 1417 us, 2.5 times what their bytes take at the measured copy bandwidth.  That is the way through the steps above, on a full
-// machine: S's pieces 2,200 cycles (three BF16 pieces take 11 cycles of a scheduler for two values of 32 lanes), what of
-// S k is left then 950, X 1,150, M X 800, U's pieces 1,450, U K 700, S' 700; each with some 200 for its hand-over between warps.  The schedulers issue in 58 % of the cycles, the tensor cores work in 32 %.  With fewer warps of more columns each it took 1.2 times as long.
-// The products are issued in rolled loops and the code is kept short: straight-line code of a few times this length spent half
-// its time on its own way in.  A new pair costs 3 us more than its chunks, 5 where a state is read.
+// A chunk takes 4.2 to 4.4 us (8,100 to 8,500 cycles) however many there are: sixteen prompts of up to 8192 tokens x 32 heads
+// 1420 us, 2.5 times what their bytes take at the measured copy bandwidth.  That is the way through the steps above, each with its
+// hand-over to the next one's warps, on a full machine: S's pieces 2,000 cycles (three BF16 pieces take 11 cycles of a scheduler for
+// two values of 32 lanes), what of S k is left then 850, X 1,000, M X 1,300, U's pieces 1,500, U K 700, S' 1,000.  The schedulers
+// issue in 56 % of the cycles, the tensor cores work in 38 %.
+// Most products are issued in rolled loops and the code is kept short: straight-line code of a few times this length spent half
+// its time on its own way in.  A new pair costs 2.2 us more than its chunks, 4.5 where a state is read.
 // Every wait is bounded; when one has run out no state that what did not come is part of is written.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -139,10 +140,9 @@ constexpr uint32_t kKqBytes = sizeof(PrefillShared::KQ) / kStages, kVBytes = siz
 //  * kAhead: the first w pieces as they are, and Q and P of the j segments of w pieces behind them, noted after every piece,
 //  * k_gdn_join: the states in front of every piece but the first w from those,
 //  * kPieces: those pieces, now with their outputs.
-// That takes w + 1 pieces' time of n, and (2 j + 1) and (j w + 1) CTAs a pair (one of 4096 tokens, 4 heads: 286 us in one
-// part a head, 85 cut; of 32768 tokens, 32 heads: 2281 and 1280).  The launches overlap: each begins where SMs are left, and waits for the
-// one before it only for what that wrote (3 to 6 us of those).  All three as one launch whose CTAs wait for one another's
-// counts were slower (4096 tokens, 4 heads: 120 to 130 us), the join being short of registers and of shared memory there.
+// That takes w + 1 pieces' time of n, and (2 j + 1) and (j w + 1) CTAs a pair (one of 4096 tokens, 4 heads: 280 us in one
+// part a head, 83 cut; of 32768 tokens, 32 heads: 2200 and 1250).  The launches overlap: each begins where SMs are left, and waits for the
+// one before it only for what that wrote.
 enum Mode : int32_t { kWhole, kAhead, kPieces };
 
 struct SplitParams {
@@ -154,8 +154,8 @@ struct SplitParams {
 
 // Segments of a request of nc chunks.  The join takes a product of 1.1 us for each piece of them, so no more than pay for
 // theirs; and it and one more launch some 30 us, seven chunks' time, which the j w pieces that run beside the others have to
-// save.  (One request of 32 heads, j = 1: 14 chunks 74 us whole, 79 cut, 16 chunks 83 and 83, 20 chunks 99 and 95; of 16 heads: 8 chunks
-// 48 and 52, 10 chunks 56 and 56, 12 chunks 65 and 64.)
+// save.  (One request of 32 heads, j = 1: 14 chunks 71 us whole, 76 cut, 16 chunks 80 and 80, 20 chunks 97 and 92; of 16 heads: 8
+// chunks 45 and 50, 10 chunks 54 and 54, 12 chunks 62 and 61.)
 __host__ __device__ inline int split_segments(int nc, int j, int w)
 {
     while (j > 0 && (j * j > 2 * nc || (j + 1) * w + 1 > nc)) --j;
@@ -338,7 +338,7 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane)
 // waits together (the time limit and 16 polls for every chunk), a poll sleeping up to kWaitSleepNs.  When that has run out no wait
 // lasts any more, so every role runs to its end.  What is made of what did not come is marked before it is signalled, so nothing
 // that it is part of is stored.  What is read on the way may be old or half written: so no address is made of it that is not checked
-// where it is used.  (Marked at once, in every wait: sixteen prompts of 1024 tokens x 32 heads 201 us, 190 so.)
+// where it is used.  (Marked at once, in every wait: sixteen prompts of up to 1024 tokens x 32 heads 201 us, 190 so.)
 struct Waits {
     uint32_t left;
 
@@ -406,7 +406,7 @@ struct Part {
 __device__ __forceinline__ int piece_start(const PrefillParams &p, int nc, int j, uint32_t i)
 {
     // In eighths of a piece: the first w pieces are shorter by one, since a chunk with its outputs takes longer than one of Q's or P's (one
-    // request of 32768 tokens, 32 heads: 1388 us with like pieces, 1332 so, 1390 with two eighths).
+    // request of 32768 tokens, 32 heads: 1302 us with like pieces, 1250 so, 1320 with two eighths).
     const uint32_t w = p.split.w, n = 8 * (j * w + 1) + 7 * w, like = (uint32_t)nc / n, at = i < w ? 7 * i : 8 * i - w;
     return (int)(at * like + at * (nc - n * like) / n);
 }
@@ -967,7 +967,7 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
         {
             const uint32_t b = desc_low(smem_u32(s.M[0]));
             // (Straight-line: the state waits for it, and a rolled loop issues a product in 20 cycles, this in 16, as long as it takes.
-            // One prompt of 32768 tokens, 32 heads: 1349 us rolled, 1293 with U A unrolled as well, 1270 so.)
+            // One prompt of 32768 tokens, 32 heads: 1315 us rolled, 1263 with U A straight-line as well, 1253 so.)
 #pragma unroll
             for (int q = 0; q < 6; ++q) pair(kColU, kColX, b, kPairA[q], kPairB[q], (uint32_t)q);
         }
@@ -1117,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5;
     // What comes next waits for this launch's end, in the SMs that are left.  kPieces waits later, where the states in front are read
     // (what else it reads is older than the launches before it), and lets nothing in: the next call's first launch would be
-    // dealt to fewer, busier SMs (one prompt of 2048 tokens x 32 heads, call after call: 126.4 us so, 122.7 without).
+    // dealt to fewer, busier SMs (one prompt of 2048 tokens x 32 heads, call after call: 127 us so, 121 without).
     if (p.split.mode != kPieces) {
         pdl_wait();
         pdl_launch_dependents();
@@ -1430,7 +1430,7 @@ int launch_gdn_prefill(const GdnSeqArgs &a, void *stream)
     p.split.states = reinterpret_cast<float *>(static_cast<uint8_t *>(a.scratch) + kSplitHeader);
     if ((e = run(kAhead, 2 * p.split.j + 1)) != cudaSuccess) return (int)e;
     // Two groups halve P's ways from L2, which bound it where there are many rows; one is the faster where SMs are left.  (Four
-    // requests of 4096 tokens, 4 heads: 130.2 us a call with one group, 128.4 with two; one such request: 93.8 and 107.4.)
+    // requests of up to 4096 tokens, 4 heads: 115 us a call with one group, 113 with two; one such request: 82 and 95.)
     auto join = [&](auto kernel, int groups, size_t bytes) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != cudaSuccess) return e;

@@ -12,7 +12,7 @@
 // written once, sums in FP32 in registers.  x is taken from the FP32 h', not
 // from the value that is stored: one rounding less in every layer.
 //
-// 16384 rows of 32 heads with their gate (537 MB): 74.6 us, 7.2 TB/s.  Between two blocks of 5120 values, 16384 rows: 98.9 us BF16
+// 16384 rows of 32 heads with their gate (537 MB): 74.9 us, 7.2 TB/s.  Between two blocks of 5120 values, 16384 rows: 98.9 us BF16
 // (6.8 TB/s), 148.4 us FP32 with a norm behind the block (6.8); 192 rows 2.4 and 3.8 us, call after call.  (76.7, 99.8, 149.6, 2.75
 // and 4.2 if a launch waits for the one before it to end before it begins.)
 #include <cuda_bf16.h>
