@@ -22,9 +22,9 @@ def w12():
 
 
 def busy(stream):
-    """Some milliseconds' work in front of what comes next there."""
+    """A tenth of a second's work in front of what comes next there."""
     with torch.cuda.stream(stream):
-        torch.cuda._sleep(20_000_000)
+        torch.cuda._sleep(200_000_000)
 
 
 def freed(nbytes):
