@@ -568,11 +568,13 @@ __device__ __forceinline__ void token_warps(const PrefillParams &p, PrefillShare
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[q + j] = e[j] * __uint_as_float((uint32_t)v[j * kD] << 16);
         }
-        uint32_t seen = 0;                        // (of all values, by every lane)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) seen |= __float_as_uint(x[j]);
-        seen = __reduce_or_sync(0xffffffffu, seen);
-        if (lane == 0) mbar_arrive_after(smem_u32(&s.vempty[st]), seen);
+        // (What has been read here and what a copy writes here next meet in different ways to memory, which neither the order of the
+        // program nor the arrival's own keeps apart.)
+        __syncwarp();
+        if (lane == 0) {
+            fence_async_shared();
+            mbar_arrive(smem_u32(&s.vempty[st]));
+        }
         wait(s.done_k, par);
         if (g == impatient) waits.left = 0;
 #pragma unroll

@@ -157,17 +157,6 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// An arrival that gives shared memory back to a copy into it.  What a load from shared memory reads may come after an arrival behind the
-// load has taken effect, the two going different ways, and the copy's bytes come a third; so this one is issued when `seen`, which
-// is made of everything that has been read, is there (both branches are the same arrival).
-__device__ __forceinline__ void mbar_arrive_after(uint32_t bar, uint32_t seen)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0x7f8a5c31;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t"
-        "@!p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar), "r"(seen)
-        : "memory");
-}
-
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -470,7 +459,8 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32_bmn(int M, int N)
     return (1u << 4) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// this thread's shared-memory writes, visible to the tensor cores and the copy engine
+// this thread's shared-memory writes, visible to the tensor cores and the copy engine; and what has been read in
+// front of it, read before the copy engine writes there
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
