@@ -471,7 +471,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_w12_chain(const __grid_constant
                             nb[h] = QV ? make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u)
                                        : *reinterpret_cast<const uint4 *>(rb + w12i::kViewBytes + (h * 128 + c) * 16);
                         if (u == n - 1) {
-                            // the whole pair has been read: hand the slot back
+                            // the whole pair has been read: hand the slot back (the fence: in front of the copy
+                            // that comes there next, which neither the order of the program nor the arrival itself keeps behind the loads)
+                            fence_async_shared();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(bar_rempty + 8 * s);
                         }

@@ -384,7 +384,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_w12_gemm_tc(const __grid_consta
                     for (int h = 0; h < 2; ++h)
                         nb[h] = QV ? make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u)
                                    : *reinterpret_cast<const uint4 *>(rb + w12i::kViewBytes + (h * 128 + c) * 16);
-                    // the record is in registers: hand the slot back to the producer
+                    // the record is in registers: hand the slot back to the producer (the fence: in front of the copy
+                    // that comes there next, which neither the order of the program nor the arrival itself keeps behind the loads)
+                    fence_async_shared();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_rempty + 8 * s);
                     uint32_t a[32];
