@@ -28,13 +28,13 @@
 //    blocks of 16, whose columns are solved in registers, and A,
 //  * inverse warps (20..23): M, the blocks below those from them,
 //  * warp 24 issues the products with the state, warp 25 the copies by TMA, warps 26 and 27 make M's pieces.
-// A chunk takes 4.2 to 4.4 us (8,100 to 8,500 cycles) however many there are: sixteen prompts of up to 8192 tokens x 32 heads
-// 1420 us, 2.5 times what their bytes take at the measured copy bandwidth.  That is the way through the steps above, each with its
-// hand-over to the next one's warps, on a full machine: S's pieces 2,000 cycles (three BF16 pieces take 11 cycles of a scheduler for
-// two values of 32 lanes), what of S k is left then 850, X 1,000, M X 1,300, U's pieces 1,500, U K 700, S' 1,000.  The schedulers
-// issue in 56 % of the cycles, the tensor cores work in 38 %.
+// A chunk takes 4.2 to 4.4 us (8,000 to 8,600 cycles) however many there are: sixteen prompts of up to 8192 tokens x 32 heads
+// 1425 us, 2.5 times what their bytes take at the measured copy bandwidth.  That is the way through the steps above, each with its
+// hand-over to the next one's warps, on a full machine: S's pieces 1,900 cycles (three BF16 pieces take 11 cycles of a scheduler for
+// two values of 32 lanes), what of S k is left then and X 2,000, M X 1,250, U's pieces 1,500, U K 700, S' 850.  The schedulers
+// issue in 55 % of the cycles, the tensor cores work in 37 %.
 // Most products are issued in rolled loops and the code is kept short: straight-line code of a few times this length spent half
-// its time on its own way in.  A new pair costs 2.2 us more than its chunks, 4.5 where a state is read.
+// its time on its own way in.  A new pair costs 2.0 us more than its chunks, 4.2 where a state is read.
 // Every wait is bounded; when one has run out no state that what did not come is part of is written.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -140,8 +140,8 @@ constexpr uint32_t kKqBytes = sizeof(PrefillShared::KQ) / kStages, kVBytes = siz
 //  * kAhead: the first w pieces as they are, and Q and P of the j segments of w pieces behind them, noted after every piece,
 //  * k_gdn_join: the states in front of every piece but the first w from those,
 //  * kPieces: those pieces, now with their outputs.
-// That takes w + 1 pieces' time of n, and (2 j + 1) and (j w + 1) CTAs a pair (one of 4096 tokens, 4 heads: 280 us in one
-// part a head, 83 cut; of 32768 tokens, 32 heads: 2200 and 1250).  The launches overlap: each begins where SMs are left, and waits for the
+// That takes w + 1 pieces' time of n, and (2 j + 1) and (j w + 1) CTAs a pair (one of 4096 tokens, 4 heads: 278 us in one
+// part a head, 83 cut; of 32768 tokens, 32 heads: 2207 and 1258).  The launches overlap: each begins where SMs are left, and waits for the
 // one before it only for what that wrote.
 enum Mode : int32_t { kWhole, kAhead, kPieces };
 
@@ -154,7 +154,7 @@ struct SplitParams {
 
 // Segments of a request of nc chunks.  The join takes a product of 1.1 us for each piece of them, so no more than pay for
 // theirs; and it and one more launch some 30 us, seven chunks' time, which the j w pieces that run beside the others have to
-// save.  (One request of 32 heads, j = 1: 14 chunks 71 us whole, 76 cut, 16 chunks 80 and 80, 20 chunks 97 and 92; of 16 heads: 8
+// save.  (One request of 32 heads, j = 1: 14 chunks 71 us whole, 76 cut, 16 chunks 79 and 80, 20 chunks 96 and 92; of 16 heads: 8
 // chunks 45 and 50, 10 chunks 54 and 54, 12 chunks 62 and 61.)
 __host__ __device__ inline int split_segments(int nc, int j, int w)
 {
@@ -395,7 +395,7 @@ struct Part {
 __device__ __forceinline__ int piece_start(const PrefillParams &p, int nc, int j, uint32_t i)
 {
     // In eighths of a piece: the first w pieces are shorter by one, since a chunk with its outputs takes longer than one of Q's or P's (one
-    // request of 32768 tokens, 32 heads: 1302 us with like pieces, 1250 so, 1320 with two eighths).
+    // request of 32768 tokens, 32 heads: 1316 us with like pieces, 1258 so, 1329 with two eighths).
     const uint32_t w = p.split.w, n = 8 * (j * w + 1) + 7 * w, like = (uint32_t)nc / n, at = i < w ? 7 * i : 8 * i - w;
     return (int)(at * like + at * (nc - n * like) / n);
 }
@@ -958,7 +958,7 @@ __device__ __forceinline__ void issue_thread(const PrefillParams &p, PrefillShar
         {
             const uint32_t b = desc_low(smem_u32(s.M[0]));
             // (Straight-line: the state waits for it, and a rolled loop issues a product in 20 cycles, this in 16, as long as it takes.
-            // One prompt of 32768 tokens, 32 heads: 1315 us rolled, 1263 with U A straight-line as well, 1253 so.)
+            // One prompt of 32768 tokens, 32 heads: 1344 us rolled, 1263 with U A straight-line as well, 1258 so.)
 #pragma unroll
             for (int q = 0; q < 6; ++q) pair(kColU, kColX, b, kPairA[q], kPairB[q], (uint32_t)q);
         }
@@ -1108,7 +1108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5;
     // What comes next waits for this launch's end, in the SMs that are left.  kPieces waits later, where the states in front are read
     // (what else it reads is older than the launches before it), and lets nothing in: the next call's first launch would be
-    // dealt to fewer, busier SMs (one prompt of 2048 tokens x 32 heads, call after call: 127 us so, 121 without).
+    // dealt to fewer, busier SMs (one prompt of 2048 tokens x 32 heads, call after call: 127 us so, 122 without).
     if (p.split.mode != kPieces) {
         pdl_wait();
         pdl_launch_dependents();
@@ -1258,6 +1258,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps * kGroups, 1) k_gdn_join(const
     }
     auto fetch = [&](int slot) {                  // thread 0
         const uint32_t bar = smem_u32(&s.full[slot & 1]);
+        fence_async_shared();                     // (behind what has been read there)
         mbar_expect_tx(bar, kD * kD * 4);
         bulk_load(smem_u32(s.P[slot & 1]), split_state(p.split, pair, slot, 1), kD * kD * 4, bar);
     };
@@ -1421,7 +1422,7 @@ int launch_gdn_prefill(const GdnSeqArgs &a, void *stream)
     p.split.states = reinterpret_cast<float *>(static_cast<uint8_t *>(a.scratch) + kSplitHeader);
     if ((e = run(kAhead, 2 * p.split.j + 1)) != cudaSuccess) return (int)e;
     // Two groups halve P's ways from L2, which bound it where there are many rows; one is the faster where SMs are left.  (Four
-    // requests of up to 4096 tokens, 4 heads: 115 us a call with one group, 113 with two; one such request: 82 and 95.)
+    // requests of up to 4096 tokens, 4 heads: 115 us a call with one group, 114 with two; one such request: 82 and 95.)
     auto join = [&](auto kernel, int groups, size_t bytes) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != cudaSuccess) return e;
